@@ -49,6 +49,13 @@ class Dims(ctypes.Structure):
                 ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int)]
 
 
+class CacheDesc(ctypes.Structure):
+    """The C ``qkvp_cache`` struct."""
+
+    _fields_ = ([(n, ctypes.c_int) for n in ("P", "page", "H", "d_qk", "d_v", "B", "max_pages", "fp8")]
+                + [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "weight", "pos", "table", "lengths")])
+
+
 _lib_handle = None
 _P = ctypes.c_void_p
 
@@ -92,6 +99,15 @@ def lib() -> ctypes.CDLL:
                                        + [_P] * 10 + [ctypes.c_size_t, _P]),
             "qkvp_mlp_forward": (ctypes.c_int, [ctypes.c_int] * 3 + [_P] * 12 + [ctypes.c_size_t, _P]),
             "qkvp_mlp_backward": (ctypes.c_int, [ctypes.c_int] * 3 + [_P] * 18 + [ctypes.c_size_t, _P]),
+            "qkvp_cache_append_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc)]),
+            "qkvp_decode_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc)] + [ctypes.c_int] * 2),
+            "qkvp_cache_evict_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc), ctypes.c_int]),
+            "qkvp_cache_append": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_int] + [_P] * 6
+                                  + [ctypes.c_size_t, _P]),
+            "qkvp_decode_attention": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_int, ctypes.c_float]
+                                      + [_P] * 3 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
+            "qkvp_cache_evict": (ctypes.c_int, [ctypes.POINTER(CacheDesc)] + [ctypes.c_int] * 2 + [_P] * 3
+                                 + [ctypes.c_size_t, _P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -624,3 +640,190 @@ def mlp_backward(dout, W1_8T, w1_scale, W2_8T, w2_scale, saved, ws=None, out=Non
                                    _ptr(o["dout8"]), _ptr(o["dout_scale"]), _ptr(o["dpre"]), _ptr(o["dpre8"]),
                                    _ptr(o["dpre_scale"]), _ptr(ws), ws.numel(), _stream(dev)), "qkvp_mlp_backward")
     return o
+
+
+# ----------------------------------------------------------------------------
+# Serving: paged key-value cache, attention of one new token, eviction
+# ----------------------------------------------------------------------------
+
+@dataclass
+class KVCache:
+    """A paged cache of the forward's k and v for B sequences.
+
+    Slot i of sequence b, head h is row i % page of page ``table[b, i // page]``.
+    k [P, H, page, d_qk] and v [P, H, page, d_v] hold bf16, or uint8 E4M3 codes
+    with one scale per row in k_scale and v_scale [P, H, page] float32.
+    table [B, max_pages] and lengths [B] are int32.  pos [P, H, page] int32 and
+    weight [P, H, page] float32 (each slot's position and accumulated attention
+    weight) are what cache_evict chooses by; both may be None without it.
+    """
+    k: torch.Tensor
+    v: torch.Tensor
+    table: torch.Tensor
+    lengths: torch.Tensor
+    pos: Optional[torch.Tensor] = None
+    weight: Optional[torch.Tensor] = None
+    k_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+    def desc(self) -> CacheDesc:
+        """The checked C descriptor of the tensors as they are now."""
+        k, v, table, lengths = self.k, self.v, self.table, self.lengths
+        fp8 = k.dtype == torch.uint8
+        _need_cuda(k, "cache k", torch.uint8 if fp8 else torch.bfloat16)
+        if k.dim() != 4 or v.dim() != 4 or table.dim() != 2:
+            raise ValueError("cache k and v must be [P, H, page, d], table [B, max_pages]")
+        P, H, page, d = k.shape
+        B, max_pages = table.shape
+        _need_cuda(v, "cache v", k.dtype, (P, H, page, v.shape[3]))
+        _need_cuda(table, "cache table", torch.int32)
+        _need_cuda(lengths, "cache lengths", torch.int32, (B,))
+        rows = (P, H, page)
+        if fp8:
+            _need_cuda(self.k_scale, "cache k_scale", torch.float32, rows)
+            _need_cuda(self.v_scale, "cache v_scale", torch.float32, rows)
+        if self.weight is not None:
+            _need_cuda(self.weight, "cache weight", torch.float32, rows)
+        if self.pos is not None:
+            _need_cuda(self.pos, "cache pos", torch.int32, rows)
+        addr = lambda t: 0 if t is None else t.data_ptr()   # noqa: E731
+        return CacheDesc(P, page, H, d, v.shape[3], B, max_pages, int(fp8), k.data_ptr(), v.data_ptr(),
+                         addr(self.k_scale) if fp8 else 0, addr(self.v_scale) if fp8 else 0, addr(self.weight),
+                         addr(self.pos), table.data_ptr(), lengths.data_ptr())
+
+
+def new_cache(B: int, max_tokens: int, H: int, d_qk: int = 96, d_v: int = 128, page: int = 64, fp8: bool = False,
+              eviction: bool = True, device="cuda") -> KVCache:
+    """An empty cache with its own pages for B sequences of up to max_tokens
+    each (``eviction``: with the positions and weights cache_evict needs)."""
+    pages = -(-max_tokens // page)
+    P = B * pages
+    rows = (P, H, page)
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    make = lambda *s, dtype: torch.empty(s, dtype=dtype, device=device)   # noqa: E731
+    return KVCache(k=make(*rows, d_qk, dtype=dt), v=make(*rows, d_v, dtype=dt),
+                   table=torch.arange(P, dtype=torch.int32, device=device).view(B, pages),
+                   lengths=torch.zeros(B, dtype=torch.int32, device=device),
+                   pos=make(*rows, dtype=torch.int32) if eviction else None,
+                   weight=make(*rows, dtype=torch.float32) if eviction else None,
+                   k_scale=make(*rows, dtype=torch.float32) if fp8 else None,
+                   v_scale=make(*rows, dtype=torch.float32) if fp8 else None)
+
+
+def new_cache_workspace(cache: KVCache, Hq: int, accumulate: bool = True, budget: int = 0) -> torch.Tensor:
+    """A zero-initialised workspace that serves cache_append, decode_attention
+    of Hq query heads and (budget > 0) cache_evict to ``budget`` slots."""
+    d = ctypes.byref(cache.desc())
+    sizes = [lib().qkvp_cache_append_workspace_bytes(d),
+             lib().qkvp_decode_attention_workspace_bytes(d, Hq, int(accumulate))]
+    if budget:
+        sizes.append(lib().qkvp_cache_evict_workspace_bytes(d, budget))
+    if 0 in sizes:
+        raise QKVPError(ERR_UNSUPPORTED, "new_cache_workspace")
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device=cache.k.device)
+    _check(lib().qkvp_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)), "qkvp_workspace_init")
+    return ws
+
+
+# Workspaces of the cache calls made without one, one per (device, stream).
+# A call that is being captured brings its own: a captured graph keeps the
+# address, and this one is replaced when a later call needs more.
+_cache_scratch = {}
+
+
+def _cache_ws(ws, dev, stream, nbytes: int, where: str) -> torch.Tensor:
+    if ws is not None:
+        _need_cuda(ws, "ws", torch.uint8)
+        return ws
+    if nbytes == 0:
+        raise QKVPError(ERR_UNSUPPORTED, where)
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("a captured call needs its own workspace: pass ws=new_cache_workspace(...)")
+    key = (dev.index, stream.value)
+    got = _cache_scratch.get(key)
+    if got is None or got.numel() < nbytes:
+        got = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(lib().qkvp_workspace_init(_ptr(got), nbytes, stream), "qkvp_workspace_init")
+        _cache_scratch[key] = got
+    return got
+
+
+def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
+    """Append new tokens: k [H, T, d_qk], v [H, T, d_v] bf16 (as forward()
+    returns them) and pos [T] int32.  Rows cu[b] .. cu[b + 1) (cu [B + 1] int32)
+    belong to sequence b; without cu there is one row per sequence.  The
+    lengths grow in place, or go to lengths_out.  Returns the new lengths."""
+    d = cache.desc()
+    dev = k.device
+    if k.dim() != 3:
+        raise ValueError("k must be [H, T, d_qk]")
+    T = k.shape[1]
+    _need_cuda(k, "k", torch.bfloat16, (d.H, T, d.d_qk))
+    _need_cuda(v, "v", torch.bfloat16, (d.H, T, d.d_v))
+    _need_cuda(pos, "pos", torch.int32, (T,))
+    if cu is not None:
+        _need_cuda(cu, "cu", torch.int32, (d.B + 1,))
+    if lengths_out is None:
+        lengths_out = cache.lengths
+    else:
+        _need_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
+    stream = _stream(dev)
+    L = lib()
+    ws = _cache_ws(ws, dev, stream, L.qkvp_cache_append_workspace_bytes(ctypes.byref(d)), "qkvp_cache_append")
+    _check(L.qkvp_cache_append(ctypes.byref(d), T, _ptr(k), _ptr(v), _ptr(pos), _ptr(cu), _ptr(lengths_out), _ptr(ws),
+                               ws.numel(), stream), "qkvp_cache_append")
+    return lengths_out
+
+
+def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, out=None):
+    """Attention of one new token per sequence over the cache: q [Hq, B, d_qk]
+    bf16 (as forward() returns it for B tokens; Hq a multiple of the cache's
+    H), scale 1 / sqrt(d_qk) by default.  Returns (a [B, Hq * d_v] bf16, lse [B,
+    Hq] float32), a being oproj_forward's operand; with ``accumulate`` the
+    cache's weights grow by the attention probabilities."""
+    d = cache.desc()
+    dev = q.device
+    if q.dim() != 3:
+        raise ValueError("q must be [Hq, B, d_qk]")
+    Hq = q.shape[0]
+    _need_cuda(q, "q", torch.bfloat16, (Hq, d.B, d.d_qk))
+    if accumulate and cache.weight is None:
+        raise ValueError("accumulate needs cache.weight")
+    if out is None:
+        out = (torch.empty((d.B, Hq * d.d_v), dtype=torch.bfloat16, device=dev),
+               torch.empty((d.B, Hq), dtype=torch.float32, device=dev))
+    a, lse = out
+    _need_cuda(a, "a", torch.bfloat16, (d.B, Hq * d.d_v))
+    _need_cuda(lse, "lse", torch.float32, (d.B, Hq))
+    stream = _stream(dev)
+    L = lib()
+    ws = _cache_ws(ws, dev, stream, L.qkvp_decode_attention_workspace_bytes(ctypes.byref(d), Hq, int(accumulate)),
+                   "qkvp_decode_attention")
+    _check(L.qkvp_decode_attention(ctypes.byref(d), Hq, d.d_qk ** -0.5 if scale is None else scale, _ptr(q), _ptr(a),
+                                   _ptr(lse), int(accumulate), _ptr(ws), ws.numel(), stream), "qkvp_decode_attention")
+    return a, lse
+
+
+def cache_evict(cache: KVCache, budget: int, recent: int, lengths_out=None, ws=None, out=None):
+    """Every head of a sequence longer than ``budget`` keeps that many slots:
+    the positions of the last ``recent`` tokens and, of the others, those of
+    the highest accumulated weight (ties: the lowest slot).  Kept slots at or
+    above the budget move into the freed ones below it.  Returns slots [B, H,
+    budget] int32, the slot each new one held before (-1 past the length); the
+    lengths change in place, or go to lengths_out."""
+    d = cache.desc()
+    dev = cache.k.device
+    if cache.weight is None or cache.pos is None:
+        raise ValueError("cache_evict needs cache.weight and cache.pos")
+    if lengths_out is None:
+        lengths_out = cache.lengths
+    else:
+        _need_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
+    slots = torch.empty((d.B, d.H, max(budget, 1)), dtype=torch.int32, device=dev) if out is None else out
+    _need_cuda(slots, "slots", torch.int32, (d.B, d.H, max(budget, 1)))
+    stream = _stream(dev)
+    L = lib()
+    ws = _cache_ws(ws, dev, stream, L.qkvp_cache_evict_workspace_bytes(ctypes.byref(d), budget), "qkvp_cache_evict")
+    _check(L.qkvp_cache_evict(ctypes.byref(d), budget, recent, _ptr(slots), _ptr(lengths_out), _ptr(ws), ws.numel(),
+                              stream), "qkvp_cache_evict")
+    return slots

@@ -1,0 +1,62 @@
+// The paged key-value cache as the kernels see it: pools of pages, the page
+// table and the lengths, with the checks that keep every access in bounds.
+#pragma once
+
+#include "common.cuh"
+
+namespace qkvp {
+
+// Kernel ids recorded beside an error in the status word (they continue the
+// ids of KernelId).
+enum CacheKernelId : int { KID_CACHE_APPEND = 13, KID_DECODE = 14, KID_DECODE_WEIGHT = 15, KID_EVICT_SELECT = 16,
+                           KID_EVICT_MOVE = 17 };
+
+constexpr int kMaxSeqs = 4096;
+constexpr int kMaxPage = 256;
+constexpr int kDv = 128;
+// Bytes at the start of every workspace: status word, then counters that
+// every call leaves at zero.
+constexpr size_t kCacheStatusBytes = 256;
+
+struct CacheArgs {
+  uint8_t* k;        // [P, H, page, d] bf16 or E4M3 codes
+  uint8_t* v;        // [P, H, page, 128]
+  float* k_scale;    // [P, H, page] (E4M3)
+  float* v_scale;
+  float* weight;     // [P, H, page], or null
+  int32_t* pos;      // [P, H, page], or null
+  const int32_t* table;    // [B, max_pages]
+  const int32_t* lengths;  // [B]
+  int P, H, B, max_pages, page_shift;
+  int d;             // d_qk
+  __host__ __device__ int page() const { return 1 << page_shift; }
+  __host__ __device__ int capacity() const { return max_pages << page_shift; }
+};
+
+// The length of sequence b, clamped to what its pages can hold; a length
+// outside [0, capacity] is recorded.
+__device__ __forceinline__ int checked_length(const CacheArgs& c, int b, const DevStatus& st, int kid) {
+  const int n = __ldg(c.lengths + b), cap = c.capacity();
+  if (n < 0 || n > cap) {
+    record_error(st, QKVP_ERR_DEVICE_INPUT, kid);
+    return n < 0 ? 0 : cap;
+  }
+  return n;
+}
+
+// Row (of the pools seen as [P * H * page, ...]) of slot `slot` of sequence
+// b, head h; -1, recorded, when its page lies outside the pool.  The caller
+// has checked 0 <= slot < capacity.
+__device__ __forceinline__ int64_t cache_row(const CacheArgs& c, int b, int h, int slot, const DevStatus& st, int kid) {
+  const int pid = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + (slot >> c.page_shift));
+  if (pid < 0 || pid >= c.P) {
+    record_error(st, QKVP_ERR_DEVICE_INPUT, kid);
+    return -1;
+  }
+  return ((static_cast<int64_t>(pid) * c.H + h) << c.page_shift) + (slot & (c.page() - 1));
+}
+
+// Host: QKVP_OK or the status an entry point returns for `c`; fills `a`.
+int check_cache(const qkvp_cache* c, CacheArgs* a);
+
+}  // namespace qkvp

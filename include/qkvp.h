@@ -400,6 +400,95 @@ int qkvp_mlp_backward(int T, int D, int F, const uint16_t* dout,
                       uint16_t* dpre, uint8_t* dpre8, float* dpre_scale,
                       void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Serving: a paged key-value cache of the projection's k and v, the attention
+ * of one new token per sequence over it, and eviction from it.  The heads
+ * keep their reduced width in the cache: a slot holds d_qk + 128 values, not
+ * 256.
+ *
+ * Slot i of sequence b, head h is row i % page of page table[b, i / page] in
+ * the pools [P, H, page, ...].  Slots 0 .. lengths[b] - 1 are live; what the
+ * others hold (and the table's entries past the live pages) is never read.
+ * Keys carry their rotation, so the order of the slots does not matter to
+ * the attention; `pos` keeps each slot's position for the eviction.
+ *
+ * Checked on the device, recorded in the workspace's status word as
+ * QKVP_ERR_DEVICE_INPUT: a length outside [0, max_pages * page] is clamped, a
+ * page outside [0, P) holds nothing (its slots are neither read nor written).
+ * Pages of live slots must not be shared between sequences that are written.
+ * ------------------------------------------------------------------------ */
+typedef struct qkvp_cache {
+    int P;            /* pages in the pools, 1 .. 2^26                            */
+    int page;         /* tokens per page: 16, 32, 64, 128 or 256                  */
+    int H;            /* K/V heads, 1 .. 128                                      */
+    int d_qk;         /* key width: 64, 96 or 128                                 */
+    int d_v;          /* value width: 128                                         */
+    int B;            /* sequences, 1 .. 4096                                     */
+    int max_pages;    /* page-table entries per sequence; * page <= 2^24          */
+    int fp8;          /* 0: k, v bf16; 1: E4M3 codes, one scale per row           */
+    void* k;          /* [P, H, page, d_qk] uint16_t or uint8_t                   */
+    void* v;          /* [P, H, page, d_v]                                        */
+    float* k_scale;   /* [P, H, page], fp8 only (else NULL)                       */
+    float* v_scale;
+    float* weight;    /* [P, H, page] accumulated attention weight, or NULL       */
+    int32_t* pos;     /* [P, H, page] position of the slot's token, or NULL       */
+    const int32_t* table;   /* [B, max_pages] pages of each sequence              */
+    int32_t* lengths;       /* [B] live slots                                     */
+} qkvp_cache;
+
+/* Bytes of workspace of each call below (0: unsupported).  Zero it once with
+ * qkvp_workspace_init; every call leaves its counters at zero.  Calls sharing
+ * one workspace must not overlap on the GPU.  One workspace of the largest
+ * size serves all three. */
+size_t qkvp_cache_append_workspace_bytes(const qkvp_cache* cache);
+size_t qkvp_decode_attention_workspace_bytes(const qkvp_cache* cache, int Hq, int accumulate);
+size_t qkvp_cache_evict_workspace_bytes(const qkvp_cache* cache, int budget);
+
+/* Append T new tokens (the k and v that qkvp_forward writes).  Rows cu[b] ..
+ * cu[b + 1) of k and v go to slots lengths[b] + 0, 1, ... of sequence b; their
+ * accumulated weight starts at zero.  fp8: per row the scale s = amax / 448 (1
+ * when amax is 0) and the codes E(x / s), as everywhere in this library.
+ *   k, v      in  [H, T, d_qk], [H, T, d_v] bf16
+ *   pos       in  [T] int32 position of each token (stored if cache->pos)
+ *   cu        in  [B + 1] int32 non-decreasing row offsets, cu[0] = 0, cu[B] =
+ *                 T; NULL: one row per sequence (T = B)
+ *   lengths_out  out [B] lengths after the append; cache->lengths itself (or
+ *                 NULL) updates it in place
+ * A token without room (or rows outside cu) is not stored and recorded as
+ * QKVP_ERR_DEVICE_INPUT. */
+int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const uint16_t* v, const int32_t* pos,
+                      const int32_t* cu, int32_t* lengths_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of one new token per sequence over its live slots (the token's
+ * own k and v included, once appended):
+ *   s_i = scale * q . k_i,  a = sum_i e^(s_i) v_i / sum_i e^(s_i),
+ *   lse = ln sum_i e^(s_i)
+ * Query head h * (Hq / H) + g reads K/V head h (Hq a multiple of H).  A
+ * sequence without live slots gives a = 0 and lse = -inf.
+ *   q         in  [Hq, B, d_qk] bf16 (head-major, as qkvp_forward writes it)
+ *   a         out [B, Hq * d_v] bf16: the heads side by side, the operand of
+ *                 qkvp_oproj_forward
+ *   lse       out [B, Hq] float32, or NULL
+ *   accumulate  nonzero: weight of every live slot of head h += the sum over
+ *                 the head's query heads of e^(s_i - lse)
+ * Results are the same on every run. */
+int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const uint16_t* q, uint16_t* a, float* lse,
+                          int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction.  In every sequence longer than `budget`, each head on its own
+ * keeps `budget` slots: first those whose position is within the last
+ * `recent` (pos > newest pos - recent), then by accumulated weight from the
+ * highest (NaN lowest, -0 = +0), ties to the lowest slot.  Kept slots below
+ * `budget` stay where they are; the j-th kept slot at or above it (in slot
+ * order) moves, with its scales, weight and position, to the j-th slot freed
+ * below.  Needs cache->weight and cache->pos.
+ *   budget    1 .. max_pages * page;  recent 0 .. budget
+ *   slots     out [B, H, budget] int32: the slot each new slot held before
+ *                 (itself if it stayed), -1 past the length
+ *   lengths_out  out [B] min(length, budget); cache->lengths or NULL: in place */
+int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* slots, int32_t* lengths_out, void* ws,
+                     size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

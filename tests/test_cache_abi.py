@@ -1,0 +1,118 @@
+"""Refusals of the cache calls, on the CPU: the C entry points validate their
+arguments before any CUDA call, and the binding checks tensors before those."""
+
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def qk():
+    from fp8_packed_reduced_gb300 import build as b
+    try:
+        b.nvcc()
+    except RuntimeError:
+        pytest.skip("nvcc not available")
+    b.build()
+    import fp8_packed_reduced_gb300 as pkg
+    pkg.lib()
+    return pkg
+
+
+P = 4096   # an aligned, non-null address that no call may reach
+
+
+def _desc(qk, **kw):
+    f = dict(P=8, page=64, H=6, d_qk=96, d_v=128, B=2, max_pages=4, fp8=0, k=P, v=P, k_scale=0, v_scale=0, weight=P,
+             pos=P, table=P, lengths=P)
+    f.update(kw)
+    return qk.CacheDesc(**f)
+
+
+BAD = [(dict(P=0), 1), (dict(page=0), 1), (dict(H=0), 1), (dict(B=0), 1), (dict(max_pages=0), 1), (dict(fp8=2), 1),
+       (dict(k=0), 1), (dict(v=0), 1), (dict(table=0), 1), (dict(lengths=0), 1), (dict(fp8=1), 1),
+       (dict(fp8=1, k_scale=P), 1), (dict(page=24), 2), (dict(page=8), 2), (dict(page=512), 2), (dict(H=129), 2),
+       (dict(B=4097), 2), (dict(max_pages=1 << 20), 2), (dict(P=(1 << 26) + 1), 2), (dict(d_qk=80), 2),
+       (dict(d_v=64), 2), (dict(k=P + 8), 3), (dict(lengths=P + 4), 3), (dict(weight=P + 4), 3), (dict(pos=P + 8), 3)]
+
+
+@pytest.mark.parametrize("change,code", BAD, ids=[str(c) for c, _ in BAD])
+def test_every_call_refuses_a_bad_cache(qk, change, code):
+    d = ctypes.byref(_desc(qk, **change))
+    L = qk.lib()
+    assert L.qkvp_cache_append_workspace_bytes(d) == 0
+    assert L.qkvp_decode_attention_workspace_bytes(d, 6, 1) == 0
+    assert L.qkvp_cache_evict_workspace_bytes(d, 1) == 0
+    assert L.qkvp_cache_append(d, 2, P, P, P, None, P, P, 1 << 40, None) == code
+    assert L.qkvp_decode_attention(d, change.get("H", 6) or 6, 0.1, P, P, P, 0, P, 1 << 40, None) == code
+    assert L.qkvp_cache_evict(d, 8, 4, P, P, P, 1 << 40, None) == code
+
+
+def test_null_cache(qk):
+    L = qk.lib()
+    assert L.qkvp_cache_append(None, 2, P, P, P, None, P, P, 1 << 40, None) == qk.ERR_INVALID_ARGUMENT
+    assert L.qkvp_decode_attention(None, 6, 0.1, P, P, P, 0, P, 1 << 40, None) == qk.ERR_INVALID_ARGUMENT
+    assert L.qkvp_cache_evict(None, 8, 4, P, P, P, 1 << 40, None) == qk.ERR_INVALID_ARGUMENT
+
+
+def test_append_refusals(qk):
+    f, d = qk.lib().qkvp_cache_append, ctypes.byref(_desc(qk))
+    n = qk.lib().qkvp_cache_append_workspace_bytes(d)
+    assert n > 0
+    assert f(d, -1, P, P, P, P, P, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 3, P, P, P, None, P, P, n, None) == qk.ERR_INVALID_ARGUMENT      # T != B without cu
+    for i in range(3):                                                           # k, v, pos
+        args = [P, P, P]
+        args[i] = None
+        assert f(d, 2, *args, None, P, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 2, P, P, P, None, P, None, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 2, P + 2, P, P, None, P, P, n, None) == qk.ERR_MISALIGNED
+    assert f(d, 2, P, P, P, P + 4, P, P, n, None) == qk.ERR_MISALIGNED
+    assert f(d, 2, P, P, P, None, P + 4, P, n, None) == qk.ERR_MISALIGNED
+    assert f(d, (1 << 24) + 1, P, P, P, P, P, P, n, None) == qk.ERR_UNSUPPORTED
+    assert f(d, 2, P, P, P, None, P, P, n - 1, None) == qk.ERR_WORKSPACE_TOO_SMALL
+
+
+def test_decode_refusals(qk):
+    f, d = qk.lib().qkvp_decode_attention, ctypes.byref(_desc(qk))
+    n = qk.lib().qkvp_decode_attention_workspace_bytes(d, 6, 1)
+    assert n > qk.lib().qkvp_decode_attention_workspace_bytes(d, 6, 0) > 0
+    assert f(d, 0, 0.1, P, P, P, 0, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 9, 0.1, P, P, P, 0, P, n, None) == qk.ERR_UNSUPPORTED            # not a multiple of 6
+    assert f(d, 6 * 200, 0.1, P, P, P, 0, P, 1 << 40, None) == qk.ERR_UNSUPPORTED
+    assert f(d, 6, float("nan"), P, P, P, 0, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 6, float("inf"), P, P, P, 0, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 6, 0.1, None, P, P, 0, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 6, 0.1, P, None, P, 0, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 6, 0.1, P, P, P, 0, None, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(ctypes.byref(_desc(qk, weight=0)), 6, 0.1, P, P, P, 1, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 6, 0.1, P + 2, P, P, 0, P, n, None) == qk.ERR_MISALIGNED
+    assert f(d, 6, 0.1, P, P, P + 4, 0, P, n, None) == qk.ERR_MISALIGNED
+    assert f(d, 6, 0.1, P, P, P, 1, P, n - 1, None) == qk.ERR_WORKSPACE_TOO_SMALL
+
+
+def test_evict_refusals(qk):
+    f, d = qk.lib().qkvp_cache_evict, ctypes.byref(_desc(qk))
+    n = qk.lib().qkvp_cache_evict_workspace_bytes(d, 100)
+    assert n > 0
+    assert qk.lib().qkvp_cache_evict_workspace_bytes(d, 0) == 0
+    assert qk.lib().qkvp_cache_evict_workspace_bytes(d, 4 * 64 + 1) == 0
+    for budget, recent in ((0, 0), (257, 0), (100, 101), (100, -1)):
+        assert f(d, budget, recent, P, P, P, 1 << 40, None) == qk.ERR_INVALID_ARGUMENT
+    for change in (dict(weight=0), dict(pos=0)):
+        assert f(ctypes.byref(_desc(qk, **change)), 100, 4, P, P, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 100, 4, None, P, P, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 100, 4, P, P, None, n, None) == qk.ERR_INVALID_ARGUMENT
+    assert f(d, 100, 4, P + 4, P, P, n, None) == qk.ERR_MISALIGNED
+    assert f(d, 100, 4, P, P, P, n - 1, None) == qk.ERR_WORKSPACE_TOO_SMALL
+
+
+def test_binding_refuses_tensors_off_the_gpu(qk):
+    cache = qk.new_cache(2, 100, 6, device="cpu")
+    assert cache.k.shape == (4, 6, 64, 96) and cache.table.shape == (2, 2)
+    z = torch.zeros((6, 2, 96), dtype=torch.bfloat16)
+    for call in (lambda: qk.decode_attention(z, cache), lambda: qk.cache_evict(cache, 10, 2),
+                 lambda: qk.cache_append(cache, z, z, torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()

@@ -1,0 +1,547 @@
+"""The paged cache on the GPU, through the binding, against the float64 oracle.
+
+Bounds of the attention, fixed by the arithmetic: products of bf16 (or
+de-quantised E4M3) numbers are exact in float32, so a score is off by at most
+delta = (d + 8) * 2^-23 * scale * sum_j |q_j k_j| (d additions, scale and
+exponent; 2^-23 a step, since a matrix unit may truncate where an addition
+would round), every probability by 2 delta + 2^-20 relative (numerator, sum,
+the exponential's own error), and the weights of v are rounded to bf16 (half a
+step: 2^-8 relative).  So
+  |a - ref|      <= 2^-8 |ref| + (2^-8 + 2 delta + 2^-20) sum_i p_i |v_i|
+  |lse - ref|    <= delta + 2^-20 (1 + |ref|)
+  |weight - ref| <= (2 delta + 2^-20) sum_g p_g + 2^-22 |ref|
+Appended rows, codes, scales, evicted slots and moved rows are exact."""
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import cache_oracle as co
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def qk():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from fp8_packed_reduced_gb300 import build as b
+    b.build()
+    import fp8_packed_reduced_gb300 as pkg
+    pkg.lib()
+    return pkg
+
+
+def _normal(shape, seed):
+    return synth._normal(shape, 1.0, seed)
+
+
+def make_cache(qk, lens, H, d, page, fp8, cap=None, seed=0, spare=2):
+    """A cache with random live slots.  Everything that is not live is poison:
+    NaN rows, codes and scales, and page-table entries outside the pool."""
+    B = len(lens)
+    cap = max([cap or 1] + list(lens))
+    pages = -(-cap // page)
+    g = torch.Generator().manual_seed(seed)
+    P = B * pages + spare
+    table = torch.randperm(P, generator=g)[:B * pages].view(B, pages).to(torch.int32)
+    k, v = _normal((P, H, page, d), seed + 1), _normal((P, H, page, 128), seed + 2)
+    ks = vs = None
+    if fp8:
+        def codes(x):
+            x = x.float()
+            s = (x.abs().amax(-1) / torch.tensor(448.0)).clamp(min=1e-30)
+            return (x / s[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), s
+        (k, ks), (v, vs) = codes(k), codes(v)
+    weight = torch.rand((P, H, page), generator=g) ** 3
+    pos = torch.randint(0, 100000, (P, H, page), generator=g, dtype=torch.int32)
+    live = torch.zeros((P, page), dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for i in range(pages):
+            live[table[b, i], :max(0, min(page, n - i * page))] = True
+    dead = ~live[:, None, :].expand(P, H, page)
+    for t in (ks, vs, weight):
+        if t is not None:
+            t[dead] = float("nan")
+    pos[dead] = 2 ** 31 - 1
+    for t in (k, v):
+        t[dead] = 0x7F if fp8 else float("nan")
+    full = table.clone()
+    for b, n in enumerate(lens):
+        table[b, -(-n // page):] = (-1, 2 ** 30)[b % 2]
+    to = lambda t: None if t is None else t.to(DEV).contiguous()   # noqa: E731
+    cache = qk.KVCache(to(k), to(v), to(table), torch.tensor(lens, dtype=torch.int32, device=DEV), pos=to(pos),
+                       weight=to(weight), k_scale=to(ks), v_scale=to(vs))
+    return cache, full
+
+
+def host(cache):
+    c = {}
+    for name in ("k", "v", "k_scale", "v_scale", "pos", "weight", "table", "lengths"):
+        t = getattr(cache, name)
+        c[name] = None if t is None else (synth.to_numpy_f32(t) if t.dtype == torch.bfloat16 else t.cpu().numpy()).copy()
+    return c
+
+
+def same(got, ref, name):
+    np.testing.assert_array_equal(got, ref, err_msg=name)   # NaN equals NaN here
+
+
+# ---------------------------------------------------------------------------
+# Append
+# ---------------------------------------------------------------------------
+APPEND = [  # d, page, fp8, lengths before, new rows per sequence (None: one each)
+    (96, 64, False, [0, 5, 63, 64, 65], None),
+    (96, 64, True, [0, 5, 63, 64, 65], None),
+    (64, 16, False, [0, 1, 15, 16, 30], [17, 0, 1, 33, 2]),
+    (96, 32, True, [0, 1, 31, 32, 0, 7], [0, 33, 1, 0, 64, 3]),
+    (128, 128, True, [100], [157]),
+    (128, 256, False, [0, 255, 256], [255, 1, 300]),
+    (64, 64, True, [3] * 40, [1, 0, 2, 0, 0] * 8),
+    (96, 16, False, [0, 0, 0], [0, 0, 0]),
+]
+
+
+@pytest.mark.parametrize("d,page,fp8,lens,new", APPEND, ids=[f"{c[0]}-{c[1]}-{'e4m3' if c[2] else 'bf16'}-B{len(c[3])}" for c in APPEND])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append(qk, d, page, fp8, lens, new, in_place):
+    H = 3
+    add = [1] * len(lens) if new is None else new
+    cache, full = make_cache(qk, lens, H, d, page, fp8, cap=max(a + b for a, b in zip(lens, add)), seed=d + page)
+    cache.table = full.to(DEV)
+    T = sum(add)
+    k, v = _normal((H, T, d), 7), _normal((H, T, 128), 8)
+    if T > 2:
+        k[1, 1] = 0          # a zero row: scale 1
+        v[0, 2] = 1e-38      # a scale whose reciprocal overflows
+    pos = torch.arange(T, dtype=torch.int32) * 3 + 1
+    cu = None if new is None else torch.tensor([0] + add).cumsum(0).to(torch.int32)
+    ref = host(cache)
+    want = co.cache_append(ref, synth.to_numpy_f32(k), synth.to_numpy_f32(v), pos.numpy(), None if cu is None else cu.numpy())
+    out = None if in_place else torch.full((len(lens),), -7, dtype=torch.int32, device=DEV)
+    ws = qk.new_cache_workspace(cache, H)
+    for _ in range(1 if in_place else 2):   # not in place, a second call stores the same again
+        got = qk.cache_append(cache, k.to(DEV), v.to(DEV), pos.to(DEV), None if cu is None else cu.to(DEV), out, ws=ws)
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+    same(got.cpu().numpy(), want, "lengths")
+    same(cache.lengths.cpu().numpy(), want if in_place else lens, "cache.lengths")
+    have = host(cache)
+    for name in ("k", "v", "k_scale", "v_scale", "pos", "weight"):
+        if ref[name] is not None:
+            same(have[name], ref[name], name)
+
+
+def test_append_in_place_many_times(qk):
+    """A decode loop: the lengths grow by one a call, on one workspace."""
+    H, lens = 2, [0, 62, 7]
+    cache, full = make_cache(qk, lens, H, 96, 16, False, cap=80)
+    cache.table = full.to(DEV)
+    ref = host(cache)
+    for step in range(6):
+        k, v = _normal((H, 3, 96), step), _normal((H, 3, 128), step + 50)
+        pos = torch.full((3,), step, dtype=torch.int32)
+        qk.cache_append(cache, k.to(DEV), v.to(DEV), pos.to(DEV))
+        ref["lengths"] = co.cache_append(ref, synth.to_numpy_f32(k), synth.to_numpy_f32(v), pos.numpy())
+    have = host(cache)
+    for name in ("k", "v", "pos", "weight", "lengths"):
+        same(have[name], ref[name], name)
+
+
+def test_append_reports_what_does_not_fit(qk):
+    """No room, a page outside the pool, rows outside cu: recorded, nothing
+    else touched."""
+    H, d = 2, 96
+    cache, full = make_cache(qk, [30, 4, 0], H, d, 16, False, cap=32)
+    cache.table = full.to(DEV)
+    cache.table[1, 0] = cache.k.shape[0]     # one past the pool
+    ws = qk.new_cache_workspace(cache, H)
+    k, v, pos = _normal((H, 9, d), 1).to(DEV), _normal((H, 9, 128), 2).to(DEV), torch.arange(9, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 5, 7, 8], dtype=torch.int32, device=DEV)   # the ninth row belongs to none
+    ref = host(cache)
+    got = qk.cache_append(cache, k, v, pos, cu, torch.empty_like(cache.lengths), ws=ws)
+    assert qk.poll_device_status(ws) == (qk.ERR_DEVICE_INPUT, 13)
+    assert got.tolist() == [32, 6, 1]
+    have = host(cache)
+    kk, vv = synth.to_numpy_f32(k.cpu()), synth.to_numpy_f32(v.cpu())
+    t0, t2 = ref["table"][0], ref["table"][2]
+    for h in range(H):
+        ref["k"][t0[1], h, 14:16], ref["v"][t0[1], h, 14:16] = kk[h, :2], vv[h, :2]
+        ref["k"][t2[0], h, 0], ref["v"][t2[0], h, 0] = kk[h, 7], vv[h, 7]
+    same(have["k"], ref["k"], "k")
+    same(have["v"], ref["v"], "v")
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+
+
+# ---------------------------------------------------------------------------
+# Attention of one token
+# ---------------------------------------------------------------------------
+def check_decode(qk, cache, q, scale=None, accumulate=True, ws=None):
+    H, d = cache.k.shape[1], q.shape[2]
+    Hq, B, _ = q.shape
+    sc = d ** -0.5 if scale is None else scale
+    ref = host(cache)
+    before = ref["weight"].copy()
+    own = qk.new_cache_workspace(cache, Hq) if ws is None else ws
+    a, lse = qk.decode_attention(q.to(DEV), cache, scale=scale, accumulate=accumulate, ws=own)
+    assert qk.poll_device_status(own) == (qk.OK, 0)
+    ra, rl, p, absa, size = co.decode_attention(ref, synth.to_numpy_f32(q), sc)
+    a = synth.to_numpy_f32(a.cpu()).reshape(B, Hq, 128).astype(np.float64)
+    lse = lse.cpu().numpy().astype(np.float64)
+    delta = (d + 8) * 2.0 ** -23 * size
+    bound = 2.0 ** -8 * np.abs(ra) + (2.0 ** -8 + 2 * delta[..., None] + 2.0 ** -20) * absa
+    err = np.abs(a - ra)
+    assert (err <= bound).all(), f"a: {np.max(err - bound)} beyond the bound at {np.argmax(err - bound)}"
+    live = np.array(ref["lengths"]) > 0
+    assert np.array_equal(lse[~live], rl[~live])
+    assert (np.abs(lse[live] - rl[live]) <= (delta + 2.0 ** -20 * (1 + np.abs(rl)))[live]).all(), "lse"
+    weight = cache.weight.cpu().numpy()
+    if not accumulate:
+        same(weight, before, "weight")
+        return a, lse
+    page, G = ref["k"].shape[2], Hq // H
+    want, tol = before.astype(np.float64), np.zeros(before.shape)
+    for b, n in enumerate(ref["lengths"]):
+        at = ref["table"][b][np.arange(n) // page], np.arange(n) % page
+        for h in range(H if n else 0):
+            for g in range(h * G, (h + 1) * G):
+                want[at[0], h, at[1]] += p[b][g]
+                tol[at[0], h, at[1]] += (2 * delta[b, g] + 2.0 ** -20) * p[b][g]
+    ok = np.isnan(want) | (np.abs(weight - want) <= tol + 2.0 ** -22 * np.abs(want))
+    assert ok.all() and np.array_equal(np.isnan(weight), np.isnan(want)), "weight"
+    return a, lse
+
+
+SHORT = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 0, 129]
+DECODE = [  # lengths, H, G, d, page, fp8
+    (SHORT, 2, 1, 96, 64, False),
+    (SHORT, 2, 1, 96, 16, True),
+    (SHORT, 1, 8, 64, 32, False),
+    (SHORT, 1, 3, 128, 128, True),
+    ([1], 6, 1, 96, 64, False),
+    ([0], 6, 1, 96, 64, True),
+    ([1500], 2, 1, 96, 64, False),
+    ([1500], 2, 1, 96, 64, True),
+    ([777, 2], 2, 16, 64, 256, False),
+    ([777, 2], 1, 12, 96, 16, True),
+    ([300, 0, 41], 2, 9, 128, 64, False),
+    ([300, 0, 41], 1, 33, 96, 64, False),
+    ([2000, 3, 0, 700, 1, 1999], 5, 2, 128, 16, False),
+    ([900] * 3, 16, 1, 64, 32, True),
+    ([5, 900, 0, 0, 33] * 4, 3, 4, 128, 128, True),
+]
+
+
+@pytest.mark.parametrize("lens,H,G,d,page,fp8", DECODE,
+                         ids=[f"B{len(c[0])}-max{max(c[0])}-H{c[1]}-G{c[2]}-d{c[3]}-p{c[4]}-{'e4m3' if c[5] else 'bf16'}" for c in DECODE])
+def test_decode(qk, lens, H, G, d, page, fp8):
+    cache, _ = make_cache(qk, lens, H, d, page, fp8, seed=len(lens) + d)
+    q = _normal((H * G, len(lens), d), 5)
+    check_decode(qk, cache, q, accumulate=False)
+    check_decode(qk, cache, q * 3, accumulate=True)      # sharper
+    check_decode(qk, cache, q, scale=0.0)                # the plain mean of v
+    check_decode(qk, cache, q, scale=-0.3)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_large_scores(qk, fp8):
+    """Scores in the thousands, of both signs, rising and falling along the
+    cache: only differences to the running maximum are exponentiated."""
+    lens = [400, 90]
+    cache, _ = make_cache(qk, lens, 2, 96, 64, fp8, seed=3)
+    check_decode(qk, cache, _normal((2, 2, 96), 6) * 256)
+
+
+def test_decode_without_lse_weight_and_pos(qk):
+    cache, _ = make_cache(qk, [70, 9], 2, 96, 16, False)
+    q = _normal((2, 2, 96), 1).to(DEV)
+    a, _ = qk.decode_attention(q, cache)
+    cache.weight = cache.pos = None
+    b, _ = qk.decode_attention(q, cache)
+    assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="weight"):
+        qk.decode_attention(q, cache, accumulate=True)
+
+
+def test_decode_infinities_and_nan_in_live_rows(qk):
+    """What the formula gives: +inf in a score or NaN anywhere in a head's live
+    rows makes that head NaN and no other; a score of -inf has no weight."""
+    cache, _ = make_cache(qk, [40, 40, 40], 2, 96, 16, False)
+    q = torch.ones((2, 3, 96), dtype=torch.bfloat16, device=DEV)
+    t = cache.table.cpu()
+    good, glse = qk.decode_attention(q, cache)
+    cache.k[t[0, 1], 0, 3, 5] = float("nan")
+    cache.k[t[1, 2], 1, 2, 0] = float("inf")
+    cache.k[t[2, 0], 0, 4, 0] = float("-inf")
+    a, lse = qk.decode_attention(q, cache, accumulate=True)
+    a, good = a.view(3, 2, 128).float(), good.view(3, 2, 128).float()
+    assert a[0, 0].isnan().all() and a[1, 1].isnan().all()
+    assert torch.equal(a[0, 1], good[0, 1]) and torch.equal(a[1, 0], good[1, 0]) and torch.equal(a[2, 1], good[2, 1])
+    assert a[2, 0].isfinite().all() and lse[2, 0].isfinite()
+    assert not cache.weight[t[2, 0], 0, 4].isnan()
+    # every score -inf: nothing has weight, as in an empty row
+    cache2, _ = make_cache(qk, [40], 2, 96, 16, False)
+    cache2.k[cache2.table[0].long(), 1, :, 0] = float("-inf")
+    a, lse = qk.decode_attention(q[:, :1].contiguous(), cache2)
+    assert (a.view(2, 128)[1] == 0).all() and lse[0, 1] == -float("inf") and lse[0, 0].isfinite()
+
+
+def test_decode_reports_bad_pages_and_lengths(qk):
+    """A live page outside the pool is skipped, a length beyond the capacity
+    is clamped, a negative one is empty: each is recorded."""
+    cache, full = make_cache(qk, [64, 33, 16], 2, 96, 16, False, cap=64)
+    cache.table = full.to(DEV)
+    q = _normal((2, 3, 96), 1).to(DEV)
+    ws = qk.new_cache_workspace(cache, 2)
+    for page in (-1, cache.k.shape[0], 2 ** 31 - 1):
+        cache.table[1, 1] = page
+        w = cache.weight.clone()
+        a, lse = qk.decode_attention(q, cache, accumulate=True, ws=ws)
+        assert qk.poll_device_status(ws)[0] == qk.ERR_DEVICE_INPUT
+        assert a.isfinite().all() and lse.isfinite().all()
+        cache.weight.copy_(w)
+    cache.table.copy_(full)
+    good = qk.decode_attention(q, cache, ws=ws)
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+    for n in (65, 2 ** 31 - 1, -1):
+        cache.lengths[0] = n
+        a, lse = qk.decode_attention(q, cache, ws=ws)
+        assert qk.poll_device_status(ws)[0] == qk.ERR_DEVICE_INPUT
+        assert torch.equal(a[1:], good[0][1:])
+        assert torch.equal(a[0], good[0][0]) if n > 0 else (a[0] == 0).all()
+
+
+def test_decode_is_the_same_on_every_run(qk):
+    lens = [3000, 5, 0, 811, 1200]
+    for fp8 in (False, True):
+        cache, _ = make_cache(qk, lens, 3, 96, 32, fp8)
+        q = _normal((6, 5, 96), 4).to(DEV)
+        w0 = cache.weight.clone()
+        first = None
+        for _ in range(5):
+            cache.weight.copy_(w0)
+            got = (*qk.decode_attention(q, cache, accumulate=True), cache.weight.nan_to_num())
+            first = first or tuple(t.clone() for t in got)
+            assert all(torch.equal(x, y) for x, y in zip(got, first))
+
+
+def test_offsets_beyond_32_bits(qk):
+    """A pool of more than 2^32 bytes in k and in v, the live pages at its end."""
+    H, d, page = 8, 96, 64
+    P = 50000                                     # k: 4.9 GB, v: 6.6 GB
+    free, _ = torch.cuda.mem_get_info()
+    if free < 30e9:
+        pytest.skip("needs 30 GB of device memory")
+    small, full = make_cache(qk, [150, 70], H, d, page, False)
+    big = lambda t: torch.zeros((P, *t.shape[1:]), dtype=t.dtype, device=DEV)   # noqa: E731
+    n = small.k.shape[0]
+    cache = qk.KVCache(big(small.k), big(small.v), (full + (P - n)).to(DEV), small.lengths.clone(), pos=big(small.pos),
+                       weight=big(small.weight))
+    for name in ("k", "v", "pos", "weight"):
+        getattr(cache, name)[P - n:] = getattr(small, name)
+    small.table = full.to(DEV)
+    q = _normal((H, 2, d), 3).to(DEV)
+    k, v, pos = _normal((H, 2, d), 4).to(DEV), _normal((H, 2, 128), 5).to(DEV), torch.tensor([9, 8], dtype=torch.int32, device=DEV)
+    for c in (small, cache):
+        qk.cache_append(c, k, v, pos)
+    got = [qk.decode_attention(q, c, accumulate=True) for c in (small, cache)]
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    slots = [qk.cache_evict(c, 65, 10) for c in (small, cache)]
+    assert torch.equal(*slots)
+    for name in ("k", "v", "pos", "weight"):
+        same(getattr(cache, name)[P - n:].float().cpu().numpy(), getattr(small, name).float().cpu().numpy(), name)
+        assert not getattr(cache, name)[:P - n].any()
+
+
+# ---------------------------------------------------------------------------
+# Eviction
+# ---------------------------------------------------------------------------
+EVICT = [  # lengths, H, d, page, fp8, budget, recent
+    ([40, 0, 1, 16, 17, 100], 2, 96, 16, False, 16, 4),
+    ([40, 0, 1, 16, 17, 100], 2, 96, 16, True, 16, 16),
+    ([65, 64, 63, 2], 3, 64, 64, False, 1, 0),
+    ([65, 64, 63, 2], 3, 128, 64, True, 1, 1),
+    ([2500, 1300], 2, 96, 64, False, 1200, 300),
+    ([2500, 2049], 1, 128, 256, True, 2048, 0),
+    ([333] * 5, 4, 64, 32, True, 332, 17),
+]
+
+
+@pytest.mark.parametrize("lens,H,d,page,fp8,budget,recent", EVICT,
+                         ids=[f"B{len(c[0])}-max{max(c[0])}-d{c[2]}-{'e4m3' if c[4] else 'bf16'}-{c[5]}-{c[6]}" for c in EVICT])
+@pytest.mark.parametrize("values", ["distinct", "ties", "zeros", "special"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict(qk, lens, H, d, page, fp8, budget, recent, values, in_place):
+    cache, _ = make_cache(qk, lens, H, d, page, fp8, seed=budget)
+    g = torch.Generator().manual_seed(budget + recent)
+    w = cache.weight.cpu()
+    live = ~w.isnan()
+    if values == "ties":
+        w = torch.randint(0, 4, w.shape, generator=g).float()
+    elif values == "zeros":
+        w = torch.where(torch.rand(w.shape, generator=g) < 0.5, 0.0, -0.0)
+    elif values == "special":
+        pick = torch.randint(0, 7, w.shape, generator=g)
+        w = torch.tensor([float("nan"), float("inf"), -float("inf"), 0.0, -1.0, 1e-40, 3.4e38])[pick]
+    cache.weight.copy_(torch.where(live, w, torch.tensor(float("nan"))))
+    # distinct positions, in an order of each head's own
+    n = max(lens)
+    for b, m in enumerate(lens):
+        for h in range(H):
+            order = torch.randperm(m, generator=g).to(torch.int32) * 2 + 3
+            slot = torch.arange(m)
+            cache.pos[cache.table[b].cpu()[slot // page].long(), h, slot % page] = order.to(DEV)
+    ref = host(cache)
+    want, lengths = co.cache_evict(ref, budget, recent) if budget <= n else (None, None)
+    out = None if in_place else torch.full((len(lens),), -1, dtype=torch.int32, device=DEV)
+    ws = qk.new_cache_workspace(cache, H, budget=budget)
+    slots = qk.cache_evict(cache, budget, recent, lengths_out=out, ws=ws)
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+    same(slots.cpu().numpy(), want, "slots")
+    same((cache.lengths if in_place else out).cpu().numpy(), lengths, "lengths")
+    same(cache.lengths.cpu().numpy(), lengths if in_place else lens, "cache.lengths")
+    have = host(cache)
+    for name in ("k", "v", "k_scale", "v_scale", "pos", "weight"):
+        if ref[name] is not None:
+            same(have[name], ref[name], name)
+
+
+def test_evict_equal_positions_and_extremes(qk):
+    """Positions that repeat, and the ends of int32: "recent" is an exact
+    difference, and ties among the protected go to the lowest slots."""
+    cache, _ = make_cache(qk, [50, 50], 1, 96, 16, False)
+    for b, vals in enumerate(([7] * 50, [-2 ** 31] * 20 + [2 ** 31 - 1] * 30)):
+        slot = torch.arange(50)
+        cache.pos[cache.table[b].cpu()[slot // 16].long(), 0, slot % 16] = torch.tensor(vals, dtype=torch.int32, device=DEV)
+    ref = host(cache)
+    want, _ = co.cache_evict(ref, 25, 3)
+    slots = qk.cache_evict(cache, 25, 3)
+    same(slots.cpu().numpy(), want, "slots")
+    same(slots[0, 0].cpu().numpy(), np.arange(25), "the lowest of equals")
+
+
+def test_evict_long_matches_sorted(qk):
+    """Longer than one block's slots by far, against torch's stable sort."""
+    H, n, budget, recent = 2, 70001, 30011, 500
+    cache = qk.new_cache(1, n, H, 64, page=128, fp8=True)
+    for t in (cache.k, cache.v):
+        t.random_(0, 120)
+    cache.k_scale.uniform_(), cache.v_scale.uniform_()
+    cache.weight.uniform_().mul_(100).floor_()           # ties at the border
+    cap = cache.table.shape[1] * 128
+    cache.pos.copy_(torch.arange(cap, device=DEV).view(-1, 1, 128).expand(-1, H, 128))
+    cache.lengths.fill_(n)
+    k0, w0 = cache.k.clone(), cache.weight.clone()
+    slots = qk.cache_evict(cache, budget, recent)
+    for h in range(H):
+        w = w0[:, h].reshape(-1)[:n].clone()
+        w[n - recent:] = float("inf")
+        keep = torch.zeros(n, dtype=torch.bool, device=DEV)
+        keep[torch.sort(w, descending=True, stable=True).indices[:budget]] = True
+        want = torch.arange(budget, device=DEV)
+        want[~keep[:budget]] = keep.nonzero()[:, 0][keep.nonzero()[:, 0] >= budget]
+        assert torch.equal(slots[0, h].long(), want)
+        assert torch.equal(cache.k[:, h].reshape(cap, -1)[:budget], k0[:, h].reshape(cap, -1)[want])
+    assert cache.lengths.tolist() == [budget]
+
+
+def test_evict_reports_bad_pages(qk):
+    cache, full = make_cache(qk, [64, 33], 2, 96, 16, False, cap=64)
+    cache.table = full.to(DEV)
+    cache.table[0, 1] = cache.k.shape[0]
+    ws = qk.new_cache_workspace(cache, 2, budget=20)
+    before = host(cache)
+    slots = qk.cache_evict(cache, 20, 4, ws=ws)
+    assert qk.poll_device_status(ws)[0] == qk.ERR_DEVICE_INPUT
+    assert cache.lengths.tolist() == [20, 20] and int(slots.max()) < 64 and int(slots.min()) >= 0
+    # the sequence with good pages is as the oracle has it
+    ref = dict(before, table=before["table"][1:], lengths=before["lengths"][1:])
+    want, _ = co.cache_evict(ref, 20, 4)
+    same(slots[1:].cpu().numpy(), want, "slots")
+
+
+# ---------------------------------------------------------------------------
+# Streams, graphs, workspaces
+# ---------------------------------------------------------------------------
+def test_other_stream_and_graph(qk):
+    """The three calls on a side stream, and replayed from a graph, give the
+    bits of the same calls on the default stream."""
+    lens, H, d = [100, 3, 64], 2, 96
+    k, v = _normal((H, 3, d), 1).to(DEV), _normal((H, 3, 128), 2).to(DEV)
+    q, pos = _normal((H, 3, d), 3).to(DEV), torch.tensor([100000] * 3, dtype=torch.int32, device=DEV)
+
+    def step(cache, ws, out):
+        qk.cache_append(cache, k, v, pos, ws=ws)
+        qk.decode_attention(q, cache, accumulate=True, ws=ws, out=out[:2])
+        qk.cache_evict(cache, 60, 8, ws=ws, out=out[2])
+
+    def fresh():
+        cache, full = make_cache(qk, lens, H, d, 16, False, cap=112)
+        cache.table = full.to(DEV)
+        out = (torch.empty((3, H * 128), dtype=torch.bfloat16, device=DEV), torch.empty((3, H), device=DEV),
+               torch.empty((3, H, 60), dtype=torch.int32, device=DEV))
+        return cache, qk.new_cache_workspace(cache, H, budget=60), out
+
+    def state(cache, out):
+        torch.cuda.synchronize()
+        return [t.float().nan_to_num().cpu() for t in (cache.k, cache.v, cache.weight, cache.pos, cache.lengths, *out)]
+
+    cache, ws, out = fresh()
+    for _ in range(3):
+        step(cache, ws, out)
+    want = state(cache, out)
+
+    cache, ws, out = fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step(cache, ws, out)
+    assert all(torch.equal(x, y) for x, y in zip(state(cache, out), want))
+
+    cache, ws, out = fresh()
+    step(cache, ws, out)      # outside the graph first
+    cache, ws, out = fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(cache, ws, out)
+        with pytest.raises(ValueError, match="workspace"):
+            qk.decode_attention(q, cache)
+    for _ in range(3):
+        graph.replay()
+    assert all(torch.equal(x, y) for x, y in zip(state(cache, out), want))
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+
+
+def test_one_workspace_for_different_shapes(qk):
+    """The counters are left at zero: calls of other shapes follow each other
+    on one workspace."""
+    caches = [make_cache(qk, lens, H, 96, 32, fp8, seed=i)[0]
+              for i, (lens, H, fp8) in enumerate([([900], 1, False), ([5] * 30, 3, True), ([0, 700, 31], 2, False)])]
+    ws = max((qk.new_cache_workspace(c, 4 * c.k.shape[1]) for c in caches), key=lambda t: t.numel())
+    for _ in range(2):
+        for c in caches:
+            check_decode(qk, c, _normal((4 * c.k.shape[1], c.table.shape[0], 96), 2), ws=ws)
+
+
+def test_binding_refusals(qk):
+    cache, _ = make_cache(qk, [20, 3], 2, 96, 16, False)
+    q = _normal((2, 2, 96), 1).to(DEV)
+    bad = [q[:, :1], q.float(), q[:, :, :64].contiguous(), q.transpose(0, 1), q[0]]
+    for t in bad:
+        with pytest.raises(ValueError):
+            qk.decode_attention(t, cache)
+    with pytest.raises(qk.QKVPError, match="UNSUPPORTED"):
+        qk.decode_attention(_normal((3, 2, 96), 1).to(DEV), cache)
+    with pytest.raises(qk.QKVPError):
+        qk.cache_evict(cache, 10, 11)
+    with pytest.raises(qk.QKVPError):
+        qk.cache_evict(cache, 1000, 0)
+    for name in ("k", "v", "table", "lengths", "pos", "weight"):
+        good = getattr(cache, name)
+        setattr(cache, name, good.double())
+        with pytest.raises(ValueError):
+            qk.decode_attention(q, cache)
+        setattr(cache, name, good)
