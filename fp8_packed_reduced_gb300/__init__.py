@@ -646,6 +646,16 @@ def mlp_backward(dout, W1_8T, w1_scale, W2_8T, w2_scale, saved, ws=None, out=Non
 # Serving: paged key-value cache, attention of one new token, eviction
 # ----------------------------------------------------------------------------
 
+def _quick_cuda(t, name: str, dtype, shape):
+    """_need_cuda in as few steps as a call per token can afford."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need_cuda(t, name, dtype, shape)
+
+
 @dataclass
 class KVCache:
     """A paged cache of the forward's k and v for B sequences.
@@ -668,28 +678,31 @@ class KVCache:
 
     def desc(self) -> CacheDesc:
         """The checked C descriptor of the tensors as they are now."""
-        k, v, table, lengths = self.k, self.v, self.table, self.lengths
+        k, v, table, lengths, weight, pos = self.k, self.v, self.table, self.lengths, self.weight, self.pos
         fp8 = k.dtype == torch.uint8
-        _need_cuda(k, "cache k", torch.uint8 if fp8 else torch.bfloat16)
         if k.dim() != 4 or v.dim() != 4 or table.dim() != 2:
             raise ValueError("cache k and v must be [P, H, page, d], table [B, max_pages]")
         P, H, page, d = k.shape
         B, max_pages = table.shape
-        _need_cuda(v, "cache v", k.dtype, (P, H, page, v.shape[3]))
-        _need_cuda(table, "cache table", torch.int32)
-        _need_cuda(lengths, "cache lengths", torch.int32, (B,))
+        d_v = v.shape[3]
         rows = (P, H, page)
+        _quick_cuda(k, "cache k", torch.uint8 if fp8 else torch.bfloat16, (P, H, page, d))
+        _quick_cuda(v, "cache v", k.dtype, (P, H, page, d_v))
+        _quick_cuda(table, "cache table", torch.int32, (B, max_pages))
+        _quick_cuda(lengths, "cache lengths", torch.int32, (B,))
+        ks = vs = 0
         if fp8:
-            _need_cuda(self.k_scale, "cache k_scale", torch.float32, rows)
-            _need_cuda(self.v_scale, "cache v_scale", torch.float32, rows)
-        if self.weight is not None:
-            _need_cuda(self.weight, "cache weight", torch.float32, rows)
-        if self.pos is not None:
-            _need_cuda(self.pos, "cache pos", torch.int32, rows)
-        addr = lambda t: 0 if t is None else t.data_ptr()   # noqa: E731
-        return CacheDesc(P, page, H, d, v.shape[3], B, max_pages, int(fp8), k.data_ptr(), v.data_ptr(),
-                         addr(self.k_scale) if fp8 else 0, addr(self.v_scale) if fp8 else 0, addr(self.weight),
-                         addr(self.pos), table.data_ptr(), lengths.data_ptr())
+            _quick_cuda(self.k_scale, "cache k_scale", torch.float32, rows)
+            _quick_cuda(self.v_scale, "cache v_scale", torch.float32, rows)
+            ks, vs = self.k_scale.data_ptr(), self.v_scale.data_ptr()
+        if weight is not None:
+            _quick_cuda(weight, "cache weight", torch.float32, rows)
+            weight = weight.data_ptr()
+        if pos is not None:
+            _quick_cuda(pos, "cache pos", torch.int32, rows)
+            pos = pos.data_ptr()
+        return CacheDesc(P, page, H, d, d_v, B, max_pages, fp8, k.data_ptr(), v.data_ptr(), ks, vs, weight, pos,
+                         table.data_ptr(), lengths.data_ptr())
 
 
 def new_cache(B: int, max_tokens: int, H: int, d_qk: int = 96, d_v: int = 128, page: int = 64, fp8: bool = False,
@@ -731,21 +744,31 @@ def new_cache_workspace(cache: KVCache, Hq: int, accumulate: bool = True, budget
 _cache_scratch = {}
 
 
-def _cache_ws(ws, dev, stream, nbytes: int, where: str) -> torch.Tensor:
+def _cache_call(where: str, dev, ws, nbytes, *args):
+    """Calls the entry point ``where`` with args, workspace and stream;
+    ``nbytes()`` is the workspace it needs."""
+    call = getattr(lib(), where)
+    stream = torch.cuda.current_stream(dev).cuda_stream
     if ws is not None:
         _need_cuda(ws, "ws", torch.uint8)
-        return ws
-    if nbytes == 0:
-        raise QKVPError(ERR_UNSUPPORTED, where)
+        _check(call(*args, ws.data_ptr(), ws.numel(), stream), where)
+        return
     if torch.cuda.is_current_stream_capturing():
         raise ValueError("a captured call needs its own workspace: pass ws=new_cache_workspace(...)")
-    key = (dev.index, stream.value)
-    got = _cache_scratch.get(key)
-    if got is None or got.numel() < nbytes:
-        got = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(lib().qkvp_workspace_init(_ptr(got), nbytes, stream), "qkvp_workspace_init")
-        _cache_scratch[key] = got
-    return got
+    key = (dev.index, stream)
+    ws = _cache_scratch.get(key)
+    code = ERR_WORKSPACE_TOO_SMALL
+    if ws is not None:
+        code = call(*args, ws.data_ptr(), ws.numel(), stream)
+    if code == ERR_WORKSPACE_TOO_SMALL:   # refused before any launch
+        n = int(nbytes())
+        if n == 0:
+            raise QKVPError(ERR_UNSUPPORTED, where)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(lib().qkvp_workspace_init(ws.data_ptr(), n, stream), "qkvp_workspace_init")
+        code = call(*args, ws.data_ptr(), n, stream)
+        _cache_scratch[key] = ws
+    _check(code, where)
 
 
 def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
@@ -754,24 +777,20 @@ def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
     belong to sequence b; without cu there is one row per sequence.  The
     lengths grow in place, or go to lengths_out.  Returns the new lengths."""
     d = cache.desc()
-    dev = k.device
     if k.dim() != 3:
         raise ValueError("k must be [H, T, d_qk]")
     T = k.shape[1]
-    _need_cuda(k, "k", torch.bfloat16, (d.H, T, d.d_qk))
-    _need_cuda(v, "v", torch.bfloat16, (d.H, T, d.d_v))
-    _need_cuda(pos, "pos", torch.int32, (T,))
+    _quick_cuda(k, "k", torch.bfloat16, (d.H, T, d.d_qk))
+    _quick_cuda(v, "v", torch.bfloat16, (d.H, T, d.d_v))
+    _quick_cuda(pos, "pos", torch.int32, (T,))
     if cu is not None:
-        _need_cuda(cu, "cu", torch.int32, (d.B + 1,))
+        _quick_cuda(cu, "cu", torch.int32, (d.B + 1,))
     if lengths_out is None:
         lengths_out = cache.lengths
     else:
-        _need_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
-    stream = _stream(dev)
-    L = lib()
-    ws = _cache_ws(ws, dev, stream, L.qkvp_cache_append_workspace_bytes(ctypes.byref(d)), "qkvp_cache_append")
-    _check(L.qkvp_cache_append(ctypes.byref(d), T, _ptr(k), _ptr(v), _ptr(pos), _ptr(cu), _ptr(lengths_out), _ptr(ws),
-                               ws.numel(), stream), "qkvp_cache_append")
+        _quick_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
+    _cache_call("qkvp_cache_append", k.device, ws, lambda: lib().qkvp_cache_append_workspace_bytes(d), d, T, k.data_ptr(),
+                v.data_ptr(), pos.data_ptr(), None if cu is None else cu.data_ptr(), lengths_out.data_ptr())
     return lengths_out
 
 
@@ -785,22 +804,20 @@ def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, o
     dev = q.device
     if q.dim() != 3:
         raise ValueError("q must be [Hq, B, d_qk]")
-    Hq = q.shape[0]
-    _need_cuda(q, "q", torch.bfloat16, (Hq, d.B, d.d_qk))
+    Hq, B, d_qk = q.shape
+    _quick_cuda(q, "q", torch.bfloat16, (Hq, d.B, d.d_qk))
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs cache.weight")
     if out is None:
-        out = (torch.empty((d.B, Hq * d.d_v), dtype=torch.bfloat16, device=dev),
-               torch.empty((d.B, Hq), dtype=torch.float32, device=dev))
-    a, lse = out
-    _need_cuda(a, "a", torch.bfloat16, (d.B, Hq * d.d_v))
-    _need_cuda(lse, "lse", torch.float32, (d.B, Hq))
-    stream = _stream(dev)
-    L = lib()
-    ws = _cache_ws(ws, dev, stream, L.qkvp_decode_attention_workspace_bytes(ctypes.byref(d), Hq, int(accumulate)),
-                   "qkvp_decode_attention")
-    _check(L.qkvp_decode_attention(ctypes.byref(d), Hq, d.d_qk ** -0.5 if scale is None else scale, _ptr(q), _ptr(a),
-                                   _ptr(lse), int(accumulate), _ptr(ws), ws.numel(), stream), "qkvp_decode_attention")
+        a = torch.empty((B, Hq * d.d_v), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    else:
+        a, lse = out
+        _quick_cuda(a, "a", torch.bfloat16, (B, Hq * d.d_v))
+        _quick_cuda(lse, "lse", torch.float32, (B, Hq))
+    _cache_call("qkvp_decode_attention", dev, ws,
+                lambda: lib().qkvp_decode_attention_workspace_bytes(d, Hq, int(accumulate)), d, Hq,
+                d_qk ** -0.5 if scale is None else scale, q.data_ptr(), a.data_ptr(), lse.data_ptr(), accumulate)
     return a, lse
 
 
@@ -818,12 +835,13 @@ def cache_evict(cache: KVCache, budget: int, recent: int, lengths_out=None, ws=N
     if lengths_out is None:
         lengths_out = cache.lengths
     else:
-        _need_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
-    slots = torch.empty((d.B, d.H, max(budget, 1)), dtype=torch.int32, device=dev) if out is None else out
-    _need_cuda(slots, "slots", torch.int32, (d.B, d.H, max(budget, 1)))
-    stream = _stream(dev)
-    L = lib()
-    ws = _cache_ws(ws, dev, stream, L.qkvp_cache_evict_workspace_bytes(ctypes.byref(d), budget), "qkvp_cache_evict")
-    _check(L.qkvp_cache_evict(ctypes.byref(d), budget, recent, _ptr(slots), _ptr(lengths_out), _ptr(ws), ws.numel(),
-                              stream), "qkvp_cache_evict")
-    return slots
+        _quick_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
+    if not 0 < budget <= d.max_pages * d.page:
+        raise QKVPError(ERR_INVALID_ARGUMENT, "qkvp_cache_evict")
+    if out is None:
+        out = torch.empty((d.B, d.H, budget), dtype=torch.int32, device=dev)
+    else:
+        _quick_cuda(out, "slots", torch.int32, (d.B, d.H, budget))
+    _cache_call("qkvp_cache_evict", dev, ws, lambda: lib().qkvp_cache_evict_workspace_bytes(d, budget), d, budget, recent,
+                out.data_ptr(), lengths_out.data_ptr())
+    return out

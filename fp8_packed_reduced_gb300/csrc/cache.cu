@@ -19,6 +19,7 @@ int check_cache(const qkvp_cache* c, CacheArgs* a) {
   if (c->P > (1 << 26) || c->H > 128 || c->B > kMaxSeqs) return QKVP_ERR_UNSUPPORTED;
   if (c->page < 16 || c->page > kMaxPage || (c->page & (c->page - 1))) return QKVP_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->max_pages) * c->page > (1 << 24)) return QKVP_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->max_pages) * c->page * c->B > (int64_t(1) << 34)) return QKVP_ERR_UNSUPPORTED;
   if (c->d_qk != 64 && c->d_qk != 96 && c->d_qk != 128) return QKVP_ERR_UNSUPPORTED;
   if (c->d_v != kDv) return QKVP_ERR_UNSUPPORTED;
   if (!c->k || !c->v || !c->table || !c->lengths) return QKVP_ERR_INVALID_ARGUMENT;

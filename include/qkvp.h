@@ -424,7 +424,8 @@ typedef struct qkvp_cache {
     int d_qk;         /* key width: 64, 96 or 128                                 */
     int d_v;          /* value width: 128                                         */
     int B;            /* sequences, 1 .. 4096                                     */
-    int max_pages;    /* page-table entries per sequence; * page <= 2^24          */
+    int max_pages;    /* page-table entries per sequence; * page <= 2^24, and
+                       * B * max_pages * page <= 2^34                             */
     int fp8;          /* 0: k, v bf16; 1: E4M3 codes, one scale per row           */
     void* k;          /* [P, H, page, d_qk] uint16_t or uint8_t                   */
     void* v;          /* [P, H, page, d_v]                                        */
