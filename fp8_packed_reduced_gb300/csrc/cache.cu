@@ -16,10 +16,12 @@ int check_cache(const qkvp_cache* c, CacheArgs* a) {
   if (c->P < 1 || c->page < 1 || c->H < 1 || c->d_qk < 1 || c->d_v < 1 || c->B < 1 || c->max_pages < 1)
     return QKVP_ERR_INVALID_ARGUMENT;
   if (c->fp8 != 0 && c->fp8 != 1) return QKVP_ERR_INVALID_ARGUMENT;
-  if (c->P > (1 << 26) || c->H > 128 || c->B > kMaxSeqs) return QKVP_ERR_UNSUPPORTED;
+  if (c->H > 128 || c->B > kMaxSeqs) return QKVP_ERR_UNSUPPORTED;
   if (c->page < 16 || c->page > kMaxPage || (c->page & (c->page - 1))) return QKVP_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->max_pages) * c->page > (1 << 24)) return QKVP_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->max_pages) * c->page * c->B > (int64_t(1) << 34)) return QKVP_ERR_UNSUPPORTED;
+  // rows are counted in 32 bits (2^31 of the smallest rows are 412 GB)
+  if (static_cast<int64_t>(c->P) * c->H * c->page > (int64_t(1) << 31) - 1) return QKVP_ERR_UNSUPPORTED;
   if (c->d_qk != 64 && c->d_qk != 96 && c->d_qk != 128) return QKVP_ERR_UNSUPPORTED;
   if (c->d_v != kDv) return QKVP_ERR_UNSUPPORTED;
   if (!c->k || !c->v || !c->table || !c->lengths) return QKVP_ERR_INVALID_ARGUMENT;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kSelectThreads)
   // the newest position
   int newest = INT_MIN;
   for (int i = threadIdx.x; i < n; i += kSelectThreads) {
-    const int64_t row = cache_row(c, b, h, i, st, KID_EVICT_SELECT);
+    const int row = cache_row(c, b, h, i, st, KID_EVICT_SELECT);
     if (row >= 0) newest = max(newest, c.pos[row]);
   }
   newest = __reduce_max_sync(0xffffffffu, newest);
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kSelectThreads)
   const int64_t above = static_cast<int64_t>(newest) - recent;
   // slots in a page outside the pool have the lowest key
   const auto key_of = [&](int i) {
-    const int64_t row = cache_row(c, b, h, i, st, KID_EVICT_SELECT);
+    const int row = cache_row(c, b, h, i, st, KID_EVICT_SELECT);
     return row < 0 ? 0u : evict_key(c.weight[row], c.pos[row], above);
   };
 

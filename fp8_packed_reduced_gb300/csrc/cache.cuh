@@ -47,13 +47,13 @@ __device__ __forceinline__ int checked_length(const CacheArgs& c, int b, const D
 // Row (of the pools seen as [P * H * page, ...]) of slot `slot` of sequence
 // b, head h; -1, recorded, when its page lies outside the pool.  The caller
 // has checked 0 <= slot < capacity.
-__device__ __forceinline__ int64_t cache_row(const CacheArgs& c, int b, int h, int slot, const DevStatus& st, int kid) {
+__device__ __forceinline__ int cache_row(const CacheArgs& c, int b, int h, int slot, const DevStatus& st, int kid) {
   const int pid = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + (slot >> c.page_shift));
   if (pid < 0 || pid >= c.P) {
     record_error(st, QKVP_ERR_DEVICE_INPUT, kid);
     return -1;
   }
-  return ((static_cast<int64_t>(pid) * c.H + h) << c.page_shift) + (slot & (c.page() - 1));
+  return ((pid * c.H + h) << c.page_shift) + (slot & (c.page() - 1));   // below 2^31: checked on the host
 }
 
 // Host: QKVP_OK or the status an entry point returns for `c`; fills `a`.

@@ -29,7 +29,9 @@
 // O); pieces inside one block are joined by a warp of it, pieces across blocks
 // by the block that arrives last, in the order of the slots: the result does
 // not depend on the order of arrival.
+#include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 
 #include "cache.cuh"
@@ -49,22 +51,27 @@ struct DecodeParams {
   CacheArgs c;
   int G;                 // query heads per K/V head
   int chunks, nh;        // the G heads are taken in `chunks` parts of at most nh
+  int smem_records;      // the warps' records fit into shared memory
   float scale_log2;      // scale * log2(e)
   const uint16_t* q;     // [H * G, B, d]
   uint16_t* a;           // [B, H * G, 128]
   float* lse;            // [B, H * G] natural logarithm, or null
   float* lse2;           // [B, H * G] base 2
   float* scores;         // [B, H * G, capacity] base 2, or null
-  float* records;        // [2 * warps] of record_floats(nh)
+  float* records;        // [2 * blocks] records of blocks, then [warps] of warps (unless smem_records)
   unsigned int* arrived; // [B * H * chunks] blocks that have left their records, zero between calls
 };
 
+// A record: O [nh][128] relative to 2^mo, then m [nh], l [nh], mo [nh].
 __host__ __device__ constexpr int record_floats(int nh) { return nh * (kDv + 4); }
 
 // ---------------------------------------------------------------------------
 // PTX
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -111,17 +118,29 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t lo16) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(lo16 & 0xFFFFu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// The four E4M3 codes of a word as f16, exactly: bytes 0 and 1, bytes 2 and 3.
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// exp2(x - m) with the weight of a score of -inf zero, also where m is -inf
-__device__ __forceinline__ float exp2_below(float x, float m) { return exp2f(x - (m == -INFINITY ? 0.f : m)); }
+// 2^x to 2^-22 relative; results below the normal numbers are zero.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// What scores are taken relative to: their maximum m, or 0 where all are -inf
+// (so that each of them has the weight 2^-inf = 0).
+__device__ __forceinline__ float below(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ float exp2_below(float x, float m) { return ex2(x - below(m)); }
 
 // ---------------------------------------------------------------------------
 // Shapes of a unit and of a stage
@@ -136,7 +155,7 @@ struct Tile {
   static constexpr int K_BYTES = KS * D * ES;
   static constexpr int V_BYTES = KS * kDv * ES;
   static constexpr int SCALE_BYTES = FP8 ? 2 * KS * 4 : 0;
-  static constexpr int META_BYTES = 32;
+  static constexpr int META_BYTES = 16;
   __host__ __device__ static constexpr int stage_bytes(int nh) {
     return K_BYTES + V_BYTES + SCALE_BYTES + META_BYTES + nh * D * 2;
   }
@@ -154,19 +173,44 @@ struct Tile {
 };
 
 struct Unit {
-  int64_t row[2];   // pool row of each half's first slot, -1: none
+  int row[2];       // pool row of each half's first slot, -1: none
   int b, hv, u;     // sequence, head x chunk, unit of the sequence
   int valid;        // live slots
 };
 
-// The list of units: sequence b holds units[b] per (head, chunk), prefix[b]
-// of them come before it.
+// The list of units: sequence b holds as many per (head, chunk) as lie
+// between prefix[b] and prefix[b + 1].
 struct Plan {
   const int* prefix;   // [B + 1]
   const int* length;   // [B]
   int B, Hv;
-  int64_t total, part; // units, units per warp
 };
+
+// A (sequence, head, chunk) as a piece of the list.
+struct Piece {
+  int64_t start, end;
+  int b, hv;
+};
+__device__ __forceinline__ Piece piece_of(const Plan& pl, int64_t f) {
+  int lo = 0, hi = pl.B;   // prefix[lo] * Hv <= f < prefix[hi] * Hv
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(pl.prefix[mid]) * pl.Hv <= f)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int per = pl.prefix[lo + 1] - pl.prefix[lo];
+  const int64_t base = static_cast<int64_t>(pl.prefix[lo]) * pl.Hv, rest = f - base;
+  Piece r;
+  r.b = lo;
+  // (a 64-bit division is several times as long)
+  r.hv = rest <= INT_MAX ? static_cast<int>(static_cast<unsigned int>(rest) / static_cast<unsigned int>(per))
+                         : static_cast<int>(rest / per);
+  r.start = base + static_cast<int64_t>(r.hv) * per;
+  r.end = r.start + per;
+  return r;
+}
 
 // Exclusive prefix over the block of one value per thread.
 __device__ __forceinline__ int block_exclusive(int v, int* red, int* total) {
@@ -192,25 +236,16 @@ __device__ __forceinline__ int block_exclusive(int v, int* red, int* total) {
 
 template <class TL>
 __device__ __forceinline__ Unit locate(const Plan& pl, const DecodeParams& p, int64_t f, const DevStatus& st) {
-  int lo = 0, hi = pl.B;   // prefix[lo] * Hv <= f < prefix[hi] * Hv
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(pl.prefix[mid]) * pl.Hv <= f)
-      lo = mid;
-    else
-      hi = mid;
-  }
+  const Piece pc = piece_of(pl, f);
   Unit r;
-  r.b = lo;
-  const int per = pl.prefix[lo + 1] - pl.prefix[lo];
-  const int64_t rest = f - static_cast<int64_t>(pl.prefix[lo]) * pl.Hv;
-  r.hv = static_cast<int>(rest / per);
-  r.u = static_cast<int>(rest - static_cast<int64_t>(r.hv) * per);
-  r.valid = min(TL::KS, pl.length[lo] - r.u * TL::KS);
+  r.b = pc.b;
+  r.hv = pc.hv;
+  r.u = static_cast<int>(f - pc.start);
+  r.valid = min(TL::KS, pl.length[r.b] - r.u * TL::KS);
   const int h = r.hv / p.chunks;
 #pragma unroll
   for (int s = 0; s < 2; ++s)
-    r.row[s] = s < TL::SUB && 16 * s < r.valid ? cache_row(p.c, lo, h, r.u * TL::KS + 16 * s, st, KID_DECODE) : -1;
+    r.row[s] = s < TL::SUB && 16 * s < r.valid ? cache_row(p.c, r.b, h, r.u * TL::KS + 16 * s, st, KID_DECODE) : -1;
   return r;
 }
 
@@ -234,70 +269,98 @@ __device__ __forceinline__ void write_head(const DecodeParams& p, int b, int hq,
   }
 }
 
-// Joins, for head n, the records of warps w0, w0 + step, .. <= w1 of one
-// (sequence, head): the first warp of the whole piece, `first`, holds it in
-// its second record, the others in their first.
-__device__ __forceinline__ void join_records(const DecodeParams& p, int n, int first, int w0, int w1, int step, float& m,
-                                             float& l, float& mo, float4& o) {
-  const int lane = threadIdx.x & 31, rs = record_floats(p.nh);
-  const auto rec = [&](int w) { return p.records + static_cast<int64_t>(2 * w + (w == first)) * rs; };
-  m = mo = -INFINITY;
-  for (int w = w0 + step * lane; w <= w1; w += 32 * step) {
-    m = fmaxf(m, __ldcg(rec(w) + p.nh * kDv + n));
-    mo = fmaxf(mo, __ldcg(rec(w) + p.nh * (kDv + 2) + n));
+// A running join of records for one head: m, l and four columns of O per lane.
+struct Joined {
+  float m, l, mo;
+  float4 o;
+  __device__ void clear() {
+    m = mo = -INFINITY;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, s));
+  __device__ void add(float rm, float rl, float rmo, float4 x) {
+    const float m1 = fmaxf(m, rm), mo1 = fmaxf(mo, rmo);
+    const float f = exp2_below(m, m1), g = exp2_below(rm, m1), fo = exp2_below(mo, mo1), go = exp2_below(rmo, mo1);
+    l = l * f + rl * g;
+    o.x = o.x * fo + x.x * go;
+    o.y = o.y * fo + x.y * go;
+    o.z = o.z * fo + x.z * go;
+    o.w = o.w * fo + x.w * go;
+    m = m1;
+    mo = mo1;
   }
-  l = 0.f;
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int w = w0; w <= w1; w += step) {
-    const float* r = rec(w);
-    l += exp2_below(__ldcg(r + p.nh * kDv + n), m) * __ldcg(r + p.nh * (kDv + 1) + n);
-    const float f = exp2_below(__ldcg(r + p.nh * (kDv + 2) + n), mo);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(r + n * kDv) + lane);
-    o.x += f * x.x;
-    o.y += f * x.y;
-    o.z += f * x.z;
-    o.w += f * x.w;
+  __device__ void add_record(const float* r, int n, int nh) {
+    const int lane = threadIdx.x & 31;
+    add(r[nh * kDv + n], r[nh * (kDv + 1) + n], r[nh * (kDv + 2) + n], reinterpret_cast<const float4*>(r + n * kDv)[lane]);
   }
-}
+  __device__ void store(float* r, int n, int nh) const {
+    const int lane = threadIdx.x & 31;
+    reinterpret_cast<float4*>(r + n * kDv)[lane] = o;
+    if (lane == 0) {
+      r[nh * kDv + n] = m;
+      r[nh * (kDv + 1) + n] = l;
+      r[nh * (kDv + 2) + n] = mo;
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
-// The kernel
+// The kernel.  E query heads per lane and tile of eight columns: two, or with
+// at most four heads one, on the even columns (half the work between the two
+// products).
 // ---------------------------------------------------------------------------
-template <int D, bool FP8, int NT, int S>
+template <int D, bool FP8, int NT, int E, int S>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
   using TL = Tile<D, FP8>;
+  constexpr int SUB = TL::SUB, KS = TL::KS;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int red[kWarps];
+  __shared__ int red[kWarps], red_max[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int B = p.c.B, Hq = p.c.H * p.G;
+  const int B = p.c.B, Hq = p.c.H * p.G, nrec = record_floats(p.nh);
+  const auto head_of = [&](int t, int e) { return E == 1 ? c : 8 * t + 2 * c + e; };   // of this lane's scores
 
   // --- the list of units -------------------------------------------------
   int* prefix = reinterpret_cast<int*>(smem);
   int* length = prefix + B + 1;
-  int run = 0;
+  int run = 0, longest = 0;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
     const int n = b < B ? checked_length(p.c, b, st, KID_DECODE) : 0;
     int sum;
-    const int before = block_exclusive((n + TL::KS - 1) / TL::KS, red, &sum);
+    const int before = block_exclusive((n + KS - 1) / KS, red, &sum);
     if (b < B) {
       prefix[b] = run + before;
       length[b] = n;
     }
     run += sum;
+    longest = max(longest, __reduce_max_sync(0xffffffffu, n));
   }
   if (threadIdx.x == 0) prefix[B] = run;
+  if (lane == 0) red_max[warp] = longest;
   __syncthreads();
-  Plan pl{prefix, length, B, p.c.H * p.chunks, 0, 0};
-  pl.total = static_cast<int64_t>(run) * pl.Hv;
+  const Plan pl{prefix, length, B, p.c.H * p.chunks};
+  const int64_t total = static_cast<int64_t>(run) * pl.Hv;
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  pl.part = (pl.total + nwarps - 1) / nwarps;
+  // Even parts, [c0, c1) for the block.  But where a block for every piece
+  // makes no warp's part longer by more than a few units, it has one: nothing
+  // is then joined across blocks, which costs about as much as four units
+  // (3 us against 0.7 each).
+  int64_t part = (total + nwarps - 1) / nwarps;
+  int64_t c0 = min(total, blockIdx.x * kWarps * part), c1 = min(total, c0 + kWarps * part);
+  if (static_cast<int64_t>(B) * pl.Hv <= gridDim.x) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) longest = max(longest, red_max[w]);
+    if ((longest + kWarps * KS - 1) / (kWarps * KS) <= part + 4) {
+      const int b = blockIdx.x / pl.Hv, hv = blockIdx.x % pl.Hv;
+      c0 = c1 = 0;
+      if (b < B) {
+        const int per = prefix[b + 1] - prefix[b];
+        c0 = static_cast<int64_t>(prefix[b]) * pl.Hv + static_cast<int64_t>(hv) * per;
+        c1 = c0 + per;
+        part = max(1, (per + kWarps - 1) / kWarps);
+      }
+    }
+  }
 
   // sequences without a live slot
   for (int b = blockIdx.x; b < B; b += gridDim.x)
@@ -306,103 +369,120 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         reinterpret_cast<uint4*>(p.a)[static_cast<int64_t>(b) * Hq * (kDv / 8) + i] = make_uint4(0, 0, 0, 0);
       for (int i = threadIdx.x; p.lse && i < Hq; i += kThreads) p.lse[static_cast<int64_t>(b) * Hq + i] = -INFINITY;
     }
+  if (c0 >= c1) return;
 
   // --- the warp's part ----------------------------------------------------
-  const int wid = blockIdx.x * kWarps + warp;
-  const int64_t f0 = min(pl.total, wid * pl.part), f1 = min(pl.total, f0 + pl.part);
+  const int64_t f0 = min(c1, c0 + warp * part), f1 = min(c1, f0 + part);
+  const int count = static_cast<int>(f1 - f0);
   const int stage_bytes = TL::stage_bytes(p.nh);
-  uint8_t* ring = smem + ((2 * B + 1) * 4 + 127) / 128 * 128 + warp * S * stage_bytes;
+  uint8_t* rings = smem + ((2 * B + 1) * 4 + 127) / 128 * 128;
+  uint8_t* ring = rings + warp * S * stage_bytes;
   const uint32_t ring_u32 = smem_u32(ring);
+  // Records of the warps: of a piece begun in an earlier part, here; of one
+  // begun in its own and not ended there, in the warp's ring once it is empty.
+  float* begun_before = p.smem_records ? reinterpret_cast<float*>(rings + kWarps * S * stage_bytes)
+                                       : p.records + (2 * gridDim.x + static_cast<int64_t>(blockIdx.x) * kWarps) * nrec;
+  const auto begun_here = [&](int w) { return reinterpret_cast<float*>(rings + w * S * stage_bytes); };
 
-  Unit mine;             // lane i: unit batch + i
-  int64_t batch = f0 - 32;
-  int prev_hv = -1, prev_b = -1;   // of the unit issued last
-  const auto issue = [&](int64_t f) {
-    if (f < f1) {
+  // places of the lane's chunks of 16 slots
+  int koff[TL::KC / 2], voff[TL::VC / 2];
+#pragma unroll
+  for (int i = 0; i < TL::KC / 2; ++i) koff[i] = TL::k_at((i * 32 + lane) / TL::KC, (i * 32 + lane) % TL::KC);
+#pragma unroll
+  for (int i = 0; i < TL::VC / 2; ++i)
+    voff[i] = TL::K_BYTES + TL::v_at((i * 32 + lane) / TL::VC, (i * 32 + lane) % TL::VC);
+
+  Unit mine{};           // lane i: unit batch + i of the part
+  int batch = -32, to = 0;   // the stage to fill
+  const auto issue = [&](int f) {
+    if (f < count) {
       if (f - batch >= 32) {
         batch = f;
-        if (batch + lane < f1) mine = locate<TL>(pl, p, batch + lane, st);
+        if (batch + lane < count) mine = locate<TL>(pl, p, f0 + batch + lane, st);
       }
-      const int who = static_cast<int>(f - batch);
-      const int stage = static_cast<int>((f - f0) % S);
-      const uint32_t s0 = ring_u32 + stage * stage_bytes;
-      const int b = __shfl_sync(0xffffffffu, mine.b, who), hv = __shfl_sync(0xffffffffu, mine.hv, who);
+      const int who = f - batch;
+      const uint32_t s0 = ring_u32 + to * stage_bytes;
       const int valid = __shfl_sync(0xffffffffu, mine.valid, who);
+      const bool first = f == 0 || __shfl_sync(0xffffffffu, mine.u, who) == 0;
 #pragma unroll
-      for (int s = 0; s < TL::SUB; ++s) {
-        const int64_t row = __shfl_sync(0xffffffffu, mine.row[s], who);
-        const uint8_t* ks = p.c.k + (row < 0 ? 0 : row) * (D * TL::ES);
-        const uint8_t* vs = p.c.v + (row < 0 ? 0 : row) * (kDv * TL::ES);
+      for (int s = 0; s < SUB; ++s) {
+        const int row = __shfl_sync(0xffffffffu, mine.row[s], who);
         const int live = row < 0 ? 0 : valid - 16 * s;   // live rows of this half
+        const int64_t at = row < 0 ? 0 : row;
+        const uint8_t* ks = p.c.k + at * (D * TL::ES) + lane * 16;
+        const uint8_t* vs = p.c.v + at * (kDv * TL::ES) + lane * 16;
+        const uint32_t dk = s0 + s * (16 * D * TL::ES), dv = s0 + s * (16 * kDv * TL::ES);
+        if (live >= 16) {
 #pragma unroll
-        for (int i = 0; i < TL::KC / 2; ++i) {
-          const int id = i * 32 + lane, r = id / TL::KC, ch = id % TL::KC;
-          cp16(s0 + TL::k_at(16 * s + r, ch), ks + id * 16, r < live);
-        }
+          for (int i = 0; i < TL::KC / 2; ++i) cp16(dk + koff[i], ks + i * 512);
 #pragma unroll
-        for (int i = 0; i < TL::VC / 2; ++i) {
-          const int id = i * 32 + lane, r = id / TL::VC, ch = id % TL::VC;
-          cp16(s0 + TL::K_BYTES + TL::v_at(16 * s + r, ch), vs + id * 16, r < live);
+          for (int i = 0; i < TL::VC / 2; ++i) cp16(dv + voff[i], vs + i * 512);
+        } else {   // what is not live reads as zero: 0 * NaN would be NaN
+#pragma unroll
+          for (int i = 0; i < TL::KC / 2; ++i) cp16_or_zero(dk + koff[i], ks + i * 512, (i * 32 + lane) / TL::KC < live);
+#pragma unroll
+          for (int i = 0; i < TL::VC / 2; ++i) cp16_or_zero(dv + voff[i], vs + i * 512, (i * 32 + lane) / TL::VC < live);
         }
         if (FP8 && lane < 8) {   // 16 scales of k, then of v
-          const float* sc = (lane < 4 ? p.c.k_scale : p.c.v_scale) + (row < 0 ? 0 : row) + (lane & 3) * 4;
-          cp16(s0 + TL::K_BYTES + TL::V_BYTES + (lane < 4 ? 0 : TL::KS * 4) + 64 * s + (lane & 3) * 16, sc, live > 0);
+          const float* sc = (lane < 4 ? p.c.k_scale : p.c.v_scale) + at + (lane & 3) * 4;
+          cp16_or_zero(s0 + TL::K_BYTES + TL::V_BYTES + (lane < 4 ? 0 : KS * 4) + 64 * s + (lane & 3) * 16, sc, live > 0);
         }
       }
-      if (hv != prev_hv || b != prev_b) {   // q comes with the first unit of a (sequence, head)
-        prev_hv = hv;
-        prev_b = b;
+      if (first) {   // q comes with a piece's first unit
+        const int b = __shfl_sync(0xffffffffu, mine.b, who), hv = __shfl_sync(0xffffffffu, mine.hv, who);
         const int h = hv / p.chunks, ch0 = (hv % p.chunks) * p.nh, nh = min(p.nh, p.G - ch0);
         constexpr int QC = D / 8;
         for (int i = lane; i < nh * QC; i += 32)
           cp16(s0 + TL::K_BYTES + TL::V_BYTES + TL::SCALE_BYTES + TL::META_BYTES + i * 16,
-               p.q + (static_cast<int64_t>(h * p.G + ch0 + i / QC) * B + b) * D + (i % QC) * 8, true);
+               p.q + (static_cast<int64_t>(h * p.G + ch0 + i / QC) * B + b) * D + (i % QC) * 8);
       }
       if (lane == who) {
-        int* meta = reinterpret_cast<int*>(ring + stage * stage_bytes + TL::K_BYTES + TL::V_BYTES + TL::SCALE_BYTES);
-        *reinterpret_cast<int4*>(meta) = make_int4(mine.b, mine.hv, mine.u, mine.valid);
-        *reinterpret_cast<int2*>(meta + 4) = make_int2(mine.row[0] >= 0, mine.row[1] >= 0);
+        const int flags = mine.valid | (first ? 64 : 0) | (mine.row[0] >= 0 ? 128 : 0) | (mine.row[1] >= 0 ? 256 : 0);
+        *reinterpret_cast<int4*>(ring + to * stage_bytes + TL::K_BYTES + TL::V_BYTES + TL::SCALE_BYTES) =
+            make_int4(flags, mine.u, mine.b, mine.hv);
       }
     }
+    to = to + 1 == S ? 0 : to + 1;
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(f0 + i);
+  for (int i = 0; i < S - 1; ++i) issue(i);
 
-  uint4 qf[NT][D / 32];           // q of head 8 t + g: chunk c of every 32 dims
-  float qmul[NT][2];              // score multiplier of heads 8 t + 2 c, + 1
-  float m[NT][2], l[NT][2], mo[NT][2], o[NT][8][4];
+  uint4 qf[NT][D / 32];           // q of column 8 t + g: chunk c of every 32 dims
+  float qmul[NT][E];              // score multipliers
+  float m[NT][E], l[NT][E], mo[NT][E], o[NT][8][4];
+  float* score_at[NT][E];         // where the scores of this lane's heads go, or null
   int cur_b = -1, cur_hv = -1;
   bool from_start = false;        // the piece being read begins with unit 0
 
-  // Leaves the finished piece: the whole (sequence, head) as the result, part
-  // of one as a record.
+  // Leaves the finished piece: the whole of it as the result, part of it as a
+  // record.
   const auto flush = [&](bool to_end) {
     const int h = cur_hv / p.chunks, ch0 = (cur_hv % p.chunks) * p.nh, nh = min(p.nh, p.G - ch0);
-    float* rec = p.records + static_cast<int64_t>(2 * wid + (from_start ? 1 : 0)) * record_floats(p.nh);
+    float* rec = from_start ? begun_here(warp) : begun_before + warp * nrec;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         float x = l[t][e];
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-        const int n = 8 * t + 2 * c + e;
+        const int n = head_of(t, e);
         if (n >= nh) continue;
         if (from_start && to_end) {
           const int64_t at = static_cast<int64_t>(cur_b) * Hq + h * p.G + ch0 + n;
           const bool none = x == 0.f;
           const float f = none ? 0.f : exp2_below(mo[t][e], m[t][e]) / x;
 #pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
+          for (int mt = 0; mt < 8; ++mt) {
+            const uint32_t w = none ? 0u : pack_bf16x2(o[t][mt][e] * f, o[t][mt][2 + e] * f);
             if (FP8) {
-              const uint32_t w = pack_bf16x2(o[t][mt][e] * f, o[t][mt][2 + e] * f);
-              reinterpret_cast<uint32_t*>(p.a + at * kDv)[8 * mt + g] = none ? 0u : w;
+              reinterpret_cast<uint32_t*>(p.a + at * kDv)[8 * mt + g] = w;
             } else {
-              const uint32_t w = pack_bf16x2(o[t][mt][e] * f, o[t][mt][2 + e] * f);
-              p.a[at * kDv + 16 * mt + g] = none ? 0 : static_cast<uint16_t>(w);
-              p.a[at * kDv + 16 * mt + g + 8] = none ? 0 : static_cast<uint16_t>(w >> 16);
+              p.a[at * kDv + 16 * mt + g] = static_cast<uint16_t>(w);
+              p.a[at * kDv + 16 * mt + g + 8] = static_cast<uint16_t>(w >> 16);
             }
+          }
           if (g == 0) {
             const float y = none ? -INFINITY : m[t][e] + log2f(x);
             p.lse2[at] = y;
@@ -426,28 +506,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       }
   };
 
-  for (int64_t f = f0; f < f1; ++f) {
+  int from = 0;   // the stage to read
+  for (int f = 0; f < count; ++f) {
     cp_wait<S - 2>();
     __syncwarp();
     issue(f + S - 1);   // into the stage read in the last round
-    const int stage = static_cast<int>((f - f0) % S);
-    const uint32_t s0 = ring_u32 + stage * stage_bytes;
+    const uint32_t s0 = ring_u32 + from * stage_bytes;
+    from = from + 1 == S ? 0 : from + 1;
     const uint32_t sv = s0 + TL::K_BYTES, ss = sv + TL::V_BYTES, sm = ss + TL::SCALE_BYTES, sq = sm + TL::META_BYTES;
     const uint4 meta = lds128(sm);
-    const uint2 good = lds64(sm + 16);
-    const int b = meta.x, hv = meta.y, u = meta.z, valid = meta.w;
-    if (b != cur_b || hv != cur_hv) {
-      if (cur_b >= 0) flush(true);
-      cur_b = b;
-      cur_hv = hv;
+    const int valid = meta.x & 63, u = meta.y;
+    if (meta.x & 64) {
+      if (f > 0) flush(true);
+      cur_b = meta.z;
+      cur_hv = meta.w;
       from_start = u == 0;
-      const int nh = min(p.nh, p.G - (hv % p.chunks) * p.nh);
+      const int h = cur_hv / p.chunks, ch0 = (cur_hv % p.chunks) * p.nh, nh = min(p.nh, p.G - ch0);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const bool head = 8 * t + g < nh;
+        const int n = E == 1 ? g >> 1 : 8 * t + g;
+        const bool head = n < nh && (E == 2 || (g & 1) == 0);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
-          qf[t][j] = head ? lds128(sq + (8 * t + g) * D * 2 + j * 64 + c * 16) : make_uint4(0, 0, 0, 0);
+          qf[t][j] = head ? lds128(sq + n * D * 2 + j * 64 + c * 16) : make_uint4(0, 0, 0, 0);
         float back = 1.f;   // what the scaled q is multiplied with again
         if (FP8) {
           float am = 0.f;
@@ -472,40 +553,42 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[t][mt][i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
           qmul[t][e] = p.scale_log2 * (FP8 ? __shfl_sync(0xffffffffu, back, 8 * c + 4 * e) : 1.f);
           m[t][e] = mo[t][e] = -INFINITY;
           l[t][e] = 0.f;
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) o[t][mt][e] = o[t][mt][2 + e] = 0.f;
+          const int hn = head_of(t, e);
+          score_at[t][e] = p.scores != nullptr && hn < nh
+                               ? p.scores + (static_cast<int64_t>(cur_b) * Hq + h * p.G + ch0 + hn) * p.c.capacity() + g
+                               : nullptr;
         }
       }
     }
 
-    // scores of slots 16 s + g and + 8, heads 8 t + 2 c and + 1
-    float x[NT][TL::SUB][4];
+    // scores of slots 16 s + g and + 8 (x[..][0, 1] and [2, 3])
+    float x[NT][SUB][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int s = 0; s < TL::SUB; ++s)
+      for (int s = 0; s < SUB; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[t][s][i] = 0.f;
 #pragma unroll
-    for (int s = 0; s < TL::SUB; ++s)
+    for (int j = 0; j < D / 32; ++j)
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
+      for (int s = 0; s < SUB; ++s) {
         uint32_t ka[4], kb[4];   // rows g and g + 8: dims 32 j + 8 c .. + 7
         if (FP8) {
           const uint2 ra = lds64(s0 + TL::k_at(16 * s + g, 2 * j + (c >> 1)) + (c & 1) * 8);
           const uint2 rb = lds64(s0 + TL::k_at(16 * s + g + 8, 2 * j + (c >> 1)) + (c & 1) * 8);
-          ka[0] = e4m3x2_to_f16x2(ra.x);
-          ka[1] = e4m3x2_to_f16x2(ra.x >> 16);
-          ka[2] = e4m3x2_to_f16x2(ra.y);
-          ka[3] = e4m3x2_to_f16x2(ra.y >> 16);
-          kb[0] = e4m3x2_to_f16x2(rb.x);
-          kb[1] = e4m3x2_to_f16x2(rb.x >> 16);
-          kb[2] = e4m3x2_to_f16x2(rb.y);
-          kb[3] = e4m3x2_to_f16x2(rb.y >> 16);
+          const uint2 a0 = e4m3x4_to_f16x4(ra.x), a1 = e4m3x4_to_f16x4(ra.y);
+          const uint2 b0 = e4m3x4_to_f16x4(rb.x), b1 = e4m3x4_to_f16x4(rb.y);
+          ka[0] = a0.x, ka[1] = a0.y, ka[2] = a1.x, ka[3] = a1.y;
+          kb[0] = b0.x, kb[1] = b0.y, kb[2] = b1.x, kb[3] = b1.y;
         } else {
           const uint4 ra = lds128(s0 + TL::k_at(g, 4 * j + c)), rb = lds128(s0 + TL::k_at(g + 8, 4 * j + c));
           ka[0] = ra.x, ka[1] = ra.y, ka[2] = ra.z, ka[3] = ra.w;
@@ -518,45 +601,44 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         }
       }
 
-    uint32_t pb[NT][TL::SUB][2];   // the probabilities as the second product's operand
+    // The row scales: of k into the multiplier, of v as a logarithm (E4M3);
+    // what is not live gets the score -inf.
+    float ks[SUB][2], lv[SUB][2];
+    bool live[SUB][2];
+#pragma unroll
+    for (int s = 0; s < SUB; ++s)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int i = 16 * s + 8 * r + g;
+        live[s][r] = i < valid && (meta.x & (s == 0 ? 128 : 256));
+        if (FP8) {
+          ks[s][r] = lds32(ss + i * 4);
+          lv[s][r] = __log2f(lds32(ss + KS * 4 + i * 4));
+        }
+      }
+
+    uint32_t pb[NT][SUB][2];   // the probabilities as the second product's operand
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float y[TL::SUB][4];   // E4M3: the score plus log2 of v's row scale
-      float top[2] = {-INFINITY, -INFINITY}, otop[2] = {-INFINITY, -INFINITY};
+      float y[SUB][4];   // E4M3: the score plus log2 of v's row scale
+      float top[E], otop[E];
+      bool grows = false;
 #pragma unroll
-      for (int s = 0; s < TL::SUB; ++s)
+      for (int e = 0; e < E; ++e) {
+        top[e] = otop[e] = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int i = 16 * s + 8 * r + g;
-          const bool live = i < valid && (s == 0 ? good.x : good.y) != 0;
-          float ks = 1.f, vs = 0.f;
-          if (FP8) {
-            ks = lds32(ss + i * 4);
-            vs = __log2f(lds32(ss + TL::KS * 4 + i * 4));
-          }
+        for (int s = 0; s < SUB; ++s)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int r = 0; r < 2; ++r) {
             float& v = x[t][s][2 * r + e];
-            v = live ? v * qmul[t][e] * ks : -INFINITY;
+            v = live[s][r] ? v * (FP8 ? qmul[t][e] * ks[s][r] : qmul[t][e]) : -INFINITY;
             top[e] = fmaxf(top[e], v);
             if (FP8) {
-              y[s][2 * r + e] = live ? v + vs : -INFINITY;
+              y[s][2 * r + e] = live[s][r] ? v + lv[s][r] : -INFINITY;
               otop[e] = fmaxf(otop[e], y[s][2 * r + e]);
             }
+            if (score_at[t][e] && 16 * s + 8 * r + g < valid) score_at[t][e][u * KS + 16 * s + 8 * r] = v;
           }
-          if (p.scores != nullptr && i < valid) {
-            const int h = hv / p.chunks, ch0 = (hv % p.chunks) * p.nh;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int n = 8 * t + 2 * c + e;
-              if (n < p.nh && ch0 + n < p.G)
-                p.scores[(static_cast<int64_t>(b) * Hq + h * p.G + ch0 + n) * p.c.capacity() + u * TL::KS + i] =
-                    x[t][s][2 * r + e];
-            }
-          }
-        }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) {
           top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], s));
@@ -564,11 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         }
         top[e] = fmaxf(top[e], m[t][e]);
         otop[e] = FP8 ? fmaxf(otop[e], mo[t][e]) : top[e];
+        grows |= top[e] > m[t][e] || otop[e] > mo[t][e];
       }
-      const bool grows = top[0] > m[t][0] || top[1] > m[t][1] || otop[0] > mo[t][0] || otop[1] > mo[t][1];
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
           l[t][e] *= exp2_below(m[t][e], top[e]);
           const float fo = exp2_below(mo[t][e], otop[e]);
 #pragma unroll
@@ -580,17 +662,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
           mo[t][e] = otop[e];
         }
       }
+      float w[SUB][4];
 #pragma unroll
-      for (int s = 0; s < TL::SUB; ++s) {
-        float w[4];
+      for (int s = 0; s < SUB; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float pr = exp2_below(x[t][s][i], m[t][i & 1]);
-          l[t][i & 1] += pr;
-          w[i] = FP8 ? exp2_below(y[s][i], mo[t][i & 1]) : pr;
+          const int e = i & 1;
+          if (e >= E) {
+            w[s][i] = 0.f;
+            continue;
+          }
+          const float pr = ex2(x[t][s][i] - below(m[t][e]));
+          l[t][e] += pr;
+          w[s][i] = FP8 ? ex2(y[s][i] - below(mo[t][e])) : pr;
         }
-        pb[t][s][0] = movmatrix_trans(FP8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
-        pb[t][s][1] = movmatrix_trans(FP8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
+#pragma unroll
+      for (int s = 0; s < SUB; ++s) {
+        pb[t][s][0] = movmatrix_trans(FP8 ? pack_f16x2(w[s][0], w[s][1]) : pack_bf16x2(w[s][0], w[s][1]));
+        pb[t][s][1] = movmatrix_trans(FP8 ? pack_f16x2(w[s][2], w[s][3]) : pack_bf16x2(w[s][2], w[s][3]));
       }
     }
 
@@ -598,20 +687,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     for (int mt = 0; mt < 8; ++mt) {
       uint32_t r[4];
       if (FP8) {
-        // eight slots x 16 columns each: column pairs 2 g, 2 g + 1 of slots 2 c and 2 c + 1
+        // eight slots x 16 columns each: columns 2 g and 2 g + 1 of slots 2 c and 2 c + 1
         ldmatrix4_trans(r, sv + TL::v_at(lane, mt));
-        uint32_t lo[4], hi[4];
+        uint2 w[4];   // .x column 2 g, .y column 2 g + 1
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = __byte_perm(r[i], 0, 0x3120);
-          lo[i] = e4m3x2_to_f16x2(w);
-          hi[i] = e4m3x2_to_f16x2(w >> 16);
-        }
+        for (int i = 0; i < 4; ++i) w[i] = e4m3x4_to_f16x4(__byte_perm(r[i], 0, 0x3120));
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int s = 0; s < TL::SUB; ++s)
-            mma16816<true>(o[t][mt], lo[2 * s], hi[2 * s], lo[2 * s + 1], hi[2 * s + 1], pb[t][s][0], pb[t][s][1]);
+          for (int s = 0; s < SUB; ++s)
+            mma16816<true>(o[t][mt], w[2 * s].x, w[2 * s].y, w[2 * s + 1].x, w[2 * s + 1].y, pb[t][s][0], pb[t][s][1]);
       } else {
         // slots 0-7 and 8-15, columns 16 mt .. + 7 and + 8 .. + 15
         ldmatrix4_trans(r, sv + TL::v_at((lane & 7) + (lane >> 4) * 8, 2 * mt + ((lane >> 3) & 1)));
@@ -621,123 +706,139 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
   }
   cp_wait<0>();
-  // The last piece of the part: to its end?
-  const auto piece_of = [&](int64_t f, int64_t& start, int64_t& end, int& b, int& hv) {   // the (sequence, head) of unit f
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (static_cast<int64_t>(prefix[mid]) * pl.Hv <= f)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int per = prefix[lo + 1] - prefix[lo];
-    const int64_t base = static_cast<int64_t>(prefix[lo]) * pl.Hv;
-    b = lo;
-    hv = static_cast<int>((f - base) / per);
-    start = base + static_cast<int64_t>(hv) * per;
-    end = start + per;
-  };
-  if (cur_b >= 0) {
-    int64_t s, e;
-    int b, hv;
-    piece_of(f1 - 1, s, e, b, hv);
-    flush(e == f1);
-  }
-  __threadfence();
-  __syncthreads();
+  __syncwarp();   // the ring is read: a record may take its place
 
-  // --- joining ---------------------------------------------------------------
-  const int64_t c0 = min(pl.total, blockIdx.x * kWarps * pl.part), c1 = min(pl.total, c0 + kWarps * pl.part);
-  if (c0 >= c1) return;
-  // pieces that begin in this warp's part, end in another warp's of this block
-  if (f0 < f1) {
-    int64_t s, e;
-    int b, hv;
-    piece_of(f1 - 1, s, e, b, hv);
-    if (s >= f0 && e > f1 && e <= c1) {
-      const int h = hv / p.chunks, ch0 = (hv % p.chunks) * p.nh, nh = min(p.nh, p.G - ch0);
-      const int last = static_cast<int>((e - 1) / pl.part);
-      for (int n = 0; n < nh; ++n) {
-        float jm, jl, jo;
-        float4 x;
-        join_records(p, n, wid, wid, last, 1, jm, jl, jo, x);
-        write_head(p, b, h * p.G + ch0 + n, jm, jl, jo, x);
+  // --- joining ------------------------------------------------------------
+  // The pieces at the block's ends; `mine_last`, the last of the warp's part.
+  const Piece head = piece_of(pl, c0), tail = piece_of(pl, c1 - 1);
+  Piece last_piece = tail;
+  if (count > 0) {
+    last_piece = piece_of(pl, f1 - 1);
+    flush(last_piece.end == f1);
+  }
+  __syncthreads();
+  const int part32 = static_cast<int>(part);   // (a block's parts together are below 2^31 units)
+  const auto warp_of = [&](int64_t f) { return static_cast<int>(f - c0) / part32; };
+  const auto join_warps = [&](const Piece& pc, int n) {   // the records of one piece in this block
+    Joined j;
+    j.clear();
+    const int wa = pc.start <= c0 ? 0 : warp_of(pc.start), wb = warp_of(min(pc.end, c1) - 1);
+    for (int w = wa; w <= wb; ++w)
+      j.add_record(w == wa && pc.start >= c0 ? begun_here(w) : begun_before + w * nrec, n, p.nh);
+    return j;
+  };
+  const auto heads_in = [&](const Piece& pc) { return min(p.nh, p.G - (pc.hv % p.chunks) * p.nh); };
+  const auto head_at = [&](const Piece& pc, int n) { return pc.hv / p.chunks * p.G + (pc.hv % p.chunks) * p.nh + n; };
+
+  // Pieces that reach over the block's ends (one that covers it counts as the
+  // first): one record of the block for each, then the count of arrivals.
+  const bool over0 = head.start < c0, over1 = tail.start >= c0 && tail.end > c1;
+  __shared__ int is_last[2];
+  if (over0 || over1) {
+    const int n0 = over0 ? heads_in(head) : 0, n1 = over1 ? heads_in(tail) : 0;
+    for (int i = warp; i < n0 + n1; i += kWarps) {
+      const bool second = i >= n0;
+      const int n = second ? i - n0 : i;
+      join_warps(second ? tail : head, n).store(p.records + (2 * blockIdx.x + second) * static_cast<int64_t>(nrec), n, p.nh);
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      const Piece& pc = threadIdx.x == 0 ? head : tail;
+      is_last[threadIdx.x] = 0;
+      if (threadIdx.x == 0 ? over0 : over1) {
+        const int64_t per = kWarps * part;
+        const unsigned int blocks = static_cast<unsigned int>((pc.end - 1) / per - pc.start / per + 1);
+        unsigned int* cnt = p.arrived + static_cast<int64_t>(pc.b) * pl.Hv + pc.hv;
+        if (atomicAdd(cnt, 1u) == blocks - 1) {
+          is_last[threadIdx.x] = 1;
+          *cnt = 0;
+        }
+        __threadfence();
       }
     }
   }
-  // pieces that reach over the block's ends: the first and the last of it
-  __shared__ bool is_last;
-  float* part = reinterpret_cast<float*>(smem + ((2 * B + 1) * 4 + 127) / 128 * 128);
+  // meanwhile, pieces begun in this warp's part and ended in another's of the block
+  if (count > 0 && last_piece.start >= f0 && last_piece.end > f1 && last_piece.end <= c1)
+    for (int n = 0; n < heads_in(last_piece); ++n) {
+      const Joined j = join_warps(last_piece, n);
+      write_head(p, last_piece.b, head_at(last_piece, n), j.m, j.l, j.mo, j.o);
+    }
+  if (!over0 && !over1) return;
+  __syncthreads();
+  float* parts = reinterpret_cast<float*>(rings);   // the warps' records are joined
   for (int side = 0; side < 2; ++side) {
-    int64_t s, e;
-    int b, hv;
-    piece_of(side == 0 ? c0 : c1 - 1, s, e, b, hv);
-    const bool reaches = side == 0 ? s < c0 : s >= c0 && e > c1;   // one that covers the whole block counts once
-    if (!reaches) continue;
-    const int first = static_cast<int>(s / pl.part), last = static_cast<int>((e - 1) / pl.part);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      unsigned int* cnt = p.arrived + static_cast<int64_t>(b) * pl.Hv + hv;
-      const unsigned int blocks = last / kWarps - first / kWarps + 1;
-      is_last = atomicAdd(cnt, 1u) == blocks - 1;
-      if (is_last) *cnt = 0;
-      __threadfence();
-    }
-    __syncthreads();
-    if (!is_last) continue;
-    const int h = hv / p.chunks, ch0 = (hv % p.chunks) * p.nh, nh = min(p.nh, p.G - ch0);
-    const int rs = record_floats(p.nh);
-    for (int n = 0; n < nh; ++n) {   // every warp joins some of the records, in the order of the slots
-      const int count = last - first + 1, each = (count + kWarps - 1) / kWarps;
-      float jm, jl, jo;
-      float4 x;
-      join_records(p, n, first, first + warp * each, min(last, first + (warp + 1) * each - 1), 1, jm, jl, jo, x);
-      float* r = part + warp * rs;
-      reinterpret_cast<float4*>(r + n * kDv)[lane] = x;
-      if (lane == 0) {
-        r[p.nh * kDv + n] = jm;
-        r[p.nh * (kDv + 1) + n] = jl;
-        r[p.nh * (kDv + 2) + n] = jo;
-      }
-    }
-    __syncthreads();
-    for (int n = warp; n < nh; n += kWarps) {
-      float jm = -INFINITY, jl = 0.f, jo = -INFINITY;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!is_last[side]) continue;
+    const Piece& pc = side == 0 ? head : tail;
+    const int64_t per = kWarps * part;
+    const int b0 = static_cast<int>(pc.start / per), nb = static_cast<int>((pc.end - 1) / per) - b0 + 1, nh = heads_in(pc);
+    // a warp per head, or with many records and few heads, several
+    const int split = nb > 4 ? max(1, kWarps / nh) : 1, each = (nb + split - 1) / split;
+    for (int i = warp; i < nh * split; i += kWarps) {
+      const int n = i / split, r0 = (i % split) * each, r1 = min(nb, r0 + each);
+      Joined j;
+      j.clear();
+      for (int r = r0; r < r1; r += 4) {   // four records' loads in flight
+        float rm[4], rl[4], rmo[4];
+        float4 ro[4];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        jm = fmaxf(jm, part[w * rs + p.nh * kDv + n]);
-        jo = fmaxf(jo, part[w * rs + p.nh * (kDv + 2) + n]);
-      }
+        for (int k = 0; k < 4; ++k) {
+          if (r + k >= r1) break;
+          const float* rec = p.records + (2 * (b0 + r + k) + (r + k == 0)) * static_cast<int64_t>(nrec);
+          rm[k] = __ldcg(rec + p.nh * kDv + n);
+          rl[k] = __ldcg(rec + p.nh * (kDv + 1) + n);
+          rmo[k] = __ldcg(rec + p.nh * (kDv + 2) + n);
+          ro[k] = __ldcg(reinterpret_cast<const float4*>(rec + n * kDv) + lane);
+        }
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* r = part + w * rs;
-        jl += exp2_below(r[p.nh * kDv + n], jm) * r[p.nh * (kDv + 1) + n];
-        const float fo = exp2_below(r[p.nh * (kDv + 2) + n], jo);
-        const float4 y = reinterpret_cast<const float4*>(r + n * kDv)[lane];
-        x.x += fo * y.x;
-        x.y += fo * y.y;
-        x.z += fo * y.z;
-        x.w += fo * y.w;
+        for (int k = 0; k < 4; ++k)
+          if (r + k < r1) j.add(rm[k], rl[k], rmo[k], ro[k]);
       }
-      write_head(p, b, h * p.G + ch0 + n, jm, jl, jo, x);
+      if (split == 1)
+        write_head(p, pc.b, head_at(pc, n), j.m, j.l, j.mo, j.o);
+      else
+        j.store(parts + i * record_floats(1), 0, 1);
+    }
+    if (split > 1) {
+      __syncthreads();
+      for (int n = warp; n < nh; n += kWarps) {
+        Joined j;
+        j.clear();
+        for (int i = 0; i < split; ++i) j.add_record(parts + (n * split + i) * record_floats(1), 0, 1);
+        write_head(p, pc.b, head_at(pc, n), j.m, j.l, j.mo, j.o);
+      }
+      __syncthreads();   // before the other side's
     }
   }
 }
 
-// weight += the probabilities of the head's query heads
+// weight += the probabilities of the head's query heads.  Four slots a thread:
+// a page and the row of scores both begin on 16 of them.
 __global__ void __launch_bounds__(kThreads) decode_weight_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
-  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = blockIdx.x * kThreads + threadIdx.x;
-  if (i >= checked_length(p.c, b, st, KID_DECODE_WEIGHT)) return;
-  const int64_t row = cache_row(p.c, b, h, i, st, KID_DECODE_WEIGHT);
+  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = (blockIdx.x * kThreads + threadIdx.x) * 4;
+  const int n = checked_length(p.c, b, st, KID_DECODE_WEIGHT);
+  if (i >= n) return;
+  const int row = cache_row(p.c, b, h, i, st, KID_DECODE_WEIGHT);
   if (row < 0) return;
-  float w = 0.f;
+  float4* at = reinterpret_cast<float4*>(p.c.weight + row);
+  const float4 old = *at;
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t head = static_cast<int64_t>(b) * Hq + h * p.G;
   for (int g = 0; g < p.G; ++g) {
-    const int64_t at = static_cast<int64_t>(b) * Hq + h * p.G + g;
-    w += exp2_below(p.scores[at * p.c.capacity() + i], p.lse2[at]);
+    const float z = __ldg(p.lse2 + head + g);
+    const float4 s = __ldg(reinterpret_cast<const float4*>(p.scores + (head + g) * p.c.capacity() + i));
+    w.x += exp2_below(s.x, z);
+    w.y += exp2_below(s.y, z);
+    w.z += exp2_below(s.z, z);
+    w.w += exp2_below(s.w, z);
   }
-  p.c.weight[row] += w;
+  if (i + 3 < n) {
+    *at = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+  } else {   // what lies past the length stays as it is
+    p.c.weight[row] = old.x + w.x;
+    if (i + 1 < n) p.c.weight[row + 1] = old.y + w.y;
+    if (i + 2 < n) p.c.weight[row + 2] = old.z + w.z;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -762,14 +863,19 @@ int heads_per_chunk(const CacheArgs& a, int Hq) {
 int64_t most_units(const CacheArgs& a, int Hq) {
   return static_cast<int64_t>(a.B) * a.H * head_chunks(a, Hq) * (a.capacity() / 16);
 }
+// Blocks for the units at full length, and one for every piece, up to a block
+// per SM.
+int most_blocks(const CacheArgs& a, int Hq) {
+  const int64_t pieces = static_cast<int64_t>(a.B) * a.H * head_chunks(a, Hq);
+  return static_cast<int>(std::min<int64_t>(kMaxBlocks, std::max(pieces, (most_units(a, Hq) + kWarps - 1) / kWarps)));
+}
 DecodeLayout decode_layout(const CacheArgs& a, int Hq, int accumulate) {
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  const int64_t warps = most_units(a, Hq) < kMaxBlocks * kWarps ? most_units(a, Hq) : kMaxBlocks * kWarps;
   DecodeLayout w;
   w.arrived = kCacheStatusBytes;
   w.lse2 = w.arrived + up(static_cast<size_t>(a.B) * a.H * head_chunks(a, Hq) * sizeof(unsigned int));
   w.records = w.lse2 + up(static_cast<size_t>(a.B) * Hq * sizeof(float));
-  w.scores = w.records + up(static_cast<size_t>(2 * (warps + kWarps)) * record_floats(heads_per_chunk(a, Hq)) * sizeof(float));
+  w.scores = w.records + up(static_cast<size_t>(most_blocks(a, Hq)) * (2 + kWarps) * record_floats(heads_per_chunk(a, Hq)) * sizeof(float));
   w.bytes = w.scores + (accumulate ? static_cast<size_t>(a.B) * Hq * a.capacity() * sizeof(float) : 0);
   return w;
 }
@@ -784,33 +890,39 @@ int device_sms() {
   return n;
 }
 
-template <int D, bool FP8, int NT, int S>
+template <int D, bool FP8, int NT, int E, int S>
 cudaError_t launch_decode_s(const DecodeParams& p, int grid, int smem, DevStatus st, cudaStream_t s) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(decode_kernel<D, FP8, NT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    e = cudaFuncSetAttribute(decode_kernel<D, FP8, NT, E, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
-  decode_kernel<D, FP8, NT, S><<<grid, kThreads, smem, s>>>(p, st);
+  decode_kernel<D, FP8, NT, E, S><<<grid, kThreads, smem, s>>>(p, st);
   return cudaGetLastError();
 }
 
 // As many stages as fit: three, or two beside the q rows of many heads.
-template <int D, bool FP8, int NT>
-cudaError_t launch_decode_nt(const DecodeParams& p, int grid, DevStatus st, cudaStream_t s) {
+template <int D, bool FP8, int NT, int E>
+cudaError_t launch_decode_nt(DecodeParams& p, int grid, DevStatus st, cudaStream_t s) {
   const int head = ((2 * p.c.B + 1) * 4 + 127) / 128 * 128;
-  const int stage = kWarps * Tile<D, FP8>::stage_bytes(p.nh);
-  if (head + 3 * stage <= kSmemMax) return launch_decode_s<D, FP8, NT, 3>(p, grid, head + 3 * stage, st, s);
-  return launch_decode_s<D, FP8, NT, 2>(p, grid, head + 2 * stage, st, s);
+  const int stage = kWarps * Tile<D, FP8>::stage_bytes(p.nh), recs = kWarps * record_floats(p.nh) * 4;
+  const int stages = head + 3 * stage <= kSmemMax ? 3 : 2;
+  int smem = head + stages * stage;
+  p.smem_records = smem + recs <= kSmemMax;
+  if (p.smem_records) smem += recs;
+  return stages == 3 ? launch_decode_s<D, FP8, NT, E, 3>(p, grid, smem, st, s)
+                     : launch_decode_s<D, FP8, NT, E, 2>(p, grid, smem, st, s);
 }
 
 template <int D, bool FP8>
-cudaError_t launch_decode(const DecodeParams& p, int grid, DevStatus st, cudaStream_t s) {
-  return p.nh <= 8 ? launch_decode_nt<D, FP8, 1>(p, grid, st, s) : launch_decode_nt<D, FP8, 2>(p, grid, st, s);
+cudaError_t launch_decode(DecodeParams& p, int grid, DevStatus st, cudaStream_t s) {
+  if (p.nh <= 4) return launch_decode_nt<D, FP8, 1, 1>(p, grid, st, s);
+  if (p.nh <= 8) return launch_decode_nt<D, FP8, 1, 2>(p, grid, st, s);
+  return launch_decode_nt<D, FP8, 2, 2>(p, grid, st, s);
 }
 
 }  // namespace
@@ -856,9 +968,7 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
   p.lse = lse;
   p.records = reinterpret_cast<float*>(wsb + w.records);
   p.scores = accumulate ? reinterpret_cast<float*>(wsb + w.scores) : nullptr;
-  const int64_t blocks = (most_units(p.c, Hq) + kWarps - 1) / kWarps;
-  const int most = sms < kMaxBlocks ? sms : kMaxBlocks;
-  const int grid = static_cast<int>(blocks < most ? blocks : most);
+  const int grid = std::min(sms, most_blocks(p.c, Hq));
   mark(s);
   cudaError_t e;
   switch (p.c.d) {
@@ -869,7 +979,7 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
   if (e != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   if (accumulate) {
-    decode_weight_kernel<<<dim3((p.c.capacity() + kThreads - 1) / kThreads, p.c.H, p.c.B), kThreads, 0, s>>>(p, st);
+    decode_weight_kernel<<<dim3((p.c.capacity() + 4 * kThreads - 1) / (4 * kThreads), p.c.H, p.c.B), kThreads, 0, s>>>(p, st);
     if (cudaGetLastError() != cudaSuccess) return QKVP_ERR_CUDA;
     mark(s);
   }

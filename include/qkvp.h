@@ -418,7 +418,7 @@ int qkvp_mlp_backward(int T, int D, int F, const uint16_t* dout,
  * Pages of live slots must not be shared between sequences that are written.
  * ------------------------------------------------------------------------ */
 typedef struct qkvp_cache {
-    int P;            /* pages in the pools, 1 .. 2^26                            */
+    int P;            /* pages in the pools, P * H * page < 2^31                  */
     int page;         /* tokens per page: 16, 32, 64, 128 or 256                  */
     int H;            /* K/V heads, 1 .. 128                                      */
     int d_qk;         /* key width: 64, 96 or 128                                 */

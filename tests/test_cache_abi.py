@@ -33,7 +33,7 @@ def _desc(qk, **kw):
 BAD = [(dict(P=0), 1), (dict(page=0), 1), (dict(H=0), 1), (dict(B=0), 1), (dict(max_pages=0), 1), (dict(fp8=2), 1),
        (dict(k=0), 1), (dict(v=0), 1), (dict(table=0), 1), (dict(lengths=0), 1), (dict(fp8=1), 1),
        (dict(fp8=1, k_scale=P), 1), (dict(page=24), 2), (dict(page=8), 2), (dict(page=512), 2), (dict(H=129), 2),
-       (dict(B=4097), 2), (dict(max_pages=1 << 20), 2), (dict(P=(1 << 26) + 1), 2), (dict(d_qk=80), 2),
+       (dict(B=4097), 2), (dict(max_pages=1 << 20), 2), (dict(P=(1 << 31) // (6 * 64) + 1), 2), (dict(d_qk=80), 2),
        (dict(d_v=64), 2), (dict(B=4096, max_pages=1 << 17), 2), (dict(k=P + 8), 3), (dict(lengths=P + 4), 3), (dict(weight=P + 4), 3), (dict(pos=P + 8), 3)]
 
 
