@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -47,6 +48,9 @@ class Dims(ctypes.Structure):
 
     _fields_ = [("T", ctypes.c_int), ("D", ctypes.c_int), ("H", ctypes.c_int),
                 ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int)]
+
+
+_CACHE_PACK = struct.Struct("8i8Q").pack   # the layout of CacheDesc
 
 
 class CacheDesc(ctypes.Structure):
@@ -99,14 +103,14 @@ def lib() -> ctypes.CDLL:
                                        + [_P] * 10 + [ctypes.c_size_t, _P]),
             "qkvp_mlp_forward": (ctypes.c_int, [ctypes.c_int] * 3 + [_P] * 12 + [ctypes.c_size_t, _P]),
             "qkvp_mlp_backward": (ctypes.c_int, [ctypes.c_int] * 3 + [_P] * 18 + [ctypes.c_size_t, _P]),
-            "qkvp_cache_append_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc)]),
-            "qkvp_decode_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc)] + [ctypes.c_int] * 2),
-            "qkvp_cache_evict_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc), ctypes.c_int]),
-            "qkvp_cache_append": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_int] + [_P] * 6
+            "qkvp_cache_append_workspace_bytes": (ctypes.c_size_t, [_P]),
+            "qkvp_decode_attention_workspace_bytes": (ctypes.c_size_t, [_P] + [ctypes.c_int] * 2),
+            "qkvp_cache_evict_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int]),
+            "qkvp_cache_append": (ctypes.c_int, [_P, ctypes.c_int] + [_P] * 6
                                   + [ctypes.c_size_t, _P]),
-            "qkvp_decode_attention": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_int, ctypes.c_float]
+            "qkvp_decode_attention": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_float]
                                       + [_P] * 3 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
-            "qkvp_cache_evict": (ctypes.c_int, [ctypes.POINTER(CacheDesc)] + [ctypes.c_int] * 2 + [_P] * 3
+            "qkvp_cache_evict": (ctypes.c_int, [_P] + [ctypes.c_int] * 2 + [_P] * 3
                                  + [ctypes.c_size_t, _P]),
         }
         for name, (res, args) in sig.items():
@@ -678,31 +682,62 @@ class KVCache:
 
     def desc(self) -> CacheDesc:
         """The checked C descriptor of the tensors as they are now."""
+        return CacheDesc.from_buffer_copy(self._packed()[0])
+
+    def _packed(self):
+        """The descriptor's bytes, and (H, B, d_qk, d_v, slots of a sequence).
+        The checks are _need_cuda's, in as few steps as a call per token can
+        afford; _need_cuda words the refusal."""
         k, v, table, lengths, weight, pos = self.k, self.v, self.table, self.lengths, self.weight, self.pos
-        fp8 = k.dtype == torch.uint8
-        if k.dim() != 4 or v.dim() != 4 or table.dim() != 2:
+        ks = vs = pw = pp = 0
+        try:
+            P, H, page, d = k.shape
+            B, max_pages = table.shape
+            dt = k.dtype
+            fp8 = dt is torch.uint8
+            vshape = v.shape
+            good = (k.is_cuda and (fp8 or dt is torch.bfloat16) and k.is_contiguous() and v.is_cuda and v.dtype is dt
+                    and vshape[:3] == (P, H, page) and len(vshape) == 4 and v.is_contiguous() and table.is_cuda
+                    and table.dtype is torch.int32 and table.is_contiguous() and lengths.is_cuda
+                    and lengths.dtype is torch.int32 and lengths.shape == (B,) and lengths.is_contiguous())
+            rows = (P, H, page)
+            if fp8:
+                k_scale, v_scale = self.k_scale, self.v_scale
+                good = (good and k_scale.is_cuda and k_scale.dtype is torch.float32 and k_scale.shape == rows
+                        and k_scale.is_contiguous() and v_scale.is_cuda and v_scale.dtype is torch.float32
+                        and v_scale.shape == rows and v_scale.is_contiguous())
+                ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+            if weight is not None:
+                good = (good and weight.is_cuda and weight.dtype is torch.float32 and weight.shape == rows
+                        and weight.is_contiguous())
+                pw = weight.data_ptr()
+            if pos is not None:
+                good = good and pos.is_cuda and pos.dtype is torch.int32 and pos.shape == rows and pos.is_contiguous()
+                pp = pos.data_ptr()
+        except (AttributeError, ValueError, TypeError):
+            good = False
+        if not good:
+            self._refuse()
+        d_v = vshape[3]
+        return (_CACHE_PACK(P, page, H, d, d_v, B, max_pages, fp8, k.data_ptr(), v.data_ptr(), ks, vs, pw, pp,
+                            table.data_ptr(), lengths.data_ptr()), H, B, d, d_v, max_pages * page)
+
+    def _refuse(self):
+        fp8 = isinstance(self.k, torch.Tensor) and self.k.dtype == torch.uint8
+        _need_cuda(self.k, "cache k", torch.uint8 if fp8 else torch.bfloat16)
+        _need_cuda(self.v, "cache v", self.k.dtype)
+        _need_cuda(self.table, "cache table", torch.int32)
+        if self.k.dim() != 4 or self.v.dim() != 4 or self.table.dim() != 2:
             raise ValueError("cache k and v must be [P, H, page, d], table [B, max_pages]")
-        P, H, page, d = k.shape
-        B, max_pages = table.shape
-        d_v = v.shape[3]
-        rows = (P, H, page)
-        _quick_cuda(k, "cache k", torch.uint8 if fp8 else torch.bfloat16, (P, H, page, d))
-        _quick_cuda(v, "cache v", k.dtype, (P, H, page, d_v))
-        _quick_cuda(table, "cache table", torch.int32, (B, max_pages))
-        _quick_cuda(lengths, "cache lengths", torch.int32, (B,))
-        ks = vs = 0
-        if fp8:
-            _quick_cuda(self.k_scale, "cache k_scale", torch.float32, rows)
-            _quick_cuda(self.v_scale, "cache v_scale", torch.float32, rows)
-            ks, vs = self.k_scale.data_ptr(), self.v_scale.data_ptr()
-        if weight is not None:
-            _quick_cuda(weight, "cache weight", torch.float32, rows)
-            weight = weight.data_ptr()
-        if pos is not None:
-            _quick_cuda(pos, "cache pos", torch.int32, rows)
-            pos = pos.data_ptr()
-        return CacheDesc(P, page, H, d, d_v, B, max_pages, fp8, k.data_ptr(), v.data_ptr(), ks, vs, weight, pos,
-                         table.data_ptr(), lengths.data_ptr())
+        rows = tuple(self.k.shape[:3])
+        _need_cuda(self.v, "cache v", self.k.dtype, (*rows, self.v.shape[3]))
+        _need_cuda(self.lengths, "cache lengths", torch.int32, (self.table.shape[0],))
+        for name, dt, wanted in (("k_scale", torch.float32, fp8), ("v_scale", torch.float32, fp8),
+                                 ("weight", torch.float32, self.weight is not None),
+                                 ("pos", torch.int32, self.pos is not None)):
+            if wanted:
+                _need_cuda(getattr(self, name), f"cache {name}", dt, rows)
+        raise ValueError("cache tensors do not fit together")
 
 
 def new_cache(B: int, max_tokens: int, H: int, d_qk: int = 96, d_v: int = 128, page: int = 64, fp8: bool = False,
@@ -726,7 +761,7 @@ def new_cache(B: int, max_tokens: int, H: int, d_qk: int = 96, d_v: int = 128, p
 def new_cache_workspace(cache: KVCache, Hq: int, accumulate: bool = True, budget: int = 0) -> torch.Tensor:
     """A zero-initialised workspace that serves cache_append, decode_attention
     of Hq query heads and (budget > 0) cache_evict to ``budget`` slots."""
-    d = ctypes.byref(cache.desc())
+    d = cache._packed()[0]
     sizes = [lib().qkvp_cache_append_workspace_bytes(d),
              lib().qkvp_decode_attention_workspace_bytes(d, Hq, int(accumulate))]
     if budget:
@@ -748,7 +783,7 @@ def _cache_call(where: str, dev, ws, nbytes, *args):
     """Calls the entry point ``where`` with args, workspace and stream;
     ``nbytes()`` is the workspace it needs."""
     call = getattr(lib(), where)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)   # torch.cuda.current_stream without the object
     if ws is not None:
         _need_cuda(ws, "ws", torch.uint8)
         _check(call(*args, ws.data_ptr(), ws.numel(), stream), where)
@@ -776,19 +811,19 @@ def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
     returns them) and pos [T] int32.  Rows cu[b] .. cu[b + 1) (cu [B + 1] int32)
     belong to sequence b; without cu there is one row per sequence.  The
     lengths grow in place, or go to lengths_out.  Returns the new lengths."""
-    d = cache.desc()
+    d, H, B, d_qk, d_v, _ = cache._packed()
     if k.dim() != 3:
         raise ValueError("k must be [H, T, d_qk]")
     T = k.shape[1]
-    _quick_cuda(k, "k", torch.bfloat16, (d.H, T, d.d_qk))
-    _quick_cuda(v, "v", torch.bfloat16, (d.H, T, d.d_v))
+    _quick_cuda(k, "k", torch.bfloat16, (H, T, d_qk))
+    _quick_cuda(v, "v", torch.bfloat16, (H, T, d_v))
     _quick_cuda(pos, "pos", torch.int32, (T,))
     if cu is not None:
-        _quick_cuda(cu, "cu", torch.int32, (d.B + 1,))
+        _quick_cuda(cu, "cu", torch.int32, (B + 1,))
     if lengths_out is None:
         lengths_out = cache.lengths
     else:
-        _quick_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
+        _quick_cuda(lengths_out, "lengths_out", torch.int32, (B,))
     _cache_call("qkvp_cache_append", k.device, ws, lambda: lib().qkvp_cache_append_workspace_bytes(d), d, T, k.data_ptr(),
                 v.data_ptr(), pos.data_ptr(), None if cu is None else cu.data_ptr(), lengths_out.data_ptr())
     return lengths_out
@@ -800,20 +835,20 @@ def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, o
     H), scale 1 / sqrt(d_qk) by default.  Returns (a [B, Hq * d_v] bf16, lse [B,
     Hq] float32), a being oproj_forward's operand; with ``accumulate`` the
     cache's weights grow by the attention probabilities."""
-    d = cache.desc()
-    dev = q.device
+    d, _, B, d_qk, d_v, _ = cache._packed()
     if q.dim() != 3:
         raise ValueError("q must be [Hq, B, d_qk]")
-    Hq, B, d_qk = q.shape
-    _quick_cuda(q, "q", torch.bfloat16, (Hq, d.B, d.d_qk))
+    Hq = q.shape[0]
+    _quick_cuda(q, "q", torch.bfloat16, (Hq, B, d_qk))
+    dev = q.device
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs cache.weight")
     if out is None:
-        a = torch.empty((B, Hq * d.d_v), dtype=torch.bfloat16, device=dev)
+        a = torch.empty((B, Hq * d_v), dtype=torch.bfloat16, device=dev)
         lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
     else:
         a, lse = out
-        _quick_cuda(a, "a", torch.bfloat16, (B, Hq * d.d_v))
+        _quick_cuda(a, "a", torch.bfloat16, (B, Hq * d_v))
         _quick_cuda(lse, "lse", torch.float32, (B, Hq))
     _cache_call("qkvp_decode_attention", dev, ws,
                 lambda: lib().qkvp_decode_attention_workspace_bytes(d, Hq, int(accumulate)), d, Hq,
@@ -828,20 +863,20 @@ def cache_evict(cache: KVCache, budget: int, recent: int, lengths_out=None, ws=N
     above the budget move into the freed ones below it.  Returns slots [B, H,
     budget] int32, the slot each new one held before (-1 past the length); the
     lengths change in place, or go to lengths_out."""
-    d = cache.desc()
+    d, H, B, _, _, capacity = cache._packed()
     dev = cache.k.device
     if cache.weight is None or cache.pos is None:
         raise ValueError("cache_evict needs cache.weight and cache.pos")
     if lengths_out is None:
         lengths_out = cache.lengths
     else:
-        _quick_cuda(lengths_out, "lengths_out", torch.int32, (d.B,))
-    if not 0 < budget <= d.max_pages * d.page:
+        _quick_cuda(lengths_out, "lengths_out", torch.int32, (B,))
+    if not 0 < budget <= capacity:
         raise QKVPError(ERR_INVALID_ARGUMENT, "qkvp_cache_evict")
     if out is None:
-        out = torch.empty((d.B, d.H, budget), dtype=torch.int32, device=dev)
+        out = torch.empty((B, H, budget), dtype=torch.int32, device=dev)
     else:
-        _quick_cuda(out, "slots", torch.int32, (d.B, d.H, budget))
+        _quick_cuda(out, "slots", torch.int32, (B, H, budget))
     _cache_call("qkvp_cache_evict", dev, ws, lambda: lib().qkvp_cache_evict_workspace_bytes(d, budget), d, budget, recent,
                 out.data_ptr(), lengths_out.data_ptr())
     return out

@@ -1,5 +1,6 @@
 // The paged key-value cache: argument checks, append and eviction.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "cache.cuh"
@@ -45,6 +46,16 @@ int check_cache(const qkvp_cache* c, CacheArgs* a) {
   while ((1 << a->page_shift) < c->page) ++a->page_shift;
   a->d = c->d_qk;
   return QKVP_OK;
+}
+
+int device_sms() {
+  static std::atomic<int> cache[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed))) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 namespace {
@@ -200,8 +211,15 @@ cudaError_t launch_append(const CacheArgs& c, int T, const uint16_t* k, const ui
                           cudaStream_t s) {
   const int in_place = lengths_out == c.lengths;
   const auto blocks = [&](int r) { return std::max(1, (T + 16 * r - 1) / (16 * r)); };
-  append_kernel<D, FP8, 1><<<dim3(blocks(1), c.H), kAppendThreads, 0, s>>>(c, T, k, v, pos, cu, lengths_out, in_place,
-                                                                           arrived, st);
+  // Four rows a half-warp share the search for their place and keep more loads
+  // in flight, once that still leaves two blocks for every SM of the largest
+  // part; fewer tokens are spread over as many warps as there are.
+  if (static_cast<int64_t>(blocks(4)) * c.H >= 304)
+    append_kernel<D, FP8, 4><<<dim3(blocks(4), c.H), kAppendThreads, 0, s>>>(c, T, k, v, pos, cu, lengths_out, in_place,
+                                                                             arrived, st);
+  else
+    append_kernel<D, FP8, 1><<<dim3(blocks(1), c.H), kAppendThreads, 0, s>>>(c, T, k, v, pos, cu, lengths_out, in_place,
+                                                                             arrived, st);
   return cudaGetLastError();
 }
 
@@ -218,13 +236,19 @@ cudaError_t launch_append_d(const CacheArgs& c, int T, const uint16_t* k, const 
 }
 
 // ---------------------------------------------------------------------------
-// Eviction: which slots stay.  One block per (head, sequence) finds the
-// budget-th largest key by four passes over its digits (radix selection),
-// then ranks ties, freed and moving slots in slot order.  A key orders first
-// by "protected", then by weight.
+// Eviction: which slots stay.  A cluster of blocks per (head, sequence) reads
+// weights and positions once, into keys that order first by "protected", then
+// by weight, kept in shared memory; finds the budget-th largest key by three
+// passes over its digits (radix selection, the blocks' histograms added
+// through distributed shared memory), then ranks ties, freed and moving slots
+// in slot order.  Every step costs little beside its latency, so the slots of
+// one head are spread over as many blocks as a cluster and the GPU hold.
 // ---------------------------------------------------------------------------
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kSelectSmem = 200 * 1024;   // of keys, at most
 
 __device__ __forceinline__ uint32_t evict_key(float w, int pos, int64_t protect_above) {
   if (pos > protect_above) return 0xffffffffu;
@@ -233,8 +257,20 @@ __device__ __forceinline__ uint32_t evict_key(float w, int pos, int64_t protect_
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);   // -inf -> 0x007fffff, +inf -> 0xff800000
 }
 
-// Exclusive sum over the block's warps of one value per warp (valid on every
-// thread); *total receives the sum.  red: kSelectWarps ints.
+__device__ __forceinline__ uint32_t cluster_blocks() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+// The value of this block's shared variable `p` in block `rank` of the cluster.
+__device__ __forceinline__ int ld_rank(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_rank(p, rank)) : "memory");
+  return v;
+}
+
+// Exclusive sum over the block's threads' warps of one value per warp; *total
+// receives the sum.  red: kSelectWarps ints.
 __device__ __forceinline__ int warp_offsets(int mine, int* red, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
@@ -251,82 +287,147 @@ __device__ __forceinline__ int warp_offsets(int mine, int* red, int* total) {
   return incl - mine;
 }
 
+struct SelectShared {
+  int hist[3][kBins];
+  int red[kSelectWarps];
+  int newest, digit, need, ties, freed, moving;
+};
+
 __global__ void __launch_bounds__(kSelectThreads)
-    evict_select_kernel(CacheArgs c, int budget, int recent, int32_t* __restrict__ slots, int32_t* __restrict__ holes,
-                        DevStatus st) {
-  const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    evict_select_kernel(CacheArgs c, int budget, int recent, int key_slots, int32_t* __restrict__ slots,
+                        int32_t* __restrict__ holes, DevStatus st) {
+  extern __shared__ __align__(16) uint32_t keys[];   // [key_slots], or none
+  __shared__ SelectShared x;
+  const int blocks = cluster_blocks(), rank = cluster_rank();
+  const int h = blockIdx.x / blocks, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = checked_length(c, b, st, KID_EVICT_SELECT);
   const int64_t out = (static_cast<int64_t>(b) * c.H + h) * budget;
   slots += out;
   holes += out;
-  if (n <= budget) {
-    for (int j = threadIdx.x; j < budget; j += kSelectThreads) slots[j] = j < n ? j : -1;
+  if (n <= budget) {   // (the same for the whole cluster)
+    for (int j = rank * kSelectThreads + threadIdx.x; j < budget; j += blocks * kSelectThreads) slots[j] = j < n ? j : -1;
     return;
   }
-  __shared__ unsigned int hist[256];
-  __shared__ int red[kSelectWarps];
-  __shared__ unsigned int s_prefix, s_need;
+  // this block's consecutive slots, a multiple of 32 for every warp
+  const int seg = ((n + blocks - 1) / blocks + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
+  const int s0 = min(n, rank * seg), cnt = min(n, s0 + seg) - s0;
+  for (int i = threadIdx.x; i < 3 * kBins; i += kSelectThreads) (&x.hist[0][0])[i] = 0;
 
   // the newest position
   int newest = INT_MIN;
-  for (int i = threadIdx.x; i < n; i += kSelectThreads) {
-    const int row = cache_row(c, b, h, i, st, KID_EVICT_SELECT);
-    if (row >= 0) newest = max(newest, c.pos[row]);
+  for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {   // four slots lie in one page
+    const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
+    if (row < 0) continue;
+    const int4 p = *reinterpret_cast<const int4*>(c.pos + row);
+    newest = max(newest, p.x);
+    if (i + 1 < cnt) newest = max(newest, p.y);
+    if (i + 2 < cnt) newest = max(newest, p.z);
+    if (i + 3 < cnt) newest = max(newest, p.w);
   }
   newest = __reduce_max_sync(0xffffffffu, newest);
-  if (lane == 0) red[warp] = newest;
+  if (lane == 0) x.red[warp] = newest;
   __syncthreads();
-  newest = __reduce_max_sync(0xffffffffu, red[lane]);
+  newest = __reduce_max_sync(0xffffffffu, x.red[lane]);
+  if (threadIdx.x == 0) x.newest = newest;
+  cluster_sync_all();
+  for (int r = 0; r < blocks; ++r) newest = max(newest, ld_rank(&x.newest, r));
   const int64_t above = static_cast<int64_t>(newest) - recent;
+
   // slots in a page outside the pool have the lowest key
+  const bool cached = seg <= key_slots;
   const auto key_of = [&](int i) {
-    const int row = cache_row(c, b, h, i, st, KID_EVICT_SELECT);
+    if (cached) return keys[i];
+    const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
     return row < 0 ? 0u : evict_key(c.weight[row], c.pos[row], above);
   };
-
-  unsigned int prefix = 0, need = budget;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    __syncthreads();
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-    __syncthreads();
-    const unsigned int mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
-      const uint32_t key = key_of(i);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1u);
+  const auto count = [&](int pass, uint32_t key, uint32_t prefix) {
+    if (pass == 0) {
+      atomicAdd(&x.hist[0][key >> 21], 1);
+    } else if (pass == 1) {
+      if (key >> 21 == prefix) atomicAdd(&x.hist[1][(key >> 10) & 2047], 1);
+    } else {
+      if (key >> 10 == prefix) atomicAdd(&x.hist[2][key & 1023], 1);
+    }
+  };
+  if (cached) {
+    for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {
+      const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
+      uint4 k = make_uint4(0, 0, 0, 0);
+      if (row >= 0) {
+        const int4 p = *reinterpret_cast<const int4*>(c.pos + row);
+        const float4 w = *reinterpret_cast<const float4*>(c.weight + row);
+        k = make_uint4(evict_key(w.x, p.x, above), evict_key(w.y, p.y, above), evict_key(w.z, p.z, above),
+                       evict_key(w.w, p.w, above));
+      }
+      *reinterpret_cast<uint4*>(keys + i) = k;
+      count(0, k.x, 0);
+      if (i + 1 < cnt) count(0, k.y, 0);
+      if (i + 2 < cnt) count(0, k.z, 0);
+      if (i + 3 < cnt) count(0, k.w, 0);
+    }
+  }
+  uint32_t prefix = 0;
+  int need = budget;
+  for (int pass = 0; pass < 3; ++pass) {
+    if (pass > 0 || !cached)
+      for (int i = threadIdx.x; i < cnt; i += kSelectThreads) count(pass, key_of(i), prefix);
+    cluster_sync_all();
+    // bins from the highest, two a thread: where does the sum reach `need`?
+    const int hi = kBins - 1 - 2 * threadIdx.x;
+    int v0 = 0, v1 = 0;
+    for (int r = 0; r < blocks; ++r) {
+      v0 += ld_rank(&x.hist[pass][hi], r);
+      v1 += ld_rank(&x.hist[pass][hi - 1], r);
+    }
+    int incl = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    int total;
+    const int before = warp_offsets(__shfl_sync(0xffffffffu, incl, 31), x.red, &total) + incl - v0 - v1;
+    if (before < need && need <= before + v0) {
+      x.digit = hi;
+      x.need = need - before;
+    } else if (before + v0 < need && need <= before + v0 + v1) {
+      x.digit = hi - 1;
+      x.need = need - before - v0;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int d = 255;
-      while (d > 0 && hist[d] < need) need -= hist[d--];
-      s_prefix = prefix | (static_cast<unsigned int>(d) << shift);
-      s_need = need;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
+    prefix = pass == 2 ? prefix << 10 | x.digit : prefix << 11 | x.digit;
+    need = x.need;
   }
   // kept: keys above `prefix`, and the first `need` slots whose key equals it
 
-  const int seg = (n + kSelectThreads - 1) / kSelectThreads * 32;   // a warp's consecutive slots
-  const int i0 = min(n, warp * seg), i1 = min(n, i0 + seg);
-  int ties = 0;
+  // offsets of this warp's slots among the cluster's: before the block, and in it
+  const int wseg = seg / kSelectWarps, i0 = min(cnt, warp * wseg), i1 = min(cnt, i0 + wseg);
+  const auto lower_blocks = [&](const int* p) {
+    int s = 0;
+    for (int r = 0; r < rank; ++r) s += ld_rank(p, r);
+    return s;
+  };
+  int ties = 0, total;
   for (int i = i0 + lane; i - lane < i1; i += 32)
     ties += __popc(__ballot_sync(0xffffffffu, i < i1 && key_of(i) == prefix));
-  int total;
-  const int ties0 = warp_offsets(ties, red, &total);
+  int ties0 = warp_offsets(ties, x.red, &total);
+  if (threadIdx.x == 0) x.ties = total;
+  cluster_sync_all();
+  ties0 += lower_blocks(&x.ties);
   // A walk over the warp's slots in order: calls f(slot, kept, freed before
   // it, moving before it) and returns both counts.
   const auto walk = [&](int freed, int moving, auto f) {
     int t = ties0;
     for (int i = i0 + lane; i - lane < i1; i += 32) {
       const bool in = i < i1;
+      const int slot = s0 + i;
       const uint32_t key = in ? key_of(i) : 0u;
       const unsigned int below = (1u << lane) - 1u;
       const unsigned int tie = __ballot_sync(0xffffffffu, in && key == prefix);
-      const bool kept = in && (key > prefix || (key == prefix && t + __popc(tie & below) < static_cast<int>(need)));
-      const unsigned int fr = __ballot_sync(0xffffffffu, in && !kept && i < budget);
-      const unsigned int mv = __ballot_sync(0xffffffffu, kept && i >= budget);
-      if (in) f(i, kept, freed + __popc(fr & below), moving + __popc(mv & below));
+      const bool kept = in && (key > prefix || (key == prefix && t + __popc(tie & below) < need));
+      const unsigned int fr = __ballot_sync(0xffffffffu, in && !kept && slot < budget);
+      const unsigned int mv = __ballot_sync(0xffffffffu, kept && slot >= budget);
+      if (in) f(slot, kept, freed + __popc(fr & below), moving + __popc(mv & below));
       t += __popc(tie);
       freed += __popc(fr);
       moving += __popc(mv);
@@ -334,36 +435,44 @@ __global__ void __launch_bounds__(kSelectThreads)
     return make_int2(freed, moving);
   };
   const int2 counts = walk(0, 0, [](int, bool, int, int) {});
-  const int freed0 = warp_offsets(counts.x, red, &total);
-  const int moving0 = warp_offsets(counts.y, red, &total);
-  walk(freed0, moving0, [&](int i, bool kept, int freed, int) {
-    if (i >= budget) return;
+  int freed0 = warp_offsets(counts.x, x.red, &total);
+  if (threadIdx.x == 0) x.freed = total;
+  int moving0 = warp_offsets(counts.y, x.red, &total);
+  if (threadIdx.x == 0) x.moving = total;
+  cluster_sync_all();
+  freed0 += lower_blocks(&x.freed);
+  moving0 += lower_blocks(&x.moving);
+  walk(freed0, moving0, [&](int slot, bool kept, int freed, int) {
+    if (slot >= budget) return;
     if (kept)
-      slots[i] = i;
+      slots[slot] = slot;
     else
-      holes[freed] = i;
+      __stcg(holes + freed, slot);
   });
-  __syncthreads();   // holes[] is complete
-  walk(freed0, moving0, [&](int i, bool kept, int, int moving) {
-    if (kept && i >= budget) slots[holes[moving]] = i;
+  cluster_sync_all();   // holes[] is complete, and no block leaves while another reads its shared memory
+  walk(freed0, moving0, [&](int slot, bool kept, int, int moving) {
+    if (kept && slot >= budget) slots[__ldcg(holes + moving)] = slot;
   });
 }
 
 // ---------------------------------------------------------------------------
-// Eviction: the moves, and the lengths.  A warp takes 32 new slots and copies
-// the rows that change, one after the other, 16 bytes a lane.  Sources lie at
-// or above the budget and destinations below it, so no copy disturbs another.
+// Eviction: the moves, and the lengths.  Reads and writes the rows that move,
+// 16 bytes a lane: a warp takes 32 new slots and copies the rows that change,
+// one (E4M3: two) a step with four steps' loads in flight.  Sources lie at or
+// above the budget and destinations below it, so no copy disturbs another.
 // ---------------------------------------------------------------------------
+template <bool FP8>
 __global__ void __launch_bounds__(256)
-    evict_move_kernel(CacheArgs c, int budget, const int32_t* __restrict__ slots, int32_t* lengths_out, int kchunks,
-                      int vchunks, DevStatus st) {
+    evict_move_kernel(CacheArgs c, int budget, const int32_t* __restrict__ slots, int32_t* lengths_out, DevStatus st) {
+  constexpr int ES = FP8 ? 1 : 2, VC = kDv * ES / 16, ROWS = FP8 ? 2 : 1, STEPS = 4;
+  const int kc = c.d * ES / 16;
   const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
   const int j = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 + lane;
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
     const int n = c.lengths[b], cap = c.capacity();
     lengths_out[b] = min(budget, max(0, min(n, cap)));
   }
-  int64_t src = -1, dst = -1;
+  int src = -1, dst = -1;
   if (j < budget) {
     const int from = __ldg(slots + (static_cast<int64_t>(b) * c.H + h) * budget + j);
     if (from != j && from >= 0) {
@@ -374,23 +483,80 @@ __global__ void __launch_bounds__(256)
   const bool moves = src >= 0 && dst >= 0;
   unsigned int todo = __ballot_sync(0xffffffffu, moves);
   if (moves) {
-    c.weight[dst] = c.weight[src];
-    c.pos[dst] = c.pos[src];
-    if (c.k_scale) {
-      c.k_scale[dst] = c.k_scale[src];
-      c.v_scale[dst] = c.v_scale[src];
+    const float w = c.weight[src];
+    const int p = c.pos[src];
+    const float ks = FP8 ? c.k_scale[src] : 0.f, vs = FP8 ? c.v_scale[src] : 0.f;
+    c.weight[dst] = w;
+    c.pos[dst] = p;
+    if (FP8) {
+      c.k_scale[dst] = ks;
+      c.v_scale[dst] = vs;
     }
   }
+  const int part = FP8 ? lane >> 4 : 0, l = FP8 ? lane & 15 : lane;   // which of a step's rows, and the lane in it
+  const bool is_k = l < kc;
+  const uint4* from = reinterpret_cast<const uint4*>(is_k ? c.k : c.v);
+  uint4* to = reinterpret_cast<uint4*>(is_k ? c.k : c.v);
+  const int chunks = is_k ? kc : VC, ch = is_k ? l : l - kc;
   while (todo) {
-    const int who = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int64_t s = __shfl_sync(0xffffffffu, src, who), d = __shfl_sync(0xffffffffu, dst, who);
-    if (lane < kchunks)
-      reinterpret_cast<uint4*>(c.k)[d * kchunks + lane] = reinterpret_cast<const uint4*>(c.k)[s * kchunks + lane];
-    else if (lane < kchunks + vchunks)
-      reinterpret_cast<uint4*>(c.v)[d * vchunks + lane - kchunks] =
-          reinterpret_cast<const uint4*>(c.v)[s * vchunks + lane - kchunks];
+    uint4 r[STEPS];
+    int d[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      int who[ROWS];
+#pragma unroll
+      for (int q = 0; q < ROWS; ++q) {
+        who[q] = todo ? __ffs(todo) - 1 : -1;
+        todo &= todo - 1;
+      }
+      const int w = ROWS == 2 && part ? who[ROWS - 1] : who[0];
+      const int s = __shfl_sync(0xffffffffu, src, w & 31);
+      d[i] = __shfl_sync(0xffffffffu, dst, w & 31);
+      if (w < 0 || l >= kc + VC) d[i] = -1;
+      if (d[i] >= 0) r[i] = from[static_cast<int64_t>(s) * chunks + ch];
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+      if (d[i] >= 0) to[static_cast<int64_t>(d[i]) * chunks + ch] = r[i];
   }
+}
+
+// Blocks per (head, sequence): more while a block would still have over 2048
+// slots (two a thread) and the GPU holds them all at once, or while the keys
+// do not fit into shared memory.
+cudaError_t launch_evict_select(const CacheArgs& c, int budget, int recent, int sms, int32_t* slots, int32_t* holes,
+                                DevStatus st, cudaStream_t s) {
+  const int64_t pieces = static_cast<int64_t>(c.B) * c.H;
+  const auto per_block = [&](int n) {
+    return ((c.capacity() + n - 1) / n + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
+  };
+  int blocks = 1;
+  while (blocks < kMaxCluster && ((per_block(blocks) > 2048 && 2 * blocks * pieces <= 2 * sms) ||
+                                  per_block(blocks) * 4 > kSelectSmem))
+    blocks *= 2;
+  const int key_slots = per_block(blocks) * 4 <= kSelectSmem ? per_block(blocks) : 0;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(c.H * blocks, c.B);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(key_slots) * 4;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, c, budget, recent, key_slots, slots, holes, st);
 }
 
 }  // namespace
@@ -447,16 +613,19 @@ int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* s
   for (const void* p : ptrs)
     if (!aligned16(p)) return QKVP_ERR_MISALIGNED;
   if (ws_bytes < qkvp_cache_evict_workspace_bytes(cache, budget)) return QKVP_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = device_sms();
+  if (sms <= 0) return QKVP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const DevStatus st{static_cast<int*>(ws), 0};
   int32_t* holes = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kCacheStatusBytes);
   mark(s);
-  evict_select_kernel<<<dim3(a.H, a.B), kSelectThreads, 0, s>>>(a, budget, recent, slots, holes, st);
-  if (cudaGetLastError() != cudaSuccess) return QKVP_ERR_CUDA;
+  if (launch_evict_select(a, budget, recent, sms, slots, holes, st, s) != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
-  const int esize = cache->fp8 ? 1 : 2;
-  evict_move_kernel<<<dim3((budget + 255) / 256, a.H, a.B), 256, 0, s>>>(a, budget, slots, lengths_out,
-                                                                         a.d * esize / 16, kDv * esize / 16, st);
+  const dim3 grid((budget + 255) / 256, a.H, a.B);
+  if (cache->fp8)
+    evict_move_kernel<true><<<grid, 256, 0, s>>>(a, budget, slots, lengths_out, st);
+  else
+    evict_move_kernel<false><<<grid, 256, 0, s>>>(a, budget, slots, lengths_out, st);
   if (cudaGetLastError() != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   return QKVP_OK;

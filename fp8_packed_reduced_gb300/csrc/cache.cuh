@@ -58,5 +58,7 @@ __device__ __forceinline__ int cache_row(const CacheArgs& c, int b, int h, int s
 
 // Host: QKVP_OK or the status an entry point returns for `c`; fills `a`.
 int check_cache(const qkvp_cache* c, CacheArgs* a);
+// Multiprocessors of the current device, 0 on error.
+int device_sms();
 
 }  // namespace qkvp

@@ -880,16 +880,6 @@ DecodeLayout decode_layout(const CacheArgs& a, int Hq, int accumulate) {
   return w;
 }
 
-int device_sms() {
-  static std::atomic<int> cache[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed))) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 template <int D, bool FP8, int NT, int E, int S>
 cudaError_t launch_decode_s(const DecodeParams& p, int grid, int smem, DevStatus st, cudaStream_t s) {
   static std::atomic<bool> done[64];
