@@ -62,11 +62,12 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Append.  Reads every new row once and writes it once, so it is bound by
-// memory (by latency for one token per sequence).  A half-warp holds one row
-// of k (D / 8 lanes) and of v (16 lanes), 16 bytes a lane, which puts the row
-// maximum of the E4M3 form into four shuffles; a warp takes 2 R consecutive
-// tokens of one head, whose rows are contiguous in k and v and, within a
-// page, in the pools.
+// memory (by latency for one token per sequence).  Four lanes hold a row of k
+// (D / 32 chunks of 16 bytes each) and of v (four), so a warp takes eight
+// consecutive tokens of one head with 3.5 KB of loads in flight, and the work
+// per row of the E4M3 form (maximum, scale, its reciprocal) is done for eight
+// rows at once: with sixteen lanes a row it took 75 us for 49152 tokens x 6
+// heads.  Every access is 64 bytes (32 of codes) of a row, whole sectors.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 
@@ -86,10 +87,9 @@ __device__ __forceinline__ int warp_upper_bound(const int32_t* cu, int n, int t)
   return lo;
 }
 
-__device__ __forceinline__ float half_warp_max(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
 __device__ __forceinline__ float absmax8(uint4 w) {
@@ -100,48 +100,79 @@ __device__ __forceinline__ float absmax8(uint4 w) {
   return m;
 }
 
-// Eight codes of the bf16 values w at scale s.  Below 2^-100 the scale's
-// reciprocal may overflow, so the products that bracket the quotient cannot
-// be formed and the division itself decides.
-__device__ __forceinline__ uint2 codes8(uint4 w, float s) {
-  const f2 x[4] = {f2_from_bf16x2(w.x), f2_from_bf16x2(w.y), f2_from_bf16x2(w.z), f2_from_bf16x2(w.w)};
-  if (s < 7.888609e-31f) return quant8_exact(x[0], x[1], x[2], x[3], s);
-  return quant8(x, make_bracket2(s));
+// The codes E(x / s) of N chunks of eight bf16 values, to out[4 i].  With one
+// scale per row the bracketing products of quant8 straddle a rounding boundary
+// in every few instructions of a warp (a row whose largest mantissa is 128 or
+// 224 has ties throughout), so the float32 quotient itself is formed, correctly
+// rounded, by Markstein's iteration (IBM J. Res. Dev. 34, 1990): from y =
+// RN(1/s) and an approximation q, r = x - q s is exact and RN(q + r y) the
+// rounded quotient once q is within one unit of it; one step brings it there
+// and the second rounds it.  r is exact and no power leaves the normal numbers
+// for s in [2^-80, inf) wherever the quotient reaches 2^-11 (below that every
+// code is zero); other scales, of rows that no projection gives, are left to
+// the division.  A zero loses its sign in q + r y, so signs come from x.
+template <int N>
+__device__ __forceinline__ void store_codes(uint2* out, const uint4 (&w)[N], float s) {
+  const bool usual = s >= 8.271806125530277e-25f && s < INFINITY;
+  const float y1 = __frcp_rn(s);
+  const f2 y = f2_make(y1, y1), ns = f2_make(-s, -s);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    if (!usual) {
+      out[4 * i] = quant8_exact(f2_from_bf16x2(u[0]), f2_from_bf16x2(u[1]), f2_from_bf16x2(u[2]), f2_from_bf16x2(u[3]), s);
+      continue;
+    }
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f2 x = f2_from_bf16x2(u[j]);
+      f2 q = f2_mul(x, y);
+      q = f2_fma(f2_fma(q, ns, x), y, q);
+      q = f2_fma(f2_fma(q, ns, x), y, q);
+      c[j] = cvt_e4m3x2(q);
+    }
+    out[4 * i] = make_uint2(__byte_perm(c[0], c[1], 0x5410) | (__byte_perm(u[0], u[1], 0x7531) & 0x80808080u),
+                            __byte_perm(c[2], c[3], 0x5410) | (__byte_perm(u[2], u[3], 0x7531) & 0x80808080u));
+  }
 }
 
-template <int D, bool FP8, int R>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(kAppendThreads)
     append_kernel(CacheArgs c, int T, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                   const int32_t* __restrict__ pos, const int32_t* __restrict__ cu, int32_t* lengths_out, int in_place,
                   unsigned int* arrived, DevStatus st) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+  constexpr int KN = D / 32, VN = kDv / 32;   // chunks of a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 3;
   const int h = blockIdx.y;
-  const int t0 = (blockIdx.x * (kAppendThreads / 32) + warp) * 2 * R;
-  constexpr int KL = D / 8;   // lanes of a k row
+  const int t0 = (blockIdx.x * (kAppendThreads / 32) + warp) * 8, t = t0 + (lane >> 2);
 
-  uint4 kx[R], vx[R];
+  uint4 kx[KN], vx[VN];
+  if (t < T) {
+    const int64_t in = static_cast<int64_t>(h) * T + t;
+    const uint4* kp = reinterpret_cast<const uint4*>(k) + in * (4 * KN) + l;
+    const uint4* vp = reinterpret_cast<const uint4*>(v) + in * (4 * VN) + l;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int t = t0 + 2 * r + half;
-    kx[r] = vx[r] = make_uint4(0, 0, 0, 0);
-    if (t < T) {
-      const int64_t row = static_cast<int64_t>(h) * T + t;
-      if (l < KL) kx[r] = __ldg(reinterpret_cast<const uint4*>(k) + row * KL + l);
-      vx[r] = __ldg(reinterpret_cast<const uint4*>(v) + row * 16 + l);
-    }
+    for (int i = 0; i < KN; ++i) kx[i] = __ldg(kp + 4 * i);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) vx[i] = __ldg(vp + 4 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < KN; ++i) kx[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) vx[i] = make_uint4(0, 0, 0, 0);
   }
 
-  // lane j < 2 R finds the place of token t0 + j
-  int64_t dst = -1;
+  // the place of the lane's token
+  int64_t row = -1;
   if (t0 < T) {
-    const int t = t0 + (lane % (2 * R));
     int b = t, start = t;
     if (cu != nullptr) {
       b = warp_upper_bound(cu, c.B + 1, t0) - 1;
       while (b < c.B && t < T && __ldg(cu + b + 1) <= t) ++b;   // the warp's later tokens, past empty sequences
       start = b >= 0 && b < c.B ? __ldg(cu + b) : 0;
     }
-    if (t < T && lane < 2 * R) {
+    if (t < T) {
       if (b < 0 || b >= c.B) {
         record_error(st, QKVP_ERR_DEVICE_INPUT, KID_CACHE_APPEND);
       } else {
@@ -149,33 +180,35 @@ __global__ void __launch_bounds__(kAppendThreads)
         if (slot < 0 || slot >= c.capacity())
           record_error(st, QKVP_ERR_DEVICE_INPUT, KID_CACHE_APPEND);
         else
-          dst = cache_row(c, b, h, static_cast<int>(slot), st, KID_CACHE_APPEND);
+          row = cache_row(c, b, h, static_cast<int>(slot), st, KID_CACHE_APPEND);
       }
-      if (dst >= 0) {
-        if (c.weight) c.weight[dst] = 0.f;
-        if (c.pos) c.pos[dst] = __ldg(pos + t);
+      if (row >= 0 && l == 0) {
+        if (c.weight) c.weight[row] = 0.f;
+        if (c.pos) c.pos[row] = __ldg(pos + t);
       }
     }
   }
 
+  if (FP8) {
+    float ak = 0.f, av = 0.f;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t row = __shfl_sync(0xffffffffu, dst, 2 * r + half);
-    if (FP8) {
-      const float sk = scale_from_amax(half_warp_max(absmax8(kx[r])));
-      const float sv = scale_from_amax(half_warp_max(absmax8(vx[r])));
-      if (row >= 0) {
-        if (l < KL) reinterpret_cast<uint2*>(c.k)[row * KL + l] = codes8(kx[r], sk);
-        reinterpret_cast<uint2*>(c.v)[row * 16 + l] = codes8(vx[r], sv);
-        if (l == 0) {
-          c.k_scale[row] = sk;
-          c.v_scale[row] = sv;
-        }
+    for (int i = 0; i < KN; ++i) ak = fmaxf(ak, absmax8(kx[i]));
+#pragma unroll
+    for (int i = 0; i < VN; ++i) av = fmaxf(av, absmax8(vx[i]));
+    const float sk = scale_from_amax(quad_max(ak)), sv = scale_from_amax(quad_max(av));
+    if (row >= 0) {
+      store_codes(reinterpret_cast<uint2*>(c.k) + row * (4 * KN) + l, kx, sk);
+      store_codes(reinterpret_cast<uint2*>(c.v) + row * (4 * VN) + l, vx, sv);
+      if (l == 0) {
+        c.k_scale[row] = sk;
+        c.v_scale[row] = sv;
       }
-    } else if (row >= 0) {
-      if (l < KL) reinterpret_cast<uint4*>(c.k)[row * KL + l] = kx[r];
-      reinterpret_cast<uint4*>(c.v)[row * 16 + l] = vx[r];
     }
+  } else if (row >= 0) {
+#pragma unroll
+    for (int i = 0; i < KN; ++i) reinterpret_cast<uint4*>(c.k)[row * (4 * KN) + l + 4 * i] = kx[i];
+#pragma unroll
+    for (int i = 0; i < VN; ++i) reinterpret_cast<uint4*>(c.v)[row * (4 * VN) + l + 4 * i] = vx[i];
   }
 
   // The lengths after the append.  In place they may change only once every
@@ -209,17 +242,9 @@ template <int D, bool FP8>
 cudaError_t launch_append(const CacheArgs& c, int T, const uint16_t* k, const uint16_t* v, const int32_t* pos,
                           const int32_t* cu, int32_t* lengths_out, unsigned int* arrived, DevStatus st,
                           cudaStream_t s) {
-  const int in_place = lengths_out == c.lengths;
-  const auto blocks = [&](int r) { return std::max(1, (T + 16 * r - 1) / (16 * r)); };
-  // Four rows a half-warp share the search for their place and keep more loads
-  // in flight, once that still leaves two blocks for every SM of the largest
-  // part; fewer tokens are spread over as many warps as there are.
-  if (static_cast<int64_t>(blocks(4)) * c.H >= 304)
-    append_kernel<D, FP8, 4><<<dim3(blocks(4), c.H), kAppendThreads, 0, s>>>(c, T, k, v, pos, cu, lengths_out, in_place,
-                                                                             arrived, st);
-  else
-    append_kernel<D, FP8, 1><<<dim3(blocks(1), c.H), kAppendThreads, 0, s>>>(c, T, k, v, pos, cu, lengths_out, in_place,
-                                                                             arrived, st);
+  const dim3 grid(std::max(1, (T + kAppendThreads / 4 - 1) / (kAppendThreads / 4)), c.H);
+  append_kernel<D, FP8><<<grid, kAppendThreads, 0, s>>>(c, T, k, v, pos, cu, lengths_out, lengths_out == c.lengths,
+                                                        arrived, st);
   return cudaGetLastError();
 }
 
@@ -240,11 +265,12 @@ cudaError_t launch_append_d(const CacheArgs& c, int T, const uint16_t* k, const 
 // weights and positions once, into keys that order first by "protected", then
 // by weight, kept in shared memory; finds the budget-th largest key by three
 // passes over its digits (radix selection, the blocks' histograms added
-// through distributed shared memory), then ranks ties, freed and moving slots
-// in slot order.  Every step costs little beside its latency, so the slots of
-// one head are spread over as many blocks as a cluster and the GPU hold.
+// through distributed shared memory), then ranks freed and moving slots in
+// slot order: the j-th of both make a pair for the moves.  Every step costs
+// little beside its latency, so the slots of one head are spread over as many
+// blocks as a cluster and the GPU hold.
 // ---------------------------------------------------------------------------
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
@@ -269,56 +295,75 @@ __device__ __forceinline__ int ld_rank(const int* p, uint32_t rank) {
   return v;
 }
 
-// Exclusive sum over the block's threads' warps of one value per warp; *total
-// receives the sum.  red: kSelectWarps ints.
+__device__ __forceinline__ int4 ld_rank4(const int* p, uint32_t rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(mapa_rank(p, rank))
+               : "memory");
+  return v;
+}
+
+// Exclusive sum over the block's warps of one value per warp (0 where a lane
+// has none to give: every lane passes the warp's); *total receives the sum.
 __device__ __forceinline__ int warp_offsets(int mine, int* red, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
   if (lane == 0) red[warp] = mine;
   __syncthreads();
-  int v = red[lane];
+  int v = lane < kSelectWarps ? red[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   *total = __shfl_sync(0xffffffffu, v, 31);
-  const int incl = __shfl_sync(0xffffffffu, v, warp);
-  return incl - mine;
+  return __shfl_sync(0xffffffffu, v, warp) - mine;
 }
 
-struct SelectShared {
+struct __align__(16) SelectShared {
   int hist[3][kBins];
   int red[kSelectWarps];
-  int newest, digit, need, ties, freed, moving;
+  int newest, digit, need;
+  int above_lo, above_hi, ties_lo, ties_hi;   // the block's slots with a larger, an equal key, below and above the budget
 };
 
-__global__ void __launch_bounds__(kSelectThreads)
-    evict_select_kernel(CacheArgs c, int budget, int recent, int key_slots, int32_t* __restrict__ slots,
-                        int32_t* __restrict__ holes, DevStatus st) {
+// Workspace of an eviction: pairs of (freed, moving) slots and their number.
+struct EvictPairs {
+  int* count;     // [B, H]
+  int* freed;     // [B, H, budget]
+  int* moving;    // [B, H, budget]
+};
+
+__global__ void __launch_bounds__(kSelectThreads, 2)
+    evict_select_kernel(CacheArgs c, int budget, int recent, int key_slots, int32_t* __restrict__ slots, EvictPairs pairs,
+                        DevStatus st) {
   extern __shared__ __align__(16) uint32_t keys[];   // [key_slots], or none
   __shared__ SelectShared x;
   const int blocks = cluster_blocks(), rank = cluster_rank();
   const int h = blockIdx.x / blocks, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = checked_length(c, b, st, KID_EVICT_SELECT);
-  const int64_t out = (static_cast<int64_t>(b) * c.H + h) * budget;
-  slots += out;
-  holes += out;
+  const int64_t piece = static_cast<int64_t>(b) * c.H + h;
+  slots += piece * budget;
   if (n <= budget) {   // (the same for the whole cluster)
     for (int j = rank * kSelectThreads + threadIdx.x; j < budget; j += blocks * kSelectThreads) slots[j] = j < n ? j : -1;
+    if (rank == 0 && threadIdx.x == 0) pairs.count[piece] = 0;
     return;
   }
   // this block's consecutive slots, a multiple of 32 for every warp
   const int seg = ((n + blocks - 1) / blocks + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
   const int s0 = min(n, rank * seg), cnt = min(n, s0 + seg) - s0;
   for (int i = threadIdx.x; i < 3 * kBins; i += kSelectThreads) (&x.hist[0][0])[i] = 0;
+  const bool cached = seg <= key_slots;
 
-  // the newest position
+  // The newest position; the weights go into keys[] meanwhile.
   int newest = INT_MIN;
+#pragma unroll 2
   for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {   // four slots lie in one page
     const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
     if (row < 0) continue;
     const int4 p = *reinterpret_cast<const int4*>(c.pos + row);
+    if (cached) *reinterpret_cast<float4*>(keys + i) = *reinterpret_cast<const float4*>(c.weight + row);
     newest = max(newest, p.x);
     if (i + 1 < cnt) newest = max(newest, p.y);
     if (i + 2 < cnt) newest = max(newest, p.z);
@@ -327,14 +372,13 @@ __global__ void __launch_bounds__(kSelectThreads)
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (lane == 0) x.red[warp] = newest;
   __syncthreads();
-  newest = __reduce_max_sync(0xffffffffu, x.red[lane]);
+  newest = __reduce_max_sync(0xffffffffu, x.red[lane % kSelectWarps]);
   if (threadIdx.x == 0) x.newest = newest;
   cluster_sync_all();
   for (int r = 0; r < blocks; ++r) newest = max(newest, ld_rank(&x.newest, r));
   const int64_t above = static_cast<int64_t>(newest) - recent;
 
   // slots in a page outside the pool have the lowest key
-  const bool cached = seg <= key_slots;
   const auto key_of = [&](int i) {
     if (cached) return keys[i];
     const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
@@ -349,13 +393,14 @@ __global__ void __launch_bounds__(kSelectThreads)
       if (key >> 10 == prefix) atomicAdd(&x.hist[2][key & 1023], 1);
     }
   };
-  if (cached) {
+  if (cached)   // (each thread finds the weights that it has put there; the positions come from L1 or L2)
+#pragma unroll 2
     for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {
       const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
       uint4 k = make_uint4(0, 0, 0, 0);
       if (row >= 0) {
         const int4 p = *reinterpret_cast<const int4*>(c.pos + row);
-        const float4 w = *reinterpret_cast<const float4*>(c.weight + row);
+        const float4 w = *reinterpret_cast<const float4*>(keys + i);
         k = make_uint4(evict_key(w.x, p.x, above), evict_key(w.y, p.y, above), evict_key(w.z, p.z, above),
                        evict_key(w.w, p.w, above));
       }
@@ -365,34 +410,42 @@ __global__ void __launch_bounds__(kSelectThreads)
       if (i + 2 < cnt) count(0, k.z, 0);
       if (i + 3 < cnt) count(0, k.w, 0);
     }
-  }
   uint32_t prefix = 0;
   int need = budget;
   for (int pass = 0; pass < 3; ++pass) {
     if (pass > 0 || !cached)
+#pragma unroll 4
       for (int i = threadIdx.x; i < cnt; i += kSelectThreads) count(pass, key_of(i), prefix);
     cluster_sync_all();
-    // bins from the highest, two a thread: where does the sum reach `need`?
-    const int hi = kBins - 1 - 2 * threadIdx.x;
-    int v0 = 0, v1 = 0;
+    // bins from the highest, four a thread: where does the sum reach `need`?
+    constexpr int PER = kBins / kSelectThreads;
+    const int hi = kBins - 1 - PER * threadIdx.x;
+    int v[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = 0;
     for (int r = 0; r < blocks; ++r) {
-      v0 += ld_rank(&x.hist[pass][hi], r);
-      v1 += ld_rank(&x.hist[pass][hi - 1], r);
+      const int4 q = ld_rank4(&x.hist[pass][hi - 3], r);
+      v[0] += q.w;
+      v[1] += q.z;
+      v[2] += q.y;
+      v[3] += q.x;
     }
-    int incl = v0 + v1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += v[i];
+    int incl = sum, total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
-    int total;
-    const int before = warp_offsets(__shfl_sync(0xffffffffu, incl, 31), x.red, &total) + incl - v0 - v1;
-    if (before < need && need <= before + v0) {
-      x.digit = hi;
-      x.need = need - before;
-    } else if (before + v0 < need && need <= before + v0 + v1) {
-      x.digit = hi - 1;
-      x.need = need - before - v0;
+    int before = warp_offsets(__shfl_sync(0xffffffffu, incl, 31), x.red, &total) + incl - sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (before < need && need <= before + v[i]) {
+        x.digit = hi - i;
+        x.need = need - before;
+      }
+      before += v[i];
     }
     __syncthreads();
     prefix = pass == 2 ? prefix << 10 | x.digit : prefix << 11 | x.digit;
@@ -400,97 +453,112 @@ __global__ void __launch_bounds__(kSelectThreads)
   }
   // kept: keys above `prefix`, and the first `need` slots whose key equals it
 
-  // offsets of this warp's slots among the cluster's: before the block, and in it
+  // The warp's slots with a larger and with an equal key, below and above the
+  // budget, and those of the slots before: in lower blocks, in lower warps.
   const int wseg = seg / kSelectWarps, i0 = min(cnt, warp * wseg), i1 = min(cnt, i0 + wseg);
-  const auto lower_blocks = [&](const int* p) {
-    int s = 0;
-    for (int r = 0; r < rank; ++r) s += ld_rank(p, r);
-    return s;
-  };
-  int ties = 0, total;
-  for (int i = i0 + lane; i - lane < i1; i += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, i < i1 && key_of(i) == prefix));
-  int ties0 = warp_offsets(ties, x.red, &total);
-  if (threadIdx.x == 0) x.ties = total;
+  int a_lo = 0, a_hi = 0, t_lo = 0, t_hi = 0;
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const bool in = i < i1, lo = s0 + i < budget;
+    const uint32_t key = in ? key_of(i) : 0u;
+    const unsigned int a = __ballot_sync(0xffffffffu, in && key > prefix), t = __ballot_sync(0xffffffffu, in && key == prefix);
+    const unsigned int m = __ballot_sync(0xffffffffu, lo);
+    a_lo += __popc(a & m);
+    a_hi += __popc(a & ~m);
+    t_lo += __popc(t & m);
+    t_hi += __popc(t & ~m);
+  }
+  int total_a_lo, total_a_hi, total_t_lo, total_t_hi;
+  a_lo = warp_offsets(a_lo, x.red, &total_a_lo);
+  a_hi = warp_offsets(a_hi, x.red, &total_a_hi);
+  t_lo = warp_offsets(t_lo, x.red, &total_t_lo);
+  t_hi = warp_offsets(t_hi, x.red, &total_t_hi);
+  if (threadIdx.x == 0) {
+    x.above_lo = total_a_lo;
+    x.above_hi = total_a_hi;
+    x.ties_lo = total_t_lo;
+    x.ties_hi = total_t_hi;
+  }
   cluster_sync_all();
-  ties0 += lower_blocks(&x.ties);
-  // A walk over the warp's slots in order: calls f(slot, kept, freed before
-  // it, moving before it) and returns both counts.
-  const auto walk = [&](int freed, int moving, auto f) {
-    int t = ties0;
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-      const bool in = i < i1;
-      const int slot = s0 + i;
-      const uint32_t key = in ? key_of(i) : 0u;
-      const unsigned int below = (1u << lane) - 1u;
-      const unsigned int tie = __ballot_sync(0xffffffffu, in && key == prefix);
-      const bool kept = in && (key > prefix || (key == prefix && t + __popc(tie & below) < need));
-      const unsigned int fr = __ballot_sync(0xffffffffu, in && !kept && slot < budget);
-      const unsigned int mv = __ballot_sync(0xffffffffu, kept && slot >= budget);
-      if (in) f(slot, kept, freed + __popc(fr & below), moving + __popc(mv & below));
-      t += __popc(tie);
-      freed += __popc(fr);
-      moving += __popc(mv);
+  int all_t_lo = 0, all_a_lo = 0;
+  for (int r = 0; r < blocks; ++r) {
+    const int tl = ld_rank(&x.ties_lo, r), al = ld_rank(&x.above_lo, r);
+    all_t_lo += tl;
+    all_a_lo += al;
+    if (r < rank) {
+      t_lo += tl;
+      a_lo += al;
+      t_hi += ld_rank(&x.ties_hi, r);
+      a_hi += ld_rank(&x.above_hi, r);
     }
-    return make_int2(freed, moving);
-  };
-  const int2 counts = walk(0, 0, [](int, bool, int, int) {});
-  int freed0 = warp_offsets(counts.x, x.red, &total);
-  if (threadIdx.x == 0) x.freed = total;
-  int moving0 = warp_offsets(counts.y, x.red, &total);
-  if (threadIdx.x == 0) x.moving = total;
-  cluster_sync_all();
-  freed0 += lower_blocks(&x.freed);
-  moving0 += lower_blocks(&x.moving);
-  walk(freed0, moving0, [&](int slot, bool kept, int freed, int) {
-    if (slot >= budget) return;
-    if (kept)
-      slots[slot] = slot;
-    else
-      __stcg(holes + freed, slot);
-  });
-  cluster_sync_all();   // holes[] is complete, and no block leaves while another reads its shared memory
-  walk(freed0, moving0, [&](int slot, bool kept, int, int moving) {
-    if (kept && slot >= budget) slots[__ldcg(holes + moving)] = slot;
-  });
+  }
+  cluster_sync_all();   // no block leaves while another reads its shared memory
+  const int kept_lo = all_a_lo + min(need, all_t_lo);   // of all slots below the budget
+  int* freed_at = pairs.freed + piece * budget;
+  int* moving_at = pairs.moving + piece * budget;
+  int ties = t_lo + t_hi, kept = a_lo + a_hi + min(need, ties);   // before the warp's next slot
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const bool in = i < i1;
+    const int slot = s0 + i;
+    const uint32_t key = in ? key_of(i) : 0u;
+    const unsigned int before = (1u << lane) - 1u;
+    const unsigned int t = __ballot_sync(0xffffffffu, in && key == prefix);
+    const bool keep = in && (key > prefix || (key == prefix && ties + __popc(t & before) < need));
+    const unsigned int k = __ballot_sync(0xffffffffu, keep);
+    const int rank_kept = kept + __popc(k & before);   // kept slots before this one
+    if (in && slot < budget) {
+      if (keep)
+        slots[slot] = slot;
+      else
+        freed_at[slot - rank_kept] = slot;
+    } else if (keep) {
+      moving_at[rank_kept - kept_lo] = slot;
+    }
+    ties += __popc(t);
+    kept += __popc(k);
+  }
+  if (rank == 0 && threadIdx.x == 0) pairs.count[piece] = budget - kept_lo;
 }
 
 // ---------------------------------------------------------------------------
 // Eviction: the moves, and the lengths.  Reads and writes the rows that move,
-// 16 bytes a lane: a warp takes 32 new slots and copies the rows that change,
-// one (E4M3: two) a step with four steps' loads in flight.  Sources lie at or
-// above the budget and destinations below it, so no copy disturbs another.
+// 16 bytes a lane: a warp takes 16 pairs and copies one row (E4M3: two) a step
+// with four steps' loads in flight.  Sources lie at or above the budget and
+// destinations below it, so no copy disturbs another.
 // ---------------------------------------------------------------------------
+constexpr int kMovePairs = 16;   // of a warp
+
 template <bool FP8>
 __global__ void __launch_bounds__(256)
-    evict_move_kernel(CacheArgs c, int budget, const int32_t* __restrict__ slots, int32_t* lengths_out, DevStatus st) {
+    evict_move_kernel(CacheArgs c, int budget, int32_t* __restrict__ slots, EvictPairs pairs, int32_t* lengths_out,
+                      DevStatus st) {
   constexpr int ES = FP8 ? 1 : 2, VC = kDv * ES / 16, ROWS = FP8 ? 2 : 1, STEPS = 4;
   const int kc = c.d * ES / 16;
   const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
-  const int j = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 + lane;
+  const int64_t piece = static_cast<int64_t>(b) * c.H + h;
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
     const int n = c.lengths[b], cap = c.capacity();
     lengths_out[b] = min(budget, max(0, min(n, cap)));
   }
+  const int j0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kMovePairs;
+  const int n = min(kMovePairs, __ldg(pairs.count + piece) - j0);
+  if (n <= 0) return;
   int src = -1, dst = -1;
-  if (j < budget) {
-    const int from = __ldg(slots + (static_cast<int64_t>(b) * c.H + h) * budget + j);
-    if (from != j && from >= 0) {
-      src = cache_row(c, b, h, from, st, KID_EVICT_MOVE);
-      dst = cache_row(c, b, h, j, st, KID_EVICT_MOVE);
-    }
-  }
-  const bool moves = src >= 0 && dst >= 0;
-  unsigned int todo = __ballot_sync(0xffffffffu, moves);
-  if (moves) {
-    const float w = c.weight[src];
-    const int p = c.pos[src];
-    const float ks = FP8 ? c.k_scale[src] : 0.f, vs = FP8 ? c.v_scale[src] : 0.f;
-    c.weight[dst] = w;
-    c.pos[dst] = p;
-    if (FP8) {
-      c.k_scale[dst] = ks;
-      c.v_scale[dst] = vs;
+  if (lane < n) {
+    const int to = __ldg(pairs.freed + piece * budget + j0 + lane), from = __ldg(pairs.moving + piece * budget + j0 + lane);
+    slots[piece * budget + to] = from;
+    src = cache_row(c, b, h, from, st, KID_EVICT_MOVE);
+    dst = cache_row(c, b, h, to, st, KID_EVICT_MOVE);
+    if (src < 0) dst = -1;
+    if (dst >= 0) {
+      const float w = c.weight[src];
+      const int p = c.pos[src];
+      const float ks = FP8 ? c.k_scale[src] : 0.f, vs = FP8 ? c.v_scale[src] : 0.f;
+      c.weight[dst] = w;
+      c.pos[dst] = p;
+      if (FP8) {
+        c.k_scale[dst] = ks;
+        c.v_scale[dst] = vs;
+      }
     }
   }
   const int part = FP8 ? lane >> 4 : 0, l = FP8 ? lane & 15 : lane;   // which of a step's rows, and the lane in it
@@ -498,21 +566,15 @@ __global__ void __launch_bounds__(256)
   const uint4* from = reinterpret_cast<const uint4*>(is_k ? c.k : c.v);
   uint4* to = reinterpret_cast<uint4*>(is_k ? c.k : c.v);
   const int chunks = is_k ? kc : VC, ch = is_k ? l : l - kc;
-  while (todo) {
+  for (int i0 = 0; i0 < n; i0 += STEPS * ROWS) {
     uint4 r[STEPS];
     int d[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      int who[ROWS];
-#pragma unroll
-      for (int q = 0; q < ROWS; ++q) {
-        who[q] = todo ? __ffs(todo) - 1 : -1;
-        todo &= todo - 1;
-      }
-      const int w = ROWS == 2 && part ? who[ROWS - 1] : who[0];
+      const int w = i0 + i * ROWS + part;   // (past the last pair: a lane that has none)
       const int s = __shfl_sync(0xffffffffu, src, w & 31);
       d[i] = __shfl_sync(0xffffffffu, dst, w & 31);
-      if (w < 0 || l >= kc + VC) d[i] = -1;
+      if (l >= kc + VC) d[i] = -1;
       if (d[i] >= 0) r[i] = from[static_cast<int64_t>(s) * chunks + ch];
     }
 #pragma unroll
@@ -522,10 +584,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // Blocks per (head, sequence): more while a block would still have over 2048
-// slots (two a thread) and the GPU holds them all at once, or while the keys
-// do not fit into shared memory.
-cudaError_t launch_evict_select(const CacheArgs& c, int budget, int recent, int sms, int32_t* slots, int32_t* holes,
-                                DevStatus st, cudaStream_t s) {
+// slots (four a thread) and the GPU holds them all at once, two to an SM, or
+// while the keys do not fit into shared memory.
+cudaError_t launch_evict_select(const CacheArgs& c, int budget, int recent, int sms, int32_t* slots,
+                                const EvictPairs& pairs, DevStatus st, cudaStream_t s) {
   const int64_t pieces = static_cast<int64_t>(c.B) * c.H;
   const auto per_block = [&](int n) {
     return ((c.capacity() + n - 1) / n + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
@@ -556,7 +618,7 @@ cudaError_t launch_evict_select(const CacheArgs& c, int budget, int recent, int 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, c, budget, recent, key_slots, slots, holes, st);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, c, budget, recent, key_slots, slots, pairs, st);
 }
 
 }  // namespace
@@ -598,7 +660,7 @@ int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const u
 size_t qkvp_cache_evict_workspace_bytes(const qkvp_cache* cache, int budget) {
   CacheArgs a;
   if (check_cache(cache, &a) != QKVP_OK || budget < 1 || budget > a.capacity()) return 0;
-  return kCacheStatusBytes + static_cast<size_t>(a.B) * a.H * budget * sizeof(int32_t);
+  return kCacheStatusBytes + static_cast<size_t>(a.B) * a.H * (2 * static_cast<size_t>(budget) + 1) * sizeof(int32_t);
 }
 
 int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* slots, int32_t* lengths_out, void* ws,
@@ -617,15 +679,18 @@ int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* s
   if (sms <= 0) return QKVP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const DevStatus st{static_cast<int*>(ws), 0};
-  int32_t* holes = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kCacheStatusBytes);
+  EvictPairs pairs;
+  pairs.count = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kCacheStatusBytes);
+  pairs.freed = pairs.count + static_cast<int64_t>(a.B) * a.H;
+  pairs.moving = pairs.freed + static_cast<int64_t>(a.B) * a.H * budget;
   mark(s);
-  if (launch_evict_select(a, budget, recent, sms, slots, holes, st, s) != cudaSuccess) return QKVP_ERR_CUDA;
+  if (launch_evict_select(a, budget, recent, sms, slots, pairs, st, s) != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
-  const dim3 grid((budget + 255) / 256, a.H, a.B);
+  const dim3 grid((budget + 8 * kMovePairs - 1) / (8 * kMovePairs), a.H, a.B);
   if (cache->fp8)
-    evict_move_kernel<true><<<grid, 256, 0, s>>>(a, budget, slots, lengths_out, st);
+    evict_move_kernel<true><<<grid, 256, 0, s>>>(a, budget, slots, pairs, lengths_out, st);
   else
-    evict_move_kernel<false><<<grid, 256, 0, s>>>(a, budget, slots, lengths_out, st);
+    evict_move_kernel<false><<<grid, 256, 0, s>>>(a, budget, slots, pairs, lengths_out, st);
   if (cudaGetLastError() != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   return QKVP_OK;

@@ -6,7 +6,7 @@
 // is bound by memory, and its parts are chosen to keep loads in flight:
 //   - The live slots of all (sequence, head) pairs, in units of KS slots, form
 //     one list that is cut into equal contiguous parts, one for each warp of
-//     the grid (one block of eight warps per SM), whatever the lengths are.
+//     the grid (one block of 12 warps, or 8 for more than four query heads, per SM), whatever the lengths are.
 //     Warps never meet inside their parts.
 //   - Each warp has its own ring of stages in shared memory, filled by
 //     cp.async.  A unit lies inside one page (E4M3: its two halves do), so
@@ -40,11 +40,10 @@
 namespace qkvp {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 12;
+constexpr int kWeightThreads = 256;
 constexpr int kMaxBlocks = 160;            // one per SM, and the workspace's bound
 constexpr int kSmemMax = 232448 - 1024;
-constexpr int kMaxHeadTile = 16;           // query heads of one K/V head that share a read
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct DecodeParams {
@@ -213,6 +212,7 @@ __device__ __forceinline__ Piece piece_of(const Plan& pl, int64_t f) {
 }
 
 // Exclusive prefix over the block of one value per thread.
+template <int kWarps>
 __device__ __forceinline__ int block_exclusive(int v, int* red, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int x = v;
@@ -309,10 +309,10 @@ struct Joined {
 // at most four heads one, on the even columns (half the work between the two
 // products).
 // ---------------------------------------------------------------------------
-template <int D, bool FP8, int NT, int E, int S>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
+template <int D, bool FP8, int NT, int E, int kWarps, int S>
+__global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
   using TL = Tile<D, FP8>;
-  constexpr int SUB = TL::SUB, KS = TL::KS;
+  constexpr int SUB = TL::SUB, KS = TL::KS, kThreads = 32 * kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int red[kWarps], red_max[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     const int b = b0 + threadIdx.x;
     const int n = b < B ? checked_length(p.c, b, st, KID_DECODE) : 0;
     int sum;
-    const int before = block_exclusive((n + KS - 1) / KS, red, &sum);
+    const int before = block_exclusive<kWarps>((n + KS - 1) / KS, red, &sum);
     if (b < B) {
       prefix[b] = run + before;
       length[b] = n;
@@ -814,8 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
 // weight += the probabilities of the head's query heads.  Four slots a thread:
 // a page and the row of scores both begin on 16 of them.
-__global__ void __launch_bounds__(kThreads) decode_weight_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
-  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = (blockIdx.x * kThreads + threadIdx.x) * 4;
+__global__ void __launch_bounds__(kWeightThreads) decode_weight_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
+  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = (blockIdx.x * kWeightThreads + threadIdx.x) * 4;
   const int n = checked_length(p.c, b, st, KID_DECODE_WEIGHT);
   if (i >= n) return;
   const int row = cache_row(p.c, b, h, i, st, KID_DECODE_WEIGHT);
@@ -855,7 +855,12 @@ int check_heads(const CacheArgs& a, int Hq) {
 struct DecodeLayout {
   size_t arrived, lse2, records, scores, bytes;
 };
-int head_chunks(const CacheArgs& a, int Hq) { return (Hq / a.H + kMaxHeadTile - 1) / kMaxHeadTile; }
+// Query heads of one K/V head that share a read: up to 16, or 8 where the
+// list of very many sequences takes the shared memory that their q needs.
+int head_chunks(const CacheArgs& a, int Hq) {
+  const int most = a.B <= 2048 ? 16 : 8;
+  return (Hq / a.H + most - 1) / most;
+}
 int heads_per_chunk(const CacheArgs& a, int Hq) {
   const int G = Hq / a.H, n = head_chunks(a, Hq);
   return (G + n - 1) / n;
@@ -867,7 +872,7 @@ int64_t most_units(const CacheArgs& a, int Hq) {
 // per SM.
 int most_blocks(const CacheArgs& a, int Hq) {
   const int64_t pieces = static_cast<int64_t>(a.B) * a.H * head_chunks(a, Hq);
-  return static_cast<int>(std::min<int64_t>(kMaxBlocks, std::max(pieces, (most_units(a, Hq) + kWarps - 1) / kWarps)));
+  return static_cast<int>(std::min<int64_t>(kMaxBlocks, std::max(pieces, (most_units(a, Hq) + 7) / 8)));
 }
 DecodeLayout decode_layout(const CacheArgs& a, int Hq, int accumulate) {
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -875,44 +880,56 @@ DecodeLayout decode_layout(const CacheArgs& a, int Hq, int accumulate) {
   w.arrived = kCacheStatusBytes;
   w.lse2 = w.arrived + up(static_cast<size_t>(a.B) * a.H * head_chunks(a, Hq) * sizeof(unsigned int));
   w.records = w.lse2 + up(static_cast<size_t>(a.B) * Hq * sizeof(float));
-  w.scores = w.records + up(static_cast<size_t>(most_blocks(a, Hq)) * (2 + kWarps) * record_floats(heads_per_chunk(a, Hq)) * sizeof(float));
+  w.scores = w.records + up(static_cast<size_t>(most_blocks(a, Hq)) * (2 + kMaxWarps) * record_floats(heads_per_chunk(a, Hq)) * sizeof(float));
   w.bytes = w.scores + (accumulate ? static_cast<size_t>(a.B) * Hq * a.capacity() * sizeof(float) : 0);
   return w;
 }
 
-template <int D, bool FP8, int NT, int E, int S>
+template <int D, bool FP8, int NT, int E, int W, int S>
 cudaError_t launch_decode_s(const DecodeParams& p, int grid, int smem, DevStatus st, cudaStream_t s) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(decode_kernel<D, FP8, NT, E, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    e = cudaFuncSetAttribute(decode_kernel<D, FP8, NT, E, W, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
-  decode_kernel<D, FP8, NT, E, S><<<grid, kThreads, smem, s>>>(p, st);
+  decode_kernel<D, FP8, NT, E, W, S><<<grid, 32 * W, smem, s>>>(p, st);
   return cudaGetLastError();
 }
 
-// As many stages as fit: three, or two beside the q rows of many heads.
-template <int D, bool FP8, int NT, int E>
-cudaError_t launch_decode_nt(DecodeParams& p, int grid, DevStatus st, cudaStream_t s) {
-  const int head = ((2 * p.c.B + 1) * 4 + 127) / 128 * 128;
-  const int stage = kWarps * Tile<D, FP8>::stage_bytes(p.nh), recs = kWarps * record_floats(p.nh) * 4;
-  const int stages = head + 3 * stage <= kSmemMax ? 3 : 2;
-  int smem = head + stages * stage;
-  p.smem_records = smem + recs <= kSmemMax;
-  if (p.smem_records) smem += recs;
-  return stages == 3 ? launch_decode_s<D, FP8, NT, E, 3>(p, grid, smem, st, s)
-                     : launch_decode_s<D, FP8, NT, E, 2>(p, grid, smem, st, s);
+// Shared memory of W warps with S stages; with the warps' records where they
+// fit.
+template <int D, bool FP8, int NT, int E, int W, int S>
+bool fits(DecodeParams& p, int* smem) {
+  *smem = ((2 * p.c.B + 1) * 4 + 127) / 128 * 128 + W * S * Tile<D, FP8>::stage_bytes(p.nh);
+  if (*smem > kSmemMax) return false;
+  const int recs = W * record_floats(p.nh) * 4;
+  p.smem_records = *smem + recs <= kSmemMax;
+  if (p.smem_records) *smem += recs;
+  return true;
 }
 
 template <int D, bool FP8>
 cudaError_t launch_decode(DecodeParams& p, int grid, DevStatus st, cudaStream_t s) {
-  if (p.nh <= 4) return launch_decode_nt<D, FP8, 1, 1>(p, grid, st, s);
-  if (p.nh <= 8) return launch_decode_nt<D, FP8, 1, 2>(p, grid, st, s);
-  return launch_decode_nt<D, FP8, 2, 2>(p, grid, st, s);
+  int smem;
+  if (p.nh <= 4) {
+    // Twelve warps with two stages against eight with three: 104.0 / 106.8 us
+    // (64 sequences up to 8191 tokens), 58.1 / 60.6 us (48 of E4M3): each warp's
+    // chain of dependent steps is what the others have to cover.
+    if (fits<D, FP8, 1, 1, 12, 2>(p, &smem)) return launch_decode_s<D, FP8, 1, 1, 12, 2>(p, grid, smem, st, s);
+    fits<D, FP8, 1, 1, 8, 2>(p, &smem);   // beside the list of very many sequences
+    return launch_decode_s<D, FP8, 1, 1, 8, 2>(p, grid, smem, st, s);
+  }
+  if (p.nh <= 8) {
+    if (fits<D, FP8, 1, 2, 8, 3>(p, &smem)) return launch_decode_s<D, FP8, 1, 2, 8, 3>(p, grid, smem, st, s);
+    fits<D, FP8, 1, 2, 8, 2>(p, &smem);
+    return launch_decode_s<D, FP8, 1, 2, 8, 2>(p, grid, smem, st, s);
+  }
+  fits<D, FP8, 2, 2, 8, 2>(p, &smem);
+  return launch_decode_s<D, FP8, 2, 2, 8, 2>(p, grid, smem, st, s);
 }
 
 }  // namespace
@@ -969,7 +986,7 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
   if (e != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   if (accumulate) {
-    decode_weight_kernel<<<dim3((p.c.capacity() + 4 * kThreads - 1) / (4 * kThreads), p.c.H, p.c.B), kThreads, 0, s>>>(p, st);
+    decode_weight_kernel<<<dim3((p.c.capacity() + 4 * kWeightThreads - 1) / (4 * kWeightThreads), p.c.H, p.c.B), kWeightThreads, 0, s>>>(p, st);
     if (cudaGetLastError() != cudaSuccess) return QKVP_ERR_CUDA;
     mark(s);
   }

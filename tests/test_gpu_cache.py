@@ -133,6 +133,32 @@ def test_append(qk, d, page, fp8, lens, new, in_place):
             same(have[name], ref[name], name)
 
 
+def test_append_codes_of_every_mantissa(qk):
+    """Every pair of a row maximum's and a value's bf16 mantissa, at scales from
+    the smallest to the largest numbers: ties and near-ties of the quotient."""
+    m = torch.arange(128, 256).to(torch.float32)
+    vals = torch.cat([m, -m, m / 16, torch.tensor([0.0, -0.0, 1.0, -3.0] * 8)])       # 416 values a maximum
+    rows = []
+    for exp in (-126, -110, -80, -60, -3, 0, 40, 118):
+        for top in range(128, 256, 5 if exp else 1):
+            for part in vals.clamp(-top, top).view(-1, 104):
+                r = torch.zeros(128)
+                r[:104], r[127] = part, top
+                rows.append(r.double() * 2.0 ** exp)
+    v = torch.stack(rows).to(torch.bfloat16)[None]
+    T = v.shape[1]
+    k = v[:, :, 32:].contiguous()
+    cache = qk.new_cache(1, T, 1, 96, fp8=True)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    ref = host(cache)
+    co.cache_append(ref, synth.to_numpy_f32(k), synth.to_numpy_f32(v), np.zeros(T, np.int32), np.array([0, T]))
+    qk.cache_append(cache, k.to(DEV), v.to(DEV), torch.zeros(T, dtype=torch.int32, device=DEV), cu)
+    have = host(cache)
+    slots = np.arange(T)
+    for name in ("k_scale", "v_scale", "k", "v"):
+        same(have[name][slots // 64, 0, slots % 64], ref[name][slots // 64, 0, slots % 64], name)
+
+
 def test_append_in_place_many_times(qk):
     """A decode loop: the lengths grow by one a call, on one workspace."""
     H, lens = 2, [0, 62, 7]
