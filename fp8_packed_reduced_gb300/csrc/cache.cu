@@ -283,11 +283,6 @@ __device__ __forceinline__ uint32_t evict_key(float w, int pos, int64_t protect_
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);   // -inf -> 0x007fffff, +inf -> 0xff800000
 }
 
-__device__ __forceinline__ uint32_t cluster_blocks() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-  return r;
-}
 // The value of this block's shared variable `p` in block `rank` of the cluster.
 __device__ __forceinline__ int ld_rank(const int* p, uint32_t rank) {
   int v;
@@ -323,9 +318,10 @@ __device__ __forceinline__ int warp_offsets(int mine, int* red, int* total) {
 
 struct __align__(16) SelectShared {
   int hist[3][kBins];
+  // the block's slots with a larger, an equal key, below and above the budget (read as one int4)
+  int above_lo, above_hi, ties_lo, ties_hi;
   int red[kSelectWarps];
   int newest, digit, need;
-  int above_lo, above_hi, ties_lo, ties_hi;   // the block's slots with a larger, an equal key, below and above the budget
 };
 
 // Workspace of an eviction: pairs of (freed, moving) slots and their number.
@@ -335,12 +331,14 @@ struct EvictPairs {
   int* moving;    // [B, H, budget]
 };
 
+template <int BLOCKS>
 __global__ void __launch_bounds__(kSelectThreads, 2)
     evict_select_kernel(CacheArgs c, int budget, int recent, int key_slots, int32_t* __restrict__ slots, EvictPairs pairs,
                         DevStatus st) {
   extern __shared__ __align__(16) uint32_t keys[];   // [key_slots], or none
   __shared__ SelectShared x;
-  const int blocks = cluster_blocks(), rank = cluster_rank();
+  constexpr int blocks = BLOCKS;   // of a cluster: their remote loads are issued together
+  const int rank = BLOCKS > 1 ? cluster_rank() : 0;
   const int h = blockIdx.x / blocks, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = checked_length(c, b, st, KID_EVICT_SELECT);
   const int64_t piece = static_cast<int64_t>(b) * c.H + h;
@@ -375,6 +373,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   newest = __reduce_max_sync(0xffffffffu, x.red[lane % kSelectWarps]);
   if (threadIdx.x == 0) x.newest = newest;
   cluster_sync_all();
+#pragma unroll
   for (int r = 0; r < blocks; ++r) newest = max(newest, ld_rank(&x.newest, r));
   const int64_t above = static_cast<int64_t>(newest) - recent;
 
@@ -423,12 +422,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     int v[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = 0;
+    int4 q[blocks];
+#pragma unroll
+    for (int r = 0; r < blocks; ++r) q[r] = ld_rank4(&x.hist[pass][hi - 3], r);
+#pragma unroll
     for (int r = 0; r < blocks; ++r) {
-      const int4 q = ld_rank4(&x.hist[pass][hi - 3], r);
-      v[0] += q.w;
-      v[1] += q.z;
-      v[2] += q.y;
-      v[3] += q.x;
+      v[0] += q[r].w;
+      v[1] += q[r].z;
+      v[2] += q[r].y;
+      v[3] += q[r].x;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) sum += v[i];
@@ -480,18 +482,22 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   }
   cluster_sync_all();
   int all_t_lo = 0, all_a_lo = 0;
+  int4 others[blocks];
+#pragma unroll
+  for (int r = 0; r < blocks; ++r) others[r] = ld_rank4(&x.above_lo, r);
+#pragma unroll
   for (int r = 0; r < blocks; ++r) {
-    const int tl = ld_rank(&x.ties_lo, r), al = ld_rank(&x.above_lo, r);
-    all_t_lo += tl;
-    all_a_lo += al;
+    all_a_lo += others[r].x;
+    all_t_lo += others[r].z;
     if (r < rank) {
-      t_lo += tl;
-      a_lo += al;
-      t_hi += ld_rank(&x.ties_hi, r);
-      a_hi += ld_rank(&x.above_hi, r);
+      a_lo += others[r].x;
+      a_hi += others[r].y;
+      t_lo += others[r].z;
+      t_hi += others[r].w;
     }
   }
   cluster_sync_all();   // no block leaves while another reads its shared memory
+  allow_dependents();
   const int kept_lo = all_a_lo + min(need, all_t_lo);   // of all slots below the budget
   int* freed_at = pairs.freed + piece * budget;
   int* moving_at = pairs.moving + piece * budget;
@@ -535,16 +541,17 @@ __global__ void __launch_bounds__(256)
   const int kc = c.d * ES / 16;
   const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
   const int64_t piece = static_cast<int64_t>(b) * c.H + h;
-  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
+  wait_for_previous();
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {   // (in place: the selection has read it)
     const int n = c.lengths[b], cap = c.capacity();
     lengths_out[b] = min(budget, max(0, min(n, cap)));
   }
   const int j0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kMovePairs;
-  const int n = min(kMovePairs, __ldg(pairs.count + piece) - j0);
+  const int n = min(kMovePairs, __ldcg(pairs.count + piece) - j0);
   if (n <= 0) return;
   int src = -1, dst = -1;
   if (lane < n) {
-    const int to = __ldg(pairs.freed + piece * budget + j0 + lane), from = __ldg(pairs.moving + piece * budget + j0 + lane);
+    const int to = __ldcg(pairs.freed + piece * budget + j0 + lane), from = __ldcg(pairs.moving + piece * budget + j0 + lane);
     slots[piece * budget + to] = from;
     src = cache_row(c, b, h, from, st, KID_EVICT_MOVE);
     dst = cache_row(c, b, h, to, st, KID_EVICT_MOVE);
@@ -583,6 +590,33 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+template <int BLOCKS>
+cudaError_t launch_evict_select_n(const CacheArgs& c, int budget, int recent, int key_slots, int32_t* slots,
+                                  const EvictPairs& pairs, DevStatus st, cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(evict_select_kernel<BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(c.H * BLOCKS, c.B);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(key_slots) * 4;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = BLOCKS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<BLOCKS>, c, budget, recent, key_slots, slots, pairs, st);
+}
+
 // Blocks per (head, sequence): more while a block would still have over 2048
 // slots (four a thread) and the GPU holds them all at once, two to an SM, or
 // while the keys do not fit into shared memory.
@@ -597,30 +631,13 @@ cudaError_t launch_evict_select(const CacheArgs& c, int budget, int recent, int 
                                   per_block(blocks) * 4 > kSelectSmem))
     blocks *= 2;
   const int key_slots = per_block(blocks) * 4 <= kSelectSmem ? per_block(blocks) : 0;
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  switch (blocks) {
+    case 1: return launch_evict_select_n<1>(c, budget, recent, key_slots, slots, pairs, st, s);
+    case 2: return launch_evict_select_n<2>(c, budget, recent, key_slots, slots, pairs, st, s);
+    case 4: return launch_evict_select_n<4>(c, budget, recent, key_slots, slots, pairs, st, s);
+    default: return launch_evict_select_n<8>(c, budget, recent, key_slots, slots, pairs, st, s);
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(c.H * blocks, c.B);
-  cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(key_slots) * 4;
-  cfg.stream = s;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, c, budget, recent, key_slots, slots, pairs, st);
 }
-
 }  // namespace
 }  // namespace qkvp
 
@@ -687,11 +704,9 @@ int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* s
   if (launch_evict_select(a, budget, recent, sms, slots, pairs, st, s) != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   const dim3 grid((budget + 8 * kMovePairs - 1) / (8 * kMovePairs), a.H, a.B);
-  if (cache->fp8)
-    evict_move_kernel<true><<<grid, 256, 0, s>>>(a, budget, slots, pairs, lengths_out, st);
-  else
-    evict_move_kernel<false><<<grid, 256, 0, s>>>(a, budget, slots, pairs, lengths_out, st);
-  if (cudaGetLastError() != cudaSuccess) return QKVP_ERR_CUDA;
+  if (launch_dependent(cache->fp8 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 256, s, a, budget, slots,
+                       pairs, lengths_out, st) != cudaSuccess)
+    return QKVP_ERR_CUDA;
   mark(s);
   return QKVP_OK;
 }

@@ -2,6 +2,8 @@
 // table and the lengths, with the checks that keep every access in bounds.
 #pragma once
 
+#include <utility>
+
 #include "common.cuh"
 
 namespace qkvp {
@@ -54,6 +56,27 @@ __device__ __forceinline__ int cache_row(const CacheArgs& c, int b, int h, int s
     return -1;
   }
   return ((pid * c.H + h) << c.page_shift) + (slot & (c.page() - 1));   // below 2^31: checked on the host
+}
+
+// A kernel launched by launch_dependent may start before the one ahead of it
+// in its stream is done, when every block of that one has left or has called
+// allow_dependents.  Every thread calls wait_for_previous before it touches
+// what the kernel ahead writes, and before it returns.
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... KArgs, class... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // Host: QKVP_OK or the status an entry point returns for `c`; fills `a`.

@@ -269,30 +269,10 @@ __device__ __forceinline__ void write_head(const DecodeParams& p, int b, int hq,
   }
 }
 
-// A running join of records for one head: m, l and four columns of O per lane.
+// Records joined, for one head: m, l and four columns of O per lane.
 struct Joined {
   float m, l, mo;
   float4 o;
-  __device__ void clear() {
-    m = mo = -INFINITY;
-    l = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __device__ void add(float rm, float rl, float rmo, float4 x) {
-    const float m1 = fmaxf(m, rm), mo1 = fmaxf(mo, rmo);
-    const float f = exp2_below(m, m1), g = exp2_below(rm, m1), fo = exp2_below(mo, mo1), go = exp2_below(rmo, mo1);
-    l = l * f + rl * g;
-    o.x = o.x * fo + x.x * go;
-    o.y = o.y * fo + x.y * go;
-    o.z = o.z * fo + x.z * go;
-    o.w = o.w * fo + x.w * go;
-    m = m1;
-    mo = mo1;
-  }
-  __device__ void add_record(const float* r, int n, int nh) {
-    const int lane = threadIdx.x & 31;
-    add(r[nh * kDv + n], r[nh * (kDv + 1) + n], r[nh * (kDv + 2) + n], reinterpret_cast<const float4*>(r + n * kDv)[lane]);
-  }
   __device__ void store(float* r, int n, int nh) const {
     const int lane = threadIdx.x & 31;
     reinterpret_cast<float4*>(r + n * kDv)[lane] = o;
@@ -303,6 +283,65 @@ struct Joined {
     }
   }
 };
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Records of this block (in shared memory, or not), and of other blocks.
+struct AnyLoad {
+  template <class T>
+  __device__ T operator()(const T* p) const { return *p; }
+};
+struct L2Load {
+  template <class T>
+  __device__ T operator()(const T* p) const { return __ldcg(p); }
+};
+
+// Counts an arrival; everything the block has written (before a barrier) is
+// visible to whoever counts after it.  Returns the arrivals before.
+__device__ __forceinline__ unsigned int count_arrival(unsigned int* p) {
+  unsigned int old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
+
+// The join of head n of `count` records, record i at rec(i).  32 at a time: a
+// lane takes the maximum and the sum of one of them, so that every record's
+// factor is known at once and the loads of O do not wait for each other.
+template <class Load, class Rec>
+__device__ __forceinline__ Joined join_records(const Load& load, const Rec& rec, int count, int n, int nh) {
+  const int lane = threadIdx.x & 31;
+  Joined j{-INFINITY, 0.f, -INFINITY, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int k = min(32, count - i0);
+    float rm = -INFINITY, rl = 0.f, rmo = -INFINITY;
+    if (lane < k) {
+      const float* r = rec(i0 + lane);
+      rm = load(r + nh * kDv + n);
+      rl = load(r + nh * (kDv + 1) + n);
+      rmo = load(r + nh * (kDv + 2) + n);
+    }
+    const float m = fmaxf(j.m, warp_max(rm)), mo = fmaxf(j.mo, warp_max(rmo));
+    const float f = exp2_below(rmo, mo), back = exp2_below(j.mo, mo);
+    j.l = j.l * exp2_below(j.m, m) + warp_sum(rl * exp2_below(rm, m));
+    j.o = make_float4(j.o.x * back, j.o.y * back, j.o.z * back, j.o.w * back);
+    j.m = m;
+    j.mo = mo;
+#pragma unroll 4
+    for (int i = 0; i < k; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float4 x = load(reinterpret_cast<const float4*>(rec(i0 + i) + n * kDv) + lane);
+      j.o.x += fi * x.x;
+      j.o.y += fi * x.y;
+      j.o.z += fi * x.z;
+      j.o.w += fi * x.w;
+    }
+  }
+  return j;
+}
 
 // ---------------------------------------------------------------------------
 // The kernel.  E query heads per lane and tile of eight columns: two, or with
@@ -447,6 +486,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(i);
+
+  // The pieces at the block's ends and at the end of the warp's part, while the
+  // first loads are on their way.
+  __shared__ Piece ends[2];
+  if (threadIdx.x == 0) ends[0] = piece_of(pl, c0);
+  if (threadIdx.x == 32) ends[1] = piece_of(pl, c1 - 1);
+  const Piece last_piece = piece_of(pl, count > 0 ? f1 - 1 : c1 - 1);
 
   uint4 qf[NT][D / 32];           // q of column 8 t + g: chunk c of every 32 dims
   float qmul[NT][E];              // score multipliers
@@ -709,23 +755,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   __syncwarp();   // the ring is read: a record may take its place
 
   // --- joining ------------------------------------------------------------
-  // The pieces at the block's ends; `mine_last`, the last of the warp's part.
-  const Piece head = piece_of(pl, c0), tail = piece_of(pl, c1 - 1);
-  Piece last_piece = tail;
-  if (count > 0) {
-    last_piece = piece_of(pl, f1 - 1);
-    flush(last_piece.end == f1);
-  }
+  if (count > 0) flush(last_piece.end == f1);
   __syncthreads();
+  allow_dependents();
+  const Piece head = ends[0], tail = ends[1];
   const int part32 = static_cast<int>(part);   // (a block's parts together are below 2^31 units)
-  const auto warp_of = [&](int64_t f) { return static_cast<int>(f - c0) / part32; };
+  const auto warp_of = [&](int64_t f) { return static_cast<int>(static_cast<unsigned int>(f - c0) / part32); };
   const auto join_warps = [&](const Piece& pc, int n) {   // the records of one piece in this block
-    Joined j;
-    j.clear();
     const int wa = pc.start <= c0 ? 0 : warp_of(pc.start), wb = warp_of(min(pc.end, c1) - 1);
-    for (int w = wa; w <= wb; ++w)
-      j.add_record(w == wa && pc.start >= c0 ? begun_here(w) : begun_before + w * nrec, n, p.nh);
-    return j;
+    const bool begins = pc.start >= c0;
+    return join_records(AnyLoad{}, [&](int i) { return i == 0 && begins ? begun_here(wa) : begun_before + (wa + i) * nrec; },
+                        wb - wa + 1, n, p.nh);
   };
   const auto heads_in = [&](const Piece& pc) { return min(p.nh, p.G - (pc.hv % p.chunks) * p.nh); };
   const auto head_at = [&](const Piece& pc, int n) { return pc.hv / p.chunks * p.G + (pc.hv % p.chunks) * p.nh + n; };
@@ -741,7 +781,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
       const int n = second ? i - n0 : i;
       join_warps(second ? tail : head, n).store(p.records + (2 * blockIdx.x + second) * static_cast<int64_t>(nrec), n, p.nh);
     }
-    __threadfence();
     __syncthreads();
     if (threadIdx.x < 2) {
       const Piece& pc = threadIdx.x == 0 ? head : tail;
@@ -750,11 +789,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
         const int64_t per = kWarps * part;
         const unsigned int blocks = static_cast<unsigned int>((pc.end - 1) / per - pc.start / per + 1);
         unsigned int* cnt = p.arrived + static_cast<int64_t>(pc.b) * pl.Hv + pc.hv;
-        if (atomicAdd(cnt, 1u) == blocks - 1) {
+        if (count_arrival(cnt) == blocks - 1) {   // releases the block's record, acquires the others'
           is_last[threadIdx.x] = 1;
           *cnt = 0;
         }
-        __threadfence();
       }
     }
   }
@@ -773,27 +811,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
     const int64_t per = kWarps * part;
     const int b0 = static_cast<int>(pc.start / per), nb = static_cast<int>((pc.end - 1) / per) - b0 + 1, nh = heads_in(pc);
     // a warp per head, or with many records and few heads, several
-    const int split = nb > 4 ? max(1, kWarps / nh) : 1, each = (nb + split - 1) / split;
+    const int split = nb > 8 ? max(1, kWarps / nh) : 1, each = (nb + split - 1) / split;
     for (int i = warp; i < nh * split; i += kWarps) {
       const int n = i / split, r0 = (i % split) * each, r1 = min(nb, r0 + each);
-      Joined j;
-      j.clear();
-      for (int r = r0; r < r1; r += 4) {   // four records' loads in flight
-        float rm[4], rl[4], rmo[4];
-        float4 ro[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (r + k >= r1) break;
-          const float* rec = p.records + (2 * (b0 + r + k) + (r + k == 0)) * static_cast<int64_t>(nrec);
-          rm[k] = __ldcg(rec + p.nh * kDv + n);
-          rl[k] = __ldcg(rec + p.nh * (kDv + 1) + n);
-          rmo[k] = __ldcg(rec + p.nh * (kDv + 2) + n);
-          ro[k] = __ldcg(reinterpret_cast<const float4*>(rec + n * kDv) + lane);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r + k < r1) j.add(rm[k], rl[k], rmo[k], ro[k]);
-      }
+      const Joined j = join_records(
+          L2Load{}, [&](int r) { return p.records + (2 * (b0 + r0 + r) + (r0 + r == 0)) * static_cast<int64_t>(nrec); }, r1 - r0, n, p.nh);
       if (split == 1)
         write_head(p, pc.b, head_at(pc, n), j.m, j.l, j.mo, j.o);
       else
@@ -802,9 +824,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
     if (split > 1) {
       __syncthreads();
       for (int n = warp; n < nh; n += kWarps) {
-        Joined j;
-        j.clear();
-        for (int i = 0; i < split; ++i) j.add_record(parts + (n * split + i) * record_floats(1), 0, 1);
+        const Joined j = join_records(AnyLoad{}, [&](int i) { return parts + (n * split + i) * record_floats(1); }, split, 0, 1);
         write_head(p, pc.b, head_at(pc, n), j.m, j.l, j.mo, j.o);
       }
       __syncthreads();   // before the other side's
@@ -817,16 +837,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
 __global__ void __launch_bounds__(kWeightThreads) decode_weight_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
   const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = (blockIdx.x * kWeightThreads + threadIdx.x) * 4;
   const int n = checked_length(p.c, b, st, KID_DECODE_WEIGHT);
-  if (i >= n) return;
-  const int row = cache_row(p.c, b, h, i, st, KID_DECODE_WEIGHT);
+  const int row = i < n ? cache_row(p.c, b, h, i, st, KID_DECODE_WEIGHT) : -1;
+  float4* at = reinterpret_cast<float4*>(p.c.weight + max(row, 0));
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row >= 0) old = *at;   // the attention does not write it
+  wait_for_previous();
   if (row < 0) return;
-  float4* at = reinterpret_cast<float4*>(p.c.weight + row);
-  const float4 old = *at;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
   const int64_t head = static_cast<int64_t>(b) * Hq + h * p.G;
   for (int g = 0; g < p.G; ++g) {
-    const float z = __ldg(p.lse2 + head + g);
-    const float4 s = __ldg(reinterpret_cast<const float4*>(p.scores + (head + g) * p.c.capacity() + i));
+    const float z = __ldcg(p.lse2 + head + g);
+    const float4 s = __ldcg(reinterpret_cast<const float4*>(p.scores + (head + g) * p.c.capacity() + i));
     w.x += exp2_below(s.x, z);
     w.y += exp2_below(s.y, z);
     w.z += exp2_below(s.z, z);
@@ -986,8 +1007,8 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
   if (e != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   if (accumulate) {
-    decode_weight_kernel<<<dim3((p.c.capacity() + 4 * kWeightThreads - 1) / (4 * kWeightThreads), p.c.H, p.c.B), kWeightThreads, 0, s>>>(p, st);
-    if (cudaGetLastError() != cudaSuccess) return QKVP_ERR_CUDA;
+    const dim3 wgrid((p.c.capacity() + 4 * kWeightThreads - 1) / (4 * kWeightThreads), p.c.H, p.c.B);
+    if (launch_dependent(decode_weight_kernel, wgrid, kWeightThreads, s, p, st) != cudaSuccess) return QKVP_ERR_CUDA;
     mark(s);
   }
   return QKVP_OK;
