@@ -274,7 +274,8 @@ constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kSelectSmem = 200 * 1024;   // of keys, at most
+constexpr int kListed = 2048, kGathered = 4096;   // keys that share the first digit, of a block and of all
+constexpr int kSelectKeys = 176 * 1024 / 4;       // keys in shared memory, at most
 
 __device__ __forceinline__ uint32_t evict_key(float w, int pos, int64_t protect_above) {
   if (pos > protect_above) return 0xffffffffu;
@@ -299,30 +300,52 @@ __device__ __forceinline__ int4 ld_rank4(const int* p, uint32_t rank) {
   return v;
 }
 
-// Exclusive sum over the block's warps of one value per warp (0 where a lane
-// has none to give: every lane passes the warp's); *total receives the sum.
-__device__ __forceinline__ int warp_offsets(int mine, int* red, int* total) {
+// Sums over the block of one value per thread, in thread order: the
+// inclusive prefix up to this thread, and *total.  red: kSelectWarps ints.
+__device__ __forceinline__ int block_prefix(int v, int* red, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();
-  if (lane == 0) red[warp] = mine;
-  __syncthreads();
-  int v = lane < kSelectWarps ? red[lane] : 0;
+  int incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
   }
-  *total = __shfl_sync(0xffffffffu, v, 31);
-  return __shfl_sync(0xffffffffu, v, warp) - mine;
+  __syncthreads();   // red is free
+  if (lane == 31) red[warp] = incl;
+  __syncthreads();
+  const int w = lane < kSelectWarps ? red[lane] : 0;
+  *total = __reduce_add_sync(0xffffffffu, w);
+  return incl + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
 }
 
 struct __align__(16) SelectShared {
   int hist[3][kBins];
   // the block's slots with a larger, an equal key, below and above the budget (read as one int4)
   int above_lo, above_hi, ties_lo, ties_hi;
+  int4 warps[kSelectWarps];   // the same of its warps
   int red[kSelectWarps];
-  int newest, digit, need;
+  int newest, slice, listed, digit, need;
 };
+
+// Where, counted from the highest bin, does the sum of counts reach `need`
+// (which it does)?  `v`: the counts of bins top - 4 t - 0 .. 3 on thread t (0
+// past the bins).  Leaves the bin and what is still needed of it in x.digit
+// and x.need, for every thread after the barrier inside.
+__device__ __forceinline__ void find_digit(const int4& v, int top, int need, SelectShared& x) {
+  const int n[4] = {v.x, v.y, v.z, v.w};
+  const int sum = n[0] + n[1] + n[2] + n[3];
+  int total, before = block_prefix(sum, x.red, &total) - sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (before < need && need <= before + n[i]) {
+      x.digit = top - 4 * static_cast<int>(threadIdx.x) - i;
+      x.need = need - before;
+    }
+    before += n[i];
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ int4 reversed(const int4& v) { return make_int4(v.w, v.z, v.y, v.x); }
 
 // Workspace of an eviction: pairs of (freed, moving) slots and their number.
 struct EvictPairs {
@@ -335,7 +358,7 @@ template <int BLOCKS>
 __global__ void __launch_bounds__(kSelectThreads, 2)
     evict_select_kernel(CacheArgs c, int budget, int recent, int key_slots, int32_t* __restrict__ slots, EvictPairs pairs,
                         DevStatus st) {
-  extern __shared__ __align__(16) uint32_t keys[];   // [key_slots], or none
+  extern __shared__ __align__(16) uint32_t keys[];   // [key_slots], or none, then the lists
   __shared__ SelectShared x;
   constexpr int blocks = BLOCKS;   // of a cluster: their remote loads are issued together
   const int rank = BLOCKS > 1 ? cluster_rank() : 0;
@@ -352,6 +375,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   const int seg = ((n + blocks - 1) / blocks + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
   const int s0 = min(n, rank * seg), cnt = min(n, s0 + seg) - s0;
   for (int i = threadIdx.x; i < 3 * kBins; i += kSelectThreads) (&x.hist[0][0])[i] = 0;
+  if (threadIdx.x == 0) x.listed = 0;
   const bool cached = seg <= key_slots;
 
   // The newest position; the weights go into keys[] meanwhile.
@@ -383,16 +407,9 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
     return row < 0 ? 0u : evict_key(c.weight[row], c.pos[row], above);
   };
-  const auto count = [&](int pass, uint32_t key, uint32_t prefix) {
-    if (pass == 0) {
-      atomicAdd(&x.hist[0][key >> 21], 1);
-    } else if (pass == 1) {
-      if (key >> 21 == prefix) atomicAdd(&x.hist[1][(key >> 10) & 2047], 1);
-    } else {
-      if (key >> 10 == prefix) atomicAdd(&x.hist[2][key & 1023], 1);
-    }
-  };
-  if (cached)   // (each thread finds the weights that it has put there; the positions come from L1 or L2)
+
+  // First digit: the highest 11 bits (sign, exponent and two of the mantissa).
+  if (cached) {   // (each thread finds the weights that it has put there; the positions come from L1 or L2)
 #pragma unroll 2
     for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {
       const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
@@ -404,54 +421,120 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
                        evict_key(w.w, p.w, above));
       }
       *reinterpret_cast<uint4*>(keys + i) = k;
-      count(0, k.x, 0);
-      if (i + 1 < cnt) count(0, k.y, 0);
-      if (i + 2 < cnt) count(0, k.z, 0);
-      if (i + 3 < cnt) count(0, k.w, 0);
+      atomicAdd(&x.hist[0][k.x >> 21], 1);
+      if (i + 1 < cnt) atomicAdd(&x.hist[0][k.y >> 21], 1);
+      if (i + 2 < cnt) atomicAdd(&x.hist[0][k.z >> 21], 1);
+      if (i + 3 < cnt) atomicAdd(&x.hist[0][k.w >> 21], 1);
     }
-  uint32_t prefix = 0;
+  } else {
+    for (int i = threadIdx.x; i < cnt; i += kSelectThreads) atomicAdd(&x.hist[0][key_of(i) >> 21], 1);
+  }
+  cluster_sync_all();
   int need = budget;
-  for (int pass = 0; pass < 3; ++pass) {
-    if (pass > 0 || !cached)
-#pragma unroll 4
-      for (int i = threadIdx.x; i < cnt; i += kSelectThreads) count(pass, key_of(i), prefix);
+  if (blocks == 1) {
+    find_digit(reversed(*reinterpret_cast<const int4*>(&x.hist[0][kBins - 4 - 4 * threadIdx.x])), kBins - 1, need, x);
+  } else {
+    // Each block adds up its part of the bins; all then read the sums of the
+    // parts, and of the part that the digit lies in its bins.  (Every block
+    // reading every bin of every block took 3 us a digit.)
+    constexpr int PART = kBins / blocks;
+    int4 v = make_int4(0, 0, 0, 0);
+    if (4 * threadIdx.x < PART) {
+      int4 q[blocks];
+#pragma unroll
+      for (int r = 0; r < blocks; ++r) q[r] = ld_rank4(&x.hist[0][rank * PART + 4 * threadIdx.x], r);
+#pragma unroll
+      for (int r = 0; r < blocks; ++r) {
+        v.x += q[r].x;
+        v.y += q[r].y;
+        v.z += q[r].z;
+        v.w += q[r].w;
+      }
+      *reinterpret_cast<int4*>(&x.hist[1][4 * threadIdx.x]) = v;
+    }
+    int total;
+    block_prefix(v.x + v.y + v.z + v.w, x.red, &total);
+    if (threadIdx.x == 0) x.slice = total;
     cluster_sync_all();
-    // bins from the highest, four a thread: where does the sum reach `need`?
-    constexpr int PER = kBins / kSelectThreads;
-    const int hi = kBins - 1 - PER * threadIdx.x;
-    int v[PER], sum = 0;
+    int sums[blocks], part = blocks - 1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = 0;
-    int4 q[blocks];
+    for (int r = 0; r < blocks; ++r) sums[r] = ld_rank(&x.slice, r);
 #pragma unroll
-    for (int r = 0; r < blocks; ++r) q[r] = ld_rank4(&x.hist[pass][hi - 3], r);
+    for (int r = blocks - 1; r > 0; --r)
+      if (part == r && sums[r] < need) {
+        need -= sums[r];
+        part = r - 1;
+      }
+    v = make_int4(0, 0, 0, 0);
+    if (4 * threadIdx.x < PART) v = reversed(ld_rank4(&x.hist[1][PART - 4 - 4 * threadIdx.x], part));
+    find_digit(v, part * PART + PART - 1, need, x);
+  }
+  uint32_t prefix = x.digit;
+  need = x.need;
+
+  // The keys with that digit, gathered from the whole cluster, are few unless
+  // weights repeat: then every block finds the other digits by itself.
+  uint32_t* listed = keys + key_slots;   // [kListed] of this block, then [kGathered] of all
+  uint32_t* gathered = listed + kListed;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < cnt; i += kSelectThreads) {
+    const uint32_t key = key_of(i);
+    if (key >> 21 == prefix) {
+      const int at = atomicAdd(&x.listed, 1);
+      if (at < kListed) listed[at] = key;
+    }
+  }
+  cluster_sync_all();   // (also: the part sums in hist[1] have been read)
+  int counts[blocks], all = 0;
+  bool few = true;
+#pragma unroll
+  for (int r = 0; r < blocks; ++r) {
+    counts[r] = ld_rank(&x.listed, r);
+    few = few && counts[r] <= kListed;
+    all += counts[r];
+  }
+  few = few && all <= kGathered;
+  if (blocks > 1)   // clear what the part sums have used
+    for (int i = threadIdx.x; i < kBins; i += kSelectThreads) x.hist[1][i] = 0;
+  if (few) {
+    int at = 0;
 #pragma unroll
     for (int r = 0; r < blocks; ++r) {
-      v[0] += q[r].w;
-      v[1] += q[r].z;
-      v[2] += q[r].y;
-      v[3] += q[r].x;
+      for (int i = threadIdx.x; i < counts[r]; i += kSelectThreads)
+        gathered[at + i] = ld_rank(reinterpret_cast<const int*>(listed + i), r);
+      at += counts[r];
     }
+  } else if (blocks > 1) {
+    cluster_sync_all();   // every block's hist[1] is clear
+  }
+  __syncthreads();
+  for (int pass = 1; pass < 3; ++pass) {
+    const auto count = [&](uint32_t key) {
+      if (pass == 1 ? key >> 21 == prefix : key >> 10 == prefix)
+        atomicAdd(&x.hist[pass][pass == 1 ? (key >> 10) & 2047 : key & 1023], 1);
+    };
+    int4 v = make_int4(0, 0, 0, 0);
+    const int first = kBins - 4 - 4 * threadIdx.x;
+    if (few) {
+      for (int i = threadIdx.x; i < all; i += kSelectThreads) count(gathered[i]);
+      __syncthreads();
+      v = *reinterpret_cast<const int4*>(&x.hist[pass][first]);
+    } else {
+      for (int i = threadIdx.x; i < cnt; i += kSelectThreads) count(key_of(i));
+      cluster_sync_all();
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum += v[i];
-    int incl = sum, total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
-    }
-    int before = warp_offsets(__shfl_sync(0xffffffffu, incl, 31), x.red, &total) + incl - sum;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (before < need && need <= before + v[i]) {
-        x.digit = hi - i;
-        x.need = need - before;
+      for (int r = 0; r < blocks; ++r) {
+        const int4 q = ld_rank4(&x.hist[pass][first], r);
+        v.x += q.x;
+        v.y += q.y;
+        v.z += q.z;
+        v.w += q.w;
       }
-      before += v[i];
     }
-    __syncthreads();
-    prefix = pass == 2 ? prefix << 10 | x.digit : prefix << 11 | x.digit;
+    find_digit(reversed(v), kBins - 1, need, x);
+    prefix = pass == 1 ? prefix << 11 | x.digit : prefix << 10 | x.digit;
     need = x.need;
+    __syncthreads();   // x.digit is read
   }
   // kept: keys above `prefix`, and the first `need` slots whose key equals it
 
@@ -459,6 +542,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   // budget, and those of the slots before: in lower blocks, in lower warps.
   const int wseg = seg / kSelectWarps, i0 = min(cnt, warp * wseg), i1 = min(cnt, i0 + wseg);
   int a_lo = 0, a_hi = 0, t_lo = 0, t_hi = 0;
+#pragma unroll 2
   for (int i = i0 + lane; i - lane < i1; i += 32) {
     const bool in = i < i1, lo = s0 + i < budget;
     const uint32_t key = in ? key_of(i) : 0u;
@@ -469,17 +553,18 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     t_lo += __popc(t & m);
     t_hi += __popc(t & ~m);
   }
-  int total_a_lo, total_a_hi, total_t_lo, total_t_hi;
-  a_lo = warp_offsets(a_lo, x.red, &total_a_lo);
-  a_hi = warp_offsets(a_hi, x.red, &total_a_hi);
-  t_lo = warp_offsets(t_lo, x.red, &total_t_lo);
-  t_hi = warp_offsets(t_hi, x.red, &total_t_hi);
-  if (threadIdx.x == 0) {
-    x.above_lo = total_a_lo;
-    x.above_hi = total_a_hi;
-    x.ties_lo = total_t_lo;
-    x.ties_hi = total_t_hi;
+  if (lane == 0) x.warps[warp] = make_int4(a_lo, a_hi, t_lo, t_hi);
+  __syncthreads();
+  const int4 wv = lane < kSelectWarps ? x.warps[lane] : make_int4(0, 0, 0, 0);
+  if (warp == 0) {
+    const int ta = __reduce_add_sync(0xffffffffu, wv.x), tb = __reduce_add_sync(0xffffffffu, wv.y);
+    const int tc = __reduce_add_sync(0xffffffffu, wv.z), td = __reduce_add_sync(0xffffffffu, wv.w);
+    if (lane == 0) *reinterpret_cast<int4*>(&x.above_lo) = make_int4(ta, tb, tc, td);
   }
+  a_lo = __reduce_add_sync(0xffffffffu, lane < warp ? wv.x : 0);
+  a_hi = __reduce_add_sync(0xffffffffu, lane < warp ? wv.y : 0);
+  t_lo = __reduce_add_sync(0xffffffffu, lane < warp ? wv.z : 0);
+  t_hi = __reduce_add_sync(0xffffffffu, lane < warp ? wv.w : 0);
   cluster_sync_all();
   int all_t_lo = 0, all_a_lo = 0;
   int4 others[blocks];
@@ -527,17 +612,18 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
 
 // ---------------------------------------------------------------------------
 // Eviction: the moves, and the lengths.  Reads and writes the rows that move,
-// 16 bytes a lane: a warp takes 16 pairs and copies one row (E4M3: two) a step
-// with four steps' loads in flight.  Sources lie at or above the budget and
-// destinations below it, so no copy disturbs another.
+// 16 bytes a lane: a warp takes 32 pairs and copies one row (E4M3: two) a step,
+// the next four steps' loads on their way before the last four are stored.
+// Sources lie at or above the budget and destinations below it, so no copy
+// disturbs another.
 // ---------------------------------------------------------------------------
-constexpr int kMovePairs = 16;   // of a warp
+constexpr int kMoveWarps = 1;   // one: 77 us for the prompts' eviction, two 87, eight 103 (blocks end one by one)
 
 template <bool FP8>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kMoveWarps)
     evict_move_kernel(CacheArgs c, int budget, int32_t* __restrict__ slots, EvictPairs pairs, int32_t* lengths_out,
                       DevStatus st) {
-  constexpr int ES = FP8 ? 1 : 2, VC = kDv * ES / 16, ROWS = FP8 ? 2 : 1, STEPS = 4;
+  constexpr int ES = FP8 ? 1 : 2, VC = kDv * ES / 16, ROWS = FP8 ? 2 : 1, STEPS = 4, BATCH = STEPS * ROWS;
   const int kc = c.d * ES / 16;
   const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
   const int64_t piece = static_cast<int64_t>(b) * c.H + h;
@@ -546,25 +632,24 @@ __global__ void __launch_bounds__(256)
     const int n = c.lengths[b], cap = c.capacity();
     lengths_out[b] = min(budget, max(0, min(n, cap)));
   }
-  const int j0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kMovePairs;
-  const int n = min(kMovePairs, __ldcg(pairs.count + piece) - j0);
+  const int j0 = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * 32;
+  const int n = min(32, __ldcg(pairs.count + piece) - j0);
   if (n <= 0) return;
-  int src = -1, dst = -1;
+  int src = -1, dst = -1, to_slot = 0, from_slot = 0;
+  float w = 0.f, ks = 0.f, vs = 0.f;
+  int p = 0;
   if (lane < n) {
-    const int to = __ldcg(pairs.freed + piece * budget + j0 + lane), from = __ldcg(pairs.moving + piece * budget + j0 + lane);
-    slots[piece * budget + to] = from;
-    src = cache_row(c, b, h, from, st, KID_EVICT_MOVE);
-    dst = cache_row(c, b, h, to, st, KID_EVICT_MOVE);
+    to_slot = __ldcg(pairs.freed + piece * budget + j0 + lane);
+    from_slot = __ldcg(pairs.moving + piece * budget + j0 + lane);
+    src = cache_row(c, b, h, from_slot, st, KID_EVICT_MOVE);
+    dst = cache_row(c, b, h, to_slot, st, KID_EVICT_MOVE);
     if (src < 0) dst = -1;
     if (dst >= 0) {
-      const float w = c.weight[src];
-      const int p = c.pos[src];
-      const float ks = FP8 ? c.k_scale[src] : 0.f, vs = FP8 ? c.v_scale[src] : 0.f;
-      c.weight[dst] = w;
-      c.pos[dst] = p;
+      w = c.weight[src];
+      p = c.pos[src];
       if (FP8) {
-        c.k_scale[dst] = ks;
-        c.v_scale[dst] = vs;
+        ks = c.k_scale[src];
+        vs = c.v_scale[src];
       }
     }
   }
@@ -573,20 +658,38 @@ __global__ void __launch_bounds__(256)
   const uint4* from = reinterpret_cast<const uint4*>(is_k ? c.k : c.v);
   uint4* to = reinterpret_cast<uint4*>(is_k ? c.k : c.v);
   const int chunks = is_k ? kc : VC, ch = is_k ? l : l - kc;
-  for (int i0 = 0; i0 < n; i0 += STEPS * ROWS) {
-    uint4 r[STEPS];
-    int d[STEPS];
+  const auto load = [&](int i0, uint4 (&r)[STEPS], int (&d)[STEPS]) {
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const int w = i0 + i * ROWS + part;   // (past the last pair: a lane that has none)
-      const int s = __shfl_sync(0xffffffffu, src, w & 31);
-      d[i] = __shfl_sync(0xffffffffu, dst, w & 31);
-      if (l >= kc + VC) d[i] = -1;
-      if (d[i] >= 0) r[i] = from[static_cast<int64_t>(s) * chunks + ch];
+      const int pair = i0 + i * ROWS + part;
+      const int s = __shfl_sync(0xffffffffu, src, pair & 31);
+      d[i] = __shfl_sync(0xffffffffu, dst, pair & 31);
+      if (l >= kc + VC || pair >= n) d[i] = -1;
+      if (d[i] >= 0) r[i] = __ldcg(from + static_cast<int64_t>(s) * chunks + ch);
     }
+  };
+  const auto store = [&](const uint4 (&r)[STEPS], const int (&d)[STEPS]) {
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
       if (d[i] >= 0) to[static_cast<int64_t>(d[i]) * chunks + ch] = r[i];
+  };
+  uint4 r0[STEPS], r1[STEPS];
+  int d0[STEPS], d1[STEPS];
+  load(0, r0, d0);
+  for (int i0 = 0; i0 < n; i0 += 2 * BATCH) {
+    load(i0 + BATCH, r1, d1);
+    store(r0, d0);
+    load(i0 + 2 * BATCH, r0, d0);
+    store(r1, d1);
+  }
+  if (lane < n) slots[piece * budget + to_slot] = from_slot;
+  if (dst >= 0) {
+    c.weight[dst] = w;
+    c.pos[dst] = p;
+    if (FP8) {
+      c.k_scale[dst] = ks;
+      c.v_scale[dst] = vs;
+    }
   }
 }
 
@@ -598,7 +701,8 @@ cudaError_t launch_evict_select_n(const CacheArgs& c, int budget, int recent, in
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(evict_select_kernel<BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
+    e = cudaFuncSetAttribute(evict_select_kernel<BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (kSelectKeys + kListed + kGathered) * 4);
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
@@ -606,7 +710,7 @@ cudaError_t launch_evict_select_n(const CacheArgs& c, int budget, int recent, in
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(c.H * BLOCKS, c.B);
   cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(key_slots) * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(key_slots + kListed + kGathered) * 4;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = BLOCKS;
@@ -628,9 +732,9 @@ cudaError_t launch_evict_select(const CacheArgs& c, int budget, int recent, int 
   };
   int blocks = 1;
   while (blocks < kMaxCluster && ((per_block(blocks) > 2048 && 2 * blocks * pieces <= 2 * sms) ||
-                                  per_block(blocks) * 4 > kSelectSmem))
+                                  per_block(blocks) > kSelectKeys))
     blocks *= 2;
-  const int key_slots = per_block(blocks) * 4 <= kSelectSmem ? per_block(blocks) : 0;
+  const int key_slots = per_block(blocks) <= kSelectKeys ? per_block(blocks) : 0;
   switch (blocks) {
     case 1: return launch_evict_select_n<1>(c, budget, recent, key_slots, slots, pairs, st, s);
     case 2: return launch_evict_select_n<2>(c, budget, recent, key_slots, slots, pairs, st, s);
@@ -703,8 +807,8 @@ int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* s
   mark(s);
   if (launch_evict_select(a, budget, recent, sms, slots, pairs, st, s) != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
-  const dim3 grid((budget + 8 * kMovePairs - 1) / (8 * kMovePairs), a.H, a.B);
-  if (launch_dependent(cache->fp8 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 256, s, a, budget, slots,
+  const dim3 grid((budget + 32 * kMoveWarps - 1) / (32 * kMoveWarps), a.H, a.B);
+  if (launch_dependent(cache->fp8 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 32 * kMoveWarps, s, a, budget, slots,
                        pairs, lengths_out, st) != cudaSuccess)
     return QKVP_ERR_CUDA;
   mark(s);
