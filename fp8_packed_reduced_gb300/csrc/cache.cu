@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 3;
   const int h = blockIdx.y;
   const int t0 = (blockIdx.x * (kAppendThreads / 32) + warp) * 8, t = t0 + (lane >> 2);
+  wait_for_previous();
 
   uint4 kx[KN], vx[VN];
   if (t < T) {
@@ -243,9 +244,8 @@ cudaError_t launch_append(const CacheArgs& c, int T, const uint16_t* k, const ui
                           const int32_t* cu, int32_t* lengths_out, unsigned int* arrived, DevStatus st,
                           cudaStream_t s) {
   const dim3 grid(std::max(1, (T + kAppendThreads / 4 - 1) / (kAppendThreads / 4)), c.H);
-  append_kernel<D, FP8><<<grid, kAppendThreads, 0, s>>>(c, T, k, v, pos, cu, lengths_out, lengths_out == c.lengths,
-                                                        arrived, st);
-  return cudaGetLastError();
+  return launch_dependent(append_kernel<D, FP8>, grid, kAppendThreads, 0, s, c, T, k, v, pos, cu, lengths_out,
+                          static_cast<int>(lengths_out == c.lengths), arrived, st);
 }
 
 template <bool FP8>
@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   constexpr int blocks = BLOCKS;   // of a cluster: their remote loads are issued together
   const int rank = BLOCKS > 1 ? cluster_rank() : 0;
   const int h = blockIdx.x / blocks, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_previous();
   const int n = checked_length(c, b, st, KID_EVICT_SELECT);
   const int64_t piece = static_cast<int64_t>(b) * c.H + h;
   slots += piece * budget;
@@ -707,7 +708,7 @@ cudaError_t launch_evict_select_n(const CacheArgs& c, int budget, int recent, in
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(c.H * BLOCKS, c.B);
   cfg.blockDim = dim3(kSelectThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(key_slots + kListed + kGathered) * 4;
@@ -716,8 +717,10 @@ cudaError_t launch_evict_select_n(const CacheArgs& c, int budget, int recent, in
   attr[0].val.clusterDim.x = BLOCKS;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, evict_select_kernel<BLOCKS>, c, budget, recent, key_slots, slots, pairs, st);
 }
 
@@ -808,7 +811,7 @@ int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* s
   if (launch_evict_select(a, budget, recent, sms, slots, pairs, st, s) != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   const dim3 grid((budget + 32 * kMoveWarps - 1) / (32 * kMoveWarps), a.H, a.B);
-  if (launch_dependent(cache->fp8 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 32 * kMoveWarps, s, a, budget, slots,
+  if (launch_dependent(cache->fp8 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 32 * kMoveWarps, 0, s, a, budget, slots,
                        pairs, lengths_out, st) != cudaSuccess)
     return QKVP_ERR_CUDA;
   mark(s);

@@ -36,9 +36,10 @@ struct CacheArgs {
 };
 
 // The length of sequence b, clamped to what its pages can hold; a length
-// outside [0, capacity] is recorded.
+// outside [0, capacity] is recorded.  L2: past L1.
+template <bool L2 = false>
 __device__ __forceinline__ int checked_length(const CacheArgs& c, int b, const DevStatus& st, int kid) {
-  const int n = __ldg(c.lengths + b), cap = c.capacity();
+  const int n = L2 ? __ldcg(c.lengths + b) : __ldg(c.lengths + b), cap = c.capacity();
   if (n < 0 || n > cap) {
     record_error(st, QKVP_ERR_DEVICE_INPUT, kid);
     return n < 0 ? 0 : cap;
@@ -49,8 +50,10 @@ __device__ __forceinline__ int checked_length(const CacheArgs& c, int b, const D
 // Row (of the pools seen as [P * H * page, ...]) of slot `slot` of sequence
 // b, head h; -1, recorded, when its page lies outside the pool.  The caller
 // has checked 0 <= slot < capacity.
+template <bool L2 = false>
 __device__ __forceinline__ int cache_row(const CacheArgs& c, int b, int h, int slot, const DevStatus& st, int kid) {
-  const int pid = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + (slot >> c.page_shift));
+  const int* at = c.table + static_cast<int64_t>(b) * c.max_pages + (slot >> c.page_shift);
+  const int pid = L2 ? __ldcg(at) : __ldg(at);
   if (pid < 0 || pid >= c.P) {
     record_error(st, QKVP_ERR_DEVICE_INPUT, kid);
     return -1;
@@ -59,18 +62,20 @@ __device__ __forceinline__ int cache_row(const CacheArgs& c, int b, int h, int s
 }
 
 // A kernel launched by launch_dependent may start before the one ahead of it
-// in its stream is done, when every block of that one has left or has called
-// allow_dependents.  Every thread calls wait_for_previous before it touches
-// what the kernel ahead writes, and before it returns.
+// in its stream is done: when every block of that one has left or has called
+// allow_dependents (a kernel of another library does not, so nothing of ours
+// runs beside it).  Every thread calls wait_for_previous before it touches
+// what the kernels ahead write, and before it returns.
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <class... KArgs, class... Args>
-cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, cudaStream_t s, Args&&... args) {
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -41,7 +41,7 @@ namespace qkvp {
 namespace {
 
 constexpr int kMaxWarps = 12;
-constexpr int kWeightThreads = 256;
+constexpr int kWeightThreads = 256;        // at most
 constexpr int kMaxBlocks = 160;            // one per SM, and the workspace's bound
 constexpr int kSmemMax = 232448 - 1024;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -358,6 +358,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   const int B = p.c.B, Hq = p.c.H * p.G, nrec = record_floats(p.nh);
   const auto head_of = [&](int t, int e) { return E == 1 ? c : 8 * t + 2 * c + e; };   // of this lane's scores
 
+  wait_for_previous();
+  // The page table is first needed after the lengths: it comes into L2 meanwhile.
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 32; i < static_cast<int64_t>(B) * p.c.max_pages;
+       i += static_cast<int64_t>(gridDim.x) * kThreads * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.c.table + i));
+
   // --- the list of units -------------------------------------------------
   int* prefix = reinterpret_cast<int*>(smem);
   int* length = prefix + B + 1;
@@ -380,16 +386,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   const Plan pl{prefix, length, B, p.c.H * p.chunks};
   const int64_t total = static_cast<int64_t>(run) * pl.Hv;
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  // Even parts, [c0, c1) for the block.  But where a block for every piece
-  // makes no warp's part longer by more than a few units, it has one: nothing
-  // is then joined across blocks, which costs about as much as four units
-  // (3 us against 0.7 each).
-  int64_t part = (total + nwarps - 1) / nwarps;
-  int64_t c0 = min(total, blockIdx.x * kWarps * part), c1 = min(total, c0 + kWarps * part);
+  // Even parts, [c0, c1) for the block.  An end of it that lies within one
+  // warp's part of a piece's end moves there: a piece cut between blocks costs
+  // about 5 us (two rounds through L2 after the last load).
+  const int64_t even = (total + nwarps - 1) / nwarps;
+  int64_t part = even;
+  const auto block_start = [&](int64_t blk) {
+    const int64_t f = blk * kWarps * even;
+    if (f >= total) return total;
+    const Piece pc = piece_of(pl, f);
+    return f - pc.start <= even && f - pc.start <= pc.end - f ? pc.start : pc.end - f <= even ? pc.end : f;
+  };
+  int64_t c0 = block_start(blockIdx.x), c1 = block_start(blockIdx.x + 1);
+  if (c1 - c0 > 0) part = (c1 - c0 + kWarps - 1) / kWarps;
+  // But where a block for every piece makes no warp's part longer by more than
+  // a few units (0.7 us each), it has one.
   if (static_cast<int64_t>(B) * pl.Hv <= gridDim.x) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) longest = max(longest, red_max[w]);
-    if ((longest + kWarps * KS - 1) / (kWarps * KS) <= part + 4) {
+    if ((longest + kWarps * KS - 1) / (kWarps * KS) <= even + 4) {
       const int b = blockIdx.x / pl.Hv, hv = blockIdx.x % pl.Hv;
       c0 = c1 = 0;
       if (b < B) {
@@ -400,7 +415,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
       }
     }
   }
-
   // sequences without a live slot
   for (int b = blockIdx.x; b < B; b += gridDim.x)
     if (length[b] == 0) {
@@ -489,9 +503,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
 
   // The pieces at the block's ends and at the end of the warp's part, while the
   // first loads are on their way.
-  __shared__ Piece ends[2];
-  if (threadIdx.x == 0) ends[0] = piece_of(pl, c0);
-  if (threadIdx.x == 32) ends[1] = piece_of(pl, c1 - 1);
+  struct End {
+    Piece piece;
+    int first, last;   // the blocks that hold it
+  };
+  __shared__ End ends[2];
+  if (lane == 0 && warp < 2) {
+    // the block that holds unit f, from where it would be with even parts
+    const auto block_of = [&](int64_t f) {
+      int64_t blk = f / (kWarps * even);
+      while (f < block_start(blk)) --blk;
+      while (f >= block_start(blk + 1)) ++blk;
+      return static_cast<int>(blk);
+    };
+    End e;
+    e.piece = piece_of(pl, warp == 0 ? c0 : c1 - 1);
+    e.first = e.last = blockIdx.x;
+    if (e.piece.start < c0) e.first = block_of(e.piece.start);
+    if (e.piece.end > c1) e.last = block_of(e.piece.end - 1);
+    ends[warp] = e;
+  }
   const Piece last_piece = piece_of(pl, count > 0 ? f1 - 1 : c1 - 1);
 
   uint4 qf[NT][D / 32];           // q of column 8 t + g: chunk c of every 32 dims
@@ -758,7 +789,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   if (count > 0) flush(last_piece.end == f1);
   __syncthreads();
   allow_dependents();
-  const Piece head = ends[0], tail = ends[1];
+  const Piece &head = ends[0].piece, &tail = ends[1].piece;
   const int part32 = static_cast<int>(part);   // (a block's parts together are below 2^31 units)
   const auto warp_of = [&](int64_t f) { return static_cast<int>(static_cast<unsigned int>(f - c0) / part32); };
   const auto join_warps = [&](const Piece& pc, int n) {   // the records of one piece in this block
@@ -786,8 +817,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
       const Piece& pc = threadIdx.x == 0 ? head : tail;
       is_last[threadIdx.x] = 0;
       if (threadIdx.x == 0 ? over0 : over1) {
-        const int64_t per = kWarps * part;
-        const unsigned int blocks = static_cast<unsigned int>((pc.end - 1) / per - pc.start / per + 1);
+        const unsigned int blocks = ends[threadIdx.x].last - ends[threadIdx.x].first + 1;
         unsigned int* cnt = p.arrived + static_cast<int64_t>(pc.b) * pl.Hv + pc.hv;
         if (count_arrival(cnt) == blocks - 1) {   // releases the block's record, acquires the others'
           is_last[threadIdx.x] = 1;
@@ -808,8 +838,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   for (int side = 0; side < 2; ++side) {
     if (!is_last[side]) continue;
     const Piece& pc = side == 0 ? head : tail;
-    const int64_t per = kWarps * part;
-    const int b0 = static_cast<int>(pc.start / per), nb = static_cast<int>((pc.end - 1) / per) - b0 + 1, nh = heads_in(pc);
+    const int b0 = ends[side].first, nb = ends[side].last - b0 + 1, nh = heads_in(pc);
     // a warp per head, or with many records and few heads, several
     const int split = nb > 8 ? max(1, kWarps / nh) : 1, each = (nb + split - 1) / split;
     for (int i = warp; i < nh * split; i += kWarps) {
@@ -835,12 +864,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
 // weight += the probabilities of the head's query heads.  Four slots a thread:
 // a page and the row of scores both begin on 16 of them.
 __global__ void __launch_bounds__(kWeightThreads) decode_weight_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
-  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = (blockIdx.x * kWeightThreads + threadIdx.x) * 4;
-  const int n = checked_length(p.c, b, st, KID_DECODE_WEIGHT);
-  const int row = i < n ? cache_row(p.c, b, h, i, st, KID_DECODE_WEIGHT) : -1;
+  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  // What the attention does not write is read ahead of its end, from L2 (which
+  // the kernels before it have left up to date; it has waited for them).
+  const int n = checked_length<true>(p.c, b, st, KID_DECODE_WEIGHT);
+  const int row = i < n ? cache_row<true>(p.c, b, h, i, st, KID_DECODE_WEIGHT) : -1;
   float4* at = reinterpret_cast<float4*>(p.c.weight + max(row, 0));
   float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (row >= 0) old = *at;   // the attention does not write it
+  if (row >= 0) old = __ldcg(at);
   wait_for_previous();
   if (row < 0) return;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -917,8 +948,7 @@ cudaError_t launch_decode_s(const DecodeParams& p, int grid, int smem, DevStatus
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
-  decode_kernel<D, FP8, NT, E, W, S><<<grid, 32 * W, smem, s>>>(p, st);
-  return cudaGetLastError();
+  return launch_dependent(decode_kernel<D, FP8, NT, E, W, S>, dim3(grid), 32 * W, smem, s, p, st);
 }
 
 // Shared memory of W warps with S stages; with the warps' records where they
@@ -1007,8 +1037,9 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
   if (e != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   if (accumulate) {
-    const dim3 wgrid((p.c.capacity() + 4 * kWeightThreads - 1) / (4 * kWeightThreads), p.c.H, p.c.B);
-    if (launch_dependent(decode_weight_kernel, wgrid, kWeightThreads, s, p, st) != cudaSuccess) return QKVP_ERR_CUDA;
+    const int threads = std::min(kWeightThreads, (p.c.capacity() / 4 + 31) / 32 * 32);   // four slots each
+    const dim3 wgrid((p.c.capacity() + 4 * threads - 1) / (4 * threads), p.c.H, p.c.B);
+    if (launch_dependent(decode_weight_kernel, wgrid, threads, 0, s, p, st) != cudaSuccess) return QKVP_ERR_CUDA;
     mark(s);
   }
   return QKVP_OK;
