@@ -185,6 +185,13 @@ struct Plan {
   int B, Hv;
 };
 
+// Quotients of numbers that are below 2^31 but for caches of the largest size:
+// a 64-bit division is several times as long.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? static_cast<int64_t>(static_cast<unsigned int>(a) / static_cast<unsigned int>(b)) : a / b;
+}
+__device__ __forceinline__ int64_t divide_up(int64_t a, int64_t b) { return divide(a + b - 1, b); }
+
 // A (sequence, head, chunk) as a piece of the list.
 struct Piece {
   int64_t start, end;
@@ -203,9 +210,7 @@ __device__ __forceinline__ Piece piece_of(const Plan& pl, int64_t f) {
   const int64_t base = static_cast<int64_t>(pl.prefix[lo]) * pl.Hv, rest = f - base;
   Piece r;
   r.b = lo;
-  // (a 64-bit division is several times as long)
-  r.hv = rest <= INT_MAX ? static_cast<int>(static_cast<unsigned int>(rest) / static_cast<unsigned int>(per))
-                         : static_cast<int>(rest / per);
+  r.hv = static_cast<int>(divide(rest, per));
   r.start = base + static_cast<int64_t>(r.hv) * per;
   r.end = r.start + per;
   return r;
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   // Even parts, [c0, c1) for the block.  An end of it that lies within one
   // warp's part of a piece's end moves there: a piece cut between blocks costs
   // about 5 us (two rounds through L2 after the last load).
-  const int64_t even = (total + nwarps - 1) / nwarps;
+  const int64_t even = divide_up(total, nwarps);
   int64_t part = even;
   const auto block_start = [&](int64_t blk) {
     const int64_t f = blk * kWarps * even;
@@ -397,7 +402,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
     const Piece pc = piece_of(pl, f);
     return f - pc.start <= even && f - pc.start <= pc.end - f ? pc.start : pc.end - f <= even ? pc.end : f;
   };
-  int64_t c0 = block_start(blockIdx.x), c1 = block_start(blockIdx.x + 1);
+  const int64_t start = block_start(blockIdx.x + (lane & 1));   // both ends at once
+  int64_t c0 = __shfl_sync(0xffffffffu, start, 0), c1 = __shfl_sync(0xffffffffu, start, 1);
   if (c1 - c0 > 0) part = (c1 - c0 + kWarps - 1) / kWarps;
   // But where a block for every piece makes no warp's part longer by more than
   // a few units (0.7 us each), it has one.
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   if (lane == 0 && warp < 2) {
     // the block that holds unit f, from where it would be with even parts
     const auto block_of = [&](int64_t f) {
-      int64_t blk = f / (kWarps * even);
+      int64_t blk = divide(f, kWarps * even);
       while (f < block_start(blk)) --blk;
       while (f >= block_start(blk + 1)) ++blk;
       return static_cast<int>(blk);
