@@ -296,6 +296,10 @@ __device__ __forceinline__ int ld_rank(const int* p, uint32_t rank) {
   return v;
 }
 
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ int4 ld_rank4(const int* p, uint32_t rank) {
   int4 v;
   asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
@@ -329,13 +333,14 @@ struct __align__(16) SelectShared {
   int above_lo, above_hi, ties_lo, ties_hi;
   int4 warps[kSelectWarps];   // the same of its warps
   int red[kSelectWarps];
-  int newest, slice, listed, digit, need;
+  int newest, slice, listed, digit, need, ties;
 };
 
 // Where, counted from the highest bin, does the sum of counts reach `need`
 // (which it does)?  `v`: the counts of bins top - 4 t - 0 .. 3 on thread t (0
-// past the bins).  Leaves the bin and what is still needed of it in x.digit
-// and x.need, for every thread after the barrier inside.
+// past the bins).  Leaves the bin, what is still needed of it and what it
+// holds in x.digit, x.need and x.ties, for every thread after the barrier
+// inside.
 __device__ __forceinline__ void find_digit(const int4& v, int top, int need, SelectShared& x) {
   const int n[4] = {v.x, v.y, v.z, v.w};
   const int sum = n[0] + n[1] + n[2] + n[3];
@@ -345,6 +350,7 @@ __device__ __forceinline__ void find_digit(const int4& v, int top, int need, Sel
     if (before < need && need <= before + n[i]) {
       x.digit = top - 4 * static_cast<int>(threadIdx.x) - i;
       x.need = need - before;
+      x.ties = n[i];
     }
     before += n[i];
   }
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
 
   // The newest position; the weights go into keys[] meanwhile.
   int newest = INT_MIN;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {   // four slots lie in one page
     const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
     if (row < 0) continue;
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
 
   // First digit: the highest 11 bits (sign, exponent and two of the mantissa).
   if (cached) {   // (each thread finds the weights that it has put there; the positions come from L1 or L2)
-#pragma unroll 2
+#pragma unroll 4
     for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {
       const int row = cache_row(c, b, h, s0 + i, st, KID_EVICT_SELECT);
       uint4 k = make_uint4(0, 0, 0, 0);
@@ -483,12 +489,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   uint32_t* listed = keys + key_slots;   // [kListed] of this block, then [kGathered] of all
   uint32_t* gathered = listed + kListed;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < cnt; i += kSelectThreads) {
-    const uint32_t key = key_of(i);
-    if (key >> 21 == prefix) {
-      const int at = atomicAdd(&x.listed, 1);
-      if (at < kListed) listed[at] = key;
-    }
+  for (int i = threadIdx.x; i - lane < cnt; i += kSelectThreads) {
+    const uint32_t key = i < cnt ? key_of(i) : 0u;
+    const bool mine = i < cnt && key >> 21 == prefix;
+    const unsigned int m = __ballot_sync(0xffffffffu, mine);
+    if (m == 0) continue;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&x.listed, __popc(m));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+    if (mine && at < kListed) listed[at] = key;
   }
   cluster_sync_all();   // (also: the part sums in hist[1] have been read)
   int counts[blocks], all = 0;
@@ -503,12 +512,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   if (blocks > 1)   // clear what the part sums have used
     for (int i = threadIdx.x; i < kBins; i += kSelectThreads) x.hist[1][i] = 0;
   if (few) {
-    int at = 0;
+    for (int i = threadIdx.x; i < all; i += kSelectThreads) {
+      int r = 0, at = i;   // the block that has listed it, and where
 #pragma unroll
-    for (int r = 0; r < blocks; ++r) {
-      for (int i = threadIdx.x; i < counts[r]; i += kSelectThreads)
-        gathered[at + i] = ld_rank(reinterpret_cast<const int*>(listed + i), r);
-      at += counts[r];
+      for (int k = 0; k < blocks - 1; ++k)
+        if (r == k && at >= counts[k]) {
+          at -= counts[k];
+          r = k + 1;
+        }
+      gathered[i] = ld_rank(reinterpret_cast<const int*>(listed + at), r);
     }
   } else if (blocks > 1) {
     cluster_sync_all();   // every block's hist[1] is clear
@@ -544,21 +556,31 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   }
   // kept: keys above `prefix`, and the first `need` slots whose key equals it
 
+  // Ties matter only where not all of them are kept.
+  const bool all_ties = x.ties == need;
+  if (all_ties) --prefix;   // then: keys above `prefix` (a kept key is not 0: `need` of a 0 are all only if n = budget)
+
   // The warp's slots with a larger and with an equal key, below and above the
   // budget, and those of the slots before: in lower blocks, in lower warps.
   const int wseg = seg / kSelectWarps, i0 = min(cnt, warp * wseg), i1 = min(cnt, i0 + wseg);
   int a_lo = 0, a_hi = 0, t_lo = 0, t_hi = 0;
-#pragma unroll 2
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const bool in = i < i1, lo = s0 + i < budget;
-    const uint32_t key = in ? key_of(i) : 0u;
-    const unsigned int a = __ballot_sync(0xffffffffu, in && key > prefix), t = __ballot_sync(0xffffffffu, in && key == prefix);
-    const unsigned int m = __ballot_sync(0xffffffffu, lo);
-    a_lo += __popc(a & m);
-    a_hi += __popc(a & ~m);
-    t_lo += __popc(t & m);
-    t_hi += __popc(t & ~m);
+#pragma unroll 4
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t key = key_of(i);
+    const bool lo = s0 + i < budget;
+    if (key > prefix) {
+      a_lo += lo;
+      a_hi += !lo;
+    }
+    if (!all_ties && key == prefix) {
+      t_lo += lo;
+      t_hi += !lo;
+    }
   }
+  a_lo = __reduce_add_sync(0xffffffffu, a_lo);
+  a_hi = __reduce_add_sync(0xffffffffu, a_hi);
+  t_lo = __reduce_add_sync(0xffffffffu, t_lo);
+  t_hi = __reduce_add_sync(0xffffffffu, t_hi);
   if (lane == 0) x.warps[warp] = make_int4(a_lo, a_hi, t_lo, t_hi);
   __syncthreads();
   const int4 wv = lane < kSelectWarps ? x.warps[lane] : make_int4(0, 0, 0, 0);
@@ -587,19 +609,25 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
       t_hi += others[r].w;
     }
   }
-  cluster_sync_all();   // no block leaves while another reads its shared memory
+  cluster_arrive();   // this block reads no other's shared memory any more
   allow_dependents();
+  if (all_ties) need = 0;
   const int kept_lo = all_a_lo + min(need, all_t_lo);   // of all slots below the budget
   int* freed_at = pairs.freed + piece * budget;
   int* moving_at = pairs.moving + piece * budget;
   int ties = t_lo + t_hi, kept = a_lo + a_hi + min(need, ties);   // before the warp's next slot
+  const unsigned int before = (1u << lane) - 1u;
+#pragma unroll 2
   for (int i = i0 + lane; i - lane < i1; i += 32) {
     const bool in = i < i1;
     const int slot = s0 + i;
     const uint32_t key = in ? key_of(i) : 0u;
-    const unsigned int before = (1u << lane) - 1u;
-    const unsigned int t = __ballot_sync(0xffffffffu, in && key == prefix);
-    const bool keep = in && (key > prefix || (key == prefix && ties + __popc(t & before) < need));
+    bool keep = in && key > prefix;
+    if (!all_ties) {
+      const unsigned int t = __ballot_sync(0xffffffffu, in && key == prefix);
+      keep = keep || (in && key == prefix && ties + __popc(t & before) < need);
+      ties += __popc(t);
+    }
     const unsigned int k = __ballot_sync(0xffffffffu, keep);
     const int rank_kept = kept + __popc(k & before);   // kept slots before this one
     if (in && slot < budget) {
@@ -610,10 +638,10 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     } else if (keep) {
       moving_at[rank_kept - kept_lo] = slot;
     }
-    ties += __popc(t);
     kept += __popc(k);
   }
   if (rank == 0 && threadIdx.x == 0) pairs.count[piece] = budget - kept_lo;
+  cluster_wait();   // no block leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------------------
