@@ -787,7 +787,7 @@ extern "C" {
 
 size_t qkvp_cache_append_workspace_bytes(const qkvp_cache* cache) {
   CacheArgs a;
-  return check_cache(cache, &a) == QKVP_OK ? kCacheStatusBytes : 0;
+  return check_cache(cache, &a) == QKVP_OK ? kCacheHeaderBytes : 0;
 }
 
 int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const uint16_t* v, const int32_t* pos,
@@ -802,9 +802,9 @@ int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const u
   const void* ptrs[] = {k, v, pos, cu, lengths_out, ws};
   for (const void* p : ptrs)
     if (!aligned16(p)) return QKVP_ERR_MISALIGNED;
-  if (ws_bytes < kCacheStatusBytes) return QKVP_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < kCacheHeaderBytes) return QKVP_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  unsigned int* arrived = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + 192);
+  unsigned int* arrived = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + kAppendCounter);
   const DevStatus st{static_cast<int*>(ws), 0};
   mark(s);
   const cudaError_t e = cache->fp8 ? launch_append_d<true>(a, T, k, v, pos, cu, lengths_out, arrived, st, s)
@@ -817,7 +817,7 @@ int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const u
 size_t qkvp_cache_evict_workspace_bytes(const qkvp_cache* cache, int budget) {
   CacheArgs a;
   if (check_cache(cache, &a) != QKVP_OK || budget < 1 || budget > a.capacity()) return 0;
-  return kCacheStatusBytes + static_cast<size_t>(a.B) * a.H * (2 * static_cast<size_t>(budget) + 1) * sizeof(int32_t);
+  return kCacheHeaderBytes + static_cast<size_t>(a.B) * a.H * (2 * static_cast<size_t>(budget) + 1) * sizeof(int32_t);
 }
 
 int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* slots, int32_t* lengths_out, void* ws,
@@ -837,7 +837,7 @@ int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* s
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const DevStatus st{static_cast<int*>(ws), 0};
   EvictPairs pairs;
-  pairs.count = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kCacheStatusBytes);
+  pairs.count = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kCacheHeaderBytes);
   pairs.freed = pairs.count + static_cast<int64_t>(a.B) * a.H;
   pairs.moving = pairs.freed + static_cast<int64_t>(a.B) * a.H * budget;
   mark(s);

@@ -16,9 +16,14 @@ enum CacheKernelId : int { KID_CACHE_APPEND = 13, KID_DECODE = 14, KID_DECODE_WE
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxPage = 256;
 constexpr int kDv = 128;
-// Bytes at the start of every workspace: status word, then counters that
-// every call leaves at zero.
-constexpr size_t kCacheStatusBytes = 256;
+// The start of every workspace: the status word, then counters that every call
+// leaves at zero.  They lie at the same place whatever the call and its shape
+// are, so that nothing else is ever written there.
+constexpr size_t kAppendCounter = 128;      // blocks of an append that have arrived
+constexpr size_t kDecodeCounters = 256;     // of an attention, for every block the piece that it ends with
+constexpr int kMaxDecodeBlocks = 192;
+constexpr size_t kCacheHeaderBytes = 1024;
+static_assert(kDecodeCounters + kMaxDecodeBlocks * sizeof(unsigned int) <= kCacheHeaderBytes, "header too small");
 
 struct CacheArgs {
   uint8_t* k;        // [P, H, page, d] bf16 or E4M3 codes

@@ -43,6 +43,7 @@ namespace {
 constexpr int kMaxWarps = 12;
 constexpr int kWeightThreads = 256;        // at most
 constexpr int kMaxBlocks = 160;            // one per SM, and the workspace's bound
+static_assert(kMaxBlocks <= kMaxDecodeBlocks, "too few counters");
 constexpr int kSmemMax = 232448 - 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -58,7 +59,8 @@ struct DecodeParams {
   float* lse2;           // [B, H * G] base 2
   float* scores;         // [B, H * G, capacity] base 2, or null
   float* records;        // [2 * blocks] records of blocks, then [warps] of warps (unless smem_records)
-  unsigned int* arrived; // [B * H * chunks] blocks that have left their records, zero between calls
+  unsigned int* arrived; // [blocks] for the piece that a block ends with, the blocks that have left their records of
+                         // it; zero between calls
 };
 
 // A record: O [nh][128] relative to 2^mo, then m [nh], l [nh], mo [nh].
@@ -820,11 +822,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
     }
     __syncthreads();
     if (threadIdx.x < 2) {
-      const Piece& pc = threadIdx.x == 0 ? head : tail;
       is_last[threadIdx.x] = 0;
       if (threadIdx.x == 0 ? over0 : over1) {
         const unsigned int blocks = ends[threadIdx.x].last - ends[threadIdx.x].first + 1;
-        unsigned int* cnt = p.arrived + static_cast<int64_t>(pc.b) * pl.Hv + pc.hv;
+        unsigned int* cnt = p.arrived + ends[threadIdx.x].first;
         if (count_arrival(cnt) == blocks - 1) {   // releases the block's record, acquires the others'
           is_last[threadIdx.x] = 1;
           *cnt = 0;
@@ -909,9 +910,9 @@ int check_heads(const CacheArgs& a, int Hq) {
   return Hq % a.H || Hq > 1024 ? QKVP_ERR_UNSUPPORTED : QKVP_OK;
 }
 
-// Parts of the workspace: status, arrival counters, lse2, records, scores.
+// Parts of the workspace after its header: lse2, records, scores.
 struct DecodeLayout {
-  size_t arrived, lse2, records, scores, bytes;
+  size_t lse2, records, scores, bytes;
 };
 // Query heads of one K/V head that share a read: up to 16, or 8 where the
 // list of very many sequences takes the shared memory that their q needs.
@@ -935,8 +936,7 @@ int most_blocks(const CacheArgs& a, int Hq) {
 DecodeLayout decode_layout(const CacheArgs& a, int Hq, int accumulate) {
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   DecodeLayout w;
-  w.arrived = kCacheStatusBytes;
-  w.lse2 = w.arrived + up(static_cast<size_t>(a.B) * a.H * head_chunks(a, Hq) * sizeof(unsigned int));
+  w.lse2 = kCacheHeaderBytes;
   w.records = w.lse2 + up(static_cast<size_t>(a.B) * Hq * sizeof(float));
   w.scores = w.records + up(static_cast<size_t>(most_blocks(a, Hq)) * (2 + kMaxWarps) * record_floats(heads_per_chunk(a, Hq)) * sizeof(float));
   w.bytes = w.scores + (accumulate ? static_cast<size_t>(a.B) * Hq * a.capacity() * sizeof(float) : 0);
@@ -1027,7 +1027,7 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
   p.scale_log2 = scale * kLog2e;
   p.q = q;
   p.a = out;
-  p.arrived = reinterpret_cast<unsigned int*>(wsb + w.arrived);
+  p.arrived = reinterpret_cast<unsigned int*>(wsb + kDecodeCounters);
   p.lse2 = reinterpret_cast<float*>(wsb + w.lse2);
   p.lse = lse;
   p.records = reinterpret_cast<float*>(wsb + w.records);

@@ -438,9 +438,10 @@ typedef struct qkvp_cache {
 } qkvp_cache;
 
 /* Bytes of workspace of each call below (0: unsupported).  Zero it once with
- * qkvp_workspace_init; every call leaves its counters at zero.  Calls sharing
- * one workspace must not overlap on the GPU.  One workspace of the largest
- * size serves all three. */
+ * qkvp_workspace_init; every call leaves its counters, in the first 1024
+ * bytes, at zero.  Calls sharing one workspace must not overlap on the GPU.  One
+ * workspace of the largest size serves all three, for caches of any shape, but
+ * none of the calls above (they write where the counters are). */
 size_t qkvp_cache_append_workspace_bytes(const qkvp_cache* cache);
 size_t qkvp_decode_attention_workspace_bytes(const qkvp_cache* cache, int Hq, int accumulate);
 size_t qkvp_cache_evict_workspace_bytes(const qkvp_cache* cache, int budget);

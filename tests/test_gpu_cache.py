@@ -552,6 +552,42 @@ def test_one_workspace_for_different_shapes(qk):
             check_decode(qk, c, _normal((4 * c.k.shape[1], c.table.shape[0], 96), 2), ws=ws)
 
 
+def test_workspace_of_any_order_of_calls(qk):
+    """What one call leaves in the workspace must not be taken for another's
+    counters: attentions of few and of many sequences whose pieces reach over
+    blocks, evictions and appends, in turn on one workspace without a wait."""
+    kinds = [([5000, 4000], 1, False), ([700, 650, 3] * 20, 4, True), ([3000], 2, False), ([900] * 33, 5, False),
+             ([0, 1, 2500, 77], 3, True)]
+    jobs = []
+    for i, (lens, H, fp8) in enumerate(kinds):
+        cache, full = make_cache(qk, lens, H, 64, 32, fp8, cap=max(lens) + 64, seed=i)
+        cache.table = full.to(DEV)
+        q = _normal((H, len(lens), 64), 40 + i).to(DEV)
+        fresh = qk.new_cache_workspace(cache, H, budget=300)
+        before = cache.weight.clone()
+        want = [t.clone() for t in qk.decode_attention(q, cache, accumulate=True, ws=fresh)] + [cache.weight.nan_to_num()]
+        cache.weight.copy_(before)
+        jobs.append((cache, q, before, want, fresh.numel()))
+    for ws in (torch.zeros(max(j[4] for j in jobs), dtype=torch.uint8, device=DEV), None):
+        for order in ([0, 1, 2, 3, 4], [4, 3, 1, 0, 2], [1, 0, 1, 3, 0], [2, 2, 4, 1, 1]):
+            got = []
+            for i in order:
+                cache, q, before, _, _ = jobs[i]
+                got.append((i, [*qk.decode_attention(q, cache, accumulate=True, ws=ws)], cache.weight.nan_to_num()))
+                cache.weight.copy_(before)
+                B, H = cache.table.shape[0], cache.k.shape[1]
+                copy = qk.KVCache(cache.k.clone(), cache.v.clone(), cache.table, cache.lengths.clone(), cache.pos.clone(),
+                                  cache.weight.clone(), cache.k_scale, cache.v_scale)
+                if cache.k_scale is None:
+                    qk.cache_evict(copy, 300, 50, ws=ws)
+                    qk.cache_append(copy, q[:H], _normal((H, B, 128), 1).to(DEV), copy.lengths.clone(), ws=ws)
+            for i, out, weight in got:
+                for x, y in zip((*out, weight), jobs[i][3]):
+                    assert torch.equal(x, y), (order, i)
+        if ws is not None:
+            assert qk.poll_device_status(ws) == (qk.OK, 0)
+
+
 def test_binding_refusals(qk):
     cache, _ = make_cache(qk, [20, 3], 2, 96, 16, False)
     q = _normal((2, 2, 96), 1).to(DEV)
