@@ -782,7 +782,7 @@ _cache_scratch = {}
 def _cache_call(where: str, dev, ws, nbytes, *args):
     """Calls the entry point ``where`` with args, workspace and stream;
     ``nbytes()`` is the workspace it needs."""
-    call = getattr(lib(), where)
+    call = getattr(_lib_handle or lib(), where)
     stream = torch._C._cuda_getCurrentRawStream(dev.index)   # torch.cuda.current_stream without the object
     if ws is not None:
         _need_cuda(ws, "ws", torch.uint8)
@@ -803,7 +803,8 @@ def _cache_call(where: str, dev, ws, nbytes, *args):
         _check(lib().qkvp_workspace_init(ws.data_ptr(), n, stream), "qkvp_workspace_init")
         code = call(*args, ws.data_ptr(), n, stream)
         _cache_scratch[key] = ws
-    _check(code, where)
+    if code:
+        raise QKVPError(code, where)
 
 
 def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
@@ -815,9 +816,12 @@ def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
     if k.dim() != 3:
         raise ValueError("k must be [H, T, d_qk]")
     T = k.shape[1]
-    _quick_cuda(k, "k", torch.bfloat16, (H, T, d_qk))
-    _quick_cuda(v, "v", torch.bfloat16, (H, T, d_v))
-    _quick_cuda(pos, "pos", torch.int32, (T,))
+    if not (k.is_cuda and k.dtype is torch.bfloat16 and k.shape == (H, T, d_qk) and k.is_contiguous() and v.is_cuda
+            and v.dtype is torch.bfloat16 and v.shape == (H, T, d_v) and v.is_contiguous() and pos.is_cuda
+            and pos.dtype is torch.int32 and pos.shape == (T,) and pos.is_contiguous()):
+        _need_cuda(k, "k", torch.bfloat16, (H, T, d_qk))
+        _need_cuda(v, "v", torch.bfloat16, (H, T, d_v))
+        _need_cuda(pos, "pos", torch.int32, (T,))
     if cu is not None:
         _quick_cuda(cu, "cu", torch.int32, (B + 1,))
     if lengths_out is None:

@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   }
   cluster_sync_all();
   int need = budget;
-  if (blocks == 1) {
+  if constexpr (blocks == 1) {
     find_digit(reversed(*reinterpret_cast<const int4*>(&x.hist[0][kBins - 4 - 4 * threadIdx.x])), kBins - 1, need, x);
   } else {
     // Each block adds up its part of the bins; all then read the sums of the
@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     for (int i = threadIdx.x; i < all; i += kSelectThreads) {
       int r = 0, at = i;   // the block that has listed it, and where
 #pragma unroll
-      for (int k = 0; k < blocks - 1; ++k)
-        if (r == k && at >= counts[k]) {
+      for (int k = 0; k < blocks; ++k)
+        if (r == k && k + 1 < blocks && at >= counts[k]) {
           at -= counts[k];
           r = k + 1;
         }
