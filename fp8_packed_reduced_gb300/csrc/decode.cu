@@ -6,8 +6,8 @@
 // is bound by memory, and its parts are chosen to keep loads in flight:
 //   - The live slots of all (sequence, head) pairs, in units of KS slots, form
 //     one list that is cut into equal contiguous parts, one for each warp of
-//     the grid (one block of 12 warps, or 8 for more than four query heads, per SM), whatever the lengths are.
-//     Warps never meet inside their parts.
+//     the grid (a block per SM, of 12 warps, or of 8 for more than four query
+//     heads), whatever the lengths are.  Warps never meet inside their parts.
 //   - Each warp has its own ring of stages in shared memory, filled by
 //     cp.async.  A unit lies inside one page (E4M3: its two halves do), so
 //     its k and v are contiguous; chunks are swizzled so that the reads below
@@ -17,11 +17,12 @@
 //     its one read.  k's dims may be permuted freely if q's are too, so a
 //     lane's operands are whole 16-byte (8-byte) chunks of a row.
 //   - Running maximum and sum per head in float32, exponentials of base 2.
-//   - E4M3: codes become f16 exactly.  q is scaled per head by a power of two
-//     into f16's range (a bf16 loses nothing above 2^-14 of its row's largest,
-//     2^-25 of it below), row scales multiply scores and probabilities in
-//     float32.  The probabilities times v's row scales are held relative to
-//     their own running maximum, since rows of very different scale may meet.
+//   - E4M3: codes become f16 exactly.  q is scaled per head by a power of two to
+//     the top of f16's range (a bf16 is exact down to 2^-31 of its row's
+//     largest), row scales multiply scores and probabilities in float32.  The
+//     probabilities times v's row scales are held relative to 2^-15 of their own
+//     running maximum (rows of very different scale may meet), again at the top
+//     of the range, so that rounding is relative down to 2^-29 of it.
 //   - Probabilities enter the second product as bf16 (E4M3: f16): half a step
 //     of 2^-8 (2^-11) relative, no more than the rounding of the output; the
 //     sum of the probabilities, lse and the weights use them unrounded.
@@ -29,6 +30,16 @@
 // O); pieces inside one block are joined by a warp of it, pieces across blocks
 // by the block that arrives last, in the order of the slots: the result does
 // not depend on the order of arrival.
+//
+// Measured (GB300, bytes of the live rows over the whole call): 64 sequences
+// of up to 8191 slots x 6 heads, 606 MB, 103.6 us, 5.85 TB/s (86 % of a copy's
+// rate); one of 131072 slots 64.5 us, 5.46 TB/s; 256 of up to 333 slots x 8
+// heads of 128 with weights 34.4 us, 4.30 TB/s; 32 of up to 6001 slots, 4 x 4
+// heads of 64 with weights 37 us, 3.44 TB/s; 48 of up to 8192 slots of E4M3
+// with weights 55.6 us, 4.22 TB/s.  While a block reads it does so at the
+// copy's rate; the rest is 2.5 us until the first loads are issued, up to 4 us
+// between the first and the last SM to end (those of some GPCs are slower in
+// every run), 4 - 7 us of joins and 3 us of the weights' kernel.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -363,6 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   __shared__ int red[kWarps], red_max[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int B = p.c.B, Hq = p.c.H * p.G, nrec = record_floats(p.nh);
+  constexpr float kTop = FP8 ? 15.f : 0.f;   // O is relative to 2^(mo - kTop)
   const auto head_of = [&](int t, int e) { return E == 1 ? c : 8 * t + 2 * c + e; };   // of this lane's scores
 
   wait_for_previous();
@@ -557,7 +569,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
         if (from_start && to_end) {
           const int64_t at = static_cast<int64_t>(cur_b) * Hq + h * p.G + ch0 + n;
           const bool none = x == 0.f;
-          const float f = none ? 0.f : exp2_below(mo[t][e], m[t][e]) / x;
+          const float f = none ? 0.f : exp2_below(mo[t][e] - kTop, m[t][e]) / x;
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) {
             const uint32_t w = none ? 0u : pack_bf16x2(o[t][mt][e] * f, o[t][mt][2 + e] * f);
@@ -585,7 +597,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
           if (g == 0) {
             rec[p.nh * kDv + n] = m[t][e];
             rec[p.nh * (kDv + 1) + n] = x;
-            rec[p.nh * (kDv + 2) + n] = mo[t][e];
+            rec[p.nh * (kDv + 2) + n] = mo[t][e] - kTop;
           }
         }
       }
@@ -625,10 +637,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
           }
           am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
           am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-          // 2^-e and 2^e for am in [2^e, 2^(e+1)), from am's exponent bits, kept to normal numbers
-          const int eb = min(253, max(1, static_cast<int>(__float_as_uint(am) >> 23)));
-          const float down = __uint_as_float(static_cast<uint32_t>(254 - eb) << 23);
-          back = __uint_as_float(static_cast<uint32_t>(eb) << 23);
+          // 2^(14-e) and 2^(e-14) for am in [2^e, 2^(e+1)), from am's exponent bits, kept to normal numbers
+          const int eb = min(253, max(15, static_cast<int>(__float_as_uint(am) >> 23)));
+          const float down = __uint_as_float(static_cast<uint32_t>(268 - eb) << 23);
+          back = __uint_as_float(static_cast<uint32_t>(eb - 14) << 23);
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
             uint32_t w[4] = {qf[t][j].x, qf[t][j].y, qf[t][j].z, qf[t][j].w};
@@ -759,7 +771,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
           }
           const float pr = ex2(x[t][s][i] - below(m[t][e]));
           l[t][e] += pr;
-          w[s][i] = FP8 ? ex2(y[s][i] - below(mo[t][e])) : pr;
+          w[s][i] = FP8 ? ex2(y[s][i] - (below(mo[t][e]) - kTop)) : pr;
         }
 #pragma unroll
       for (int s = 0; s < SUB; ++s) {

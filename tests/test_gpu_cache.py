@@ -279,6 +279,26 @@ def test_decode_large_scores(qk, fp8):
     check_decode(qk, cache, _normal((2, 2, 96), 6) * 256)
 
 
+def test_decode_e4m3_rows_of_any_scale(qk):
+    """k and v rows whose scales span 2^-40 .. 2^40, and a q whose values span
+    2^20: what is small beside its neighbours is kept relatively."""
+    cache, _ = make_cache(qk, [60, 200], 2, 96, 16, True, seed=9)
+    g = torch.Generator().manual_seed(2)
+    rows = cache.v_scale.shape
+    cache.v_scale.mul_(torch.exp2(torch.randint(-40, 41, rows, generator=g).float()).to(DEV))
+    cache.k_scale.mul_(torch.exp2(torch.randint(-12, 3, rows, generator=g).float()).to(DEV))
+    q = _normal((2, 2, 96), 6)
+    q[:, :, ::7] *= 2.0 ** -20
+    check_decode(qk, cache, q)
+    # one slot takes nearly all weight and is zero in the first half of its values
+    t = cache.table.cpu()
+    cache.k_scale.fill_(1 / 64)
+    cache.v_scale.fill_(1.0)
+    cache.k[t[0, 0], :, 3] = 0x78                       # 256 in every dim
+    cache.v[t[0, 0], :, 3, :64] = 0
+    check_decode(qk, cache, torch.full((2, 2, 96), 0.4, dtype=torch.bfloat16))
+
+
 def test_decode_without_lse_weight_and_pos(qk):
     cache, _ = make_cache(qk, [70, 9], 2, 96, 16, False)
     q = _normal((2, 2, 96), 1).to(DEV)
