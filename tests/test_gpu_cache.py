@@ -256,6 +256,10 @@ DECODE = [  # lengths, H, G, d, page, fp8
     ([2000, 3, 0, 700, 1, 1999], 5, 2, 128, 16, False),
     ([900] * 3, 16, 1, 64, 32, True),
     ([5, 900, 0, 0, 33] * 4, 3, 4, 128, 128, True),
+    ([700, 0, 55], 2, 6, 128, 64, False),
+    ([1200, 7], 1, 8, 96, 32, False),
+    ([1200, 7], 2, 7, 96, 64, True),
+    ([900, 31, 1], 1, 16, 128, 16, True),
 ]
 
 
@@ -268,6 +272,14 @@ def test_decode(qk, lens, H, G, d, page, fp8):
     check_decode(qk, cache, q * 3, accumulate=True)      # sharper
     check_decode(qk, cache, q, scale=0.0)                # the plain mean of v
     check_decode(qk, cache, q, scale=-0.3)
+
+
+@pytest.mark.parametrize("G,d,fp8", [(1, 128, False), (1, 96, True), (16, 128, True), (8, 96, False), (2, 64, False)])
+def test_decode_of_the_most_sequences(qk, G, d, fp8):
+    """4096 sequences, whose list takes shared memory from the rings."""
+    lens = [(i * 7) % 4 if i % 1000 else 70 + i // 100 for i in range(4096)]
+    cache, _ = make_cache(qk, lens, 1, d, 16, fp8, seed=G)
+    check_decode(qk, cache, _normal((G, 4096, d), 3))
 
 
 @pytest.mark.parametrize("fp8", [False, True])
