@@ -680,13 +680,9 @@ class KVCache:
     k_scale: Optional[torch.Tensor] = None
     v_scale: Optional[torch.Tensor] = None
 
-    def desc(self) -> CacheDesc:
-        """The checked C descriptor of the tensors as they are now."""
-        return CacheDesc.from_buffer_copy(self._packed()[0])
-
     def _packed(self):
-        """The descriptor's bytes, and (H, B, d_qk, d_v, slots of a sequence).
-        The checks are _need_cuda's, in as few steps as a call per token can
+        """The C descriptor of the tensors as they are now (a packed CacheDesc),
+        and H, B, d_qk, d_v and the slots that a sequence can hold.  The checks are _need_cuda's, in as few steps as a call per token can
         afford; _need_cuda words the refusal."""
         k, v, table, lengths, weight, pos = self.k, self.v, self.table, self.lengths, self.weight, self.pos
         ks = vs = pw = pp = 0

@@ -116,3 +116,18 @@ def test_binding_refuses_tensors_off_the_gpu(qk):
                  lambda: qk.cache_append(cache, z, z, torch.zeros(2, dtype=torch.int32))):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_packed_descriptor_is_the_struct(qk, monkeypatch):
+    """The bytes that the binding packs are those of the C struct."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    for fp8 in (False, True):
+        cache = qk.new_cache(3, 100, 6, page=32, fp8=fp8, device="cpu")
+        raw, H, B, d, d_v, capacity = cache._packed()
+        assert (H, B, d, d_v, capacity) == (6, 3, 96, 128, 128)
+        s = qk.CacheDesc.from_buffer_copy(raw)
+        assert ctypes.sizeof(s) == len(raw)
+        assert (s.P, s.page, s.H, s.d_qk, s.d_v, s.B, s.max_pages, s.fp8) == (12, 32, 6, 96, 128, 3, 4, int(fp8))
+        for name in ("k", "v", "k_scale", "v_scale", "weight", "pos", "table", "lengths"):
+            t = getattr(cache, name)
+            assert (getattr(s, name) or 0) == (0 if t is None else t.data_ptr()), name
