@@ -682,8 +682,9 @@ class KVCache:
 
     def _packed(self):
         """The C descriptor of the tensors as they are now (a packed CacheDesc),
-        and H, B, d_qk, d_v and the slots that a sequence can hold.  The checks are _need_cuda's, in as few steps as a call per token can
-        afford; _need_cuda words the refusal."""
+        and H, B, d_qk, d_v and the slots that a sequence can hold.  The checks
+        are _need_cuda's, in as few steps as a call per token can afford;
+        _need_cuda words the refusal."""
         k, v, table, lengths, weight, pos = self.k, self.v, self.table, self.lengths, self.weight, self.pos
         ks = vs = pw = pp = 0
         try:

@@ -649,80 +649,80 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
 // 16 bytes a lane: a warp takes 32 pairs and copies one row (E4M3: two) a step,
 // the next four steps' loads on their way before the last four are stored.
 // Sources lie at or above the budget and destinations below it, so no copy
-// disturbs another.
+// disturbs another.  Blocks of one warp, since they end one by one (eviction of
+// 24 x 8192 slots: 74 us, 87 with two warps, 103 with eight).
 // ---------------------------------------------------------------------------
-constexpr int kMoveWarps = 1;   // one: 77 us for the prompts' eviction, two 87, eight 103 (blocks end one by one)
-
 template <bool FP8>
-__global__ void __launch_bounds__(32 * kMoveWarps)
+__global__ void __launch_bounds__(32)
     evict_move_kernel(CacheArgs c, int budget, int32_t* __restrict__ slots, EvictPairs pairs, int32_t* lengths_out,
                       DevStatus st) {
   constexpr int ES = FP8 ? 1 : 2, VC = kDv * ES / 16, ROWS = FP8 ? 2 : 1, STEPS = 4, BATCH = STEPS * ROWS;
   const int kc = c.d * ES / 16;
-  const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int64_t piece = static_cast<int64_t>(b) * c.H + h;
   wait_for_previous();
-  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {   // (in place: the selection has read it)
+  if (blockIdx.x == 0 && h == 0 && lane == 0) {   // (in place: the selection has read it)
     const int n = c.lengths[b], cap = c.capacity();
     lengths_out[b] = min(budget, max(0, min(n, cap)));
-  }
-  const int j0 = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * 32;
-  const int n = min(32, __ldcg(pairs.count + piece) - j0);
-  if (n <= 0) return;
-  int src = -1, dst = -1, to_slot = 0, from_slot = 0;
-  float w = 0.f, ks = 0.f, vs = 0.f;
-  int p = 0;
-  if (lane < n) {
-    to_slot = __ldcg(pairs.freed + piece * budget + j0 + lane);
-    from_slot = __ldcg(pairs.moving + piece * budget + j0 + lane);
-    src = cache_row(c, b, h, from_slot, st, KID_EVICT_MOVE);
-    dst = cache_row(c, b, h, to_slot, st, KID_EVICT_MOVE);
-    if (src < 0) dst = -1;
-    if (dst >= 0) {
-      w = c.weight[src];
-      p = c.pos[src];
-      if (FP8) {
-        ks = c.k_scale[src];
-        vs = c.v_scale[src];
-      }
-    }
   }
   const int part = FP8 ? lane >> 4 : 0, l = FP8 ? lane & 15 : lane;   // which of a step's rows, and the lane in it
   const bool is_k = l < kc;
   const uint4* from = reinterpret_cast<const uint4*>(is_k ? c.k : c.v);
   uint4* to = reinterpret_cast<uint4*>(is_k ? c.k : c.v);
   const int chunks = is_k ? kc : VC, ch = is_k ? l : l - kc;
-  const auto load = [&](int i0, uint4 (&r)[STEPS], int (&d)[STEPS]) {
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int pair = i0 + i * ROWS + part;
-      const int s = __shfl_sync(0xffffffffu, src, pair & 31);
-      d[i] = __shfl_sync(0xffffffffu, dst, pair & 31);
-      if (l >= kc + VC || pair >= n) d[i] = -1;
-      if (d[i] >= 0) r[i] = __ldcg(from + static_cast<int64_t>(s) * chunks + ch);
+  const int count = __ldcg(pairs.count + piece);
+  for (int j0 = blockIdx.x * 32; j0 < count; j0 += gridDim.x * 32) {
+    const int n = min(32, count - j0);
+    int src = -1, dst = -1, to_slot = 0, from_slot = 0;
+    float w = 0.f, ks = 0.f, vs = 0.f;
+    int p = 0;
+    if (lane < n) {
+      to_slot = __ldcg(pairs.freed + piece * budget + j0 + lane);
+      from_slot = __ldcg(pairs.moving + piece * budget + j0 + lane);
+      src = cache_row(c, b, h, from_slot, st, KID_EVICT_MOVE);
+      dst = cache_row(c, b, h, to_slot, st, KID_EVICT_MOVE);
+      if (src < 0) dst = -1;
+      if (dst >= 0) {
+        w = c.weight[src];
+        p = c.pos[src];
+        if (FP8) {
+          ks = c.k_scale[src];
+          vs = c.v_scale[src];
+        }
+      }
     }
-  };
-  const auto store = [&](const uint4 (&r)[STEPS], const int (&d)[STEPS]) {
+    const auto load = [&](int i0, uint4 (&r)[STEPS], int (&d)[STEPS]) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i)
-      if (d[i] >= 0) to[static_cast<int64_t>(d[i]) * chunks + ch] = r[i];
-  };
-  uint4 r0[STEPS], r1[STEPS];
-  int d0[STEPS], d1[STEPS];
-  load(0, r0, d0);
-  for (int i0 = 0; i0 < n; i0 += 2 * BATCH) {
-    load(i0 + BATCH, r1, d1);
-    store(r0, d0);
-    load(i0 + 2 * BATCH, r0, d0);
-    store(r1, d1);
-  }
-  if (lane < n) slots[piece * budget + to_slot] = from_slot;
-  if (dst >= 0) {
-    c.weight[dst] = w;
-    c.pos[dst] = p;
-    if (FP8) {
-      c.k_scale[dst] = ks;
-      c.v_scale[dst] = vs;
+      for (int i = 0; i < STEPS; ++i) {
+        const int pair = i0 + i * ROWS + part;
+        const int s = __shfl_sync(0xffffffffu, src, pair & 31);
+        d[i] = __shfl_sync(0xffffffffu, dst, pair & 31);
+        if (l >= kc + VC || pair >= n) d[i] = -1;
+        if (d[i] >= 0) r[i] = __ldcg(from + static_cast<int64_t>(s) * chunks + ch);
+      }
+    };
+    const auto store = [&](const uint4 (&r)[STEPS], const int (&d)[STEPS]) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+        if (d[i] >= 0) to[static_cast<int64_t>(d[i]) * chunks + ch] = r[i];
+    };
+    uint4 r0[STEPS], r1[STEPS];
+    int d0[STEPS], d1[STEPS];
+    load(0, r0, d0);
+    for (int i0 = 0; i0 < n; i0 += 2 * BATCH) {
+      load(i0 + BATCH, r1, d1);
+      store(r0, d0);
+      load(i0 + 2 * BATCH, r0, d0);
+      store(r1, d1);
+    }
+    if (lane < n) slots[piece * budget + to_slot] = from_slot;
+    if (dst >= 0) {
+      c.weight[dst] = w;
+      c.pos[dst] = p;
+      if (FP8) {
+        c.k_scale[dst] = ks;
+        c.v_scale[dst] = vs;
+      }
     }
   }
 }
@@ -843,8 +843,13 @@ int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* s
   mark(s);
   if (launch_evict_select(a, budget, recent, sms, slots, pairs, st, s) != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
-  const dim3 grid((budget + 32 * kMoveWarps - 1) / (32 * kMoveWarps), a.H, a.B);
-  if (launch_dependent(cache->fp8 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 32 * kMoveWarps, 0, s, a, budget, slots,
+  // Blocks for as many pairs as there may be, up to three times the 32 that an
+  // SM holds: there may be far fewer pairs, and blocks without any cost too
+  // (256 x 8 heads of 300 slots, a budget of 16384: 31 us for the call, 549 with
+  // blocks for them all).
+  const int64_t pieces = static_cast<int64_t>(a.B) * a.H, full = (96 * sms + pieces - 1) / pieces;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((budget + 31) / 32, full)), a.H, a.B);
+  if (launch_dependent(cache->fp8 ? evict_move_kernel<true> : evict_move_kernel<false>, grid, 32, 0, s, a, budget, slots,
                        pairs, lengths_out, st) != cudaSuccess)
     return QKVP_ERR_CUDA;
   mark(s);

@@ -883,32 +883,41 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
 // weight += the probabilities of the head's query heads.  Four slots a thread:
 // a page and the row of scores both begin on 16 of them.
 __global__ void __launch_bounds__(kWeightThreads) decode_weight_kernel(const __grid_constant__ DecodeParams p, DevStatus st) {
-  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  const int h = blockIdx.y, b = blockIdx.z, Hq = p.c.H * p.G, i0 = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
   // What the attention does not write is read ahead of its end, from L2 (which
   // the kernels before it have left up to date; it has waited for them).
   const int n = checked_length<true>(p.c, b, st, KID_DECODE_WEIGHT);
-  const int row = i < n ? cache_row<true>(p.c, b, h, i, st, KID_DECODE_WEIGHT) : -1;
-  float4* at = reinterpret_cast<float4*>(p.c.weight + max(row, 0));
-  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (row >= 0) old = __ldcg(at);
+  const auto row_of = [&](int i) { return i < n ? cache_row<true>(p.c, b, h, i, st, KID_DECODE_WEIGHT) : -1; };
+  const auto weights_at = [&](int row) {
+    return row >= 0 ? __ldcg(reinterpret_cast<const float4*>(p.c.weight + row)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  int row = row_of(i0);
+  float4 old = weights_at(row);
   wait_for_previous();
-  if (row < 0) return;
-  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
   const int64_t head = static_cast<int64_t>(b) * Hq + h * p.G;
-  for (int g = 0; g < p.G; ++g) {
-    const float z = __ldcg(p.lse2 + head + g);
-    const float4 s = __ldcg(reinterpret_cast<const float4*>(p.scores + (head + g) * p.c.capacity() + i));
-    w.x += exp2_below(s.x, z);
-    w.y += exp2_below(s.y, z);
-    w.z += exp2_below(s.z, z);
-    w.w += exp2_below(s.w, z);
-  }
-  if (i + 3 < n) {
-    *at = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
-  } else {   // what lies past the length stays as it is
-    p.c.weight[row] = old.x + w.x;
-    if (i + 1 < n) p.c.weight[row + 1] = old.y + w.y;
-    if (i + 2 < n) p.c.weight[row + 2] = old.z + w.z;
+  for (int i = i0; i < n; i += gridDim.x * blockDim.x * 4) {
+    if (i > i0) {
+      row = row_of(i);
+      old = weights_at(row);
+    }
+    if (row < 0) continue;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < p.G; ++g) {
+      const float z = __ldcg(p.lse2 + head + g);
+      const float4 s = __ldcg(reinterpret_cast<const float4*>(p.scores + (head + g) * p.c.capacity() + i));
+      w.x += exp2_below(s.x, z);
+      w.y += exp2_below(s.y, z);
+      w.z += exp2_below(s.z, z);
+      w.w += exp2_below(s.w, z);
+    }
+    float* at = p.c.weight + row;
+    if (i + 3 < n) {
+      *reinterpret_cast<float4*>(at) = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+    } else {   // what lies past the length stays as it is
+      at[0] = old.x + w.x;
+      if (i + 1 < n) at[1] = old.y + w.y;
+      if (i + 2 < n) at[2] = old.z + w.z;
+    }
   }
 }
 
@@ -1059,8 +1068,13 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
   if (e != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   if (accumulate) {
-    const int threads = std::min(kWeightThreads, (p.c.capacity() / 4 + 31) / 32 * 32);   // four slots each
-    const dim3 wgrid((p.c.capacity() + 4 * threads - 1) / (4 * threads), p.c.H, p.c.B);
+    // Four slots a thread, up to two rounds of the blocks that the GPU holds: a
+    // sequence may be far shorter than its pages allow (64 x 8 heads with 100 of
+    // 131072 slots: 23 us for the call, 116 with blocks for them all).
+    const int threads = std::min(kWeightThreads, (p.c.capacity() / 4 + 31) / 32 * 32);
+    const int64_t pieces = static_cast<int64_t>(p.c.B) * p.c.H, full = (16 * sms + pieces - 1) / pieces;
+    const int64_t blocks = std::min<int64_t>((p.c.capacity() + 4 * threads - 1) / (4 * threads), full);
+    const dim3 wgrid(static_cast<unsigned>(blocks), p.c.H, p.c.B);
     if (launch_dependent(decode_weight_kernel, wgrid, threads, 0, s, p, st) != cudaSuccess) return QKVP_ERR_CUDA;
     mark(s);
   }

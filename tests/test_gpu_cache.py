@@ -504,6 +504,39 @@ def test_evict_long_matches_sorted(qk):
     assert cache.lengths.tolist() == [budget]
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_few_long_sequences_among_many(qk, fp8):
+    """2600 sequences with room for 2048 slots each, nearly all of them short:
+    the weights and the moves of the long ones take blocks several rounds."""
+    B, cap, page, d = 2600, 2048, 16, 96
+    lens = [i % 4 for i in range(B)]
+    lens[0], lens[1300], lens[2599] = 2048, 1501, 1999
+    cache, _ = make_cache(qk, [page] * (sum(lens) // page + B), 1, d, page, fp8, seed=4)   # its pages, and their poison's places
+    table, first = torch.full((B, cap // page), -1, dtype=torch.int32), 0
+    pages = cache.table[:, 0].cpu()
+    for b, n in enumerate(lens):
+        m = -(-n // page)
+        table[b, :m] = pages[first:first + m]
+        first += m
+        for name in ("k", "v", "k_scale", "v_scale", "weight"):
+            if m and n % page and getattr(cache, name) is not None:
+                getattr(cache, name)[table[b, m - 1], :, n % page:] = 0x7F if fp8 and name in "kv" else float("nan")
+    cache.table, cache.lengths = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = qk.new_cache_workspace(cache, 2, budget=700)
+    check_decode(qk, cache, _normal((2, B, d), 3), ws=ws)
+    ref = host(cache)
+    want, lengths = co.cache_evict(ref, 700, 9)
+    slots = qk.cache_evict(cache, 700, 9, ws=ws)
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+    assert (slots[0, 0] >= 700).sum() > 192             # more than its blocks take in one round
+    same(slots.cpu().numpy(), want, "slots")
+    same(cache.lengths.cpu().numpy(), lengths, "lengths")
+    have = host(cache)
+    for name in ("k", "v", "k_scale", "v_scale", "pos", "weight"):
+        if ref[name] is not None:
+            same(have[name], ref[name], name)
+
+
 def test_evict_reports_bad_pages(qk):
     cache, full = make_cache(qk, [64, 33], 2, 96, 16, False, cap=64)
     cache.table = full.to(DEV)
