@@ -488,17 +488,40 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   // weights repeat: then every block finds the other digits by itself.
   uint32_t* listed = keys + key_slots;   // [kListed] of this block, then [kGathered] of all
   uint32_t* gathered = listed + kListed;
+  // (One place in the list per warp: a shared counter asked for every 32 keys
+  // would be waited for every time.)
+  const auto each_mine = [&](const auto& f) {
+    if (cached) {
 #pragma unroll 4
-  for (int i = threadIdx.x; i - lane < cnt; i += kSelectThreads) {
-    const uint32_t key = i < cnt ? key_of(i) : 0u;
-    const bool mine = i < cnt && key >> 21 == prefix;
-    const unsigned int m = __ballot_sync(0xffffffffu, mine);
-    if (m == 0) continue;
-    int at = 0;
-    if (lane == 0) at = atomicAdd(&x.listed, __popc(m));
-    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
-    if (mine && at < kListed) listed[at] = key;
+      for (int i = threadIdx.x * 4; i < cnt; i += kSelectThreads * 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        if (k.x >> 21 == prefix) f(k.x);
+        if (i + 1 < cnt && k.y >> 21 == prefix) f(k.y);
+        if (i + 2 < cnt && k.z >> 21 == prefix) f(k.z);
+        if (i + 3 < cnt && k.w >> 21 == prefix) f(k.w);
+      }
+    } else {
+      for (int i = threadIdx.x; i < cnt; i += kSelectThreads) {
+        const uint32_t k = key_of(i);
+        if (k >> 21 == prefix) f(k);
+      }
+    }
+  };
+  int own = 0;
+  each_mine([&](uint32_t) { ++own; });
+  int at = own;   // inclusive prefix over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += u;
   }
+  int base = 0;
+  if (lane == 31) base = atomicAdd(&x.listed, at);
+  at += __shfl_sync(0xffffffffu, base, 31) - own;
+  each_mine([&](uint32_t key) {
+    if (at < kListed) listed[at] = key;
+    ++at;
+  });
   cluster_sync_all();   // (also: the part sums in hist[1] have been read)
   int counts[blocks], all = 0;
   bool few = true;
@@ -512,6 +535,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   if (blocks > 1)   // clear what the part sums have used
     for (int i = threadIdx.x; i < kBins; i += kSelectThreads) x.hist[1][i] = 0;
   if (few) {
+#pragma unroll 4
     for (int i = threadIdx.x; i < all; i += kSelectThreads) {
       int r = 0, at = i;   // the block that has listed it, and where
 #pragma unroll
