@@ -279,6 +279,7 @@ constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
+constexpr int kSelectAlone = 4 * kSelectThreads;  // slots that one block selects from, whatever the cluster
 constexpr int kListed = 2048, kGathered = 4096;   // keys that share the first digit, of a block and of all
 constexpr int kSelectKeys = 176 * 1024 / 4;       // keys in shared memory, at most
 
@@ -296,6 +297,14 @@ __device__ __forceinline__ int ld_rank(const int* p, uint32_t rank) {
   return v;
 }
 
+// A barrier of the blocks of one piece.
+template <int BLOCKS>
+__device__ __forceinline__ void sync_blocks() {
+  if (BLOCKS > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+}
 // The two halves of cluster_sync_all.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -365,24 +374,14 @@ struct EvictPairs {
   int* moving;    // [B, H, budget]
 };
 
+// The selection of one piece by BLOCKS blocks of the cluster.
 template <int BLOCKS>
-__global__ void __launch_bounds__(kSelectThreads, 2)
-    evict_select_kernel(CacheArgs c, int budget, int recent, int key_slots, int32_t* __restrict__ slots, EvictPairs pairs,
-                        DevStatus st) {
-  extern __shared__ __align__(16) uint32_t keys[];   // [key_slots], or none, then the lists
-  __shared__ SelectShared x;
-  constexpr int blocks = BLOCKS;   // of a cluster: their remote loads are issued together
-  const int rank = BLOCKS > 1 ? cluster_rank() : 0;
-  const int h = blockIdx.x / blocks, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  wait_for_previous();
-  const int n = checked_length(c, b, st, KID_EVICT_SELECT);
+__device__ __forceinline__ void select_slots(const CacheArgs& c, int b, int h, int n, int budget, int recent, int rank,
+                                             uint32_t* keys, int key_slots, SelectShared& x,
+                                             int32_t* __restrict__ slots, const EvictPairs& pairs, const DevStatus& st) {
+  constexpr int blocks = BLOCKS;   // their remote loads are issued together
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t piece = static_cast<int64_t>(b) * c.H + h;
-  slots += piece * budget;
-  if (n <= budget) {   // (the same for the whole cluster)
-    for (int j = rank * kSelectThreads + threadIdx.x; j < budget; j += blocks * kSelectThreads) slots[j] = j < n ? j : -1;
-    if (rank == 0 && threadIdx.x == 0) pairs.count[piece] = 0;
-    return;
-  }
   // this block's consecutive slots, a multiple of 32 for every warp
   const int seg = ((n + blocks - 1) / blocks + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
   const int s0 = min(n, rank * seg), cnt = min(n, s0 + seg) - s0;
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   __syncthreads();
   newest = __reduce_max_sync(0xffffffffu, x.red[lane % kSelectWarps]);
   if (threadIdx.x == 0) x.newest = newest;
-  cluster_sync_all();
+  sync_blocks<BLOCKS>();
 #pragma unroll
   for (int r = 0; r < blocks; ++r) newest = max(newest, ld_rank(&x.newest, r));
   const int64_t above = static_cast<int64_t>(newest) - recent;
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   } else {
     for (int i = threadIdx.x; i < cnt; i += kSelectThreads) atomicAdd(&x.hist[0][key_of(i) >> 21], 1);
   }
-  cluster_sync_all();
+  sync_blocks<BLOCKS>();
   int need = budget;
   if constexpr (blocks == 1) {
     find_digit(reversed(*reinterpret_cast<const int4*>(&x.hist[0][kBins - 4 - 4 * threadIdx.x])), kBins - 1, need, x);
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     int total;
     block_prefix(v.x + v.y + v.z + v.w, x.red, &total);
     if (threadIdx.x == 0) x.slice = total;
-    cluster_sync_all();
+    sync_blocks<BLOCKS>();
     int sums[blocks], part = blocks - 1;
 #pragma unroll
     for (int r = 0; r < blocks; ++r) sums[r] = ld_rank(&x.slice, r);
@@ -522,7 +521,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     if (at < kListed) listed[at] = key;
     ++at;
   });
-  cluster_sync_all();   // (also: the part sums in hist[1] have been read)
+  sync_blocks<BLOCKS>();   // (also: the part sums in hist[1] have been read)
   int counts[blocks], all = 0;
   bool few = true;
 #pragma unroll
@@ -547,7 +546,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
       gathered[i] = ld_rank(reinterpret_cast<const int*>(listed + at), r);
     }
   } else if (blocks > 1) {
-    cluster_sync_all();   // every block's hist[1] is clear
+    sync_blocks<BLOCKS>();   // every block's hist[1] is clear
   }
   __syncthreads();
   for (int pass = 1; pass < 3; ++pass) {
@@ -563,7 +562,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
       v = *reinterpret_cast<const int4*>(&x.hist[pass][first]);
     } else {
       for (int i = threadIdx.x; i < cnt; i += kSelectThreads) count(key_of(i));
-      cluster_sync_all();
+      sync_blocks<BLOCKS>();
 #pragma unroll
       for (int r = 0; r < blocks; ++r) {
         const int4 q = ld_rank4(&x.hist[pass][first], r);
@@ -617,7 +616,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   a_hi = __reduce_add_sync(0xffffffffu, lane < warp ? wv.y : 0);
   t_lo = __reduce_add_sync(0xffffffffu, lane < warp ? wv.z : 0);
   t_hi = __reduce_add_sync(0xffffffffu, lane < warp ? wv.w : 0);
-  cluster_sync_all();
+  sync_blocks<BLOCKS>();
   int all_t_lo = 0, all_a_lo = 0;
   int4 others[blocks];
 #pragma unroll
@@ -633,7 +632,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
       t_hi += others[r].w;
     }
   }
-  cluster_arrive();   // this block reads no other's shared memory any more
+  if (blocks > 1) cluster_arrive();   // this block reads no other's shared memory any more
   allow_dependents();
   if (all_ties) need = 0;
   const int kept_lo = all_a_lo + min(need, all_t_lo);   // of all slots below the budget
@@ -665,7 +664,32 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
     kept += __popc(k);
   }
   if (rank == 0 && threadIdx.x == 0) pairs.count[piece] = budget - kept_lo;
-  cluster_wait();   // no block leaves while another reads its shared memory
+  if (blocks > 1) cluster_wait();   // no block leaves while another reads its shared memory
+}
+
+template <int BLOCKS>
+__global__ void __launch_bounds__(kSelectThreads, 2)
+    evict_select_kernel(CacheArgs c, int budget, int recent, int key_slots, int32_t* __restrict__ slots, EvictPairs pairs,
+                        DevStatus st) {
+  extern __shared__ __align__(16) uint32_t keys[];   // [key_slots], then the lists
+  __shared__ SelectShared x;
+  const int rank = BLOCKS > 1 ? cluster_rank() : 0;
+  const int h = blockIdx.x / BLOCKS, b = blockIdx.y;
+  wait_for_previous();
+  const int n = checked_length(c, b, st, KID_EVICT_SELECT);
+  const int64_t piece = static_cast<int64_t>(b) * c.H + h;
+  slots += piece * budget;
+  if (n <= budget) {   // (the same for the whole cluster)
+    for (int j = rank * kSelectThreads + threadIdx.x; j < budget; j += BLOCKS * kSelectThreads) slots[j] = j < n ? j : -1;
+    if (rank == 0 && threadIdx.x == 0) pairs.count[piece] = 0;
+    return;
+  }
+  if constexpr (BLOCKS > 1)
+    if (n <= min(kSelectAlone, key_slots)) {
+      if (rank == 0) select_slots<1>(c, b, h, n, budget, recent, 0, keys, key_slots, x, slots, pairs, st);
+      return;   // nobody reads these blocks' shared memory
+    }
+  select_slots<BLOCKS>(c, b, h, n, budget, recent, rank, keys, key_slots, x, slots, pairs, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -791,10 +815,10 @@ cudaError_t launch_evict_select(const CacheArgs& c, int budget, int recent, int 
     return ((c.capacity() + n - 1) / n + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
   };
   int blocks = 1;
-  while (blocks < kMaxCluster && ((per_block(blocks) > 2048 && 2 * blocks * pieces <= 2 * sms) ||
+  while (blocks < kMaxCluster && ((per_block(blocks) > kSelectAlone && 2 * blocks * pieces <= 2 * sms) ||
                                   per_block(blocks) > kSelectKeys))
     blocks *= 2;
-  const int key_slots = per_block(blocks) <= kSelectKeys ? per_block(blocks) : 0;
+  const int key_slots = std::min(per_block(blocks), kSelectKeys);
   switch (blocks) {
     case 1: return launch_evict_select_n<1>(c, budget, recent, key_slots, slots, pairs, st, s);
     case 2: return launch_evict_select_n<2>(c, budget, recent, key_slots, slots, pairs, st, s);

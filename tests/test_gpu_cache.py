@@ -465,6 +465,25 @@ def test_evict(qk, lens, H, d, page, fp8, budget, recent, values, in_place):
             same(have[name], ref[name], name)
 
 
+@pytest.mark.parametrize("lens", [[2048, 2049, 100, 5000, 4], [100, 1536, 1537, 2100], [20000, 2047, 2048, 3000, 500]],
+                         ids=["cap5000", "cap2100", "cap20000"])
+def test_evict_short_and_long_in_one_call(qk, lens):
+    """Sequences that one block selects from, beside others that a cluster does."""
+    H, page, budget = 2, 16, 60
+    cache, _ = make_cache(qk, lens, H, 96, page, False, seed=8)
+    cache.weight.copy_((cache.weight * 8).round() / 8)          # ties too
+    ref = host(cache)
+    want, lengths = co.cache_evict(ref, budget, 7)
+    ws = qk.new_cache_workspace(cache, H, budget=budget)
+    slots = qk.cache_evict(cache, budget, 7, ws=ws)
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+    same(slots.cpu().numpy(), want, "slots")
+    same(cache.lengths.cpu().numpy(), lengths, "lengths")
+    have = host(cache)
+    for name in ("k", "v", "pos", "weight"):
+        same(have[name], ref[name], name)
+
+
 def test_evict_equal_positions_and_extremes(qk):
     """Positions that repeat, and the ends of int32: "recent" is an exact
     difference, and ties among the protected go to the lowest slots."""
