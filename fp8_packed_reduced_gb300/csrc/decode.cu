@@ -23,9 +23,14 @@
 //     probabilities times v's row scales are held relative to 2^-15 of their own
 //     running maximum (rows of very different scale may meet), again at the top
 //     of the range, so that rounding is relative down to 2^-29 of it.
-//   - Probabilities enter the second product as bf16 (E4M3: f16): half a step
-//     of 2^-8 (2^-11) relative, no more than the rounding of the output; the
-//     sum of the probabilities, lse and the weights use them unrounded.
+//   - Probabilities enter the second product as two bf16, which hold 2^-15 of
+//     them relatively (one holds 2^-8, as much again as the rounding of the
+//     output): the second takes the tile's odd columns, which up to four heads
+//     leave empty, or with more heads a product of its own (32 sequences of up to
+//     6001 slots, 4 x 8 heads of 96 50.4 us, with one bf16 50.3; 4 x 16 of 64
+//     49.6 / 48.4).
+//     E4M3: as one f16, 2^-11, an eighth of the output's rounding.  The sum of
+//     the probabilities, lse and the weights use them unrounded.
 // A part that holds only a piece of a (sequence, head) leaves a record (m, l,
 // O); pieces inside one block are joined by a warp of it, pieces across blocks
 // by the block that arrives last, in the order of the slots: the result does
@@ -148,6 +153,13 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// The bf16 next to x >= 0 towards zero, and what it leaves of x: never zero
+// beside an x that is not, so that infinities of v times it are those of v
+// times x.
+__device__ __forceinline__ float bf16_below(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ float bf16_rest(float x) {
+  return x > 0.f ? fmaxf(x - bf16_below(x), 1.1754943508222875e-38f) : 0.f;
 }
 // What scores are taken relative to: their maximum m, or 0 where all are -inf
 // (so that each of them has the weight 2^-inf = 0).
@@ -555,6 +567,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   // Leaves the finished piece: the whole of it as the result, part of it as a
   // record.
   const auto flush = [&](bool to_end) {
+    if (E == 1 && !FP8)   // what bf16 has left of the probabilities joins them
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        o[0][mt][0] += o[0][mt][1];
+        o[0][mt][2] += o[0][mt][3];
+      }
     const int h = cur_hv / p.chunks, ch0 = (cur_hv % p.chunks) * p.nh, nh = min(p.nh, p.G - ch0);
     float* rec = from_start ? begun_here(warp) : begun_before + warp * nrec;
 #pragma unroll
@@ -715,6 +733,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
       }
 
     uint32_t pb[NT][SUB][2];   // the probabilities as the second product's operand
+    uint32_t rest[NT][2];      // and what bf16 leaves of them, where they fill the tile
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float y[SUB][4];   // E4M3: the score plus log2 of v's row scale
@@ -754,6 +773,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
           for (int mt = 0; mt < 8; ++mt) {
             o[t][mt][e] *= fo;
             o[t][mt][2 + e] *= fo;
+            if (E == 1 && !FP8) {
+              o[t][mt][1] *= fo;
+              o[t][mt][3] *= fo;
+            }
           }
           m[t][e] = top[e];
           mo[t][e] = otop[e];
@@ -766,7 +789,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
         for (int i = 0; i < 4; ++i) {
           const int e = i & 1;
           if (e >= E) {
-            w[s][i] = 0.f;
+            w[s][i] = FP8 ? 0.f : bf16_rest(w[s][i - 1]);
             continue;
           }
           const float pr = ex2(x[t][s][i] - below(m[t][e]));
@@ -774,10 +797,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
           w[s][i] = FP8 ? ex2(y[s][i] - (below(mo[t][e]) - kTop)) : pr;
         }
 #pragma unroll
-      for (int s = 0; s < SUB; ++s) {
-        pb[t][s][0] = movmatrix_trans(FP8 ? pack_f16x2(w[s][0], w[s][1]) : pack_bf16x2(w[s][0], w[s][1]));
-        pb[t][s][1] = movmatrix_trans(FP8 ? pack_f16x2(w[s][2], w[s][3]) : pack_bf16x2(w[s][2], w[s][3]));
-      }
+      for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float w0 = w[s][2 * r], w1 = w[s][2 * r + 1];
+          pb[t][s][r] = movmatrix_trans(FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(bf16_below(w0), E == 1 ? w1 : bf16_below(w1)));
+          if (!FP8 && E == 2) rest[t][r] = movmatrix_trans(pack_bf16x2(bf16_rest(w0), bf16_rest(w1)));
+        }
     }
 
 #pragma unroll
@@ -798,7 +824,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
         // slots 0-7 and 8-15, columns 16 mt .. + 7 and + 8 .. + 15
         ldmatrix4_trans(r, sv + TL::v_at((lane & 7) + (lane >> 4) * 8, 2 * mt + ((lane >> 3) & 1)));
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816<false>(o[t][mt], r[0], r[1], r[2], r[3], pb[t][0][0], pb[t][0][1]);
+        for (int t = 0; t < NT; ++t) {
+          mma16816<false>(o[t][mt], r[0], r[1], r[2], r[3], pb[t][0][0], pb[t][0][1]);
+          if (E == 2)
+            mma16816<false>(o[t][mt], r[0], r[1], r[2], r[3], rest[t][0], rest[t][1]);
+        }
       }
     }
   }

@@ -311,6 +311,39 @@ def test_decode_e4m3_rows_of_any_scale(qk):
     check_decode(qk, cache, torch.full((2, 2, 96), 0.4, dtype=torch.bfloat16))
 
 
+@pytest.mark.parametrize("G,d", [(1, 96), (2, 64), (4, 128), (5, 96), (8, 64), (9, 128), (16, 96)])
+def test_decode_holds_probabilities_beyond_bf16(qk, G, d):
+    """Beside the rounding of the output (half a step, 2^-8 |ref|) a bf16 cache
+    adds what two bf16 leave of a probability (2^-15), what the scores' errors
+    and the exponential do to it (2 delta + 2^-20), and at most 2^-23 a step
+    for n additions and 32 of the joins; one bf16 would add 2^-8."""
+    lens = [600, 37, 1, 250]
+    cache, _ = make_cache(qk, lens, 2, d, 32, False, seed=G)
+    q = _normal((2 * G, len(lens), d), 11)
+    a, _ = qk.decode_attention(q.to(DEV), cache)
+    ref, _, _, absa, size = co.decode_attention(host(cache), synth.to_numpy_f32(q), d ** -0.5)
+    delta = (d + 8) * 2.0 ** -23 * size
+    steps = (np.array(lens) + 32)[:, None] * 2.0 ** -23
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -15 + 2 * delta + 2.0 ** -20 + steps)[..., None] * absa
+    err = np.abs(synth.to_numpy_f32(a.cpu()).reshape(ref.shape) - ref)
+    assert (err <= bound).all(), f"{(err > bound).sum()} values, up to {np.max(err / bound)} of the bound"
+
+
+@pytest.mark.parametrize("G", [1, 8])
+def test_decode_infinities_in_live_values(qk, G):
+    """What the formula gives: p * inf is inf for every p above zero."""
+    cache, _ = make_cache(qk, [40, 3], 2, 96, 16, False)
+    q = _normal((2 * G, 2, 96), 2).to(DEV)
+    good = qk.decode_attention(q, cache)[0].view(2, 2 * G, 128).clone()
+    t = cache.table.cpu()
+    cache.v[t[0, 1], 0, 5, 7] = float("inf")
+    cache.v[t[0, 2], 0, 2, 100] = float("-inf")
+    cache.v[t[1, 0], 1, 1, 0] = float("inf")
+    a = qk.decode_attention(q, cache)[0].view(2, 2 * G, 128)
+    good[0, :G, 7], good[0, :G, 100], good[1, G:, 0] = float("inf"), -float("inf"), float("inf")
+    assert torch.equal(a, good)
+
+
 def test_decode_without_lse_weight_and_pos(qk):
     cache, _ = make_cache(qk, [70, 9], 2, 96, 16, False)
     q = _normal((2, 2, 96), 1).to(DEV)
