@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -774,11 +775,21 @@ def new_cache_workspace(cache: KVCache, Hq: int, accumulate: bool = True, budget
 # A call that is being captured brings its own: a captured graph keeps the
 # address, and this one is replaced when a later call needs more.
 _cache_scratch = {}
+# Held around every call: an attention or an eviction launches two kernels that
+# pass data through the workspace, and ctypes lets other threads run meanwhile.
+# Threads share their default stream (so a workspace, too), and the stream
+# orders kernels, not pairs of them.
+_cache_lock = threading.RLock()
 
 
 def _cache_call(where: str, dev, ws, nbytes, *args):
     """Calls the entry point ``where`` with args, workspace and stream;
     ``nbytes()`` is the workspace it needs."""
+    with _cache_lock:
+        _cache_call_locked(where, dev, ws, nbytes, *args)
+
+
+def _cache_call_locked(where: str, dev, ws, nbytes, *args):
     call = getattr(_lib_handle or lib(), where)
     stream = torch._C._cuda_getCurrentRawStream(dev.index)   # torch.cuda.current_stream without the object
     if ws is not None:

@@ -439,9 +439,12 @@ typedef struct qkvp_cache {
 
 /* Bytes of workspace of each call below (0: unsupported).  Zero it once with
  * qkvp_workspace_init; every call leaves its counters, in the first 1024
- * bytes, at zero.  Calls sharing one workspace must not overlap on the GPU.  One
- * workspace of the largest size serves all three, for caches of any shape, but
- * none of the calls above (they write where the counters are). */
+ * bytes, at zero.  Calls sharing one workspace must not overlap, neither on the
+ * GPU nor on the host: an attention and an eviction launch two kernels each
+ * that pass data through it, so two host threads that launch on one stream
+ * take turns by the whole call, or have a workspace each.  One workspace of the
+ * largest size serves all three, for caches of any shape, but none of the calls
+ * above (they write where the counters are). */
 size_t qkvp_cache_append_workspace_bytes(const qkvp_cache* cache);
 size_t qkvp_decode_attention_workspace_bytes(const qkvp_cache* cache, int Hq, int accumulate);
 size_t qkvp_cache_evict_workspace_bytes(const qkvp_cache* cache, int budget);

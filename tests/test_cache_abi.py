@@ -2,6 +2,9 @@
 arguments before any CUDA call, and the binding checks tensors before those."""
 
 import ctypes
+import threading
+import time
+import types
 
 import pytest
 import torch
@@ -131,3 +134,31 @@ def test_packed_descriptor_is_the_struct(qk, monkeypatch):
         for name in ("k", "v", "k_scale", "v_scale", "weight", "pos", "table", "lengths"):
             t = getattr(cache, name)
             assert (getattr(s, name) or 0) == (0 if t is None else t.data_ptr()), name
+
+
+@pytest.mark.parametrize("given", [False, True], ids=["kept", "given"])
+def test_calls_of_two_threads_take_turns(qk, monkeypatch, given):
+    """A call's kernels pass data through the workspace: no other thread's call
+    may come between them (ctypes lets the other thread run)."""
+    inside, met = [], []
+
+    def entry(*args):
+        met.append(len(inside))
+        inside.append(args)
+        time.sleep(0.02)
+        inside.pop()
+        return 0
+
+    monkeypatch.setattr(qk, "_lib_handle", types.SimpleNamespace(qkvp_cache_evict=entry, qkvp_workspace_init=lambda *a: 0))
+    monkeypatch.setattr(qk, "_cache_scratch", {})
+    monkeypatch.setattr(qk, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 7, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    ws = torch.empty(64, dtype=torch.uint8) if given else None
+    threads = [threading.Thread(target=qk._cache_call, args=("qkvp_cache_evict", torch.device("cpu"), ws, lambda: 64))
+               for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert met == [0] * 4

@@ -12,6 +12,8 @@ step: 2^-8 relative).  So
   |weight - ref| <= (2 delta + 2^-20) sum_g p_g + 2^-22 |ref|
 Appended rows, codes, scales, evicted slots and moved rows are exact."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -667,6 +669,42 @@ def test_one_workspace_for_different_shapes(qk):
     for _ in range(2):
         for c in caches:
             check_decode(qk, c, _normal((4 * c.k.shape[1], c.table.shape[0], 96), 2), ws=ws)
+
+
+def test_two_threads_on_one_stream(qk):
+    """Attentions with weights and evictions of two threads on the default
+    stream, on caches of different shapes, without workspaces of their own."""
+    jobs = []
+    for i, (lens, H, page, budget) in enumerate((([900, 33, 0], 2, 32, 40), ([300, 299, 301, 20, 7], 3, 16, 100))):
+        cache, _ = make_cache(qk, lens, H, 96, page, False, seed=i)
+        q = _normal((H, len(lens), 96), 7 + i).to(DEV)
+        before = {n: getattr(cache, n).clone() for n in ("k", "v", "weight", "pos", "lengths")}
+
+        def one(cache=cache, q=q, before=before, budget=budget):
+            for n, t in before.items():
+                getattr(cache, n).copy_(t)
+            out = qk.decode_attention(q, cache, accumulate=True)
+            return (*out, qk.cache_evict(cache, budget, 9),
+                    *(getattr(cache, n).float().nan_to_num() for n in before))
+
+        jobs.append((one, one()))
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(2)
+
+    def work(i):
+        one, want = jobs[i]
+        start.wait()
+        for r in range(100):
+            got = one()
+            if not all(torch.equal(x, y) for x, y in zip(got, want)):
+                wrong.append((i, r))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_workspace_of_any_order_of_calls(qk):
