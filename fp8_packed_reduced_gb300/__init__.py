@@ -809,17 +809,31 @@ def _cache_call_locked(where: str, dev, ws, nbytes, *args):
             raise QKVPError(ERR_UNSUPPORTED, where)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         _check(lib().qkvp_workspace_init(ws.data_ptr(), n, stream), "qkvp_workspace_init")
+        if key in _cache_scratch:
+            ws[:8].copy_(_cache_scratch[key][:8])   # the status word, for poll_cache_status
         code = call(*args, ws.data_ptr(), n, stream)
         _cache_scratch[key] = ws
     if code:
         raise QKVPError(code, where)
 
 
+def poll_cache_status(device="cuda"):
+    """(status, kernel id) that the cache calls made without ``ws`` on the
+    device's current stream have recorded since the last poll (a token without
+    room, a length or a page out of range); clears it.  Waits for the stream."""
+    with _cache_lock:
+        stream = torch.cuda.current_stream(device)
+        ws = _cache_scratch.get((stream.device.index, stream.cuda_stream))
+        return (OK, 0) if ws is None else poll_device_status(ws)
+
+
 def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
     """Append new tokens: k [H, T, d_qk], v [H, T, d_v] bf16 (as forward()
     returns them) and pos [T] int32.  Rows cu[b] .. cu[b + 1) (cu [B + 1] int32)
     belong to sequence b; without cu there is one row per sequence.  The
-    lengths grow in place, or go to lengths_out.  Returns the new lengths."""
+    lengths grow in place, or go to lengths_out.  Returns the new lengths.
+    A token without room is not stored: poll_device_status(ws), or without ws
+    poll_cache_status(), tells."""
     d, H, B, d_qk, d_v, _ = cache._packed()
     if k.dim() != 3:
         raise ValueError("k must be [H, T, d_qk]")

@@ -202,6 +202,26 @@ def test_append_reports_what_does_not_fit(qk):
     assert qk.poll_device_status(ws) == (qk.OK, 0)
 
 
+def test_errors_without_a_workspace_are_polled(qk):
+    """What a call without ws records can be read, also once a later call has
+    needed a larger workspace; another stream has its own."""
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert qk.poll_cache_status() == (qk.OK, 0)
+        cache, full = make_cache(qk, [32, 4], 2, 96, 16, False, cap=32)
+        cache.table = full.to(DEV)
+        k, v, pos = _normal((2, 2, 96), 1).to(DEV), _normal((2, 2, 128), 2).to(DEV), torch.arange(2, dtype=torch.int32, device=DEV)
+        qk.cache_append(cache, k, v, pos)            # sequence 0 is full
+        assert cache.lengths.tolist() == [32, 5]
+        qk.decode_attention(k, cache, accumulate=True)   # a larger workspace
+        assert qk.poll_cache_status(DEV) == (qk.ERR_DEVICE_INPUT, 13)
+        assert qk.poll_cache_status() == (qk.OK, 0)
+        qk.cache_append(cache, k, v, pos)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            assert qk.poll_cache_status() == (qk.OK, 0)
+        assert qk.poll_cache_status() == (qk.ERR_DEVICE_INPUT, 13)
+
+
 # ---------------------------------------------------------------------------
 # Attention of one token
 # ---------------------------------------------------------------------------
