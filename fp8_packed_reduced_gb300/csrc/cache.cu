@@ -153,6 +153,12 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int t0 = (blockIdx.x * (kAppendThreads / 32) + warp) * 8, t = t0 + (lane >> 2);
   wait_for_previous();
 
+  // Offsets that fall anywhere give rows to no sequence or to two: every block
+  // then stores nothing, and no length grows.
+  bool fall = false;
+  if (cu != nullptr)
+    for (int b = threadIdx.x; b < c.B; b += kAppendThreads) fall |= __ldg(cu + b + 1) < __ldg(cu + b);
+
   uint4 kx[KN], vx[VN];
   if (t < T) {
     const int64_t in = static_cast<int64_t>(h) * T + t;
@@ -170,13 +176,14 @@ __global__ void __launch_bounds__(kAppendThreads)
   }
 
   // the place of the lane's token
+  fall = __syncthreads_or(fall);
   int64_t row = -1;
-  if (t0 < T) {
+  if (t0 < T && !fall) {
     int b = t, start = t;
     if (cu != nullptr) {
       b = warp_upper_bound(cu, c.B + 1, t0) - 1;
       while (b < c.B && t < T && __ldg(cu + b + 1) <= t) ++b;   // the warp's later tokens, past empty sequences
-      start = b >= 0 && b < c.B ? __ldg(cu + b) : 0;
+      start = b >= 0 && b < c.B ? max(0, __ldg(cu + b)) : 0;
     }
     if (t < T) {
       if (b < 0 || b >= c.B) {
@@ -236,10 +243,14 @@ __global__ void __launch_bounds__(kAppendThreads)
   if (!writes) return;
   for (int b = threadIdx.x; b < c.B; b += kAppendThreads) {
     const int n = __ldcg(c.lengths + b), cap = c.capacity();
-    int64_t add = cu != nullptr ? static_cast<int64_t>(__ldg(cu + b + 1)) - __ldg(cu + b) : 1;
-    if (add < 0 || n < 0 || n + add > cap) record_error(st, QKVP_ERR_DEVICE_INPUT, KID_CACHE_APPEND);
-    if (add < 0) add = 0;
+    int add = 1;   // rows that there are for the sequence
+    if (cu != nullptr) {
+      const int first = __ldg(cu + b), end = __ldg(cu + b + 1);
+      if (fall || (b == 0 && first != 0) || (b == c.B - 1 && end != T)) record_error(st, QKVP_ERR_DEVICE_INPUT, KID_CACHE_APPEND);
+      add = fall ? 0 : min(T, max(0, end)) - min(T, max(0, first));
+    }
     const int64_t m = static_cast<int64_t>(n < 0 ? 0 : n) + add;
+    if (n < 0 || m > cap) record_error(st, QKVP_ERR_DEVICE_INPUT, KID_CACHE_APPEND);
     lengths_out[b] = static_cast<int32_t>(m > cap ? cap : m);
   }
 }

@@ -459,8 +459,10 @@ size_t qkvp_cache_evict_workspace_bytes(const qkvp_cache* cache, int budget);
  *                 T; NULL: one row per sequence (T = B)
  *   lengths_out  out [B] lengths after the append; cache->lengths itself (or
  *                 NULL) updates it in place
- * A token without room (or rows outside cu) is not stored and recorded as
- * QKVP_ERR_DEVICE_INPUT. */
+ * The lengths grow by the rows that there are: offsets outside [0, T] count as
+ * the nearer end, and where cu decreases anywhere nothing is stored and no
+ * length grows.  Both, a token without room and rows outside cu (not stored)
+ * are recorded as QKVP_ERR_DEVICE_INPUT. */
 int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const uint16_t* v, const int32_t* pos,
                       const int32_t* cu, int32_t* lengths_out, void* ws, size_t ws_bytes, void* stream);
 

@@ -202,6 +202,39 @@ def test_append_reports_what_does_not_fit(qk):
     assert qk.poll_device_status(ws) == (qk.OK, 0)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("cu,rows", [
+    ([0, 2, 2, 9], [[0, 1], [], [2, 3, 4, 5]]),                # more rows than there are
+    ([0, 2, 8, 20], [[0, 1], [2, 3, 4, 5], []]),
+    ([1, 3, 3, 6], [[1, 2], [], [3, 4, 5]]),                   # the first row belongs to none
+    ([-4, 2, 5, 6], [[0, 1], [2, 3, 4], [5]]),
+    ([-9, -5, 2, 6], [[], [0, 1], [2, 3, 4, 5]]),
+    ([-2 ** 31, -5, 2 ** 31 - 1, 2 ** 31 - 1], [[], [0, 1, 2, 3, 4, 5], []]),
+    ([0, 5, 3, 6], [[], [], []]),                              # rows of two sequences, or of none
+    ([6, 4, 2, 0], [[], [], []]),
+], ids=str)
+def test_append_offsets_that_do_not_fit_the_rows(qk, cu, rows, in_place):
+    """Lengths grow by the rows that are stored, whatever cu says."""
+    H, T, lens = 2, 6, [3, 15, 0]
+    cache, full = make_cache(qk, lens, H, 96, 16, False, cap=32)
+    cache.table = full.to(DEV)
+    k, v, pos = _normal((H, T, 96), 1), _normal((H, T, 128), 2), torch.arange(T, dtype=torch.int32) + 50
+    ref = host(cache)
+    kk, vv = synth.to_numpy_f32(k), synth.to_numpy_f32(v)
+    for b, mine in enumerate(rows):
+        for i, t in enumerate(mine):
+            at = ref["table"][b, (lens[b] + i) // 16], slice(None), (lens[b] + i) % 16
+            ref["k"][at], ref["v"][at], ref["pos"][at], ref["weight"][at] = kk[:, t], vv[:, t], pos[t], 0
+    ws = qk.new_cache_workspace(cache, H)
+    got = qk.cache_append(cache, k.to(DEV), v.to(DEV), pos.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV),
+                          None if in_place else torch.empty_like(cache.lengths), ws=ws)
+    assert qk.poll_device_status(ws) == (qk.ERR_DEVICE_INPUT, 13)
+    assert got.tolist() == [n + len(mine) for n, mine in zip(lens, rows)]
+    have = host(cache)
+    for name in ("k", "v", "pos", "weight"):
+        same(have[name], ref[name], name)
+
+
 def test_errors_without_a_workspace_are_polled(qk):
     """What a call without ws records can be read, also once a later call has
     needed a larger workspace; another stream has its own."""
