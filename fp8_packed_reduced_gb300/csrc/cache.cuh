@@ -41,10 +41,12 @@ struct CacheArgs {
 };
 
 // The length of sequence b, clamped to what its pages can hold; a length
-// outside [0, capacity] is recorded.  L2: past L1.
+// outside [0, capacity] is recorded.  L2: past L1; else a plain load, not one
+// of read-only data, since the append in place writes the lengths at its end
+// (past L1 it takes 32.0 us instead of 30.9 for 23843 ragged rows x 8 heads).
 template <bool L2 = false>
 __device__ __forceinline__ int checked_length(const CacheArgs& c, int b, const DevStatus& st, int kid) {
-  const int n = L2 ? __ldcg(c.lengths + b) : __ldg(c.lengths + b), cap = c.capacity();
+  const int n = L2 ? __ldcg(c.lengths + b) : c.lengths[b], cap = c.capacity();
   if (n < 0 || n > cap) {
     record_error(st, QKVP_ERR_DEVICE_INPUT, kid);
     return n < 0 ? 0 : cap;
