@@ -651,14 +651,21 @@ def mlp_backward(dout, W1_8T, w1_scale, W2_8T, w2_scale, saved, ws=None, out=Non
 # Serving: paged key-value cache, attention of one new token, eviction
 # ----------------------------------------------------------------------------
 
-def _quick_cuda(t, name: str, dtype, shape):
-    """_need_cuda in as few steps as a call per token can afford."""
+def _need_cuda_at(t, name: str, dtype, shape, dev: int):
+    """_need_cuda, on the cache's device cuda:``dev``."""
+    _need_cuda(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, where the cache is, got {t.device}")
+
+
+def _quick_cuda(t, name: str, dtype, shape, dev: int):
+    """_need_cuda_at in as few steps as a call per token can afford."""
     try:
-        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
             return
     except AttributeError:
         pass
-    _need_cuda(t, name, dtype, shape)
+    _need_cuda_at(t, name, dtype, shape, dev)
 
 
 @dataclass
@@ -684,33 +691,35 @@ class KVCache:
     def _packed(self):
         """The C descriptor of the tensors as they are now (a packed CacheDesc),
         and H, B, d_qk, d_v and the slots that a sequence can hold.  The checks
-        are _need_cuda's, in as few steps as a call per token can afford;
-        _need_cuda words the refusal."""
+        are _need_cuda_at's, in as few steps as a call per token can afford;
+        it words the refusal."""
         k, v, table, lengths, weight, pos = self.k, self.v, self.table, self.lengths, self.weight, self.pos
         ks = vs = pw = pp = 0
         try:
             P, H, page, d = k.shape
             B, max_pages = table.shape
-            dt = k.dtype
+            dt, dev = k.dtype, k.get_device()
             fp8 = dt is torch.uint8
             vshape = v.shape
-            good = (k.is_cuda and (fp8 or dt is torch.bfloat16) and k.is_contiguous() and v.is_cuda and v.dtype is dt
-                    and vshape[:3] == (P, H, page) and len(vshape) == 4 and v.is_contiguous() and table.is_cuda
-                    and table.dtype is torch.int32 and table.is_contiguous() and lengths.is_cuda
-                    and lengths.dtype is torch.int32 and lengths.shape == (B,) and lengths.is_contiguous())
+            good = (k.is_cuda and (fp8 or dt is torch.bfloat16) and k.is_contiguous() and v.get_device() == dev
+                    and v.dtype is dt and vshape[:3] == (P, H, page) and len(vshape) == 4 and v.is_contiguous()
+                    and table.get_device() == dev and table.dtype is torch.int32 and table.is_contiguous()
+                    and lengths.get_device() == dev and lengths.dtype is torch.int32 and lengths.shape == (B,)
+                    and lengths.is_contiguous())
             rows = (P, H, page)
             if fp8:
                 k_scale, v_scale = self.k_scale, self.v_scale
-                good = (good and k_scale.is_cuda and k_scale.dtype is torch.float32 and k_scale.shape == rows
-                        and k_scale.is_contiguous() and v_scale.is_cuda and v_scale.dtype is torch.float32
+                good = (good and k_scale.get_device() == dev and k_scale.dtype is torch.float32 and k_scale.shape == rows
+                        and k_scale.is_contiguous() and v_scale.get_device() == dev and v_scale.dtype is torch.float32
                         and v_scale.shape == rows and v_scale.is_contiguous())
                 ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
             if weight is not None:
-                good = (good and weight.is_cuda and weight.dtype is torch.float32 and weight.shape == rows
+                good = (good and weight.get_device() == dev and weight.dtype is torch.float32 and weight.shape == rows
                         and weight.is_contiguous())
                 pw = weight.data_ptr()
             if pos is not None:
-                good = good and pos.is_cuda and pos.dtype is torch.int32 and pos.shape == rows and pos.is_contiguous()
+                good = (good and pos.get_device() == dev and pos.dtype is torch.int32 and pos.shape == rows
+                        and pos.is_contiguous())
                 pp = pos.data_ptr()
         except (AttributeError, ValueError, TypeError):
             good = False
@@ -723,18 +732,19 @@ class KVCache:
     def _refuse(self):
         fp8 = isinstance(self.k, torch.Tensor) and self.k.dtype == torch.uint8
         _need_cuda(self.k, "cache k", torch.uint8 if fp8 else torch.bfloat16)
-        _need_cuda(self.v, "cache v", self.k.dtype)
-        _need_cuda(self.table, "cache table", torch.int32)
+        dev = self.k.get_device()
+        _need_cuda_at(self.v, "cache v", self.k.dtype, None, dev)
+        _need_cuda_at(self.table, "cache table", torch.int32, None, dev)
         if self.k.dim() != 4 or self.v.dim() != 4 or self.table.dim() != 2:
             raise ValueError("cache k and v must be [P, H, page, d], table [B, max_pages]")
         rows = tuple(self.k.shape[:3])
         _need_cuda(self.v, "cache v", self.k.dtype, (*rows, self.v.shape[3]))
-        _need_cuda(self.lengths, "cache lengths", torch.int32, (self.table.shape[0],))
+        _need_cuda_at(self.lengths, "cache lengths", torch.int32, (self.table.shape[0],), dev)
         for name, dt, wanted in (("k_scale", torch.float32, fp8), ("v_scale", torch.float32, fp8),
                                  ("weight", torch.float32, self.weight is not None),
                                  ("pos", torch.int32, self.pos is not None)):
             if wanted:
-                _need_cuda(getattr(self, name), f"cache {name}", dt, rows)
+                _need_cuda_at(getattr(self, name), f"cache {name}", dt, rows, dev)
         raise ValueError("cache tensors do not fit together")
 
 
@@ -766,8 +776,9 @@ def new_cache_workspace(cache: KVCache, Hq: int, accumulate: bool = True, budget
         sizes.append(lib().qkvp_cache_evict_workspace_bytes(d, budget))
     if 0 in sizes:
         raise QKVPError(ERR_UNSUPPORTED, "new_cache_workspace")
-    ws = torch.empty(max(sizes), dtype=torch.uint8, device=cache.k.device)
-    _check(lib().qkvp_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)), "qkvp_workspace_init")
+    with torch.cuda.device(cache.k.device):
+        ws = torch.empty(max(sizes), dtype=torch.uint8, device=cache.k.device)
+        _check(lib().qkvp_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)), "qkvp_workspace_init")
     return ws
 
 
@@ -782,39 +793,38 @@ _cache_scratch = {}
 _cache_lock = threading.RLock()
 
 
-def _cache_call(where: str, dev, ws, nbytes, *args):
-    """Calls the entry point ``where`` with args, workspace and stream;
-    ``nbytes()`` is the workspace it needs."""
+def _cache_call(where: str, dev: int, ws, nbytes, *args):
+    """Calls the entry point ``where`` with args, workspace and the current
+    stream of cuda:``dev``; ``nbytes()`` is the workspace it needs."""
+    if torch._C._cuda_getDevice() != dev:   # kernels are launched on the current device
+        with torch.cuda.device(dev):
+            return _cache_call(where, dev, ws, nbytes, *args)
     with _cache_lock:
-        _cache_call_locked(where, dev, ws, nbytes, *args)
-
-
-def _cache_call_locked(where: str, dev, ws, nbytes, *args):
-    call = getattr(_lib_handle or lib(), where)
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)   # torch.cuda.current_stream without the object
-    if ws is not None:
-        _need_cuda(ws, "ws", torch.uint8)
-        _check(call(*args, ws.data_ptr(), ws.numel(), stream), where)
-        return
-    if torch.cuda.is_current_stream_capturing():
-        raise ValueError("a captured call needs its own workspace: pass ws=new_cache_workspace(...)")
-    key = (dev.index, stream)
-    ws = _cache_scratch.get(key)
-    code = ERR_WORKSPACE_TOO_SMALL
-    if ws is not None:
-        code = call(*args, ws.data_ptr(), ws.numel(), stream)
-    if code == ERR_WORKSPACE_TOO_SMALL:   # refused before any launch
-        n = int(nbytes())
-        if n == 0:
-            raise QKVPError(ERR_UNSUPPORTED, where)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        _check(lib().qkvp_workspace_init(ws.data_ptr(), n, stream), "qkvp_workspace_init")
-        if key in _cache_scratch:
-            ws[:8].copy_(_cache_scratch[key][:8])   # the status word, for poll_cache_status
-        code = call(*args, ws.data_ptr(), n, stream)
-        _cache_scratch[key] = ws
-    if code:
-        raise QKVPError(code, where)
+        call = getattr(_lib_handle or lib(), where)
+        stream = torch._C._cuda_getCurrentRawStream(dev)   # torch.cuda.current_stream without the object
+        if ws is not None:
+            _need_cuda_at(ws, "ws", torch.uint8, None, dev)
+            _check(call(*args, ws.data_ptr(), ws.numel(), stream), where)
+            return
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured call needs its own workspace: pass ws=new_cache_workspace(...)")
+        key = (dev, stream)
+        ws = _cache_scratch.get(key)
+        code = ERR_WORKSPACE_TOO_SMALL
+        if ws is not None:
+            code = call(*args, ws.data_ptr(), ws.numel(), stream)
+        if code == ERR_WORKSPACE_TOO_SMALL:   # refused before any launch
+            n = int(nbytes())
+            if n == 0:
+                raise QKVPError(ERR_UNSUPPORTED, where)
+            ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+            _check(lib().qkvp_workspace_init(ws.data_ptr(), n, stream), "qkvp_workspace_init")
+            if key in _cache_scratch:
+                ws[:8].copy_(_cache_scratch[key][:8])   # the status word, for poll_cache_status
+            code = call(*args, ws.data_ptr(), n, stream)
+            _cache_scratch[key] = ws
+        if code:
+            raise QKVPError(code, where)
 
 
 def poll_cache_status(device="cuda"):
@@ -838,19 +848,20 @@ def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
     if k.dim() != 3:
         raise ValueError("k must be [H, T, d_qk]")
     T = k.shape[1]
-    if not (k.is_cuda and k.dtype is torch.bfloat16 and k.shape == (H, T, d_qk) and k.is_contiguous() and v.is_cuda
-            and v.dtype is torch.bfloat16 and v.shape == (H, T, d_v) and v.is_contiguous() and pos.is_cuda
-            and pos.dtype is torch.int32 and pos.shape == (T,) and pos.is_contiguous()):
-        _need_cuda(k, "k", torch.bfloat16, (H, T, d_qk))
-        _need_cuda(v, "v", torch.bfloat16, (H, T, d_v))
-        _need_cuda(pos, "pos", torch.int32, (T,))
+    dev = cache.k.get_device()
+    if not (k.get_device() == dev and k.dtype is torch.bfloat16 and k.shape == (H, T, d_qk) and k.is_contiguous()
+            and v.get_device() == dev and v.dtype is torch.bfloat16 and v.shape == (H, T, d_v) and v.is_contiguous()
+            and pos.get_device() == dev and pos.dtype is torch.int32 and pos.shape == (T,) and pos.is_contiguous()):
+        _need_cuda_at(k, "k", torch.bfloat16, (H, T, d_qk), dev)
+        _need_cuda_at(v, "v", torch.bfloat16, (H, T, d_v), dev)
+        _need_cuda_at(pos, "pos", torch.int32, (T,), dev)
     if cu is not None:
-        _quick_cuda(cu, "cu", torch.int32, (B + 1,))
+        _quick_cuda(cu, "cu", torch.int32, (B + 1,), dev)
     if lengths_out is None:
         lengths_out = cache.lengths
     else:
-        _quick_cuda(lengths_out, "lengths_out", torch.int32, (B,))
-    _cache_call("qkvp_cache_append", k.device, ws, lambda: lib().qkvp_cache_append_workspace_bytes(d), d, T, k.data_ptr(),
+        _quick_cuda(lengths_out, "lengths_out", torch.int32, (B,), dev)
+    _cache_call("qkvp_cache_append", dev, ws, lambda: lib().qkvp_cache_append_workspace_bytes(d), d, T, k.data_ptr(),
                 v.data_ptr(), pos.data_ptr(), None if cu is None else cu.data_ptr(), lengths_out.data_ptr())
     return lengths_out
 
@@ -865,17 +876,17 @@ def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, o
     if q.dim() != 3:
         raise ValueError("q must be [Hq, B, d_qk]")
     Hq = q.shape[0]
-    _quick_cuda(q, "q", torch.bfloat16, (Hq, B, d_qk))
-    dev = q.device
+    dev = cache.k.get_device()
+    _quick_cuda(q, "q", torch.bfloat16, (Hq, B, d_qk), dev)
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs cache.weight")
     if out is None:
-        a = torch.empty((B, Hq * d_v), dtype=torch.bfloat16, device=dev)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        a = torch.empty((B, Hq * d_v), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     else:
         a, lse = out
-        _quick_cuda(a, "a", torch.bfloat16, (B, Hq * d_v))
-        _quick_cuda(lse, "lse", torch.float32, (B, Hq))
+        _quick_cuda(a, "a", torch.bfloat16, (B, Hq * d_v), dev)
+        _quick_cuda(lse, "lse", torch.float32, (B, Hq), dev)
     _cache_call("qkvp_decode_attention", dev, ws,
                 lambda: lib().qkvp_decode_attention_workspace_bytes(d, Hq, int(accumulate)), d, Hq,
                 d_qk ** -0.5 if scale is None else scale, q.data_ptr(), a.data_ptr(), lse.data_ptr(), accumulate)
@@ -890,19 +901,19 @@ def cache_evict(cache: KVCache, budget: int, recent: int, lengths_out=None, ws=N
     budget] int32, the slot each new one held before (-1 past the length); the
     lengths change in place, or go to lengths_out."""
     d, H, B, _, _, capacity = cache._packed()
-    dev = cache.k.device
+    dev = cache.k.get_device()
     if cache.weight is None or cache.pos is None:
         raise ValueError("cache_evict needs cache.weight and cache.pos")
     if lengths_out is None:
         lengths_out = cache.lengths
     else:
-        _quick_cuda(lengths_out, "lengths_out", torch.int32, (B,))
+        _quick_cuda(lengths_out, "lengths_out", torch.int32, (B,), dev)
     if not 0 < budget <= capacity:
         raise QKVPError(ERR_INVALID_ARGUMENT, "qkvp_cache_evict")
     if out is None:
-        out = torch.empty((B, H, budget), dtype=torch.int32, device=dev)
+        out = torch.empty((B, H, budget), dtype=torch.int32, device=cache.k.device)
     else:
-        _quick_cuda(out, "slots", torch.int32, (B, H, budget))
+        _quick_cuda(out, "slots", torch.int32, (B, H, budget), dev)
     _cache_call("qkvp_cache_evict", dev, ws, lambda: lib().qkvp_cache_evict_workspace_bytes(d, budget), d, budget, recent,
                 out.data_ptr(), lengths_out.data_ptr())
     return out

@@ -153,12 +153,67 @@ def test_calls_of_two_threads_take_turns(qk, monkeypatch, given):
     monkeypatch.setattr(qk, "_cache_scratch", {})
     monkeypatch.setattr(qk, "_need_cuda", lambda *a: None)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 7, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(qk, "_need_cuda_at", lambda *a: None)
+    monkeypatch.setattr(torch, "device", lambda *a: "cpu")
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     ws = torch.empty(64, dtype=torch.uint8) if given else None
-    threads = [threading.Thread(target=qk._cache_call, args=("qkvp_cache_evict", torch.device("cpu"), ws, lambda: 64))
+    threads = [threading.Thread(target=qk._cache_call, args=("qkvp_cache_evict", 0, ws, lambda: 64))
                for _ in range(4)]
     for t in threads:
         t.start()
     for t in threads:
         t.join()
     assert met == [0] * 4
+
+
+def test_tensors_on_two_devices_are_refused(qk, monkeypatch):
+    """Every tensor of a call lies where the cache's k does."""
+    other = []     # stands for tensors on a second GPU
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: int(any(t is o for o in other)))
+    monkeypatch.setattr(torch.Tensor, "device",
+                        property(lambda t: torch.device("cuda", int(any(t is o for o in other)))))
+    monkeypatch.setattr(qk, "_cache_call", lambda *a: None)
+    cache = qk.new_cache(2, 100, 6, fp8=True, device="cpu")
+    make = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cpu")   # noqa: E731
+    i32, f32 = torch.int32, torch.float32
+    k, v, pos, cu = make(6, 2, 96), make(6, 2, 128), make(2, dtype=i32), make(3, dtype=i32)
+    n, a, lse, slots = make(2, dtype=i32), make(2, 6 * 128), make(2, 6, dtype=f32), make(2, 6, 10, dtype=i32)
+
+    def calls():
+        qk.cache_append(cache, k, v, pos, cu, n)
+        qk.decode_attention(k, cache, out=(a, lse))
+        qk.cache_evict(cache, 10, 2, n, out=slots)
+
+    calls()
+    for t in (cache.v, cache.table, cache.lengths, cache.pos, cache.weight, cache.k_scale, cache.v_scale, k, v, pos, cu, n,
+              a, lse, slots):
+        other[:] = [t]
+        with pytest.raises(ValueError, match="must be on cuda:0"):
+            calls()
+
+
+def test_calls_run_on_the_device_of_the_cache(qk, monkeypatch):
+    """Whatever the current device is: kernels are launched on that one."""
+    at, seen = [0], []
+
+    class Guard:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            at.append(self.dev)
+
+        def __exit__(self, *e):
+            at.pop()
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: at[-1], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 40 + i, raising=False)
+    monkeypatch.setattr(qk, "_need_cuda_at", lambda *a: None)
+    monkeypatch.setattr(qk, "_lib_handle", types.SimpleNamespace(qkvp_cache_evict=lambda *a: seen.append((at[-1], a)) or 0))
+    ws = torch.empty(64, dtype=torch.uint8)
+    for i in (0, 1):
+        qk._cache_call("qkvp_cache_evict", i, ws, lambda: 64, "x")
+    assert seen == [(i, ("x", ws.data_ptr(), 64, 40 + i)) for i in (0, 1)] and at == [0]
