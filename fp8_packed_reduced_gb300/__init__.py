@@ -782,7 +782,8 @@ def new_cache_workspace(cache: KVCache, Hq: int, accumulate: bool = True, budget
     return ws
 
 
-# Workspaces of the cache calls made without one, one per (device, stream).
+# Workspaces of the cache calls made without one, one per (device, stream), kept
+# until release_cache_workspaces.
 # A call that is being captured brings its own: a captured graph keeps the
 # address, and this one is replaced when a later call needs more.
 _cache_scratch = {}
@@ -835,6 +836,15 @@ def poll_cache_status(device="cuda"):
         stream = torch.cuda.current_stream(device)
         ws = _cache_scratch.get((stream.device.index, stream.cuda_stream))
         return (OK, 0) if ws is None else poll_device_status(ws)
+
+
+def release_cache_workspaces():
+    """Frees the workspaces that the cache calls made without ``ws`` keep for
+    their stream's next ones: as large as the largest call has needed, with
+    ``accumulate`` 4 bytes for every sequence, query head and slot that the page
+    table has room for.  What they have recorded and no poll has read goes, too."""
+    with _cache_lock:
+        _cache_scratch.clear()
 
 
 def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):

@@ -724,6 +724,22 @@ def test_one_workspace_for_different_shapes(qk):
             check_decode(qk, c, _normal((4 * c.k.shape[1], c.table.shape[0], 96), 2), ws=ws)
 
 
+def test_kept_workspaces_are_released(qk):
+    """300 MB of scores are not kept for the life of the process."""
+    cache = qk.new_cache(4, 200000, 1)
+    cache.lengths.fill_(0)
+    q = _normal((96, 4, 96), 1).to(DEV)
+    qk.release_cache_workspaces()
+    before = torch.cuda.memory_allocated()
+    qk.decode_attention(q, cache, accumulate=True)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() - before > 300e6
+    qk.release_cache_workspaces()
+    assert torch.cuda.memory_allocated() - before < 1e6
+    a, _ = qk.decode_attention(q, cache)
+    assert not a.any() and qk.poll_cache_status() == (qk.OK, 0)
+
+
 def test_two_threads_on_one_stream(qk):
     """Attentions with weights and evictions of two threads on the default
     stream, on caches of different shapes, without workspaces of their own."""
