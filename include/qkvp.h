@@ -452,7 +452,9 @@ size_t qkvp_cache_evict_workspace_bytes(const qkvp_cache* cache, int budget);
 /* Append T new tokens (the k and v that qkvp_forward writes).  Rows cu[b] ..
  * cu[b + 1) of k and v go to slots lengths[b] + 0, 1, ... of sequence b; their
  * accumulated weight starts at zero.  fp8: per row the scale s = amax / 448 (1
- * when amax is 0) and the codes E(x / s), as everywhere in this library.
+ * when amax is 0) and the codes E(x / s), as everywhere in this library.  The
+ * maximum passes over NaN, whose code is NaN; beside an infinity s is infinite,
+ * the codes of the row's numbers are zero and that of the infinity is NaN.
  *   k, v      in  [H, T, d_qk], [H, T, d_v] bf16
  *   pos       in  [T] int32 position of each token (stored if cache->pos)
  *   cu        in  [B + 1] int32 non-decreasing row offsets, cu[0] = 0, cu[B] =

@@ -18,6 +18,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import synth
 from oracle import cache_oracle as co
 
@@ -159,6 +160,32 @@ def test_append_codes_of_every_mantissa(qk):
     slots = np.arange(T)
     for name in ("k_scale", "v_scale", "k", "v"):
         same(have[name][slots // 64, 0, slots % 64], ref[name][slots // 64, 0, slots % 64], name)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_append_codes_beside_nan_and_infinity(qk, d):
+    """The scale is that of the row's numbers, a NaN's code is NaN; beside an
+    infinity numbers are zero."""
+    k, v = _normal((1, 5, d), 1), _normal((1, 5, 128), 2)
+    for x in (k, v):
+        x[0, 0, 3], x[0, 0, -1] = float("nan"), -float("nan")
+        x[0, 1] = float("nan")
+        x[0, 2, 7] = -float("inf")
+        x[0, 3, 5], x[0, 3, 6] = float("inf"), float("nan")
+    cache = qk.new_cache(1, 5, 1, d, page=16, fp8=True)
+    qk.cache_append(cache, k.to(DEV), v.to(DEV), torch.arange(5, dtype=torch.int32, device=DEV),
+                    torch.tensor([0, 5], dtype=torch.int32, device=DEV))
+    for x, pool, scales in ((k, cache.k, cache.k_scale), (v, cache.v, cache.v_scale)):
+        codes = pool[0, 0, :5].view(torch.float8_e4m3fn).float().cpu().numpy()
+        scales, rows = scales[0, 0, :5].cpu().numpy(), synth.to_numpy_f32(x)[0]
+        for t in (0, 4):
+            want, s, _ = oracle.quantize(np.nan_to_num(rows[t]))
+            assert scales[t] == s
+            same(codes[t], np.where(np.isnan(rows[t]), np.nan, oracle.dequantize(want, 1.0)), f"row {t}")
+        assert scales[1] == 1 and np.isnan(codes[1]).all()
+        for t in (2, 3):
+            assert scales[t] == np.inf
+            same(codes[t], np.where(np.isfinite(rows[t]), 0, np.nan), f"row {t}")
 
 
 def test_append_in_place_many_times(qk):
