@@ -905,9 +905,10 @@ def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, o
 
 def cache_evict(cache: KVCache, budget: int, recent: int, lengths_out=None, ws=None, out=None):
     """Every head of a sequence longer than ``budget`` keeps that many slots:
-    the positions of the last ``recent`` tokens and, of the others, those of
-    the highest accumulated weight (ties: the lowest slot).  Kept slots at or
-    above the budget move into the freed ones below it.  Returns slots [B, H,
+    the positions of the last ``recent`` tokens (should repeated positions make
+    them more than the budget, the lowest slots) and, of the others, those of the
+    highest accumulated weight (ties: the lowest slot).  Kept slots at or above
+    the budget move into the freed ones below it.  Returns slots [B, H,
     budget] int32, the slot each new one held before (-1 past the length); the
     lengths change in place, or go to lengths_out."""
     d, H, B, _, _, capacity = cache._packed()

@@ -487,7 +487,9 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
 /* Eviction.  In every sequence longer than `budget`, each head on its own
  * keeps `budget` slots: first those whose position is within the last
  * `recent` (pos > newest pos - recent), then by accumulated weight from the
- * highest (NaN lowest, -0 = +0), ties to the lowest slot.  Kept slots below
+ * highest (NaN below -inf, -0 = +0), ties to the lowest slot.  Those of the first
+ * kind rank alike, whatever their weights: where positions repeat and there are
+ * more of them than the budget, the lowest slots stay.  Kept slots below
  * `budget` stay where they are; the j-th kept slot at or above it (in slot
  * order) moves, with its scales, weight and position, to the j-th slot freed
  * below.  Needs cache->weight and cache->pos.
