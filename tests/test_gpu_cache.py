@@ -364,6 +364,14 @@ def test_decode_of_the_most_sequences(qk, G, d, fp8):
     check_decode(qk, cache, _normal((G, 4096, d), 3))
 
 
+@pytest.mark.parametrize("G,d,fp8", [(8, 96, False), (16, 64, False), (8, 64, True), (16, 128, True), (1, 96, False)])
+def test_decode_of_a_long_sequence(qk, G, d, fp8):
+    """One sequence over more than 32 blocks, whose records the last of them
+    joins in more than one round (with many heads, one warp a head)."""
+    cache, _ = make_cache(qk, [14001], 1, d, 64, fp8, seed=G)
+    check_decode(qk, cache, _normal((G, 1, d), 4))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_large_scores(qk, fp8):
     """Scores in the thousands, of both signs, rising and falling along the
@@ -636,6 +644,40 @@ def test_evict_long_matches_sorted(qk):
         assert torch.equal(slots[0, h].long(), want)
         assert torch.equal(cache.k[:, h].reshape(cap, -1)[:budget], k0[:, h].reshape(cap, -1)[want])
     assert cache.lengths.tolist() == [budget]
+
+
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_more_slots_than_shared_memory_holds(qk, ties):
+    """A sequence whose keys do not fit into a cluster's shared memory (360448),
+    and one whose keys a block holds, against torch's stable sort."""
+    lens, budget, recent, page, d = [400001, 3000], 2500, 700, 256, 64
+    cap = -(-max(lens) // page) * page
+    cache = qk.new_cache(2, cap, 1, d, page=page, fp8=True)
+    for t in (cache.k, cache.v):
+        t.random_(0, 120)
+    cache.k_scale.uniform_(), cache.v_scale.uniform_()
+    g = torch.Generator().manual_seed(3)
+    w = torch.randperm(2 * cap, generator=g).float()              # distinct, exact in float32
+    cache.weight.copy_((w % 50 if ties else w).view(cache.weight.shape))
+    pos = torch.stack([torch.randperm(cap, generator=g) for _ in lens]).to(torch.int32).to(DEV)
+    cache.pos.copy_(pos.view(cache.pos.shape))
+    cache.lengths.copy_(torch.tensor(lens))
+    flat = lambda t: t.reshape(2, cap, *t.shape[3:])              # noqa: E731   (the table is the identity)
+    before = {n: flat(getattr(cache, n)).clone() for n in ("k", "v", "k_scale", "v_scale", "weight", "pos")}
+    ws = qk.new_cache_workspace(cache, 1, budget=budget)
+    slots = qk.cache_evict(cache, budget, recent, ws=ws)
+    assert qk.poll_device_status(ws) == (qk.OK, 0) and cache.lengths.tolist() == [budget, budget]
+    for b, n in enumerate(lens):
+        key = before["weight"][b, :n].clone()
+        key[before["pos"][b, :n] > before["pos"][b, :n].max() - recent] = float("inf")
+        kept = torch.sort(key, descending=True, stable=True).indices[:budget].sort().values
+        want = torch.arange(budget, device=DEV)
+        stays = torch.zeros(budget, dtype=torch.bool, device=DEV)
+        stays[kept[kept < budget]] = True
+        want[~stays] = kept[kept >= budget]
+        assert torch.equal(slots[b, 0].long(), want)
+        for name, t in before.items():
+            assert torch.equal(flat(getattr(cache, name))[b, :budget], t[b, want]), name
 
 
 @pytest.mark.parametrize("fp8", [False, True])
