@@ -878,10 +878,11 @@ def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
 
 def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, out=None):
     """Attention of one new token per sequence over the cache: q [Hq, B, d_qk]
-    bf16 (as forward() returns it for B tokens; Hq a multiple of the cache's
-    H), scale 1 / sqrt(d_qk) by default.  Returns (a [B, Hq * d_v] bf16, lse [B,
-    Hq] float32), a being oproj_forward's operand; with ``accumulate`` the
-    cache's weights grow by the attention probabilities."""
+    bf16 (as forward() returns it for B tokens, Hq = H; queries from elsewhere
+    may have any multiple of the cache's H), scale 1 / sqrt(d_qk) by default.
+    Returns (a [B, Hq * d_v] bf16, lse [B, Hq] float32), a being oproj_forward's
+    operand; with ``accumulate`` the cache's weights grow by the attention
+    probabilities."""
     d, _, B, d_qk, d_v, _ = cache._packed()
     if q.dim() != 3:
         raise ValueError("q must be [Hq, B, d_qk]")
@@ -907,8 +908,9 @@ def cache_evict(cache: KVCache, budget: int, recent: int, lengths_out=None, ws=N
     """Every head of a sequence longer than ``budget`` keeps that many slots:
     the positions of the last ``recent`` tokens (should repeated positions make
     them more than the budget, the lowest slots) and, of the others, those of the
-    highest accumulated weight (ties: the lowest slot).  Kept slots at or above
-    the budget move into the freed ones below it.  Returns slots [B, H,
+    highest accumulated weight (ties: the lowest slot; right after a prompt, with
+    no decode_attention since that accumulates, all of them).  Kept slots at or
+    above the budget move into the freed ones below it.  Returns slots [B, H,
     budget] int32, the slot each new one held before (-1 past the length); the
     lengths change in place, or go to lengths_out."""
     d, H, B, _, _, capacity = cache._packed()

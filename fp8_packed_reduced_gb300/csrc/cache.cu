@@ -67,9 +67,9 @@ namespace {
 // consecutive tokens of one head with 3.5 KB of loads in flight, and the work
 // per row of the E4M3 form (maximum, scale, its reciprocal) is done for eight
 // rows at once.  Every access is 64 bytes (32 of codes) of a row, whole
-// sectors.  49152 tokens x 6 heads to E4M3, 203 MB: 35.6 us, 5.70 TB/s (with
-// sixteen lanes a row 75 us; in blocks of 256 threads 37.1); 22650 tokens x 8
-// heads of d_qk = 128 as bf16, 197 MB: 31.0 us, 6.36 TB/s.
+// sectors.  49152 tokens x 6 heads to E4M3, 203 MB: 35.2 us, 5.77 TB/s (with
+// sixteen lanes a row 75 us; in blocks of 256 threads 37.1); 23843 tokens x 8
+// heads of d_qk = 128 as bf16, 197 MB: 31.0 us, 6.35 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
 
@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kAppendThreads)
   wait_for_previous();
 
   // Offsets that fall anywhere give rows to no sequence or to two: every block
-  // then stores nothing, and no length grows.
+  // then stores nothing, and no length grows.  (Asked for ahead of k and v: with
+  // the offsets behind them the calls above took 36.1 and 31.5 us.  4096
+  // sequences of one token each x 8 heads: 12.4 us, without the test 10.9.)
   bool fall = false;
   if (cu != nullptr)
     for (int b = threadIdx.x; b < c.B; b += kAppendThreads) fall |= __ldg(cu + b + 1) < __ldg(cu + b);

@@ -472,7 +472,8 @@ int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const u
  * own k and v included, once appended):
  *   s_i = scale * q . k_i,  a = sum_i e^(s_i) v_i / sum_i e^(s_i),
  *   lse = ln sum_i e^(s_i)
- * Query head h * (Hq / H) + g reads K/V head h (Hq a multiple of H).  A
+ * Query head h * (Hq / H) + g reads K/V head h (Hq a multiple of H; qkvp_forward
+ * gives Hq = H, more are for queries from elsewhere).  A
  * sequence without live slots gives a = 0 and lse = -inf.
  *   q         in  [Hq, B, d_qk] bf16 (head-major, as qkvp_forward writes it)
  *   a         out [B, Hq * d_v] bf16: the heads side by side, the operand of
@@ -492,7 +493,9 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
  * more of them than the budget, the lowest slots stay.  Kept slots below
  * `budget` stay where they are; the j-th kept slot at or above it (in slot
  * order) moves, with its scales, weight and position, to the j-th slot freed
- * below.  Needs cache->weight and cache->pos.
+ * below.  Needs cache->weight and cache->pos.  (Appended slots start with the
+ * weight zero and only qkvp_decode_attention adds to it: right after a prompt
+ * all but the recent slots tie.)
  *   budget    1 .. max_pages * page;  recent 0 .. budget
  *   slots     out [B, H, budget] int32: the slot each new slot held before
  *                 (itself if it stayed), -1 past the length
