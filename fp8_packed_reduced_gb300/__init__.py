@@ -832,10 +832,9 @@ def poll_cache_status(device="cuda"):
     """(status, kernel id) that the cache calls made without ``ws`` on the
     device's current stream have recorded since the last poll (a token without
     room, a length or a page out of range); clears it.  Waits for the stream."""
-    with _cache_lock:
-        stream = torch.cuda.current_stream(device)
-        ws = _cache_scratch.get((stream.device.index, stream.cuda_stream))
-        return (OK, 0) if ws is None else poll_device_status(ws)
+    stream = torch.cuda.current_stream(device)
+    ws = _cache_scratch.get((stream.device.index, stream.cuda_stream))
+    return (OK, 0) if ws is None else poll_device_status(ws)   # (no lock: other threads go on launching)
 
 
 def release_cache_workspaces():
