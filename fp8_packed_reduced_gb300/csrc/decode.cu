@@ -22,7 +22,9 @@
 //     largest), row scales multiply scores and probabilities in float32.  The
 //     probabilities times v's row scales are held relative to 2^-15 of their own
 //     running maximum (rows of very different scale may meet), again at the top
-//     of the range, so that rounding is relative down to 2^-29 of it.
+//     of the range, so that rounding is relative down to 2^-29 of it.  Both are
+//     taken relative to the scores' maximum first: the logarithm of a scale
+//     added to a score of 2^16 would keep 2^-8 of itself.
 //   - Probabilities enter the second product as two bf16, which hold 2^-15 of
 //     them relatively (one holds 2^-8, as much again as the rounding of the
 //     output): the second takes the tile's odd columns, which up to four heads
@@ -79,7 +81,7 @@ struct DecodeParams {
                          // it; zero between calls
 };
 
-// A record: O [nh][128] relative to 2^mo, then m [nh], l [nh], mo [nh].
+// A record: O [nh][128] relative to 2^(m + mo), then m [nh], l [nh] (relative to 2^m), mo [nh].
 __host__ __device__ constexpr int record_floats(int nh) { return nh * (kDv + 4); }
 
 // ---------------------------------------------------------------------------
@@ -283,11 +285,11 @@ __device__ __forceinline__ Unit locate(const Plan& pl, const DecodeParams& p, in
 // Results
 // ---------------------------------------------------------------------------
 // Writes a and lse of query head hq from l, m (base 2) and four columns of O
-// relative to 2^mo per lane.
+// relative to 2^(m + mo) per lane.
 __device__ __forceinline__ void write_head(const DecodeParams& p, int b, int hq, float m, float l, float mo, float4 o) {
   const int lane = threadIdx.x & 31, Hq = p.c.H * p.G;
   const bool none = l == 0.f;
-  const float f = none ? 0.f : exp2_below(mo, m) / l;
+  const float f = none ? 0.f : ex2(mo) / l;
   const int64_t at = static_cast<int64_t>(b) * Hq + hq;
   uint2 w = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
   if (none) w = make_uint2(0, 0);
@@ -344,19 +346,21 @@ __device__ __forceinline__ unsigned int count_arrival(unsigned int* p) {
 template <class Load, class Rec>
 __device__ __forceinline__ Joined join_records(const Load& load, const Rec& rec, int count, int n, int nh) {
   const int lane = threadIdx.x & 31;
-  Joined j{-INFINITY, 0.f, -INFINITY, make_float4(0.f, 0.f, 0.f, 0.f)};
+  Joined j{-INFINITY, 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   for (int i0 = 0; i0 < count; i0 += 32) {
     const int k = min(32, count - i0);
-    float rm = -INFINITY, rl = 0.f, rmo = -INFINITY;
+    float rm = -INFINITY, rl = 0.f, rmo = 0.f;
     if (lane < k) {
       const float* r = rec(i0 + lane);
       rm = load(r + nh * kDv + n);
       rl = load(r + nh * (kDv + 1) + n);
       rmo = load(r + nh * (kDv + 2) + n);
     }
-    const float m = fmaxf(j.m, warp_max(rm)), mo = fmaxf(j.mo, warp_max(rmo));
-    const float f = exp2_below(rmo, mo), back = exp2_below(j.mo, mo);
-    j.l = j.l * exp2_below(j.m, m) + warp_sum(rl * exp2_below(rm, m));
+    const float m = fmaxf(j.m, warp_max(rm)), up = below(m);
+    const float z = rm - up + rmo, zj = j.m - up + j.mo;   // where the records' O stand, relative to 2^m
+    const float mo = below(fmaxf(zj, warp_max(z)));
+    const float f = ex2(z - mo), back = ex2(zj - mo);
+    j.l = j.l * ex2(j.m - up) + warp_sum(rl * ex2(rm - up));
     j.o = make_float4(j.o.x * back, j.o.y * back, j.o.z * back, j.o.w * back);
     j.m = m;
     j.mo = mo;
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
   __shared__ int red[kWarps], red_max[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int B = p.c.B, Hq = p.c.H * p.G, nrec = record_floats(p.nh);
-  constexpr float kTop = FP8 ? 15.f : 0.f;   // O is relative to 2^(mo - kTop)
+  constexpr float kTop = FP8 ? 15.f : 0.f;   // O is relative to 2^(m + mo - kTop); bf16: mo is 0
   const auto head_of = [&](int t, int e) { return E == 1 ? c : 8 * t + 2 * c + e; };   // of this lane's scores
 
   wait_for_previous();
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
         if (from_start && to_end) {
           const int64_t at = static_cast<int64_t>(cur_b) * Hq + h * p.G + ch0 + n;
           const bool none = x == 0.f;
-          const float f = none ? 0.f : exp2_below(mo[t][e] - kTop, m[t][e]) / x;
+          const float f = none ? 0.f : ex2(below(mo[t][e]) - kTop) / x;
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) {
             const uint32_t w = none ? 0u : pack_bf16x2(o[t][mt][e] * f, o[t][mt][2 + e] * f);
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
           if (g == 0) {
             rec[p.nh * kDv + n] = m[t][e];
             rec[p.nh * (kDv + 1) + n] = x;
-            rec[p.nh * (kDv + 2) + n] = mo[t][e] - kTop;
+            rec[p.nh * (kDv + 2) + n] = below(mo[t][e]) - kTop;
           }
         }
       }
@@ -674,7 +678,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           qmul[t][e] = p.scale_log2 * (FP8 ? __shfl_sync(0xffffffffu, back, 8 * c + 4 * e) : 1.f);
-          m[t][e] = mo[t][e] = -INFINITY;
+          m[t][e] = -INFINITY;
+          mo[t][e] = FP8 ? -INFINITY : 0.f;
           l[t][e] = 0.f;
           const int hn = head_of(t, e);
           score_at[t][e] = p.scores != nullptr && hn < nh
@@ -736,39 +741,50 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
     uint32_t rest[NT][2];      // and what bf16 leaves of them, where they fill the tile
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float y[SUB][4];   // E4M3: the score plus log2 of v's row scale
-      float top[E], otop[E];
+      float y[SUB][4];   // E4M3: the score relative to the maximum, plus log2 of v's row scale
+      float next[E];     // the maximum with this unit
       bool grows = false;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        top[e] = otop[e] = -INFINITY;
+        float top = m[t][e];
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             float& v = x[t][s][2 * r + e];
             v = live[s][r] ? v * (FP8 ? qmul[t][e] * ks[s][r] : qmul[t][e]) : -INFINITY;
-            top[e] = fmaxf(top[e], v);
-            if (FP8) {
-              y[s][2 * r + e] = live[s][r] ? v + lv[s][r] : -INFINITY;
-              otop[e] = fmaxf(otop[e], y[s][2 * r + e]);
-            }
+            top = fmaxf(top, v);
             if (score_at[t][e] && 16 * s + 8 * r + g < valid) score_at[t][e][u * KS + 16 * s + 8 * r] = v;
           }
 #pragma unroll
-        for (int s = 4; s < 32; s <<= 1) {
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], s));
-          if (FP8) otop[e] = fmaxf(otop[e], __shfl_xor_sync(0xffffffffu, otop[e], s));
+        for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        next[e] = top;
+        grows |= top > m[t][e];
+      }
+      float otop[E];
+      if (FP8) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          otop[e] = mo[t][e] + (m[t][e] - below(next[e]));
+#pragma unroll
+          for (int s = 0; s < SUB; ++s)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float& v = y[s][2 * r + e];
+              v = live[s][r] ? x[t][s][2 * r + e] - below(next[e]) + lv[s][r] : -INFINITY;
+              otop[e] = fmaxf(otop[e], v);
+            }
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) otop[e] = fmaxf(otop[e], __shfl_xor_sync(0xffffffffu, otop[e], s));
+          grows |= otop[e] > mo[t][e];
         }
-        top[e] = fmaxf(top[e], m[t][e]);
-        otop[e] = FP8 ? fmaxf(otop[e], mo[t][e]) : top[e];
-        grows |= top[e] > m[t][e] || otop[e] > mo[t][e];
       }
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          l[t][e] *= exp2_below(m[t][e], top[e]);
-          const float fo = exp2_below(mo[t][e], otop[e]);
+          const float fall = m[t][e] - below(next[e]), fl = ex2(fall);
+          const float fo = FP8 ? ex2(fall + (mo[t][e] - below(otop[e]))) : fl;
+          l[t][e] *= fl;
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) {
             o[t][mt][e] *= fo;
@@ -778,8 +794,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const __grid_con
               o[t][mt][3] *= fo;
             }
           }
-          m[t][e] = top[e];
-          mo[t][e] = otop[e];
+          m[t][e] = next[e];
+          if (FP8) mo[t][e] = otop[e];
         }
       }
       float w[SUB][4];

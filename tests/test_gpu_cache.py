@@ -381,6 +381,30 @@ def test_decode_large_scores(qk, fp8):
     check_decode(qk, cache, _normal((2, 2, 96), 6) * 256)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("size", [10, 16, 22])
+@pytest.mark.parametrize("G", [1, 8, 16])
+def test_decode_where_one_slot_takes_all(qk, fp8, size, G):
+    """Scores so large that one probability is 1 and the others are nothing:
+    a is that slot's v, however large the scores are, rounded to bf16 (2^-8),
+    the probability having been rounded once (E4M3: 2^-11) and the scale's
+    logarithm taken (2^-18)."""
+    lens = [1, 3, 700, 1, 5000]
+    cache, _ = make_cache(qk, lens, 1, 96, 32, fp8, seed=5)
+    q = _normal((G, len(lens), 96), 9) * 2.0 ** size
+    a, _ = qk.decode_attention(q.to(DEV), cache)
+    ref, _, _, _, most = co.decode_attention(host(cache), synth.to_numpy_f32(q), 96 ** -0.5)
+    one = np.zeros(most.shape, bool)      # where the best score is ahead by more than the scores may be off
+    for b in range(len(lens)):
+        s = synth.to_numpy_f32(q)[:, b].astype(np.float64) @ co.live_rows(host(cache), b, 0)[0].T * 96 ** -0.5
+        s = np.sort(np.concatenate([s, np.full((G, 1), -np.inf)], 1), 1)
+        one[b] = s[:, -1] - s[:, -2] > 25 + 4 * 104 * 2.0 ** -23 * most[b]
+    assert one[[0, 3]].all() and one.mean() > 0.8
+    err = np.abs(synth.to_numpy_f32(a.cpu()).reshape(ref.shape) - ref)
+    bound = (2.0 ** -8 + (2.0 ** -11 + 2.0 ** -18 if fp8 else 0)) * np.abs(ref)
+    assert (err <= bound)[one].all(), np.max((err / np.maximum(np.abs(ref), 1e-30))[one])
+
+
 def test_decode_e4m3_rows_of_any_scale(qk):
     """k and v rows whose scales span 2^-40 .. 2^40, and a q whose values span
     2^20: what is small beside its neighbours is kept relatively."""
