@@ -54,6 +54,22 @@ class Dims(ctypes.Structure):
 _CACHE_PACK = struct.Struct("8i8Q").pack   # the layout of CacheDesc
 
 
+class AttentionDesc(ctypes.Structure):
+    """The C ``qkvp_attention`` struct."""
+
+    _fields_ = ([(n, ctypes.c_int) for n in ("T", "Hq", "H", "d_qk", "d_v", "B", "window", "sinks")]
+                + [("scale", ctypes.c_float), ("cu", ctypes.c_void_p)])
+
+
+class NormRopeDesc(ctypes.Structure):
+    """The C ``qkvp_norm_rope`` struct."""
+
+    _fields_ = ([(n, ctypes.c_int) for n in ("T", "Hq", "H", "d_qk", "d_v", "axes")]
+                + [("sections", ctypes.c_int * 3), ("max_pos", ctypes.c_int), ("eps", ctypes.c_float),
+                   ("ldy", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("rope_table", "pos", "q_gain", "k_gain")])
+
+
 class CacheDesc(ctypes.Structure):
     """The C ``qkvp_cache`` struct."""
 
@@ -111,6 +127,14 @@ def lib() -> ctypes.CDLL:
                                   + [ctypes.c_size_t, _P]),
             "qkvp_decode_attention": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_float]
                                       + [_P] * 3 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
+            "qkvp_decode_window_attention": (ctypes.c_int, [_P] + [ctypes.c_int] * 3 + [ctypes.c_float]
+                                             + [_P] * 3 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
+            "qkvp_norm_rope_workspace_bytes": (ctypes.c_size_t, [_P]),
+            "qkvp_norm_rope_forward": (ctypes.c_int, [_P] * 7 + [ctypes.c_size_t, _P]),
+            "qkvp_norm_rope_backward": (ctypes.c_int, [_P] * 10 + [ctypes.c_size_t, _P]),
+            "qkvp_attention_workspace_bytes": (ctypes.c_size_t, [_P]),
+            "qkvp_attention_forward": (ctypes.c_int, [_P] * 7 + [ctypes.c_size_t, _P]),
+            "qkvp_attention_backward": (ctypes.c_int, [_P] * 11 + [ctypes.c_size_t, _P]),
             "qkvp_cache_evict": (ctypes.c_int, [_P] + [ctypes.c_int] * 2 + [_P] * 3
                                  + [ctypes.c_size_t, _P]),
         }
@@ -808,7 +832,8 @@ def _cache_call(where: str, dev: int, ws, nbytes, *args):
             _check(call(*args, ws.data_ptr(), ws.numel(), stream), where)
             return
         if torch.cuda.is_current_stream_capturing():
-            raise ValueError("a captured call needs its own workspace: pass ws=new_cache_workspace(...)")
+            raise ValueError("a captured call needs its own workspace: pass ws=new_cache_workspace(...),"
+                             " new_attention_workspace(...) or new_norm_rope_workspace(...)")
         key = (dev, stream)
         ws = _cache_scratch.get(key)
         code = ERR_WORKSPACE_TOO_SMALL
@@ -846,6 +871,18 @@ def release_cache_workspaces():
         _cache_scratch.clear()
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _window_of(window, sinks):
+    """window (None: 0, no window) and sinks as the library takes them."""
+    if window is not None and window < 1:
+        raise ValueError(f"window must be at least 1 (None: no window), got {window}")
+    if sinks < 0:
+        raise ValueError(f"sinks must not be negative, got {sinks}")
+    return 0 if window is None else min(window, _INT_MAX), min(sinks, _INT_MAX)
+
+
 def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
     """Append new tokens: k [H, T, d_qk], v [H, T, d_v] bf16 (as forward()
     returns them) and pos [T] int32.  Rows cu[b] .. cu[b + 1) (cu [B + 1] int32)
@@ -875,13 +912,15 @@ def cache_append(cache: KVCache, k, v, pos, cu=None, lengths_out=None, ws=None):
     return lengths_out
 
 
-def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, out=None):
+def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, out=None, window=None, sinks=0):
     """Attention of one new token per sequence over the cache: q [Hq, B, d_qk]
     bf16 (as forward() returns it for B tokens, Hq = H; queries from elsewhere
     may have any multiple of the cache's H), scale 1 / sqrt(d_qk) by default.
     Returns (a [B, Hq * d_v] bf16, lse [B, Hq] float32), a being oproj_forward's
     operand; with ``accumulate`` the cache's weights grow by the attention
-    probabilities."""
+    probabilities.  With ``window`` only a sequence's first ``sinks`` slots and
+    its last ``window`` ones are seen (slots, so in a cache that cache_evict has
+    not changed)."""
     d, _, B, d_qk, d_v, _ = cache._packed()
     if q.dim() != 3:
         raise ValueError("q must be [Hq, B, d_qk]")
@@ -890,6 +929,8 @@ def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, o
     _quick_cuda(q, "q", torch.bfloat16, (Hq, B, d_qk), dev)
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs cache.weight")
+    if window is not None:
+        window, sinks = _window_of(window, sinks)
     if out is None:
         a = torch.empty((B, Hq * d_v), dtype=torch.bfloat16, device=q.device)
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
@@ -897,9 +938,14 @@ def decode_attention(q, cache: KVCache, scale=None, accumulate=False, ws=None, o
         a, lse = out
         _quick_cuda(a, "a", torch.bfloat16, (B, Hq * d_v), dev)
         _quick_cuda(lse, "lse", torch.float32, (B, Hq), dev)
-    _cache_call("qkvp_decode_attention", dev, ws,
-                lambda: lib().qkvp_decode_attention_workspace_bytes(d, Hq, int(accumulate)), d, Hq,
-                d_qk ** -0.5 if scale is None else scale, q.data_ptr(), a.data_ptr(), lse.data_ptr(), accumulate)
+    need = lambda: lib().qkvp_decode_attention_workspace_bytes(d, Hq, int(accumulate))   # noqa: E731
+    scale = d_qk ** -0.5 if scale is None else scale
+    if window is None:
+        _cache_call("qkvp_decode_attention", dev, ws, need, d, Hq, scale, q.data_ptr(), a.data_ptr(), lse.data_ptr(),
+                    accumulate)
+    else:
+        _cache_call("qkvp_decode_window_attention", dev, ws, need, d, Hq, window, sinks, scale, q.data_ptr(), a.data_ptr(),
+                    lse.data_ptr(), accumulate)
     return a, lse
 
 
@@ -929,3 +975,178 @@ def cache_evict(cache: KVCache, budget: int, recent: int, lengths_out=None, ws=N
     _cache_call("qkvp_cache_evict", dev, ws, lambda: lib().qkvp_cache_evict_workspace_bytes(d, budget), d, budget, recent,
                 out.data_ptr(), lengths_out.data_ptr())
     return out
+
+
+# ----------------------------------------------------------------------------
+# Between the projections: split, norm and rotation; causal attention
+# ----------------------------------------------------------------------------
+
+def _attention_desc(q, k, v, cu, window, sinks, scale):
+    """The C descriptor of an attention's arguments, and their device."""
+    if not (isinstance(q, torch.Tensor) and q.dim() == 3 and isinstance(k, torch.Tensor) and k.dim() == 3):
+        raise ValueError("q must be [Hq, T, d_qk], k [H, T, d_qk]")
+    _need_cuda(q, "q", torch.bfloat16)
+    Hq, T, d = q.shape
+    H, dev = k.shape[0], q.get_device()
+    _quick_cuda(k, "k", torch.bfloat16, (H, T, d), dev)
+    _quick_cuda(v, "v", torch.bfloat16, (H, T, 128), dev)
+    B, at = 1, None
+    if cu is not None:
+        if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
+            raise ValueError("cu must be [B + 1], B >= 1")
+        B = cu.shape[0] - 1
+        _quick_cuda(cu, "cu", torch.int32, (B + 1,), dev)
+        at = cu.data_ptr()
+    window, sinks = _window_of(window, sinks)
+    return AttentionDesc(T, Hq, H, d, 128, B, window, sinks, d ** -0.5 if scale is None else scale, at), dev
+
+
+def new_attention_workspace(T: int, Hq: int, device="cuda") -> torch.Tensor:
+    """A zero-initialised workspace for attention_forward and attention_backward
+    of up to T tokens and Hq query heads."""
+    n = int(lib().qkvp_attention_workspace_bytes(ctypes.byref(AttentionDesc(T, Hq, 1, 96, 128, 1, 0, 0, 1.0, None))))
+    if n == 0:
+        raise QKVPError(ERR_UNSUPPORTED, "new_attention_workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        _check(lib().qkvp_workspace_init(_ptr(ws), n, _stream(ws.device)), "qkvp_workspace_init")
+    return ws
+
+
+def attention_forward(q, k, v, cu=None, window=None, sinks=0, scale=None, ws=None, out=None):
+    """Causal attention over packed sequences: q [Hq, T, d_qk], k [H, T, d_qk],
+    v [H, T, 128] bf16 as forward() or norm_rope_forward() return them (Hq a
+    multiple of H); rows cu[b] .. cu[b + 1) (cu [B + 1] int32; None: all T) are
+    sequence b.  A token sees its sequence's tokens up to itself, with ``window``
+    the last ``window`` of them and the sequence's first ``sinks``.  scale: 1 /
+    sqrt(d_qk) by default.  Returns (a [T, Hq * 128] bf16, oproj_forward's
+    operand, lse [Hq, T] float32); rows of no sequence give 0 and -inf.  Bad
+    offsets: poll_device_status(ws), or without ws poll_cache_status(), tells."""
+    d, dev = _attention_desc(q, k, v, cu, window, sinks, scale)
+    if out is None:
+        a = torch.empty((d.T, d.Hq * 128), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((d.Hq, d.T), dtype=torch.float32, device=q.device)
+    else:
+        a, lse = out
+        _quick_cuda(a, "a", torch.bfloat16, (d.T, d.Hq * 128), dev)
+        _quick_cuda(lse, "lse", torch.float32, (d.Hq, d.T), dev)
+    r = ctypes.byref(d)
+    _cache_call("qkvp_attention_forward", dev, ws, lambda: lib().qkvp_attention_workspace_bytes(r), r, q.data_ptr(),
+                k.data_ptr(), v.data_ptr(), a.data_ptr(), lse.data_ptr())
+    return a, lse
+
+
+def attention_backward(da, q, k, v, a, lse, cu=None, window=None, sinks=0, scale=None, ws=None, out=None):
+    """Gradient of attention_forward from da [T, Hq * 128] (oproj_backward's) and
+    the forward's inputs and results; the other arguments as there.  Returns a
+    dict with dq [Hq, T, d_qk], dk [H, T, d_qk], dv [H, T, 128] (bf16, backward()'s
+    operands), the same on every run."""
+    d, dev = _attention_desc(q, k, v, cu, window, sinks, scale)
+    _quick_cuda(da, "da", torch.bfloat16, (d.T, d.Hq * 128), dev)
+    _quick_cuda(a, "a", torch.bfloat16, (d.T, d.Hq * 128), dev)
+    _quick_cuda(lse, "lse", torch.float32, (d.Hq, d.T), dev)
+    o = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v)) if out is None else out
+    for name, like in (("dq", q), ("dk", k), ("dv", v)):
+        _quick_cuda(o[name], name, torch.bfloat16, like.shape, dev)
+    r = ctypes.byref(d)
+    _cache_call("qkvp_attention_backward", dev, ws, lambda: lib().qkvp_attention_workspace_bytes(r), r, da.data_ptr(),
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), lse.data_ptr(), o["dq"].data_ptr(),
+                o["dk"].data_ptr(), o["dv"].data_ptr())
+    return o
+
+
+def _norm_rope_desc(y, pos, rope_table, Hq, H, d, q_gain, k_gain, eps, sections):
+    """The C descriptor of a split's arguments, and their device."""
+    N = (Hq + H) * d + H * 128
+    if not isinstance(y, torch.Tensor) or not y.is_cuda or y.dtype != torch.bfloat16 or y.dim() != 2 or y.shape[1] != N:
+        raise ValueError(f"y must be a CUDA bfloat16 tensor [T, {N}]")
+    T, dev = y.shape[0], y.get_device()
+    if y.stride(1) != 1 or (T > 1 and y.stride(0) < N):
+        raise ValueError("y's rows must be contiguous and must not overlap")
+    ldy = y.stride(0) if T > 1 else -(-N // 8) * 8
+    axes = 1 if sections is None else len(sections)
+    if not 1 <= axes <= 3:
+        raise ValueError("sections must name one to three axes")
+    _quick_cuda(pos, "pos", torch.int32, (T,) if sections is None else (axes, T), dev)
+    _need_cuda_at(rope_table, "rope_table", torch.float32, None, dev)
+    if rope_table.dim() != 3 or rope_table.shape[0] != d // 4 or rope_table.shape[2] != 4:
+        raise ValueError("rope_table must be build_rope_table(max_pos, d_qk)")
+    if (q_gain is None) != (k_gain is None):
+        raise ValueError("q_gain and k_gain: both or neither")
+    at = [None, None]
+    if q_gain is not None:
+        _quick_cuda(q_gain, "q_gain", torch.float32, (d,), dev)
+        _quick_cuda(k_gain, "k_gain", torch.float32, (d,), dev)
+        at = [q_gain.data_ptr(), k_gain.data_ptr()]
+    parts = (d // 2,) if sections is None else tuple(sections)
+    return NormRopeDesc(T, Hq, H, d, 128, axes, (ctypes.c_int * 3)(*parts), rope_table.shape[1], eps, ldy,
+                        rope_table.data_ptr(), pos.data_ptr(), *at), dev
+
+
+def new_norm_rope_workspace(device="cuda") -> torch.Tensor:
+    """A zero-initialised workspace for norm_rope_forward and norm_rope_backward
+    of any shape."""
+    one = 16   # an aligned address that the size does not depend on
+    d = NormRopeDesc(1, 1, 1, 128, 128, 1, (ctypes.c_int * 3)(), 1, 0.0, 384, one, one, one, one)
+    ws = torch.empty(int(lib().qkvp_norm_rope_workspace_bytes(ctypes.byref(d))), dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        _check(lib().qkvp_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)), "qkvp_workspace_init")
+    return ws
+
+
+def norm_rope_forward(y, pos, rope_table, Hq, H, d_qk=96, q_gain=None, k_gain=None, eps=1e-6, sections=None, ws=None,
+                      out=None):
+    """The rows of a packed projection split, normalised and rotated: y [T, N]
+    bf16 with N = (Hq + H) * d_qk + H * 128 (q, k and v heads side by side; its
+    rows may be part of wider ones), pos [T] int32, rope_table from
+    build_rope_table, gains [d_qk] float32.  ``sections`` (up to three even
+    numbers of pairs, d_qk / 2 in all) gives every axis of pos [axes, T] its part
+    of the rotation.  Returns (q [Hq, T, d_qk], k [H, T, d_qk], v [H, T, 128],
+    rstd [Hq + H, T] float32).  A position outside the table counts as the nearer
+    end: poll_device_status(ws), or without ws poll_cache_status(), tells."""
+    d, dev = _norm_rope_desc(y, pos, rope_table, Hq, H, d_qk, q_gain, k_gain, eps, sections)
+    T = d.T
+    if out is None:
+        bf = dict(dtype=torch.bfloat16, device=y.device)
+        out = (torch.empty((Hq, T, d_qk), **bf), torch.empty((H, T, d_qk), **bf), torch.empty((H, T, 128), **bf),
+               torch.empty((Hq + H, T), dtype=torch.float32, device=y.device))
+    q, k, v, rstd = out
+    _quick_cuda(q, "q", torch.bfloat16, (Hq, T, d_qk), dev)
+    _quick_cuda(k, "k", torch.bfloat16, (H, T, d_qk), dev)
+    _quick_cuda(v, "v", torch.bfloat16, (H, T, 128), dev)
+    _quick_cuda(rstd, "rstd", torch.float32, (Hq + H, T), dev)
+    r = ctypes.byref(d)
+    _cache_call("qkvp_norm_rope_forward", dev, ws, lambda: lib().qkvp_norm_rope_workspace_bytes(r), r, y.data_ptr(),
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), rstd.data_ptr())
+    return q, k, v, rstd
+
+
+def norm_rope_backward(dq, dk, dv, y, rstd, pos, rope_table, q_gain=None, k_gain=None, sections=None, ws=None, out=None):
+    """Gradient of norm_rope_forward from dq [Hq, T, d_qk], dk [H, T, d_qk], dv
+    [H, T, 128] bf16 (attention_backward's) and the forward's y and rstd.  Returns
+    a dict with dy [T, N] bf16 and dq_gain, dk_gain [d_qk] float32 (None without
+    gains), the same on every run."""
+    if not all(isinstance(t, torch.Tensor) and t.dim() == 3 for t in (dq, dk)):
+        raise ValueError("dq must be [Hq, T, d_qk], dk [H, T, d_qk]")
+    Hq, T, d_qk = dq.shape
+    H = dk.shape[0]
+    d, dev = _norm_rope_desc(y, pos, rope_table, Hq, H, d_qk, q_gain, k_gain, 0.0, sections)
+    if d.T != T:
+        raise ValueError(f"y must have the {T} rows of dq")
+    _quick_cuda(dq, "dq", torch.bfloat16, (Hq, T, d_qk), dev)
+    _quick_cuda(dk, "dk", torch.bfloat16, (H, T, d_qk), dev)
+    _quick_cuda(dv, "dv", torch.bfloat16, (H, T, 128), dev)
+    _quick_cuda(rstd, "rstd", torch.float32, (Hq + H, T), dev)
+    if out is None:
+        make = lambda: None if q_gain is None else torch.empty((d_qk,), dtype=torch.float32, device=y.device)   # noqa: E731
+        out = dict(dy=torch.empty((T, y.shape[1]), dtype=torch.bfloat16, device=y.device), dq_gain=make(), dk_gain=make())
+    o = out
+    _quick_cuda(o["dy"], "dy", torch.bfloat16, tuple(y.shape), dev)
+    if q_gain is not None:
+        _quick_cuda(o["dq_gain"], "dq_gain", torch.float32, (d_qk,), dev)
+        _quick_cuda(o["dk_gain"], "dk_gain", torch.float32, (d_qk,), dev)
+    r = ctypes.byref(d)
+    _cache_call("qkvp_norm_rope_backward", dev, ws, lambda: lib().qkvp_norm_rope_workspace_bytes(r), r, dq.data_ptr(),
+                dk.data_ptr(), dv.data_ptr(), y.data_ptr(), rstd.data_ptr(), o["dy"].data_ptr(),
+                *((None, None) if q_gain is None else (o["dq_gain"].data_ptr(), o["dk_gain"].data_ptr())))
+    return o

@@ -1,0 +1,216 @@
+// Causal attention over packed sequences with a sliding window and first tokens
+// that stay visible: arguments, the sequences' bounds and the rows of the
+// products on the CUDA cores.
+//   token i of a sequence that starts at s sees its tokens j <= i with
+//   i - j < window or j < s + sinks
+//   x_ij = scale q_i . k_j,  p_ij = e^(x_ij - lse_i),  a_i = sum_j p_ij v_j
+//   dv_j = sum_i p_ij da_i,  ds_ij = p_ij (da_i . v_j - da_i . a_i)
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+#pragma once
+
+#include "cache.cuh"
+#include "kernels.cuh"
+
+namespace qkvp {
+
+enum AttnKernelId : int { KID_ATTN_FWD = 18, KID_ATTN_DELTA = 19, KID_ATTN_DQ = 20, KID_ATTN_DKV = 21 };
+
+struct AttnArgs {
+  int T, Hq, H, G, d;        // G = Hq / H
+  int B;                     // sequences
+  int window, sinks;         // window: T and more is no window
+  float scale, scale_log2;   // scale * log2(e)
+  const int32_t* cu;         // [B + 1], or null: one sequence of T tokens
+  const uint16_t *q, *k, *v; // [Hq, T, d], [H, T, d], [H, T, 128] bf16
+  uint16_t* a;               // [T, Hq * 128] bf16
+  float* lse;                // [Hq, T], natural logarithm
+  const uint16_t* da;        // [T, Hq * 128]
+  float* delta;              // [Hq, T] da . a
+  uint16_t *dq, *dk, *dv;
+};
+
+// A token's sequence, [start, end); start < 0: none.
+struct Span {
+  int start, end;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& p, int row) {
+  if (p.cu == nullptr) return Span{0, p.T};
+  int lo = -1, hi = p.B;   // cu[lo] <= row < cu[hi], taking cu[-1] as 0 and cu[B] as found below
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu + mid) <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  if (lo < 0) return Span{-1, -1};
+  const int end = min(__ldg(p.cu + lo + 1), p.T);
+  if (end <= row) return Span{-1, -1};   // behind the last sequence
+  return Span{max(__ldg(p.cu + lo), 0), end};
+}
+// The first token of the window of token `row` of a sequence that starts at `start`.
+__device__ __forceinline__ int window_start(const AttnArgs& p, int row, int start) {
+  return max(start, row - p.window + 1);
+}
+__device__ __forceinline__ bool sees(const AttnArgs& p, int i, int j, int start) {
+  return j >= start && j <= i && (i - j < p.window || j < start + p.sinks);
+}
+// A token that sees only itself has the probability one and passes nothing on
+// to q and k, exactly; the difference of two sums would leave their rounding.
+__device__ __forceinline__ bool alone(const AttnArgs& p, int row, int start) {
+  return row == start || (p.window == 1 && p.sinks == 0);
+}
+
+// Records offsets that are out of range or decrease; one block calls it.
+__device__ __forceinline__ void check_offsets(const AttnArgs& p, const DevStatus& st, int kid) {
+  if (p.cu == nullptr) return;
+  for (int b = threadIdx.x; b <= p.B; b += blockDim.x) {
+    const int c = __ldg(p.cu + b);
+    if (c < 0 || c > p.T || (b > 0 && __ldg(p.cu + b - 1) > c)) record_error(st, QKVP_ERR_DEVICE_INPUT, kid);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows on the CUDA cores, one warp each: a lane takes one token of 32 for the
+// scores, four (d / 32) columns for the sums.  Only pairs that are seen enter.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int D>
+__device__ __forceinline__ float row_dot(const uint16_t* a, const uint16_t* b) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a) + i), y = __ldg(reinterpret_cast<const uint4*>(b) + i);
+    s += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y) +
+         bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) + bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+  }
+  return s;
+}
+__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return static_cast<uint16_t>(pack_bf16x2(x, 0.f)); }
+
+template <int D>
+__device__ __forceinline__ void attend_row(const AttnArgs& p, int row, int hq) {
+  const int lane = threadIdx.x & 31, h = hq / p.G;
+  const Span sp = span_of(p, row);
+  const uint16_t* q = p.q + (static_cast<int64_t>(hq) * p.T + row) * D;
+  const uint16_t *k = p.k + static_cast<int64_t>(h) * p.T * D, *v = p.v + static_cast<int64_t>(h) * p.T * kDv;
+  float m = -INFINITY, l = 0.f, o[4] = {};
+  const auto part = [&](int j0, int j1) {
+    for (; j0 < j1; j0 += 32) {
+      const int n = min(32, j1 - j0);
+      const float x = lane < n ? p.scale_log2 * row_dot<D>(q, k + static_cast<int64_t>(j0 + lane) * D) : -INFINITY;
+      const float next = fmaxf(m, warp_max(x)), up = finite_or_zero(next);
+      const float w = ex2(x - up), f = ex2(m - up);
+      m = next;
+      l = l * f + w;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] *= f;
+      for (int t = 0; t < n; ++t) {
+        const float wt = __shfl_sync(0xffffffffu, w, t);
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(v + static_cast<int64_t>(j0 + t) * kDv) + lane);
+        o[0] += wt * bf16_lo(y.x);
+        o[1] += wt * bf16_hi(y.x);
+        o[2] += wt * bf16_lo(y.y);
+        o[3] += wt * bf16_hi(y.y);
+      }
+    }
+  };
+  if (sp.start >= 0) {
+    const int w0 = window_start(p, row, sp.start);
+    part(sp.start, min(w0, sp.start + min(p.sinks, p.T)));
+    part(w0, row + 1);
+  }
+  l = warp_add(l);
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(p.a + (static_cast<int64_t>(row) * p.Hq + hq) * kDv)[lane] =
+      l == 0.f ? make_uint2(0, 0) : make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
+  if (lane == 0)
+    p.lse[static_cast<int64_t>(hq) * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// p and ds of one pair.
+template <int D>
+__device__ __forceinline__ float2 pair_grad(const AttnArgs& p, int i, int j, int hq, int h, bool alone) {
+  const int64_t ri = static_cast<int64_t>(hq) * p.T + i, rj = static_cast<int64_t>(h) * p.T + j;
+  const float x = p.scale_log2 * row_dot<D>(p.q + ri * D, p.k + rj * D);
+  const float dp = row_dot<kDv>(p.da + (static_cast<int64_t>(i) * p.Hq + hq) * kDv, p.v + rj * kDv);
+  const float w = ex2(x - finite_or_zero(__ldg(p.lse + ri)) * 1.4426950408889634f);
+  return make_float2(w, alone ? 0.f : w * (dp - p.delta[ri]));
+}
+
+template <int D>
+__device__ __forceinline__ void dq_row(const AttnArgs& p, int row, int hq) {
+  const int lane = threadIdx.x & 31, h = hq / p.G;
+  const Span sp = span_of(p, row);
+  float o[D / 32] = {};
+  const auto part = [&](int j0, int j1) {
+    for (; j0 < j1; j0 += 32) {
+      const int n = min(32, j1 - j0);
+      const float ds = lane < n ? pair_grad<D>(p, row, j0 + lane, hq, h, alone(p, row, sp.start)).y : 0.f;
+      for (int t = 0; t < n; ++t) {
+        const float x = __shfl_sync(0xffffffffu, ds, t);
+        const uint16_t* k = p.k + (static_cast<int64_t>(h) * p.T + j0 + t) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] += x * bf16_at(k + 32 * c + lane);
+      }
+    }
+  };
+  if (sp.start >= 0 && !alone(p, row, sp.start)) {
+    const int w0 = window_start(p, row, sp.start);
+    part(sp.start, min(w0, sp.start + min(p.sinks, p.T)));
+    part(w0, row + 1);
+  }
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+    p.dq[(static_cast<int64_t>(hq) * p.T + row) * D + 32 * c + lane] = bf16_bits(o[c] * p.scale);
+}
+
+template <int D>
+__device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h) {
+  const int lane = threadIdx.x & 31;
+  const Span sp = span_of(p, row);
+  float ok[D / 32] = {}, ov[4] = {};
+  // the last token that sees this one
+  const int end = sp.start < 0                                     ? row
+                  : row - sp.start < p.sinks || sp.end - row <= p.window ? sp.end
+                                                                    : row + p.window;
+  for (int hq = h * p.G; hq < (h + 1) * p.G; ++hq)
+    for (int i0 = row; i0 < end; i0 += 32) {
+      const int n = min(32, end - i0);
+      const float2 g = lane < n ? pair_grad<D>(p, i0 + lane, row, hq, h, alone(p, i0 + lane, sp.start)) : make_float2(0.f, 0.f);
+      for (int t = 0; t < n; ++t) {
+        const float w = __shfl_sync(0xffffffffu, g.x, t), ds = __shfl_sync(0xffffffffu, g.y, t);
+        const uint16_t* q = p.q + (static_cast<int64_t>(hq) * p.T + i0 + t) * D;
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(p.da + (static_cast<int64_t>(i0 + t) * p.Hq + hq) * kDv) + lane);
+        ov[0] += w * bf16_lo(y.x);
+        ov[1] += w * bf16_hi(y.x);
+        ov[2] += w * bf16_lo(y.y);
+        ov[3] += w * bf16_hi(y.y);
+        if (!alone(p, i0 + t, sp.start))
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) ok[c] += ds * bf16_at(q + 32 * c + lane);
+      }
+    }
+  const int64_t at = static_cast<int64_t>(h) * p.T + row;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) p.dk[at * D + 32 * c + lane] = bf16_bits(ok[c] * p.scale);
+  reinterpret_cast<uint2*>(p.dv + at * kDv)[lane] = make_uint2(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]));
+}
+
+// Host: fills `a` from the caller's description, QKVP_OK or the status that an
+// entry point returns.
+int check_attention(const qkvp_attention* at, AttnArgs* a);
+constexpr size_t kAttnHeaderBytes = 1024;
+
+}  // namespace qkvp

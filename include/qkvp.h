@@ -485,6 +485,15 @@ int qkvp_cache_append(const qkvp_cache* cache, int T, const uint16_t* k, const u
 int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const uint16_t* q, uint16_t* a, float* lse,
                           int accumulate, void* ws, size_t ws_bytes, void* stream);
 
+/* The same attention under a sliding window: of a sequence of n live slots it
+ * sees those below `sinks` and the last `window`, n - window .. n - 1 (window >=
+ * 1, sinks >= 0; other slots are not read, whatever they hold).  Slots count, not
+ * positions: the cache is one whose slots are still in the order of its tokens,
+ * so one that qkvp_cache_evict has not changed.  With `accumulate` the weights
+ * of the slots that are seen grow.  Workspace: as qkvp_decode_attention. */
+int qkvp_decode_window_attention(const qkvp_cache* cache, int Hq, int window, int sinks, float scale, const uint16_t* q,
+                                 uint16_t* a, float* lse, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
 /* Eviction.  In every sequence longer than `budget`, each head on its own
  * keeps `budget` slots: first those whose position is within the last
  * `recent` (pos > newest pos - recent), then by accumulated weight from the
@@ -502,6 +511,100 @@ int qkvp_decode_attention(const qkvp_cache* cache, int Hq, float scale, const ui
  *   lengths_out  out [B] min(length, budget); cache->lengths or NULL: in place */
 int qkvp_cache_evict(const qkvp_cache* cache, int budget, int recent, int32_t* slots, int32_t* lengths_out, void* ws,
                      size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Split, norm and rotation of a packed projection's rows.  What the epilogue
+ * of qkvp_forward does to its FP8 product, for rows y that come from elsewhere
+ * (a bf16 product, more query heads than key heads, learned gains, positions
+ * with several axes): y [T, N], N = Hq * d_qk + H * d_qk + H * 128, holds the q
+ * heads, the k heads and the v heads of a token side by side.
+ *   r = 1 / sqrt(mean(x^2) + eps) of each q and k head x, out = R(x r gain)
+ * R turns the pairs (i, i + d_qk / 2) by the angles of qkvp_build_rope_table.
+ * With several axes (time, height, width of images and video) the first
+ * sections[0] pairs are turned by the positions of the first axis, the next
+ * sections[1] by those of the second, and so on.
+ * ------------------------------------------------------------------------ */
+typedef struct qkvp_norm_rope {
+    int T;            /* tokens, 0 .. 2^24                                         */
+    int Hq, H;        /* query heads (a multiple of H, up to 1024), K/V heads 1 .. 128 */
+    int d_qk, d_v;    /* 64, 96 or 128; 128                                        */
+    int axes;         /* of the positions: 1, 2 or 3                               */
+    int sections[3];  /* pairs of each axis: even, d_qk / 2 in all (axes = 1: not read) */
+    int max_pos;      /* of the table                                              */
+    float eps;        /* inside the square root                                    */
+    int64_t ldy;      /* elements from a row of y to the next: >= N, a multiple of 8 */
+    const float* rope_table;   /* qkvp_build_rope_table(max_pos, d_qk)             */
+    const int32_t* pos;        /* [axes, T]                                        */
+    const float* q_gain;       /* [d_qk], both or neither (NULL: 1)                */
+    const float* k_gain;
+} qkvp_norm_rope;
+
+/* Workspace of the two calls (0: unsupported).  It starts with the status word
+ * (zero it once with qkvp_workspace_init): a position outside [0, max_pos) counts
+ * as the nearer end and is recorded as QKVP_ERR_DEVICE_INPUT.  Calls sharing one
+ * must not overlap on the GPU. */
+size_t qkvp_norm_rope_workspace_bytes(const qkvp_norm_rope* n);
+
+/*   y         in  [T, N] bf16, rows ldy elements apart
+ *   q, k      out [Hq, T, d_qk], [H, T, d_qk] bf16       v  out [H, T, 128] bf16
+ *   rstd      out [Hq + H, T] float32: r of the q heads, then of the k heads */
+int qkvp_norm_rope_forward(const qkvp_norm_rope* n, const uint16_t* y, uint16_t* q, uint16_t* k, uint16_t* v, float* rstd,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient, with g = R^T(dq):  dgain = sum over tokens and heads of g x r,
+ *   dx = r (g gain - x r mean(g gain x r)),  dv as it is
+ *   dq, dk, dv  in  as q, k, v             y, rstd  in  the forward's
+ *   dy          out [T, N] bf16, contiguous
+ *   dq_gain, dk_gain  out [d_qk] float32 (with gains; sums in a fixed order)  */
+int qkvp_norm_rope_backward(const qkvp_norm_rope* n, const uint16_t* dq, const uint16_t* dk, const uint16_t* dv,
+                            const uint16_t* y, const float* rstd, uint16_t* dy, float* dq_gain, float* dk_gain, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Causal attention over packed sequences, between the packed projection and
+ * the output projection, forward and backward.  Token i of a sequence sees its
+ * tokens j <= i with i - j < window (all of them with window = 0) and, whatever
+ * the window, the sequence's first `sinks` tokens:
+ *   s_ij = scale q_i . k_j,  a_i = sum_j e^(s_ij - lse_i) v_j,  lse_i = ln sum_j e^s_ij
+ * Query head h * (Hq / H) + g reads K/V head h.  Rows before cu[0] or from
+ * cu[B] on belong to no sequence: a = 0, lse = -inf, zero gradients.  What a
+ * token does not see has no part in its results, NaN and infinities included;
+ * what it sees of them makes its results NaN or infinite.
+ * ------------------------------------------------------------------------ */
+typedef struct qkvp_attention {
+    int T;            /* tokens of all sequences, 0 .. 2^24                        */
+    int Hq, H;        /* query heads (a multiple of H, up to 1024), K/V heads 1 .. 128 */
+    int d_qk, d_v;    /* 64, 96 or 128; 128                                        */
+    int B;            /* sequences, 1 .. 2^20                                      */
+    int window;       /* tokens, itself included; 0: no window                     */
+    int sinks;        /* first tokens of a sequence that stay visible, >= 0        */
+    float scale;      /* of the scores, positive                                   */
+    const int32_t* cu;   /* [B + 1] row offsets of the sequences, non-decreasing, on
+                          * the device; NULL: one sequence (B = 1) of T tokens.  Offsets
+                          * outside [0, T] count as the nearer end; those and
+                          * decreasing ones (whose rows' results are not defined) are
+                          * recorded as QKVP_ERR_DEVICE_INPUT                       */
+} qkvp_attention;
+
+/* Workspace of the two calls (0: unsupported); zero it once with
+ * qkvp_workspace_init.  Calls sharing one must not overlap on the GPU. */
+size_t qkvp_attention_workspace_bytes(const qkvp_attention* at);
+
+/*   q, k, v   in  [Hq, T, d_qk], [H, T, d_qk], [H, T, 128] bf16 (as qkvp_forward
+ *                 and qkvp_norm_rope_forward write them)
+ *   a         out [T, Hq * 128] bf16, the operand of qkvp_oproj_forward
+ *   lse       out [Hq, T] float32                                            */
+int qkvp_attention_forward(const qkvp_attention* at, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* a,
+                           float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient, with p_ij = e^(s_ij - lse_i) and ds_ij = p_ij (da_i . v_j - da_i . a_i):
+ *   dv_j = sum_i p_ij da_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+ * (dk and dv sum over the query heads of their head).  The same on every run.
+ *   da        in  [T, Hq * 128] bf16       q, k, v, a, lse  in  the forward's
+ *   dq, dk, dv  out as q, k, v: the operands of qkvp_backward                */
+int qkvp_attention_backward(const qkvp_attention* at, const uint16_t* da, const uint16_t* q, const uint16_t* k,
+                            const uint16_t* v, const uint16_t* a, const float* lse, uint16_t* dq, uint16_t* dk, uint16_t* dv,
+                            void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
