@@ -52,8 +52,10 @@ bool map2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inn
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 // 3-D map over a [d2][d1][d0] row-major tensor.
-bool map3d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
+bool qkvp::map3d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
            uint32_t b0, uint32_t b1, uint32_t b2, CUtensorMapSwizzle sw) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
@@ -64,6 +66,14 @@ bool map3d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* ptr, u
   return fn(m, dt, 3, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+bool qkvp::map2d_bf16(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
+  return map2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, inner, outer, inner * 2, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+DevStatus qkvp::dev_status(void* ws) { return DevStatus{static_cast<int*>(ws), g_timeout_ns}; }
+
+namespace {
 
 int sm_count() {
   static std::atomic<int> cache[64];   // per device, written once (any thread may race to write the same value)
@@ -144,8 +154,6 @@ int choose_splits(int tiles, int kblocks, int sms) {
   }
   return best;
 }
-
-DevStatus dev_status(void* ws) { return DevStatus{static_cast<int*>(ws), g_timeout_ns}; }
 
 // Optional kernel-boundary events (qkvp_set_timing_events).
 struct TimingHook {

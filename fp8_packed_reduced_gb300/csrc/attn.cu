@@ -9,14 +9,6 @@ namespace {
 
 constexpr int kWarps = 8;
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) forward_kernel(const __grid_constant__ AttnArgs p, DevStatus st) {
-  wait_for_previous();
-  const int row = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p, st, KID_ATTN_FWD);
-  if (row < p.T) attend_row<D>(p, row, blockIdx.y);
-}
-
 // delta = da . a of every row and head.
 __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const __grid_constant__ AttnArgs p, DevStatus st) {
   wait_for_previous();
@@ -46,11 +38,6 @@ __global__ void __launch_bounds__(32 * kWarps) dkv_kernel(const __grid_constant_
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t delta_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Hq) * a.T * sizeof(float) + 255) / 256 * 256; }
-
-template <int D>
-cudaError_t forward(const AttnArgs& a, DevStatus st, cudaStream_t s) {
-  return launch_dependent(forward_kernel<D>, dim3((a.T + kWarps - 1) / kWarps, a.Hq), 32 * kWarps, 0, s, a, st);
-}
 
 template <int D>
 cudaError_t backward(const AttnArgs& a, DevStatus st, cudaStream_t s) {
@@ -118,11 +105,9 @@ int qkvp_attention_forward(const qkvp_attention* at, const uint16_t* q, const ui
   p.v = v;
   p.a = a;
   p.lse = lse;
-  const DevStatus st{static_cast<int*>(ws), 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   mark(s);
-  const cudaError_t e = p.d == 64 ? forward<64>(p, st, s) : p.d == 96 ? forward<96>(p, st, s) : forward<128>(p, st, s);
-  if (e != cudaSuccess) return QKVP_ERR_CUDA;
+  if (launch_attention_forward(p, dev_status(ws), s) != cudaSuccess) return QKVP_ERR_CUDA;
   mark(s);
   return QKVP_OK;
 }

@@ -8,6 +8,8 @@
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
 #pragma once
 
+#include <climits>
+
 #include "cache.cuh"
 #include "kernels.cuh"
 
@@ -208,9 +210,28 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h) {
   reinterpret_cast<uint2*>(p.dv + at * kDv)[lane] = make_uint2(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]));
 }
 
+// mbar_wait without a call (a kernel that moves registers between its warps
+// has no room for one's saved registers).
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort, const DevStatus& st, int kid) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (abort != nullptr && *abort) return false;
+    if (globaltimer_ns() - t0 > st.timeout_ns) {
+      record_error(st, QKVP_ERR_TIMEOUT, kid);
+      if (abort != nullptr) *abort = 1;
+      return false;
+    }
+  }
+}
+
 // Host: fills `a` from the caller's description, QKVP_OK or the status that an
 // entry point returns.
 int check_attention(const qkvp_attention* at, AttnArgs* a);
+cudaError_t launch_attention_forward(const AttnArgs& a, DevStatus st, cudaStream_t s);
 constexpr size_t kAttnHeaderBytes = 1024;
 
 }  // namespace qkvp

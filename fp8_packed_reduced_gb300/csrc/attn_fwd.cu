@@ -1,0 +1,356 @@
+// Causal attention over packed sequences, forward, on the 5th-generation tensor
+// cores (attn.cuh has the formulas).
+#include <atomic>
+
+#include "attn.cuh"
+
+namespace qkvp {
+namespace {
+
+constexpr int kTile = 128;                   // query rows of an accumulator, keys of a step
+constexpr int kRows = 2 * kTile;             // query rows of a block
+constexpr int kThreads = 384;                // two softmax warpgroups; a loading and an issuing warp, and two that only give
+                                             // their registers: 384 x 168 = 2 x 128 x 224 + 128 x 56
+constexpr int kStages = 2;
+constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
+constexpr int kQBytes = 2 * kBox;            // of one query tile; the output's staging afterwards
+constexpr int kVBytes = 2 * kBox;
+__host__ __device__ constexpr int boxes(int d) { return (d + 63) / 64; }
+__host__ __device__ constexpr int smem_bytes(int d) { return 1024 + 2 * kQBytes + kStages * (boxes(d) * kBox + kVBytes); }
+constexpr float kSlack = 8.f;                // powers of two by which scores may pass the maximum that they are relative to
+
+// Key tiles (of 128, on the grid of the packed rows) that a query tile needs:
+// those that hold its sequence's first tokens, and those from its window on.
+struct Range {
+  int sink0, sink1, first, last;   // [sink0, sink1) and [first, last)
+  __device__ bool has(int kt) const { return (kt >= sink0 && kt < sink1) || (kt >= first && kt < last); }
+};
+
+struct Shared {
+  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], done;
+  uint32_t tmem;
+  int abort;
+  int lo[2][4], hi[2][4], start[2][4];
+  Range range[2];
+};
+
+// The next key tile at or after kt that either query tile needs, or INT_MAX.
+__device__ __forceinline__ int next_tile(const Range& a, const Range& b, int kt) {
+  if (a.has(kt) || b.has(kt)) return kt;
+  int n = INT_MAX;
+  const int at[4] = {a.sink0 < a.sink1 ? a.sink0 : INT_MAX, a.first < a.last ? a.first : INT_MAX,
+                     b.sink0 < b.sink1 ? b.sink0 : INT_MAX, b.first < b.last ? b.first : INT_MAX};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (at[i] >= kt) n = min(n, at[i]);
+  return n;
+}
+
+// Bits lo .. hi - 1 of the 32 from `base` on.
+__device__ __forceinline__ uint32_t bits(int lo, int hi, int base) {
+  const int a = min(max(lo - base, 0), 32), b = min(max(hi - base, 0), 32);
+  if (a >= b) return 0u;
+  return (b == 32 ? ~0u : (1u << b) - 1u) & ~((1u << a) - 1u);   // a < 32 here
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_a,
+                   const __grid_constant__ AttnArgs p, DevStatus st) {
+  constexpr int KB = boxes(D), kKBytes = KB * kBox;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared g;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sq = smem, *sk = sq + 2 * kQBytes, *sv = sk + kStages * kKBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hq = blockIdx.y, h = hq / p.G;
+  const int r0 = (gridDim.x - 1 - blockIdx.x) * kRows;   // the later rows see more: they come first
+
+  if (threadIdx.x == 0) {
+    g.abort = 0;
+    mbar_init(&g.q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&g.k_full[s], 1);
+      mbar_init(&g.k_empty[s], 1);
+      mbar_init(&g.v_full[s], 1);
+      mbar_init(&g.v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&g.s_full[t], 1);
+      mbar_init(&g.p_full[t], 4);
+      mbar_init(&g.o_full[t], 1);
+    }
+    mbar_init(&g.done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&g.tmem, 512);
+    tmem_relinquish();
+  }
+  wait_for_previous();
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p, st, KID_ATTN_FWD);
+  // the rows' sequences, and from them the key tiles
+  const int t = warp >> 2;              // query tile of a softmax warp
+  const int row = r0 + threadIdx.x;     // of a softmax thread
+  Span sp{-1, -1};
+  int seen0 = 0;                        // first token of the row's window
+  if (warp < 8) {
+    if (row < p.T) sp = span_of(p, row);
+    seen0 = sp.start < 0 ? INT_MAX : window_start(p, row, sp.start);
+    const int lo = __reduce_min_sync(0xffffffffu, seen0), hi = __reduce_max_sync(0xffffffffu, sp.start < 0 ? -1 : row);
+    const int s0 = __reduce_min_sync(0xffffffffu, sp.start < 0 ? INT_MAX : sp.start);
+    if (lane == 0) g.lo[t][warp & 3] = lo, g.hi[t][warp & 3] = hi, g.start[t][warp & 3] = s0;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    int lo = INT_MAX, hi = -1, s0 = INT_MAX;
+    for (int i = 0; i < 4; ++i)
+      lo = min(lo, g.lo[threadIdx.x][i]), hi = max(hi, g.hi[threadIdx.x][i]), s0 = min(s0, g.start[threadIdx.x][i]);
+    Range r{0, 0, 0, 0};
+    if (hi >= 0) {
+      r.first = lo / kTile;
+      r.last = hi / kTile + 1;
+      r.sink0 = s0 / kTile;
+      r.sink1 = p.sinks ? min(r.first, (min(s0 + min(p.sinks, p.T), p.T) + kTile - 1) / kTile) : r.sink0;
+    }
+    g.range[threadIdx.x] = r;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Range &ra = g.range[0], &rb = g.range[1];
+  const uint32_t tmem = g.tmem;
+  const int kt0 = next_tile(ra, rb, 0);
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8) {
+      if (lane == 0 && kt0 != INT_MAX) {
+        const bool used[2] = {ra.first < ra.last, rb.first < rb.last};
+        mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * KB * kBox);
+        for (int i = 0; i < 2; ++i)
+          if (used[i])
+            for (int b = 0; b < KB; ++b) tma_load_3d(sq + i * kQBytes + b * kBox, &tm_q, &g.q_full, b * 64, r0 + i * kTile, hq);
+        int n = 0;
+        for (int kt = kt0; kt != INT_MAX; kt = next_tile(ra, rb, kt + 1), ++n) {
+          const int s = n % kStages, par = (n / kStages) & 1;
+          if (!wait_inline(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) break;
+          mbar_arrive_expect_tx(&g.k_full[s], kKBytes);
+          for (int b = 0; b < KB; ++b) tma_load_3d(sk + s * kKBytes + b * kBox, &tm_k, &g.k_full[s], b * 64, kt * kTile, h);
+          if (!wait_inline(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) {
+            wait_inline(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
+            break;
+          }
+          mbar_arrive_expect_tx(&g.v_full[s], kVBytes);
+          for (int b = 0; b < 2; ++b) tma_load_3d(sv + s * kVBytes + b * kBox, &tm_v, &g.v_full[s], b * 64, kt * kTile, h);
+        }
+        // every copy has landed before the block may leave
+        wait_inline(&g.q_full, 0, nullptr, st, KID_ATTN_FWD);
+        for (int i = max(0, n - kStages); i < n; ++i) {
+          wait_inline(&g.k_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
+          wait_inline(&g.v_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
+        }
+      }
+    } else if (warp == 9) {
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_o = idesc_bf16_f32(kTile, kDv, true);
+        const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
+        const auto scores = [&](int i, int s) {
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+            umma_bf16_ss(tmem + i * kTile, sdesc_k_sw128(q0 + i * kQBytes + at), sdesc_k_sw128(k0 + s * kKBytes + at), id_s, kk > 0);
+          }
+          umma_commit(&g.s_full[i]);
+        };
+        int pn[2] = {0, 0};   // products with v so far
+        bool ok = kt0 != INT_MAX && wait_inline(&g.q_full, 0, &g.abort, st, KID_ATTN_FWD) &&
+                  wait_inline(&g.k_full[0], 0, &g.abort, st, KID_ATTN_FWD);
+        if (ok) {
+          tc_fence_after();
+          if (ra.has(kt0)) scores(0, 0);
+          if (rb.has(kt0)) scores(1, 0);
+          umma_commit(&g.k_empty[0]);
+        }
+        int n = 0;
+        for (int kt = kt0; ok && kt != INT_MAX; ++n) {
+          const int s = n % kStages, next = next_tile(ra, rb, kt + 1), s1 = (n + 1) % kStages;
+          ok = wait_inline(&g.v_full[s], (n / kStages) & 1, &g.abort, st, KID_ATTN_FWD) &&
+               (next == INT_MAX || wait_inline(&g.k_full[s1], ((n + 1) / kStages) & 1, &g.abort, st, KID_ATTN_FWD));
+  #pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const Range& r = i == 0 ? ra : rb;
+            if (ok && r.has(kt)) {
+              ok = wait_inline(&g.p_full[i], pn[i] & 1, &g.abort, st, KID_ATTN_FWD);
+              if (!ok) break;
+              tc_fence_after();
+  #pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                umma_bf16_ts(tmem + kRows + i * kDv, tmem + i * kTile + kk * 8, sdesc_sw128(v0 + s * kVBytes + kk * 2048, kBox, 1024), id_o,
+                             pn[i] > 0 || kk > 0);
+              ++pn[i];
+            }
+            if (ok && next != INT_MAX && r.has(next)) scores(i, s1);
+          }
+          if (!ok) break;
+          umma_commit(&g.v_empty[s]);
+          if (next != INT_MAX) umma_commit(&g.k_empty[s1]);
+          kt = next;
+        }
+        umma_commit(&g.o_full[0]);
+        umma_commit(&g.o_full[1]);
+        umma_commit(&g.done);
+        wait_inline(&g.done, 0, nullptr, st, KID_ATTN_FWD);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const Range r = t == 0 ? ra : rb;
+    const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + t * kTile + quarter, to = tmem + kRows + t * kDv + quarter;
+    float m = -INFINITY, l = 0.f;   // m: what the scores are relative to (raw)
+    int n = 0;
+    bool ok = true;
+    const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
+    for (int kt = r.sink0 < r.sink1 ? r.sink0 : r.first; kt < r.last; kt = kt + 1 == r.sink1 ? r.first : kt + 1, ++n) {
+      if (!wait_inline(&g.s_full[t], n & 1, &g.abort, st, KID_ATTN_FWD)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[kTile];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
+      tmem_ld_wait();
+      const int j0 = kt * kTile;
+      if (!__all_sync(0xffffffffu, sp.start >= 0 && j0 >= seen0 && j0 + kTile <= row + 1)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t see = 0;
+          if (sp.start >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(sp.start, min(sink_end, row + 1), j0 + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[32 * c + i] = see >> i & 1 ? x[32 * c + i] : 0xFF800000u;
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kTile; i += 2) top = fmax3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      // A maximum that grows by little stays: its probabilities are at most 2^8.
+      const bool grows = top > m && (top - m) * p.scale_log2 > kSlack;
+      if (__any_sync(0xffffffffu, grows)) {
+        const float f = !grows ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
+        if (n > 0) {   // (the products before this step's scores are done)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(to + 32 * c, o);
+          }
+        }
+        if (grows) {
+          l *= f;
+          m = top;
+        }
+      }
+      const float m2 = finite_or_zero(m) * p.scale_log2;
+      const f2 sc = f2_make(p.scale_log2, p.scale_log2), mm = f2_make(-m2, -m2);
+      f2 sum = f2_make(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1])), sc, mm));
+          const float a = ex2(z.x), b = ex2(z.y);
+          sum = f2_add(sum, f2_make(a, b));
+          w[i] = pack_bf16x2(a, b);
+        }
+        tmem_st16(ts + 16 * c, w);
+      }
+      const float2 part = f2_split(sum);
+      l += part.x + part.y;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&g.p_full[t]);
+    }
+    if (ok) ok = wait_inline(&g.o_full[t], 0, &g.abort, st, KID_ATTN_FWD);
+    if (ok) {
+      tc_fence_after();
+      const bool none = l == 0.f;
+      const float f = none ? 0.f : 1.f / l;
+      bool bad = !(l < INFINITY);
+      uint8_t* stage = sq + t * kQBytes + (warp & 3) * 8192;   // two boxes of 32 rows x 64 columns
+      uint32_t o[32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld32(to + 32 * c, o);
+        tmem_ld_wait();
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float(o[i + 2 * k]) * f, b = __uint_as_float(o[i + 2 * k + 1]) * f;
+            big += fabsf(a) + fabsf(b);
+            w[k] = none ? 0u : pack_bf16x2(a, b);
+          }
+          const int chunk = (c & 1) * 4 + i / 8;
+          *reinterpret_cast<uint4*>(stage + (c >> 1) * 4096 + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        bad |= !(big < INFINITY);
+      }
+      if (row < p.T) p.lse[static_cast<int64_t>(hq) * p.T + row] = none ? -INFINITY : (finite_or_zero(m) * p.scale_log2 + log2f(l)) * 0.6931471805599453f;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0 && row < p.T) {
+        for (int b = 0; b < 2; ++b) tma_store_2d(&tm_a, stage + b * 4096, hq * kDv + b * 64, row);
+        bulk_commit();
+        bulk_wait_all<0>();
+      }
+      __syncwarp();
+      // A value that is not finite may come from what the row does not see
+      // (0 * NaN): such rows are computed again from what they see.
+      uint32_t again = __ballot_sync(0xffffffffu, bad && !none && row < p.T);
+      for (; again; again &= again - 1) attend_row<D>(p, r0 + t * kTile + (warp & 3) * 32 + __ffs(again) - 1, hq);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, DevStatus st, cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(forward_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(D));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  }
+  constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap q, k, v, o;
+  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, 64, kTile, 1, sw) || !map3d(&k, bf16, 2, a.k, D, a.T, a.H, 64, kTile, 1, sw) ||
+      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, 64, kTile, 1, sw) || !map2d_bf16(&o, a.a, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, 32))
+    return cudaErrorInvalidValue;
+  return launch_dependent(forward_kernel<D>, dim3((a.T + kRows - 1) / kRows, a.Hq), kThreads, smem_bytes(D), s, q, k, v, o, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_forward(const AttnArgs& a, DevStatus st, cudaStream_t s) {
+  return a.d == 64 ? launch<64>(a, st, s) : a.d == 96 ? launch<96>(a, st, s) : launch<128>(a, st, s);
+}
+
+}  // namespace qkvp

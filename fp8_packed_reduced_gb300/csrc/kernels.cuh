@@ -13,6 +13,13 @@ constexpr int kMaxLayers = 128;
 int check_dims(const qkvp_dims* d);
 // mark: records the next armed timing event (qkvp_set_timing_events) on `s`.
 void mark(cudaStream_t s);
+// dev_status: the status word at the start of a workspace, with the limit of device-side waits.
+DevStatus dev_status(void* ws);
+// Tensor maps: of a [d2][d1][d0] row-major tensor, and with 128-byte swizzling
+// of a contiguous bf16 one [outer][inner].  False if the driver refuses.
+bool map3d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2,
+           uint32_t b0, uint32_t b1, uint32_t b2, CUtensorMapSwizzle sw);
+bool map2d_bf16(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer);
 
 // ---------------------------------------------------------------------------
 // Bank refresh
