@@ -27,9 +27,12 @@ struct AttnArgs {
   uint16_t* a;               // [T, Hq * 128] bf16
   float* lse;                // [Hq, T], natural logarithm
   const uint16_t* da;        // [T, Hq * 128]
-  float* delta;              // [Hq, T] da . a
+  int Tp;                    // T rounded up to whole tiles
+  float2* stat;              // [Hq, Tp] lse in base 2 (+inf: no weight), da . a
   uint16_t *dq, *dk, *dv;
 };
+
+constexpr int kAttnTile = 128;   // query rows and keys of the products
 
 // A token's sequence, [start, end); start < 0: none.
 struct Span {
@@ -61,6 +64,38 @@ __device__ __forceinline__ bool sees(const AttnArgs& p, int i, int j, int start)
 // to q and k, exactly; the difference of two sums would leave their rounding.
 __device__ __forceinline__ bool alone(const AttnArgs& p, int row, int start) {
   return row == start || (p.window == 1 && p.sinks == 0);
+}
+
+// Key tiles (of kAttnTile, on the grid of the packed rows) that a query tile needs:
+// those that hold its sequence's first tokens, and those from its window on.
+struct Range {
+  int sink0, sink1, first, last;   // [sink0, sink1) and [first, last)
+  __device__ bool has(int kt) const { return (kt >= sink0 && kt < sink1) || (kt >= first && kt < last); }
+};
+
+// That of 128 query rows from what their four warps found: the first token of a
+// window, the last row, the first token of a sequence (INT_MAX, -1, INT_MAX: none).
+__device__ __forceinline__ Range range_of(const AttnArgs& p, const int (&lo)[4], const int (&hi)[4], const int (&start)[4]) {
+  const int last = max(max(hi[0], hi[1]), max(hi[2], hi[3]));
+  if (last < 0) return Range{0, 0, 0, 0};
+  const int first = min(min(lo[0], lo[1]), min(lo[2], lo[3])), s0 = min(min(start[0], start[1]), min(start[2], start[3]));
+  Range r;
+  r.first = first / kAttnTile;
+  r.last = last / kAttnTile + 1;
+  r.sink0 = s0 / kAttnTile;
+  r.sink1 = p.sinks ? min(r.first, (min(s0 + min(p.sinks, p.T), p.T) + kAttnTile - 1) / kAttnTile) : r.sink0;
+  return r;
+}
+// Bits lo .. hi - 1 of the 32 from `base` on.
+__device__ __forceinline__ uint32_t bits(int lo, int hi, int base) {
+  const int a = min(max(lo - base, 0), 32), b = min(max(hi - base, 0), 32);
+  if (a >= b) return 0u;
+  return (b == 32 ? ~0u : (1u << b) - 1u) & ~((1u << a) - 1u);   // a < 32 here
+}
+
+// The queries that see token `row` of sequence sp end here.
+__device__ __forceinline__ int last_seer(const AttnArgs& p, int row, Span sp) {
+  return row - sp.start < p.sinks || sp.end - row <= p.window ? sp.end : row + p.window;
 }
 
 // Records offsets that are out of range or decrease; one block calls it.
@@ -147,8 +182,9 @@ __device__ __forceinline__ float2 pair_grad(const AttnArgs& p, int i, int j, int
   const int64_t ri = static_cast<int64_t>(hq) * p.T + i, rj = static_cast<int64_t>(h) * p.T + j;
   const float x = p.scale_log2 * row_dot<D>(p.q + ri * D, p.k + rj * D);
   const float dp = row_dot<kDv>(p.da + (static_cast<int64_t>(i) * p.Hq + hq) * kDv, p.v + rj * kDv);
-  const float w = ex2(x - finite_or_zero(__ldg(p.lse + ri)) * 1.4426950408889634f);
-  return make_float2(w, alone ? 0.f : w * (dp - p.delta[ri]));
+  const float2 s = __ldcg(p.stat + static_cast<int64_t>(hq) * p.Tp + i);
+  const float w = ex2(x - s.x);
+  return make_float2(w, alone ? 0.f : w * (dp - s.y));
 }
 
 template <int D>
@@ -183,10 +219,7 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h) {
   const int lane = threadIdx.x & 31;
   const Span sp = span_of(p, row);
   float ok[D / 32] = {}, ov[4] = {};
-  // the last token that sees this one
-  const int end = sp.start < 0                                     ? row
-                  : row - sp.start < p.sinks || sp.end - row <= p.window ? sp.end
-                                                                    : row + p.window;
+  const int end = sp.start < 0 ? row : last_seer(p, row, sp);
   for (int hq = h * p.G; hq < (h + 1) * p.G; ++hq)
     for (int i0 = row; i0 < end; i0 += 32) {
       const int n = min(32, end - i0);
@@ -232,6 +265,7 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, vola
 // entry point returns.
 int check_attention(const qkvp_attention* at, AttnArgs* a);
 cudaError_t launch_attention_forward(const AttnArgs& a, DevStatus st, cudaStream_t s);
+cudaError_t launch_attention_backward(const AttnArgs& a, DevStatus st, cudaStream_t s);
 constexpr size_t kAttnHeaderBytes = 1024;
 
 }  // namespace qkvp

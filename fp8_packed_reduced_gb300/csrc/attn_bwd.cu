@@ -1,0 +1,602 @@
+// Gradient of the causal attention over packed sequences on the 5th-generation
+// tensor cores (attn.cuh has the formulas), in two passes that both form the
+// scores and da . v again: one over the keys of 128 queries for dq, one over the
+// queries of 128 keys for dk and dv.  A single pass would have to add dq up in
+// memory, in an order that changes from run to run.
+#include <atomic>
+
+#include "attn.cuh"
+
+namespace qkvp {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kThreads = 320;                // eight computing warps, a loading and an issuing one
+constexpr int kStages = 2;
+constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
+constexpr int kFull = 2 * kBox;              // of 128 rows x up to 128 columns
+__host__ __device__ constexpr int boxes(int d) { return (d + 63) / 64; }
+__host__ __device__ constexpr int dq_smem(int) { return 1024 + 2 * kStages * kFull; }
+__host__ __device__ constexpr int dkv_smem(int) { return 1024 + 2 * kFull + 2 * kStages * kFull; }
+// Columns of TMEM
+constexpr int kScores = 0, kDp = 128, kAcc0 = 256, kAcc1 = 384, kOpQ = 384, kOpDa = 448;
+
+struct Shared {
+  uint64_t fixed_full, a_full[kStages], a_empty[kStages], b_full[kStages], b_empty[kStages];
+  uint64_t s_full, dp_full, s_free, p_full, ds_full, acc_full, done;
+  uint32_t tmem;
+  int abort;
+  int lo[4], hi[4], start[4];
+  uint32_t again[4];            // rows to be computed again
+  Range range;
+  alignas(128) float2 row[kStages][kTile];   // lse (base 2) and delta of a tile of queries, in pairs
+};
+
+__device__ __forceinline__ void init_barriers(Shared& g) {
+  g.abort = 0;
+  mbar_init(&g.fixed_full, 1);
+  for (int s = 0; s < kStages; ++s) {
+    mbar_init(&g.a_full[s], 1);
+    mbar_init(&g.a_empty[s], 1);
+    mbar_init(&g.b_full[s], 1);
+    mbar_init(&g.b_empty[s], 1);
+  }
+  mbar_init(&g.s_full, 1);
+  mbar_init(&g.dp_full, 1);
+  mbar_init(&g.s_free, 8);
+  mbar_init(&g.p_full, 8);
+  mbar_init(&g.ds_full, 8);
+  mbar_init(&g.acc_full, 1);
+  mbar_init(&g.done, 1);
+  fence_mbar_init();
+}
+// 8 warps of a group have done something to TMEM: arrive once per warp.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// delta = da . a of every row and head, and beside it the row's lse in base 2
+// (+inf where the row has no weight at all, so that its probabilities are 0).
+constexpr int kPrepWarps = 8;
+__global__ void __launch_bounds__(32 * kPrepWarps) delta_kernel(const __grid_constant__ AttnArgs p, DevStatus st) {
+  wait_for_previous();
+  if (blockIdx.x == 0) check_offsets(p, st, KID_ATTN_DELTA);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kPrepWarps + (threadIdx.x >> 5);   // row * Hq + head
+  if (r >= static_cast<int64_t>(p.Tp) * p.Hq) return;
+  const int lane = threadIdx.x & 31, row = static_cast<int>(r / p.Hq), hq = static_cast<int>(r % p.Hq);
+  float s = 0.f, z = -INFINITY;
+  if (row < p.T) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p.da + r * kDv) + lane), y = __ldg(reinterpret_cast<const uint2*>(p.a + r * kDv) + lane);
+    s = warp_add(bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y));
+    z = __ldg(p.lse + static_cast<int64_t>(hq) * p.T + row);
+  }
+  if (lane == 0) p.stat[static_cast<int64_t>(hq) * p.Tp + row] = make_float2(z == -INFINITY ? INFINITY : z * 1.4426950408889634f, s);
+}
+
+// ---------------------------------------------------------------------------
+// dq: 128 queries of a head.  q and da are operands in TMEM for the whole of
+// it, dq adds up there; per tile of 128 keys
+//   S = q k^T, dP = da v^T, ds = e^(S - lse) (dP - delta), dq += ds k
+// The products are issued dP(j), S(j + 1), dq(j): S(j + 1) covers the forming of ds(j).
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+              const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ AttnArgs p, DevStatus st) {
+  constexpr int KB = boxes(D), kKBytes = KB * kBox;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared g;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sk = smem, *sv = sk + kStages * kFull;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hq = blockIdx.y, h = hq / p.G;
+  const int r0 = (gridDim.x - 1 - blockIdx.x) * kTile;
+
+  if (threadIdx.x == 0) init_barriers(g);
+  if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
+  if (warp == 9) {
+    tmem_alloc(&g.tmem, 512);
+    tmem_relinquish();
+  }
+  wait_for_previous();
+  const int half = warp >> 2, row = r0 + (threadIdx.x & 127);
+  Span sp{-1, -1};
+  int seen0 = 0;
+  if (warp < 8) {
+    if (row < p.T) sp = span_of(p, row);
+    if (sp.start >= 0 && alone(p, row, sp.start)) sp.start = -1;   // it passes nothing on
+    seen0 = sp.start < 0 ? INT_MAX : window_start(p, row, sp.start);
+    const int lo = __reduce_min_sync(0xffffffffu, seen0), hi = __reduce_max_sync(0xffffffffu, sp.start < 0 ? -1 : row);
+    const int s0 = __reduce_min_sync(0xffffffffu, sp.start < 0 ? INT_MAX : sp.start);
+    if (lane == 0 && half == 0) g.lo[warp] = lo, g.hi[warp] = hi, g.start[warp] = s0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0) g.range = range_of(p, g.lo, g.hi, g.start);
+  const uint32_t tmem = g.tmem, quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  if (warp < 8) {   // one half of the warps loads q, the other da
+    const uint4* from = reinterpret_cast<const uint4*>(half == 0 ? p.q + (static_cast<int64_t>(hq) * p.T + row) * D
+                                                                 : p.da + (static_cast<int64_t>(row) * p.Hq + hq) * kDv);
+    const uint32_t to = tmem + (half == 0 ? kOpQ : kOpDa) + quarter;
+    const int parts = half == 0 ? D / 32 : kDv / 32;
+    for (int c = 0; c < parts; ++c) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = row < p.T ? __ldg(from + 4 * c + i) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+      tmem_st16(to + 16 * c, w);
+    }
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Range r = g.range;
+  const int kt0 = r.sink0 < r.sink1 ? r.sink0 : r.first;
+  const auto next_of = [&](int kt) { return kt + 1 == r.sink1 ? r.first : kt + 1; };
+
+  if (warp == 8) {
+    if (lane == 0) {
+      int n = 0;
+      for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
+        const int s = n % kStages, par = (n / kStages) & 1;
+        if (!mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) break;
+        mbar_arrive_expect_tx(&g.a_full[s], kKBytes);
+        for (int b = 0; b < KB; ++b) tma_load_3d(sk + s * kFull + b * kBox, &tm_k, &g.a_full[s], b * 64, kt * kTile, h);
+        if (!mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) {
+          mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DQ);
+          break;
+        }
+        mbar_arrive_expect_tx(&g.b_full[s], kFull);
+        for (int b = 0; b < 2; ++b) tma_load_3d(sv + s * kFull + b * kBox, &tm_v, &g.b_full[s], b * 64, kt * kTile, h);
+      }
+      for (int i = max(0, n - kStages); i < n; ++i) {   // every copy has landed before the block may leave
+        mbar_wait(&g.a_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
+        mbar_wait(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_q = idesc_bf16_f32(kTile, D, true);
+      const uint32_t k0 = smem_u32(sk), v0 = smem_u32(sv);
+      const auto scores = [&](int s) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, sdesc_k_sw128(k0 + s * kFull + (kk / 4) * kBox + (kk % 4) * 32), id_s, kk > 0);
+        umma_commit(&g.s_full);
+      };
+      const auto dps = [&](int s) {
+#pragma unroll
+        for (int kk = 0; kk < kDv / 16; ++kk)
+          umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, sdesc_k_sw128(v0 + s * kFull + (kk / 4) * kBox + (kk % 4) * 32), id_s, kk > 0);
+        umma_commit(&g.dp_full);
+        umma_commit(&g.b_empty[s]);
+      };
+      bool ok = kt0 < r.last && mbar_wait(&g.a_full[0], 0, &g.abort, st, KID_ATTN_DQ) &&
+                mbar_wait(&g.b_full[0], 0, &g.abort, st, KID_ATTN_DQ);
+      if (ok) {
+        tc_fence_after();
+        scores(0);
+        dps(0);
+      }
+      int n = 0;
+      for (int kt = kt0; ok && kt < r.last; ++n) {
+        const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1, next = next_of(kt);
+        if (next < r.last) {
+          ok = mbar_wait(&g.a_full[s1], par1, &g.abort, st, KID_ATTN_DQ) && mbar_wait(&g.s_free, n & 1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) break;
+          tc_fence_after();
+          scores(s1);
+        }
+        ok = mbar_wait(&g.ds_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, sdesc_sw128(k0 + s * kFull + kk * 2048, kBox, 1024), id_q,
+                       n > 0 || kk > 0);
+        umma_commit(&g.a_empty[s]);
+        if (next < r.last) {
+          ok = mbar_wait(&g.b_full[s1], par1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) break;
+          tc_fence_after();
+          dps(s1);
+        }
+        kt = next;
+      }
+      umma_commit(&g.acc_full);
+      umma_commit(&g.done);
+      mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DQ);
+    }
+  } else {
+    // this thread's row, and the half of the keys that its warpgroup takes
+    const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;
+    const float2 stat = row < p.T ? __ldcg(p.stat + static_cast<int64_t>(hq) * p.Tp + row) : make_float2(INFINITY, 0.f);
+    const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
+    const f2 sc = f2_make(p.scale_log2, p.scale_log2), mz = f2_make(-stat.x, -stat.x), md = f2_make(-stat.y, -stat.y);
+    bool ok = true;
+    int n = 0;
+    for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
+      ok = mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[64];
+      tmem_ld32(ts, x);
+      tmem_ld32(ts + 32, x + 32);
+      tmem_ld_wait();
+      arrive_warp(&g.s_free);
+      f2 w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mz));
+        w[i] = f2_make(ex2(z.x), ex2(z.y));
+      }
+      const int j0 = kt * kTile + 64 * half;
+      const bool whole = __all_sync(0xffffffffu, sp.start >= 0 && j0 >= seen0 && j0 + 64 <= row + 1);
+      ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(td, x);
+      tmem_ld32(td + 32, x + 32);
+      tmem_ld_wait();
+      uint32_t out[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const f2 d = f2_mul(f2_add(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), md), w[i]);
+        out[i] = f2_to_bf16x2(d);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t see = 0;
+          if (sp.start >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(sp.start, min(sink_end, row + 1), j0 + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            out[16 * c + i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+        }
+      }
+      tmem_st32(td, out);
+      tmem_st_wait();
+      arrive_warp(&g.ds_full);
+    }
+    if (ok) ok = mbar_wait(&g.acc_full, 0, &g.abort, st, KID_ATTN_DQ);
+    if (ok) {
+      tc_fence_after();
+      // each warpgroup writes one box of 64 columns (with d = 64 the first alone)
+      bool bad = false;
+      const bool some = kt0 < r.last;
+      uint8_t* stage = smem + half * kBox + (warp & 3) * 4096;
+      if (half < KB) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + kAcc0 + quarter + 64 * half + 32 * c, o);
+          tmem_ld_wait();
+          const bool in = 64 * half + 32 * c < D;
+          float big = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = __uint_as_float(o[i + 2 * k]) * p.scale, b = __uint_as_float(o[i + 2 * k + 1]) * p.scale;
+              big += fabsf(a) + fabsf(b);
+              w[k] = some ? pack_bf16x2(a, b) : 0u;
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + i / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          bad |= in && !(big < INFINITY);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && row < p.T) {
+          tma_store_3d(&tm_dq, stage, 64 * half, row, hq);
+          bulk_commit();
+          bulk_wait_all<0>();
+        }
+      }
+      __syncwarp();
+      const uint32_t again = __ballot_sync(0xffffffffu, bad && some && row < p.T);
+      if (lane == 0 && again) atomicOr(&g.again[warp & 3], again);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+  // Rows that are not finite may owe that to what they do not see (0 * NaN):
+  // they are computed again from what they see.
+  if (warp < 4)
+    for (uint32_t again = g.again[warp]; again; again &= again - 1) dq_row<D>(p, r0 + warp * 32 + __ffs(again) - 1, hq);
+}
+
+// ---------------------------------------------------------------------------
+// dk and dv: 128 keys of a head, and the query tiles that see them, of all
+// query heads in turn, the keys along the rows:
+//   S^T = k q^T, P^T = e^(S^T - lse), dv += P^T da
+//   dP^T = v da^T, ds^T = P^T (dP^T - delta), dk += ds^T q
+// issued dv(i), S(i + 1), dk(i), dP(i + 1): each step's forming of P^T and ds^T is
+// covered by two products.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_da,
+               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
+               const __grid_constant__ AttnArgs p, DevStatus st) {
+  constexpr int KB = boxes(D), kKBytes = KB * kBox;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared g;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sk = smem, *sv = sk + kFull, *sq = sv + kFull, *sd = sq + kStages * kFull;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y, r0 = blockIdx.x * kTile;
+
+  if (threadIdx.x == 0) init_barriers(g);
+  if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
+  if (warp == 9) {
+    tmem_alloc(&g.tmem, 512);
+    tmem_relinquish();
+  }
+  wait_for_previous();
+  // queries [row, end) see this thread's key; those from ds0 on pass something on
+  const int half = warp >> 2, row = r0 + (threadIdx.x & 127);
+  int begin = row, end = row, ds0 = row;
+  if (warp < 8) {
+    const Span sp = row < p.T ? span_of(p, row) : Span{-1, -1};
+    if (sp.start >= 0) {
+      end = last_seer(p, row, sp);
+      ds0 = row + (alone(p, row, sp.start) ? 1 : 0);
+    }
+    const int hi = __reduce_max_sync(0xffffffffu, end > row ? end : -1), lo = __reduce_min_sync(0xffffffffu, end > row ? row : INT_MAX);
+    if (lane == 0 && half == 0) g.hi[warp] = hi, g.lo[warp] = lo;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = g.tmem, quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const int hi = max(max(g.hi[0], g.hi[1]), max(g.hi[2], g.hi[3]));
+  const int tiles = hi < 0 ? 0 : (hi + kTile - 1) / kTile - blockIdx.x;   // query tiles of a head, from this one on
+  const int count = tiles * p.G;
+
+  if (warp == 8) {
+    if (lane == 0 && count > 0) {
+      mbar_arrive_expect_tx(&g.fixed_full, kKBytes + kFull);
+      for (int b = 0; b < KB; ++b) tma_load_3d(sk + b * kBox, &tm_k, &g.fixed_full, b * 64, r0, h);
+      for (int b = 0; b < 2; ++b) tma_load_3d(sv + b * kBox, &tm_v, &g.fixed_full, b * 64, r0, h);
+      int n = 0;
+      for (; n < count; ++n) {
+        const int s = n % kStages, par = (n / kStages) & 1, hq = h * p.G + n / tiles, i0 = r0 + (n % tiles) * kTile;
+        if (!mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DKV)) break;
+        mbar_arrive_expect_tx(&g.a_full[s], kKBytes + kTile * sizeof(float2));
+        for (int b = 0; b < KB; ++b) tma_load_3d(sq + s * kFull + b * kBox, &tm_q, &g.a_full[s], b * 64, i0, hq);
+        bulk_load(g.row[s], p.stat + static_cast<int64_t>(hq) * p.Tp + i0, kTile * sizeof(float2), &g.a_full[s]);
+        if (!mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DKV)) {
+          mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DKV);
+          break;
+        }
+        mbar_arrive_expect_tx(&g.b_full[s], kFull);
+        for (int b = 0; b < 2; ++b) tma_load_2d(sd + s * kFull + b * kBox, &tm_da, &g.b_full[s], hq * kDv + b * 64, i0);
+      }
+      mbar_wait(&g.fixed_full, 0, nullptr, st, KID_ATTN_DKV);
+      for (int i = max(0, n - kStages); i < n; ++i) {   // every copy has landed before the block may leave
+        mbar_wait(&g.a_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DKV);
+        mbar_wait(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DKV);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_k = idesc_bf16_f32(kTile, D, true),
+                         id_v = idesc_bf16_f32(kTile, kDv, true);
+      const uint32_t k0 = smem_u32(sk), v0 = smem_u32(sv), q0 = smem_u32(sq), d0 = smem_u32(sd);
+      const auto scores = [&](int s) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+          umma_bf16_ss(tmem + kScores, sdesc_k_sw128(k0 + at), sdesc_k_sw128(q0 + s * kFull + at), id_s, kk > 0);
+        }
+        umma_commit(&g.s_full);
+      };
+      const auto dps = [&](int s) {
+#pragma unroll
+        for (int kk = 0; kk < kDv / 16; ++kk) {
+          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+          umma_bf16_ss(tmem + kDp, sdesc_k_sw128(v0 + at), sdesc_k_sw128(d0 + s * kFull + at), id_s, kk > 0);
+        }
+        umma_commit(&g.dp_full);
+      };
+      bool ok = count > 0 && mbar_wait(&g.fixed_full, 0, &g.abort, st, KID_ATTN_DKV) &&
+                mbar_wait(&g.a_full[0], 0, &g.abort, st, KID_ATTN_DKV) && mbar_wait(&g.b_full[0], 0, &g.abort, st, KID_ATTN_DKV);
+      if (ok) {
+        tc_fence_after();
+        scores(0);
+        dps(0);
+      }
+      for (int n = 0; ok && n < count; ++n) {
+        const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1;
+        ok = mbar_wait(&g.p_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, sdesc_sw128(d0 + s * kFull + kk * 2048, kBox, 1024), id_v,
+                       n > 0 || kk > 0);
+        umma_commit(&g.b_empty[s]);
+        if (n + 1 < count) {
+          ok = mbar_wait(&g.a_full[s1], par1, &g.abort, st, KID_ATTN_DKV);
+          if (!ok) break;
+          tc_fence_after();
+          scores(s1);
+        }
+        ok = mbar_wait(&g.ds_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, sdesc_sw128(q0 + s * kFull + kk * 2048, kBox, 1024), id_k,
+                       n > 0 || kk > 0);
+        umma_commit(&g.a_empty[s]);
+        if (n + 1 < count) {
+          ok = mbar_wait(&g.b_full[s1], par1, &g.abort, st, KID_ATTN_DKV);
+          if (!ok) break;
+          tc_fence_after();
+          dps(s1);
+        }
+      }
+      umma_commit(&g.acc_full);
+      umma_commit(&g.done);
+      mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DKV);
+    }
+  } else {
+    // this thread's key, and the half of the queries that its warpgroup takes
+    const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;
+    const f2 sc = f2_make(p.scale_log2, p.scale_log2);
+    bool ok = true;
+    for (int n = 0; n < count; ++n) {
+      const int s = n % kStages, i0 = r0 + (n % tiles) * kTile + 64 * half;
+      ok = mbar_wait(&g.a_full[s], (n / kStages) & 1, &g.abort, st, KID_ATTN_DKV) && mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+      if (!ok) break;
+      tc_fence_after();
+      const float4* stat = reinterpret_cast<const float4*>(&g.row[s][64 * half]);   // two queries an entry
+      const bool whole = __all_sync(0xffffffffu, i0 >= ds0 && i0 + 64 <= end);
+      uint32_t x[64];
+      tmem_ld32(ts, x);
+      tmem_ld32(ts + 32, x + 32);
+      tmem_ld_wait();
+      f2 w[32];
+      uint32_t out[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float4 z = stat[i];
+        const float2 y = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, f2_make(-z.x, -z.z)));
+        w[i] = f2_make(ex2(y.x), ex2(y.y));
+        out[i] = f2_to_bf16x2(w[i]);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t see = bits(begin, end, i0 + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            out[16 * c + i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+        }
+      }
+      tmem_st32(ts, out);
+      tmem_st_wait();
+      arrive_warp(&g.p_full);
+      ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(td, x);
+      tmem_ld32(td + 32, x + 32);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float4 z = stat[i];
+        out[i] = f2_to_bf16x2(f2_mul(f2_sub(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2_make(z.y, z.w)), w[i]));
+      }
+      if (!whole) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t see = bits(ds0, end, i0 + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            out[16 * c + i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+        }
+      }
+      tmem_st32(td, out);
+      tmem_st_wait();
+      arrive_warp(&g.ds_full);
+    }
+    if (ok) ok = mbar_wait(&g.acc_full, 0, &g.abort, st, KID_ATTN_DKV);
+    if (ok) {
+      tc_fence_after();
+      // one warpgroup writes dv, the other dk
+      const int width = half == 0 ? kDv : D, nb = boxes(width);
+      const float f = half == 0 ? 1.f : p.scale;
+      uint8_t* stage = (half == 0 ? sv : sk) + (warp & 3) * 8192;
+      bool bad = false;
+      for (int c = 0; c < 2 * nb; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tmem + (half == 0 ? kAcc0 : kAcc1) + quarter + 32 * c, o);
+        tmem_ld_wait();
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float(o[i + 2 * k]) * f, b = __uint_as_float(o[i + 2 * k + 1]) * f;
+            big += fabsf(a) + fabsf(b);
+            w[k] = count > 0 ? pack_bf16x2(a, b) : 0u;
+          }
+          *reinterpret_cast<uint4*>(stage + (c >> 1) * 4096 + lane * 128 + (((4 * (c & 1) + i / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        bad |= 32 * c < width && !(big < INFINITY);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0 && row < p.T) {
+        for (int b = 0; b < nb; ++b) tma_store_3d(half == 0 ? &tm_dv : &tm_dk, stage + b * 4096, 64 * b, row, h);
+        bulk_commit();
+        bulk_wait_all<0>();
+      }
+      __syncwarp();
+      const uint32_t again = __ballot_sync(0xffffffffu, bad && count > 0 && row < p.T);
+      if (lane == 0 && again) atomicOr(&g.again[warp & 3], again);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp < 4)   // as for dq
+    for (uint32_t again = g.again[warp]; again; again &= again - 1) dkv_row<D>(p, r0 + warp * 32 + __ffs(again) - 1, h);
+}
+
+template <class... Args>
+cudaError_t allow_smem(void (*kernel)(Args...), int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, DevStatus st, cudaStream_t s) {
+  static std::atomic<bool> ready[2][64];
+  cudaError_t e = allow_smem(dq_kernel<D>, dq_smem(D), ready[0]);
+  if (e == cudaSuccess) e = allow_smem(dkv_kernel<D>, dkv_smem(D), ready[1]);
+  if (e != cudaSuccess) return e;
+  constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap q, k, v, da, dq, dk, dv;
+  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, 64, kTile, 1, sw) || !map3d(&k, bf16, 2, a.k, D, a.T, a.H, 64, kTile, 1, sw) ||
+      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, 64, kTile, 1, sw) ||
+      !map2d_bf16(&da, a.da, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, kTile) ||
+      !map3d(&dq, bf16, 2, a.dq, D, a.T, a.Hq, 64, 32, 1, sw) || !map3d(&dk, bf16, 2, a.dk, D, a.T, a.H, 64, 32, 1, sw) ||
+      !map3d(&dv, bf16, 2, a.dv, kDv, a.T, a.H, 64, 32, 1, sw))
+    return cudaErrorInvalidValue;
+  const int64_t rows = static_cast<int64_t>(a.Tp) * a.Hq;
+  e = launch_dependent(delta_kernel, dim3(static_cast<unsigned>((rows + kPrepWarps - 1) / kPrepWarps)), 32 * kPrepWarps, 0, s, a, st);
+  if (e != cudaSuccess) return e;
+  const unsigned tiles = (a.T + kTile - 1) / kTile;
+  e = launch_dependent(dkv_kernel<D>, dim3(tiles, a.H), kThreads, dkv_smem(D), s, q, da, k, v, dk, dv, a, st);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(dq_kernel<D>, dim3(tiles, a.Hq), kThreads, dq_smem(D), s, k, v, dq, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_backward(const AttnArgs& a, DevStatus st, cudaStream_t s) {
+  return a.d == 64 ? launch<64>(a, st, s) : a.d == 96 ? launch<96>(a, st, s) : launch<128>(a, st, s);
+}
+
+}  // namespace qkvp

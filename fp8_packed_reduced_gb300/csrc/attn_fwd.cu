@@ -19,13 +19,6 @@ __host__ __device__ constexpr int boxes(int d) { return (d + 63) / 64; }
 __host__ __device__ constexpr int smem_bytes(int d) { return 1024 + 2 * kQBytes + kStages * (boxes(d) * kBox + kVBytes); }
 constexpr float kSlack = 8.f;                // powers of two by which scores may pass the maximum that they are relative to
 
-// Key tiles (of 128, on the grid of the packed rows) that a query tile needs:
-// those that hold its sequence's first tokens, and those from its window on.
-struct Range {
-  int sink0, sink1, first, last;   // [sink0, sink1) and [first, last)
-  __device__ bool has(int kt) const { return (kt >= sink0 && kt < sink1) || (kt >= first && kt < last); }
-};
-
 struct Shared {
   uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], done;
@@ -45,13 +38,6 @@ __device__ __forceinline__ int next_tile(const Range& a, const Range& b, int kt)
   for (int i = 0; i < 4; ++i)
     if (at[i] >= kt) n = min(n, at[i]);
   return n;
-}
-
-// Bits lo .. hi - 1 of the 32 from `base` on.
-__device__ __forceinline__ uint32_t bits(int lo, int hi, int base) {
-  const int a = min(max(lo - base, 0), 32), b = min(max(hi - base, 0), 32);
-  if (a >= b) return 0u;
-  return (b == 32 ? ~0u : (1u << b) - 1u) & ~((1u << a) - 1u);   // a < 32 here
 }
 
 template <int D>
@@ -104,19 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) g.lo[t][warp & 3] = lo, g.hi[t][warp & 3] = hi, g.start[t][warp & 3] = s0;
   }
   __syncthreads();
-  if (threadIdx.x < 2) {
-    int lo = INT_MAX, hi = -1, s0 = INT_MAX;
-    for (int i = 0; i < 4; ++i)
-      lo = min(lo, g.lo[threadIdx.x][i]), hi = max(hi, g.hi[threadIdx.x][i]), s0 = min(s0, g.start[threadIdx.x][i]);
-    Range r{0, 0, 0, 0};
-    if (hi >= 0) {
-      r.first = lo / kTile;
-      r.last = hi / kTile + 1;
-      r.sink0 = s0 / kTile;
-      r.sink1 = p.sinks ? min(r.first, (min(s0 + min(p.sinks, p.T), p.T) + kTile - 1) / kTile) : r.sink0;
-    }
-    g.range[threadIdx.x] = r;
-  }
+  if (threadIdx.x < 2) g.range[threadIdx.x] = range_of(p, g.lo[threadIdx.x], g.hi[threadIdx.x], g.start[threadIdx.x]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
