@@ -8,6 +8,7 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+size_t order_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Tp) / kAttnTile * sizeof(int) + 255) / 256 * 256; }
 size_t stat_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Hq) * a.Tp * sizeof(float2) + 255) / 256 * 256; }
 
 }  // namespace
@@ -47,7 +48,7 @@ extern "C" {
 size_t qkvp_attention_workspace_bytes(const qkvp_attention* at) {
   AttnArgs a;
   if (check_attention(at, &a) != QKVP_OK) return 0;
-  return kAttnHeaderBytes + stat_bytes(a);
+  return kAttnHeaderBytes + 2 * order_bytes(a) + stat_bytes(a);
 }
 
 int qkvp_attention_forward(const qkvp_attention* at, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* a,
@@ -61,13 +62,14 @@ int qkvp_attention_forward(const qkvp_attention* at, const uint16_t* q, const ui
     if (!x && p.T) return QKVP_ERR_INVALID_ARGUMENT;
     if (!aligned16(x)) return QKVP_ERR_MISALIGNED;
   }
-  if (ws_bytes < kAttnHeaderBytes) return QKVP_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < kAttnHeaderBytes + order_bytes(p)) return QKVP_ERR_WORKSPACE_TOO_SMALL;
   if (p.T == 0) return QKVP_OK;
   p.q = q;
   p.k = k;
   p.v = v;
   p.a = a;
   p.lse = lse;
+  p.order[0] = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kAttnHeaderBytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   mark(s);
   if (launch_attention_forward(p, dev_status(ws), s) != cudaSuccess) return QKVP_ERR_CUDA;
@@ -87,7 +89,7 @@ int qkvp_attention_backward(const qkvp_attention* at, const uint16_t* da, const 
     if (!x && p.T) return QKVP_ERR_INVALID_ARGUMENT;
     if (!aligned16(x)) return QKVP_ERR_MISALIGNED;
   }
-  if (ws_bytes < kAttnHeaderBytes + stat_bytes(p)) return QKVP_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < kAttnHeaderBytes + 2 * order_bytes(p) + stat_bytes(p)) return QKVP_ERR_WORKSPACE_TOO_SMALL;
   if (p.T == 0) return QKVP_OK;
   p.q = q;
   p.k = k;
@@ -95,7 +97,10 @@ int qkvp_attention_backward(const qkvp_attention* at, const uint16_t* da, const 
   p.a = const_cast<uint16_t*>(a);
   p.lse = const_cast<float*>(lse);
   p.da = da;
-  p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + kAttnHeaderBytes);
+  uint8_t* w = static_cast<uint8_t*>(ws) + kAttnHeaderBytes;
+  p.order[0] = reinterpret_cast<int*>(w);
+  p.order[1] = reinterpret_cast<int*>(w + order_bytes(p));
+  p.stat = reinterpret_cast<float2*>(w + 2 * order_bytes(p));
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;

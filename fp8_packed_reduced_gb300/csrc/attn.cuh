@@ -30,7 +30,18 @@ struct AttnArgs {
   int Tp;                    // T rounded up to whole tiles
   float2* stat;              // [Hq, Tp] lse in base 2 (+inf: no weight), da . a
   uint16_t *dq, *dk, *dv;
+  int* order[2];             // tiles from the longest on (backward: of dq, of dk and dv), or null: as they come
 };
+
+// Row and head of a block: the grid is tiles x heads, all heads of a tile next
+// to each other.
+struct Place {
+  int tile, head;
+};
+__device__ __forceinline__ Place place_of(const int* order, int heads) {
+  const int i = blockIdx.x / heads;
+  return Place{order ? __ldcg(order + i) : i, static_cast<int>(blockIdx.x) - i * heads};
+}
 
 constexpr int kAttnTile = 128;   // query rows and keys of the products
 
@@ -96,6 +107,53 @@ __device__ __forceinline__ uint32_t bits(int lo, int hi, int base) {
 // The queries that see token `row` of sequence sp end here.
 __device__ __forceinline__ int last_seer(const AttnArgs& p, int row, Span sp) {
   return row - sp.start < p.sinks || sp.end - row <= p.window ? sp.end : row + p.window;
+}
+
+// The tiles of an attention in the order of their work, longest first, so that
+// the blocks that start last are the short ones.  One block; order [tiles].
+//   keys: the tiles are of keys (dk, dv), else of queries of `rows` rows each
+__device__ __forceinline__ int tile_work(const AttnArgs& p, int tile, int rows, bool keys) {
+  const int r0 = tile * rows, r1 = min(r0 + rows, p.T) - 1;
+  const Span a = span_of(p, r0), b = span_of(p, r1);
+  if (keys) {
+    int end = 0;
+    if (a.start >= 0) end = last_seer(p, r0, a);
+    if (b.start >= 0) end = max(end, b.start >= r0 ? last_seer(p, b.start, b) : last_seer(p, r1, b));
+    return max(0, (end - r0 + kAttnTile - 1) / kAttnTile);
+  }
+  if (a.start < 0 && b.start < 0) return 0;   // (a sequence in between is shorter than the tile)
+  const int first = a.start < 0 ? r0 : window_start(p, r0, a.start);
+  const int sinks = a.start < 0 || !p.sinks ? 0 : min(first - a.start, p.sinks);
+  return (r1 - first) / kAttnTile + 1 + (sinks + kAttnTile - 1) / kAttnTile;
+}
+template <int kThreads>
+__device__ __forceinline__ void sort_tiles(const AttnArgs& p, int tiles, int rows, bool keys, int* order) {
+  constexpr int kBins = 1024;
+  __shared__ int bin[kBins], most;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) bin[i] = 0;
+  if (threadIdx.x == 0) most = 1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < tiles; i += kThreads) atomicMax(&most, tile_work(p, i, rows, keys));
+  __syncthreads();
+  const auto bin_of = [&](int i) { return kBins - 1 - static_cast<int>(static_cast<int64_t>(tile_work(p, i, rows, keys)) * (kBins - 1) / most); };
+  for (int i = threadIdx.x; i < tiles; i += kThreads) atomicAdd(&bin[bin_of(i)], 1);
+  __syncthreads();
+  if (threadIdx.x < 32) {   // places of the bins
+    int run = 0;
+    for (int b0 = 0; b0 < kBins; b0 += 32) {
+      const int v = bin[b0 + threadIdx.x];
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (threadIdx.x >= o) x += y;
+      }
+      bin[b0 + threadIdx.x] = run + x - v;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tiles; i += kThreads) order[atomicAdd(&bin[bin_of(i)], 1)] = i;
 }
 
 // Records offsets that are out of range or decrease; one block calls it.

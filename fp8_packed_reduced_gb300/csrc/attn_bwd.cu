@@ -59,20 +59,41 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
 
 // delta = da . a of every row and head, and beside it the row's lse in base 2
 // (+inf where the row has no weight at all, so that its probabilities are 0).
-constexpr int kPrepWarps = 8;
-__global__ void __launch_bounds__(32 * kPrepWarps) delta_kernel(const __grid_constant__ AttnArgs p, DevStatus st) {
+// A half warp a row, 16 rows a warp.  Its first blocks put the tiles of the two
+// passes in order.
+constexpr int kPrepThreads = 256, kPrepRows = kPrepThreads / 32 * 16;
+static_assert(kPrepRows == kTile, "the statistics cover whole tiles");
+__global__ void __launch_bounds__(kPrepThreads) delta_kernel(const __grid_constant__ AttnArgs p, int tiles, DevStatus st) {
   wait_for_previous();
   if (blockIdx.x == 0) check_offsets(p, st, KID_ATTN_DELTA);
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kPrepWarps + (threadIdx.x >> 5);   // row * Hq + head
-  if (r >= static_cast<int64_t>(p.Tp) * p.Hq) return;
-  const int lane = threadIdx.x & 31, row = static_cast<int>(r / p.Hq), hq = static_cast<int>(r % p.Hq);
-  float s = 0.f, z = -INFINITY;
-  if (row < p.T) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p.da + r * kDv) + lane), y = __ldg(reinterpret_cast<const uint2*>(p.a + r * kDv) + lane);
-    s = warp_add(bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y));
-    z = __ldg(p.lse + static_cast<int64_t>(hq) * p.T + row);
+  const int sorts = p.order[0] ? 2 : 0;
+  if (static_cast<int>(blockIdx.x) < sorts) {
+    sort_tiles<kPrepThreads>(p, tiles, kTile, blockIdx.x == 1, p.order[blockIdx.x]);
+    return;
   }
-  if (lane == 0) p.stat[static_cast<int64_t>(hq) * p.Tp + row] = make_float2(z == -INFINITY ? INFINITY : z * 1.4426950408889634f, s);
+  const int block = blockIdx.x - sorts, hq = block / tiles;
+  const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
+  const int r0 = (block - hq * tiles) * kTile + (threadIdx.x >> 5) * 16;
+  float mine = 0.f;   // lane c < 8 of a half keeps row r0 + 2 c + half
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = r0 + 2 * i + half;
+    float s = 0.f;
+    if (row < p.T) {
+      const int64_t at = (static_cast<int64_t>(row) * p.Hq + hq) * kDv;
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.da + at) + c), y = __ldg(reinterpret_cast<const uint4*>(p.a + at) + c);
+      s = bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) + bf16_hi(x.y) * bf16_hi(y.y) +
+          bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) + bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (c == i) mine = s;
+  }
+  const int row = r0 + 2 * c + half;
+  if (c < 8) {
+    const float z = row < p.T ? __ldg(p.lse + static_cast<int64_t>(hq) * p.T + row) : -INFINITY;
+    p.stat[static_cast<int64_t>(hq) * p.Tp + row] = make_float2(z == -INFINITY ? INFINITY : z * 1.4426950408889634f, mine);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -91,8 +112,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sk = smem, *sv = sk + kStages * kFull;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hq = blockIdx.y, h = hq / p.G;
-  const int r0 = (gridDim.x - 1 - blockIdx.x) * kTile;
 
   if (threadIdx.x == 0) init_barriers(g);
   if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
@@ -101,6 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   wait_for_previous();
+  const Place at = place_of(p.order[0], p.Hq);
+  const int hq = at.head, h = hq / p.G, r0 = at.tile * kTile;
   const int half = warp >> 2, row = r0 + (threadIdx.x & 127);
   Span sp{-1, -1};
   int seen0 = 0;
@@ -335,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sk = smem, *sv = sk + kFull, *sq = sv + kFull, *sd = sq + kStages * kFull;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, r0 = blockIdx.x * kTile;
 
   if (threadIdx.x == 0) init_barriers(g);
   if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
@@ -344,6 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   wait_for_previous();
+  const Place at = place_of(p.order[1], p.H);
+  const int h = at.head, r0 = at.tile * kTile;
   // queries [row, end) see this thread's key; those from ds0 on pass something on
   const int half = warp >> 2, row = r0 + (threadIdx.x & 127);
   int begin = row, end = row, ds0 = row;
@@ -361,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = g.tmem, quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const int hi = max(max(g.hi[0], g.hi[1]), max(g.hi[2], g.hi[3]));
-  const int tiles = hi < 0 ? 0 : (hi + kTile - 1) / kTile - blockIdx.x;   // query tiles of a head, from this one on
+  const int tiles = hi < 0 ? 0 : (hi + kTile - 1) / kTile - at.tile;   // query tiles of a head, from this one on
   const int count = tiles * p.G;
 
   if (warp == 8) {
@@ -570,7 +592,7 @@ cudaError_t allow_smem(void (*kernel)(Args...), int bytes, std::atomic<bool> (&d
 }
 
 template <int D>
-cudaError_t launch(const AttnArgs& a, DevStatus st, cudaStream_t s) {
+cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   static std::atomic<bool> ready[2][64];
   cudaError_t e = allow_smem(dq_kernel<D>, dq_smem(D), ready[0]);
   if (e == cudaSuccess) e = allow_smem(dkv_kernel<D>, dkv_smem(D), ready[1]);
@@ -584,13 +606,14 @@ cudaError_t launch(const AttnArgs& a, DevStatus st, cudaStream_t s) {
       !map3d(&dq, bf16, 2, a.dq, D, a.T, a.Hq, 64, 32, 1, sw) || !map3d(&dk, bf16, 2, a.dk, D, a.T, a.H, 64, 32, 1, sw) ||
       !map3d(&dv, bf16, 2, a.dv, kDv, a.T, a.H, 64, 32, 1, sw))
     return cudaErrorInvalidValue;
-  const int64_t rows = static_cast<int64_t>(a.Tp) * a.Hq;
-  e = launch_dependent(delta_kernel, dim3(static_cast<unsigned>((rows + kPrepWarps - 1) / kPrepWarps)), 32 * kPrepWarps, 0, s, a, st);
+  const int tiles = a.Tp / kTile;
+  if (static_cast<int64_t>(tiles) * a.Hq <= device_sms()) a.order[0] = a.order[1] = nullptr;   // all blocks start at once
+  const unsigned prep = (a.order[0] ? 2 : 0) + static_cast<unsigned>(tiles) * a.Hq;
+  e = launch_dependent(delta_kernel, dim3(prep), kPrepThreads, 0, s, a, tiles, st);
   if (e != cudaSuccess) return e;
-  const unsigned tiles = (a.T + kTile - 1) / kTile;
-  e = launch_dependent(dkv_kernel<D>, dim3(tiles, a.H), kThreads, dkv_smem(D), s, q, da, k, v, dk, dv, a, st);
+  e = launch_dependent(dkv_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.H), kThreads, dkv_smem(D), s, q, da, k, v, dk, dv, a, st);
   if (e != cudaSuccess) return e;
-  return launch_dependent(dq_kernel<D>, dim3(tiles, a.Hq), kThreads, dq_smem(D), s, k, v, dq, a, st);
+  return launch_dependent(dq_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.Hq), kThreads, dq_smem(D), s, k, v, dq, a, st);
 }
 
 }  // namespace

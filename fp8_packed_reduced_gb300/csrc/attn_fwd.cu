@@ -51,9 +51,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sq = smem, *sk = sq + 2 * kQBytes, *sv = sk + kStages * kKBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hq = blockIdx.y, h = hq / p.G;
-  const int r0 = (gridDim.x - 1 - blockIdx.x) * kRows;   // the later rows see more: they come first
-
   if (threadIdx.x == 0) {
     g.abort = 0;
     mbar_init(&g.q_full, 1);
@@ -76,7 +73,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   wait_for_previous();
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p, st, KID_ATTN_FWD);
+  const Place at = place_of(p.order[0], p.Hq);
+  const int hq = at.head, h = hq / p.G, r0 = at.tile * kRows;
+  if (blockIdx.x == 0) check_offsets(p, st, KID_ATTN_FWD);
   // the rows' sequences, and from them the key tiles
   const int t = warp >> 2;              // query tile of a softmax warp
   const int row = r0 + threadIdx.x;     // of a softmax thread
@@ -301,8 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
+__global__ void __launch_bounds__(1024) order_kernel(const __grid_constant__ AttnArgs p, int tiles) {
+  wait_for_previous();
+  sort_tiles<1024>(p, tiles, kRows, false, p.order[0]);
+}
+
 template <int D>
-cudaError_t launch(const AttnArgs& a, DevStatus st, cudaStream_t s) {
+cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -312,13 +316,22 @@ cudaError_t launch(const AttnArgs& a, DevStatus st, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
+  // With no more blocks than multiprocessors all of them start at once.
+  const int tiles = (a.T + kRows - 1) / kRows;
+  const int64_t blocks = static_cast<int64_t>(tiles) * a.Hq;
+  if (blocks > device_sms()) {
+    e = launch_dependent(order_kernel, dim3(1), 1024, 0, s, a, tiles);
+    if (e != cudaSuccess) return e;
+  } else {
+    a.order[0] = nullptr;
+  }
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   CUtensorMap q, k, v, o;
   if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, 64, kTile, 1, sw) || !map3d(&k, bf16, 2, a.k, D, a.T, a.H, 64, kTile, 1, sw) ||
       !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, 64, kTile, 1, sw) || !map2d_bf16(&o, a.a, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, 32))
     return cudaErrorInvalidValue;
-  return launch_dependent(forward_kernel<D>, dim3((a.T + kRows - 1) / kRows, a.Hq), kThreads, smem_bytes(D), s, q, k, v, o, a, st);
+  return launch_dependent(forward_kernel<D>, dim3(static_cast<unsigned>(blocks)), kThreads, smem_bytes(D), s, q, k, v, o, a, st);
 }
 
 }  // namespace

@@ -49,7 +49,7 @@ def test_attention_refuses_bad_pointers(qk):
     L, d = qk.lib(), _at(qk)
     n = L.qkvp_attention_workspace_bytes(d)
     assert n >= 1024 + 4 * 4 * 100
-    for call, pointers, size in ((L.qkvp_attention_forward, 6, 1024), (L.qkvp_attention_backward, 10, n)):
+    for call, pointers, size in ((L.qkvp_attention_forward, 6, 1024 + 256), (L.qkvp_attention_backward, 10, n)):
         assert call(None, *[P] * pointers, BIG, None) == qk.ERR_INVALID_ARGUMENT
         for i in range(pointers):
             args = [P] * pointers
