@@ -182,58 +182,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_q = idesc_bf16_f32(kTile, D, true);
-      const uint32_t k0 = smem_u32(sk), v0 = smem_u32(sv);
-      const auto scores = [&](int s) {
+    // The whole warp goes the same way (umma_bf16_ss says why).
+    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_q = idesc_bf16_f32(kTile, D, true);
+    const uint32_t elected = elect_one();
+    const uint64_t k0 = sdesc_k_sw128(smem_u32(sk)), v0 = sdesc_k_sw128(smem_u32(sv)), k0_mn = sdesc_sw128(smem_u32(sk), kBox, 1024);
+    const auto wait = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DQ));
+    };
+    const auto scores = [&](int s) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, sdesc_k_sw128(k0 + s * kFull + (kk / 4) * kBox + (kk % 4) * 32), id_s, kk > 0);
-        umma_commit(&g.s_full);
-      };
-      const auto dps = [&](int s) {
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
+      umma_commit_elected(&g.s_full, elected);
+    };
+    const auto dps = [&](int s) {
 #pragma unroll
-        for (int kk = 0; kk < kDv / 16; ++kk)
-          umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, sdesc_k_sw128(v0 + s * kFull + (kk / 4) * kBox + (kk % 4) * 32), id_s, kk > 0);
-        umma_commit(&g.dp_full);
-        umma_commit(&g.b_empty[s]);
-      };
-      bool ok = kt0 < r.last && mbar_wait(&g.a_full[0], 0, &g.abort, st, KID_ATTN_DQ) &&
-                mbar_wait(&g.b_full[0], 0, &g.abort, st, KID_ATTN_DQ);
-      if (ok) {
-        tc_fence_after();
-        scores(0);
-        dps(0);
-      }
-      int n = 0;
-      for (int kt = kt0; ok && kt < r.last; ++n) {
-        const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1, next = next_of(kt);
-        if (next < r.last) {
-          ok = mbar_wait(&g.a_full[s1], par1, &g.abort, st, KID_ATTN_DQ) && mbar_wait(&g.s_free, n & 1, &g.abort, st, KID_ATTN_DQ);
-          if (!ok) break;
-          tc_fence_after();
-          scores(s1);
-        }
-        ok = mbar_wait(&g.ds_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+      for (int kk = 0; kk < kDv / 16; ++kk)
+        umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, v0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
+      umma_commit_elected(&g.dp_full, elected);
+      umma_commit_elected(&g.b_empty[s], elected);
+    };
+    bool ok = kt0 < r.last && wait(&g.a_full[0], 0) && wait(&g.b_full[0], 0);
+    if (ok) {
+      tc_fence_after();
+      scores(0);
+      dps(0);
+    }
+    int n = 0;
+    for (int kt = kt0; ok && kt < r.last; ++n) {
+      const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1, next = next_of(kt);
+      if (next < r.last) {
+        ok = wait(&g.a_full[s1], par1) && wait(&g.s_free, n & 1);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, sdesc_sw128(k0 + s * kFull + kk * 2048, kBox, 1024), id_q,
-                       n > 0 || kk > 0);
-        umma_commit(&g.a_empty[s]);
-        if (next < r.last) {
-          ok = mbar_wait(&g.b_full[s1], par1, &g.abort, st, KID_ATTN_DQ);
-          if (!ok) break;
-          tc_fence_after();
-          dps(s1);
-        }
-        kt = next;
+        scores(s1);
       }
-      umma_commit(&g.acc_full);
-      umma_commit(&g.done);
-      mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DQ);
+      ok = wait(&g.ds_full, n & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0_mn + ((s * kFull + kk * 2048) >> 4), id_q, n > 0 || kk > 0,
+                     elected);
+      umma_commit_elected(&g.a_empty[s], elected);
+      if (next < r.last) {
+        ok = wait(&g.b_full[s1], par1);
+        if (!ok) break;
+        tc_fence_after();
+        dps(s1);
+      }
+      kt = next;
     }
+    umma_commit_elected(&g.acc_full, elected);
+    umma_commit_elected(&g.done, elected);
+    mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DQ);
   } else {
     // this thread's row, and the half of the keys that its warpgroup takes
     const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;
@@ -412,68 +414,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_k = idesc_bf16_f32(kTile, D, true),
-                         id_v = idesc_bf16_f32(kTile, kDv, true);
-      const uint32_t k0 = smem_u32(sk), v0 = smem_u32(sv), q0 = smem_u32(sq), d0 = smem_u32(sd);
-      const auto scores = [&](int s) {
+    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_k = idesc_bf16_f32(kTile, D, true),
+                       id_v = idesc_bf16_f32(kTile, kDv, true);
+    const uint32_t elected = elect_one();
+    const uint64_t k0 = sdesc_k_sw128(smem_u32(sk)), v0 = sdesc_k_sw128(smem_u32(sv)), q0 = sdesc_k_sw128(smem_u32(sq)),
+                   d0 = sdesc_k_sw128(smem_u32(sd)), q0_mn = sdesc_sw128(smem_u32(sq), kBox, 1024),
+                   d0_mn = sdesc_sw128(smem_u32(sd), kBox, 1024);
+    const auto wait = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DKV));
+    };
+    const auto scores = [&](int s) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-          umma_bf16_ss(tmem + kScores, sdesc_k_sw128(k0 + at), sdesc_k_sw128(q0 + s * kFull + at), id_s, kk > 0);
-        }
-        umma_commit(&g.s_full);
-      };
-      const auto dps = [&](int s) {
-#pragma unroll
-        for (int kk = 0; kk < kDv / 16; ++kk) {
-          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-          umma_bf16_ss(tmem + kDp, sdesc_k_sw128(v0 + at), sdesc_k_sw128(d0 + s * kFull + at), id_s, kk > 0);
-        }
-        umma_commit(&g.dp_full);
-      };
-      bool ok = count > 0 && mbar_wait(&g.fixed_full, 0, &g.abort, st, KID_ATTN_DKV) &&
-                mbar_wait(&g.a_full[0], 0, &g.abort, st, KID_ATTN_DKV) && mbar_wait(&g.b_full[0], 0, &g.abort, st, KID_ATTN_DKV);
-      if (ok) {
-        tc_fence_after();
-        scores(0);
-        dps(0);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+        umma_bf16_ss(tmem + kScores, k0 + (at >> 4), q0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
       }
-      for (int n = 0; ok && n < count; ++n) {
-        const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1;
-        ok = mbar_wait(&g.p_full, n & 1, &g.abort, st, KID_ATTN_DKV);
-        if (!ok) break;
-        tc_fence_after();
+      umma_commit_elected(&g.s_full, elected);
+    };
+    const auto dps = [&](int s) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, sdesc_sw128(d0 + s * kFull + kk * 2048, kBox, 1024), id_v,
-                       n > 0 || kk > 0);
-        umma_commit(&g.b_empty[s]);
-        if (n + 1 < count) {
-          ok = mbar_wait(&g.a_full[s1], par1, &g.abort, st, KID_ATTN_DKV);
-          if (!ok) break;
-          tc_fence_after();
-          scores(s1);
-        }
-        ok = mbar_wait(&g.ds_full, n & 1, &g.abort, st, KID_ATTN_DKV);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, sdesc_sw128(q0 + s * kFull + kk * 2048, kBox, 1024), id_k,
-                       n > 0 || kk > 0);
-        umma_commit(&g.a_empty[s]);
-        if (n + 1 < count) {
-          ok = mbar_wait(&g.b_full[s1], par1, &g.abort, st, KID_ATTN_DKV);
-          if (!ok) break;
-          tc_fence_after();
-          dps(s1);
-        }
+      for (int kk = 0; kk < kDv / 16; ++kk) {
+        const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+        umma_bf16_ss(tmem + kDp, v0 + (at >> 4), d0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
       }
-      umma_commit(&g.acc_full);
-      umma_commit(&g.done);
-      mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DKV);
+      umma_commit_elected(&g.dp_full, elected);
+    };
+    bool ok = count > 0 && wait(&g.fixed_full, 0) && wait(&g.a_full[0], 0) && wait(&g.b_full[0], 0);
+    if (ok) {
+      tc_fence_after();
+      scores(0);
+      dps(0);
     }
+    for (int n = 0; ok && n < count; ++n) {
+      const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1;
+      ok = wait(&g.p_full, n & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0_mn + ((s * kFull + kk * 2048) >> 4), id_v, n > 0 || kk > 0,
+                     elected);
+      umma_commit_elected(&g.b_empty[s], elected);
+      if (n + 1 < count) {
+        ok = wait(&g.a_full[s1], par1);
+        if (!ok) break;
+        tc_fence_after();
+        scores(s1);
+      }
+      ok = wait(&g.ds_full, n & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0_mn + ((s * kFull + kk * 2048) >> 4), id_k, n > 0 || kk > 0,
+                     elected);
+      umma_commit_elected(&g.a_empty[s], elected);
+      if (n + 1 < count) {
+        ok = wait(&g.b_full[s1], par1);
+        if (!ok) break;
+        tc_fence_after();
+        dps(s1);
+      }
+    }
+    umma_commit_elected(&g.acc_full, elected);
+    umma_commit_elected(&g.done, elected);
+    mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DKV);
   } else {
     // this thread's key, and the half of the queries that its warpgroup takes
     const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;

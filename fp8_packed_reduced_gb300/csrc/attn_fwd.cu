@@ -127,56 +127,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 9) {
-      if (lane == 0) {
-        constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_o = idesc_bf16_f32(kTile, kDv, true);
-        const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
-        const auto scores = [&](int i, int s) {
-  #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-            umma_bf16_ss(tmem + i * kTile, sdesc_k_sw128(q0 + i * kQBytes + at), sdesc_k_sw128(k0 + s * kKBytes + at), id_s, kk > 0);
-          }
-          umma_commit(&g.s_full[i]);
-        };
-        int pn[2] = {0, 0};   // products with v so far
-        bool ok = kt0 != INT_MAX && wait_inline(&g.q_full, 0, &g.abort, st, KID_ATTN_FWD) &&
-                  wait_inline(&g.k_full[0], 0, &g.abort, st, KID_ATTN_FWD);
-        if (ok) {
-          tc_fence_after();
-          if (ra.has(kt0)) scores(0, 0);
-          if (rb.has(kt0)) scores(1, 0);
-          umma_commit(&g.k_empty[0]);
+      // The whole warp goes the same way (umma_bf16_ss says why).
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_o = idesc_bf16_f32(kTile, kDv, true);
+      const uint32_t elected = elect_one();
+      const uint64_t q0 = sdesc_k_sw128(smem_u32(sq)), k0 = sdesc_k_sw128(smem_u32(sk)), v0 = sdesc_sw128(smem_u32(sv), kBox, 1024);
+      const auto wait = [&](uint64_t* bar, uint32_t par) {
+        return __all_sync(0xffffffffu, wait_inline(bar, par, &g.abort, st, KID_ATTN_FWD));
+      };
+      const auto scores = [&](int i, int s) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+          umma_bf16_ss(tmem + i * kTile, q0 + ((i * kQBytes + at) >> 4), k0 + ((s * kKBytes + at) >> 4), id_s, kk > 0, elected);
         }
-        int n = 0;
-        for (int kt = kt0; ok && kt != INT_MAX; ++n) {
-          const int s = n % kStages, next = next_tile(ra, rb, kt + 1), s1 = (n + 1) % kStages;
-          ok = wait_inline(&g.v_full[s], (n / kStages) & 1, &g.abort, st, KID_ATTN_FWD) &&
-               (next == INT_MAX || wait_inline(&g.k_full[s1], ((n + 1) / kStages) & 1, &g.abort, st, KID_ATTN_FWD));
-  #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const Range& r = i == 0 ? ra : rb;
-            if (ok && r.has(kt)) {
-              ok = wait_inline(&g.p_full[i], pn[i] & 1, &g.abort, st, KID_ATTN_FWD);
-              if (!ok) break;
-              tc_fence_after();
-  #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_bf16_ts(tmem + kRows + i * kDv, tmem + i * kTile + kk * 8, sdesc_sw128(v0 + s * kVBytes + kk * 2048, kBox, 1024), id_o,
-                             pn[i] > 0 || kk > 0);
-              ++pn[i];
-            }
-            if (ok && next != INT_MAX && r.has(next)) scores(i, s1);
-          }
-          if (!ok) break;
-          umma_commit(&g.v_empty[s]);
-          if (next != INT_MAX) umma_commit(&g.k_empty[s1]);
-          kt = next;
-        }
-        umma_commit(&g.o_full[0]);
-        umma_commit(&g.o_full[1]);
-        umma_commit(&g.done);
-        wait_inline(&g.done, 0, nullptr, st, KID_ATTN_FWD);
+        umma_commit_elected(&g.s_full[i], elected);
+      };
+      int pn[2] = {0, 0};   // products with v so far
+      bool ok = kt0 != INT_MAX && wait(&g.q_full, 0) && wait(&g.k_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        if (ra.has(kt0)) scores(0, 0);
+        if (rb.has(kt0)) scores(1, 0);
+        umma_commit_elected(&g.k_empty[0], elected);
       }
+      int n = 0;
+      for (int kt = kt0; ok && kt != INT_MAX; ++n) {
+        const int s = n % kStages, next = next_tile(ra, rb, kt + 1), s1 = (n + 1) % kStages;
+        ok = wait(&g.v_full[s], (n / kStages) & 1) && (next == INT_MAX || wait(&g.k_full[s1], ((n + 1) / kStages) & 1));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Range& r = i == 0 ? ra : rb;
+          if (ok && r.has(kt)) {
+            ok = wait(&g.p_full[i], pn[i] & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_bf16_ts(tmem + kRows + i * kDv, tmem + i * kTile + kk * 8, v0 + ((s * kVBytes + kk * 2048) >> 4), id_o, pn[i] > 0 || kk > 0,
+                           elected);
+            ++pn[i];
+          }
+          if (ok && next != INT_MAX && r.has(next)) scores(i, s1);
+        }
+        if (!ok) break;
+        umma_commit_elected(&g.v_empty[s], elected);
+        if (next != INT_MAX) umma_commit_elected(&g.k_empty[s1], elected);
+        kt = next;
+      }
+      umma_commit_elected(&g.o_full[0], elected);
+      umma_commit_elected(&g.o_full[1], elected);
+      umma_commit_elected(&g.done, elected);
+      wait_inline(&g.done, 0, nullptr, st, KID_ATTN_FWD);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
