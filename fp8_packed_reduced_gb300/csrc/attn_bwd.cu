@@ -11,7 +11,7 @@ namespace qkvp {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 320;                // eight computing warps, a loading and an issuing one
+constexpr int kThreads = 352;                // eight computing warps, a loading and two issuing ones
 constexpr int kStages = 2;
 constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
 constexpr int kFull = 2 * kBox;              // of 128 rows x up to 128 columns
@@ -23,7 +23,7 @@ constexpr int kScores = 0, kDp = 128, kAcc0 = 256, kAcc1 = 384, kOpQ = 384, kOpD
 
 struct Shared {
   uint64_t fixed_full, a_full[kStages], a_empty[kStages], b_full[kStages], b_empty[kStages];
-  uint64_t s_full, dp_full, s_free, p_full, ds_full, acc_full, done;
+  uint64_t s_full, dp_full, s_free, p_full, ds_full, acc_full;
   uint32_t tmem;
   int abort;
   int lo[4], hi[4], start[4];
@@ -32,22 +32,22 @@ struct Shared {
   alignas(128) float2 row[kStages][kTile];   // lse (base 2) and delta of a tile of queries, in pairs
 };
 
-__device__ __forceinline__ void init_barriers(Shared& g) {
+// b_users: issuing warps that release a stage of b.
+__device__ __forceinline__ void init_barriers(Shared& g, int b_users) {
   g.abort = 0;
   mbar_init(&g.fixed_full, 1);
   for (int s = 0; s < kStages; ++s) {
     mbar_init(&g.a_full[s], 1);
     mbar_init(&g.a_empty[s], 1);
     mbar_init(&g.b_full[s], 1);
-    mbar_init(&g.b_empty[s], 1);
+    mbar_init(&g.b_empty[s], b_users);
   }
   mbar_init(&g.s_full, 1);
   mbar_init(&g.dp_full, 1);
   mbar_init(&g.s_free, 8);
   mbar_init(&g.p_full, 8);
   mbar_init(&g.ds_full, 8);
-  mbar_init(&g.acc_full, 1);
-  mbar_init(&g.done, 1);
+  mbar_init(&g.acc_full, 2);
   fence_mbar_init();
 }
 // 8 warps of a group have done something to TMEM: arrive once per warp.
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sk = smem, *sv = sk + kStages * kFull;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) init_barriers(g);
+  if (threadIdx.x == 0) init_barriers(g, 1);
   if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
   if (warp == 9) {
     tmem_alloc(&g.tmem, 512);
@@ -181,61 +181,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
       }
     }
-  } else if (warp == 9) {
-    // The whole warp goes the same way (umma_bf16_ss says why).
+  } else if (warp >= 9) {
+    // One warp issues the scores, the other the rest: while one finds out what
+    // is ready, the products of the other run.  A whole warp goes the same way
+    // (umma_bf16_ss says why).
     constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_q = idesc_bf16_f32(kTile, D, true);
     const uint32_t elected = elect_one();
-    const uint64_t k0 = sdesc_k_sw128(smem_u32(sk)), v0 = sdesc_k_sw128(smem_u32(sv)), k0_mn = sdesc_sw128(smem_u32(sk), kBox, 1024);
     const auto wait = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DQ));
     };
-    const auto scores = [&](int s) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
-      umma_commit_elected(&g.s_full, elected);
-    };
-    const auto dps = [&](int s) {
-#pragma unroll
-      for (int kk = 0; kk < kDv / 16; ++kk)
-        umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, v0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
-      umma_commit_elected(&g.dp_full, elected);
-      umma_commit_elected(&g.b_empty[s], elected);
-    };
-    bool ok = kt0 < r.last && wait(&g.a_full[0], 0) && wait(&g.b_full[0], 0);
-    if (ok) {
-      tc_fence_after();
-      scores(0);
-      dps(0);
-    }
     int n = 0;
-    for (int kt = kt0; ok && kt < r.last; ++n) {
-      const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1, next = next_of(kt);
-      if (next < r.last) {
-        ok = wait(&g.a_full[s1], par1) && wait(&g.s_free, n & 1);
-        if (!ok) break;
+    if (warp == 9) {
+      const uint64_t k0 = sdesc_k_sw128(smem_u32(sk));
+      for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
+        const int s = n % kStages;
+        if (!wait(&g.a_full[s], (n / kStages) & 1) || (n > 0 && !wait(&g.s_free, (n - 1) & 1))) break;
         tc_fence_after();
-        scores(s1);
-      }
-      ok = wait(&g.ds_full, n & 1);
-      if (!ok) break;
-      tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0_mn + ((s * kFull + kk * 2048) >> 4), id_q, n > 0 || kk > 0,
-                     elected);
-      umma_commit_elected(&g.a_empty[s], elected);
-      if (next < r.last) {
-        ok = wait(&g.b_full[s1], par1);
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
+        umma_commit_elected(&g.s_full, elected);
+      }
+    } else {
+      const uint64_t v0 = sdesc_k_sw128(smem_u32(sv)), k0 = sdesc_sw128(smem_u32(sk), kBox, 1024);
+      const auto dps = [&](int s) {
+#pragma unroll
+        for (int kk = 0; kk < kDv / 16; ++kk)
+          umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, v0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
+        umma_commit_elected(&g.dp_full, elected);
+        umma_commit_elected(&g.b_empty[s], elected);
+      };
+      bool ok = kt0 < r.last && wait(&g.b_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        dps(0);
+      }
+      for (int kt = kt0; ok && kt < r.last; ++n) {
+        const int s = n % kStages, s1 = (n + 1) % kStages, next = next_of(kt);
+        ok = wait(&g.a_full[s], (n / kStages) & 1) && (next >= r.last || wait(&g.b_full[s1], ((n + 1) / kStages) & 1)) &&
+             wait(&g.ds_full, n & 1);
         if (!ok) break;
         tc_fence_after();
-        dps(s1);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0 + ((s * kFull + kk * 2048) >> 4), id_q, n > 0 || kk > 0,
+                       elected);
+        umma_commit_elected(&g.a_empty[s], elected);
+        if (next < r.last) dps(s1);
+        kt = next;
       }
-      kt = next;
     }
     umma_commit_elected(&g.acc_full, elected);
-    umma_commit_elected(&g.done, elected);
-    mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DQ);
+    mbar_wait(&g.acc_full, 0, nullptr, st, KID_ATTN_DQ);   // all products are done
   } else {
     // this thread's row, and the half of the keys that its warpgroup takes
     const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;
@@ -359,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sk = smem, *sv = sk + kFull, *sq = sv + kFull, *sd = sq + kStages * kFull;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) init_barriers(g);
+  if (threadIdx.x == 0) init_barriers(g, 2);
   if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
   if (warp == 9) {
     tmem_alloc(&g.tmem, 512);
@@ -413,72 +410,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DKV);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp >= 9) {
+    // As for dq: one warp issues dv and the scores, the other dk and dP.
     constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_k = idesc_bf16_f32(kTile, D, true),
                        id_v = idesc_bf16_f32(kTile, kDv, true);
     const uint32_t elected = elect_one();
-    const uint64_t k0 = sdesc_k_sw128(smem_u32(sk)), v0 = sdesc_k_sw128(smem_u32(sv)), q0 = sdesc_k_sw128(smem_u32(sq)),
-                   d0 = sdesc_k_sw128(smem_u32(sd)), q0_mn = sdesc_sw128(smem_u32(sq), kBox, 1024),
-                   d0_mn = sdesc_sw128(smem_u32(sd), kBox, 1024);
     const auto wait = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DKV));
     };
-    const auto scores = [&](int s) {
+    bool ok = count > 0 && wait(&g.fixed_full, 0);
+    if (warp == 9) {
+      const uint64_t k0 = sdesc_k_sw128(smem_u32(sk)), q0 = sdesc_k_sw128(smem_u32(sq)), d0 = sdesc_sw128(smem_u32(sd), kBox, 1024);
+      const auto scores = [&](int s) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-        umma_bf16_ss(tmem + kScores, k0 + (at >> 4), q0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+          umma_bf16_ss(tmem + kScores, k0 + (at >> 4), q0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
+        }
+        umma_commit_elected(&g.s_full, elected);
+      };
+      ok = ok && wait(&g.a_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        scores(0);
       }
-      umma_commit_elected(&g.s_full, elected);
-    };
-    const auto dps = [&](int s) {
-#pragma unroll
-      for (int kk = 0; kk < kDv / 16; ++kk) {
-        const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-        umma_bf16_ss(tmem + kDp, v0 + (at >> 4), d0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
-      }
-      umma_commit_elected(&g.dp_full, elected);
-    };
-    bool ok = count > 0 && wait(&g.fixed_full, 0) && wait(&g.a_full[0], 0) && wait(&g.b_full[0], 0);
-    if (ok) {
-      tc_fence_after();
-      scores(0);
-      dps(0);
-    }
-    for (int n = 0; ok && n < count; ++n) {
-      const int s = n % kStages, s1 = (n + 1) % kStages, par1 = ((n + 1) / kStages) & 1;
-      ok = wait(&g.p_full, n & 1);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0_mn + ((s * kFull + kk * 2048) >> 4), id_v, n > 0 || kk > 0,
-                     elected);
-      umma_commit_elected(&g.b_empty[s], elected);
-      if (n + 1 < count) {
-        ok = wait(&g.a_full[s1], par1);
+      for (int n = 0; ok && n < count; ++n) {
+        const int s = n % kStages, s1 = (n + 1) % kStages;
+        ok = wait(&g.b_full[s], (n / kStages) & 1) && (n + 1 == count || wait(&g.a_full[s1], ((n + 1) / kStages) & 1)) &&
+             wait(&g.p_full, n & 1);
         if (!ok) break;
         tc_fence_after();
-        scores(s1);
-      }
-      ok = wait(&g.ds_full, n & 1);
-      if (!ok) break;
-      tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0_mn + ((s * kFull + kk * 2048) >> 4), id_k, n > 0 || kk > 0,
-                     elected);
-      umma_commit_elected(&g.a_empty[s], elected);
-      if (n + 1 < count) {
-        ok = wait(&g.b_full[s1], par1);
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0 + ((s * kFull + kk * 2048) >> 4), id_v, n > 0 || kk > 0,
+                       elected);
+        umma_commit_elected(&g.b_empty[s], elected);
+        if (n + 1 < count) scores(s1);
+      }
+    } else {
+      const uint64_t v0 = sdesc_k_sw128(smem_u32(sv)), d0 = sdesc_k_sw128(smem_u32(sd)), q0 = sdesc_sw128(smem_u32(sq), kBox, 1024);
+      const auto dps = [&](int s) {
+#pragma unroll
+        for (int kk = 0; kk < kDv / 16; ++kk) {
+          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
+          umma_bf16_ss(tmem + kDp, v0 + (at >> 4), d0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
+        }
+        umma_commit_elected(&g.dp_full, elected);
+        umma_commit_elected(&g.b_empty[s], elected);
+      };
+      ok = ok && wait(&g.b_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        dps(0);
+      }
+      for (int n = 0; ok && n < count; ++n) {
+        const int s = n % kStages, s1 = (n + 1) % kStages;
+        ok = wait(&g.a_full[s], (n / kStages) & 1) && (n + 1 == count || wait(&g.b_full[s1], ((n + 1) / kStages) & 1)) &&
+             wait(&g.ds_full, n & 1);
         if (!ok) break;
         tc_fence_after();
-        dps(s1);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0 + ((s * kFull + kk * 2048) >> 4), id_k, n > 0 || kk > 0,
+                       elected);
+        umma_commit_elected(&g.a_empty[s], elected);
+        if (n + 1 < count) dps(s1);
       }
     }
     umma_commit_elected(&g.acc_full, elected);
-    umma_commit_elected(&g.done, elected);
-    mbar_wait(&g.done, 0, nullptr, st, KID_ATTN_DKV);
+    mbar_wait(&g.acc_full, 0, nullptr, st, KID_ATTN_DKV);   // all products are done
   } else {
     // this thread's key, and the half of the queries that its warpgroup takes
     const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;

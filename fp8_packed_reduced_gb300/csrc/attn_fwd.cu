@@ -9,8 +9,8 @@ namespace {
 
 constexpr int kTile = 128;                   // query rows of an accumulator, keys of a step
 constexpr int kRows = 2 * kTile;             // query rows of a block
-constexpr int kThreads = 384;                // two softmax warpgroups; a loading and an issuing warp, and two that only give
-                                             // their registers: 384 x 168 = 2 x 128 x 224 + 128 x 56
+constexpr int kThreads = 384;                // two softmax warpgroups; a loading warp, an issuing one for each query tile,
+                                             // and one that only gives its registers: 384 x 168 = 2 x 128 x 216 + 128 x 72
 constexpr int kStages = 2;
 constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
 constexpr int kQBytes = 2 * kBox;            // of one query tile; the output's staging afterwards
@@ -21,7 +21,7 @@ constexpr float kSlack = 8.f;                // powers of two by which scores ma
 
 struct Shared {
   uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], done;
+  uint64_t s_full[2], p_full[2][2], o_full[2];   // (probabilities in two halves)
   uint32_t tmem;
   int abort;
   int lo[2][4], hi[2][4], start[2][4];
@@ -56,16 +56,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&g.q_full, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&g.k_full[s], 1);
-      mbar_init(&g.k_empty[s], 1);
+      mbar_init(&g.k_empty[s], 2);
       mbar_init(&g.v_full[s], 1);
-      mbar_init(&g.v_empty[s], 1);
+      mbar_init(&g.v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&g.s_full[t], 1);
-      mbar_init(&g.p_full[t], 4);
+      mbar_init(&g.p_full[t][0], 4);
+      mbar_init(&g.p_full[t][1], 4);
       mbar_init(&g.o_full[t], 1);
     }
-    mbar_init(&g.done, 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kt0 = next_tile(ra, rb, 0);
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
       if (lane == 0 && kt0 != INT_MAX) {
         const bool used[2] = {ra.first < ra.last, rb.first < rb.last};
@@ -126,61 +126,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_inline(&g.v_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
         }
       }
-    } else if (warp == 9) {
-      // The whole warp goes the same way (umma_bf16_ss says why).
+    } else if (warp < 11) {
+      // One warp for each query tile: while one finds out what is ready, the
+      // products of the other run (few are queued ahead, so one warp's waits
+      // would be the tensor cores' too).  A whole warp goes the same way
+      // (umma_bf16_ss says why).
+      const int i = warp - 9;
       constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_o = idesc_bf16_f32(kTile, kDv, true);
-      const uint32_t elected = elect_one();
-      const uint64_t q0 = sdesc_k_sw128(smem_u32(sq)), k0 = sdesc_k_sw128(smem_u32(sk)), v0 = sdesc_sw128(smem_u32(sv), kBox, 1024);
+      const uint32_t elected = elect_one(), ts = tmem + i * kTile, to = tmem + kRows + i * kDv;
+      const uint64_t q0 = sdesc_k_sw128(smem_u32(sq) + i * kQBytes), k0 = sdesc_k_sw128(smem_u32(sk)),
+                     v0 = sdesc_sw128(smem_u32(sv), kBox, 1024);
       const auto wait = [&](uint64_t* bar, uint32_t par) {
         return __all_sync(0xffffffffu, wait_inline(bar, par, &g.abort, st, KID_ATTN_FWD));
       };
-      const auto scores = [&](int i, int s) {
+      const auto scores = [&](int s) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-          umma_bf16_ss(tmem + i * kTile, q0 + ((i * kQBytes + at) >> 4), k0 + ((s * kKBytes + at) >> 4), id_s, kk > 0, elected);
+          umma_bf16_ss(ts, q0 + (at >> 4), k0 + ((s * kKBytes + at) >> 4), id_s, kk > 0, elected);
         }
         umma_commit_elected(&g.s_full[i], elected);
       };
-      int pn[2] = {0, 0};   // products with v so far
+      const Range mine = g.range[i];
+      int done = 0;   // products with v so far
       bool ok = kt0 != INT_MAX && wait(&g.q_full, 0) && wait(&g.k_full[0], 0);
       if (ok) {
         tc_fence_after();
-        if (ra.has(kt0)) scores(0, 0);
-        if (rb.has(kt0)) scores(1, 0);
+        if (mine.has(kt0)) scores(0);
         umma_commit_elected(&g.k_empty[0], elected);
       }
       int n = 0;
       for (int kt = kt0; ok && kt != INT_MAX; ++n) {
         const int s = n % kStages, next = next_tile(ra, rb, kt + 1), s1 = (n + 1) % kStages;
+        const bool now = mine.has(kt), then = next != INT_MAX && mine.has(next);
         ok = wait(&g.v_full[s], (n / kStages) & 1) && (next == INT_MAX || wait(&g.k_full[s1], ((n + 1) / kStages) & 1));
+        if (!ok) break;
+        if (now) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Range& r = i == 0 ? ra : rb;
-          if (ok && r.has(kt)) {
-            ok = wait(&g.p_full[i], pn[i] & 1);
+          for (int half = 0; half < 2; ++half) {
+            ok = wait(&g.p_full[i][half], done & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_bf16_ts(tmem + kRows + i * kDv, tmem + i * kTile + kk * 8, v0 + ((s * kVBytes + kk * 2048) >> 4), id_o, pn[i] > 0 || kk > 0,
-                           elected);
-            ++pn[i];
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              umma_bf16_ts(to, ts + kk * 8, v0 + ((s * kVBytes + kk * 2048) >> 4), id_o, done > 0 || kk > 0, elected);
           }
-          if (ok && next != INT_MAX && r.has(next)) scores(i, s1);
+          if (!ok) break;
+          ++done;
         }
-        if (!ok) break;
+        if (then) scores(s1);
         umma_commit_elected(&g.v_empty[s], elected);
         if (next != INT_MAX) umma_commit_elected(&g.k_empty[s1], elected);
         kt = next;
       }
-      umma_commit_elected(&g.o_full[0], elected);
-      umma_commit_elected(&g.o_full[1], elected);
-      umma_commit_elected(&g.done, elected);
-      wait_inline(&g.done, 0, nullptr, st, KID_ATTN_FWD);
+      umma_commit_elected(&g.o_full[i], elected);
+      wait_inline(&g.o_full[i], 0, nullptr, st, KID_ATTN_FWD);   // all of the warp's products are done
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const Range r = t == 0 ? ra : rb;
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kTile + quarter, to = tmem + kRows + t * kDv + quarter;
@@ -208,9 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) x[32 * c + i] = see >> i & 1 ? x[32 * c + i] : 0xFF800000u;
         }
       }
-      float top = -INFINITY;
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < kTile; i += 2) top = fmax3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      for (int i = 0; i < kTile; i += 2) tops[i / 2 % 4] = fmax3(tops[i / 2 % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      const float top = fmax3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
       // A maximum that grows by little stays: its probabilities are at most 2^8.
       const bool grows = top > m && (top - m) * p.scale_log2 > kSlack;
       if (__any_sync(0xffffffffu, grows)) {
@@ -245,13 +249,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[i] = pack_bf16x2(a, b);
         }
         tmem_st16(ts + 16 * c, w);
+        if (c & 1) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&g.p_full[t][c >> 1]);
+        }
       }
       const float2 part = f2_split(sum);
       l += part.x + part.y;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&g.p_full[t]);
     }
     if (ok) ok = wait_inline(&g.o_full[t], 0, &g.abort, st, KID_ATTN_FWD);
     if (ok) {
