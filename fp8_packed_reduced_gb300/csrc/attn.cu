@@ -9,7 +9,7 @@ namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t order_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Tp) / kAttnTile * sizeof(int) + 255) / 256 * 256; }
-size_t stat_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Hq) * a.Tp * sizeof(float2) + 255) / 256 * 256; }
+size_t stat_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Hq) * a.Tp * 2 * sizeof(float) + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -100,7 +100,7 @@ int qkvp_attention_backward(const qkvp_attention* at, const uint16_t* da, const 
   uint8_t* w = static_cast<uint8_t*>(ws) + kAttnHeaderBytes;
   p.order[0] = reinterpret_cast<int*>(w);
   p.order[1] = reinterpret_cast<int*>(w + order_bytes(p));
-  p.stat = reinterpret_cast<float2*>(w + 2 * order_bytes(p));
+  p.stat = reinterpret_cast<float*>(w + 2 * order_bytes(p));
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;

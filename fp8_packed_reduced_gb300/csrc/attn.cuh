@@ -28,7 +28,7 @@ struct AttnArgs {
   float* lse;                // [Hq, T], natural logarithm
   const uint16_t* da;        // [T, Hq * 128]
   int Tp;                    // T rounded up to whole tiles
-  float2* stat;              // [Hq, Tp] lse in base 2 (+inf: no weight), da . a
+  float* stat;               // [Hq, 2, Tp] -lse in base 2 (-inf: no weight), -da . a
   uint16_t *dq, *dk, *dv;
   int* order[2];             // tiles from the longest on (backward: of dq, of dk and dv), or null: as they come
 };
@@ -240,9 +240,9 @@ __device__ __forceinline__ float2 pair_grad(const AttnArgs& p, int i, int j, int
   const int64_t ri = static_cast<int64_t>(hq) * p.T + i, rj = static_cast<int64_t>(h) * p.T + j;
   const float x = p.scale_log2 * row_dot<D>(p.q + ri * D, p.k + rj * D);
   const float dp = row_dot<kDv>(p.da + (static_cast<int64_t>(i) * p.Hq + hq) * kDv, p.v + rj * kDv);
-  const float2 s = __ldcg(p.stat + static_cast<int64_t>(hq) * p.Tp + i);
-  const float w = ex2(x - s.x);
-  return make_float2(w, alone ? 0.f : w * (dp - s.y));
+  const float* s = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + i;
+  const float w = ex2(x + __ldcg(s));
+  return make_float2(w, alone ? 0.f : w * (dp + __ldcg(s + p.Tp)));
 }
 
 template <int D>

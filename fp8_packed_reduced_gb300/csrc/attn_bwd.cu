@@ -12,31 +12,35 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kThreads = 352;                // eight computing warps, a loading and two issuing ones
-constexpr int kStages = 2;
+constexpr int kMaxStages = 4;
 constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
 constexpr int kFull = 2 * kBox;              // of 128 rows x up to 128 columns
 __host__ __device__ constexpr int boxes(int d) { return (d + 63) / 64; }
-__host__ __device__ constexpr int dq_smem(int) { return 1024 + 2 * kStages * kFull; }
-__host__ __device__ constexpr int dkv_smem(int) { return 1024 + 2 * kFull + 2 * kStages * kFull; }
+// A stage holds a tile of q or k and one of da or v; as many as fit.
+__host__ __device__ constexpr int stage_bytes(int d) { return boxes(d) * kBox + kFull; }
+__host__ __device__ constexpr int dq_stages(int d) { return d == 64 ? 4 : 3; }
+__host__ __device__ constexpr int dkv_stages(int d) { return d == 64 ? 3 : 2; }
+__host__ __device__ constexpr int dq_smem(int d) { return 1024 + dq_stages(d) * stage_bytes(d); }
+__host__ __device__ constexpr int dkv_smem(int d) { return 1024 + (1 + dkv_stages(d)) * stage_bytes(d); }
 // Columns of TMEM
 constexpr int kScores = 0, kDp = 128, kAcc0 = 256, kAcc1 = 384, kOpQ = 384, kOpDa = 448;
 
 struct Shared {
-  uint64_t fixed_full, a_full[kStages], a_empty[kStages], b_full[kStages], b_empty[kStages];
-  uint64_t s_full, dp_full, s_free, p_full, ds_full, acc_full;
+  uint64_t fixed_full, a_full[kMaxStages], a_empty[kMaxStages], b_full[kMaxStages], b_empty[kMaxStages];
+  uint64_t s_full, dp_full, s_free, p_full[2], ds_full[2], acc_full;   // (p and ds in two parts)
   uint32_t tmem;
   int abort;
   int lo[4], hi[4], start[4];
   uint32_t again[4];            // rows to be computed again
   Range range;
-  alignas(128) float2 row[kStages][kTile];   // lse (base 2) and delta of a tile of queries, in pairs
+  alignas(128) float stat[kMaxStages][2][kTile];   // -lse (base 2) and -delta of a tile of queries
 };
 
 // b_users: issuing warps that release a stage of b.
 __device__ __forceinline__ void init_barriers(Shared& g, int b_users) {
   g.abort = 0;
   mbar_init(&g.fixed_full, 1);
-  for (int s = 0; s < kStages; ++s) {
+  for (int s = 0; s < kMaxStages; ++s) {
     mbar_init(&g.a_full[s], 1);
     mbar_init(&g.a_empty[s], 1);
     mbar_init(&g.b_full[s], 1);
@@ -45,10 +49,16 @@ __device__ __forceinline__ void init_barriers(Shared& g, int b_users) {
   mbar_init(&g.s_full, 1);
   mbar_init(&g.dp_full, 1);
   mbar_init(&g.s_free, 8);
-  mbar_init(&g.p_full, 8);
-  mbar_init(&g.ds_full, 8);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&g.p_full[i], 8);
+    mbar_init(&g.ds_full[i], 8);
+  }
   mbar_init(&g.acc_full, 2);
   fence_mbar_init();
+}
+// Two pairs of floats of shared memory.
+__device__ __forceinline__ void lds_f2x2(uint32_t at, f2 (&z)[2]) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(z[0]), "=l"(z[1]) : "r"(at));
 }
 // 8 warps of a group have done something to TMEM: arrive once per warp.
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
@@ -58,8 +68,8 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
 }
 
 // delta = da . a of every row and head, and beside it the row's lse in base 2
-// (+inf where the row has no weight at all, so that its probabilities are 0).
-// A half warp a row, 16 rows a warp.  Its first blocks put the tiles of the two
+// (+inf where the row has no weight at all, so that its probabilities are 0), both
+// negative.  A half warp a row, 16 rows a warp.  Its first blocks put the tiles of the two
 // passes in order.
 constexpr int kPrepThreads = 256, kPrepRows = kPrepThreads / 32 * 16;
 static_assert(kPrepRows == kTile, "the statistics cover whole tiles");
@@ -92,7 +102,9 @@ __global__ void __launch_bounds__(kPrepThreads) delta_kernel(const __grid_consta
   const int row = r0 + 2 * c + half;
   if (c < 8) {
     const float z = row < p.T ? __ldg(p.lse + static_cast<int64_t>(hq) * p.T + row) : -INFINITY;
-    p.stat[static_cast<int64_t>(hq) * p.Tp + row] = make_float2(z == -INFINITY ? INFINITY : z * 1.4426950408889634f, mine);
+    float* to = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;
+    to[0] = z == -INFINITY ? -INFINITY : z * -1.4426950408889634f;
+    to[p.Tp] = -mine;
   }
 }
 
@@ -106,11 +118,11 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ AttnArgs p, DevStatus st) {
-  constexpr int KB = boxes(D), kKBytes = KB * kBox;
+  constexpr int KB = boxes(D), kKBytes = KB * kBox, kStages = dq_stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sk = smem, *sv = sk + kStages * kFull;
+  uint8_t *sk = smem, *sv = sk + kStages * kKBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) init_barriers(g, 1);
@@ -168,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = n % kStages, par = (n / kStages) & 1;
         if (!mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) break;
         mbar_arrive_expect_tx(&g.a_full[s], kKBytes);
-        for (int b = 0; b < KB; ++b) tma_load_3d(sk + s * kFull + b * kBox, &tm_k, &g.a_full[s], b * 64, kt * kTile, h);
+        for (int b = 0; b < KB; ++b) tma_load_3d(sk + s * kKBytes + b * kBox, &tm_k, &g.a_full[s], b * 64, kt * kTile, h);
         if (!mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) {
           mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DQ);
           break;
@@ -199,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
+          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kKBytes + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
         umma_commit_elected(&g.s_full, elected);
       }
     } else {
@@ -219,13 +231,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kt = kt0; ok && kt < r.last; ++n) {
         const int s = n % kStages, s1 = (n + 1) % kStages, next = next_of(kt);
         ok = wait(&g.a_full[s], (n / kStages) & 1) && (next >= r.last || wait(&g.b_full[s1], ((n + 1) / kStages) & 1)) &&
-             wait(&g.ds_full, n & 1);
+             wait(&g.ds_full[0], n & 1);
         if (!ok) break;
-        tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0 + ((s * kFull + kk * 2048) >> 4), id_q, n > 0 || kk > 0,
-                       elected);
+        for (int part = 0; part < 2; ++part) {
+          if (part == 1) ok = wait(&g.ds_full[1], n & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {   // 32 keys of each half
+            const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
+            umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0 + ((s * kKBytes + kk * 2048) >> 4), id_q,
+                         n > 0 || part > 0 || i > 0, elected);
+          }
+        }
+        if (!ok) break;
         umma_commit_elected(&g.a_empty[s], elected);
         if (next < r.last) dps(s1);
         kt = next;
@@ -236,9 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // this thread's row, and the half of the keys that its warpgroup takes
     const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;
-    const float2 stat = row < p.T ? __ldcg(p.stat + static_cast<int64_t>(hq) * p.Tp + row) : make_float2(INFINITY, 0.f);
+    const float* stat = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;   // (row < Tp)
+    const float z0 = __ldcg(stat), delta = __ldcg(stat + p.Tp);
     const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
-    const f2 sc = f2_make(p.scale_log2, p.scale_log2), mz = f2_make(-stat.x, -stat.x), md = f2_make(-stat.y, -stat.y);
+    const f2 sc = f2_make(p.scale_log2, p.scale_log2), mz = f2_make(z0, z0), md = f2_make(delta, delta);
     bool ok = true;
     int n = 0;
     for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
@@ -261,28 +282,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DQ);
       if (!ok) break;
       tc_fence_after();
-      tmem_ld32(td, x);
-      tmem_ld32(td + 32, x + 32);
-      tmem_ld_wait();
-      uint32_t out[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const f2 d = f2_mul(f2_add(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), md), w[i]);
-        out[i] = f2_to_bf16x2(d);
-      }
-      if (!whole) {
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld32(td + 32 * c, x);
+        tmem_ld_wait();
+        uint32_t out[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 16; ++i)
+          out[i] = f2_to_bf16x2(f2_mul(f2_add(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), md), w[16 * c + i]));
+        if (!whole) {
           uint32_t see = 0;
           if (sp.start >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(sp.start, min(sink_end, row + 1), j0 + 32 * c);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            out[16 * c + i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+          for (int i = 0; i < 16; ++i) out[i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
         }
+        tmem_st16(td + 16 * c, out);   // over what this warp has read
+        tmem_st_wait();
+        arrive_warp(&g.ds_full[c]);
       }
-      tmem_st32(td, out);
-      tmem_st_wait();
-      arrive_warp(&g.ds_full);
     }
     if (ok) ok = mbar_wait(&g.acc_full, 0, &g.abort, st, KID_ATTN_DQ);
     if (ok) {
@@ -349,11 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                const __grid_constant__ AttnArgs p, DevStatus st) {
-  constexpr int KB = boxes(D), kKBytes = KB * kBox;
+  constexpr int KB = boxes(D), kKBytes = KB * kBox, kStages = dkv_stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sk = smem, *sv = sk + kFull, *sq = sv + kFull, *sd = sq + kStages * kFull;
+  uint8_t *sk = smem, *sv = sk + kKBytes, *sq = sv + kFull, *sd = sq + kStages * kKBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) init_barriers(g, 2);
@@ -394,9 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; n < count; ++n) {
         const int s = n % kStages, par = (n / kStages) & 1, hq = h * p.G + n / tiles, i0 = r0 + (n % tiles) * kTile;
         if (!mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DKV)) break;
-        mbar_arrive_expect_tx(&g.a_full[s], kKBytes + kTile * sizeof(float2));
-        for (int b = 0; b < KB; ++b) tma_load_3d(sq + s * kFull + b * kBox, &tm_q, &g.a_full[s], b * 64, i0, hq);
-        bulk_load(g.row[s], p.stat + static_cast<int64_t>(hq) * p.Tp + i0, kTile * sizeof(float2), &g.a_full[s]);
+        mbar_arrive_expect_tx(&g.a_full[s], kKBytes + sizeof(g.stat[0]));
+        for (int b = 0; b < KB; ++b) tma_load_3d(sq + s * kKBytes + b * kBox, &tm_q, &g.a_full[s], b * 64, i0, hq);
+        for (int b = 0; b < 2; ++b)
+          bulk_load(g.stat[s][b], p.stat + (static_cast<int64_t>(hq) * 2 + b) * p.Tp + i0, sizeof(g.stat[s][b]), &g.a_full[s]);
         if (!mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DKV)) {
           mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DKV);
           break;
@@ -425,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-          umma_bf16_ss(tmem + kScores, k0 + (at >> 4), q0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
+          umma_bf16_ss(tmem + kScores, k0 + (at >> 4), q0 + ((s * kKBytes + at) >> 4), id_s, kk > 0, elected);
         }
         umma_commit_elected(&g.s_full, elected);
       };
@@ -437,13 +455,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; ok && n < count; ++n) {
         const int s = n % kStages, s1 = (n + 1) % kStages;
         ok = wait(&g.b_full[s], (n / kStages) & 1) && (n + 1 == count || wait(&g.a_full[s1], ((n + 1) / kStages) & 1)) &&
-             wait(&g.p_full, n & 1);
+             wait(&g.p_full[0], n & 1);
         if (!ok) break;
-        tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0 + ((s * kFull + kk * 2048) >> 4), id_v, n > 0 || kk > 0,
-                       elected);
+        for (int part = 0; part < 2; ++part) {
+          if (part == 1) ok = wait(&g.p_full[1], n & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {   // 32 queries of each half
+            const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
+            umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0 + ((s * kFull + kk * 2048) >> 4), id_v,
+                         n > 0 || part > 0 || i > 0, elected);
+          }
+        }
+        if (!ok) break;
         umma_commit_elected(&g.b_empty[s], elected);
         if (n + 1 < count) scores(s1);
       }
@@ -466,13 +492,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; ok && n < count; ++n) {
         const int s = n % kStages, s1 = (n + 1) % kStages;
         ok = wait(&g.a_full[s], (n / kStages) & 1) && (n + 1 == count || wait(&g.b_full[s1], ((n + 1) / kStages) & 1)) &&
-             wait(&g.ds_full, n & 1);
+             wait(&g.ds_full[0], n & 1);
         if (!ok) break;
-        tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0 + ((s * kFull + kk * 2048) >> 4), id_k, n > 0 || kk > 0,
-                       elected);
+        for (int part = 0; part < 2; ++part) {
+          if (part == 1) ok = wait(&g.ds_full[1], n & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {   // 32 queries of each half
+            const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
+            umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0 + ((s * kKBytes + kk * 2048) >> 4), id_k,
+                         n > 0 || part > 0 || i > 0, elected);
+          }
+        }
+        if (!ok) break;
         umma_commit_elected(&g.a_empty[s], elected);
         if (n + 1 < count) dps(s1);
       }
@@ -489,56 +523,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait(&g.a_full[s], (n / kStages) & 1, &g.abort, st, KID_ATTN_DKV) && mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
       if (!ok) break;
       tc_fence_after();
-      const float4* stat = reinterpret_cast<const float4*>(&g.row[s][64 * half]);   // two queries an entry
+      const uint32_t stat = smem_u32(g.stat[s][0]) + 4 * 64 * half;
       const bool whole = __all_sync(0xffffffffu, i0 >= ds0 && i0 + 64 <= end);
       uint32_t x[64];
       tmem_ld32(ts, x);
       tmem_ld32(ts + 32, x + 32);
       tmem_ld_wait();
       f2 w[32];
-      uint32_t out[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float4 z = stat[i];
-        const float2 y = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, f2_make(-z.x, -z.z)));
-        w[i] = f2_make(ex2(y.x), ex2(y.y));
-        out[i] = f2_to_bf16x2(w[i]);
-      }
-      if (!whole) {
+      for (int c = 0; c < 2; ++c) {
+        uint32_t out[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 16; i += 2) {
+          f2 z[2];
+          lds_f2x2(stat + 128 * c + 8 * i, z);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int at = 16 * c + i + k;
+            const float2 y = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * at]), __uint_as_float(x[2 * at + 1])), sc, z[k]));
+            w[at] = f2_make(ex2(y.x), ex2(y.y));
+            out[i + k] = f2_to_bf16x2(w[at]);
+          }
+        }
+        if (!whole) {
           const uint32_t see = bits(begin, end, i0 + 32 * c);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            out[16 * c + i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+          for (int i = 0; i < 16; ++i) out[i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
         }
+        tmem_st16(ts + 16 * c, out);   // over what this warp has read
+        tmem_st_wait();
+        arrive_warp(&g.p_full[c]);
       }
-      tmem_st32(ts, out);
-      tmem_st_wait();
-      arrive_warp(&g.p_full);
       ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DKV);
       if (!ok) break;
       tc_fence_after();
-      tmem_ld32(td, x);
-      tmem_ld32(td + 32, x + 32);
-      tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float4 z = stat[i];
-        out[i] = f2_to_bf16x2(f2_mul(f2_sub(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2_make(z.y, z.w)), w[i]));
-      }
-      if (!whole) {
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld32(td + 32 * c, x);
+        tmem_ld_wait();
+        uint32_t out[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 16; i += 2) {
+          f2 z[2];
+          lds_f2x2(stat + 4 * kTile + 128 * c + 8 * i, z);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            out[i + k] = f2_to_bf16x2(f2_mul(f2_add(f2_make(__uint_as_float(x[2 * (i + k)]), __uint_as_float(x[2 * (i + k) + 1])), z[k]),
+                                             w[16 * c + i + k]));
+        }
+        if (!whole) {
           const uint32_t see = bits(ds0, end, i0 + 32 * c);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            out[16 * c + i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+          for (int i = 0; i < 16; ++i) out[i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
         }
+        tmem_st16(td + 16 * c, out);
+        tmem_st_wait();
+        arrive_warp(&g.ds_full[c]);
       }
-      tmem_st32(td, out);
-      tmem_st_wait();
-      arrive_warp(&g.ds_full);
     }
     if (ok) ok = mbar_wait(&g.acc_full, 0, &g.abort, st, KID_ATTN_DKV);
     if (ok) {
@@ -546,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one warpgroup writes dv, the other dk
       const int width = half == 0 ? kDv : D, nb = boxes(width);
       const float f = half == 0 ? 1.f : p.scale;
-      uint8_t* stage = (half == 0 ? sv : sk) + (warp & 3) * 8192;
+      uint8_t* stage = (half == 0 ? sv : sk) + (warp & 3) * nb * 4096;
       bool bad = false;
       for (int c = 0; c < 2 * nb; ++c) {
         uint32_t o[32];

@@ -11,16 +11,17 @@ constexpr int kTile = 128;                   // query rows of an accumulator, ke
 constexpr int kRows = 2 * kTile;             // query rows of a block
 constexpr int kThreads = 384;                // two softmax warpgroups; a loading warp, an issuing one for each query tile,
                                              // and one that only gives its registers: 384 x 168 = 2 x 128 x 216 + 128 x 72
-constexpr int kStages = 2;
+constexpr int kMaxStages = 3;
+__host__ __device__ constexpr int stages(int d) { return d == 64 ? 3 : 2; }   // as many as fit
 constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
 constexpr int kQBytes = 2 * kBox;            // of one query tile; the output's staging afterwards
 constexpr int kVBytes = 2 * kBox;
 __host__ __device__ constexpr int boxes(int d) { return (d + 63) / 64; }
-__host__ __device__ constexpr int smem_bytes(int d) { return 1024 + 2 * kQBytes + kStages * (boxes(d) * kBox + kVBytes); }
+__host__ __device__ constexpr int smem_bytes(int d) { return 1024 + 2 * kQBytes + stages(d) * (boxes(d) * kBox + kVBytes); }
 constexpr float kSlack = 8.f;                // powers of two by which scores may pass the maximum that they are relative to
 
 struct Shared {
-  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[2], p_full[2][2], o_full[2];   // (probabilities in two halves)
   uint32_t tmem;
   int abort;
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ AttnArgs p, DevStatus st) {
-  constexpr int KB = boxes(D), kKBytes = KB * kBox;
+  constexpr int KB = boxes(D), kKBytes = KB * kBox, kStages = stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
