@@ -17,6 +17,8 @@ namespace qkvp {
 
 enum AttnKernelId : int { KID_ATTN_FWD = 18, KID_ATTN_DELTA = 19, KID_ATTN_DQ = 20, KID_ATTN_DKV = 21 };
 
+constexpr int kAttnTile = 128;   // query rows and keys of the products
+
 struct AttnArgs {
   int T, Hq, H, G, d;        // G = Hq / H
   int B;                     // sequences
@@ -33,6 +35,27 @@ struct AttnArgs {
   int* order[2];             // tiles from the longest on (backward: of dq, of dk and dv), or null: as they come
 };
 
+// A tile of kAttnTile rows of q or k in shared memory: boxes of 64 columns with
+// 128-byte swizzling, or for d = 96 three of 32 with 64-byte swizzling (a box of
+// the 32 columns that 64 leave would take a full one's room).  v and da are
+// those of 128 columns.
+template <int D>
+struct AttnTile {
+  static constexpr int kCols = D % 64 == 0 ? 64 : 32, kBoxes = D / kCols, kRowBytes = 2 * kCols;
+  static constexpr int kBox = kAttnTile * kRowBytes, kBytes = kBoxes * kBox;
+  static constexpr CUtensorMapSwizzle kSwizzle = kCols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  static __device__ __forceinline__ uint64_t desc(const void* p) {
+    return kCols == 64 ? sdesc_sw128(smem_u32(p), kBox, 8 * kRowBytes) : sdesc_sw64(smem_u32(p), kBox, 8 * kRowBytes);
+  }
+  // What moves a descriptor on by 16 columns (as K) or by 16 rows (as K).
+  static __host__ __device__ constexpr uint32_t cols16(int kk) { return (kk / (kCols / 16) * kBox + kk % (kCols / 16) * 32) >> 4; }
+  static __host__ __device__ constexpr uint32_t rows16(int kk) { return (kk * 16 * kRowBytes) >> 4; }
+  static __device__ __forceinline__ void load(uint8_t* to, const CUtensorMap* map, uint64_t* bar, int row, int head) {
+#pragma unroll
+    for (int b = 0; b < kBoxes; ++b) tma_load_3d(to + b * kBox, map, bar, b * kCols, row, head);
+  }
+};
+
 // Row and head of a block: the grid is tiles x heads, all heads of a tile next
 // to each other.
 struct Place {
@@ -42,8 +65,6 @@ __device__ __forceinline__ Place place_of(const int* order, int heads) {
   const int i = blockIdx.x / heads;
   return Place{order ? __ldcg(order + i) : i, static_cast<int>(blockIdx.x) - i * heads};
 }
-
-constexpr int kAttnTile = 128;   // query rows and keys of the products
 
 // A token's sequence, [start, end); start < 0: none.
 struct Span {

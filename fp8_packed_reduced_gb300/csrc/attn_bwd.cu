@@ -12,19 +12,25 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kThreads = 352;                // eight computing warps, a loading and two issuing ones
-constexpr int kMaxStages = 4;
 constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
-constexpr int kFull = 2 * kBox;              // of 128 rows x up to 128 columns
-__host__ __device__ constexpr int boxes(int d) { return (d + 63) / 64; }
-// A stage holds a tile of q or k and one of da or v; as many as fit.
-__host__ __device__ constexpr int stage_bytes(int d) { return boxes(d) * kBox + kFull; }
-__host__ __device__ constexpr int dq_stages(int d) { return d == 64 ? 4 : 3; }
-__host__ __device__ constexpr int dkv_stages(int d) { return d == 64 ? 3 : 2; }
-__host__ __device__ constexpr int dq_smem(int d) { return 1024 + dq_stages(d) * stage_bytes(d); }
-__host__ __device__ constexpr int dkv_smem(int d) { return 1024 + (1 + dkv_stages(d)) * stage_bytes(d); }
+using VTile = AttnTile<kDv>;                 // of v and da
+// Rings of tiles: in dq of k and v, in dk and dv of q and da.  As many stages as
+// fit; in dk and dv a tile of q is back in use sooner than one of da.
+__host__ __device__ constexpr int dq_stages(int d) { return d == 128 ? 3 : 4; }
+__host__ __device__ constexpr int q_stages(int d) { return d == 128 ? 2 : 4; }
+__host__ __device__ constexpr int da_stages(int d) { return d == 64 ? 3 : 2; }
+template <int D>
+constexpr int dq_smem() {
+  return 1024 + dq_stages(D) * (AttnTile<D>::kBytes + VTile::kBytes);
+}
+template <int D>
+constexpr int dkv_smem() {
+  return 1024 + (1 + q_stages(D)) * AttnTile<D>::kBytes + (1 + da_stages(D)) * VTile::kBytes;
+}
 // Columns of TMEM
 constexpr int kScores = 0, kDp = 128, kAcc0 = 256, kAcc1 = 384, kOpQ = 384, kOpDa = 448;
 
+constexpr int kMaxStages = 4;
 struct Shared {
   uint64_t fixed_full, a_full[kMaxStages], a_empty[kMaxStages], b_full[kMaxStages], b_empty[kMaxStages];
   uint64_t s_full, dp_full, s_free, p_full[2], ds_full[2], acc_full;   // (p and ds in two parts)
@@ -33,7 +39,6 @@ struct Shared {
   int lo[4], hi[4], start[4];
   uint32_t again[4];            // rows to be computed again
   Range range;
-  alignas(128) float stat[kMaxStages][2][kTile];   // -lse (base 2) and -delta of a tile of queries
 };
 
 // b_users: issuing warps that release a stage of b.
@@ -118,7 +123,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ AttnArgs p, DevStatus st) {
-  constexpr int KB = boxes(D), kKBytes = KB * kBox, kStages = dq_stages(D);
+  using KTile = AttnTile<D>;
+  constexpr int kKBytes = KTile::kBytes, kVBytes = VTile::kBytes, kStages = dq_stages(D), KB = (D + 63) / 64;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -180,13 +186,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = n % kStages, par = (n / kStages) & 1;
         if (!mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) break;
         mbar_arrive_expect_tx(&g.a_full[s], kKBytes);
-        for (int b = 0; b < KB; ++b) tma_load_3d(sk + s * kKBytes + b * kBox, &tm_k, &g.a_full[s], b * 64, kt * kTile, h);
+        KTile::load(sk + s * kKBytes, &tm_k, &g.a_full[s], kt * kTile, h);
         if (!mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) {
           mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DQ);
           break;
         }
-        mbar_arrive_expect_tx(&g.b_full[s], kFull);
-        for (int b = 0; b < 2; ++b) tma_load_3d(sv + s * kFull + b * kBox, &tm_v, &g.b_full[s], b * 64, kt * kTile, h);
+        mbar_arrive_expect_tx(&g.b_full[s], kVBytes);
+        VTile::load(sv + s * kVBytes, &tm_v, &g.b_full[s], kt * kTile, h);
       }
       for (int i = max(0, n - kStages); i < n; ++i) {   // every copy has landed before the block may leave
         mbar_wait(&g.a_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
@@ -204,22 +210,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int n = 0;
     if (warp == 9) {
-      const uint64_t k0 = sdesc_k_sw128(smem_u32(sk));
+      const uint64_t k0 = KTile::desc(sk);
       for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
         const int s = n % kStages;
         if (!wait(&g.a_full[s], (n / kStages) & 1) || (n > 0 && !wait(&g.s_free, (n - 1) & 1))) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kKBytes + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
+          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kKBytes) >> 4) + KTile::cols16(kk), id_s, kk > 0, elected);
         umma_commit_elected(&g.s_full, elected);
       }
     } else {
-      const uint64_t v0 = sdesc_k_sw128(smem_u32(sv)), k0 = sdesc_sw128(smem_u32(sk), kBox, 1024);
+      const uint64_t v0 = VTile::desc(sv), k0 = KTile::desc(sk);
       const auto dps = [&](int s) {
 #pragma unroll
         for (int kk = 0; kk < kDv / 16; ++kk)
-          umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, v0 + ((s * kFull + (kk / 4) * kBox + (kk % 4) * 32) >> 4), id_s, kk > 0, elected);
+          umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::cols16(kk), id_s, kk > 0, elected);
         umma_commit_elected(&g.dp_full, elected);
         umma_commit_elected(&g.b_empty[s], elected);
       };
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {   // 32 keys of each half
             const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
-            umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0 + ((s * kKBytes + kk * 2048) >> 4), id_q,
+            umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0 + ((s * kKBytes) >> 4) + KTile::rows16(kk), id_q,
                          n > 0 || part > 0 || i > 0, elected);
           }
         }
@@ -366,11 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                const __grid_constant__ AttnArgs p, DevStatus st) {
-  constexpr int KB = boxes(D), kKBytes = KB * kBox, kStages = dkv_stages(D);
+  using KTile = AttnTile<D>;
+  constexpr int kKBytes = KTile::kBytes, kVBytes = VTile::kBytes, SQ = q_stages(D), SD = da_stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
+  __shared__ alignas(128) float stats[SQ][2][kTile];   // -lse (base 2) and -delta of a tile of queries
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sk = smem, *sv = sk + kKBytes, *sq = sv + kFull, *sd = sq + kStages * kKBytes;
+  uint8_t *sk = smem, *sv = sk + kKBytes, *sq = sv + kVBytes, *sd = sq + SQ * kKBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) init_barriers(g, 2);
@@ -404,29 +412,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 8) {
     if (lane == 0 && count > 0) {
-      mbar_arrive_expect_tx(&g.fixed_full, kKBytes + kFull);
-      for (int b = 0; b < KB; ++b) tma_load_3d(sk + b * kBox, &tm_k, &g.fixed_full, b * 64, r0, h);
-      for (int b = 0; b < 2; ++b) tma_load_3d(sv + b * kBox, &tm_v, &g.fixed_full, b * 64, r0, h);
-      int n = 0;
-      for (; n < count; ++n) {
-        const int s = n % kStages, par = (n / kStages) & 1, hq = h * p.G + n / tiles, i0 = r0 + (n % tiles) * kTile;
-        if (!mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DKV)) break;
-        mbar_arrive_expect_tx(&g.a_full[s], kKBytes + sizeof(g.stat[0]));
-        for (int b = 0; b < KB; ++b) tma_load_3d(sq + s * kKBytes + b * kBox, &tm_q, &g.a_full[s], b * 64, i0, hq);
-        for (int b = 0; b < 2; ++b)
-          bulk_load(g.stat[s][b], p.stat + (static_cast<int64_t>(hq) * 2 + b) * p.Tp + i0, sizeof(g.stat[s][b]), &g.a_full[s]);
-        if (!mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DKV)) {
-          mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DKV);
-          break;
+      mbar_arrive_expect_tx(&g.fixed_full, kKBytes + kVBytes);
+      KTile::load(sk, &tm_k, &g.fixed_full, r0, h);
+      VTile::load(sv, &tm_v, &g.fixed_full, r0, h);
+      int na = 0, nb = 0;
+      for (; nb < count; ++nb) {
+        // da of this step behind q of it and of as many as there is room for
+        const int s = nb % SD, hq = h * p.G + nb / tiles, i0 = r0 + (nb % tiles) * kTile;
+        bool ok = true;
+        for (; na < count && na <= nb + (SQ - SD); ++na) {
+          const int sa = na % SQ, ha = h * p.G + na / tiles, ia = r0 + (na % tiles) * kTile;
+          ok = mbar_wait(&g.a_empty[sa], (na / SQ & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&g.a_full[sa], kKBytes + sizeof(stats[0]));
+          KTile::load(sq + sa * kKBytes, &tm_q, &g.a_full[sa], ia, ha);
+          for (int b = 0; b < 2; ++b)
+            bulk_load(stats[sa][b], p.stat + (static_cast<int64_t>(ha) * 2 + b) * p.Tp + ia, sizeof(stats[sa][b]), &g.a_full[sa]);
         }
-        mbar_arrive_expect_tx(&g.b_full[s], kFull);
-        for (int b = 0; b < 2; ++b) tma_load_2d(sd + s * kFull + b * kBox, &tm_da, &g.b_full[s], hq * kDv + b * 64, i0);
+        if (!ok || !mbar_wait(&g.b_empty[s], (nb / SD & 1) ^ 1, &g.abort, st, KID_ATTN_DKV)) break;
+        mbar_arrive_expect_tx(&g.b_full[s], kVBytes);
+        for (int b = 0; b < 2; ++b) tma_load_2d(sd + s * kVBytes + b * kBox, &tm_da, &g.b_full[s], hq * kDv + b * 64, i0);
       }
       mbar_wait(&g.fixed_full, 0, nullptr, st, KID_ATTN_DKV);
-      for (int i = max(0, n - kStages); i < n; ++i) {   // every copy has landed before the block may leave
-        mbar_wait(&g.a_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DKV);
-        mbar_wait(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DKV);
-      }
+      // every copy has landed before the block may leave
+      for (int i = max(0, na - SQ); i < na; ++i) mbar_wait(&g.a_full[i % SQ], (i / SQ) & 1, nullptr, st, KID_ATTN_DKV);
+      for (int i = max(0, nb - SD); i < nb; ++i) mbar_wait(&g.b_full[i % SD], (i / SD) & 1, nullptr, st, KID_ATTN_DKV);
     }
   } else if (warp >= 9) {
     // As for dq: one warp issues dv and the scores, the other dk and dP.
@@ -438,13 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = count > 0 && wait(&g.fixed_full, 0);
     if (warp == 9) {
-      const uint64_t k0 = sdesc_k_sw128(smem_u32(sk)), q0 = sdesc_k_sw128(smem_u32(sq)), d0 = sdesc_sw128(smem_u32(sd), kBox, 1024);
+      const uint64_t k0 = KTile::desc(sk), q0 = KTile::desc(sq), d0 = VTile::desc(sd);
       const auto scores = [&](int s) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-          umma_bf16_ss(tmem + kScores, k0 + (at >> 4), q0 + ((s * kKBytes + at) >> 4), id_s, kk > 0, elected);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_ss(tmem + kScores, k0 + KTile::cols16(kk), q0 + ((s * kKBytes) >> 4) + KTile::cols16(kk), id_s, kk > 0, elected);
         umma_commit_elected(&g.s_full, elected);
       };
       ok = ok && wait(&g.a_full[0], 0);
@@ -453,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         scores(0);
       }
       for (int n = 0; ok && n < count; ++n) {
-        const int s = n % kStages, s1 = (n + 1) % kStages;
-        ok = wait(&g.b_full[s], (n / kStages) & 1) && (n + 1 == count || wait(&g.a_full[s1], ((n + 1) / kStages) & 1)) &&
+        const int s = n % SD, s1 = (n + 1) % SQ;
+        ok = wait(&g.b_full[s], (n / SD) & 1) && (n + 1 == count || wait(&g.a_full[s1], ((n + 1) / SQ) & 1)) &&
              wait(&g.p_full[0], n & 1);
         if (!ok) break;
 #pragma unroll
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {   // 32 queries of each half
             const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
-            umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0 + ((s * kFull + kk * 2048) >> 4), id_v,
+            umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0 + ((s * kVBytes) >> 4) + VTile::rows16(kk), id_v,
                          n > 0 || part > 0 || i > 0, elected);
           }
         }
@@ -474,13 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n + 1 < count) scores(s1);
       }
     } else {
-      const uint64_t v0 = sdesc_k_sw128(smem_u32(sv)), d0 = sdesc_k_sw128(smem_u32(sd)), q0 = sdesc_sw128(smem_u32(sq), kBox, 1024);
+      const uint64_t v0 = VTile::desc(sv), d0 = VTile::desc(sd), q0 = KTile::desc(sq);
       const auto dps = [&](int s) {
 #pragma unroll
-        for (int kk = 0; kk < kDv / 16; ++kk) {
-          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-          umma_bf16_ss(tmem + kDp, v0 + (at >> 4), d0 + ((s * kFull + at) >> 4), id_s, kk > 0, elected);
-        }
+        for (int kk = 0; kk < kDv / 16; ++kk)
+          umma_bf16_ss(tmem + kDp, v0 + VTile::cols16(kk), d0 + ((s * kVBytes) >> 4) + VTile::cols16(kk), id_s, kk > 0, elected);
         umma_commit_elected(&g.dp_full, elected);
         umma_commit_elected(&g.b_empty[s], elected);
       };
@@ -490,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dps(0);
       }
       for (int n = 0; ok && n < count; ++n) {
-        const int s = n % kStages, s1 = (n + 1) % kStages;
-        ok = wait(&g.a_full[s], (n / kStages) & 1) && (n + 1 == count || wait(&g.b_full[s1], ((n + 1) / kStages) & 1)) &&
+        const int s = n % SQ, s1 = (n + 1) % SD;
+        ok = wait(&g.a_full[s], (n / SQ) & 1) && (n + 1 == count || wait(&g.b_full[s1], ((n + 1) / SD) & 1)) &&
              wait(&g.ds_full[0], n & 1);
         if (!ok) break;
 #pragma unroll
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {   // 32 queries of each half
             const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
-            umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0 + ((s * kKBytes + kk * 2048) >> 4), id_k,
+            umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0 + ((s * kKBytes) >> 4) + KTile::rows16(kk), id_k,
                          n > 0 || part > 0 || i > 0, elected);
           }
         }
@@ -519,11 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const f2 sc = f2_make(p.scale_log2, p.scale_log2);
     bool ok = true;
     for (int n = 0; n < count; ++n) {
-      const int s = n % kStages, i0 = r0 + (n % tiles) * kTile + 64 * half;
-      ok = mbar_wait(&g.a_full[s], (n / kStages) & 1, &g.abort, st, KID_ATTN_DKV) && mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+      const int s = n % SQ, i0 = r0 + (n % tiles) * kTile + 64 * half;
+      ok = mbar_wait(&g.a_full[s], (n / SQ) & 1, &g.abort, st, KID_ATTN_DKV) && mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t stat = smem_u32(g.stat[s][0]) + 4 * 64 * half;
+      const uint32_t stat = smem_u32(stats[s][0]) + 4 * 64 * half;
       const bool whole = __all_sync(0xffffffffu, i0 >= ds0 && i0 + 64 <= end);
       uint32_t x[64];
       tmem_ld32(ts, x);
@@ -585,9 +591,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       tc_fence_after();
       // one warpgroup writes dv, the other dk
-      const int width = half == 0 ? kDv : D, nb = boxes(width);
+      const int width = half == 0 ? kDv : D, nb = (width + 63) / 64;
       const float f = half == 0 ? 1.f : p.scale;
-      uint8_t* stage = (half == 0 ? sv : sk) + (warp & 3) * nb * 4096;
+      uint8_t* stage = (half == 0 ? sv : sq) + (warp & 3) * nb * 4096;
       bool bad = false;
       for (int c = 0; c < 2 * nb; ++c) {
         uint32_t o[32];
@@ -640,14 +646,16 @@ cudaError_t allow_smem(void (*kernel)(Args...), int bytes, std::atomic<bool> (&d
 template <int D>
 cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   static std::atomic<bool> ready[2][64];
-  cudaError_t e = allow_smem(dq_kernel<D>, dq_smem(D), ready[0]);
-  if (e == cudaSuccess) e = allow_smem(dkv_kernel<D>, dkv_smem(D), ready[1]);
+  cudaError_t e = allow_smem(dq_kernel<D>, dq_smem<D>(), ready[0]);
+  if (e == cudaSuccess) e = allow_smem(dkv_kernel<D>, dkv_smem<D>(), ready[1]);
   if (e != cudaSuccess) return e;
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  using KTile = AttnTile<D>;
   CUtensorMap q, k, v, da, dq, dk, dv;
-  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, 64, kTile, 1, sw) || !map3d(&k, bf16, 2, a.k, D, a.T, a.H, 64, kTile, 1, sw) ||
-      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, 64, kTile, 1, sw) ||
+  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, KTile::kCols, kTile, 1, KTile::kSwizzle) ||
+      !map3d(&k, bf16, 2, a.k, D, a.T, a.H, KTile::kCols, kTile, 1, KTile::kSwizzle) ||
+      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kTile, 1, VTile::kSwizzle) ||
       !map2d_bf16(&da, a.da, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, kTile) ||
       !map3d(&dq, bf16, 2, a.dq, D, a.T, a.Hq, 64, 32, 1, sw) || !map3d(&dk, bf16, 2, a.dk, D, a.T, a.H, 64, 32, 1, sw) ||
       !map3d(&dv, bf16, 2, a.dv, kDv, a.T, a.H, 64, 32, 1, sw))
@@ -657,9 +665,9 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   const unsigned prep = (a.order[0] ? 2 : 0) + static_cast<unsigned>(tiles) * a.Hq;
   e = launch_dependent(delta_kernel, dim3(prep), kPrepThreads, 0, s, a, tiles, st);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(dkv_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.H), kThreads, dkv_smem(D), s, q, da, k, v, dk, dv, a, st);
+  e = launch_dependent(dkv_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.H), kThreads, dkv_smem<D>(), s, q, da, k, v, dk, dv, a, st);
   if (e != cudaSuccess) return e;
-  return launch_dependent(dq_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.Hq), kThreads, dq_smem(D), s, k, v, dq, a, st);
+  return launch_dependent(dq_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.Hq), kThreads, dq_smem<D>(), s, k, v, dq, a, st);
 }
 
 }  // namespace

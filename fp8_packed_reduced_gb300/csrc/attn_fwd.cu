@@ -11,13 +11,13 @@ constexpr int kTile = 128;                   // query rows of an accumulator, ke
 constexpr int kRows = 2 * kTile;             // query rows of a block
 constexpr int kThreads = 384;                // two softmax warpgroups; a loading warp, an issuing one for each query tile,
                                              // and one that only gives its registers: 384 x 168 = 2 x 128 x 216 + 128 x 72
-constexpr int kMaxStages = 3;
-__host__ __device__ constexpr int stages(int d) { return d == 64 ? 3 : 2; }   // as many as fit
-constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
-constexpr int kQBytes = 2 * kBox;            // of one query tile; the output's staging afterwards
-constexpr int kVBytes = 2 * kBox;
-__host__ __device__ constexpr int boxes(int d) { return (d + 63) / 64; }
-__host__ __device__ constexpr int smem_bytes(int d) { return 1024 + 2 * kQBytes + stages(d) * (boxes(d) * kBox + kVBytes); }
+constexpr int kMaxStages = 4;
+__host__ __device__ constexpr int stages(int d) { return d == 64 ? 4 : d == 96 ? 3 : 2; }   // as many as fit
+using VTile = AttnTile<kDv>;
+template <int D>
+constexpr int smem_bytes() {
+  return 1024 + 2 * AttnTile<D>::kBytes + stages(D) * (AttnTile<D>::kBytes + VTile::kBytes);
+}
 constexpr float kSlack = 8.f;                // powers of two by which scores may pass the maximum that they are relative to
 
 struct Shared {
@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ AttnArgs p, DevStatus st) {
-  constexpr int KB = boxes(D), kKBytes = KB * kBox, kStages = stages(D);
+  using QTile = AttnTile<D>;
+  constexpr int kKBytes = QTile::kBytes, kVBytes = VTile::kBytes, kQBytes = kKBytes, kStages = stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -103,22 +104,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       if (lane == 0 && kt0 != INT_MAX) {
         const bool used[2] = {ra.first < ra.last, rb.first < rb.last};
-        mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * KB * kBox);
+        mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * kQBytes);
         for (int i = 0; i < 2; ++i)
-          if (used[i])
-            for (int b = 0; b < KB; ++b) tma_load_3d(sq + i * kQBytes + b * kBox, &tm_q, &g.q_full, b * 64, r0 + i * kTile, hq);
+          if (used[i]) QTile::load(sq + i * kQBytes, &tm_q, &g.q_full, r0 + i * kTile, hq);
         int n = 0;
         for (int kt = kt0; kt != INT_MAX; kt = next_tile(ra, rb, kt + 1), ++n) {
           const int s = n % kStages, par = (n / kStages) & 1;
           if (!wait_inline(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) break;
           mbar_arrive_expect_tx(&g.k_full[s], kKBytes);
-          for (int b = 0; b < KB; ++b) tma_load_3d(sk + s * kKBytes + b * kBox, &tm_k, &g.k_full[s], b * 64, kt * kTile, h);
+          QTile::load(sk + s * kKBytes, &tm_k, &g.k_full[s], kt * kTile, h);
           if (!wait_inline(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) {
             wait_inline(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
             break;
           }
           mbar_arrive_expect_tx(&g.v_full[s], kVBytes);
-          for (int b = 0; b < 2; ++b) tma_load_3d(sv + s * kVBytes + b * kBox, &tm_v, &g.v_full[s], b * 64, kt * kTile, h);
+          VTile::load(sv + s * kVBytes, &tm_v, &g.v_full[s], kt * kTile, h);
         }
         // every copy has landed before the block may leave
         wait_inline(&g.q_full, 0, nullptr, st, KID_ATTN_FWD);
@@ -135,17 +135,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = warp - 9;
       constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_o = idesc_bf16_f32(kTile, kDv, true);
       const uint32_t elected = elect_one(), ts = tmem + i * kTile, to = tmem + kRows + i * kDv;
-      const uint64_t q0 = sdesc_k_sw128(smem_u32(sq) + i * kQBytes), k0 = sdesc_k_sw128(smem_u32(sk)),
-                     v0 = sdesc_sw128(smem_u32(sv), kBox, 1024);
+      const uint64_t q0 = QTile::desc(sq + i * kQBytes), k0 = QTile::desc(sk), v0 = VTile::desc(sv);
       const auto wait = [&](uint64_t* bar, uint32_t par) {
         return __all_sync(0xffffffffu, wait_inline(bar, par, &g.abort, st, KID_ATTN_FWD));
       };
       const auto scores = [&](int s) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk / 4) * kBox + (kk % 4) * 32;
-          umma_bf16_ss(ts, q0 + (at >> 4), k0 + ((s * kKBytes + at) >> 4), id_s, kk > 0, elected);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_ss(ts, q0 + QTile::cols16(kk), k0 + ((s * kKBytes) >> 4) + QTile::cols16(kk), id_s, kk > 0, elected);
         umma_commit_elected(&g.s_full[i], elected);
       };
       const Range mine = g.range[i];
@@ -170,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              umma_bf16_ts(to, ts + kk * 8, v0 + ((s * kVBytes + kk * 2048) >> 4), id_o, done > 0 || kk > 0, elected);
+              umma_bf16_ts(to, ts + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::rows16(kk), id_o, done > 0 || kk > 0, elected);
           }
           if (!ok) break;
           ++done;
@@ -266,35 +263,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool none = l == 0.f;
       const float f = none ? 0.f : 1.f / l;
       bool bad = !(l < INFINITY);
-      uint8_t* stage = sq + t * kQBytes + (warp & 3) * 8192;   // two boxes of 32 rows x 64 columns
-      uint32_t o[32];
+      // one box of 32 rows x 64 columns after the other, in the place of q
+      uint8_t* stage = sq + t * kQBytes + (warp & 3) * (kQBytes / 4);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld32(to + 32 * c, o);
+      for (int b = 0; b < 2; ++b) {
+        uint32_t o[64];
+        tmem_ld32(to + 64 * b, o);
+        tmem_ld32(to + 64 * b + 32, o + 32);
         tmem_ld_wait();
+        if (b == 1) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+        }
         float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 64; i += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float a = __uint_as_float(o[i + 2 * k]) * f, b = __uint_as_float(o[i + 2 * k + 1]) * f;
-            big += fabsf(a) + fabsf(b);
-            w[k] = none ? 0u : pack_bf16x2(a, b);
+            const float a = __uint_as_float(o[i + 2 * k]) * f, c = __uint_as_float(o[i + 2 * k + 1]) * f;
+            big += fabsf(a) + fabsf(c);
+            w[k] = none ? 0u : pack_bf16x2(a, c);
           }
-          const int chunk = (c & 1) * 4 + i / 8;
-          *reinterpret_cast<uint4*>(stage + (c >> 1) * 4096 + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + lane * 128 + (((i / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         bad |= !(big < INFINITY);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && row < p.T) {
+          tma_store_2d(&tm_a, stage, hq * kDv + b * 64, row);
+          bulk_commit();
+        }
       }
-      if (row < p.T) p.lse[static_cast<int64_t>(hq) * p.T + row] = none ? -INFINITY : (finite_or_zero(m) * p.scale_log2 + log2f(l)) * 0.6931471805599453f;
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0 && row < p.T) {
-        for (int b = 0; b < 2; ++b) tma_store_2d(&tm_a, stage + b * 4096, hq * kDv + b * 64, row);
-        bulk_commit();
-        bulk_wait_all<0>();
-      }
+      if (row < p.T)
+        p.lse[static_cast<int64_t>(hq) * p.T + row] =
+            none ? -INFINITY : (finite_or_zero(m) * p.scale_log2 + log2f(l)) * 0.6931471805599453f;
+      if (lane == 0) bulk_wait_all<0>();
       __syncwarp();
       // A value that is not finite may come from what the row does not see
       // (0 * NaN): such rows are computed again from what they see.
@@ -320,7 +324,7 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(forward_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(D));
+    e = cudaFuncSetAttribute(forward_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
@@ -334,12 +338,13 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
     a.order[0] = nullptr;
   }
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  using QTile = AttnTile<D>;
   CUtensorMap q, k, v, o;
-  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, 64, kTile, 1, sw) || !map3d(&k, bf16, 2, a.k, D, a.T, a.H, 64, kTile, 1, sw) ||
-      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, 64, kTile, 1, sw) || !map2d_bf16(&o, a.a, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, 32))
+  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, QTile::kCols, kTile, 1, QTile::kSwizzle) ||
+      !map3d(&k, bf16, 2, a.k, D, a.T, a.H, QTile::kCols, kTile, 1, QTile::kSwizzle) ||
+      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kTile, 1, VTile::kSwizzle) || !map2d_bf16(&o, a.a, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, 32))
     return cudaErrorInvalidValue;
-  return launch_dependent(forward_kernel<D>, dim3(static_cast<unsigned>(blocks)), kThreads, smem_bytes(D), s, q, k, v, o, a, st);
+  return launch_dependent(forward_kernel<D>, dim3(static_cast<unsigned>(blocks)), kThreads, smem_bytes<D>(), s, q, k, v, o, a, st);
 }
 
 }  // namespace

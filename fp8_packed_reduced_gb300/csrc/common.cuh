@@ -407,6 +407,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn) {
   return idesc_e4m3_f32(M, N) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u);
 }
 
+// As sdesc_sw128 with 64-byte swizzling (layout 4): rows of 64 bytes.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (sdesc_sw128(saddr, lbo, sbo) & ~(uint64_t(7) << 61)) | uint64_t(4) << 61;
+}
+
 // Instruction descriptor as above with A and/or B read MN-major (bit 15 for
 // A, bit 16 for B; allowed for 8-bit operands).
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32_major(int M, int N, bool a_mn, bool b_mn) {
