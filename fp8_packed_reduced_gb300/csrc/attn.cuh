@@ -35,14 +35,14 @@ struct AttnArgs {
   int* order[2];             // tiles from the longest on (backward: of dq, of dk and dv), or null: as they come
 };
 
-// A tile of kAttnTile rows of q or k in shared memory: boxes of 64 columns with
+// A tile of ROWS rows of q or k in shared memory: boxes of 64 columns with
 // 128-byte swizzling, or for d = 96 three of 32 with 64-byte swizzling (a box of
 // the 32 columns that 64 leave would take a full one's room).  v and da are
 // those of 128 columns.
-template <int D>
+template <int D, int ROWS>
 struct AttnTile {
   static constexpr int kCols = D % 64 == 0 ? 64 : 32, kBoxes = D / kCols, kRowBytes = 2 * kCols;
-  static constexpr int kBox = kAttnTile * kRowBytes, kBytes = kBoxes * kBox;
+  static constexpr int kBox = ROWS * kRowBytes, kBytes = kBoxes * kBox;
   static constexpr CUtensorMapSwizzle kSwizzle = kCols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   static __device__ __forceinline__ uint64_t desc(const void* p) {
     return kCols == 64 ? sdesc_sw128(smem_u32(p), kBox, 8 * kRowBytes) : sdesc_sw64(smem_u32(p), kBox, 8 * kRowBytes);
@@ -98,7 +98,7 @@ __device__ __forceinline__ bool alone(const AttnArgs& p, int row, int start) {
   return row == start || (p.window == 1 && p.sinks == 0);
 }
 
-// Key tiles (of kAttnTile, on the grid of the packed rows) that a query tile needs:
+// Key tiles (of as many keys as a kernel takes at a time, on the grid of the packed rows) that a query tile needs:
 // those that hold its sequence's first tokens, and those from its window on.
 struct Range {
   int sink0, sink1, first, last;   // [sink0, sink1) and [first, last)
@@ -107,15 +107,16 @@ struct Range {
 
 // That of 128 query rows from what their four warps found: the first token of a
 // window, the last row, the first token of a sequence (INT_MAX, -1, INT_MAX: none).
+template <int KEYS>
 __device__ __forceinline__ Range range_of(const AttnArgs& p, const int (&lo)[4], const int (&hi)[4], const int (&start)[4]) {
   const int last = max(max(hi[0], hi[1]), max(hi[2], hi[3]));
   if (last < 0) return Range{0, 0, 0, 0};
   const int first = min(min(lo[0], lo[1]), min(lo[2], lo[3])), s0 = min(min(start[0], start[1]), min(start[2], start[3]));
   Range r;
-  r.first = first / kAttnTile;
-  r.last = last / kAttnTile + 1;
-  r.sink0 = s0 / kAttnTile;
-  r.sink1 = p.sinks ? min(r.first, (min(s0 + min(p.sinks, p.T), p.T) + kAttnTile - 1) / kAttnTile) : r.sink0;
+  r.first = first / KEYS;
+  r.last = last / KEYS + 1;
+  r.sink0 = s0 / KEYS;
+  r.sink1 = p.sinks ? min(r.first, (min(s0 + min(p.sinks, p.T), p.T) + KEYS - 1) / KEYS) : r.sink0;
   return r;
 }
 // Bits lo .. hi - 1 of the 32 from `base` on.

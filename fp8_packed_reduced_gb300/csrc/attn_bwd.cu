@@ -13,7 +13,7 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kThreads = 352;                // eight computing warps, a loading and two issuing ones
 constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
-using VTile = AttnTile<kDv>;                 // of v and da
+using VTile = AttnTile<kDv, kTile>;                 // of v and da
 // Rings of tiles: in dq of k and v, in dk and dv of q and da.  As many stages as
 // fit; in dk and dv a tile of q is back in use sooner than one of da.
 __host__ __device__ constexpr int dq_stages(int d) { return d == 128 ? 3 : 4; }
@@ -21,11 +21,11 @@ __host__ __device__ constexpr int q_stages(int d) { return d == 128 ? 2 : 4; }
 __host__ __device__ constexpr int da_stages(int d) { return d == 64 ? 3 : 2; }
 template <int D>
 constexpr int dq_smem() {
-  return 1024 + dq_stages(D) * (AttnTile<D>::kBytes + VTile::kBytes);
+  return 1024 + dq_stages(D) * (AttnTile<D, kTile>::kBytes + VTile::kBytes);
 }
 template <int D>
 constexpr int dkv_smem() {
-  return 1024 + (1 + q_stages(D)) * AttnTile<D>::kBytes + (1 + da_stages(D)) * VTile::kBytes;
+  return 1024 + (1 + q_stages(D)) * AttnTile<D, kTile>::kBytes + (1 + da_stages(D)) * VTile::kBytes;
 }
 // Columns of TMEM
 constexpr int kScores = 0, kDp = 128, kAcc0 = 256, kAcc1 = 384, kOpQ = 384, kOpDa = 448;
@@ -123,7 +123,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ AttnArgs p, DevStatus st) {
-  using KTile = AttnTile<D>;
+  using KTile = AttnTile<D, kTile>;
   constexpr int kKBytes = KTile::kBytes, kVBytes = VTile::kBytes, kStages = dq_stages(D), KB = (D + 63) / 64;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0) g.range = range_of(p, g.lo, g.hi, g.start);
+  if (threadIdx.x == 0) g.range = range_of<kTile>(p, g.lo, g.hi, g.start);
   const uint32_t tmem = g.tmem, quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
   if (warp < 8) {   // one half of the warps loads q, the other da
     const uint4* from = reinterpret_cast<const uint4*>(half == 0 ? p.q + (static_cast<int64_t>(hq) * p.T + row) * D
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                const __grid_constant__ AttnArgs p, DevStatus st) {
-  using KTile = AttnTile<D>;
+  using KTile = AttnTile<D, kTile>;
   constexpr int kKBytes = KTile::kBytes, kVBytes = VTile::kBytes, SQ = q_stages(D), SD = da_stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
@@ -651,7 +651,7 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  using KTile = AttnTile<D>;
+  using KTile = AttnTile<D, kTile>;
   CUtensorMap q, k, v, da, dq, dk, dv;
   if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, KTile::kCols, kTile, 1, KTile::kSwizzle) ||
       !map3d(&k, bf16, 2, a.k, D, a.T, a.H, KTile::kCols, kTile, 1, KTile::kSwizzle) ||

@@ -1,5 +1,20 @@
 // Causal attention over packed sequences, forward, on the 5th-generation tensor
 // cores (attn.cuh has the formulas).
+//
+// A block takes 256 query rows of a head, as two tiles of 128 that share its
+// keys, 80 at a time.  Per tile and step
+//   S = q k^T into TMEM; a softmax warpgroup, a row a thread, takes it into
+//   registers and writes P = 2^(S - m) as bf16 beside it; O += P v.
+// Scores and probabilities have places of their own (80 and 40 columns, with
+// the 128 of O twice in the 512 there are), so that S of the next step is formed
+// while this one's softmax runs: where P takes the place of S (steps of 128
+// keys fit then), each step waits for the round from P over the two products to
+// the next S.
+// Scores are relative to a maximum that is replaced only when it grows by more
+// than 2^8 (O is multiplied in TMEM then, which is rare): probabilities are at
+// most 2^8, and a bf16 holds them as exactly as those below one.  They are
+// rounded to bf16 (2^-8) for the product with v; the sum and lse use them
+// unrounded.
 #include <atomic>
 
 #include "attn.cuh"
@@ -7,22 +22,32 @@
 namespace qkvp {
 namespace {
 
-constexpr int kTile = 128;                   // query rows of an accumulator, keys of a step
-constexpr int kRows = 2 * kTile;             // query rows of a block
-constexpr int kThreads = 384;                // two softmax warpgroups; a loading warp, an issuing one for each query tile,
-                                             // and one that only gives its registers: 384 x 168 = 2 x 128 x 216 + 128 x 72
-constexpr int kMaxStages = 4;
-__host__ __device__ constexpr int stages(int d) { return d == 64 ? 4 : d == 96 ? 3 : 2; }   // as many as fit
-using VTile = AttnTile<kDv>;
+constexpr int kTile = kAttnTile;             // query rows of an accumulator
+constexpr int kRows = 2 * kTile;             // of a block
+constexpr int kKeys = 80;                    // of a step
+constexpr int kThreads = 384;                // two softmax warpgroups; a loading warp and three issuing ones
+constexpr float kSlack = 8.f;                // powers of two by which scores may pass the maximum that they are relative to
+template <int D>
+using QTile = AttnTile<D, kTile>;
+template <int D>
+using KTile = AttnTile<D, kKeys>;
+using VTile = AttnTile<kDv, kKeys>;
+constexpr int kMaxStages = 6;
+__host__ __device__ constexpr int stages(int d) { return d == 64 ? 6 : d == 96 ? 5 : 4; }   // as many as fit
 template <int D>
 constexpr int smem_bytes() {
-  return 1024 + 2 * AttnTile<D>::kBytes + stages(D) * (AttnTile<D>::kBytes + VTile::kBytes);
+  return 1024 + 2 * QTile<D>::kBytes + stages(D) * (KTile<D>::kBytes + VTile::kBytes);
 }
-constexpr float kSlack = 8.f;                // powers of two by which scores may pass the maximum that they are relative to
+// Columns of TMEM: scores and probabilities of the tiles, then their accumulators.
+__device__ constexpr uint32_t s_col(int t) { return t * (kKeys + kKeys / 2); }
+__device__ constexpr uint32_t p_col(int t) { return s_col(t) + kKeys; }
+__device__ constexpr uint32_t o_col(int t) { return 256 + t * kDv; }
+static_assert(p_col(1) + kKeys / 2 <= o_col(0), "scores reach into the accumulators");
 
 struct Shared {
   uint64_t q_full, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  uint64_t s_full[2], p_full[2][2], o_full[2];   // (probabilities in two halves)
+  uint64_t s_full[2], s_free[2], p_full[2], o_done[2];   // o_done: a step's product with v has been added
+  uint64_t end;                                          // all products are done
   uint32_t tmem;
   int abort;
   int lo[2][4], hi[2][4], start[2][4];
@@ -46,8 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ AttnArgs p, DevStatus st) {
-  using QTile = AttnTile<D>;
-  constexpr int kKBytes = QTile::kBytes, kVBytes = VTile::kBytes, kQBytes = kKBytes, kStages = stages(D);
+  constexpr int kQBytes = QTile<D>::kBytes, kKBytes = KTile<D>::kBytes, kVBytes = VTile::kBytes, kStages = stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -58,16 +82,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&g.q_full, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&g.k_full[s], 1);
-      mbar_init(&g.k_empty[s], 2);
+      mbar_init(&g.k_empty[s], 1);
       mbar_init(&g.v_full[s], 1);
       mbar_init(&g.v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&g.s_full[t], 1);
-      mbar_init(&g.p_full[t][0], 4);
-      mbar_init(&g.p_full[t][1], 4);
-      mbar_init(&g.o_full[t], 1);
+      mbar_init(&g.s_free[t], 4);
+      mbar_init(&g.p_full[t], 4);
+      mbar_init(&g.o_done[t], 1);
     }
+    mbar_init(&g.end, 3);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -91,133 +116,162 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) g.lo[t][warp & 3] = lo, g.hi[t][warp & 3] = hi, g.start[t][warp & 3] = s0;
   }
   __syncthreads();
-  if (threadIdx.x < 2) g.range[threadIdx.x] = range_of(p, g.lo[threadIdx.x], g.hi[threadIdx.x], g.start[threadIdx.x]);
+  if (threadIdx.x < 2)
+    g.range[threadIdx.x] = range_of<kKeys>(p, g.lo[threadIdx.x], g.hi[threadIdx.x], g.start[threadIdx.x]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Range &ra = g.range[0], &rb = g.range[1];
+  const Range ra = g.range[0], rb = g.range[1];
   const uint32_t tmem = g.tmem;
   const int kt0 = next_tile(ra, rb, 0);
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) {
-      if (lane == 0 && kt0 != INT_MAX) {
-        const bool used[2] = {ra.first < ra.last, rb.first < rb.last};
-        mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * kQBytes);
-        for (int i = 0; i < 2; ++i)
-          if (used[i]) QTile::load(sq + i * kQBytes, &tm_q, &g.q_full, r0 + i * kTile, hq);
-        int n = 0;
-        for (int kt = kt0; kt != INT_MAX; kt = next_tile(ra, rb, kt + 1), ++n) {
-          const int s = n % kStages, par = (n / kStages) & 1;
-          if (!wait_inline(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) break;
-          mbar_arrive_expect_tx(&g.k_full[s], kKBytes);
-          QTile::load(sk + s * kKBytes, &tm_k, &g.k_full[s], kt * kTile, h);
-          if (!wait_inline(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) {
-            wait_inline(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
-            break;
-          }
-          mbar_arrive_expect_tx(&g.v_full[s], kVBytes);
-          VTile::load(sv + s * kVBytes, &tm_v, &g.v_full[s], kt * kTile, h);
-        }
-        // every copy has landed before the block may leave
-        wait_inline(&g.q_full, 0, nullptr, st, KID_ATTN_FWD);
-        for (int i = max(0, n - kStages); i < n; ++i) {
-          wait_inline(&g.k_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
-          wait_inline(&g.v_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
-        }
-      }
-    } else if (warp < 11) {
-      // One warp for each query tile: while one finds out what is ready, the
-      // products of the other run (few are queued ahead, so one warp's waits
-      // would be the tensor cores' too).  A whole warp goes the same way
-      // (umma_bf16_ss says why).
-      const int i = warp - 9;
-      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_o = idesc_bf16_f32(kTile, kDv, true);
-      const uint32_t elected = elect_one(), ts = tmem + i * kTile, to = tmem + kRows + i * kDv;
-      const uint64_t q0 = QTile::desc(sq + i * kQBytes), k0 = QTile::desc(sk), v0 = VTile::desc(sv);
-      const auto wait = [&](uint64_t* bar, uint32_t par) {
-        return __all_sync(0xffffffffu, wait_inline(bar, par, &g.abort, st, KID_ATTN_FWD));
-      };
-      const auto scores = [&](int s) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ss(ts, q0 + QTile::cols16(kk), k0 + ((s * kKBytes) >> 4) + QTile::cols16(kk), id_s, kk > 0, elected);
-        umma_commit_elected(&g.s_full[i], elected);
-      };
-      const Range mine = g.range[i];
-      int done = 0;   // products with v so far
-      bool ok = kt0 != INT_MAX && wait(&g.q_full, 0) && wait(&g.k_full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        if (mine.has(kt0)) scores(0);
-        umma_commit_elected(&g.k_empty[0], elected);
-      }
+  if (warp == 8) {
+    if (lane == 0 && kt0 != INT_MAX) {
+      const bool used[2] = {ra.first < ra.last, rb.first < rb.last};
+      mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * kQBytes);
+      for (int i = 0; i < 2; ++i)
+        if (used[i]) QTile<D>::load(sq + i * kQBytes, &tm_q, &g.q_full, r0 + i * kTile, hq);
       int n = 0;
-      for (int kt = kt0; ok && kt != INT_MAX; ++n) {
-        const int s = n % kStages, next = next_tile(ra, rb, kt + 1), s1 = (n + 1) % kStages;
-        const bool now = mine.has(kt), then = next != INT_MAX && mine.has(next);
-        ok = wait(&g.v_full[s], (n / kStages) & 1) && (next == INT_MAX || wait(&g.k_full[s1], ((n + 1) / kStages) & 1));
-        if (!ok) break;
-        if (now) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = wait(&g.p_full[i][half], done & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              umma_bf16_ts(to, ts + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::rows16(kk), id_o, done > 0 || kk > 0, elected);
-          }
-          if (!ok) break;
-          ++done;
+      for (int kt = kt0; kt != INT_MAX; kt = next_tile(ra, rb, kt + 1), ++n) {
+        const int s = n % kStages, par = (n / kStages) & 1;
+        if (!wait_inline(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) break;
+        mbar_arrive_expect_tx(&g.k_full[s], kKBytes);
+        KTile<D>::load(sk + s * kKBytes, &tm_k, &g.k_full[s], kt * kKeys, h);
+        if (!wait_inline(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) {
+          wait_inline(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
+          break;
         }
-        if (then) scores(s1);
-        umma_commit_elected(&g.v_empty[s], elected);
-        if (next != INT_MAX) umma_commit_elected(&g.k_empty[s1], elected);
+        mbar_arrive_expect_tx(&g.v_full[s], kVBytes);
+        VTile::load(sv + s * kVBytes, &tm_v, &g.v_full[s], kt * kKeys, h);
+      }
+      // every copy has landed before the block may leave
+      wait_inline(&g.q_full, 0, nullptr, st, KID_ATTN_FWD);
+      for (int i = max(0, n - kStages); i < n; ++i) {
+        wait_inline(&g.k_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
+        wait_inline(&g.v_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
+      }
+    }
+  } else if (warp > 8) {
+    // One warp issues the scores of both tiles, and one for each tile the
+    // products with v: while one finds out what is ready, the products of the
+    // others run (few are queued ahead, so one warp's waits would be the tensor
+    // cores' too).  A whole warp goes the same way (umma_bf16_ss says why).
+    const uint32_t elected = elect_one();
+    const auto wait = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, wait_inline(bar, par, &g.abort, st, KID_ATTN_FWD));
+    };
+    if (warp == 9) {
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kKeys, false);
+      const uint64_t q0 = QTile<D>::desc(sq), k0 = KTile<D>::desc(sk);
+      int formed[2] = {0, 0};
+      bool ok = kt0 != INT_MAX && wait(&g.q_full, 0);
+      for (int kt = kt0, n = 0; ok && kt != INT_MAX; ++n) {
+        const int s = n % kStages, next = next_tile(ra, rb, kt + 1);
+        ok = wait(&g.k_full[s], (n / kStages) & 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || !(i == 0 ? ra : rb).has(kt)) continue;
+          ok = formed[i] == 0 || wait(&g.s_free[i], (formed[i] - 1) & 1);   // the last scores have been read
+          if (!ok) continue;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ss(tmem + s_col(i), q0 + ((i * kQBytes) >> 4) + QTile<D>::cols16(kk),
+                         k0 + ((s * kKBytes) >> 4) + KTile<D>::cols16(kk), id_s, kk > 0, elected);
+          umma_commit_elected(&g.s_full[i], elected);
+          ++formed[i];
+        }
+        umma_commit_elected(&g.k_empty[s], elected);
         kt = next;
       }
-      umma_commit_elected(&g.o_full[i], elected);
-      wait_inline(&g.o_full[i], 0, nullptr, st, KID_ATTN_FWD);   // all of the warp's products are done
+    } else {
+      const int i = warp - 10;
+      constexpr uint32_t id_o = idesc_bf16_f32(kTile, kDv, true);
+      const uint32_t tp = tmem + p_col(i), to = tmem + o_col(i);
+      const uint64_t v0 = VTile::desc(sv);
+      const Range mine = i == 0 ? ra : rb;
+      int added = 0;
+      bool ok = true;
+      for (int kt = kt0, n = 0; ok && kt != INT_MAX; ++n) {
+        const int s = n % kStages, next = next_tile(ra, rb, kt + 1);
+        ok = wait(&g.v_full[s], (n / kStages) & 1);   // (of a tile that only the other needs, too: its release counts both)
+        if (ok && mine.has(kt)) {
+          ok = wait(&g.p_full[i], added & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_bf16_ts(to, tp + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::rows16(kk), id_o, added > 0 || kk > 0, elected);
+          umma_commit_elected(&g.o_done[i], elected);
+          ++added;
+        }
+        umma_commit_elected(&g.v_empty[s], elected);
+        kt = next;
+      }
     }
+    umma_commit_elected(&g.end, elected);   // before the block leaves
+    wait_inline(&g.end, 0, nullptr, st, KID_ATTN_FWD);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const Range r = t == 0 ? ra : rb;
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + t * kTile + quarter, to = tmem + kRows + t * kDv + quarter;
+    const uint32_t ts = tmem + s_col(t) + quarter, tp = tmem + p_col(t) + quarter, to = tmem + o_col(t) + quarter;
+    const f2 sc = f2_make(p.scale_log2, p.scale_log2);
     float m = -INFINITY, l = 0.f;   // m: what the scores are relative to (raw)
     int n = 0;
     bool ok = true;
     const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
+    // key tiles that every row of the warp sees whole
+    const int whole0 = (min(__reduce_max_sync(0xffffffffu, seen0), INT_MAX - kKeys) + kKeys - 1) / kKeys;
+    const int whole1 = __reduce_min_sync(0xffffffffu, row + 1) / kKeys;
     for (int kt = r.sink0 < r.sink1 ? r.sink0 : r.first; kt < r.last; kt = kt + 1 == r.sink1 ? r.first : kt + 1, ++n) {
-      if (!wait_inline(&g.s_full[t], n & 1, &g.abort, st, KID_ATTN_FWD)) {
-        ok = false;
-        break;
-      }
+      ok = wait_inline(&g.s_full[t], n & 1, &g.abort, st, KID_ATTN_FWD);
+      if (!ok) break;
       tc_fence_after();
-      uint32_t x[kTile];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
+      uint32_t x[kKeys];
+      tmem_load<kKeys>(ts, x);
       tmem_ld_wait();
-      const int j0 = kt * kTile;
-      if (!__all_sync(0xffffffffu, sp.start >= 0 && j0 >= seen0 && j0 + kTile <= row + 1)) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&g.s_free[t]);
+      const int j0 = kt * kKeys;
+      if (kt < whole0 || kt >= whole1) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < (kKeys + 31) / 32; ++c) {
           uint32_t see = 0;
           if (sp.start >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(sp.start, min(sink_end, row + 1), j0 + 32 * c);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[32 * c + i] = see >> i & 1 ? x[32 * c + i] : 0xFF800000u;
+          for (int i = 0; i < 32 && 32 * c + i < kKeys; ++i) x[32 * c + i] = see >> i & 1 ? x[32 * c + i] : 0xFF800000u;
         }
       }
       float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < kTile; i += 2) tops[i / 2 % 4] = fmax3(tops[i / 2 % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      for (int i = 0; i < kKeys; i += 2)
+        tops[i / 2 % 4] = fmax3(tops[i / 2 % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
       const float top = fmax3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
-      // A maximum that grows by little stays: its probabilities are at most 2^8.
       const bool grows = top > m && (top - m) * p.scale_log2 > kSlack;
-      if (__any_sync(0xffffffffu, grows)) {
-        const float f = !grows ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
-        if (n > 0) {   // (the products before this step's scores are done)
+      const float f = !grows ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
+      if (grows) m = top;
+      l *= f;
+      const bool free = n == 0 || mbar_try_wait(&g.o_done[t], (n - 1) & 1);   // (looked at here, used below)
+      const float m2 = finite_or_zero(m) * p.scale_log2;
+      const f2 mm = f2_make(-m2, -m2);
+      f2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+      uint32_t w[kKeys / 2];
+#pragma unroll
+      for (int i = 0; i < kKeys / 2; ++i) {
+        const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mm));
+        const float a = ex2(z.x), b = ex2(z.y);
+        sum[i & 1] = f2_add(sum[i & 1], f2_make(a, b));
+        w[i] = pack_bf16x2(a, b);
+      }
+      const float2 part = f2_split(f2_add(sum[0], sum[1]));
+      l += part.x + part.y;
+      // the last step's product is done: its probabilities may go, and O may be multiplied
+      if (n > 0) {
+        ok = free || wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
+        if (!ok) break;
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
@@ -228,36 +282,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(to + 32 * c, o);
           }
         }
-        if (grows) {
-          l *= f;
-          m = top;
-        }
       }
-      const float m2 = finite_or_zero(m) * p.scale_log2;
-      const f2 sc = f2_make(p.scale_log2, p.scale_log2), mm = f2_make(-m2, -m2);
-      f2 sum = f2_make(0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1])), sc, mm));
-          const float a = ex2(z.x), b = ex2(z.y);
-          sum = f2_add(sum, f2_make(a, b));
-          w[i] = pack_bf16x2(a, b);
-        }
-        tmem_st16(ts + 16 * c, w);
-        if (c & 1) {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&g.p_full[t][c >> 1]);
-        }
-      }
-      const float2 part = f2_split(sum);
-      l += part.x + part.y;
+      tmem_store<kKeys / 2>(tp, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&g.p_full[t]);
     }
-    if (ok) ok = wait_inline(&g.o_full[t], 0, &g.abort, st, KID_ATTN_FWD);
+    if (ok && n > 0) ok = wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
     if (ok) {
       tc_fence_after();
       const bool none = l == 0.f;
@@ -268,8 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         uint32_t o[64];
-        tmem_ld32(to + 64 * b, o);
-        tmem_ld32(to + 64 * b + 32, o + 32);
+        tmem_load<64>(to + 64 * b, o);
         tmem_ld_wait();
         if (b == 1) {
           if (lane == 0) bulk_wait_read<0>();
@@ -338,11 +369,11 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
     a.order[0] = nullptr;
   }
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  using QTile = AttnTile<D>;
   CUtensorMap q, k, v, o;
-  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, QTile::kCols, kTile, 1, QTile::kSwizzle) ||
-      !map3d(&k, bf16, 2, a.k, D, a.T, a.H, QTile::kCols, kTile, 1, QTile::kSwizzle) ||
-      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kTile, 1, VTile::kSwizzle) || !map2d_bf16(&o, a.a, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, 32))
+  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, QTile<D>::kCols, kTile, 1, QTile<D>::kSwizzle) ||
+      !map3d(&k, bf16, 2, a.k, D, a.T, a.H, KTile<D>::kCols, kKeys, 1, KTile<D>::kSwizzle) ||
+      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kKeys, 1, VTile::kSwizzle) ||
+      !map2d_bf16(&o, a.a, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, 32))
     return cudaErrorInvalidValue;
   return launch_dependent(forward_kernel<D>, dim3(static_cast<unsigned>(blocks)), kThreads, smem_bytes<D>(), s, q, k, v, o, a, st);
 }
