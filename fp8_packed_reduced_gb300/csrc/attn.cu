@@ -6,12 +6,35 @@
 namespace qkvp {
 namespace {
 
+void use_workspace(AttnArgs* p, void* ws) {
+  const AttnLayout w = attention_layout(*p);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  p->spans = reinterpret_cast<int2*>(b + w.spans);
+  p->ranges = reinterpret_cast<int4*>(b + w.ranges);
+  p->ends = reinterpret_cast<int*>(b + w.ends);
+  p->jobs[0] = reinterpret_cast<int4*>(b + w.jobs[0]);
+  p->jobs[1] = reinterpret_cast<int4*>(b + w.jobs[1]);
+  p->counter = reinterpret_cast<unsigned int*>(b + kAttnCounter);
+  p->stat = reinterpret_cast<float*>(b + w.stat);   // (of a backward's workspace)
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-size_t order_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Tp) / kAttnTile * sizeof(int) + 255) / 256 * 256; }
-size_t stat_bytes(const AttnArgs& a) { return (static_cast<size_t>(a.Hq) * a.Tp * 2 * sizeof(float) + 255) / 256 * 256; }
-
 }  // namespace
+
+AttnLayout attention_layout(const AttnArgs& a) {
+  const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t tiles = a.Tp / kAttnTile;
+  AttnLayout w;
+  w.spans = kAttnHeaderBytes;
+  w.ranges = w.spans + up(a.Tp * sizeof(int2));
+  w.jobs[0] = w.ranges + up(tiles * sizeof(int4));
+  w.ends = w.jobs[0] + up(3 * tiles * sizeof(int4));
+  w.jobs[1] = w.ends + up(tiles * sizeof(int));
+  w.stat = w.jobs[1] + up(tiles * sizeof(int4));
+  w.bytes = w.stat + up(static_cast<size_t>(a.Hq) * a.Tp * 2 * sizeof(float));
+  return w;
+}
 
 int check_attention(const qkvp_attention* at, AttnArgs* a) {
   if (!at) return QKVP_ERR_INVALID_ARGUMENT;
@@ -25,7 +48,7 @@ int check_attention(const qkvp_attention* at, AttnArgs* a) {
   if (!aligned16(at->cu)) return QKVP_ERR_MISALIGNED;
   *a = AttnArgs{};
   a->T = at->T;
-  a->Tp = (at->T + kAttnTile - 1) / kAttnTile * kAttnTile;
+  a->Tp = (at->T + kAttnTile - 1) / kAttnTile * kAttnTile + kAttnTile;   // (tiles of fewer rows may reach over the end)
   a->Hq = at->Hq;
   a->H = at->H;
   a->G = at->Hq / at->H;
@@ -48,7 +71,7 @@ extern "C" {
 size_t qkvp_attention_workspace_bytes(const qkvp_attention* at) {
   AttnArgs a;
   if (check_attention(at, &a) != QKVP_OK) return 0;
-  return kAttnHeaderBytes + 2 * order_bytes(a) + stat_bytes(a);
+  return attention_layout(a).bytes;
 }
 
 int qkvp_attention_forward(const qkvp_attention* at, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* a,
@@ -62,14 +85,14 @@ int qkvp_attention_forward(const qkvp_attention* at, const uint16_t* q, const ui
     if (!x && p.T) return QKVP_ERR_INVALID_ARGUMENT;
     if (!aligned16(x)) return QKVP_ERR_MISALIGNED;
   }
-  if (ws_bytes < kAttnHeaderBytes + order_bytes(p)) return QKVP_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < attention_layout(p).bytes) return QKVP_ERR_WORKSPACE_TOO_SMALL;
   if (p.T == 0) return QKVP_OK;
   p.q = q;
   p.k = k;
   p.v = v;
   p.a = a;
   p.lse = lse;
-  p.order[0] = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kAttnHeaderBytes);
+  use_workspace(&p, ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   mark(s);
   if (launch_attention_forward(p, dev_status(ws), s) != cudaSuccess) return QKVP_ERR_CUDA;
@@ -89,7 +112,7 @@ int qkvp_attention_backward(const qkvp_attention* at, const uint16_t* da, const 
     if (!x && p.T) return QKVP_ERR_INVALID_ARGUMENT;
     if (!aligned16(x)) return QKVP_ERR_MISALIGNED;
   }
-  if (ws_bytes < kAttnHeaderBytes + 2 * order_bytes(p) + stat_bytes(p)) return QKVP_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < attention_layout(p).bytes) return QKVP_ERR_WORKSPACE_TOO_SMALL;
   if (p.T == 0) return QKVP_OK;
   p.q = q;
   p.k = k;
@@ -97,10 +120,7 @@ int qkvp_attention_backward(const qkvp_attention* at, const uint16_t* da, const 
   p.a = const_cast<uint16_t*>(a);
   p.lse = const_cast<float*>(lse);
   p.da = da;
-  uint8_t* w = static_cast<uint8_t*>(ws) + kAttnHeaderBytes;
-  p.order[0] = reinterpret_cast<int*>(w);
-  p.order[1] = reinterpret_cast<int*>(w + order_bytes(p));
-  p.stat = reinterpret_cast<float*>(w + 2 * order_bytes(p));
+  use_workspace(&p, ws);
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;

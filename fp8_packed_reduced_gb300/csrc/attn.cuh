@@ -32,7 +32,12 @@ struct AttnArgs {
   int Tp;                    // T rounded up to whole tiles
   float* stat;               // [Hq, 2, Tp] -lse in base 2 (-inf: no weight), -da . a
   uint16_t *dq, *dk, *dv;
-  int* order[2];             // tiles from the longest on (backward: of dq, of dk and dv), or null: as they come
+  // The plan of a call with more tiles than multiprocessors (spans is null without):
+  int2* spans;               // [Tp] every token's sequence
+  int4* ranges;              // [Tp / 128] key tiles of 128 queries (backward: of dq)
+  int* ends;                 // [Tp / 128] end of the queries that see 128 keys (backward)
+  int4* jobs[2];             // the blocks' work, longest first: [tiles][3] of the forward or of dq; [tiles] of dk and dv
+  unsigned int* counter;     // of the plan's blocks that are done; zero between calls
 };
 
 // A tile of ROWS rows of q or k in shared memory: boxes of 64 columns with
@@ -56,16 +61,6 @@ struct AttnTile {
   }
 };
 
-// Row and head of a block: the grid is tiles x heads, all heads of a tile next
-// to each other.
-struct Place {
-  int tile, head;
-};
-__device__ __forceinline__ Place place_of(const int* order, int heads) {
-  const int i = blockIdx.x / heads;
-  return Place{order ? __ldcg(order + i) : i, static_cast<int>(blockIdx.x) - i * heads};
-}
-
 // A token's sequence, [start, end); start < 0: none.
 struct Span {
   int start, end;
@@ -88,9 +83,6 @@ __device__ __forceinline__ Span span_of(const AttnArgs& p, int row) {
 // The first token of the window of token `row` of a sequence that starts at `start`.
 __device__ __forceinline__ int window_start(const AttnArgs& p, int row, int start) {
   return max(start, row - p.window + 1);
-}
-__device__ __forceinline__ bool sees(const AttnArgs& p, int i, int j, int start) {
-  return j >= start && j <= i && (i - j < p.window || j < start + p.sinks);
 }
 // A token that sees only itself has the probability one and passes nothing on
 // to q and k, exactly; the difference of two sums would leave their rounding.
@@ -131,34 +123,19 @@ __device__ __forceinline__ int last_seer(const AttnArgs& p, int row, Span sp) {
   return row - sp.start < p.sinks || sp.end - row <= p.window ? sp.end : row + p.window;
 }
 
-// The tiles of an attention in the order of their work, longest first, so that
-// the blocks that start last are the short ones.  One block; order [tiles].
-//   keys: the tiles are of keys (dk, dv), else of queries of `rows` rows each
-__device__ __forceinline__ int tile_work(const AttnArgs& p, int tile, int rows, bool keys) {
-  const int r0 = tile * rows, r1 = min(r0 + rows, p.T) - 1;
-  const Span a = span_of(p, r0), b = span_of(p, r1);
-  if (keys) {
-    int end = 0;
-    if (a.start >= 0) end = last_seer(p, r0, a);
-    if (b.start >= 0) end = max(end, b.start >= r0 ? last_seer(p, b.start, b) : last_seer(p, r1, b));
-    return max(0, (end - r0 + kAttnTile - 1) / kAttnTile);
-  }
-  if (a.start < 0 && b.start < 0) return 0;   // (a sequence in between is shorter than the tile)
-  const int first = a.start < 0 ? r0 : window_start(p, r0, a.start);
-  const int sinks = a.start < 0 || !p.sinks ? 0 : min(first - a.start, p.sinks);
-  return (r1 - first) / kAttnTile + 1 + (sinks + kAttnTile - 1) / kAttnTile;
-}
-template <int kThreads>
-__device__ __forceinline__ void sort_tiles(const AttnArgs& p, int tiles, int rows, bool keys, int* order) {
+// Numbers 0 .. count - 1 from the largest work(i) to the smallest (to one part in
+// a thousand of the largest): emit(place, i).  One block.
+template <int kThreads, class Work, class Emit>
+__device__ __forceinline__ void sort_by_work(int count, const Work& work, const Emit& emit) {
   constexpr int kBins = 1024;
   __shared__ int bin[kBins], most;
   for (int i = threadIdx.x; i < kBins; i += kThreads) bin[i] = 0;
   if (threadIdx.x == 0) most = 1;
   __syncthreads();
-  for (int i = threadIdx.x; i < tiles; i += kThreads) atomicMax(&most, tile_work(p, i, rows, keys));
+  for (int i = threadIdx.x; i < count; i += kThreads) atomicMax(&most, work(i));
   __syncthreads();
-  const auto bin_of = [&](int i) { return kBins - 1 - static_cast<int>(static_cast<int64_t>(tile_work(p, i, rows, keys)) * (kBins - 1) / most); };
-  for (int i = threadIdx.x; i < tiles; i += kThreads) atomicAdd(&bin[bin_of(i)], 1);
+  const auto bin_of = [&](int i) { return kBins - 1 - static_cast<int>(static_cast<int64_t>(work(i)) * (kBins - 1) / most); };
+  for (int i = threadIdx.x; i < count; i += kThreads) atomicAdd(&bin[bin_of(i)], 1);
   __syncthreads();
   if (threadIdx.x < 32) {   // places of the bins
     int run = 0;
@@ -168,14 +145,81 @@ __device__ __forceinline__ void sort_tiles(const AttnArgs& p, int tiles, int row
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (threadIdx.x >= o) x += y;
+        if (static_cast<int>(threadIdx.x) >= o) x += y;
       }
       bin[b0 + threadIdx.x] = run + x - v;
       run += __shfl_sync(0xffffffffu, x, 31);
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < tiles; i += kThreads) order[atomicAdd(&bin[bin_of(i)], 1)] = i;
+  for (int i = threadIdx.x; i < count; i += kThreads) emit(atomicAdd(&bin[bin_of(i)], 1), i);
+  __syncthreads();
+}
+
+// The plan: every token's sequence, the key tiles of 128 queries (KEYS keys
+// each), and the blocks' work in the order of its length; the last block to be
+// done with its part of the first two sorts.  BACK: for the backward.
+constexpr int kPlanThreads = 1024;
+template <int KEYS, bool BACK>
+__device__ __forceinline__ void make_plan(const AttnArgs& p, int block, int blocks) {
+  constexpr int kTiles = kPlanThreads / kAttnTile;
+  __shared__ int lo[kTiles][4], hi[kTiles][4], start[kTiles][4], end[kTiles][4], last_block;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tiles = (p.T + kAttnTile - 1) / kAttnTile;
+  const int row = block * kPlanThreads + threadIdx.x;
+  Span sp{-1, -1};
+  if (row < p.T) sp = span_of(p, row);
+  if (row < p.Tp) p.spans[row] = make_int2(sp.start, sp.end);
+  const bool in = sp.start >= 0, query = in && !(BACK && alone(p, row, sp.start));
+  const int w_lo = __reduce_min_sync(0xffffffffu, query ? window_start(p, row, sp.start) : INT_MAX);
+  const int w_hi = __reduce_max_sync(0xffffffffu, query ? row : -1);
+  const int w_start = __reduce_min_sync(0xffffffffu, query ? sp.start : INT_MAX);
+  const int w_end = __reduce_max_sync(0xffffffffu, in ? last_seer(p, row, sp) : -1);
+  if (lane == 0) {
+    lo[warp >> 2][warp & 3] = w_lo;
+    hi[warp >> 2][warp & 3] = w_hi;
+    start[warp >> 2][warp & 3] = w_start;
+    end[warp >> 2][warp & 3] = w_end;
+  }
+  __syncthreads();
+  const int tile = block * kTiles + threadIdx.x;
+  if (threadIdx.x < kTiles && tile < tiles) {
+    const Range r = range_of<KEYS>(p, lo[threadIdx.x], hi[threadIdx.x], start[threadIdx.x]);
+    p.ranges[tile] = make_int4(r.sink0, r.sink1, r.first, r.last);
+    if (BACK) p.ends[tile] = max(max(end[threadIdx.x][0], end[threadIdx.x][1]), max(end[threadIdx.x][2], end[threadIdx.x][3]));
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last_block = atomicAdd(p.counter, 1) == static_cast<unsigned int>(blocks) - 1;
+  __syncthreads();
+  if (!last_block) return;
+  __threadfence();
+  if (threadIdx.x == 0) *p.counter = 0;
+  const auto length = [](int4 r) { return r.w - r.z + max(0, r.y - r.x); };
+  if (BACK) {
+    sort_by_work<kPlanThreads>(
+        tiles, [&](int i) { return length(__ldcg(p.ranges + i)); },
+        [&](int at, int i) {
+          p.jobs[0][3 * at] = make_int4(i, 0, 0, 0);
+          p.jobs[0][3 * at + 1] = __ldcg(p.ranges + i);
+        });
+    sort_by_work<kPlanThreads>(
+        tiles, [&](int i) { return max(0, __ldcg(p.ends + i) - i * kAttnTile); },
+        [&](int at, int i) { p.jobs[1][at] = make_int4(i, __ldcg(p.ends + i), 0, 0); });
+  } else {   // two tiles a job
+    const auto range = [&](int i) { return i < tiles ? __ldcg(p.ranges + i) : make_int4(0, 0, 0, 0); };
+    sort_by_work<kPlanThreads>(
+        (tiles + 1) / 2, [&](int i) { return length(range(2 * i)) + length(range(2 * i + 1)); },
+        [&](int at, int i) {
+          p.jobs[0][3 * at] = make_int4(i, 0, 0, 0);
+          p.jobs[0][3 * at + 1] = range(2 * i);
+          p.jobs[0][3 * at + 2] = range(2 * i + 1);
+        });
+  }
+}
+// The job of a block's k-th turn: the blocks take turns forwards and backwards,
+// so that each gets as much of the longest first order as the others.
+__device__ __forceinline__ int job_of(int k) {
+  return k * static_cast<int>(gridDim.x) + static_cast<int>(k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
 // Records offsets that are out of range or decrease; one block calls it.
@@ -267,8 +311,9 @@ __device__ __forceinline__ float2 pair_grad(const AttnArgs& p, int i, int j, int
   return make_float2(w, alone ? 0.f : w * (dp + __ldcg(s + p.Tp)));
 }
 
+// Columns 32 c0 .. 32 c1 - 1 of a row of dq.
 template <int D>
-__device__ __forceinline__ void dq_row(const AttnArgs& p, int row, int hq) {
+__device__ __forceinline__ void dq_row(const AttnArgs& p, int row, int hq, int c0, int c1) {
   const int lane = threadIdx.x & 31, h = hq / p.G;
   const Span sp = span_of(p, row);
   float o[D / 32] = {};
@@ -291,11 +336,12 @@ __device__ __forceinline__ void dq_row(const AttnArgs& p, int row, int hq) {
   }
 #pragma unroll
   for (int c = 0; c < D / 32; ++c)
-    p.dq[(static_cast<int64_t>(hq) * p.T + row) * D + 32 * c + lane] = bf16_bits(o[c] * p.scale);
+    if (c >= c0 && c < c1) p.dq[(static_cast<int64_t>(hq) * p.T + row) * D + 32 * c + lane] = bf16_bits(o[c] * p.scale);
 }
 
+// A row of dv, or of dk.
 template <int D>
-__device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h) {
+__device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h, bool dv) {
   const int lane = threadIdx.x & 31;
   const Span sp = span_of(p, row);
   float ok[D / 32] = {}, ov[4] = {};
@@ -318,9 +364,12 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h) {
       }
     }
   const int64_t at = static_cast<int64_t>(h) * p.T + row;
+  if (dv) {
+    reinterpret_cast<uint2*>(p.dv + at * kDv)[lane] = make_uint2(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]));
+  } else {
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) p.dk[at * D + 32 * c + lane] = bf16_bits(ok[c] * p.scale);
-  reinterpret_cast<uint2*>(p.dv + at * kDv)[lane] = make_uint2(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]));
+    for (int c = 0; c < D / 32; ++c) p.dk[at * D + 32 * c + lane] = bf16_bits(ok[c] * p.scale);
+  }
 }
 
 // mbar_wait without a call (a kernel that moves registers between its warps
@@ -341,11 +390,17 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, vola
   }
 }
 
+// Parts of the workspace behind its header.  Host: fills p's pointers into it.
+struct AttnLayout {
+  size_t spans, ranges, ends, jobs[2], stat, bytes;
+};
+AttnLayout attention_layout(const AttnArgs& a);
+
 // Host: fills `a` from the caller's description, QKVP_OK or the status that an
 // entry point returns.
 int check_attention(const qkvp_attention* at, AttnArgs* a);
 cudaError_t launch_attention_forward(const AttnArgs& a, DevStatus st, cudaStream_t s);
 cudaError_t launch_attention_backward(const AttnArgs& a, DevStatus st, cudaStream_t s);
-constexpr size_t kAttnHeaderBytes = 1024;
+constexpr size_t kAttnHeaderBytes = 1024, kAttnCounter = 192;   // (its own place beside those of the cache's calls)
 
 }  // namespace qkvp

@@ -1,8 +1,14 @@
 // Gradient of the causal attention over packed sequences on the 5th-generation
 // tensor cores (attn.cuh has the formulas), in two passes that both form the
-// scores and da . v again: one over the keys of 128 queries for dq, one over the
-// queries of 128 keys for dk and dv.  A single pass would have to add dq up in
+// scores and da . v again: one over the queries of 128 keys for dk and dv, one
+// over the keys of 128 queries for dq.  A single pass would have to add dq up in
 // memory, in an order that changes from run to run.
+//
+// As in the forward, every product has a place of its own in TMEM, so that the
+// next step's scores and da . v are formed while this one's probabilities and ds
+// are.  What is rounded to bf16 (2^-8): probabilities for the product with da, ds
+// for those with q and k, and the results; da . a uses the bf16 a.
+#include <algorithm>
 #include <atomic>
 
 #include "attn.cuh"
@@ -10,41 +16,65 @@
 namespace qkvp {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTile = kAttnTile;
 constexpr int kThreads = 352;                // eight computing warps, a loading and two issuing ones
-constexpr int kBox = kTile * 128;            // bytes of 128 rows x 64 bf16
-using VTile = AttnTile<kDv, kTile>;                 // of v and da
-// Rings of tiles: in dq of k and v, in dk and dv of q and da.  As many stages as
-// fit; in dk and dv a tile of q is back in use sooner than one of da.
-__host__ __device__ constexpr int dq_stages(int d) { return d == 128 ? 3 : 4; }
-__host__ __device__ constexpr int q_stages(int d) { return d == 128 ? 2 : 4; }
-__host__ __device__ constexpr int da_stages(int d) { return d == 64 ? 3 : 2; }
+constexpr int kMaxStages = 5;
+constexpr int kOutBytes = 32 * 128;          // of a computing warp's output, 32 rows x 64 columns at a time
+template <int D>
+using Fixed = AttnTile<D, kTile>;            // 128 rows
+
+// --- dq: steps of 96 keys ----------------------------------------------------
+constexpr int kKeys = 96;
+template <int D>
+using KTile = AttnTile<D, kKeys>;
+using VTile = AttnTile<kDv, kKeys>;
+__host__ __device__ constexpr int dq_stages(int d) { return d == 64 ? 5 : 4; }
 template <int D>
 constexpr int dq_smem() {
-  return 1024 + dq_stages(D) * (AttnTile<D, kTile>::kBytes + VTile::kBytes);
+  return 1024 + dq_stages(D) * (KTile<D>::kBytes + VTile::kBytes) + 8 * kOutBytes;
 }
+// columns of TMEM: scores, da . v, ds, dq, and q and da as operands
+constexpr uint32_t kQS = 0, kQDp = 96, kQDs = 192, kQAcc = 256, kQOpQ = 384, kQOpDa = 448;
+
+// --- dk and dv: steps of 96 or 80 queries -------------------------------------
+// (scores, probabilities, da . v and ds take three times as many columns, beside
+// the 128 + d of dv and dk)
+__host__ __device__ constexpr int queries(int d) { return d == 128 ? 80 : 96; }
+template <int D>
+using QTile = AttnTile<D, queries(D)>;
+template <int D>
+using DaTile = AttnTile<kDv, queries(D)>;
+__host__ __device__ constexpr int q_stages(int d) { return d == 64 ? 4 : 3; }
+__host__ __device__ constexpr int da_stages(int) { return 3; }
 template <int D>
 constexpr int dkv_smem() {
-  return 1024 + (1 + q_stages(D)) * AttnTile<D, kTile>::kBytes + (1 + da_stages(D)) * VTile::kBytes;
+  return 1024 + Fixed<D>::kBytes + Fixed<kDv>::kBytes + q_stages(D) * QTile<D>::kBytes + da_stages(D) * DaTile<D>::kBytes +
+         8 * kOutBytes;
 }
-// Columns of TMEM
-constexpr int kScores = 0, kDp = 128, kAcc0 = 256, kAcc1 = 384, kOpQ = 384, kOpDa = 448;
+__host__ __device__ constexpr uint32_t k_s(int) { return 0; }
+__host__ __device__ constexpr uint32_t k_p(int d) { return queries(d); }
+__host__ __device__ constexpr uint32_t k_dp(int d) { return queries(d) * 3 / 2; }
+__host__ __device__ constexpr uint32_t k_ds(int d) { return queries(d) * 5 / 2; }
+__host__ __device__ constexpr uint32_t k_dv(int d) { return d == 128 ? 256 : 288; }
+__host__ __device__ constexpr uint32_t k_dk(int d) { return k_dv(d) + kDv; }
 
-constexpr int kMaxStages = 4;
 struct Shared {
-  uint64_t fixed_full, a_full[kMaxStages], a_empty[kMaxStages], b_full[kMaxStages], b_empty[kMaxStages];
-  uint64_t s_full, dp_full, s_free, p_full[2], ds_full[2], acc_full;   // (p and ds in two parts)
+  uint64_t fixed_full, fixed_empty;   // dk and dv: the job's keys; dq: q and da are in TMEM (fixed_full)
+  uint64_t a_full[kMaxStages], a_empty[kMaxStages], b_full[kMaxStages], b_empty[kMaxStages];
+  uint64_t s_full, s_free, p_full, p_free, dp_full, dp_free, ds_full, ds_free;
+  uint64_t acc_full, acc_free[2];     // a job's sums are complete; each warpgroup has read its own
+  uint64_t end;                       // all products are done
   uint32_t tmem;
   int abort;
   int lo[4], hi[4], start[4];
-  uint32_t again[4];            // rows to be computed again
-  Range range;
+  Range range;                        // of a block's only job, without a plan
 };
 
-// b_users: issuing warps that release a stage of b.
-__device__ __forceinline__ void init_barriers(Shared& g, int b_users) {
+// Warps that arrive at, or commits that complete, each barrier.
+__device__ __forceinline__ void init_barriers(Shared& g, int fixed_full, int b_users) {
   g.abort = 0;
-  mbar_init(&g.fixed_full, 1);
+  mbar_init(&g.fixed_full, fixed_full);
+  mbar_init(&g.fixed_empty, 2);
   for (int s = 0; s < kMaxStages; ++s) {
     mbar_init(&g.a_full[s], 1);
     mbar_init(&g.a_empty[s], 1);
@@ -52,43 +82,85 @@ __device__ __forceinline__ void init_barriers(Shared& g, int b_users) {
     mbar_init(&g.b_empty[s], b_users);
   }
   mbar_init(&g.s_full, 1);
-  mbar_init(&g.dp_full, 1);
   mbar_init(&g.s_free, 8);
-  for (int i = 0; i < 2; ++i) {
-    mbar_init(&g.p_full[i], 8);
-    mbar_init(&g.ds_full[i], 8);
-  }
+  mbar_init(&g.p_full, 8);
+  mbar_init(&g.p_free, 1);
+  mbar_init(&g.dp_full, 1);
+  mbar_init(&g.dp_free, 8);
+  mbar_init(&g.ds_full, 8);
+  mbar_init(&g.ds_free, 1);
   mbar_init(&g.acc_full, 2);
+  mbar_init(&g.acc_free[0], 4);
+  mbar_init(&g.acc_free[1], 4);
+  mbar_init(&g.end, 2);
   fence_mbar_init();
 }
 // Two pairs of floats of shared memory.
 __device__ __forceinline__ void lds_f2x2(uint32_t at, f2 (&z)[2]) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(z[0]), "=l"(z[1]) : "r"(at));
 }
-// 8 warps of a group have done something to TMEM: arrive once per warp.
+// A warp has done something to TMEM: it arrives once.
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   tc_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
+// The halves of a packed word whose bit of `see` (two bits from 2 i on) is set.
+__device__ __forceinline__ uint32_t seen_halves(uint32_t see, int i) {
+  return (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+}
 
+// 64 columns of an accumulator in TMEM (its first `width` count), times f, as one
+// box of 32 rows in `stage`, and from there to rows `row` on of head `head`; zeros
+// unless `some`.  Whether a value is not finite.  free: arrives when the columns
+// have been read.
+__device__ __forceinline__ bool write_box(uint32_t taddr, int width, float f, bool some, uint8_t* stage, const CUtensorMap* map,
+                                          int col, int row, int head, int T, uint64_t* free) {
+  const int lane = threadIdx.x & 31;
+  uint32_t o[64];
+  tmem_load<64>(taddr, o);
+  tmem_ld_wait();
+  if (free) arrive_warp(free);
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < 64; i += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = __uint_as_float(o[i + 2 * k]) * f, b = __uint_as_float(o[i + 2 * k + 1]) * f;
+      if (i < width) big += fabsf(a) + fabsf(b);
+      w[k] = some ? pack_bf16x2(a, b) : 0u;
+    }
+    *reinterpret_cast<uint4*>(stage + lane * 128 + (((i / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0 && row < T) {   // (lane 0 has the first row)
+    tma_store_3d(map, stage, col, row, head);
+    bulk_commit();
+  }
+  return some && !(big < INFINITY);
+}
+
+// ---------------------------------------------------------------------------
 // delta = da . a of every row and head, and beside it the row's lse in base 2
 // (+inf where the row has no weight at all, so that its probabilities are 0), both
-// negative.  A half warp a row, 16 rows a warp.  Its first blocks put the tiles of the two
-// passes in order.
-constexpr int kPrepThreads = 256, kPrepRows = kPrepThreads / 32 * 16;
-static_assert(kPrepRows == kTile, "the statistics cover whole tiles");
-__global__ void __launch_bounds__(kPrepThreads) delta_kernel(const __grid_constant__ AttnArgs p, int tiles, DevStatus st) {
+// negative.  A half warp a row, 16 rows a warp.  The first blocks make the plan.
+// ---------------------------------------------------------------------------
+constexpr int kPrepRows = kPlanThreads / 32 * 16;
+__global__ void __launch_bounds__(kPlanThreads) delta_kernel(const __grid_constant__ AttnArgs p, int plan_blocks, int row_blocks,
+                                                             DevStatus st) {
   wait_for_previous();
   if (blockIdx.x == 0) check_offsets(p, st, KID_ATTN_DELTA);
-  const int sorts = p.order[0] ? 2 : 0;
-  if (static_cast<int>(blockIdx.x) < sorts) {
-    sort_tiles<kPrepThreads>(p, tiles, kTile, blockIdx.x == 1, p.order[blockIdx.x]);
+  if (static_cast<int>(blockIdx.x) < plan_blocks) {
+    make_plan<kKeys, true>(p, blockIdx.x, plan_blocks);
     return;
   }
-  const int block = blockIdx.x - sorts, hq = block / tiles;
+  const int block = blockIdx.x - plan_blocks, hq = block / row_blocks;
   const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-  const int r0 = (block - hq * tiles) * kTile + (threadIdx.x >> 5) * 16;
+  const int r0 = (block - hq * row_blocks) * kPrepRows + (threadIdx.x >> 5) * 16;
   float mine = 0.f;   // lane c < 8 of a half keeps row r0 + 2 c + half
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -105,7 +177,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_kernel(const __grid_consta
     if (c == i) mine = s;
   }
   const int row = r0 + 2 * c + half;
-  if (c < 8) {
+  if (c < 8 && row < p.Tp) {
     const float z = row < p.T ? __ldg(p.lse + static_cast<int64_t>(hq) * p.T + row) : -INFINITY;
     float* to = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;
     to[0] = z == -INFINITY ? -INFINITY : z * -1.4426950408889634f;
@@ -114,523 +186,637 @@ __global__ void __launch_bounds__(kPrepThreads) delta_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// dq: 128 queries of a head.  q and da are operands in TMEM for the whole of
-// it, dq adds up there; per tile of 128 keys
+// dq: 128 queries of a head.  q and da are operands in TMEM for the whole job, dq
+// adds up there; per step
 //   S = q k^T, dP = da v^T, ds = e^(S - lse) (dP - delta), dq += ds k
-// The products are issued dP(j), S(j + 1), dq(j): S(j + 1) covers the forming of ds(j).
 // ---------------------------------------------------------------------------
+struct DqJob {
+  int tile, head;
+  Range r;
+  __device__ int begin() const { return r.sink0 < r.sink1 ? r.sink0 : r.first; }
+  __device__ int after(int kt) const { return kt + 1 == r.sink1 ? r.first : kt + 1; }
+};
+struct DqJobs {
+  const AttnArgs& p;
+  const Shared& g;
+  int total, k, tile, head;
+  int4 r;
+  bool more;
+  __device__ DqJobs(const AttnArgs& p, const Shared& g, int total) : p(p), g(g), total(total), k(0) { fetch(); }
+  __device__ void fetch() {
+    if (!p.spans) {
+      more = k == 0;
+      return;
+    }
+    const int i = job_of(k), at = i / p.Hq;
+    more = i < total;
+    head = i - at * p.Hq;
+    if (more) {
+      tile = __ldcg(&p.jobs[0][3 * at].x);
+      r = __ldcg(p.jobs[0] + 3 * at + 1);
+    }
+  }
+  __device__ bool next(DqJob& j) {
+    if (!more) return false;
+    if (!p.spans) {
+      j.tile = blockIdx.x / p.Hq;
+      j.head = blockIdx.x - j.tile * p.Hq;
+      j.r = g.range;
+    } else {
+      j.tile = tile;
+      j.head = head;
+      j.r = Range{r.x, r.y, r.z, r.w};
+    }
+    ++k;
+    fetch();
+    return true;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-              const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ AttnArgs p, DevStatus st) {
-  using KTile = AttnTile<D, kTile>;
-  constexpr int kKBytes = KTile::kBytes, kVBytes = VTile::kBytes, kStages = dq_stages(D), KB = (D + 63) / 64;
+              const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ AttnArgs p, int total, DevStatus st) {
+  constexpr int kKBytes = KTile<D>::kBytes, kVBytes = VTile::kBytes, kStages = dq_stages(D), kHalf = kKeys / 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sk = smem, *sv = sk + kStages * kKBytes;
+  uint8_t *sk = smem, *sv = sk + kStages * kKBytes, *so = sv + kStages * kVBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) init_barriers(g, 1);
-  if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
+  if (threadIdx.x == 0) init_barriers(g, 8, 1);
   if (warp == 9) {
     tmem_alloc(&g.tmem, 512);
     tmem_relinquish();
   }
   wait_for_previous();
-  const Place at = place_of(p.order[0], p.Hq);
-  const int hq = at.head, h = hq / p.G, r0 = at.tile * kTile;
-  const int half = warp >> 2, row = r0 + (threadIdx.x & 127);
-  Span sp{-1, -1};
-  int seen0 = 0;
-  if (warp < 8) {
-    if (row < p.T) sp = span_of(p, row);
-    if (sp.start >= 0 && alone(p, row, sp.start)) sp.start = -1;   // it passes nothing on
-    seen0 = sp.start < 0 ? INT_MAX : window_start(p, row, sp.start);
-    const int lo = __reduce_min_sync(0xffffffffu, seen0), hi = __reduce_max_sync(0xffffffffu, sp.start < 0 ? -1 : row);
-    const int s0 = __reduce_min_sync(0xffffffffu, sp.start < 0 ? INT_MAX : sp.start);
-    if (lane == 0 && half == 0) g.lo[warp] = lo, g.hi[warp] = hi, g.start[warp] = s0;
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (threadIdx.x == 0) g.range = range_of<kTile>(p, g.lo, g.hi, g.start);
-  const uint32_t tmem = g.tmem, quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  if (warp < 8) {   // one half of the warps loads q, the other da
-    const uint4* from = reinterpret_cast<const uint4*>(half == 0 ? p.q + (static_cast<int64_t>(hq) * p.T + row) * D
-                                                                 : p.da + (static_cast<int64_t>(row) * p.Hq + hq) * kDv);
-    const uint32_t to = tmem + (half == 0 ? kOpQ : kOpDa) + quarter;
-    const int parts = half == 0 ? D / 32 : kDv / 32;
-    for (int c = 0; c < parts; ++c) {
-      uint32_t w[16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = row < p.T ? __ldg(from + 4 * c + i) : make_uint4(0, 0, 0, 0);
-        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-      }
-      tmem_st16(to + 16 * c, w);
+  // A token alone passes nothing on: it counts as of no sequence.
+  const auto start_of = [&](int row) {
+    if (row >= p.T) return -1;
+    const int s = p.spans ? __ldcg(p.spans + row).x : span_of(p, row).start;
+    return s >= 0 && alone(p, row, s) ? -1 : s;
+  };
+  if (!p.spans) {   // a call without a plan: the block finds out about its rows by itself
+    if (warp < 4) {
+      const int row = static_cast<int>(blockIdx.x) / p.Hq * kTile + threadIdx.x, s = start_of(row);
+      const int lo = __reduce_min_sync(0xffffffffu, s < 0 ? INT_MAX : window_start(p, row, s));
+      const int hi = __reduce_max_sync(0xffffffffu, s < 0 ? -1 : row), s0 = __reduce_min_sync(0xffffffffu, s < 0 ? INT_MAX : s);
+      if (lane == 0) g.lo[warp] = lo, g.hi[warp] = hi, g.start[warp] = s0;
     }
-    tmem_st_wait();
+    __syncthreads();
+    if (threadIdx.x == 0) g.range = range_of<kKeys>(p, g.lo, g.hi, g.start);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Range r = g.range;
-  const int kt0 = r.sink0 < r.sink1 ? r.sink0 : r.first;
-  const auto next_of = [&](int kt) { return kt + 1 == r.sink1 ? r.first : kt + 1; };
+  const uint32_t tmem = g.tmem;
+  DqJobs jobs(p, g, total);
+  DqJob job;
 
   if (warp == 8) {
     if (lane == 0) {
       int n = 0;
-      for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
-        const int s = n % kStages, par = (n / kStages) & 1;
-        if (!mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) break;
-        mbar_arrive_expect_tx(&g.a_full[s], kKBytes);
-        KTile::load(sk + s * kKBytes, &tm_k, &g.a_full[s], kt * kTile, h);
-        if (!mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ)) {
-          mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DQ);
-          break;
+      bool ok = true;
+      while (ok && jobs.next(job)) {
+        const int h = job.head / p.G;
+        for (int kt = job.begin(); kt < job.r.last; kt = job.after(kt), ++n) {
+          const int s = n % kStages, par = (n / kStages) & 1;
+          ok = mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&g.a_full[s], kKBytes);
+          KTile<D>::load(sk + s * kKBytes, &tm_k, &g.a_full[s], kt * kKeys, h);
+          ok = mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) {
+            mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DQ);
+            break;
+          }
+          mbar_arrive_expect_tx(&g.b_full[s], kVBytes);
+          VTile::load(sv + s * kVBytes, &tm_v, &g.b_full[s], kt * kKeys, h);
         }
-        mbar_arrive_expect_tx(&g.b_full[s], kVBytes);
-        VTile::load(sv + s * kVBytes, &tm_v, &g.b_full[s], kt * kTile, h);
       }
       for (int i = max(0, n - kStages); i < n; ++i) {   // every copy has landed before the block may leave
         mbar_wait(&g.a_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
         mbar_wait(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
       }
     }
-  } else if (warp >= 9) {
+  } else if (warp > 8) {
     // One warp issues the scores, the other the rest: while one finds out what
     // is ready, the products of the other run.  A whole warp goes the same way
     // (umma_bf16_ss says why).
-    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_q = idesc_bf16_f32(kTile, D, true);
+    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kKeys, false), id_q = idesc_bf16_f32(kTile, D, true);
     const uint32_t elected = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DQ));
     };
-    int n = 0;
+    bool ok = true;
+    int n = 0, turn = 0;   // steps; jobs with any
     if (warp == 9) {
-      const uint64_t k0 = KTile::desc(sk);
-      for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
-        const int s = n % kStages;
-        if (!wait(&g.a_full[s], (n / kStages) & 1) || (n > 0 && !wait(&g.s_free, (n - 1) & 1))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ts(tmem + kScores, tmem + kOpQ + kk * 8, k0 + ((s * kKBytes) >> 4) + KTile::cols16(kk), id_s, kk > 0, elected);
-        umma_commit_elected(&g.s_full, elected);
-      }
-    } else {
-      const uint64_t v0 = VTile::desc(sv), k0 = KTile::desc(sk);
-      const auto dps = [&](int s) {
-#pragma unroll
-        for (int kk = 0; kk < kDv / 16; ++kk)
-          umma_bf16_ts(tmem + kDp, tmem + kOpDa + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::cols16(kk), id_s, kk > 0, elected);
-        umma_commit_elected(&g.dp_full, elected);
-        umma_commit_elected(&g.b_empty[s], elected);
-      };
-      bool ok = kt0 < r.last && wait(&g.b_full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        dps(0);
-      }
-      for (int kt = kt0; ok && kt < r.last; ++n) {
-        const int s = n % kStages, s1 = (n + 1) % kStages, next = next_of(kt);
-        ok = wait(&g.a_full[s], (n / kStages) & 1) && (next >= r.last || wait(&g.b_full[s1], ((n + 1) / kStages) & 1)) &&
-             wait(&g.ds_full[0], n & 1);
-        if (!ok) break;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (part == 1) ok = wait(&g.ds_full[1], n & 1);
+      const uint64_t k0 = KTile<D>::desc(sk);
+      while (ok && jobs.next(job)) {
+        if (job.begin() >= job.r.last) continue;
+        ok = wait(&g.fixed_full, turn++ & 1);
+        for (int kt = job.begin(); ok && kt < job.r.last; kt = job.after(kt), ++n) {
+          const int s = n % kStages;
+          ok = wait(&g.a_full[s], (n / kStages) & 1) && (n == 0 || wait(&g.s_free, (n - 1) & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {   // 32 keys of each half
-            const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
-            umma_bf16_ts(tmem + kAcc0, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, k0 + ((s * kKBytes) >> 4) + KTile::rows16(kk), id_q,
-                         n > 0 || part > 0 || i > 0, elected);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ts(tmem + kQS, tmem + kQOpQ + kk * 8, k0 + ((s * kKBytes) >> 4) + KTile<D>::cols16(kk), id_s, kk > 0, elected);
+          umma_commit_elected(&g.s_full, elected);
         }
-        if (!ok) break;
-        umma_commit_elected(&g.a_empty[s], elected);
-        if (next < r.last) dps(s1);
-        kt = next;
+        umma_commit_elected(&g.acc_full, elected);
+      }
+    } else {
+      const uint64_t v0 = VTile::desc(sv), k0 = KTile<D>::desc(sk);
+      // da . v of step n, when the last one has been read
+      const auto dps = [&](int n) {
+        const int s = n % kStages;
+        if (!wait(&g.b_full[s], (n / kStages) & 1) || (n > 0 && !wait(&g.dp_free, (n - 1) & 1))) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kDv / 16; ++kk)
+          umma_bf16_ts(tmem + kQDp, tmem + kQOpDa + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::cols16(kk), id_s, kk > 0, elected);
+        umma_commit_elected(&g.dp_full, elected);
+        umma_commit_elected(&g.b_empty[s], elected);
+        return true;
+      };
+      while (ok && jobs.next(job)) {
+        if (job.begin() >= job.r.last) continue;
+        ok = wait(&g.fixed_full, turn++ & 1) && dps(n);
+        bool first = true;
+        for (int kt = job.begin(); ok && kt < job.r.last; ++n) {
+          const int s = n % kStages, next = job.after(kt);
+          if (next < job.r.last) ok = dps(n + 1);
+          ok = ok && wait(&g.a_full[s], (n / kStages) & 1) && wait(&g.ds_full, n & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_bf16_ts(tmem + kQAcc, tmem + kQDs + kk * 8, k0 + ((s * kKBytes) >> 4) + KTile<D>::rows16(kk), id_q, !first || kk > 0,
+                         elected);
+          umma_commit_elected(&g.ds_free, elected);
+          umma_commit_elected(&g.a_empty[s], elected);
+          first = false;
+          kt = next;
+        }
+        umma_commit_elected(&g.acc_full, elected);
       }
     }
-    umma_commit_elected(&g.acc_full, elected);
-    mbar_wait(&g.acc_full, 0, nullptr, st, KID_ATTN_DQ);   // all products are done
+    umma_commit_elected(&g.end, elected);   // before the block leaves
+    mbar_wait(&g.end, 0, nullptr, st, KID_ATTN_DQ);
   } else {
     // this thread's row, and the half of the keys that its warpgroup takes
-    const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;
-    const float* stat = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;   // (row < Tp)
-    const float z0 = __ldcg(stat), delta = __ldcg(stat + p.Tp);
-    const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
-    const f2 sc = f2_make(p.scale_log2, p.scale_log2), mz = f2_make(z0, z0), md = f2_make(delta, delta);
+    const int half = warp >> 2, mine = threadIdx.x & 127;
+    const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + kQS + kHalf * half + quarter, tdp = tmem + kQDp + kHalf * half + quarter;
+    const uint32_t tds = tmem + kQDs + kHalf / 2 * half + quarter;
+    const f2 sc = f2_make(p.scale_log2, p.scale_log2);
+    uint8_t* stage = so + warp * kOutBytes;
+    // One warpgroup brings q into TMEM, the other da; the next job's are read while this one ends.
+    constexpr int kParts = (D > kDv ? D : kDv) / 8;
+    uint4 rows[kParts];
+    const int parts = half == 0 ? D / 8 : kDv / 8;
+    int start = -1;
+    const auto read_rows = [&](int tile, int head) {
+      const int row = tile * kTile + mine;
+      const uint4* from = reinterpret_cast<const uint4*>(half == 0 ? p.q + (static_cast<int64_t>(head) * p.T + row) * D
+                                                                   : p.da + (static_cast<int64_t>(row) * p.Hq + head) * kDv);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) rows[i] = i < parts && row < p.T ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+      start = start_of(row);
+    };
+    const auto store_rows = [&] {
+      const uint32_t to = tmem + (half == 0 ? kQOpQ : kQOpDa) + quarter;
+#pragma unroll
+      for (int i = 0; i < kParts; i += 4)
+        if (i < parts) {
+          const uint32_t w[16] = {rows[i].x,     rows[i].y,     rows[i].z,     rows[i].w,     rows[i + 1].x, rows[i + 1].y,
+                                  rows[i + 1].z, rows[i + 1].w, rows[i + 2].x, rows[i + 2].y, rows[i + 2].z, rows[i + 2].w,
+                                  rows[i + 3].x, rows[i + 3].y, rows[i + 3].z, rows[i + 3].w};
+          tmem_st16(to + 4 * i, w);
+        }
+      tmem_st_wait();
+    };
+    int n = 0, turn = 0;   // steps; jobs with any
     bool ok = true;
-    int n = 0;
-    for (int kt = kt0; kt < r.last; kt = next_of(kt), ++n) {
-      ok = mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DQ);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t x[64];
-      tmem_ld32(ts, x);
-      tmem_ld32(ts + 32, x + 32);
-      tmem_ld_wait();
-      arrive_warp(&g.s_free);
-      f2 w[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mz));
-        w[i] = f2_make(ex2(z.x), ex2(z.y));
-      }
-      const int j0 = kt * kTile + 64 * half;
-      const bool whole = __all_sync(0xffffffffu, sp.start >= 0 && j0 >= seen0 && j0 + 64 <= row + 1);
-      ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DQ);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_ld32(td + 32 * c, x);
-        tmem_ld_wait();
-        uint32_t out[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          out[i] = f2_to_bf16x2(f2_mul(f2_add(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), md), w[16 * c + i]));
-        if (!whole) {
-          uint32_t see = 0;
-          if (sp.start >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(sp.start, min(sink_end, row + 1), j0 + 32 * c);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) out[i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
-        }
-        tmem_st16(td + 16 * c, out);   // over what this warp has read
-        tmem_st_wait();
-        arrive_warp(&g.ds_full[c]);
-      }
-    }
-    if (ok) ok = mbar_wait(&g.acc_full, 0, &g.abort, st, KID_ATTN_DQ);
-    if (ok) {
-      tc_fence_after();
-      // each warpgroup writes one box of 64 columns (with d = 64 the first alone)
-      bool bad = false;
-      const bool some = kt0 < r.last;
-      uint8_t* stage = smem + half * kBox + (warp & 3) * 4096;
-      if (half < KB) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem + kAcc0 + quarter + 64 * half + 32 * c, o);
+    while (ok && jobs.next(job)) {
+      const int row = job.tile * kTile + mine, hq = job.head;
+      const bool some = job.begin() < job.r.last;
+      if (jobs.k == 1) read_rows(job.tile, hq);
+      const int begin = start, seen0 = begin < 0 ? INT_MAX : window_start(p, row, begin);
+      const int sink_end = begin < 0 ? 0 : begin + min(p.sinks, p.T);
+      if (some) {
+        store_rows();
+        arrive_warp(&g.fixed_full);
+        const float* stat = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;
+        const float z0 = __ldcg(stat), delta = __ldcg(stat + p.Tp);
+        const f2 mz = f2_make(z0, z0), md = f2_make(delta, delta);
+        // key tiles that every row of the warp sees whole
+        const int whole0 = (min(__reduce_max_sync(0xffffffffu, seen0), INT_MAX - kKeys) + kKeys - 1) / kKeys;
+        const int whole1 = __reduce_min_sync(0xffffffffu, row + 1) / kKeys;
+        for (int kt = job.begin(); kt < job.r.last; kt = job.after(kt), ++n) {
+          ok = mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t x[kHalf];
+          tmem_load<kHalf>(ts, x);
           tmem_ld_wait();
-          const bool in = 64 * half + 32 * c < D;
-          float big = 0.f;
+          arrive_warp(&g.s_free);
+          f2 w[kHalf / 2];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(o[i + 2 * k]) * p.scale, b = __uint_as_float(o[i + 2 * k + 1]) * p.scale;
-              big += fabsf(a) + fabsf(b);
-              w[k] = some ? pack_bf16x2(a, b) : 0u;
-            }
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + i / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < kHalf / 2; ++i) {
+            const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mz));
+            w[i] = f2_make(ex2(z.x), ex2(z.y));
           }
-          bad |= in && !(big < INFINITY);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0 && row < p.T) {
-          tma_store_3d(&tm_dq, stage, 64 * half, row, hq);
-          bulk_commit();
-          bulk_wait_all<0>();
+          ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_load<kHalf>(tdp, x);
+          tmem_ld_wait();
+          arrive_warp(&g.dp_free);
+          const bool free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);   // (looked at here, used below)
+          uint32_t out[kHalf / 2];
+#pragma unroll
+          for (int i = 0; i < kHalf / 2; ++i)
+            out[i] = f2_to_bf16x2(f2_mul(f2_add(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), md), w[i]));
+          if (__builtin_expect(kt < whole0 || kt >= whole1, 0)) {
+            const int j0 = kt * kKeys + kHalf * half;
+#pragma unroll
+            for (int c = 0; c < (kHalf + 31) / 32; ++c) {
+              uint32_t see = 0;
+              if (begin >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(begin, min(sink_end, row + 1), j0 + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 16 && 16 * c + i < kHalf / 2; ++i) out[16 * c + i] &= seen_halves(see, i);
+            }
+          }
+          ok = free || mbar_wait(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) break;
+          tmem_store<kHalf / 2>(tds, out);
+          tmem_st_wait();
+          arrive_warp(&g.ds_full);
         }
       }
-      __syncwarp();
-      const uint32_t again = __ballot_sync(0xffffffffu, bad && some && row < p.T);
-      if (lane == 0 && again) atomicOr(&g.again[warp & 3], again);
+      if (!ok) break;
+      const bool more = jobs.more;
+      if (more) read_rows(jobs.tile, jobs.head);   // the next job's, on their way while this one ends
+      if (some) ok = mbar_wait(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DQ);
+      if (!ok) break;
+      tc_fence_after();
+      // each warpgroup writes 64 columns (with d = 64 the first alone)
+      bool bad = false;
+      if (64 * half < D)
+        bad = write_box(tmem + kQAcc + quarter + 64 * half, min(64, D - 64 * half), p.scale, some, stage, &tm_dq, 64 * half, row, hq,
+                        p.T, nullptr);
+      // Rows that are not finite may owe that to what they do not see (0 * NaN):
+      // they are computed again from what they see, each warpgroup's columns by it.
+      uint32_t again = __ballot_sync(0xffffffffu, bad && row < p.T);
+      if (again) {
+        if (lane == 0) bulk_wait_all<0>();   // what they replace has been written
+        __syncwarp();
+        for (; again; again &= again - 1) dq_row<D>(p, row - lane + __ffs(again) - 1, hq, 2 * half, 2 * half + 2);
+      }
     }
+    if (lane == 0) bulk_wait_all<0>();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
-  // Rows that are not finite may owe that to what they do not see (0 * NaN):
-  // they are computed again from what they see.
-  if (warp < 4)
-    for (uint32_t again = g.again[warp]; again; again &= again - 1) dq_row<D>(p, r0 + warp * 32 + __ffs(again) - 1, hq);
 }
 
 // ---------------------------------------------------------------------------
-// dk and dv: 128 keys of a head, and the query tiles that see them, of all
-// query heads in turn, the keys along the rows:
+// dk and dv: 128 keys of a head, and the queries that see them, of all query
+// heads in turn, the keys along the rows; per step
 //   S^T = k q^T, P^T = e^(S^T - lse), dv += P^T da
 //   dP^T = v da^T, ds^T = P^T (dP^T - delta), dk += ds^T q
-// issued dv(i), S(i + 1), dk(i), dP(i + 1): each step's forming of P^T and ds^T is
-// covered by two products.
 // ---------------------------------------------------------------------------
+struct DkvJob {
+  int tile, head, count, tiles;   // steps, and those of one query head
+};
+struct DkvJobs {
+  const AttnArgs& p;
+  const Shared& g;
+  int total, queries, k, head;
+  int4 r;
+  bool more;
+  __device__ DkvJobs(const AttnArgs& p, const Shared& g, int total, int queries) : p(p), g(g), total(total), queries(queries), k(0) { fetch(); }
+  __device__ void fetch() {
+    if (!p.spans) {
+      more = k == 0;
+      return;
+    }
+    const int i = job_of(k), at = i / p.H;
+    more = i < total;
+    head = i - at * p.H;
+    if (more) r = __ldcg(p.jobs[1] + at);
+  }
+  __device__ bool next(DkvJob& j) {
+    if (!more) return false;
+    int end;
+    if (!p.spans) {
+      j.tile = blockIdx.x / p.H;
+      j.head = blockIdx.x - j.tile * p.H;
+      end = max(max(g.hi[0], g.hi[1]), max(g.hi[2], g.hi[3]));
+    } else {
+      j.tile = r.x;
+      j.head = head;
+      end = r.y;
+    }
+    j.tiles = (max(0, end - j.tile * kTile) + queries - 1) / queries;
+    j.count = j.tiles * p.G;
+    ++k;
+    fetch();
+    return true;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_da,
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
-               const __grid_constant__ AttnArgs p, DevStatus st) {
-  using KTile = AttnTile<D, kTile>;
-  constexpr int kKBytes = KTile::kBytes, kVBytes = VTile::kBytes, SQ = q_stages(D), SD = da_stages(D);
+               const __grid_constant__ AttnArgs p, int total, DevStatus st) {
+  using Q = QTile<D>;
+  using Da = DaTile<D>;
+  constexpr int QN = queries(D), kHalf = QN / 2, SQ = q_stages(D), SD = da_stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
-  __shared__ alignas(128) float stats[SQ][2][kTile];   // -lse (base 2) and -delta of a tile of queries
+  __shared__ alignas(128) float stats[SQ][2][QN];   // -lse (base 2) and -delta of a step's queries
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sk = smem, *sv = sk + kKBytes, *sq = sv + kVBytes, *sd = sq + SQ * kKBytes;
+  uint8_t *sk = smem, *sv = sk + Fixed<D>::kBytes, *sq = sv + Fixed<kDv>::kBytes, *sd = sq + SQ * Q::kBytes, *so = sd + SD * Da::kBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) init_barriers(g, 2);
-  if (threadIdx.x < 4) g.again[threadIdx.x] = 0;
+  if (threadIdx.x == 0) init_barriers(g, 1, 2);
   if (warp == 9) {
     tmem_alloc(&g.tmem, 512);
     tmem_relinquish();
   }
   wait_for_previous();
-  const Place at = place_of(p.order[1], p.H);
-  const int h = at.head, r0 = at.tile * kTile;
-  // queries [row, end) see this thread's key; those from ds0 on pass something on
-  const int half = warp >> 2, row = r0 + (threadIdx.x & 127);
-  int begin = row, end = row, ds0 = row;
-  if (warp < 8) {
-    const Span sp = row < p.T ? span_of(p, row) : Span{-1, -1};
-    if (sp.start >= 0) {
-      end = last_seer(p, row, sp);
-      ds0 = row + (alone(p, row, sp.start) ? 1 : 0);
-    }
-    const int hi = __reduce_max_sync(0xffffffffu, end > row ? end : -1), lo = __reduce_min_sync(0xffffffffu, end > row ? row : INT_MAX);
-    if (lane == 0 && half == 0) g.hi[warp] = hi, g.lo[warp] = lo;
+  const auto span_at = [&](int row) {
+    if (row >= p.T) return Span{-1, -1};
+    if (!p.spans) return span_of(p, row);
+    const int2 s = __ldcg(p.spans + row);
+    return Span{s.x, s.y};
+  };
+  if (!p.spans && warp < 4) {   // a call without a plan: the block finds out about its rows by itself
+    const int row = static_cast<int>(blockIdx.x) / p.H * kTile + threadIdx.x;
+    const Span sp = span_at(row);
+    const int hi = __reduce_max_sync(0xffffffffu, sp.start < 0 ? -1 : last_seer(p, row, sp));
+    if (lane == 0) g.hi[warp] = hi;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = g.tmem, quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const int hi = max(max(g.hi[0], g.hi[1]), max(g.hi[2], g.hi[3]));
-  const int tiles = hi < 0 ? 0 : (hi + kTile - 1) / kTile - at.tile;   // query tiles of a head, from this one on
-  const int count = tiles * p.G;
+  const uint32_t tmem = g.tmem;
+  DkvJobs jobs(p, g, total, QN);
+  DkvJob job;
 
   if (warp == 8) {
-    if (lane == 0 && count > 0) {
-      mbar_arrive_expect_tx(&g.fixed_full, kKBytes + kVBytes);
-      KTile::load(sk, &tm_k, &g.fixed_full, r0, h);
-      VTile::load(sv, &tm_v, &g.fixed_full, r0, h);
-      int na = 0, nb = 0;
-      for (; nb < count; ++nb) {
-        // da of this step behind q of it and of as many as there is room for
-        const int s = nb % SD, hq = h * p.G + nb / tiles, i0 = r0 + (nb % tiles) * kTile;
-        bool ok = true;
-        for (; na < count && na <= nb + (SQ - SD); ++na) {
-          const int sa = na % SQ, ha = h * p.G + na / tiles, ia = r0 + (na % tiles) * kTile;
+    if (lane == 0) {
+      int na = 0, nb = 0, turn = 0;   // steps whose q, whose da has been asked for; jobs with any
+      bool ok = true;
+      while (ok && jobs.next(job)) {
+        if (job.count == 0) continue;
+        const int r0 = job.tile * kTile;
+        ok = mbar_wait(&g.fixed_empty, (turn & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&g.fixed_full, Fixed<D>::kBytes + Fixed<kDv>::kBytes);
+        Fixed<D>::load(sk, &tm_k, &g.fixed_full, r0, job.head);
+        Fixed<kDv>::load(sv, &tm_v, &g.fixed_full, r0, job.head);
+        ++turn;
+        int i0 = r0, hq = job.head * p.G;
+        for (int n = 0, left = job.tiles; n < job.count; ++n) {
+          const int sa = na % SQ, sb = nb % SD;
           ok = mbar_wait(&g.a_empty[sa], (na / SQ & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
           if (!ok) break;
-          mbar_arrive_expect_tx(&g.a_full[sa], kKBytes + sizeof(stats[0]));
-          KTile::load(sq + sa * kKBytes, &tm_q, &g.a_full[sa], ia, ha);
+          mbar_arrive_expect_tx(&g.a_full[sa], Q::kBytes + sizeof(stats[0]));
+          Q::load(sq + sa * Q::kBytes, &tm_q, &g.a_full[sa], i0, hq);
           for (int b = 0; b < 2; ++b)
-            bulk_load(stats[sa][b], p.stat + (static_cast<int64_t>(ha) * 2 + b) * p.Tp + ia, sizeof(stats[sa][b]), &g.a_full[sa]);
+            bulk_load(stats[sa][b], p.stat + (static_cast<int64_t>(hq) * 2 + b) * p.Tp + i0, sizeof(stats[sa][b]), &g.a_full[sa]);
+          ++na;
+          ok = mbar_wait(&g.b_empty[sb], (nb / SD & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&g.b_full[sb], Da::kBytes);
+          for (int b = 0; b < Da::kBoxes; ++b)
+            tma_load_2d(sd + sb * Da::kBytes + b * Da::kBox, &tm_da, &g.b_full[sb], hq * kDv + b * Da::kCols, i0);
+          ++nb;
+          i0 += QN;
+          if (--left == 0) {
+            left = job.tiles;
+            i0 = r0;
+            ++hq;
+          }
         }
-        if (!ok || !mbar_wait(&g.b_empty[s], (nb / SD & 1) ^ 1, &g.abort, st, KID_ATTN_DKV)) break;
-        mbar_arrive_expect_tx(&g.b_full[s], kVBytes);
-        for (int b = 0; b < 2; ++b) tma_load_2d(sd + s * kVBytes + b * kBox, &tm_da, &g.b_full[s], hq * kDv + b * 64, i0);
       }
-      mbar_wait(&g.fixed_full, 0, nullptr, st, KID_ATTN_DKV);
       // every copy has landed before the block may leave
+      if (turn > 0) mbar_wait(&g.fixed_full, (turn - 1) & 1, nullptr, st, KID_ATTN_DKV);
       for (int i = max(0, na - SQ); i < na; ++i) mbar_wait(&g.a_full[i % SQ], (i / SQ) & 1, nullptr, st, KID_ATTN_DKV);
       for (int i = max(0, nb - SD); i < nb; ++i) mbar_wait(&g.b_full[i % SD], (i / SD) & 1, nullptr, st, KID_ATTN_DKV);
     }
-  } else if (warp >= 9) {
-    // As for dq: one warp issues dv and the scores, the other dk and dP.
-    constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile, false), id_k = idesc_bf16_f32(kTile, D, true),
+  } else if (warp > 8) {
+    // As for dq: one warp issues the scores and dv, the other da . v and dk.
+    constexpr uint32_t id_s = idesc_bf16_f32(kTile, QN, false), id_k = idesc_bf16_f32(kTile, D, true),
                        id_v = idesc_bf16_f32(kTile, kDv, true);
     const uint32_t elected = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DKV));
     };
-    bool ok = count > 0 && wait(&g.fixed_full, 0);
+    bool ok = true;
+    int n = 0, turn = 0;   // steps; jobs with any
     if (warp == 9) {
-      const uint64_t k0 = KTile::desc(sk), q0 = KTile::desc(sq), d0 = VTile::desc(sd);
-      const auto scores = [&](int s) {
+      const uint64_t k0 = Fixed<D>::desc(sk), q0 = Q::desc(sq), d0 = Da::desc(sd);
+      // scores of step n, when the last ones have been read
+      const auto scores = [&](int n) {
+        const int s = n % SQ;
+        if (!wait(&g.a_full[s], (n / SQ) & 1) || (n > 0 && !wait(&g.s_free, (n - 1) & 1))) return false;
+        tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ss(tmem + kScores, k0 + KTile::cols16(kk), q0 + ((s * kKBytes) >> 4) + KTile::cols16(kk), id_s, kk > 0, elected);
+          umma_bf16_ss(tmem + k_s(D), k0 + Fixed<D>::cols16(kk), q0 + ((s * Q::kBytes) >> 4) + Q::cols16(kk), id_s, kk > 0, elected);
         umma_commit_elected(&g.s_full, elected);
+        return true;
       };
-      ok = ok && wait(&g.a_full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        scores(0);
-      }
-      for (int n = 0; ok && n < count; ++n) {
-        const int s = n % SD, s1 = (n + 1) % SQ;
-        ok = wait(&g.b_full[s], (n / SD) & 1) && (n + 1 == count || wait(&g.a_full[s1], ((n + 1) / SQ) & 1)) &&
-             wait(&g.p_full[0], n & 1);
-        if (!ok) break;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (part == 1) ok = wait(&g.p_full[1], n & 1);
+      while (ok && jobs.next(job)) {
+        if (job.count == 0) continue;
+        ok = wait(&g.fixed_full, turn & 1) && scores(n);
+        for (int i = 0; ok && i < job.count; ++i, ++n) {
+          const int s = n % SD;
+          if (i + 1 < job.count) ok = scores(n + 1);
+          if (ok && (i + 2 == job.count || job.count == 1)) umma_commit_elected(&g.fixed_empty, elected);   // the last use of the job's keys
+          if (i == 0 && turn > 0) ok = ok && wait(&g.acc_free[0], (turn - 1) & 1);   // the last job's dv has been read
+          ok = ok && wait(&g.b_full[s], (n / SD) & 1) && wait(&g.p_full, n & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {   // 32 queries of each half
-            const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
-            umma_bf16_ts(tmem + kAcc0, tmem + kScores + (kk / 4) * 64 + (kk % 4) * 8, d0 + ((s * kVBytes) >> 4) + VTile::rows16(kk), id_v,
-                         n > 0 || part > 0 || i > 0, elected);
-          }
+          for (int kk = 0; kk < QN / 16; ++kk)
+            umma_bf16_ts(tmem + k_dv(D), tmem + k_p(D) + kk * 8, d0 + ((s * Da::kBytes) >> 4) + Da::rows16(kk), id_v, i > 0 || kk > 0,
+                         elected);
+          umma_commit_elected(&g.p_free, elected);
+          umma_commit_elected(&g.b_empty[s], elected);
         }
-        if (!ok) break;
-        umma_commit_elected(&g.b_empty[s], elected);
-        if (n + 1 < count) scores(s1);
+        umma_commit_elected(&g.acc_full, elected);
+        ++turn;
       }
     } else {
-      const uint64_t v0 = VTile::desc(sv), d0 = VTile::desc(sd), q0 = KTile::desc(sq);
-      const auto dps = [&](int s) {
+      const uint64_t v0 = Fixed<kDv>::desc(sv), d0 = Da::desc(sd), q0 = Q::desc(sq);
+      const auto dps = [&](int n) {
+        const int s = n % SD;
+        if (!wait(&g.b_full[s], (n / SD) & 1) || (n > 0 && !wait(&g.dp_free, (n - 1) & 1))) return false;
+        tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kDv / 16; ++kk)
-          umma_bf16_ss(tmem + kDp, v0 + VTile::cols16(kk), d0 + ((s * kVBytes) >> 4) + VTile::cols16(kk), id_s, kk > 0, elected);
+          umma_bf16_ss(tmem + k_dp(D), v0 + Fixed<kDv>::cols16(kk), d0 + ((s * Da::kBytes) >> 4) + Da::cols16(kk), id_s, kk > 0, elected);
         umma_commit_elected(&g.dp_full, elected);
         umma_commit_elected(&g.b_empty[s], elected);
+        return true;
       };
-      ok = ok && wait(&g.b_full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        dps(0);
-      }
-      for (int n = 0; ok && n < count; ++n) {
-        const int s = n % SQ, s1 = (n + 1) % SD;
-        ok = wait(&g.a_full[s], (n / SQ) & 1) && (n + 1 == count || wait(&g.b_full[s1], ((n + 1) / SD) & 1)) &&
-             wait(&g.ds_full[0], n & 1);
-        if (!ok) break;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (part == 1) ok = wait(&g.ds_full[1], n & 1);
+      while (ok && jobs.next(job)) {
+        if (job.count == 0) continue;
+        ok = wait(&g.fixed_full, turn & 1) && dps(n);
+        for (int i = 0; ok && i < job.count; ++i, ++n) {
+          const int s = n % SQ;
+          if (i + 1 < job.count) ok = dps(n + 1);
+          if (ok && (i + 2 == job.count || job.count == 1)) umma_commit_elected(&g.fixed_empty, elected);   // the last use of the job's keys
+          if (i == 0 && turn > 0) ok = ok && wait(&g.acc_free[1], (turn - 1) & 1);   // the last job's dk has been read
+          ok = ok && wait(&g.a_full[s], (n / SQ) & 1) && wait(&g.ds_full, n & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {   // 32 queries of each half
-            const int kk = (i >> 1) * 4 + 2 * part + (i & 1);
-            umma_bf16_ts(tmem + kAcc1, tmem + kDp + (kk / 4) * 64 + (kk % 4) * 8, q0 + ((s * kKBytes) >> 4) + KTile::rows16(kk), id_k,
-                         n > 0 || part > 0 || i > 0, elected);
-          }
+          for (int kk = 0; kk < QN / 16; ++kk)
+            umma_bf16_ts(tmem + k_dk(D), tmem + k_ds(D) + kk * 8, q0 + ((s * Q::kBytes) >> 4) + Q::rows16(kk), id_k, i > 0 || kk > 0,
+                         elected);
+          umma_commit_elected(&g.ds_free, elected);
+          umma_commit_elected(&g.a_empty[s], elected);
         }
-        if (!ok) break;
-        umma_commit_elected(&g.a_empty[s], elected);
-        if (n + 1 < count) dps(s1);
+        umma_commit_elected(&g.acc_full, elected);
+        ++turn;
       }
     }
-    umma_commit_elected(&g.acc_full, elected);
-    mbar_wait(&g.acc_full, 0, nullptr, st, KID_ATTN_DKV);   // all products are done
+    umma_commit_elected(&g.end, elected);   // before the block leaves
+    mbar_wait(&g.end, 0, nullptr, st, KID_ATTN_DKV);
   } else {
     // this thread's key, and the half of the queries that its warpgroup takes
-    const uint32_t ts = tmem + kScores + 64 * half + quarter, td = tmem + kDp + 64 * half + quarter;
+    const int half = warp >> 2, mine = threadIdx.x & 127;
+    const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + k_s(D) + kHalf * half + quarter, tp = tmem + k_p(D) + kHalf / 2 * half + quarter;
+    const uint32_t tdp = tmem + k_dp(D) + kHalf * half + quarter, tds = tmem + k_ds(D) + kHalf / 2 * half + quarter;
     const f2 sc = f2_make(p.scale_log2, p.scale_log2);
+    uint8_t* stage = so + warp * kOutBytes;
+    int n = 0, turn = 0;   // steps; jobs with any
     bool ok = true;
-    for (int n = 0; n < count; ++n) {
-      const int s = n % SQ, i0 = r0 + (n % tiles) * kTile + 64 * half;
-      ok = mbar_wait(&g.a_full[s], (n / SQ) & 1, &g.abort, st, KID_ATTN_DKV) && mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t stat = smem_u32(stats[s][0]) + 4 * 64 * half;
-      const bool whole = __all_sync(0xffffffffu, i0 >= ds0 && i0 + 64 <= end);
-      uint32_t x[64];
-      tmem_ld32(ts, x);
-      tmem_ld32(ts + 32, x + 32);
-      tmem_ld_wait();
-      f2 w[32];
+    Span ahead{-1, -1};
+    while (ok && jobs.next(job)) {
+      const int r0 = job.tile * kTile, row = r0 + mine;
+      if (jobs.k == 1) ahead = span_at(row);   // the others are read ahead
+      // queries [row, end) see this thread's key; those from ds0 on pass something on
+      const int end = ahead.start < 0 ? row : last_seer(p, row, ahead);
+      const int ds0 = row + (ahead.start >= 0 && alone(p, row, ahead.start) ? 1 : 0);
+      int i0 = r0 + kHalf * half;
+      for (int i = 0, left = job.tiles; i < job.count; ++i, ++n) {
+        const int s = n % SQ;
+        ok = mbar_wait(&g.a_full[s], (n / SQ) & 1, &g.abort, st, KID_ATTN_DKV) &&
+             mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t stat = smem_u32(stats[s][0]) + 4 * kHalf * half;
+        const bool whole = __all_sync(0xffffffffu, i0 >= ds0 && i0 + kHalf <= end);
+        uint32_t x[kHalf], out[kHalf / 2];
+        tmem_load<kHalf>(ts, x);
+        tmem_ld_wait();
+        arrive_warp(&g.s_free);
+        bool free = n == 0 || mbar_try_wait(&g.p_free, (n - 1) & 1);   // (looked at here, used below)
+        f2 w[kHalf / 2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t out[16];
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int j = 0; j < kHalf / 2; j += 2) {
           f2 z[2];
-          lds_f2x2(stat + 128 * c + 8 * i, z);
+          lds_f2x2(stat + 8 * j, z);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int at = 16 * c + i + k;
-            const float2 y = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * at]), __uint_as_float(x[2 * at + 1])), sc, z[k]));
-            w[at] = f2_make(ex2(y.x), ex2(y.y));
-            out[i + k] = f2_to_bf16x2(w[at]);
+            const float2 y = f2_split(
+                f2_fma(f2_make(__uint_as_float(x[2 * (j + k)]), __uint_as_float(x[2 * (j + k) + 1])), sc, z[k]));
+            w[j + k] = f2_make(ex2(y.x), ex2(y.y));
+            out[j + k] = f2_to_bf16x2(w[j + k]);
           }
         }
-        if (!whole) {
-          const uint32_t see = bits(begin, end, i0 + 32 * c);
+        if (__builtin_expect(!whole, 0)) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) out[i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+          for (int c = 0; c < (kHalf + 31) / 32; ++c) {
+            const uint32_t see = bits(row, end, i0 + 32 * c);
+#pragma unroll
+            for (int j = 0; j < 16 && 16 * c + j < kHalf / 2; ++j) out[16 * c + j] &= seen_halves(see, j);
+          }
         }
-        tmem_st16(ts + 16 * c, out);   // over what this warp has read
+        ok = free || mbar_wait(&g.p_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DKV);
+        if (!ok) break;
+        tmem_store<kHalf / 2>(tp, out);
         tmem_st_wait();
-        arrive_warp(&g.p_full[c]);
-      }
-      ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DKV);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_ld32(td + 32 * c, x);
+        arrive_warp(&g.p_full);
+        ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_load<kHalf>(tdp, x);
         tmem_ld_wait();
-        uint32_t out[16];
+        arrive_warp(&g.dp_free);
+        free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int j = 0; j < kHalf / 2; j += 2) {
           f2 z[2];
-          lds_f2x2(stat + 4 * kTile + 128 * c + 8 * i, z);
+          lds_f2x2(stat + 4 * QN + 8 * j, z);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            out[i + k] = f2_to_bf16x2(f2_mul(f2_add(f2_make(__uint_as_float(x[2 * (i + k)]), __uint_as_float(x[2 * (i + k) + 1])), z[k]),
-                                             w[16 * c + i + k]));
+            out[j + k] = f2_to_bf16x2(
+                f2_mul(f2_add(f2_make(__uint_as_float(x[2 * (j + k)]), __uint_as_float(x[2 * (j + k) + 1])), z[k]), w[j + k]));
         }
-        if (!whole) {
-          const uint32_t see = bits(ds0, end, i0 + 32 * c);
+        if (__builtin_expect(!whole, 0)) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) out[i] &= (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+          for (int c = 0; c < (kHalf + 31) / 32; ++c) {
+            const uint32_t see = bits(ds0, end, i0 + 32 * c);
+#pragma unroll
+            for (int j = 0; j < 16 && 16 * c + j < kHalf / 2; ++j) out[16 * c + j] &= seen_halves(see, j);
+          }
         }
-        tmem_st16(td + 16 * c, out);
+        ok = free || mbar_wait(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DKV);
+        if (!ok) break;
+        tmem_store<kHalf / 2>(tds, out);
         tmem_st_wait();
-        arrive_warp(&g.ds_full[c]);
+        arrive_warp(&g.ds_full);
+        i0 += QN;
+        if (--left == 0) {
+          left = job.tiles;
+          i0 = r0 + kHalf * half;
+        }
       }
-    }
-    if (ok) ok = mbar_wait(&g.acc_full, 0, &g.abort, st, KID_ATTN_DKV);
-    if (ok) {
+      if (!ok) break;
+      const bool some = job.count > 0;
+      if (jobs.more) ahead = span_at(jobs.r.x * kTile + mine);   // the next job's
+      if (some) ok = mbar_wait(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DKV);
+      if (!ok) break;
       tc_fence_after();
       // one warpgroup writes dv, the other dk
-      const int width = half == 0 ? kDv : D, nb = (width + 63) / 64;
-      const float f = half == 0 ? 1.f : p.scale;
-      uint8_t* stage = (half == 0 ? sv : sq) + (warp & 3) * nb * 4096;
-      bool bad = false;
-      for (int c = 0; c < 2 * nb; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tmem + (half == 0 ? kAcc0 : kAcc1) + quarter + 32 * c, o);
-        tmem_ld_wait();
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float a = __uint_as_float(o[i + 2 * k]) * f, b = __uint_as_float(o[i + 2 * k + 1]) * f;
-            big += fabsf(a) + fabsf(b);
-            w[k] = count > 0 ? pack_bf16x2(a, b) : 0u;
-          }
-          *reinterpret_cast<uint4*>(stage + (c >> 1) * 4096 + lane * 128 + (((4 * (c & 1) + i / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        bad |= 32 * c < width && !(big < INFINITY);
+      bool bad;
+      if (half == 0) {
+        bad = write_box(tmem + k_dv(D) + quarter, 64, 1.f, some, stage, &tm_dv, 0, row, job.head, p.T, nullptr);
+        bad |= write_box(tmem + k_dv(D) + quarter + 64, 64, 1.f, some, stage, &tm_dv, 64, row, job.head, p.T, some ? &g.acc_free[0] : nullptr);
+      } else {
+        constexpr bool kTwo = D > 64;
+        bad = write_box(tmem + k_dk(D) + quarter, 64, p.scale, some, stage, &tm_dk, 0, row, job.head, p.T,
+                        !kTwo && some ? &g.acc_free[1] : nullptr);
+        if (kTwo)
+          bad |= write_box(tmem + k_dk(D) + quarter + (D == 96 ? 32 : 64), D == 96 ? 64 : D - 64, p.scale, some, stage, &tm_dk,
+                           D == 96 ? 32 : 64, row, job.head, p.T, some ? &g.acc_free[1] : nullptr);
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0 && row < p.T) {
-        for (int b = 0; b < nb; ++b) tma_store_3d(half == 0 ? &tm_dv : &tm_dk, stage + b * 4096, 64 * b, row, h);
-        bulk_commit();
-        bulk_wait_all<0>();
+      uint32_t again = __ballot_sync(0xffffffffu, bad && row < p.T);   // as for dq
+      if (again) {
+        if (lane == 0) bulk_wait_all<0>();
+        __syncwarp();
+        for (; again; again &= again - 1) dkv_row<D>(p, row - lane + __ffs(again) - 1, job.head, half == 0);
       }
-      __syncwarp();
-      const uint32_t again = __ballot_sync(0xffffffffu, bad && count > 0 && row < p.T);
-      if (lane == 0 && again) atomicOr(&g.again[warp & 3], again);
     }
+    if (lane == 0) bulk_wait_all<0>();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
-  if (warp < 4)   // as for dq
-    for (uint32_t again = g.again[warp]; again; again &= again - 1) dkv_row<D>(p, r0 + warp * 32 + __ffs(again) - 1, h);
 }
 
 template <class... Args>
@@ -651,23 +837,31 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  using KTile = AttnTile<D, kTile>;
-  CUtensorMap q, k, v, da, dq, dk, dv;
-  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, KTile::kCols, kTile, 1, KTile::kSwizzle) ||
-      !map3d(&k, bf16, 2, a.k, D, a.T, a.H, KTile::kCols, kTile, 1, KTile::kSwizzle) ||
-      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kTile, 1, VTile::kSwizzle) ||
-      !map2d_bf16(&da, a.da, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, kTile) ||
+  using Q = QTile<D>;
+  using K = KTile<D>;
+  using F = Fixed<D>;
+  using Fv = Fixed<kDv>;
+  CUtensorMap q, da, k, v, steps_k, steps_v, dq, dk, dv;
+  if (!map3d(&q, bf16, 2, a.q, D, a.T, a.Hq, Q::kCols, queries(D), 1, Q::kSwizzle) ||
+      !map2d_bf16(&da, a.da, static_cast<uint64_t>(a.Hq) * kDv, a.T, DaTile<D>::kCols, queries(D)) ||
+      !map3d(&k, bf16, 2, a.k, D, a.T, a.H, F::kCols, kTile, 1, F::kSwizzle) ||
+      !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, Fv::kCols, kTile, 1, Fv::kSwizzle) ||
+      !map3d(&steps_k, bf16, 2, a.k, D, a.T, a.H, K::kCols, kKeys, 1, K::kSwizzle) ||
+      !map3d(&steps_v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kKeys, 1, VTile::kSwizzle) ||
       !map3d(&dq, bf16, 2, a.dq, D, a.T, a.Hq, 64, 32, 1, sw) || !map3d(&dk, bf16, 2, a.dk, D, a.T, a.H, 64, 32, 1, sw) ||
       !map3d(&dv, bf16, 2, a.dv, kDv, a.T, a.H, 64, 32, 1, sw))
     return cudaErrorInvalidValue;
-  const int tiles = a.Tp / kTile;
-  if (static_cast<int64_t>(tiles) * a.Hq <= device_sms()) a.order[0] = a.order[1] = nullptr;   // all blocks start at once
-  const unsigned prep = (a.order[0] ? 2 : 0) + static_cast<unsigned>(tiles) * a.Hq;
-  e = launch_dependent(delta_kernel, dim3(prep), kPrepThreads, 0, s, a, tiles, st);
+  const int sms = device_sms(), tiles = (a.T + kTile - 1) / kTile;
+  const bool plan = tiles * a.Hq > sms;   // else each block has one job
+  if (!plan) a.spans = nullptr;
+  const int plan_blocks = plan ? (a.Tp + kPlanThreads - 1) / kPlanThreads : 0, row_blocks = (a.Tp + kPrepRows - 1) / kPrepRows;
+  e = launch_dependent(delta_kernel, dim3(static_cast<unsigned>(plan_blocks + row_blocks * a.Hq)), kPlanThreads, 0, s, a, plan_blocks,
+                       row_blocks, st);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(dkv_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.H), kThreads, dkv_smem<D>(), s, q, da, k, v, dk, dv, a, st);
+  e = launch_dependent(dkv_kernel<D>, dim3(std::min(sms, tiles * a.H)), kThreads, dkv_smem<D>(), s, q, da, k, v, dk, dv, a, tiles * a.H, st);
   if (e != cudaSuccess) return e;
-  return launch_dependent(dq_kernel<D>, dim3(static_cast<unsigned>(tiles) * a.Hq), kThreads, dq_smem<D>(), s, k, v, dq, a, st);
+  return launch_dependent(dq_kernel<D>, dim3(std::min(sms, tiles * a.Hq)), kThreads, dq_smem<D>(), s, steps_k, steps_v, dq, a, tiles * a.Hq,
+                          st);
 }
 
 }  // namespace

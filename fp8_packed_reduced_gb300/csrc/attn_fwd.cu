@@ -15,6 +15,7 @@
 // most 2^8, and a bf16 holds them as exactly as those below one.  They are
 // rounded to bf16 (2^-8) for the product with v; the sum and lse use them
 // unrounded.
+#include <algorithm>
 #include <atomic>
 
 #include "attn.cuh"
@@ -33,10 +34,11 @@ template <int D>
 using KTile = AttnTile<D, kKeys>;
 using VTile = AttnTile<kDv, kKeys>;
 constexpr int kMaxStages = 6;
-__host__ __device__ constexpr int stages(int d) { return d == 64 ? 6 : d == 96 ? 5 : 4; }   // as many as fit
+__host__ __device__ constexpr int stages(int d) { return d == 64 ? 5 : d == 96 ? 4 : 3; }   // as many as fit
+constexpr int kOutBytes = 32 * 128;          // of a softmax warp's output, 32 rows x 64 columns at a time
 template <int D>
 constexpr int smem_bytes() {
-  return 1024 + 2 * QTile<D>::kBytes + stages(D) * (KTile<D>::kBytes + VTile::kBytes);
+  return 1024 + 2 * QTile<D>::kBytes + stages(D) * (KTile<D>::kBytes + VTile::kBytes) + 8 * kOutBytes;
 }
 // Columns of TMEM: scores and probabilities of the tiles, then their accumulators.
 __device__ constexpr uint32_t s_col(int t) { return t * (kKeys + kKeys / 2); }
@@ -45,41 +47,87 @@ __device__ constexpr uint32_t o_col(int t) { return 256 + t * kDv; }
 static_assert(p_col(1) + kKeys / 2 <= o_col(0), "scores reach into the accumulators");
 
 struct Shared {
-  uint64_t q_full, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  uint64_t s_full[2], s_free[2], p_full[2], o_done[2];   // o_done: a step's product with v has been added
-  uint64_t end;                                          // all products are done
+  uint64_t q_full, q_empty, k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+  uint64_t s_full[2], s_free[2], p_full[2];
+  uint64_t o_done[2], o_free[2];   // a step's product with v has been added; O of a job has been read
+  uint64_t end;                    // all products are done
   uint32_t tmem;
   int abort;
   int lo[2][4], hi[2][4], start[2][4];
-  Range range[2];
+  Range range[2];                  // of a block's only job, without a plan
 };
 
-// The next key tile at or after kt that either query tile needs, or INT_MAX.
-__device__ __forceinline__ int next_tile(const Range& a, const Range& b, int kt) {
-  if (a.has(kt) || b.has(kt)) return kt;
-  int n = INT_MAX;
-  const int at[4] = {a.sink0 < a.sink1 ? a.sink0 : INT_MAX, a.first < a.last ? a.first : INT_MAX,
-                     b.sink0 < b.sink1 ? b.sink0 : INT_MAX, b.first < b.last ? b.first : INT_MAX};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (at[i] >= kt) n = min(n, at[i]);
-  return n;
-}
+// The jobs of a block, one after the other: 256 query rows of a head.
+struct Job {
+  int tile, head;
+  Range range[2];
+  // The key tiles: [a0, a1), then [b0, b1); those that neither query tile needs
+  // (between the first tokens of two sequences) pass unused.
+  int a0, a1, b0, b1;
+  __device__ void steps() {
+    const Range &x = range[0], &y = range[1];
+    b0 = min(x.first < x.last ? x.first : INT_MAX, y.first < y.last ? y.first : INT_MAX);
+    b1 = max(x.last, y.last);
+    // (first tokens of a sequence that starts among the rows lie in the second part)
+    const bool sx = x.sink0 < min(x.sink1, b0), sy = y.sink0 < min(y.sink1, b0);
+    a0 = min(sx ? x.sink0 : b0, sy ? y.sink0 : b0);
+    a1 = sx || sy ? min(b0, max(sx ? x.sink1 : 0, sy ? y.sink1 : 0)) : b0;
+  }
+  __device__ int begin() const { return a0; }
+  __device__ int after(int kt) const { return kt + 1 == a1 ? b0 : kt + 1; }   // (past b1: the end)
+};
+struct Jobs {
+  const AttnArgs& p;
+  const Shared& g;
+  int total, k, head;
+  int4 r[3];   // the next job
+  bool more;
+  __device__ Jobs(const AttnArgs& p, const Shared& g, int total) : p(p), g(g), total(total), k(0) { fetch(); }
+  __device__ void fetch() {
+    if (!p.spans) {
+      more = k == 0;
+      return;
+    }
+    const int i = job_of(k), at = i / p.Hq;
+    more = i < total;
+    head = i - at * p.Hq;
+    if (more)
+      for (int c = 0; c < 3; ++c) r[c] = __ldcg(p.jobs[0] + 3 * at + c);
+  }
+  __device__ bool next(Job& j) {
+    if (!more) return false;
+    if (!p.spans) {
+      j.tile = blockIdx.x / p.Hq;
+      j.head = blockIdx.x - j.tile * p.Hq;
+      j.range[0] = g.range[0];
+      j.range[1] = g.range[1];
+    } else {
+      j.tile = r[0].x;
+      j.head = head;
+      for (int c = 0; c < 2; ++c) j.range[c] = Range{r[1 + c].x, r[1 + c].y, r[1 + c].z, r[1 + c].w};
+    }
+    j.steps();
+    ++k;
+    fetch();
+    return true;
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_a,
-                   const __grid_constant__ AttnArgs p, DevStatus st) {
+                   const __grid_constant__ AttnArgs p, int total, DevStatus st) {
   constexpr int kQBytes = QTile<D>::kBytes, kKBytes = KTile<D>::kBytes, kVBytes = VTile::kBytes, kStages = stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sq = smem, *sk = sq + 2 * kQBytes, *sv = sk + kStages * kKBytes;
+  uint8_t *sq = smem, *sk = sq + 2 * kQBytes, *sv = sk + kStages * kKBytes, *so = sv + kStages * kVBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     g.abort = 0;
     mbar_init(&g.q_full, 1);
+    mbar_init(&g.q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&g.k_full[s], 1);
       mbar_init(&g.k_empty[s], 1);
@@ -91,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&g.s_free[t], 4);
       mbar_init(&g.p_full[t], 4);
       mbar_init(&g.o_done[t], 1);
+      mbar_init(&g.o_free[t], 4);
     }
     mbar_init(&g.end, 3);
     fence_mbar_init();
@@ -100,52 +149,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   wait_for_previous();
-  const Place at = place_of(p.order[0], p.Hq);
-  const int hq = at.head, h = hq / p.G, r0 = at.tile * kRows;
-  if (blockIdx.x == 0) check_offsets(p, st, KID_ATTN_FWD);
-  // the rows' sequences, and from them the key tiles
-  const int t = warp >> 2;              // query tile of a softmax warp
-  const int row = r0 + threadIdx.x;     // of a softmax thread
-  Span sp{-1, -1};
-  int seen0 = 0;                        // first token of the row's window
-  if (warp < 8) {
-    if (row < p.T) sp = span_of(p, row);
-    seen0 = sp.start < 0 ? INT_MAX : window_start(p, row, sp.start);
-    const int lo = __reduce_min_sync(0xffffffffu, seen0), hi = __reduce_max_sync(0xffffffffu, sp.start < 0 ? -1 : row);
-    const int s0 = __reduce_min_sync(0xffffffffu, sp.start < 0 ? INT_MAX : sp.start);
-    if (lane == 0) g.lo[t][warp & 3] = lo, g.hi[t][warp & 3] = hi, g.start[t][warp & 3] = s0;
+  if (!p.spans) {   // a call without a plan: the block finds out about its rows by itself
+    if (blockIdx.x == 0) check_offsets(p, st, KID_ATTN_FWD);
+    if (warp < 8) {
+      const int t = warp >> 2, row = static_cast<int>(blockIdx.x) / p.Hq * kRows + threadIdx.x;
+      Span sp{-1, -1};
+      if (row < p.T) sp = span_of(p, row);
+      const int lo = __reduce_min_sync(0xffffffffu, sp.start < 0 ? INT_MAX : window_start(p, row, sp.start));
+      const int hi = __reduce_max_sync(0xffffffffu, sp.start < 0 ? -1 : row);
+      const int s0 = __reduce_min_sync(0xffffffffu, sp.start < 0 ? INT_MAX : sp.start);
+      if (lane == 0) g.lo[t][warp & 3] = lo, g.hi[t][warp & 3] = hi, g.start[t][warp & 3] = s0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2)
+      g.range[threadIdx.x] = range_of<kKeys>(p, g.lo[threadIdx.x], g.hi[threadIdx.x], g.start[threadIdx.x]);
   }
-  __syncthreads();
-  if (threadIdx.x < 2)
-    g.range[threadIdx.x] = range_of<kKeys>(p, g.lo[threadIdx.x], g.hi[threadIdx.x], g.start[threadIdx.x]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Range ra = g.range[0], rb = g.range[1];
   const uint32_t tmem = g.tmem;
-  const int kt0 = next_tile(ra, rb, 0);
+  Jobs jobs(p, g, total);
+  Job job;
 
   if (warp == 8) {
-    if (lane == 0 && kt0 != INT_MAX) {
-      const bool used[2] = {ra.first < ra.last, rb.first < rb.last};
-      mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * kQBytes);
-      for (int i = 0; i < 2; ++i)
-        if (used[i]) QTile<D>::load(sq + i * kQBytes, &tm_q, &g.q_full, r0 + i * kTile, hq);
-      int n = 0;
-      for (int kt = kt0; kt != INT_MAX; kt = next_tile(ra, rb, kt + 1), ++n) {
-        const int s = n % kStages, par = (n / kStages) & 1;
-        if (!wait_inline(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) break;
-        mbar_arrive_expect_tx(&g.k_full[s], kKBytes);
-        KTile<D>::load(sk + s * kKBytes, &tm_k, &g.k_full[s], kt * kKeys, h);
-        if (!wait_inline(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD)) {
-          wait_inline(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
-          break;
+    if (lane == 0) {
+      int n = 0, loads = 0;   // steps; jobs that have loaded q
+      bool ok = true;
+      while (ok && jobs.next(job)) {
+        if (job.begin() >= job.b1) continue;
+        const int h = job.head / p.G, r0 = job.tile * kRows;
+        const bool used[2] = {job.range[0].first < job.range[0].last, job.range[1].first < job.range[1].last};
+        ok = wait_inline(&g.q_empty, (loads & 1) ^ 1, &g.abort, st, KID_ATTN_FWD);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * kQBytes);
+        for (int i = 0; i < 2; ++i)
+          if (used[i]) QTile<D>::load(sq + i * kQBytes, &tm_q, &g.q_full, r0 + i * kTile, job.head);
+        ++loads;
+        for (int kt = job.begin(); kt < job.b1; kt = job.after(kt), ++n) {
+          const int s = n % kStages, par = (n / kStages) & 1;
+          ok = wait_inline(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&g.k_full[s], kKBytes);
+          KTile<D>::load(sk + s * kKBytes, &tm_k, &g.k_full[s], kt * kKeys, h);
+          ok = wait_inline(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD);
+          if (!ok) {
+            wait_inline(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
+            break;
+          }
+          mbar_arrive_expect_tx(&g.v_full[s], kVBytes);
+          VTile::load(sv + s * kVBytes, &tm_v, &g.v_full[s], kt * kKeys, h);
         }
-        mbar_arrive_expect_tx(&g.v_full[s], kVBytes);
-        VTile::load(sv + s * kVBytes, &tm_v, &g.v_full[s], kt * kKeys, h);
       }
       // every copy has landed before the block may leave
-      wait_inline(&g.q_full, 0, nullptr, st, KID_ATTN_FWD);
+      if (loads > 0) wait_inline(&g.q_full, (loads - 1) & 1, nullptr, st, KID_ATTN_FWD);
       for (int i = max(0, n - kStages); i < n; ++i) {
         wait_inline(&g.k_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
         wait_inline(&g.v_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
@@ -160,152 +216,174 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto wait = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, wait_inline(bar, par, &g.abort, st, KID_ATTN_FWD));
     };
+    bool ok = true;
+    int n = 0;
     if (warp == 9) {
       constexpr uint32_t id_s = idesc_bf16_f32(kTile, kKeys, false);
       const uint64_t q0 = QTile<D>::desc(sq), k0 = KTile<D>::desc(sk);
-      int formed[2] = {0, 0};
-      bool ok = kt0 != INT_MAX && wait(&g.q_full, 0);
-      for (int kt = kt0, n = 0; ok && kt != INT_MAX; ++n) {
-        const int s = n % kStages, next = next_tile(ra, rb, kt + 1);
-        ok = wait(&g.k_full[s], (n / kStages) & 1);
+      int formed[2] = {0, 0}, loads = 0;
+      while (ok && jobs.next(job)) {
+        if (job.begin() >= job.b1) continue;
+        ok = wait(&g.q_full, loads++ & 1);
+        for (int kt = job.begin(); ok && kt < job.b1; kt = job.after(kt), ++n) {
+          const int s = n % kStages;
+          ok = wait(&g.k_full[s], (n / kStages) & 1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || !(i == 0 ? ra : rb).has(kt)) continue;
-          ok = formed[i] == 0 || wait(&g.s_free[i], (formed[i] - 1) & 1);   // the last scores have been read
-          if (!ok) continue;
-          tc_fence_after();
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || !job.range[i].has(kt)) continue;
+            ok = formed[i] == 0 || wait(&g.s_free[i], (formed[i] - 1) & 1);   // the last scores have been read
+            if (!ok) continue;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_ss(tmem + s_col(i), q0 + ((i * kQBytes) >> 4) + QTile<D>::cols16(kk),
-                         k0 + ((s * kKBytes) >> 4) + KTile<D>::cols16(kk), id_s, kk > 0, elected);
-          umma_commit_elected(&g.s_full[i], elected);
-          ++formed[i];
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_bf16_ss(tmem + s_col(i), q0 + ((i * kQBytes) >> 4) + QTile<D>::cols16(kk),
+                           k0 + ((s * kKBytes) >> 4) + KTile<D>::cols16(kk), id_s, kk > 0, elected);
+            umma_commit_elected(&g.s_full[i], elected);
+            ++formed[i];
+          }
+          umma_commit_elected(&g.k_empty[s], elected);
         }
-        umma_commit_elected(&g.k_empty[s], elected);
-        kt = next;
+        umma_commit_elected(&g.q_empty, elected);
       }
     } else {
       const int i = warp - 10;
       constexpr uint32_t id_o = idesc_bf16_f32(kTile, kDv, true);
       const uint32_t tp = tmem + p_col(i), to = tmem + o_col(i);
       const uint64_t v0 = VTile::desc(sv);
-      const Range mine = i == 0 ? ra : rb;
       int added = 0;
-      bool ok = true;
-      for (int kt = kt0, n = 0; ok && kt != INT_MAX; ++n) {
-        const int s = n % kStages, next = next_tile(ra, rb, kt + 1);
-        ok = wait(&g.v_full[s], (n / kStages) & 1);   // (of a tile that only the other needs, too: its release counts both)
-        if (ok && mine.has(kt)) {
-          ok = wait(&g.p_full[i], added & 1);
-          if (!ok) break;
-          tc_fence_after();
+      for (int turn = 0; ok && jobs.next(job); ++turn) {
+        bool first = true;
+        for (int kt = job.begin(); ok && kt < job.b1; kt = job.after(kt), ++n) {
+          const int s = n % kStages;
+          ok = wait(&g.v_full[s], (n / kStages) & 1);   // (of a tile that only the other needs, too: its release counts both)
+          if (ok && (i == 0 ? job.range[0] : job.range[1]).has(kt)) {
+            ok = (!first || turn == 0 || wait(&g.o_free[i], (turn - 1) & 1)) && wait(&g.p_full[i], added & 1);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_bf16_ts(to, tp + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::rows16(kk), id_o, added > 0 || kk > 0, elected);
-          umma_commit_elected(&g.o_done[i], elected);
-          ++added;
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_bf16_ts(to, tp + kk * 8, v0 + ((s * kVBytes) >> 4) + VTile::rows16(kk), id_o, !first || kk > 0, elected);
+            umma_commit_elected(&g.o_done[i], elected);
+            first = false;
+            ++added;
+          }
+          umma_commit_elected(&g.v_empty[s], elected);
         }
-        umma_commit_elected(&g.v_empty[s], elected);
-        kt = next;
       }
     }
     umma_commit_elected(&g.end, elected);   // before the block leaves
     wait_inline(&g.end, 0, nullptr, st, KID_ATTN_FWD);
   } else {
-    const Range r = t == 0 ? ra : rb;
+    const int t = warp >> 2;   // the warp's query tile
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + s_col(t) + quarter, tp = tmem + p_col(t) + quarter, to = tmem + o_col(t) + quarter;
     const f2 sc = f2_make(p.scale_log2, p.scale_log2);
-    float m = -INFINITY, l = 0.f;   // m: what the scores are relative to (raw)
-    int n = 0;
+    uint8_t* stage = so + warp * kOutBytes;
+    int n = 0;   // steps
     bool ok = true;
-    const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
-    // key tiles that every row of the warp sees whole
-    const int whole0 = (min(__reduce_max_sync(0xffffffffu, seen0), INT_MAX - kKeys) + kKeys - 1) / kKeys;
-    const int whole1 = __reduce_min_sync(0xffffffffu, row + 1) / kKeys;
-    for (int kt = r.sink0 < r.sink1 ? r.sink0 : r.first; kt < r.last; kt = kt + 1 == r.sink1 ? r.first : kt + 1, ++n) {
-      ok = wait_inline(&g.s_full[t], n & 1, &g.abort, st, KID_ATTN_FWD);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t x[kKeys];
-      tmem_load<kKeys>(ts, x);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&g.s_free[t]);
-      const int j0 = kt * kKeys;
-      if (kt < whole0 || kt >= whole1) {
-#pragma unroll
-        for (int c = 0; c < (kKeys + 31) / 32; ++c) {
-          uint32_t see = 0;
-          if (sp.start >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(sp.start, min(sink_end, row + 1), j0 + 32 * c);
-#pragma unroll
-          for (int i = 0; i < 32 && 32 * c + i < kKeys; ++i) x[32 * c + i] = see >> i & 1 ? x[32 * c + i] : 0xFF800000u;
-        }
-      }
-      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < kKeys; i += 2)
-        tops[i / 2 % 4] = fmax3(tops[i / 2 % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-      const float top = fmax3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
-      const bool grows = top > m && (top - m) * p.scale_log2 > kSlack;
-      const float f = !grows ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
-      if (grows) m = top;
-      l *= f;
-      const bool free = n == 0 || mbar_try_wait(&g.o_done[t], (n - 1) & 1);   // (looked at here, used below)
-      const float m2 = finite_or_zero(m) * p.scale_log2;
-      const f2 mm = f2_make(-m2, -m2);
-      f2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-      uint32_t w[kKeys / 2];
-#pragma unroll
-      for (int i = 0; i < kKeys / 2; ++i) {
-        const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mm));
-        const float a = ex2(z.x), b = ex2(z.y);
-        sum[i & 1] = f2_add(sum[i & 1], f2_make(a, b));
-        w[i] = pack_bf16x2(a, b);
-      }
-      const float2 part = f2_split(f2_add(sum[0], sum[1]));
-      l += part.x + part.y;
-      // the last step's product is done: its probabilities may go, and O may be multiplied
-      if (n > 0) {
-        ok = free || wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
+    const auto start_of = [&](int tile) {   // of this thread's row
+      const int row = tile * kRows + threadIdx.x;
+      return row >= p.T ? -1 : p.spans ? __ldcg(p.spans + row).x : span_of(p, row).start;
+    };
+    int start = 0;
+    while (ok && jobs.next(job)) {
+      const Range r = t == 0 ? job.range[0] : job.range[1];
+      const int hq = job.head, row = job.tile * kRows + threadIdx.x;
+      if (jobs.k == 1) start = start_of(job.tile);   // the others are read ahead
+      const Span sp{start, 0};
+      const int seen0 = sp.start < 0 ? INT_MAX : window_start(p, row, sp.start);   // first token of the row's window
+      const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
+      // key tiles that every row of the warp sees whole
+      const int whole0 = (min(__reduce_max_sync(0xffffffffu, seen0), INT_MAX - kKeys) + kKeys - 1) / kKeys;
+      const int whole1 = __reduce_min_sync(0xffffffffu, row + 1) / kKeys;
+      float m = -INFINITY, l = 0.f;   // m: what the scores are relative to (raw)
+      bool begun = false;
+      for (int kt = r.sink0 < r.sink1 ? r.sink0 : r.first; kt < r.last; kt = kt + 1 == r.sink1 ? r.first : kt + 1, ++n) {
+        ok = wait_inline(&g.s_full[t], n & 1, &g.abort, st, KID_ATTN_FWD);
         if (!ok) break;
         tc_fence_after();
-        if (__any_sync(0xffffffffu, grows)) {
+        uint32_t x[kKeys];
+        tmem_load<kKeys>(ts, x);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&g.s_free[t]);
+        if (kt < whole0 || kt >= whole1) {
+          const int j0 = kt * kKeys;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * c, o);
-            tmem_ld_wait();
+          for (int c = 0; c < (kKeys + 31) / 32; ++c) {
+            uint32_t see = 0;
+            if (sp.start >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(sp.start, min(sink_end, row + 1), j0 + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(to + 32 * c, o);
+            for (int i = 0; i < 32 && 32 * c + i < kKeys; ++i) x[32 * c + i] = see >> i & 1 ? x[32 * c + i] : 0xFF800000u;
           }
         }
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 2)
+          tops[i / 2 % 4] = fmax3(tops[i / 2 % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        const float top = fmax3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
+        const bool grows = top > m && (top - m) * p.scale_log2 > kSlack;
+        const float f = !grows ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
+        if (grows) m = top;
+        l *= f;
+        const bool free = !begun || mbar_try_wait(&g.o_done[t], (n - 1) & 1);   // (looked at here, used below)
+        const float m2 = finite_or_zero(m) * p.scale_log2;
+        const f2 mm = f2_make(-m2, -m2);
+        f2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+        uint32_t w[kKeys / 2];
+#pragma unroll
+        for (int i = 0; i < kKeys / 2; ++i) {
+          const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mm));
+          const float a = ex2(z.x), b = ex2(z.y);
+          sum[i & 1] = f2_add(sum[i & 1], f2_make(a, b));
+          w[i] = pack_bf16x2(a, b);
+        }
+        const float2 part = f2_split(f2_add(sum[0], sum[1]));
+        l += part.x + part.y;
+        // the last step's product is done: its probabilities may go, and O may be multiplied
+        if (begun) {
+          ok = free || wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
+          if (!ok) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+        }
+        tmem_store<kKeys / 2>(tp, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&g.p_full[t]);
+        begun = true;
       }
-      tmem_store<kKeys / 2>(tp, w);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&g.p_full[t]);
-    }
-    if (ok && n > 0) ok = wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
-    if (ok) {
+      if (jobs.more) start = start_of(jobs.r[0].x);   // the next job's
+      if (ok && begun) ok = wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
+      if (!ok) break;
       tc_fence_after();
       const bool none = l == 0.f;
       const float f = none ? 0.f : 1.f / l;
       bool bad = !(l < INFINITY);
-      // one box of 32 rows x 64 columns after the other, in the place of q
-      uint8_t* stage = sq + t * kQBytes + (warp & 3) * (kQBytes / 4);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < 2; ++b) {   // 64 columns at a time
         uint32_t o[64];
         tmem_load<64>(to + 64 * b, o);
         tmem_ld_wait();
-        if (b == 1) {
-          if (lane == 0) bulk_wait_read<0>();
+        if (b == 1) {   // the next job's products may begin
+          tc_fence_before();
           __syncwarp();
+          if (lane == 0) mbar_arrive(&g.o_free[t]);
         }
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < 64; i += 8) {
@@ -329,13 +407,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row < p.T)
         p.lse[static_cast<int64_t>(hq) * p.T + row] =
             none ? -INFINITY : (finite_or_zero(m) * p.scale_log2 + log2f(l)) * 0.6931471805599453f;
-      if (lane == 0) bulk_wait_all<0>();
-      __syncwarp();
       // A value that is not finite may come from what the row does not see
       // (0 * NaN): such rows are computed again from what they see.
       uint32_t again = __ballot_sync(0xffffffffu, bad && !none && row < p.T);
-      for (; again; again &= again - 1) attend_row<D>(p, r0 + t * kTile + (warp & 3) * 32 + __ffs(again) - 1, hq);
+      if (again) {
+        if (lane == 0) bulk_wait_all<0>();   // what they replace has been written
+        __syncwarp();
+        for (; again; again &= again - 1) attend_row<D>(p, row - lane + __ffs(again) - 1, hq);
+      }
     }
+    if (lane == 0) bulk_wait_all<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -343,9 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-__global__ void __launch_bounds__(1024) order_kernel(const __grid_constant__ AttnArgs p, int tiles) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ AttnArgs p, DevStatus st) {
   wait_for_previous();
-  sort_tiles<1024>(p, tiles, kRows, false, p.order[0]);
+  if (blockIdx.x == 0) check_offsets(p, st, KID_ATTN_FWD);
+  make_plan<kKeys, false>(p, blockIdx.x, gridDim.x);
 }
 
 template <int D>
@@ -359,14 +441,13 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev].store(true, std::memory_order_relaxed);
   }
-  // With no more blocks than multiprocessors all of them start at once.
-  const int tiles = (a.T + kRows - 1) / kRows;
-  const int64_t blocks = static_cast<int64_t>(tiles) * a.Hq;
-  if (blocks > device_sms()) {
-    e = launch_dependent(order_kernel, dim3(1), 1024, 0, s, a, tiles);
+  // With no more jobs than multiprocessors each block has one and needs no plan.
+  const int sms = device_sms(), total = (a.T + kRows - 1) / kRows * a.Hq;
+  if (total > sms) {
+    e = launch_dependent(plan_kernel, dim3((a.Tp + kPlanThreads - 1) / kPlanThreads), kPlanThreads, 0, s, a, st);
     if (e != cudaSuccess) return e;
   } else {
-    a.order[0] = nullptr;
+    a.spans = nullptr;
   }
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap q, k, v, o;
@@ -375,7 +456,7 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
       !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kKeys, 1, VTile::kSwizzle) ||
       !map2d_bf16(&o, a.a, static_cast<uint64_t>(a.Hq) * kDv, a.T, 64, 32))
     return cudaErrorInvalidValue;
-  return launch_dependent(forward_kernel<D>, dim3(static_cast<unsigned>(blocks)), kThreads, smem_bytes<D>(), s, q, k, v, o, a, st);
+  return launch_dependent(forward_kernel<D>, dim3(std::min(sms, total)), kThreads, smem_bytes<D>(), s, q, k, v, o, a, total, st);
 }
 
 }  // namespace

@@ -49,7 +49,7 @@ def test_attention_refuses_bad_pointers(qk):
     L, d = qk.lib(), _at(qk)
     n = L.qkvp_attention_workspace_bytes(d)
     assert n >= 1024 + 4 * 4 * 100
-    for call, pointers, size in ((L.qkvp_attention_forward, 6, 1024 + 256), (L.qkvp_attention_backward, 10, n)):
+    for call, pointers in ((L.qkvp_attention_forward, 6), (L.qkvp_attention_backward, 10)):
         assert call(None, *[P] * pointers, BIG, None) == qk.ERR_INVALID_ARGUMENT
         for i in range(pointers):
             args = [P] * pointers
@@ -57,7 +57,7 @@ def test_attention_refuses_bad_pointers(qk):
             assert call(d, *args, BIG, None) == qk.ERR_INVALID_ARGUMENT
             args[i] = P + 8
             assert call(d, *args, BIG, None) == qk.ERR_MISALIGNED
-        assert call(d, *[P] * pointers, size - 1, None) == qk.ERR_WORKSPACE_TOO_SMALL
+        assert call(d, *[P] * pointers, n - 1, None) == qk.ERR_WORKSPACE_TOO_SMALL
         # no tokens: nothing to launch
         assert call(_at(qk, T=0), *[None] * (pointers - 1), P, BIG, None) == qk.OK
         assert call(_at(qk, T=0), *[None] * pointers, BIG, None) == qk.ERR_INVALID_ARGUMENT

@@ -132,6 +132,29 @@ def test_many_short_sequences(qk, d, B):
     check_backward(qk.attention_backward(DA, Q, K, V, a, lse, offsets(cu), 6, 2), f, b)
 
 
+@pytest.mark.parametrize("d,window,sinks", [(64, None, 0), (96, 100, 3), (128, 33, 260), (96, 1, 0)])
+def test_more_tiles_than_multiprocessors(qk, d, window, sinks):
+    """Ragged sequences in more tiles than the GPU has multiprocessors, so that
+    blocks take several in turn; rows of no sequence before and behind them."""
+    lens = [1 + (37 * i) % 413 if i % 7 else 0 for i in range(160)]
+    cu = (300 + np.concatenate([[0], np.cumsum(lens)])).tolist()
+    T, Hq = cu[-1] + 700, 2
+    assert T // 256 * Hq > 190
+    q, k, v, da = inputs(Hq, 1, T, d, seed=d)
+    f, b = ao.gradient_bounds(f32(q), f32(k), f32(v), f32(da), cu, window, sinks)
+    Q, K, V, DA = gpu(q, k, v, da)
+    ws = qk.new_attention_workspace(T, Hq)
+    a, lse = qk.attention_forward(Q, K, V, offsets(cu), window, sinks, ws=ws)
+    check_forward(a, lse, f, d)
+    g = qk.attention_backward(DA, Q, K, V, a, lse, offsets(cu), window, sinks, ws=ws)
+    check_backward(g, f, b)
+    assert qk.poll_device_status(ws) == (qk.OK, 0)
+    for _ in range(3):   # the same on every run, and the workspace is left as it has to be
+        a2, l2 = qk.attention_forward(Q, K, V, offsets(cu), window, sinks, ws=ws)
+        g2 = qk.attention_backward(DA, Q, K, V, a, lse, offsets(cu), window, sinks, ws=ws)
+        assert torch.equal(a, a2) and torch.equal(lse, l2) and all(torch.equal(g[n], g2[n]) for n in g)
+
+
 @pytest.mark.parametrize("scale", [1e-6, 0.02, 3.0])
 def test_scales(qk, scale):
     """Flat, ordinary and very peaked probabilities."""
