@@ -15,7 +15,8 @@ void use_workspace(AttnArgs* p, void* ws) {
   p->jobs[0] = reinterpret_cast<int4*>(b + w.jobs[0]);
   p->jobs[1] = reinterpret_cast<int4*>(b + w.jobs[1]);
   p->counter = reinterpret_cast<unsigned int*>(b + kAttnCounter);
-  p->stat = reinterpret_cast<float*>(b + w.stat);   // (of a backward's workspace)
+  p->stat = reinterpret_cast<float*>(b + w.stat);
+  p->stat_rows = reinterpret_cast<uint4*>(b + w.stat_rows);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -32,7 +33,8 @@ AttnLayout attention_layout(const AttnArgs& a) {
   w.ends = w.jobs[0] + up(3 * tiles * sizeof(int4));
   w.jobs[1] = w.ends + up(tiles * sizeof(int));
   w.stat = w.jobs[1] + up(tiles * sizeof(int4));
-  w.bytes = w.stat + up(static_cast<size_t>(a.Hq) * a.Tp * 2 * sizeof(float));
+  w.stat_rows = w.stat + up(static_cast<size_t>(a.Hq) * a.Tp * 2 * sizeof(float));
+  w.bytes = w.stat_rows + static_cast<size_t>(a.Hq) * a.Tp * 2 * sizeof(uint4);
   return w;
 }
 

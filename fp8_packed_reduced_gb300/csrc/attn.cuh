@@ -31,6 +31,7 @@ struct AttnArgs {
   const uint16_t* da;        // [T, Hq * 128]
   int Tp;                    // T rounded up to whole tiles
   float* stat;               // [Hq, 2, Tp] -lse in base 2 (-inf: no weight), -da . a
+  uint4* stat_rows;          // [Hq, 2, Tp] -lse in units of the scores, -da . a, each as three bf16 and five zeros
   uint16_t *dq, *dk, *dv;
   // The plan of a call with more tiles than multiprocessors (spans is null without):
   int2* spans;               // [Tp] every token's sequence
@@ -234,6 +235,7 @@ __device__ __forceinline__ void check_offsets(const AttnArgs& p, const DevStatus
 // ---------------------------------------------------------------------------
 // Rows on the CUDA cores, one warp each: a lane takes one token of 32 for the
 // scores, four (d / 32) columns for the sums.  Only pairs that are seen enter.
+// Out of line: the tensor kernels' loops have to stay in the instruction cache.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -261,7 +263,7 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_f
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return static_cast<uint16_t>(pack_bf16x2(x, 0.f)); }
 
 template <int D>
-__device__ __forceinline__ void attend_row(const AttnArgs& p, int row, int hq) {
+__device__ __noinline__ void attend_row(const AttnArgs& p, int row, int hq) {
   const int lane = threadIdx.x & 31, h = hq / p.G;
   const Span sp = span_of(p, row);
   const uint16_t* q = p.q + (static_cast<int64_t>(hq) * p.T + row) * D;
@@ -313,7 +315,7 @@ __device__ __forceinline__ float2 pair_grad(const AttnArgs& p, int i, int j, int
 
 // Columns 32 c0 .. 32 c1 - 1 of a row of dq.
 template <int D>
-__device__ __forceinline__ void dq_row(const AttnArgs& p, int row, int hq, int c0, int c1) {
+__device__ __noinline__ void dq_row(const AttnArgs& p, int row, int hq, int c0, int c1) {
   const int lane = threadIdx.x & 31, h = hq / p.G;
   const Span sp = span_of(p, row);
   float o[D / 32] = {};
@@ -341,7 +343,7 @@ __device__ __forceinline__ void dq_row(const AttnArgs& p, int row, int hq, int c
 
 // A row of dv, or of dk.
 template <int D>
-__device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h, bool dv) {
+__device__ __noinline__ void dkv_row(const AttnArgs& p, int row, int h, bool dv) {
   const int lane = threadIdx.x & 31;
   const Span sp = span_of(p, row);
   float ok[D / 32] = {}, ov[4] = {};
@@ -372,15 +374,23 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& p, int row, int h, bool 
   }
 }
 
-// mbar_wait without a call (a kernel that moves registers between its warps
-// has no room for one's saved registers).
-__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort, const DevStatus& st, int kid) {
-  if (mbar_try_wait(bar, parity)) return true;
+// mbar_wait for waits of a few hundred cycles: asleep until the phase completes, or
+// a millisecond (polling takes issue slots from the warps that compute), and
+// without reading the time, which takes about a thousand cycles, before that.
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool mbar_sleep_on(uint64_t* bar, uint32_t parity, volatile int* abort, const DevStatus& st, int kid) {
   const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+  while (!mbar_sleep(bar, parity)) {
     if (abort != nullptr && *abort) return false;
     if (globaltimer_ns() - t0 > st.timeout_ns) {
       record_error(st, QKVP_ERR_TIMEOUT, kid);
@@ -388,11 +398,17 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, vola
       return false;
     }
   }
+  return true;
 }
+__device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, volatile int* abort, const DevStatus& st, int kid) {
+  return mbar_sleep(bar, parity) || mbar_sleep_on(bar, parity, abort, st, kid);
+}
+// The same value in every lane, where the compiler cannot know that it is.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Parts of the workspace behind its header.  Host: fills p's pointers into it.
 struct AttnLayout {
-  size_t spans, ranges, ends, jobs[2], stat, bytes;
+  size_t spans, ranges, ends, jobs[2], stat, stat_rows, bytes;
 };
 AttnLayout attention_layout(const AttnArgs& a);
 

@@ -18,8 +18,8 @@ namespace {
 
 constexpr int kTile = kAttnTile;
 constexpr int kThreads = 352;                // eight computing warps, a loading and two issuing ones
-constexpr int kMaxStages = 5;
-constexpr int kOutBytes = 32 * 128;          // of a computing warp's output, 32 rows x 64 columns at a time
+constexpr int kMaxStages = 6;
+constexpr int kOutBytes = 32 * 64;           // of a computing warp's output, 32 rows x 32 columns at a time
 template <int D>
 using Fixed = AttnTile<D, kTile>;            // 128 rows
 
@@ -44,12 +44,20 @@ template <int D>
 using QTile = AttnTile<D, queries(D)>;
 template <int D>
 using DaTile = AttnTile<kDv, queries(D)>;
-__host__ __device__ constexpr int q_stages(int d) { return d == 64 ? 4 : 3; }
-__host__ __device__ constexpr int da_stages(int) { return 3; }
+// (scores run two steps ahead of dk, so a tile of q is in use for longer than one of da)
+__host__ __device__ constexpr int q_stages(int d) { return d == 64 ? 5 : 4; }
+__host__ __device__ constexpr int da_stages(int d) { return d == 64 ? 3 : 2; }
+// lse and delta are the same for a step's whole column, so they would be read from
+// shared memory by every thread, beside the operands that its bandwidth bounds
+// this pass by.  They come into the sums as 16 columns of K more: three bf16, which
+// hold a float, times ones.  (As float values read by every thread: a step took
+// 2065 cycles instead of @@.)
+constexpr int kOnesBytes = kTile * 16;       // of the ones, and of the zeros of columns 8 to 15 that all share
+constexpr int kStatBytes = 16;               // of a row
 template <int D>
 constexpr int dkv_smem() {
   return 1024 + Fixed<D>::kBytes + Fixed<kDv>::kBytes + q_stages(D) * QTile<D>::kBytes + da_stages(D) * DaTile<D>::kBytes +
-         8 * kOutBytes;
+         8 * kOutBytes + 2 * kOnesBytes + (q_stages(D) + da_stages(D)) * queries(D) * kStatBytes;
 }
 __host__ __device__ constexpr uint32_t k_s(int) { return 0; }
 __host__ __device__ constexpr uint32_t k_p(int d) { return queries(d); }
@@ -61,7 +69,7 @@ __host__ __device__ constexpr uint32_t k_dk(int d) { return k_dv(d) + kDv; }
 struct Shared {
   uint64_t fixed_full, fixed_empty;   // dk and dv: the job's keys; dq: q and da are in TMEM (fixed_full)
   uint64_t a_full[kMaxStages], a_empty[kMaxStages], b_full[kMaxStages], b_empty[kMaxStages];
-  uint64_t s_full, s_free, p_full, p_free, dp_full, dp_free, ds_full, ds_free;
+  uint64_t s_full, s_free, p_full, p_free, dp_full, dp_free, ds_full, ds_free;   // of the steps' products
   uint64_t acc_full, acc_free[2];     // a job's sums are complete; each warpgroup has read its own
   uint64_t end;                       // all products are done
   uint32_t tmem;
@@ -95,9 +103,12 @@ __device__ __forceinline__ void init_barriers(Shared& g, int fixed_full, int b_u
   mbar_init(&g.end, 2);
   fence_mbar_init();
 }
-// Two pairs of floats of shared memory.
-__device__ __forceinline__ void lds_f2x2(uint32_t at, f2 (&z)[2]) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(z[0]), "=l"(z[1]) : "r"(at));
+// A float as three bf16 that add up to it (an infinity or NaN as the first), and five zeros.
+__device__ __forceinline__ uint4 three_bf16(float x) {
+  const float a = __uint_as_float(pack_bf16x2(x, 0.f) << 16);
+  const float r = x - a, b = __uint_as_float(pack_bf16x2(r, 0.f) << 16);
+  const bool whole = fabsf(a) < INFINITY;
+  return make_uint4(pack_bf16x2(a, whole ? b : 0.f), whole ? pack_bf16x2(r - b, 0.f) : 0u, 0u, 0u);
 }
 // A warp has done something to TMEM: it arrives once.
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
@@ -110,30 +121,39 @@ __device__ __forceinline__ uint32_t seen_halves(uint32_t see, int i) {
   return (see >> (2 * i) & 1 ? 0xFFFFu : 0u) | (see >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
 }
 
-// 64 columns of an accumulator in TMEM (its first `width` count), times f, as one
-// box of 32 rows in `stage`, and from there to rows `row` on of head `head`; zeros
-// unless `some`.  Whether a value is not finite.  free: arrives when the columns
-// have been read.
-__device__ __forceinline__ bool write_box(uint32_t taddr, int width, float f, bool some, uint8_t* stage, const CUtensorMap* map,
-                                          int col, int row, int head, int T, uint64_t* free) {
+// Of packed words of numbers from `base` on, keeps those in [lo0, hi0) or [lo1, hi1).
+template <int N>
+__device__ __forceinline__ void keep_seen(uint32_t (&out)[N], int base, int lo0, int hi0, int lo1, int hi1) {
+#pragma unroll
+  for (int c = 0; c < (N + 15) / 16; ++c) {
+    const uint32_t see = bits(lo0, hi0, base + 32 * c) | bits(lo1, hi1, base + 32 * c);
+#pragma unroll
+    for (int i = 0; i < 16 && 16 * c + i < N; ++i) out[16 * c + i] &= seen_halves(see, i);
+  }
+}
+
+// 32 columns of an accumulator in TMEM, times f, as one box of 32 rows in `stage`,
+// and from there to rows `row` on of head `head`; zeros unless `some`.  Whether a
+// value is not finite.
+__device__ __forceinline__ bool write_box(uint32_t taddr, float f, bool some, uint8_t* stage, const CUtensorMap* map, int col, int row,
+                                          int head, int T) {
   const int lane = threadIdx.x & 31;
-  uint32_t o[64];
-  tmem_load<64>(taddr, o);
+  uint32_t o[32];
+  tmem_ld32(taddr, o);
   tmem_ld_wait();
-  if (free) arrive_warp(free);
   if (lane == 0) bulk_wait_read<0>();
   __syncwarp();
   float big = 0.f;
 #pragma unroll
-  for (int i = 0; i < 64; i += 8) {
+  for (int i = 0; i < 32; i += 8) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float a = __uint_as_float(o[i + 2 * k]) * f, b = __uint_as_float(o[i + 2 * k + 1]) * f;
-      if (i < width) big += fabsf(a) + fabsf(b);
+      big += fabsf(a) + fabsf(b);
       w[k] = some ? pack_bf16x2(a, b) : 0u;
     }
-    *reinterpret_cast<uint4*>(stage + lane * 128 + (((i / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(stage + lane * 64 + (((i / 8) ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   fence_async_smem();
   __syncwarp();
@@ -179,9 +199,12 @@ __global__ void __launch_bounds__(kPlanThreads) delta_kernel(const __grid_consta
   const int row = r0 + 2 * c + half;
   if (c < 8 && row < p.Tp) {
     const float z = row < p.T ? __ldg(p.lse + static_cast<int64_t>(hq) * p.T + row) : -INFINITY;
-    float* to = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;
-    to[0] = z == -INFINITY ? -INFINITY : z * -1.4426950408889634f;
-    to[p.Tp] = -mine;
+    const int64_t at = static_cast<int64_t>(hq) * 2 * p.Tp + row;
+    const float z2 = z == -INFINITY ? -INFINITY : z * -1.4426950408889634f;
+    p.stat[at] = z2;
+    p.stat[at + p.Tp] = -mine;
+    p.stat_rows[at] = three_bf16(z == -INFINITY ? -INFINITY : -z / p.scale);
+    p.stat_rows[at + p.Tp] = three_bf16(-mine);
   }
 }
 
@@ -193,6 +216,7 @@ __global__ void __launch_bounds__(kPlanThreads) delta_kernel(const __grid_consta
 struct DqJob {
   int tile, head;
   Range r;
+  __device__ void make_uniform() { r = Range{uniform(r.sink0), uniform(r.sink1), uniform(r.first), uniform(r.last)}; }
   __device__ int begin() const { return r.sink0 < r.sink1 ? r.sink0 : r.first; }
   __device__ int after(int kt) const { return kt + 1 == r.sink1 ? r.first : kt + 1; }
 };
@@ -276,17 +300,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int n = 0;
       bool ok = true;
+#pragma unroll 1
       while (ok && jobs.next(job)) {
         const int h = job.head / p.G;
+#pragma unroll 1
         for (int kt = job.begin(); kt < job.r.last; kt = job.after(kt), ++n) {
           const int s = n % kStages, par = (n / kStages) & 1;
-          ok = mbar_wait(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ);
+          ok = wait_asleep(&g.a_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ);
           if (!ok) break;
           mbar_arrive_expect_tx(&g.a_full[s], kKBytes);
           KTile<D>::load(sk + s * kKBytes, &tm_k, &g.a_full[s], kt * kKeys, h);
-          ok = mbar_wait(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ);
+          ok = wait_asleep(&g.b_empty[s], par ^ 1, &g.abort, st, KID_ATTN_DQ);
           if (!ok) {
-            mbar_wait(&g.a_full[s], par, nullptr, st, KID_ATTN_DQ);
+            wait_asleep(&g.a_full[s], par, nullptr, st, KID_ATTN_DQ);
             break;
           }
           mbar_arrive_expect_tx(&g.b_full[s], kVBytes);
@@ -294,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       for (int i = max(0, n - kStages); i < n; ++i) {   // every copy has landed before the block may leave
-        mbar_wait(&g.a_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
-        mbar_wait(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
+        wait_asleep(&g.a_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
+        wait_asleep(&g.b_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_DQ);
       }
     }
   } else if (warp > 8) {
@@ -305,15 +331,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_s = idesc_bf16_f32(kTile, kKeys, false), id_q = idesc_bf16_f32(kTile, D, true);
     const uint32_t elected = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t par) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DQ));
+      return __all_sync(0xffffffffu, wait_asleep(bar, par, &g.abort, st, KID_ATTN_DQ));
     };
     bool ok = true;
     int n = 0, turn = 0;   // steps; jobs with any
     if (warp == 9) {
       const uint64_t k0 = KTile<D>::desc(sk);
+#pragma unroll 1
       while (ok && jobs.next(job)) {
+        job.make_uniform();
         if (job.begin() >= job.r.last) continue;
         ok = wait(&g.fixed_full, turn++ & 1);
+#pragma unroll 1
         for (int kt = job.begin(); ok && kt < job.r.last; kt = job.after(kt), ++n) {
           const int s = n % kStages;
           ok = wait(&g.a_full[s], (n / kStages) & 1) && (n == 0 || wait(&g.s_free, (n - 1) & 1));
@@ -340,10 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_elected(&g.b_empty[s], elected);
         return true;
       };
+#pragma unroll 1
       while (ok && jobs.next(job)) {
+        job.make_uniform();
         if (job.begin() >= job.r.last) continue;
         ok = wait(&g.fixed_full, turn++ & 1) && dps(n);
         bool first = true;
+#pragma unroll 1
         for (int kt = job.begin(); ok && kt < job.r.last; ++n) {
           const int s = n % kStages, next = job.after(kt);
           if (next < job.r.last) ok = dps(n + 1);
@@ -363,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     umma_commit_elected(&g.end, elected);   // before the block leaves
-    mbar_wait(&g.end, 0, nullptr, st, KID_ATTN_DQ);
+    wait_asleep(&g.end, 0, nullptr, st, KID_ATTN_DQ);
   } else {
     // this thread's row, and the half of the keys that its warpgroup takes
     const int half = warp >> 2, mine = threadIdx.x & 127;
@@ -399,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int n = 0, turn = 0;   // steps; jobs with any
     bool ok = true;
+#pragma unroll 1
     while (ok && jobs.next(job)) {
       const int row = job.tile * kTile + mine, hq = job.head;
       const bool some = job.begin() < job.r.last;
@@ -414,8 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // key tiles that every row of the warp sees whole
         const int whole0 = (min(__reduce_max_sync(0xffffffffu, seen0), INT_MAX - kKeys) + kKeys - 1) / kKeys;
         const int whole1 = __reduce_min_sync(0xffffffffu, row + 1) / kKeys;
+#pragma unroll 1
         for (int kt = job.begin(); kt < job.r.last; kt = job.after(kt), ++n) {
-          ok = mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+          ok = wait_asleep(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DQ);
           if (!ok) break;
           tc_fence_after();
           uint32_t x[kHalf];
@@ -428,29 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mz));
             w[i] = f2_make(ex2(z.x), ex2(z.y));
           }
-          ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DQ);
+          const bool free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);   // (looked at here, used below)
+          ok = wait_asleep(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DQ);
           if (!ok) break;
           tc_fence_after();
           tmem_load<kHalf>(tdp, x);
           tmem_ld_wait();
           arrive_warp(&g.dp_free);
-          const bool free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);   // (looked at here, used below)
+          ok = free || wait_asleep(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DQ);
+          if (!ok) break;
+          tc_fence_after();
           uint32_t out[kHalf / 2];
 #pragma unroll
           for (int i = 0; i < kHalf / 2; ++i)
             out[i] = f2_to_bf16x2(f2_mul(f2_add(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), md), w[i]));
-          if (__builtin_expect(kt < whole0 || kt >= whole1, 0)) {
-            const int j0 = kt * kKeys + kHalf * half;
-#pragma unroll
-            for (int c = 0; c < (kHalf + 31) / 32; ++c) {
-              uint32_t see = 0;
-              if (begin >= 0) see = bits(seen0, row + 1, j0 + 32 * c) | bits(begin, min(sink_end, row + 1), j0 + 32 * c);
-#pragma unroll
-              for (int i = 0; i < 16 && 16 * c + i < kHalf / 2; ++i) out[16 * c + i] &= seen_halves(see, i);
-            }
-          }
-          ok = free || mbar_wait(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DQ);
-          if (!ok) break;
+          if (__builtin_expect(kt < whole0 || kt >= whole1, 0))
+            keep_seen(out, kt * kKeys + kHalf * half, begin < 0 ? 0 : seen0, begin < 0 ? 0 : row + 1, begin, min(sink_end, row + 1));
           tmem_store<kHalf / 2>(tds, out);
           tmem_st_wait();
           arrive_warp(&g.ds_full);
@@ -459,14 +486,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const bool more = jobs.more;
       if (more) read_rows(jobs.tile, jobs.head);   // the next job's, on their way while this one ends
-      if (some) ok = mbar_wait(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DQ);
+      if (some) ok = wait_asleep(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DQ);
       if (!ok) break;
       tc_fence_after();
-      // each warpgroup writes 64 columns (with d = 64 the first alone)
+      // one warpgroup writes the first 64 columns, the other what is left
       bool bad = false;
-      if (64 * half < D)
-        bad = write_box(tmem + kQAcc + quarter + 64 * half, min(64, D - 64 * half), p.scale, some, stage, &tm_dq, 64 * half, row, hq,
-                        p.T, nullptr);
+      for (int c = 2 * half; c < (half == 0 ? 2 : D / 32); ++c)
+        bad |= write_box(tmem + kQAcc + quarter + 32 * c, p.scale, some, stage, &tm_dq, 32 * c, row, hq, p.T);
       // Rows that are not finite may owe that to what they do not see (0 * NaN):
       // they are computed again from what they see, each warpgroup's columns by it.
       uint32_t again = __ballot_sync(0xffffffffu, bad && row < p.T);
@@ -492,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 struct DkvJob {
   int tile, head, count, tiles;   // steps, and those of one query head
+  __device__ void make_uniform() { count = uniform(count); }
 };
 struct DkvJobs {
   const AttnArgs& p;
@@ -541,11 +568,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int QN = queries(D), kHalf = QN / 2, SQ = q_stages(D), SD = da_stages(D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared g;
-  __shared__ alignas(128) float stats[SQ][2][QN];   // -lse (base 2) and -delta of a step's queries
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sk = smem, *sv = sk + Fixed<D>::kBytes, *sq = sv + Fixed<kDv>::kBytes, *sd = sq + SQ * Q::kBytes, *so = sd + SD * Da::kBytes;
+  // (the zeros last: a descriptor points to them from what they complete)
+  uint8_t *lses = so + 8 * kOutBytes, *deltas = lses + SQ * QN * kStatBytes, *ones = deltas + SD * QN * kStatBytes, *zeros = ones + kOnesBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) init_barriers(g, 1, 2);
+  if (threadIdx.x < kTile) {
+    reinterpret_cast<uint4*>(ones)[threadIdx.x] = make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u);   // 1, 1, 1, 0 ...
+    reinterpret_cast<uint4*>(zeros)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+  }
   if (warp == 9) {
     tmem_alloc(&g.tmem, 512);
     tmem_relinquish();
@@ -574,28 +607,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int na = 0, nb = 0, turn = 0;   // steps whose q, whose da has been asked for; jobs with any
       bool ok = true;
+#pragma unroll 1
       while (ok && jobs.next(job)) {
         if (job.count == 0) continue;
         const int r0 = job.tile * kTile;
-        ok = mbar_wait(&g.fixed_empty, (turn & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
+        ok = wait_asleep(&g.fixed_empty, (turn & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
         if (!ok) break;
         mbar_arrive_expect_tx(&g.fixed_full, Fixed<D>::kBytes + Fixed<kDv>::kBytes);
         Fixed<D>::load(sk, &tm_k, &g.fixed_full, r0, job.head);
         Fixed<kDv>::load(sv, &tm_v, &g.fixed_full, r0, job.head);
         ++turn;
         int i0 = r0, hq = job.head * p.G;
+#pragma unroll 1
         for (int n = 0, left = job.tiles; n < job.count; ++n) {
           const int sa = na % SQ, sb = nb % SD;
-          ok = mbar_wait(&g.a_empty[sa], (na / SQ & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
+          ok = wait_asleep(&g.a_empty[sa], (na / SQ & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
           if (!ok) break;
-          mbar_arrive_expect_tx(&g.a_full[sa], Q::kBytes + sizeof(stats[0]));
+          mbar_arrive_expect_tx(&g.a_full[sa], Q::kBytes + QN * kStatBytes);
           Q::load(sq + sa * Q::kBytes, &tm_q, &g.a_full[sa], i0, hq);
-          for (int b = 0; b < 2; ++b)
-            bulk_load(stats[sa][b], p.stat + (static_cast<int64_t>(hq) * 2 + b) * p.Tp + i0, sizeof(stats[sa][b]), &g.a_full[sa]);
+          const uint4* stat = p.stat_rows + static_cast<int64_t>(hq) * 2 * p.Tp + i0;
+          bulk_load(lses + sa * QN * kStatBytes, stat, QN * kStatBytes, &g.a_full[sa]);
           ++na;
-          ok = mbar_wait(&g.b_empty[sb], (nb / SD & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
+          ok = wait_asleep(&g.b_empty[sb], (nb / SD & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
           if (!ok) break;
-          mbar_arrive_expect_tx(&g.b_full[sb], Da::kBytes);
+          mbar_arrive_expect_tx(&g.b_full[sb], Da::kBytes + QN * kStatBytes);
+          bulk_load(deltas + sb * QN * kStatBytes, stat + p.Tp, QN * kStatBytes, &g.b_full[sb]);
           for (int b = 0; b < Da::kBoxes; ++b)
             tma_load_2d(sd + sb * Da::kBytes + b * Da::kBox, &tm_da, &g.b_full[sb], hq * kDv + b * Da::kCols, i0);
           ++nb;
@@ -608,9 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // every copy has landed before the block may leave
-      if (turn > 0) mbar_wait(&g.fixed_full, (turn - 1) & 1, nullptr, st, KID_ATTN_DKV);
-      for (int i = max(0, na - SQ); i < na; ++i) mbar_wait(&g.a_full[i % SQ], (i / SQ) & 1, nullptr, st, KID_ATTN_DKV);
-      for (int i = max(0, nb - SD); i < nb; ++i) mbar_wait(&g.b_full[i % SD], (i / SD) & 1, nullptr, st, KID_ATTN_DKV);
+      if (turn > 0) wait_asleep(&g.fixed_full, (turn - 1) & 1, nullptr, st, KID_ATTN_DKV);
+      for (int i = max(0, na - SQ); i < na; ++i) wait_asleep(&g.a_full[i % SQ], (i / SQ) & 1, nullptr, st, KID_ATTN_DKV);
+      for (int i = max(0, nb - SD); i < nb; ++i) wait_asleep(&g.b_full[i % SD], (i / SD) & 1, nullptr, st, KID_ATTN_DKV);
     }
   } else if (warp > 8) {
     // As for dq: one warp issues the scores and dv, the other da . v and dk.
@@ -618,8 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                        id_v = idesc_bf16_f32(kTile, kDv, true);
     const uint32_t elected = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t par) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, par, &g.abort, st, KID_ATTN_DKV));
+      return __all_sync(0xffffffffu, wait_asleep(bar, par, &g.abort, st, KID_ATTN_DKV));
     };
+    const uint64_t ones0 = sdesc_plain(smem_u32(ones), kOnesBytes, 128);
+    const auto stat_desc = [&](const uint8_t* at) { return sdesc_plain(smem_u32(at), static_cast<uint32_t>(zeros - at), 128); };
     bool ok = true;
     int n = 0, turn = 0;   // steps; jobs with any
     if (warp == 9) {
@@ -632,12 +670,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_bf16_ss(tmem + k_s(D), k0 + Fixed<D>::cols16(kk), q0 + ((s * Q::kBytes) >> 4) + Q::cols16(kk), id_s, kk > 0, elected);
+        umma_bf16_ss(tmem + k_s(D), ones0, stat_desc(lses + s * QN * kStatBytes), id_s, 1, elected);
         umma_commit_elected(&g.s_full, elected);
         return true;
       };
+#pragma unroll 1
       while (ok && jobs.next(job)) {
+        job.make_uniform();
         if (job.count == 0) continue;
         ok = wait(&g.fixed_full, turn & 1) && scores(n);
+#pragma unroll 1
         for (int i = 0; ok && i < job.count; ++i, ++n) {
           const int s = n % SD;
           if (i + 1 < job.count) ok = scores(n + 1);
@@ -665,13 +707,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < kDv / 16; ++kk)
           umma_bf16_ss(tmem + k_dp(D), v0 + Fixed<kDv>::cols16(kk), d0 + ((s * Da::kBytes) >> 4) + Da::cols16(kk), id_s, kk > 0, elected);
+        umma_bf16_ss(tmem + k_dp(D), ones0, stat_desc(deltas + s * QN * kStatBytes), id_s, 1, elected);
         umma_commit_elected(&g.dp_full, elected);
         umma_commit_elected(&g.b_empty[s], elected);
         return true;
       };
+#pragma unroll 1
       while (ok && jobs.next(job)) {
+        job.make_uniform();
         if (job.count == 0) continue;
         ok = wait(&g.fixed_full, turn & 1) && dps(n);
+#pragma unroll 1
         for (int i = 0; ok && i < job.count; ++i, ++n) {
           const int s = n % SQ;
           if (i + 1 < job.count) ok = dps(n + 1);
@@ -692,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     umma_commit_elected(&g.end, elected);   // before the block leaves
-    mbar_wait(&g.end, 0, nullptr, st, KID_ATTN_DKV);
+    wait_asleep(&g.end, 0, nullptr, st, KID_ATTN_DKV);
   } else {
     // this thread's key, and the half of the queries that its warpgroup takes
     const int half = warp >> 2, mine = threadIdx.x & 127;
@@ -704,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n = 0, turn = 0;   // steps; jobs with any
     bool ok = true;
     Span ahead{-1, -1};
+#pragma unroll 1
     while (ok && jobs.next(job)) {
       const int r0 = job.tile * kTile, row = r0 + mine;
       if (jobs.k == 1) ahead = span_at(row);   // the others are read ahead
@@ -711,99 +758,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int end = ahead.start < 0 ? row : last_seer(p, row, ahead);
       const int ds0 = row + (ahead.start >= 0 && alone(p, row, ahead.start) ? 1 : 0);
       int i0 = r0 + kHalf * half;
-      for (int i = 0, left = job.tiles; i < job.count; ++i, ++n) {
-        const int s = n % SQ;
-        ok = mbar_wait(&g.a_full[s], (n / SQ) & 1, &g.abort, st, KID_ATTN_DKV) &&
-             mbar_wait(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+#pragma unroll 1
+      for (int i = 0, left = job.tiles; i < job.count; ++i, ++n, i0 += QN) {
+        if (left-- == 0) {   // the next query head
+          left = job.tiles - 1;
+          i0 = r0 + kHalf * half;
+        }
+        ok = wait_asleep(&g.s_full, n & 1, &g.abort, st, KID_ATTN_DKV);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t stat = smem_u32(stats[s][0]) + 4 * kHalf * half;
         const bool whole = __all_sync(0xffffffffu, i0 >= ds0 && i0 + kHalf <= end);
-        uint32_t x[kHalf], out[kHalf / 2];
+        uint32_t x[kHalf];
         tmem_load<kHalf>(ts, x);
         tmem_ld_wait();
         arrive_warp(&g.s_free);
         bool free = n == 0 || mbar_try_wait(&g.p_free, (n - 1) & 1);   // (looked at here, used below)
         f2 w[kHalf / 2];
 #pragma unroll
-        for (int j = 0; j < kHalf / 2; j += 2) {
-          f2 z[2];
-          lds_f2x2(stat + 8 * j, z);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 y = f2_split(
-                f2_fma(f2_make(__uint_as_float(x[2 * (j + k)]), __uint_as_float(x[2 * (j + k) + 1])), sc, z[k]));
-            w[j + k] = f2_make(ex2(y.x), ex2(y.y));
-            out[j + k] = f2_to_bf16x2(w[j + k]);
-          }
+        for (int j = 0; j < kHalf / 2; ++j) {
+          const float2 y = f2_split(f2_mul(f2_make(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc));
+          w[j] = f2_make(ex2(y.x), ex2(y.y));
         }
-        if (__builtin_expect(!whole, 0)) {
-#pragma unroll
-          for (int c = 0; c < (kHalf + 31) / 32; ++c) {
-            const uint32_t see = bits(row, end, i0 + 32 * c);
-#pragma unroll
-            for (int j = 0; j < 16 && 16 * c + j < kHalf / 2; ++j) out[16 * c + j] &= seen_halves(see, j);
-          }
-        }
-        ok = free || mbar_wait(&g.p_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DKV);
+        ok = free || wait_asleep(&g.p_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DKV);
         if (!ok) break;
+        tc_fence_after();
+        uint32_t out[kHalf / 2];
+#pragma unroll
+        for (int j = 0; j < kHalf / 2; ++j) out[j] = f2_to_bf16x2(w[j]);
+        if (__builtin_expect(!whole, 0)) keep_seen(out, i0, row, end, 0, 0);
         tmem_store<kHalf / 2>(tp, out);
         tmem_st_wait();
         arrive_warp(&g.p_full);
-        ok = mbar_wait(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DKV);
+        free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);
+        ok = wait_asleep(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DKV);
         if (!ok) break;
         tc_fence_after();
         tmem_load<kHalf>(tdp, x);
         tmem_ld_wait();
         arrive_warp(&g.dp_free);
-        free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);
-#pragma unroll
-        for (int j = 0; j < kHalf / 2; j += 2) {
-          f2 z[2];
-          lds_f2x2(stat + 4 * QN + 8 * j, z);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            out[j + k] = f2_to_bf16x2(
-                f2_mul(f2_add(f2_make(__uint_as_float(x[2 * (j + k)]), __uint_as_float(x[2 * (j + k) + 1])), z[k]), w[j + k]));
-        }
-        if (__builtin_expect(!whole, 0)) {
-#pragma unroll
-          for (int c = 0; c < (kHalf + 31) / 32; ++c) {
-            const uint32_t see = bits(ds0, end, i0 + 32 * c);
-#pragma unroll
-            for (int j = 0; j < 16 && 16 * c + j < kHalf / 2; ++j) out[16 * c + j] &= seen_halves(see, j);
-          }
-        }
-        ok = free || mbar_wait(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DKV);
+        ok = free || wait_asleep(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DKV);
         if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kHalf / 2; ++j)
+          out[j] = f2_to_bf16x2(f2_mul(f2_make(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), w[j]));
+        if (__builtin_expect(!whole, 0)) keep_seen(out, i0, ds0, end, 0, 0);
         tmem_store<kHalf / 2>(tds, out);
         tmem_st_wait();
         arrive_warp(&g.ds_full);
-        i0 += QN;
-        if (--left == 0) {
-          left = job.tiles;
-          i0 = r0 + kHalf * half;
-        }
       }
       if (!ok) break;
       const bool some = job.count > 0;
       if (jobs.more) ahead = span_at(jobs.r.x * kTile + mine);   // the next job's
-      if (some) ok = mbar_wait(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DKV);
+      if (some) ok = wait_asleep(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DKV);
       if (!ok) break;
       tc_fence_after();
       // one warpgroup writes dv, the other dk
-      bool bad;
-      if (half == 0) {
-        bad = write_box(tmem + k_dv(D) + quarter, 64, 1.f, some, stage, &tm_dv, 0, row, job.head, p.T, nullptr);
-        bad |= write_box(tmem + k_dv(D) + quarter + 64, 64, 1.f, some, stage, &tm_dv, 64, row, job.head, p.T, some ? &g.acc_free[0] : nullptr);
-      } else {
-        constexpr bool kTwo = D > 64;
-        bad = write_box(tmem + k_dk(D) + quarter, 64, p.scale, some, stage, &tm_dk, 0, row, job.head, p.T,
-                        !kTwo && some ? &g.acc_free[1] : nullptr);
-        if (kTwo)
-          bad |= write_box(tmem + k_dk(D) + quarter + (D == 96 ? 32 : 64), D == 96 ? 64 : D - 64, p.scale, some, stage, &tm_dk,
-                           D == 96 ? 32 : 64, row, job.head, p.T, some ? &g.acc_free[1] : nullptr);
-      }
+      bool bad = false;
+      const uint32_t from = tmem + (half == 0 ? k_dv(D) : k_dk(D)) + quarter;
+      for (int c = 0; c < (half == 0 ? kDv : D) / 32; ++c)
+        bad |= write_box(from + 32 * c, half == 0 ? 1.f : p.scale, some, stage, half == 0 ? &tm_dv : &tm_dk, 32 * c, row, job.head, p.T);
+      if (some) arrive_warp(&g.acc_free[half]);   // it has been read
       uint32_t again = __ballot_sync(0xffffffffu, bad && row < p.T);   // as for dq
       if (again) {
         if (lane == 0) bulk_wait_all<0>();
@@ -836,7 +851,7 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
   if (e == cudaSuccess) e = allow_smem(dkv_kernel<D>, dkv_smem<D>(), ready[1]);
   if (e != cudaSuccess) return e;
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_64B;   // (of the outputs' boxes)
   using Q = QTile<D>;
   using K = KTile<D>;
   using F = Fixed<D>;
@@ -848,8 +863,8 @@ cudaError_t launch(AttnArgs a, DevStatus st, cudaStream_t s) {
       !map3d(&v, bf16, 2, a.v, kDv, a.T, a.H, Fv::kCols, kTile, 1, Fv::kSwizzle) ||
       !map3d(&steps_k, bf16, 2, a.k, D, a.T, a.H, K::kCols, kKeys, 1, K::kSwizzle) ||
       !map3d(&steps_v, bf16, 2, a.v, kDv, a.T, a.H, VTile::kCols, kKeys, 1, VTile::kSwizzle) ||
-      !map3d(&dq, bf16, 2, a.dq, D, a.T, a.Hq, 64, 32, 1, sw) || !map3d(&dk, bf16, 2, a.dk, D, a.T, a.H, 64, 32, 1, sw) ||
-      !map3d(&dv, bf16, 2, a.dv, kDv, a.T, a.H, 64, 32, 1, sw))
+      !map3d(&dq, bf16, 2, a.dq, D, a.T, a.Hq, 32, 32, 1, sw) || !map3d(&dk, bf16, 2, a.dk, D, a.T, a.H, 32, 32, 1, sw) ||
+      !map3d(&dv, bf16, 2, a.dv, kDv, a.T, a.H, 32, 32, 1, sw))
     return cudaErrorInvalidValue;
   const int sms = device_sms(), tiles = (a.T + kTile - 1) / kTile;
   const bool plan = tiles * a.Hq > sms;   // else each block has one job

@@ -73,6 +73,11 @@ struct Job {
     a0 = min(sx ? x.sink0 : b0, sy ? y.sink0 : b0);
     a1 = sx || sy ? min(b0, max(sx ? x.sink1 : 0, sy ? y.sink1 : 0)) : b0;
   }
+  __device__ void make_uniform() {
+    for (int c = 0; c < 2; ++c)
+      range[c] = Range{uniform(range[c].sink0), uniform(range[c].sink1), uniform(range[c].first), uniform(range[c].last)};
+    a0 = uniform(a0), a1 = uniform(a1), b0 = uniform(b0), b1 = uniform(b1);
+  }
   __device__ int begin() const { return a0; }
   __device__ int after(int kt) const { return kt + 1 == a1 ? b0 : kt + 1; }   // (past b1: the end)
 };
@@ -175,25 +180,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int n = 0, loads = 0;   // steps; jobs that have loaded q
       bool ok = true;
+#pragma unroll 1
       while (ok && jobs.next(job)) {
         if (job.begin() >= job.b1) continue;
         const int h = job.head / p.G, r0 = job.tile * kRows;
         const bool used[2] = {job.range[0].first < job.range[0].last, job.range[1].first < job.range[1].last};
-        ok = wait_inline(&g.q_empty, (loads & 1) ^ 1, &g.abort, st, KID_ATTN_FWD);
+        ok = wait_asleep(&g.q_empty, (loads & 1) ^ 1, &g.abort, st, KID_ATTN_FWD);
         if (!ok) break;
         mbar_arrive_expect_tx(&g.q_full, (used[0] + used[1]) * kQBytes);
         for (int i = 0; i < 2; ++i)
           if (used[i]) QTile<D>::load(sq + i * kQBytes, &tm_q, &g.q_full, r0 + i * kTile, job.head);
         ++loads;
+#pragma unroll 1
         for (int kt = job.begin(); kt < job.b1; kt = job.after(kt), ++n) {
           const int s = n % kStages, par = (n / kStages) & 1;
-          ok = wait_inline(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD);
+          ok = wait_asleep(&g.k_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD);
           if (!ok) break;
           mbar_arrive_expect_tx(&g.k_full[s], kKBytes);
           KTile<D>::load(sk + s * kKBytes, &tm_k, &g.k_full[s], kt * kKeys, h);
-          ok = wait_inline(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD);
+          ok = wait_asleep(&g.v_empty[s], par ^ 1, &g.abort, st, KID_ATTN_FWD);
           if (!ok) {
-            wait_inline(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
+            wait_asleep(&g.k_full[s], par, nullptr, st, KID_ATTN_FWD);
             break;
           }
           mbar_arrive_expect_tx(&g.v_full[s], kVBytes);
@@ -201,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // every copy has landed before the block may leave
-      if (loads > 0) wait_inline(&g.q_full, (loads - 1) & 1, nullptr, st, KID_ATTN_FWD);
+      if (loads > 0) wait_asleep(&g.q_full, (loads - 1) & 1, nullptr, st, KID_ATTN_FWD);
       for (int i = max(0, n - kStages); i < n; ++i) {
-        wait_inline(&g.k_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
-        wait_inline(&g.v_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
+        wait_asleep(&g.k_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
+        wait_asleep(&g.v_full[i % kStages], (i / kStages) & 1, nullptr, st, KID_ATTN_FWD);
       }
     }
   } else if (warp > 8) {
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // cores' too).  A whole warp goes the same way (umma_bf16_ss says why).
     const uint32_t elected = elect_one();
     const auto wait = [&](uint64_t* bar, uint32_t par) {
-      return __all_sync(0xffffffffu, wait_inline(bar, par, &g.abort, st, KID_ATTN_FWD));
+      return __all_sync(0xffffffffu, wait_asleep(bar, par, &g.abort, st, KID_ATTN_FWD));
     };
     bool ok = true;
     int n = 0;
@@ -222,9 +229,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_s = idesc_bf16_f32(kTile, kKeys, false);
       const uint64_t q0 = QTile<D>::desc(sq), k0 = KTile<D>::desc(sk);
       int formed[2] = {0, 0}, loads = 0;
+#pragma unroll 1
       while (ok && jobs.next(job)) {
+        job.make_uniform();
         if (job.begin() >= job.b1) continue;
         ok = wait(&g.q_full, loads++ & 1);
+#pragma unroll 1
         for (int kt = job.begin(); ok && kt < job.b1; kt = job.after(kt), ++n) {
           const int s = n % kStages;
           ok = wait(&g.k_full[s], (n / kStages) & 1);
@@ -253,6 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int added = 0;
       for (int turn = 0; ok && jobs.next(job); ++turn) {
         bool first = true;
+        job.make_uniform();
+#pragma unroll 1
         for (int kt = job.begin(); ok && kt < job.b1; kt = job.after(kt), ++n) {
           const int s = n % kStages;
           ok = wait(&g.v_full[s], (n / kStages) & 1);   // (of a tile that only the other needs, too: its release counts both)
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     umma_commit_elected(&g.end, elected);   // before the block leaves
-    wait_inline(&g.end, 0, nullptr, st, KID_ATTN_FWD);
+    wait_asleep(&g.end, 0, nullptr, st, KID_ATTN_FWD);
   } else {
     const int t = warp >> 2;   // the warp's query tile
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -286,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return row >= p.T ? -1 : p.spans ? __ldcg(p.spans + row).x : span_of(p, row).start;
     };
     int start = 0;
+#pragma unroll 1
     while (ok && jobs.next(job)) {
       const Range r = t == 0 ? job.range[0] : job.range[1];
       const int hq = job.head, row = job.tile * kRows + threadIdx.x;
@@ -298,8 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int whole1 = __reduce_min_sync(0xffffffffu, row + 1) / kKeys;
       float m = -INFINITY, l = 0.f;   // m: what the scores are relative to (raw)
       bool begun = false;
+#pragma unroll 1
       for (int kt = r.sink0 < r.sink1 ? r.sink0 : r.first; kt < r.last; kt = kt + 1 == r.sink1 ? r.first : kt + 1, ++n) {
-        ok = wait_inline(&g.s_full[t], n & 1, &g.abort, st, KID_ATTN_FWD);
+        ok = wait_asleep(&g.s_full[t], n & 1, &g.abort, st, KID_ATTN_FWD);
         if (!ok) break;
         tc_fence_after();
         uint32_t x[kKeys];
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&g.s_free[t]);
-        if (kt < whole0 || kt >= whole1) {
+        if (__builtin_expect(kt < whole0 || kt >= whole1, 0)) {
           const int j0 = kt * kKeys;
 #pragma unroll
           for (int c = 0; c < (kKeys + 31) / 32; ++c) {
@@ -343,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += part.x + part.y;
         // the last step's product is done: its probabilities may go, and O may be multiplied
         if (begun) {
-          ok = free || wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
+          ok = free || wait_asleep(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
           if (!ok) break;
           tc_fence_after();
-          if (__any_sync(0xffffffffu, grows)) {
+          if (__builtin_expect(__any_sync(0xffffffffu, grows), 0)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         begun = true;
       }
       if (jobs.more) start = start_of(jobs.r[0].x);   // the next job's
-      if (ok && begun) ok = wait_inline(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
+      if (ok && begun) ok = wait_asleep(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
       if (!ok) break;
       tc_fence_after();
       const bool none = l == 0.f;

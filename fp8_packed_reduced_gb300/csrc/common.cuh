@@ -412,6 +412,12 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uin
   return (sdesc_sw128(saddr, lbo, sbo) & ~(uint64_t(7) << 61)) | uint64_t(4) << 61;
 }
 
+// Without swizzling, K-major: blocks of 8 rows x 16 bytes, one after the other along M/N; the next 16
+// bytes of K lie `lbo` bytes on, the next 8 rows `sbo`.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return sdesc_sw128(saddr, lbo, sbo) & ~(uint64_t(7) << 61);
+}
+
 // Instruction descriptor as above with A and/or B read MN-major (bit 15 for
 // A, bit 16 for B; allowed for 8-bit operands).
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32_major(int M, int N, bool a_mn, bool b_mn) {
