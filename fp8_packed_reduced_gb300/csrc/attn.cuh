@@ -38,7 +38,7 @@ struct AttnArgs {
   int4* ranges;              // [Tp / 128] key tiles of 128 queries (backward: of dq)
   int* ends;                 // [Tp / 128] end of the queries that see 128 keys (backward)
   int4* jobs[2];             // the blocks' work, longest first: [tiles][3] of the forward or of dq; [tiles] of dk and dv
-  unsigned int* counter;     // of the plan's blocks that are done; zero between calls
+  unsigned int* counter;     // [0] the plan's blocks that are done, zero between calls; [1], [2] jobs of each list that have been taken
 };
 
 // A tile of ROWS rows of q or k in shared memory: boxes of 64 columns with
@@ -194,7 +194,7 @@ __device__ __forceinline__ void make_plan(const AttnArgs& p, int block, int bloc
   __syncthreads();
   if (!last_block) return;
   __threadfence();
-  if (threadIdx.x == 0) *p.counter = 0;
+  if (threadIdx.x < 3) p.counter[threadIdx.x] = 0;
   const auto length = [](int4 r) { return r.w - r.z + max(0, r.y - r.x); };
   if (BACK) {
     sort_by_work<kPlanThreads>(
@@ -217,12 +217,6 @@ __device__ __forceinline__ void make_plan(const AttnArgs& p, int block, int bloc
         });
   }
 }
-// The job of a block's k-th turn: the blocks take turns forwards and backwards,
-// so that each gets as much of the longest first order as the others.
-__device__ __forceinline__ int job_of(int k) {
-  return k * static_cast<int>(gridDim.x) + static_cast<int>(k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
-
 // Records offsets that are out of range or decrease; one block calls it.
 __device__ __forceinline__ void check_offsets(const AttnArgs& p, const DevStatus& st, int kid) {
   if (p.cu == nullptr) return;
@@ -401,8 +395,60 @@ static __device__ __noinline__ bool mbar_sleep_on(uint64_t* bar, uint32_t parity
   return true;
 }
 __device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, volatile int* abort, const DevStatus& st, int kid) {
-  return mbar_sleep(bar, parity) || mbar_sleep_on(bar, parity, abort, st, kid);
+  return mbar_try_wait(bar, parity) || mbar_sleep(bar, parity) || mbar_sleep_on(bar, parity, abort, st, kid);
 }
+// The jobs of a block pass through two slots of shared memory: its loading thread
+// takes one when it has asked for all that the last one needs (from a counter, in
+// the order of the plan), the other warps read it.  tile < 0: no more.
+struct JobSlots {
+  uint64_t full[2], empty[2];
+  int4 job[2][3];
+};
+__device__ __forceinline__ void init_slots(JobSlots& q, int readers) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&q.full[i], 1);
+    mbar_init(&q.empty[i], readers);
+  }
+}
+// The loading thread's side.
+struct JobSource {
+  JobSlots& q;
+  unsigned int* counter;   // null: the block's only job is its index
+  int k, claimed;
+  __device__ JobSource(JobSlots& q, unsigned int* counter) : q(q), counter(counter), k(0), claimed(blockIdx.x) {}
+  // The next job's number, once; the one after it is on its way then.
+  __device__ int claim() {
+    const int i = claimed;
+    claimed = counter ? static_cast<int>(gridDim.x + atomicAdd(counter, 1u)) : INT_MAX;
+    return i;
+  }
+  __device__ bool publish(const int4 (&j)[3], volatile int* abort, const DevStatus& st, int kid) {
+    if (!wait_asleep(&q.empty[k & 1], (k >> 1 & 1) ^ 1, abort, st, kid)) return false;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) q.job[k & 1][c] = j[c];
+    mbar_arrive(&q.full[k & 1]);
+    ++k;
+    return true;
+  }
+};
+// A reading warp's side.
+struct JobReader {
+  JobSlots& q;
+  int k;
+  __device__ JobReader(JobSlots& q) : q(q), k(0) {}
+  // The next job (its words), looked at; false: there is none.
+  __device__ bool peek(int4 (&j)[3], volatile int* abort, const DevStatus& st, int kid) {
+    if (!__all_sync(0xffffffffu, wait_asleep(&q.full[k & 1], k >> 1 & 1, abort, st, kid))) return false;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) j[c] = q.job[k & 1][c];
+    return j[0].x >= 0;
+  }
+  __device__ void pop() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&q.empty[k & 1]);
+    ++k;
+  }
+};
 // The same value in every lane, where the compiler cannot know that it is.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 

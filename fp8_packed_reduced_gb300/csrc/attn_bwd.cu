@@ -76,6 +76,7 @@ struct Shared {
   int abort;
   int lo[4], hi[4], start[4];
   Range range;                        // of a block's only job, without a plan
+  alignas(16) JobSlots slots;
 };
 
 // Warps that arrive at, or commits that complete, each barrier.
@@ -101,6 +102,7 @@ __device__ __forceinline__ void init_barriers(Shared& g, int fixed_full, int b_u
   mbar_init(&g.acc_free[0], 4);
   mbar_init(&g.acc_free[1], 4);
   mbar_init(&g.end, 2);
+  init_slots(g.slots, 10);
   fence_mbar_init();
 }
 // A float as three bf16 that add up to it (an infinity or NaN as the first), and five zeros.
@@ -220,42 +222,7 @@ struct DqJob {
   __device__ int begin() const { return r.sink0 < r.sink1 ? r.sink0 : r.first; }
   __device__ int after(int kt) const { return kt + 1 == r.sink1 ? r.first : kt + 1; }
 };
-struct DqJobs {
-  const AttnArgs& p;
-  const Shared& g;
-  int total, k, tile, head;
-  int4 r;
-  bool more;
-  __device__ DqJobs(const AttnArgs& p, const Shared& g, int total) : p(p), g(g), total(total), k(0) { fetch(); }
-  __device__ void fetch() {
-    if (!p.spans) {
-      more = k == 0;
-      return;
-    }
-    const int i = job_of(k), at = i / p.Hq;
-    more = i < total;
-    head = i - at * p.Hq;
-    if (more) {
-      tile = __ldcg(&p.jobs[0][3 * at].x);
-      r = __ldcg(p.jobs[0] + 3 * at + 1);
-    }
-  }
-  __device__ bool next(DqJob& j) {
-    if (!more) return false;
-    if (!p.spans) {
-      j.tile = blockIdx.x / p.Hq;
-      j.head = blockIdx.x - j.tile * p.Hq;
-      j.r = g.range;
-    } else {
-      j.tile = tile;
-      j.head = head;
-      j.r = Range{r.x, r.y, r.z, r.w};
-    }
-    ++k;
-    fetch();
-    return true;
-  }
-};
+__device__ __forceinline__ DqJob dq_job_of(const int4 (&w)[3]) { return DqJob{w[0].x, w[0].y, Range{w[1].x, w[1].y, w[1].z, w[1].w}}; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -293,15 +260,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = g.tmem;
-  DqJobs jobs(p, g, total);
-  DqJob job;
+  int4 words[3] = {};
 
   if (warp == 8) {
     if (lane == 0) {
       int n = 0;
       bool ok = true;
+      JobSource source(g.slots, p.spans ? p.counter + 1 : nullptr);
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      for (int i = source.claim(); ok; i = source.claim()) {
+        const int at = i / p.Hq;
+        if (i >= total) {
+          words[0].x = -1;
+        } else {
+          words[0] = make_int4(p.spans ? __ldcg(&p.jobs[0][3 * at].x) : at, i - at * p.Hq, 0, 0);
+          words[1] = p.spans ? __ldcg(p.jobs[0] + 3 * at + 1) : make_int4(g.range.sink0, g.range.sink1, g.range.first, g.range.last);
+        }
+        ok = source.publish(words, &g.abort, st, KID_ATTN_DQ);
+        if (!ok || i >= total) break;
+        const DqJob job = dq_job_of(words);
         const int h = job.head / p.G;
 #pragma unroll 1
         for (int kt = job.begin(); kt < job.r.last; kt = job.after(kt), ++n) {
@@ -333,12 +310,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto wait = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, wait_asleep(bar, par, &g.abort, st, KID_ATTN_DQ));
     };
+    JobReader jobs(g.slots);
     bool ok = true;
     int n = 0, turn = 0;   // steps; jobs with any
     if (warp == 9) {
       const uint64_t k0 = KTile<D>::desc(sk);
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      while (ok && jobs.peek(words, &g.abort, st, KID_ATTN_DQ)) {
+        DqJob job = dq_job_of(words);
+        jobs.pop();
         job.make_uniform();
         if (job.begin() >= job.r.last) continue;
         ok = wait(&g.fixed_full, turn++ & 1);
@@ -370,7 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      while (ok && jobs.peek(words, &g.abort, st, KID_ATTN_DQ)) {
+        DqJob job = dq_job_of(words);
+        jobs.pop();
         job.make_uniform();
         if (job.begin() >= job.r.last) continue;
         ok = wait(&g.fixed_full, turn++ & 1) && dps(n);
@@ -431,11 +413,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int n = 0, turn = 0;   // steps; jobs with any
     bool ok = true;
+    JobReader jobs(g.slots);
+    bool more = jobs.peek(words, &g.abort, st, KID_ATTN_DQ);
+    if (more) read_rows(words[0].x, words[0].y);
 #pragma unroll 1
-    while (ok && jobs.next(job)) {
+    while (ok && more) {
+      const DqJob job = dq_job_of(words);
+      jobs.pop();
       const int row = job.tile * kTile + mine, hq = job.head;
       const bool some = job.begin() < job.r.last;
-      if (jobs.k == 1) read_rows(job.tile, hq);
       const int begin = start, seen0 = begin < 0 ? INT_MAX : window_start(p, row, begin);
       const int sink_end = begin < 0 ? 0 : begin + min(p.sinks, p.T);
       if (some) {
@@ -484,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      const bool more = jobs.more;
-      if (more) read_rows(jobs.tile, jobs.head);   // the next job's, on their way while this one ends
+      more = jobs.peek(words, &g.abort, st, KID_ATTN_DQ);
+      if (more) read_rows(words[0].x, words[0].y);   // the next job's, on their way while this one ends
       if (some) ok = wait_asleep(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DQ);
       if (!ok) break;
       tc_fence_after();
@@ -520,42 +506,11 @@ struct DkvJob {
   int tile, head, count, tiles;   // steps, and those of one query head
   __device__ void make_uniform() { count = uniform(count); }
 };
-struct DkvJobs {
-  const AttnArgs& p;
-  const Shared& g;
-  int total, queries, k, head;
-  int4 r;
-  bool more;
-  __device__ DkvJobs(const AttnArgs& p, const Shared& g, int total, int queries) : p(p), g(g), total(total), queries(queries), k(0) { fetch(); }
-  __device__ void fetch() {
-    if (!p.spans) {
-      more = k == 0;
-      return;
-    }
-    const int i = job_of(k), at = i / p.H;
-    more = i < total;
-    head = i - at * p.H;
-    if (more) r = __ldcg(p.jobs[1] + at);
-  }
-  __device__ bool next(DkvJob& j) {
-    if (!more) return false;
-    int end;
-    if (!p.spans) {
-      j.tile = blockIdx.x / p.H;
-      j.head = blockIdx.x - j.tile * p.H;
-      end = max(max(g.hi[0], g.hi[1]), max(g.hi[2], g.hi[3]));
-    } else {
-      j.tile = r.x;
-      j.head = head;
-      end = r.y;
-    }
-    j.tiles = (max(0, end - j.tile * kTile) + queries - 1) / queries;
-    j.count = j.tiles * p.G;
-    ++k;
-    fetch();
-    return true;
-  }
-};
+// From the words of a slot: the tile and the head, the end of the queries.
+__device__ __forceinline__ DkvJob dkv_job_of(const int4 (&w)[3], int queries, int G) {
+  const int tiles = (max(0, w[0].z - w[0].x * kTile) + queries - 1) / queries;
+  return DkvJob{w[0].x, w[0].y, tiles * G, tiles};
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -600,15 +555,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = g.tmem;
-  DkvJobs jobs(p, g, total, QN);
-  DkvJob job;
+  int4 words[3] = {};
 
   if (warp == 8) {
     if (lane == 0) {
       int na = 0, nb = 0, turn = 0;   // steps whose q, whose da has been asked for; jobs with any
       bool ok = true;
+      JobSource source(g.slots, p.spans ? p.counter + 2 : nullptr);
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      for (int i = source.claim(); ok; i = source.claim()) {
+        const int at = i / p.H;
+        if (i >= total) {
+          words[0].x = -1;
+        } else if (p.spans) {
+          const int4 j = __ldcg(p.jobs[1] + at);
+          words[0] = make_int4(j.x, i - at * p.H, j.y, 0);
+        } else {
+          words[0] = make_int4(at, i - at * p.H, max(max(g.hi[0], g.hi[1]), max(g.hi[2], g.hi[3])), 0);
+        }
+        ok = source.publish(words, &g.abort, st, KID_ATTN_DKV);
+        if (!ok || i >= total) break;
+        const DkvJob job = dkv_job_of(words, QN, p.G);
         if (job.count == 0) continue;
         const int r0 = job.tile * kTile;
         ok = wait_asleep(&g.fixed_empty, (turn & 1) ^ 1, &g.abort, st, KID_ATTN_DKV);
@@ -658,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const uint64_t ones0 = sdesc_plain(smem_u32(ones), kOnesBytes, 128);
     const auto stat_desc = [&](const uint8_t* at) { return sdesc_plain(smem_u32(at), static_cast<uint32_t>(zeros - at), 128); };
+    JobReader jobs(g.slots);
     bool ok = true;
     int n = 0, turn = 0;   // steps; jobs with any
     if (warp == 9) {
@@ -675,7 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      while (ok && jobs.peek(words, &g.abort, st, KID_ATTN_DKV)) {
+        DkvJob job = dkv_job_of(words, QN, p.G);
+        jobs.pop();
         job.make_uniform();
         if (job.count == 0) continue;
         ok = wait(&g.fixed_full, turn & 1) && scores(n);
@@ -713,7 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      while (ok && jobs.peek(words, &g.abort, st, KID_ATTN_DKV)) {
+        DkvJob job = dkv_job_of(words, QN, p.G);
+        jobs.pop();
         job.make_uniform();
         if (job.count == 0) continue;
         ok = wait(&g.fixed_full, turn & 1) && dps(n);
@@ -749,11 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = so + warp * kOutBytes;
     int n = 0, turn = 0;   // steps; jobs with any
     bool ok = true;
-    Span ahead{-1, -1};
+    JobReader jobs(g.slots);
+    bool more = jobs.peek(words, &g.abort, st, KID_ATTN_DKV);
+    Span ahead = more ? span_at(words[0].x * kTile + mine) : Span{-1, -1};   // (the next job's is read ahead)
 #pragma unroll 1
-    while (ok && jobs.next(job)) {
+    while (ok && more) {
+      const DkvJob job = dkv_job_of(words, QN, p.G);
+      jobs.pop();
       const int r0 = job.tile * kTile, row = r0 + mine;
-      if (jobs.k == 1) ahead = span_at(row);   // the others are read ahead
       // queries [row, end) see this thread's key; those from ds0 on pass something on
       const int end = ahead.start < 0 ? row : last_seer(p, row, ahead);
       const int ds0 = row + (ahead.start >= 0 && alone(p, row, ahead.start) ? 1 : 0);
@@ -809,7 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const bool some = job.count > 0;
-      if (jobs.more) ahead = span_at(jobs.r.x * kTile + mine);   // the next job's
+      more = jobs.peek(words, &g.abort, st, KID_ATTN_DKV);
+      if (more) ahead = span_at(words[0].x * kTile + mine);
       if (some) ok = wait_asleep(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DKV);
       if (!ok) break;
       tc_fence_after();

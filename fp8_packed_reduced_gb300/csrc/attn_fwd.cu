@@ -55,6 +55,7 @@ struct Shared {
   int abort;
   int lo[2][4], hi[2][4], start[2][4];
   Range range[2];                  // of a block's only job, without a plan
+  alignas(16) JobSlots slots;
 };
 
 // The jobs of a block, one after the other: 256 query rows of a head.
@@ -81,42 +82,15 @@ struct Job {
   __device__ int begin() const { return a0; }
   __device__ int after(int kt) const { return kt + 1 == a1 ? b0 : kt + 1; }   // (past b1: the end)
 };
-struct Jobs {
-  const AttnArgs& p;
-  const Shared& g;
-  int total, k, head;
-  int4 r[3];   // the next job
-  bool more;
-  __device__ Jobs(const AttnArgs& p, const Shared& g, int total) : p(p), g(g), total(total), k(0) { fetch(); }
-  __device__ void fetch() {
-    if (!p.spans) {
-      more = k == 0;
-      return;
-    }
-    const int i = job_of(k), at = i / p.Hq;
-    more = i < total;
-    head = i - at * p.Hq;
-    if (more)
-      for (int c = 0; c < 3; ++c) r[c] = __ldcg(p.jobs[0] + 3 * at + c);
-  }
-  __device__ bool next(Job& j) {
-    if (!more) return false;
-    if (!p.spans) {
-      j.tile = blockIdx.x / p.Hq;
-      j.head = blockIdx.x - j.tile * p.Hq;
-      j.range[0] = g.range[0];
-      j.range[1] = g.range[1];
-    } else {
-      j.tile = r[0].x;
-      j.head = head;
-      for (int c = 0; c < 2; ++c) j.range[c] = Range{r[1 + c].x, r[1 + c].y, r[1 + c].z, r[1 + c].w};
-    }
-    j.steps();
-    ++k;
-    fetch();
-    return true;
-  }
-};
+// From the words of a slot: the tile and the head, and the key tiles of both query tiles.
+__device__ __forceinline__ Job job_of(const int4 (&w)[3]) {
+  Job j;
+  j.tile = w[0].x;
+  j.head = w[0].y;
+  for (int c = 0; c < 2; ++c) j.range[c] = Range{w[1 + c].x, w[1 + c].y, w[1 + c].z, w[1 + c].w};
+  j.steps();
+  return j;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -147,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&g.o_free[t], 4);
     }
     mbar_init(&g.end, 3);
+    init_slots(g.slots, 11);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -173,15 +148,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = g.tmem;
-  Jobs jobs(p, g, total);
-  Job job;
+  int4 words[3];
 
   if (warp == 8) {
     if (lane == 0) {
       int n = 0, loads = 0;   // steps; jobs that have loaded q
       bool ok = true;
+      JobSource source(g.slots, p.spans ? p.counter + 1 : nullptr);
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      for (int i = source.claim(); ok; i = source.claim()) {
+        const int at = i / p.Hq;
+        if (i >= total) {
+          words[0] = make_int4(-1, 0, 0, 0);
+        } else if (p.spans) {
+          for (int c = 0; c < 3; ++c) words[c] = __ldcg(p.jobs[0] + 3 * at + c);
+          words[0].y = i - at * p.Hq;
+        } else {
+          words[0] = make_int4(at, i - at * p.Hq, 0, 0);
+          for (int c = 0; c < 2; ++c) words[1 + c] = make_int4(g.range[c].sink0, g.range[c].sink1, g.range[c].first, g.range[c].last);
+        }
+        ok = source.publish(words, &g.abort, st, KID_ATTN_FWD);
+        if (!ok || i >= total) break;
+        const Job job = job_of(words);
         if (job.begin() >= job.b1) continue;
         const int h = job.head / p.G, r0 = job.tile * kRows;
         const bool used[2] = {job.range[0].first < job.range[0].last, job.range[1].first < job.range[1].last};
@@ -223,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto wait = [&](uint64_t* bar, uint32_t par) {
       return __all_sync(0xffffffffu, wait_asleep(bar, par, &g.abort, st, KID_ATTN_FWD));
     };
+    JobReader jobs(g.slots);
     bool ok = true;
     int n = 0;
     if (warp == 9) {
@@ -230,7 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q0 = QTile<D>::desc(sq), k0 = KTile<D>::desc(sk);
       int formed[2] = {0, 0}, loads = 0;
 #pragma unroll 1
-      while (ok && jobs.next(job)) {
+      while (ok && jobs.peek(words, &g.abort, st, KID_ATTN_FWD)) {
+        Job job = job_of(words);
+        jobs.pop();
         job.make_uniform();
         if (job.begin() >= job.b1) continue;
         ok = wait(&g.q_full, loads++ & 1);
@@ -261,7 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tp = tmem + p_col(i), to = tmem + o_col(i);
       const uint64_t v0 = VTile::desc(sv);
       int added = 0;
-      for (int turn = 0; ok && jobs.next(job); ++turn) {
+#pragma unroll 1
+      for (int turn = 0; ok && jobs.peek(words, &g.abort, st, KID_ATTN_FWD); ++turn) {
+        Job job = job_of(words);
+        jobs.pop();
         bool first = true;
         job.make_uniform();
 #pragma unroll 1
@@ -297,12 +291,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = tile * kRows + threadIdx.x;
       return row >= p.T ? -1 : p.spans ? __ldcg(p.spans + row).x : span_of(p, row).start;
     };
-    int start = 0;
+    JobReader jobs(g.slots);
+    bool more = jobs.peek(words, &g.abort, st, KID_ATTN_FWD);
+    int start = more ? start_of(words[0].x) : 0;   // (the next job's is read ahead)
 #pragma unroll 1
-    while (ok && jobs.next(job)) {
+    while (ok && more) {
+      const Job job = job_of(words);
+      jobs.pop();
       const Range r = t == 0 ? job.range[0] : job.range[1];
       const int hq = job.head, row = job.tile * kRows + threadIdx.x;
-      if (jobs.k == 1) start = start_of(job.tile);   // the others are read ahead
       const Span sp{start, 0};
       const int seen0 = sp.start < 0 ? INT_MAX : window_start(p, row, sp.start);   // first token of the row's window
       const int sink_end = sp.start < 0 ? 0 : sp.start + min(p.sinks, p.T);
@@ -379,7 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&g.p_full[t]);
         begun = true;
       }
-      if (jobs.more) start = start_of(jobs.r[0].x);   // the next job's
+      if (!ok) break;
+      more = jobs.peek(words, &g.abort, st, KID_ATTN_FWD);
+      if (more) start = start_of(words[0].x);
       if (ok && begun) ok = wait_asleep(&g.o_done[t], (n - 1) & 1, &g.abort, st, KID_ATTN_FWD);
       if (!ok) break;
       tc_fence_after();
