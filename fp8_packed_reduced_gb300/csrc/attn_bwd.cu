@@ -51,7 +51,7 @@ __host__ __device__ constexpr int da_stages(int d) { return d == 64 ? 3 : 2; }
 // shared memory by every thread, beside the operands that its bandwidth bounds
 // this pass by.  They come into the sums as 16 columns of K more: three bf16, which
 // hold a float, times ones.  (As float values read by every thread: a step took
-// 2065 cycles instead of @@.)
+// 2065 cycles instead of 1817.)
 constexpr int kOnesBytes = kTile * 16;       // of the ones, and of the zeros of columns 8 to 15 that all share
 constexpr int kStatBytes = 16;               // of a row
 template <int D>
@@ -386,28 +386,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tds = tmem + kQDs + kHalf / 2 * half + quarter;
     const f2 sc = f2_make(p.scale_log2, p.scale_log2);
     uint8_t* stage = so + warp * kOutBytes;
-    // One warpgroup brings q into TMEM, the other da; the next job's are read while this one ends.
-    constexpr int kParts = (D > kDv ? D : kDv) / 8;
-    uint4 rows[kParts];
-    const int parts = half == 0 ? D / 8 : kDv / 8;
-    int start = -1;
-    const auto read_rows = [&](int tile, int head) {
-      const int row = tile * kTile + mine;
-      const uint4* from = reinterpret_cast<const uint4*>(half == 0 ? p.q + (static_cast<int64_t>(head) * p.T + row) * D
-                                                                   : p.da + (static_cast<int64_t>(row) * p.Hq + head) * kDv);
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) rows[i] = i < parts && row < p.T ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
-      start = start_of(row);
+    // One warpgroup brings q into TMEM, the other da.  While a job ends, the next
+    // one's rows go no further than the second cache: held here they took 64
+    // registers and pushed others out to memory (six sequences of 8192, 6 heads,
+    // d = 96, both passes: 1486 us against 1389).
+    const int width = half == 0 ? D : kDv;
+    const auto rows_of = [&](int tile, int head) {
+      const int64_t row = min(tile * kTile + mine, p.T - 1);
+      return half == 0 ? p.q + (head * static_cast<int64_t>(p.T) + row) * D : p.da + (row * p.Hq + head) * kDv;
     };
-    const auto store_rows = [&] {
+    const auto bring_rows = [&](int tile, int head) {
+      const uint4* from = reinterpret_cast<const uint4*>(rows_of(tile, head));
+      const bool real = tile * kTile + mine < p.T;
       const uint32_t to = tmem + (half == 0 ? kQOpQ : kQOpDa) + quarter;
 #pragma unroll
-      for (int i = 0; i < kParts; i += 4)
-        if (i < parts) {
-          const uint32_t w[16] = {rows[i].x,     rows[i].y,     rows[i].z,     rows[i].w,     rows[i + 1].x, rows[i + 1].y,
-                                  rows[i + 1].z, rows[i + 1].w, rows[i + 2].x, rows[i + 2].y, rows[i + 2].z, rows[i + 2].w,
-                                  rows[i + 3].x, rows[i + 3].y, rows[i + 3].z, rows[i + 3].w};
-          tmem_st16(to + 4 * i, w);
+      for (int c = 0; c < 128; c += 64)
+        if (c < width) {
+          uint4 r[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = real && c + 8 * i < width ? __ldg(from + c / 8 + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            if (c + 8 * i < width) {
+              const uint32_t w[16] = {r[i].x,     r[i].y,     r[i].z,     r[i].w,     r[i + 1].x, r[i + 1].y, r[i + 1].z, r[i + 1].w,
+                                      r[i + 2].x, r[i + 2].y, r[i + 2].z, r[i + 2].w, r[i + 3].x, r[i + 3].y, r[i + 3].z, r[i + 3].w};
+              tmem_st16(to + c / 2 + 4 * i, w);
+            }
         }
       tmem_st_wait();
     };
@@ -415,17 +419,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     JobReader jobs(g.slots);
     bool more = jobs.peek(words, &g.abort, st, KID_ATTN_DQ);
-    if (more) read_rows(words[0].x, words[0].y);
 #pragma unroll 1
     while (ok && more) {
       const DqJob job = dq_job_of(words);
       jobs.pop();
       const int row = job.tile * kTile + mine, hq = job.head;
       const bool some = job.begin() < job.r.last;
-      const int begin = start, seen0 = begin < 0 ? INT_MAX : window_start(p, row, begin);
+      const int begin = start_of(row), seen0 = begin < 0 ? INT_MAX : window_start(p, row, begin);
       const int sink_end = begin < 0 ? 0 : begin + min(p.sinks, p.T);
       if (some) {
-        store_rows();
+        bring_rows(job.tile, hq);
         arrive_warp(&g.fixed_full);
         const float* stat = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;
         const float z0 = __ldcg(stat), delta = __ldcg(stat + p.Tp);
@@ -471,7 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       more = jobs.peek(words, &g.abort, st, KID_ATTN_DQ);
-      if (more) read_rows(words[0].x, words[0].y);   // the next job's, on their way while this one ends
+      if (more) {
+        const uint16_t* next = rows_of(words[0].x, words[0].y);
+        prefetch_l2(next);
+        prefetch_l2(next + width - 1);
+      }
       if (some) ok = wait_asleep(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DQ);
       if (!ok) break;
       tc_fence_after();
