@@ -1045,9 +1045,12 @@ def attention_backward(da, q, k, v, a, lse, cu=None, window=None, sinks=0, scale
     _quick_cuda(da, "da", torch.bfloat16, (d.T, d.Hq * 128), dev)
     _quick_cuda(a, "a", torch.bfloat16, (d.T, d.Hq * 128), dev)
     _quick_cuda(lse, "lse", torch.float32, (d.Hq, d.T), dev)
-    o = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v)) if out is None else out
-    for name, like in (("dq", q), ("dk", k), ("dv", v)):
-        _quick_cuda(o[name], name, torch.bfloat16, like.shape, dev)
+    if out is None:
+        o = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
+    else:
+        o = out
+        for name, like in (("dq", q), ("dk", k), ("dv", v)):
+            _quick_cuda(o[name], name, torch.bfloat16, like.shape, dev)
     r = ctypes.byref(d)
     _cache_call("qkvp_attention_backward", dev, ws, lambda: lib().qkvp_attention_workspace_bytes(r), r, da.data_ptr(),
                 q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), lse.data_ptr(), o["dq"].data_ptr(),
@@ -1108,13 +1111,14 @@ def norm_rope_forward(y, pos, rope_table, Hq, H, d_qk=96, q_gain=None, k_gain=No
     T = d.T
     if out is None:
         bf = dict(dtype=torch.bfloat16, device=y.device)
-        out = (torch.empty((Hq, T, d_qk), **bf), torch.empty((H, T, d_qk), **bf), torch.empty((H, T, 128), **bf),
-               torch.empty((Hq + H, T), dtype=torch.float32, device=y.device))
-    q, k, v, rstd = out
-    _quick_cuda(q, "q", torch.bfloat16, (Hq, T, d_qk), dev)
-    _quick_cuda(k, "k", torch.bfloat16, (H, T, d_qk), dev)
-    _quick_cuda(v, "v", torch.bfloat16, (H, T, 128), dev)
-    _quick_cuda(rstd, "rstd", torch.float32, (Hq + H, T), dev)
+        q, k, v = torch.empty((Hq, T, d_qk), **bf), torch.empty((H, T, d_qk), **bf), torch.empty((H, T, 128), **bf)
+        rstd = torch.empty((Hq + H, T), dtype=torch.float32, device=y.device)
+    else:
+        q, k, v, rstd = out
+        _quick_cuda(q, "q", torch.bfloat16, (Hq, T, d_qk), dev)
+        _quick_cuda(k, "k", torch.bfloat16, (H, T, d_qk), dev)
+        _quick_cuda(v, "v", torch.bfloat16, (H, T, 128), dev)
+        _quick_cuda(rstd, "rstd", torch.float32, (Hq + H, T), dev)
     r = ctypes.byref(d)
     _cache_call("qkvp_norm_rope_forward", dev, ws, lambda: lib().qkvp_norm_rope_workspace_bytes(r), r, y.data_ptr(),
                 q.data_ptr(), k.data_ptr(), v.data_ptr(), rstd.data_ptr())
@@ -1139,12 +1143,13 @@ def norm_rope_backward(dq, dk, dv, y, rstd, pos, rope_table, q_gain=None, k_gain
     _quick_cuda(rstd, "rstd", torch.float32, (Hq + H, T), dev)
     if out is None:
         make = lambda: None if q_gain is None else torch.empty((d_qk,), dtype=torch.float32, device=y.device)   # noqa: E731
-        out = dict(dy=torch.empty((T, y.shape[1]), dtype=torch.bfloat16, device=y.device), dq_gain=make(), dk_gain=make())
-    o = out
-    _quick_cuda(o["dy"], "dy", torch.bfloat16, tuple(y.shape), dev)
-    if q_gain is not None:
-        _quick_cuda(o["dq_gain"], "dq_gain", torch.float32, (d_qk,), dev)
-        _quick_cuda(o["dk_gain"], "dk_gain", torch.float32, (d_qk,), dev)
+        o = dict(dy=torch.empty((T, y.shape[1]), dtype=torch.bfloat16, device=y.device), dq_gain=make(), dk_gain=make())
+    else:
+        o = out
+        _quick_cuda(o["dy"], "dy", torch.bfloat16, tuple(y.shape), dev)
+        if q_gain is not None:
+            _quick_cuda(o["dq_gain"], "dq_gain", torch.float32, (d_qk,), dev)
+            _quick_cuda(o["dk_gain"], "dk_gain", torch.float32, (d_qk,), dev)
     r = ctypes.byref(d)
     _cache_call("qkvp_norm_rope_backward", dev, ws, lambda: lib().qkvp_norm_rope_workspace_bytes(r), r, dq.data_ptr(),
                 dk.data_ptr(), dv.data_ptr(), y.data_ptr(), rstd.data_ptr(), o["dy"].data_ptr(),

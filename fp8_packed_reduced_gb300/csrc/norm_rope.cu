@@ -3,9 +3,19 @@
 //   forward   r = (mean x^2 + eps)^-1/2,  q, k = R(x r gain),  v = x
 //   backward  g = R^T(dq),  dgain = sum g x r,
 //             dx = r (g gain - x r mean(g gain x r)),  dv as it is
-// with R the rotation of the pairs (i, i + d / 2) by their angles.  Each value
-// is read once and written once; a token's cosines and sines are read once for
-// all its heads.
+// with R the rotation of the pairs (i, i + d / 2) by their angles.  Sums, r and
+// the gains' gradients are float; rounded to bf16 (2^-8) are the results only.
+//
+// Each value is read once and written once, so memory is the bound, and what it
+// takes is enough bytes under way: a thread's rows come into shared memory by its
+// own asynchronous copies, a few rows ahead, with no registers held and nothing to
+// wait for but these.  Measured with 49152 tokens of 6 + 6 + 6 heads, d = 96
+// (warm; bytes at the rate of a copy: 56 / 73 us), forward / gradient with gains:
+//   rows loaded as they are needed, two at a time        109 / 187 us
+//   three (two) rows at a time, 5 (4) blocks of 128       74 / 105
+//   rows ahead in shared memory, pairs of floats          62 / 104
+//   rstd among them                                            93
+//   even turns instead of a range of tokens for a block        88
 #include <algorithm>
 #include <cmath>
 
@@ -20,6 +30,7 @@ enum NormKernelId : int { KID_NORM_FWD = 22, KID_NORM_BWD = 23 };
 struct NormArgs {
   int T, Hq, H, axes, max_pos;
   int bound[2];             // entries of the table from which on the second, the third axis turns
+  int chunk_rows;           // (backward) the most rows of a chunk
   int64_t ldy;              // elements between rows of y
   float eps;
   const float* table;       // [d / 4][max_pos][4]
@@ -34,7 +45,11 @@ struct NormArgs {
   float *dq_gain, *dk_gain;
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// Blocks a multiprocessor and rows held for a thread.  (Forward: 5 to 8 blocks, 3
+// to 8 rows are within 3 %.  Backward: 4 blocks 97 us instead of 93; 6 leave too few
+// registers, 117.  More rows change nothing.)
+constexpr int kForwardBlocks = 7, kForwardSlots = 4, kBackwardBlocks = 5, kBackwardSlots = 3;
 constexpr int kNormHeader = 1024;   // of the workspace: the status word
 constexpr int kMaxNormBlocks = 2048;
 
@@ -46,13 +61,8 @@ struct Lanes {
   static constexpr int TOKENS = kThreads / GROUP;   // of a block
 };
 
-__device__ __forceinline__ void unpack8(float (&x)[8], uint4 w) {
-  x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-  x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
+// A value that nothing reads again.
+__device__ __forceinline__ uint4 load_once(const uint4* p) { return __ldcs(p); }
 template <int GROUP>
 __device__ __forceinline__ float group_add(float v) {
 #pragma unroll
@@ -60,8 +70,15 @@ __device__ __forceinline__ float group_add(float v) {
   return v;
 }
 
+__device__ __forceinline__ void unpack_f2(f2 (&x)[4], uint4 w) {
+  x[0] = f2_from_bf16x2(w.x), x[1] = f2_from_bf16x2(w.y), x[2] = f2_from_bf16x2(w.z), x[3] = f2_from_bf16x2(w.w);
+}
+__device__ __forceinline__ uint4 pack_f2(const f2 (&x)[4]) {
+  return make_uint4(f2_to_bf16x2(x[0]), f2_to_bf16x2(x[1]), f2_to_bf16x2(x[2]), f2_to_bf16x2(x[3]));
+}
+
 // Cosines and sines of the lane's eight pairs.
-__device__ __forceinline__ void load_turn(const NormArgs& p, int t, int c, float (&cs)[8], float (&sn)[8], const DevStatus& st, int kid) {
+__device__ __forceinline__ void load_turn(const NormArgs& p, int t, int c, f2 (&cs)[4], f2 (&sn)[4], const DevStatus& st, int kid) {
   int at[3];
   bool bad = false;
 #pragma unroll
@@ -75,32 +92,42 @@ __device__ __forceinline__ void load_turn(const NormArgs& p, int t, int c, float
   for (int i = 0; i < 4; ++i) {
     const int j = 4 * c + i, x = j < p.bound[0] ? at[0] : j < p.bound[1] ? at[1] : at[2];
     const float4 e = __ldg(reinterpret_cast<const float4*>(p.table) + static_cast<int64_t>(j) * p.max_pos + x);
-    cs[2 * i] = e.x, cs[2 * i + 1] = e.y, sn[2 * i] = e.z, sn[2 * i + 1] = e.w;
+    cs[i] = f2_make(e.x, e.y);
+    sn[i] = f2_make(e.z, e.w);
   }
 }
 
-__device__ __forceinline__ void load_gain(const float* gain, int D, int c, float (&lo)[8], float (&hi)[8]) {
+__device__ __forceinline__ void load_gain(const float* gain, int D, int c, f2 (&lo)[4], f2 (&hi)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = gain ? __ldg(gain + 8 * c + i) : 1.f;
-    hi[i] = gain ? __ldg(gain + D / 2 + 8 * c + i) : 1.f;
+  for (int i = 0; i < 4; ++i) {
+    const float2* at = reinterpret_cast<const float2*>(gain + 8 * c) + i;
+    const float2 one = make_float2(1.f, 1.f), a = gain ? __ldg(at) : one, b = gain ? __ldg(at + D / 4) : one;
+    lo[i] = f2_make(a.x, a.y);
+    hi[i] = f2_make(b.x, b.y);
   }
 }
 
-// Copies the rows of v between y's form and the head-major one.
+// Rows first .. last - 1 of v, copied between y's form and the head-major one.
 template <int D, bool BACK>
 __device__ __forceinline__ void copy_v(const NormArgs& p, int t, int c, int64_t N, int first, int last) {
-  constexpr int GROUP = Lanes<D>::GROUP;
-  const int64_t col = static_cast<int64_t>(p.Hq + p.H) * D;
-#pragma unroll 2
-  for (int h = first; h < last; ++h) {
-    const uint4* from = reinterpret_cast<const uint4*>(BACK ? p.dv + (static_cast<int64_t>(h) * p.T + t) * kDv : p.y + t * p.ldy + col + h * kDv);
-    uint4* to = reinterpret_cast<uint4*>(BACK ? p.dy + t * N + col + h * kDv : p.v + (static_cast<int64_t>(h) * p.T + t) * kDv);
-    uint4 w[16 / GROUP];
+  constexpr int GROUP = Lanes<D>::GROUP, EACH = 16 / GROUP, BATCH = 8 / EACH;
+  const int64_t col = static_cast<int64_t>(p.Hq + p.H) * D, row = static_cast<int64_t>(p.T) * kDv;
+  const uint16_t* from = BACK ? p.dv + static_cast<int64_t>(t) * kDv : p.y + t * p.ldy + col;
+  uint16_t* to = BACK ? p.dy + t * N + col : p.v + static_cast<int64_t>(t) * kDv;
+  const int64_t from_step = BACK ? row : kDv, to_step = BACK ? kDv : row;
+#pragma unroll 1
+  for (int h = first; h < last; h += BATCH) {
+    uint4 w[BATCH][EACH];
 #pragma unroll
-    for (int i = 0; i < 16 / GROUP; ++i) w[i] = __ldg(from + i * GROUP + c);
+    for (int b = 0; b < BATCH; ++b)
 #pragma unroll
-    for (int i = 0; i < 16 / GROUP; ++i) to[i * GROUP + c] = w[i];
+      for (int i = 0; i < EACH; ++i)
+        if (h + b < last) w[b][i] = load_once(reinterpret_cast<const uint4*>(from + (h + b) * from_step) + i * GROUP + c);
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+      for (int i = 0; i < EACH; ++i)
+        if (h + b < last) reinterpret_cast<uint4*>(to + (h + b) * to_step)[i * GROUP + c] = w[b][i];
   }
 }
 
@@ -111,9 +138,22 @@ __device__ __forceinline__ void head_part(const NormArgs& p, int& first, int& la
   last = min(rows, first + each);
 }
 
+// Rows on their way to a thread: SLOTS places of PARTS words of 16 bytes that are
+// its own, so that nothing but its own copies has to be waited for.
+template <int PARTS, int SLOTS>
+struct Ring {
+  uint4 words[SLOTS][PARTS][kThreads];
+  __device__ __forceinline__ void bring(int at, int part, const uint4* from) {
+    cp16(smem_u32(&words[at % SLOTS][part][threadIdx.x]), from);
+  }
+  __device__ __forceinline__ uint4 get(int at, int part) const { return words[at % SLOTS][part][threadIdx.x]; }
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormArgs p, DevStatus st) {
+__global__ void __launch_bounds__(kThreads, kForwardBlocks) norm_rope_kernel(const __grid_constant__ NormArgs p, DevStatus st) {
   using L = Lanes<D>;
+  constexpr int SLOTS = kForwardSlots;
+  __shared__ Ring<2, SLOTS> ring;
   wait_for_previous();
   const int c = threadIdx.x % L::GROUP;
   const int t = blockIdx.x * L::TOKENS + threadIdx.x / L::GROUP;
@@ -121,117 +161,218 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   const int64_t N = static_cast<int64_t>(p.Hq + p.H) * D + static_cast<int64_t>(p.H) * kDv;
   int first, last;
   head_part(p, first, last);
-  float cs[8], sn[8];
-  if (used && first < p.Hq + p.H) load_turn(p, t, c, cs, sn, st, KID_NORM_FWD);
-  const auto heads = [&](int h0, int h1, const float* gain, uint16_t* out, int base) {
+  const int end = min(last, p.Hq + p.H);   // of the rows of q and k
+  const uint16_t* y = p.y + t * p.ldy + 8 * c;
+  const auto bring = [&](int h) {
+    if (used && h < end) {
+      const uint4* x = reinterpret_cast<const uint4*>(y + static_cast<int64_t>(h) * D);
+      ring.bring(h, 0, x);
+      ring.bring(h, 1, x + D / 16);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < SLOTS - 1; ++i) bring(first + i);
+  f2 cs[4], sn[4];
+  if (used && first < end) load_turn(p, t, c, cs, sn, st, KID_NORM_FWD);
+  const auto heads = [&](int h0, int h1, const float* gain, uint16_t* out) {
     if (h0 >= h1) return;
-    float glo[8], ghi[8];
-    if (used) load_gain(gain, D, c, glo, ghi);
-#pragma unroll 2
-    for (int h = h0; h < h1; ++h) {
-      float lo[8], hi[8], sum = 0.f;
+    f2 glo[4], ghi[4];
+    load_gain(gain, D, min(c, L::USED - 1), glo, ghi);
+    out += static_cast<int64_t>(t) * D + 8 * c;
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h, out += static_cast<int64_t>(p.T) * D) {
+      cp_wait<SLOTS - 2>();
+      f2 lo[4], hi[4], sum = f2_make(0.f, 0.f);
       if (used) {
-        const uint4* x = reinterpret_cast<const uint4*>(p.y + t * p.ldy + static_cast<int64_t>(h) * D);
-        unpack8(lo, __ldg(x + c));
-        unpack8(hi, __ldg(x + D / 16 + c));
+        unpack_f2(lo, ring.get(h, 0));
+        unpack_f2(hi, ring.get(h, 1));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += lo[i] * lo[i] + hi[i] * hi[i];
+        for (int i = 0; i < 4; ++i) sum = f2_fma(hi[i], hi[i], f2_fma(lo[i], lo[i], sum));
       }
-      const float r = 1.f / sqrtf(group_add<L::GROUP>(sum) * (1.f / D) + p.eps);
+      bring(h + SLOTS - 1);
+      const float2 s2 = f2_split(sum);
+      const float r = 1.f / sqrtf(group_add<L::GROUP>(s2.x + s2.y) * (1.f / D) + p.eps);
       if (!used) continue;
-      float a[8], b[8];
+      const f2 rr = f2_make(r, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float u = lo[i] * r * glo[i], w = hi[i] * r * ghi[i];
-        a[i] = u * cs[i] - w * sn[i];
-        b[i] = w * cs[i] + u * sn[i];
+      for (int i = 0; i < 4; ++i) {
+        const f2 u = f2_mul(f2_mul(lo[i], rr), glo[i]), v = f2_mul(f2_mul(hi[i], rr), ghi[i]);
+        lo[i] = f2_sub(f2_mul(u, cs[i]), f2_mul(v, sn[i]));
+        hi[i] = f2_fma(u, sn[i], f2_mul(v, cs[i]));
       }
-      uint4* to = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(h - base) * p.T + t) * D);
-      to[c] = pack8(a);
-      to[D / 16 + c] = pack8(b);
+      *reinterpret_cast<uint4*>(out) = pack_f2(lo);
+      *reinterpret_cast<uint4*>(out + D / 2) = pack_f2(hi);
       if (c == 0) p.rstd[static_cast<int64_t>(h) * p.T + t] = r;
     }
   };
-  heads(first, min(last, p.Hq), p.q_gain, p.q, 0);
-  heads(max(first, p.Hq), min(last, p.Hq + p.H), p.k_gain, p.k, p.Hq);
+  heads(first, min(end, p.Hq), p.q_gain, p.q + static_cast<int64_t>(first) * p.T * D);
+  heads(max(first, p.Hq), end, p.k_gain, p.k + static_cast<int64_t>(max(first, p.Hq) - p.Hq) * p.T * D);
   if (real) copy_v<D, false>(p, t, c, N, max(first, p.Hq + p.H) - p.Hq - p.H, last - p.Hq - p.H);
 }
 
+// Chunks [begin, end) of a kind of rows, `parts` of them a tile.  A token's cosines
+// and sines are read once a chunk, but its blocks end together only if chunks are
+// short: of at most 2 / 4 / 6 / 8 / 16 rows, six heads of 96 take 109 / 96 / 88 / 88 /
+// 88 us, 32 + 8 heads of 128 and 32768 tokens 232 / 188 / 183 / 190 / 199.
+constexpr int kChunkRows = 6;
+struct Chunks {
+  int count, parts, rows, begin, end;
+  __device__ Chunks(int tiles, int count, int most, int begin) : count(count), begin(begin) {
+    parts = (count + most - 1) / most;
+    rows = (count + parts - 1) / parts;
+    end = begin + tiles * parts;
+  }
+};
+// The rows of a block's chunks: every gridDim.x-th.
+struct Walk {
+  const Chunks& of;
+  int chunk, tile, h, last;
+  __device__ explicit Walk(const Chunks& c) : of(c) {
+    const int grid = static_cast<int>(gridDim.x), ahead = (static_cast<int>(blockIdx.x) - c.begin % grid + grid) % grid;
+    chunk = ahead < c.end - c.begin ? c.begin + ahead : c.end;
+    settle();
+  }
+  __device__ __forceinline__ void settle() {
+    const int at = chunk - of.begin;
+    tile = at / of.parts;
+    h = (at - tile * of.parts) * of.rows;
+    last = min(of.count, h + of.rows);
+  }
+  __device__ __forceinline__ bool more() const { return chunk < of.end; }
+  __device__ __forceinline__ void next_chunk() {
+    chunk = of.end - chunk > static_cast<int>(gridDim.x) ? chunk + static_cast<int>(gridDim.x) : of.end;
+    settle();
+  }
+  __device__ __forceinline__ bool next() {   // whether that is another chunk's
+    if (++h < last) return false;
+    next_chunk();
+    return true;
+  }
+};
+
 template <int D, bool GAIN>
-__global__ void __launch_bounds__(kThreads) norm_rope_back_kernel(const __grid_constant__ NormArgs p, DevStatus st) {
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks) norm_rope_back_kernel(const __grid_constant__ NormArgs p, DevStatus st) {
   using L = Lanes<D>;
+  constexpr int SLOTS = kBackwardSlots;
+  __shared__ Ring<4, SLOTS> ring;
+  __shared__ float rstd[SLOTS][kThreads];
+  __shared__ float part[GAIN ? kThreads / 32 : 1][2][D];
+  __shared__ float4 gain_of[2][D / 4];
   wait_for_previous();
+  for (int i = threadIdx.x; i < D / 2; i += kThreads) {
+    const float* gain = i < D / 4 ? p.q_gain : p.k_gain;
+    (&gain_of[0][0])[i] = gain ? __ldg(reinterpret_cast<const float4*>(gain) + i % (D / 4)) : make_float4(1.f, 1.f, 1.f, 1.f);
+  }
+  __syncthreads();
   const int c = threadIdx.x % L::GROUP;
   const int64_t N = static_cast<int64_t>(p.Hq + p.H) * D + static_cast<int64_t>(p.H) * kDv;
-  int first, last;
-  head_part(p, first, last);
-  float sums[2][16] = {};   // of q's gain, of k's
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * L::TOKENS; t0 < p.T; t0 += static_cast<int64_t>(gridDim.x) * L::TOKENS) {
-    const int64_t at = t0 + threadIdx.x / L::GROUP;
-    const bool real = at < p.T, used = real && c < L::USED;
-    const int t = static_cast<int>(at);
-    float cs[8], sn[8];
-    if (used && first < p.Hq + p.H) load_turn(p, t, c, cs, sn, st, KID_NORM_BWD);
-    const auto heads = [&](int h0, int h1, const float* gain, const uint16_t* grad, int base, float (&sum)[16]) {
-      if (h0 >= h1) return;
-      float glo[8], ghi[8];
-      if (used) load_gain(gain, D, c, glo, ghi);
-#pragma unroll 2
-      for (int h = h0; h < h1; ++h) {
-        float lo[8], hi[8], a[8], b[8], dot = 0.f, r = 0.f;
-        if (used) {
-          const uint4* x = reinterpret_cast<const uint4*>(p.y + t * p.ldy + static_cast<int64_t>(h) * D);
-          const uint4* g = reinterpret_cast<const uint4*>(grad + (static_cast<int64_t>(h - base) * p.T + t) * D);
-          unpack8(lo, __ldg(x + c));
-          unpack8(hi, __ldg(x + D / 16 + c));
-          unpack8(a, __ldg(g + c));
-          unpack8(b, __ldg(g + D / 16 + c));
-          r = __ldg(p.rstd + static_cast<int64_t>(h) * p.T + t);
+  // The blocks take chunks (a tile of TOKENS tokens times a few rows of one kind) in
+  // turn: all those of q heads, then of k heads, then of v heads.
+  const int tiles = (p.T + L::TOKENS - 1) / L::TOKENS, mine = threadIdx.x / L::GROUP;
+  const Chunks q_chunks(tiles, p.Hq, p.chunk_rows, 0), k_chunks(tiles, p.H, p.chunk_rows, q_chunks.end),
+      v_chunks(tiles, p.H, p.chunk_rows, k_chunks.end);
+  // one kind of heads after the other, so that only one gain's sums are held
+  const auto heads = [&](const Chunks& chunks, int base, const uint16_t* grad, int kind) {
+    f2 sum[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float u = a[i] * cs[i] + b[i] * sn[i], w = b[i] * cs[i] - a[i] * sn[i];
-            lo[i] *= r;
-            hi[i] *= r;
-            if (GAIN) {
-              sum[i] += u * lo[i];
-              sum[8 + i] += w * hi[i];
-            }
-            a[i] = u * glo[i];
-            b[i] = w * ghi[i];
-            dot += a[i] * lo[i] + b[i] * hi[i];
+    for (int i = 0; i < 8; ++i) sum[i] = f2_make(0.f, 0.f);
+    Walk it(chunks), on(chunks);   // the row in hand, the one that is brought next
+    if (it.more()) {
+      const float4* gains = gain_of[kind] + 2 * c;
+      int at_on = 0;
+      const auto bring = [&] {
+        if (on.more()) {
+          const int t_on = on.tile * L::TOKENS + mine;
+          if (t_on < p.T && c < L::USED) {
+            const uint4* xs = reinterpret_cast<const uint4*>(p.y + t_on * p.ldy + static_cast<int64_t>(base + on.h) * D + 8 * c);
+            const uint4* gs = reinterpret_cast<const uint4*>(grad + (static_cast<int64_t>(on.h) * p.T + t_on) * D + 8 * c);
+            ring.bring(at_on, 0, xs);
+            ring.bring(at_on, 1, xs + D / 16);
+            ring.bring(at_on, 2, gs);
+            ring.bring(at_on, 3, gs + D / 16);
+            cp4(smem_u32(&rstd[at_on % SLOTS][threadIdx.x]), p.rstd + static_cast<int64_t>(base + on.h) * p.T + t_on);
           }
+          on.next();
         }
-        dot = group_add<L::GROUP>(dot) * (1.f / D);
-        if (!used) continue;
+        ++at_on;
+        cp_commit();
+      };
+#pragma unroll 1
+      for (int i = 0; i < SLOTS - 1; ++i) bring();
+      f2 cs[4], sn[4];
+      bool turned = false;
+#pragma unroll 1
+      for (int at = 0; it.more(); ++at) {
+        const int t = it.tile * L::TOKENS + mine, h = it.h;
+        const bool used = t < p.T && c < L::USED;
+        if (used && !turned) load_turn(p, t, c, cs, sn, st, KID_NORM_BWD);
+        turned = true;
+        cp_wait<SLOTS - 2>();
+        const float r = rstd[at % SLOTS][threadIdx.x];
+        f2 lo[4], hi[4], u[4], w[4], dots = f2_make(0.f, 0.f);
+        const f2 rr = f2_make(r, r);
+        if (used) {
+          unpack_f2(lo, ring.get(at, 0));
+          unpack_f2(hi, ring.get(at, 1));
+          unpack_f2(u, ring.get(at, 2));
+          unpack_f2(w, ring.get(at, 3));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a[i] = r * (a[i] - lo[i] * dot);
-          b[i] = r * (b[i] - hi[i] * dot);
+          for (int i = 0; i < 4; ++i) {
+            const f2 m = f2_fma(w[i], sn[i], f2_mul(u[i], cs[i])), n = f2_sub(f2_mul(w[i], cs[i]), f2_mul(u[i], sn[i]));
+            lo[i] = f2_mul(lo[i], rr);
+            hi[i] = f2_mul(hi[i], rr);
+            if (GAIN) {
+              sum[i] = f2_fma(m, lo[i], sum[i]);
+              sum[4 + i] = f2_fma(n, hi[i], sum[4 + i]);
+            }
+            u[i] = m;
+            w[i] = n;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {   // (read for every row: held, they took 16 registers)
+            const float4 a = gains[i / 2], b = gains[D / 8 + i / 2];
+            u[i] = f2_mul(u[i], f2_make(a.x, a.y)), u[i + 1] = f2_mul(u[i + 1], f2_make(a.z, a.w));
+            w[i] = f2_mul(w[i], f2_make(b.x, b.y)), w[i + 1] = f2_mul(w[i + 1], f2_make(b.z, b.w));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dots = f2_fma(w[i], hi[i], f2_fma(u[i], lo[i], dots));
         }
-        uint4* to = reinterpret_cast<uint4*>(p.dy + t * N + static_cast<int64_t>(h) * D);
-        to[c] = pack8(a);
-        to[D / 16 + c] = pack8(b);
+        bring();
+        const float2 d2 = f2_split(dots);
+        const float dot = group_add<L::GROUP>(d2.x + d2.y) * (-1.f / D);
+        if (used) {
+          const f2 dd = f2_make(dot, dot);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            u[i] = f2_mul(f2_fma(lo[i], dd, u[i]), rr);
+            w[i] = f2_mul(f2_fma(hi[i], dd, w[i]), rr);
+          }
+          uint4* to = reinterpret_cast<uint4*>(p.dy + t * N + static_cast<int64_t>(base + h) * D);
+          to[c] = pack_f2(u);
+          to[D / 16 + c] = pack_f2(w);
+        }
+        turned = !it.next();
       }
-    };
-    heads(first, min(last, p.Hq), p.q_gain, p.dq, 0, sums[0]);
-    heads(max(first, p.Hq), min(last, p.Hq + p.H), p.k_gain, p.dk, p.Hq, sums[1]);
-    if (real) copy_v<D, true>(p, t, c, N, max(first, p.Hq + p.H) - p.Hq - p.H, last - p.Hq - p.H);
-  }
-  if (GAIN) {
-    // lanes with the same columns, warps, and then (by another kernel) blocks, in a fixed order
-    __shared__ float part[kThreads / 32][2][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
+    }
+    if (GAIN) {   // lanes with the same columns
+      const int lane = threadIdx.x & 31;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float x = sums[w][i];
+        float x = i % 2 ? f2_split(sum[i / 2]).y : f2_split(sum[i / 2]).x;
 #pragma unroll
         for (int o = L::GROUP; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane < L::USED) part[warp][w][(i >> 3) * (D / 2) + 8 * lane + (i & 7)] = x;
+        if (lane < L::USED) part[threadIdx.x >> 5][kind][(i >> 3) * (D / 2) + 8 * lane + (i & 7)] = x;
       }
+    }
+  };
+  heads(q_chunks, 0, p.dq, 0);
+  heads(k_chunks, p.Hq, p.dk, 1);
+  for (Walk it(v_chunks); it.more(); it.next_chunk())
+    if (it.tile * L::TOKENS + mine < p.T) copy_v<D, true>(p, it.tile * L::TOKENS + mine, c, N, it.h, it.last);
+  if (GAIN) {   // warps, and then (by another kernel) blocks, in a fixed order
     __syncthreads();
-    float* to = p.partial + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * (2 * D);
+    float* to = p.partial + static_cast<int64_t>(blockIdx.x) * (2 * D);
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
       float x = 0.f;
 #pragma unroll
@@ -241,22 +382,25 @@ __global__ void __launch_bounds__(kThreads) norm_rope_back_kernel(const __grid_c
   }
 }
 
-// Sums `blocks` partials of each of 2 d columns: 32 columns a block, its warps
-// take the partials in turn.
-__global__ void __launch_bounds__(1024) gain_sum_kernel(const __grid_constant__ NormArgs p, int d, int blocks) {
-  __shared__ float part[32][33];
+// Sums `blocks` partials of each of 2 d columns: eight columns (a sector) a block,
+// whose threads take the partials in turn.
+constexpr int kSumCols = 8, kSumRows = 128;
+__global__ void __launch_bounds__(kSumCols * kSumRows) gain_sum_kernel(const __grid_constant__ NormArgs p, int d, int blocks) {
+  __shared__ float part[kSumRows / 4][kSumCols];
   wait_for_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  const int row = threadIdx.x / kSumCols, col = threadIdx.x % kSumCols, at = blockIdx.x * kSumCols + col;
   float x = 0.f;
 #pragma unroll 4
-  for (int b = warp; b < blocks; b += 32) x += __ldcg(p.partial + static_cast<int64_t>(b) * 2 * d + col);
-  part[warp][lane] = x;
-  __syncthreads();
-  x = part[lane][warp];
+  for (int b = row; b < blocks; b += kSumRows) x += __ldcg(p.partial + static_cast<int64_t>(b) * 2 * d + at);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  const int c = blockIdx.x * 32 + warp;
-  if (lane == 0) (c < d ? p.dq_gain : p.dk_gain)[c < d ? c : c - d] = x;
+  for (int o = kSumCols; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);   // a warp's four rows
+  if ((threadIdx.x & 31) < kSumCols) part[threadIdx.x >> 5][col] = x;
+  __syncthreads();
+  if (threadIdx.x >= kSumCols) return;
+  x = 0.f;
+#pragma unroll
+  for (int w = 0; w < kSumRows / 4; ++w) x += part[w][col];
+  (at < d ? p.dq_gain : p.dk_gain)[at < d ? at : at - d] = x;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -302,9 +446,9 @@ int check_norm(const qkvp_norm_rope* n, NormArgs* a) {
   return QKVP_OK;
 }
 
-// Parts of the heads: as many as bring the blocks to two a multiprocessor.
+// Parts of the heads: as many as bring the blocks to four a multiprocessor.
 int head_parts(int64_t token_blocks, int rows, int sms) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 2 * sms / std::max<int64_t>(1, token_blocks))));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 4 * sms / std::max<int64_t>(1, token_blocks))));
 }
 
 template <int D>
@@ -314,15 +458,15 @@ cudaError_t forward(const NormArgs& a, int sms, DevStatus st, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t backward(const NormArgs& a, int sms, DevStatus st, cudaStream_t s) {
-  // Two or three blocks fit a multiprocessor: more would only leave more partials.
-  const int blocks = std::min((a.T + Lanes<D>::TOKENS - 1) / Lanes<D>::TOKENS, std::min(3 * sms, kMaxNormBlocks / 2));
-  const int parts = std::min(head_parts(blocks, a.Hq + 2 * a.H, sms), kMaxNormBlocks / blocks);
-  const dim3 grid(blocks, parts);
-  if (!a.partial) return launch_dependent(norm_rope_back_kernel<D, false>, grid, kThreads, 0, s, a, st);
-  const cudaError_t e = launch_dependent(norm_rope_back_kernel<D, true>, grid, kThreads, 0, s, a, st);
+cudaError_t backward(NormArgs a, int sms, DevStatus st, cudaStream_t s) {
+  // Blocks that are all on the GPU at once; shorter chunks where they would not all have one.
+  const int64_t units = static_cast<int64_t>((a.T + Lanes<D>::TOKENS - 1) / Lanes<D>::TOKENS) * (a.Hq + 2 * a.H);
+  const int blocks = static_cast<int>(std::min<int64_t>(units, std::min(kBackwardBlocks * sms, kMaxNormBlocks)));
+  a.chunk_rows = static_cast<int>(std::min<int64_t>(kChunkRows, units / blocks));
+  if (!a.partial) return launch_dependent(norm_rope_back_kernel<D, false>, dim3(blocks), kThreads, 0, s, a, st);
+  const cudaError_t e = launch_dependent(norm_rope_back_kernel<D, true>, dim3(blocks), kThreads, 0, s, a, st);
   if (e != cudaSuccess) return e;
-  return launch_dependent(gain_sum_kernel, dim3(2 * D / 32), 1024, 0, s, a, D, blocks * parts);
+  return launch_dependent(gain_sum_kernel, dim3(2 * D / kSumCols), kSumCols * kSumRows, 0, s, a, D, blocks);
 }
 
 }  // namespace
