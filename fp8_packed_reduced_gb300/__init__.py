@@ -61,11 +61,14 @@ class AttentionDesc(ctypes.Structure):
                 + [("scale", ctypes.c_float), ("cu", ctypes.c_void_p)])
 
 
+_Int3 = ctypes.c_int * 3
+
+
 class NormRopeDesc(ctypes.Structure):
     """The C ``qkvp_norm_rope`` struct."""
 
     _fields_ = ([(n, ctypes.c_int) for n in ("T", "Hq", "H", "d_qk", "d_v", "axes")]
-                + [("sections", ctypes.c_int * 3), ("max_pos", ctypes.c_int), ("eps", ctypes.c_float),
+                + [("sections", _Int3), ("max_pos", ctypes.c_int), ("eps", ctypes.c_float),
                    ("ldy", ctypes.c_int64)]
                 + [(n, ctypes.c_void_p) for n in ("rope_table", "pos", "q_gain", "k_gain")])
 
@@ -1024,8 +1027,7 @@ def attention_forward(q, k, v, cu=None, window=None, sinks=0, scale=None, ws=Non
     offsets: poll_device_status(ws), or without ws poll_cache_status(), tells."""
     d, dev = _attention_desc(q, k, v, cu, window, sinks, scale)
     if out is None:
-        a = torch.empty((d.T, d.Hq * 128), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((d.Hq, d.T), dtype=torch.float32, device=q.device)
+        a, lse = q.new_empty((d.T, d.Hq * 128)), q.new_empty((d.Hq, d.T), dtype=torch.float32)
     else:
         a, lse = out
         _quick_cuda(a, "a", torch.bfloat16, (d.T, d.Hq * 128), dev)
@@ -1082,7 +1084,7 @@ def _norm_rope_desc(y, pos, rope_table, Hq, H, d, q_gain, k_gain, eps, sections)
         _quick_cuda(k_gain, "k_gain", torch.float32, (d,), dev)
         at = [q_gain.data_ptr(), k_gain.data_ptr()]
     parts = (d // 2,) if sections is None else tuple(sections)
-    return NormRopeDesc(T, Hq, H, d, 128, axes, (ctypes.c_int * 3)(*parts), rope_table.shape[1], eps, ldy,
+    return NormRopeDesc(T, Hq, H, d, 128, axes, _Int3(*parts), rope_table.shape[1], eps, ldy,
                         rope_table.data_ptr(), pos.data_ptr(), *at), dev
 
 
@@ -1090,7 +1092,7 @@ def new_norm_rope_workspace(device="cuda") -> torch.Tensor:
     """A zero-initialised workspace for norm_rope_forward and norm_rope_backward
     of any shape."""
     one = 16   # an aligned address that the size does not depend on
-    d = NormRopeDesc(1, 1, 1, 128, 128, 1, (ctypes.c_int * 3)(), 1, 0.0, 384, one, one, one, one)
+    d = NormRopeDesc(1, 1, 1, 128, 128, 1, _Int3(), 1, 0.0, 384, one, one, one, one)
     ws = torch.empty(int(lib().qkvp_norm_rope_workspace_bytes(ctypes.byref(d))), dtype=torch.uint8, device=device)
     with torch.cuda.device(ws.device):
         _check(lib().qkvp_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)), "qkvp_workspace_init")
@@ -1110,9 +1112,8 @@ def norm_rope_forward(y, pos, rope_table, Hq, H, d_qk=96, q_gain=None, k_gain=No
     d, dev = _norm_rope_desc(y, pos, rope_table, Hq, H, d_qk, q_gain, k_gain, eps, sections)
     T = d.T
     if out is None:
-        bf = dict(dtype=torch.bfloat16, device=y.device)
-        q, k, v = torch.empty((Hq, T, d_qk), **bf), torch.empty((H, T, d_qk), **bf), torch.empty((H, T, 128), **bf)
-        rstd = torch.empty((Hq + H, T), dtype=torch.float32, device=y.device)
+        q, k, v = y.new_empty((Hq, T, d_qk)), y.new_empty((H, T, d_qk)), y.new_empty((H, T, 128))
+        rstd = y.new_empty((Hq + H, T), dtype=torch.float32)
     else:
         q, k, v, rstd = out
         _quick_cuda(q, "q", torch.bfloat16, (Hq, T, d_qk), dev)
@@ -1142,8 +1143,9 @@ def norm_rope_backward(dq, dk, dv, y, rstd, pos, rope_table, q_gain=None, k_gain
     _quick_cuda(dv, "dv", torch.bfloat16, (H, T, 128), dev)
     _quick_cuda(rstd, "rstd", torch.float32, (Hq + H, T), dev)
     if out is None:
-        make = lambda: None if q_gain is None else torch.empty((d_qk,), dtype=torch.float32, device=y.device)   # noqa: E731
-        o = dict(dy=torch.empty((T, y.shape[1]), dtype=torch.bfloat16, device=y.device), dq_gain=make(), dk_gain=make())
+        o = dict(dy=y.new_empty((T, y.shape[1])), dq_gain=None, dk_gain=None)
+        if q_gain is not None:
+            o.update(dq_gain=q_gain.new_empty((d_qk,)), dk_gain=q_gain.new_empty((d_qk,)))
     else:
         o = out
         _quick_cuda(o["dy"], "dy", torch.bfloat16, tuple(y.shape), dev)
