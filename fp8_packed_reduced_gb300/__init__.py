@@ -1021,8 +1021,8 @@ def attention_forward(q, k, v, cu=None, window=None, sinks=0, scale=None, ws=Non
     v [H, T, 128] bf16 as forward() or norm_rope_forward() return them (Hq a
     multiple of H); rows cu[b] .. cu[b + 1) (cu [B + 1] int32; None: all T) are
     sequence b.  A token sees its sequence's tokens up to itself, with ``window``
-    the last ``window`` of them and the sequence's first ``sinks``.  scale: 1 /
-    sqrt(d_qk) by default.  Returns (a [T, Hq * 128] bf16, oproj_forward's
+    the last ``window`` of them and the sequence's first ``sinks``.  scale (2^-64 ..
+    2^64): 1 / sqrt(d_qk) by default.  Returns (a [T, Hq * 128] bf16, oproj_forward's
     operand, lse [Hq, T] float32); rows of no sequence give 0 and -inf.  Bad
     offsets: poll_device_status(ws), or without ws poll_cache_status(), tells."""
     d, dev = _attention_desc(q, k, v, cu, window, sinks, scale)

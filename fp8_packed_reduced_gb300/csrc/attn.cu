@@ -44,6 +44,8 @@ int check_attention(const qkvp_attention* at, AttnArgs* a) {
     return QKVP_ERR_INVALID_ARGUMENT;
   if (!(at->scale > 0.f) || !(at->scale < INFINITY)) return QKVP_ERR_INVALID_ARGUMENT;
   if (!at->cu && at->B != 1) return QKVP_ERR_INVALID_ARGUMENT;
+  // The backward has lse / scale as a term of the scores, both have scale * log2(e).
+  if (at->scale < 0x1p-64f || at->scale > 0x1p64f) return QKVP_ERR_UNSUPPORTED;
   if (at->T > (1 << 24) || at->H > 128 || at->Hq > 1024 || at->Hq % at->H || at->B > (1 << 20)) return QKVP_ERR_UNSUPPORTED;
   if (at->d_qk != 64 && at->d_qk != 96 && at->d_qk != 128) return QKVP_ERR_UNSUPPORTED;
   if (at->d_v != kDv) return QKVP_ERR_UNSUPPORTED;

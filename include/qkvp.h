@@ -542,7 +542,8 @@ typedef struct qkvp_norm_rope {
 /* Workspace of the two calls (0: unsupported).  It starts with the status word
  * (zero it once with qkvp_workspace_init): a position outside [0, max_pos) counts
  * as the nearer end and is recorded as QKVP_ERR_DEVICE_INPUT.  Calls sharing one
- * must not overlap on the GPU. */
+ * must not overlap on the GPU, and what a call writes must not overlap what it
+ * reads. */
 size_t qkvp_norm_rope_workspace_bytes(const qkvp_norm_rope* n);
 
 /*   y         in  [T, N] bf16, rows ldy elements apart
@@ -578,7 +579,7 @@ typedef struct qkvp_attention {
     int B;            /* sequences, 1 .. 2^20                                      */
     int window;       /* tokens, itself included; 0: no window                     */
     int sinks;        /* first tokens of a sequence that stay visible, >= 0        */
-    float scale;      /* of the scores, positive                                   */
+    float scale;      /* of the scores, 2^-64 .. 2^64                              */
     const int32_t* cu;   /* [B + 1] row offsets of the sequences, non-decreasing, on
                           * the device; NULL: one sequence (B = 1) of T tokens.  Offsets
                           * outside [0, T] count as the nearer end; those and
@@ -587,7 +588,10 @@ typedef struct qkvp_attention {
 } qkvp_attention;
 
 /* Workspace of the two calls (0: unsupported); zero it once with
- * qkvp_workspace_init.  Calls sharing one must not overlap on the GPU. */
+ * qkvp_workspace_init.  Calls sharing one must not overlap on the GPU, and what a
+ * call writes must not overlap what it reads.  A wait inside a kernel that takes
+ * longer than its limit (qkvp_set_wait_timeout_ns) is recorded as
+ * QKVP_ERR_TIMEOUT; the call's results are then not defined. */
 size_t qkvp_attention_workspace_bytes(const qkvp_attention* at);
 
 /*   q, k, v   in  [Hq, T, d_qk], [H, T, d_qk], [H, T, 128] bf16 (as qkvp_forward

@@ -45,6 +45,14 @@ def test_attention_refuses_a_bad_description(qk, change, code):
     assert L.qkvp_attention_backward(d, P, P, P, P, P, P, P, P, P, P, BIG, None) == code
 
 
+@pytest.mark.parametrize("scale,code", [(2.0 ** -64, 0), (2.0 ** -65, 2), (2.0 ** 64, 0), (2.0 ** 65, 2)])
+def test_attention_refuses_scales_beyond_its_range(qk, scale, code):
+    L, d = qk.lib(), _at(qk, scale=scale, T=0)
+    assert (L.qkvp_attention_workspace_bytes(d) == 0) == (code != 0)
+    assert L.qkvp_attention_forward(d, P, P, P, P, P, P, BIG, None) == code
+    assert L.qkvp_attention_backward(d, P, P, P, P, P, P, P, P, P, P, BIG, None) == code
+
+
 def test_attention_refuses_bad_pointers(qk):
     L, d = qk.lib(), _at(qk)
     n = L.qkvp_attention_workspace_bytes(d)
