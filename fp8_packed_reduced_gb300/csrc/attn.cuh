@@ -38,7 +38,7 @@ struct AttnArgs {
   int4* ranges;              // [Tp / 128] key tiles of 128 queries (backward: of dq)
   int* ends;                 // [Tp / 128] end of the queries that see 128 keys (backward)
   int4* jobs[2];             // the blocks' work, longest first: [tiles][3] of the forward or of dq; [tiles] of dk and dv
-  unsigned int* counter;     // [0] the plan's blocks that are done, zero between calls; [1], [2] jobs of each list that have been taken
+  unsigned int* counter;     // [0] the plan's blocks that are done, zero between calls; [1], [2] jobs taken of each list
 };
 
 // A tile of ROWS rows of q or k in shared memory: boxes of 64 columns with

@@ -8,6 +8,25 @@
 // next step's scores and da . v are formed while this one's probabilities and ds
 // are.  What is rounded to bf16 (2^-8): probabilities for the product with da, ds
 // for those with q and k, and the results; da . a uses the bf16 a.
+//
+// Bound, of dk and dv: the tensor cores, 1570 of the 1820 cycles that a step of 96
+// queries takes (d = 96).  Of dq: the computing warps, two a scheduler; its products
+// take three fifths of the time, and the way through a step (scores, exponentials,
+// da . v, ds) is one after the other for a warp.  Measured, six sequences of 8192, 6
+// heads, d = 96 (2 (3 d + 256) operations a pair that is seen): 1389 us, 0.95
+// PFLOP/s, of it dk and dv 717 us, dq 539, da . a and the plan 28; ragged sequences of
+// up to 8192 under a window of 1024: 272 us.  On the way there:
+//   both passes, static order                                               1792 us
+//   the longest tiles first                                                 1730
+//   the issuing warp undivided, descriptors in uniform registers            1571
+//   more stages, probabilities and ds in two parts                          1497
+//   d = 96 as boxes of 32 columns (a quarter less shared memory a tile)     1464
+//   steps of 96 queries or keys, places of their own, resident blocks       1432
+//   jobs from a counter: 1486, but a ragged window                      379 -> 293
+//   no row of the next dq job in registers                                  1389
+// Slower: warpgroups that take the steps in turn instead of half of the columns
+// each (back to back 1693 against 1391 us: the registers of a whole row), three
+// warpgroups for dq (1445 against 1389).
 #include <algorithm>
 #include <atomic>
 
@@ -388,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = so + warp * kOutBytes;
     // One warpgroup brings q into TMEM, the other da.  While a job ends, the next
     // one's rows go no further than the second cache: held here they took 64
-    // registers and pushed others out to memory (six sequences of 8192, 6 heads,
-    // d = 96, both passes: 1486 us against 1389).
+    // registers and pushed others out to memory (1486 us against 1389).
     const int width = half == 0 ? D : kDv;
     const auto rows_of = [&](int tile, int head) {
       const int64_t row = min(tile * kTile + mine, p.T - 1);

@@ -1,4 +1,8 @@
-// The attention of one new token per sequence under a window (decode.cuh).
+// The attention of one new token per sequence under a window (decode.cuh).  Bound
+// by the fixed cost of that kernel, since a window leaves little to read: 64
+// sequences of up to 8192 slots, 6 heads, E4M3, window 1024 and 16 sinks, weights:
+// 28.7 us, 74 MB (10.9 us at a copy's rate); one of 131072 slots, bf16, window 4096:
+// 18.6 us, of which the host takes all (16 us on the GPU with cold caches).
 #include "decode.cuh"
 
 namespace qkvp {
