@@ -1001,7 +1001,8 @@ def _attention_desc(q, k, v, cu, window, sinks, scale):
         _quick_cuda(cu, "cu", torch.int32, (B + 1,), dev)
         at = cu.data_ptr()
     window, sinks = _window_of(window, sinks)
-    return AttentionDesc(T, Hq, H, d, 128, B, window, sinks, d ** -0.5 if scale is None else scale, at), dev
+    scale = (d or 1) ** -0.5 if scale is None else scale
+    return AttentionDesc(T, Hq, H, d, 128, min(B, _INT_MAX), window, sinks, scale, at), dev
 
 
 def new_attention_workspace(T: int, Hq: int, device="cuda") -> torch.Tensor:

@@ -144,3 +144,13 @@ def test_mixed_with_the_cache_on_a_kept_workspace(qk, fp8):
     for _ in range(2):
         assert all(torch.equal(x, o) for x, o in zip(want, run(False), strict=True))
     assert qk.poll_cache_status() == (qk.OK, 0)
+
+
+def test_attention_refuses_shapes_that_the_library_does(qk):
+    """What passes the binding's checks is refused by the library's."""
+    for Hq, H, d, dv in ((1, 1, 0, 128), (0, 1, 96, 128), (1, 0, 96, 128), (3, 2, 96, 128), (1, 1, 80, 128)):
+        q, k, v = (torch.zeros(s, dtype=torch.bfloat16, device=DEV) for s in ((Hq, 5, d), (H, 5, d), (H, 5, dv)))
+        with pytest.raises(qk.QKVPError):
+            qk.attention_forward(q, k, v)
+        with pytest.raises(qk.QKVPError):
+            qk.attention_forward(q, k, v, ws=torch.zeros(1 << 20, dtype=torch.uint8, device=DEV))
