@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 z = f2_split(f2_fma(f2_make(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, mz));
             w[i] = f2_make(ex2(z.x), ex2(z.y));
           }
-          const bool free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);   // (looked at here, used below)
+          const bool free = n == 0 || mbar_test(&g.ds_free, (n - 1) & 1);   // (looked at here, used below)
           ok = wait_asleep(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DQ);
           if (!ok) break;
           tc_fence_after();
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_load<kHalf>(ts, x);
         tmem_ld_wait();
         arrive_warp(&g.s_free);
-        bool free = n == 0 || mbar_try_wait(&g.p_free, (n - 1) & 1);   // (looked at here, used below)
+        bool free = n == 0 || mbar_test(&g.p_free, (n - 1) & 1);   // (looked at here, used below)
         f2 w[kHalf / 2];
 #pragma unroll
         for (int j = 0; j < kHalf / 2; ++j) {
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_store<kHalf / 2>(tp, out);
         tmem_st_wait();
         arrive_warp(&g.p_full);
-        free = n == 0 || mbar_try_wait(&g.ds_free, (n - 1) & 1);
+        free = n == 0 || mbar_test(&g.ds_free, (n - 1) & 1);
         ok = wait_asleep(&g.dp_full, n & 1, &g.abort, st, KID_ATTN_DKV);
         if (!ok) break;
         tc_fence_after();

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = !grows ? 1.f : m == -INFINITY ? 0.f : ex2((m - top) * p.scale_log2);
         if (grows) m = top;
         l *= f;
-        const bool free = !begun || mbar_try_wait(&g.o_done[t], (n - 1) & 1);   // (looked at here, used below)
+        const bool free = !begun || mbar_test(&g.o_done[t], (n - 1) & 1);   // (looked at here, used below)
         const float m2 = finite_or_zero(m) * p.scale_log2;
         const f2 mm = f2_make(-m2, -m2);
         f2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
