@@ -13,9 +13,9 @@
 // queries takes (d = 96).  Of dq: the computing warps, two a scheduler; its products
 // take three fifths of the time, and the way through a step (scores, exponentials,
 // da . v, ds) is one after the other for a warp.  Measured, six sequences of 8192, 6
-// heads, d = 96 (2 (3 d + 256) operations a pair that is seen): 1389 us, 0.95
+// heads, d = 96 (2 (3 d + 256) operations a pair that is seen): 1384 us, 0.95
 // PFLOP/s, of it dk and dv 717 us, dq 539, da . a and the plan 28; ragged sequences of
-// up to 8192 under a window of 1024: 272 us.  On the way there:
+// up to 8192 under a window of 1024: 270 us.  On the way there:
 //   both passes, static order                                               1792 us
 //   the longest tiles first                                                 1730
 //   the issuing warp undivided, descriptors in uniform registers            1571
@@ -24,6 +24,7 @@
 //   steps of 96 queries or keys, places of their own, resident blocks       1432
 //   jobs from a counter: 1486, but a ragged window                      379 -> 293
 //   no row of the next dq job in registers                                  1389
+//   the next dq job's first scores formed while dq is written               1384 (window 270)
 // Slower: warpgroups that take the steps in turn instead of half of the columns
 // each (back to back 1693 against 1391 us: the registers of a whole row), three
 // warpgroups for dq (1445 against 1389).
@@ -99,7 +100,7 @@ struct Shared {
 };
 
 // Warps that arrive at, or commits that complete, each barrier.
-__device__ __forceinline__ void init_barriers(Shared& g, int fixed_full, int b_users) {
+__device__ __forceinline__ void init_barriers(Shared& g, int fixed_full, int b_users, int acc_full) {
   g.abort = 0;
   mbar_init(&g.fixed_full, fixed_full);
   mbar_init(&g.fixed_empty, 2);
@@ -117,7 +118,7 @@ __device__ __forceinline__ void init_barriers(Shared& g, int fixed_full, int b_u
   mbar_init(&g.dp_free, 8);
   mbar_init(&g.ds_full, 8);
   mbar_init(&g.ds_free, 1);
-  mbar_init(&g.acc_full, 2);
+  mbar_init(&g.acc_full, acc_full);
   mbar_init(&g.acc_free[0], 4);
   mbar_init(&g.acc_free[1], 4);
   mbar_init(&g.end, 2);
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sk = smem, *sv = sk + kStages * kKBytes, *so = sv + kStages * kVBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) init_barriers(g, 8, 1);
+  if (threadIdx.x == 0) init_barriers(g, 8, 1, 1);
   if (warp == 9) {
     tmem_alloc(&g.tmem, 512);
     tmem_relinquish();
@@ -352,7 +353,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_bf16_ts(tmem + kQS, tmem + kQOpQ + kk * 8, k0 + ((s * kKBytes) >> 4) + KTile<D>::cols16(kk), id_s, kk > 0, elected);
           umma_commit_elected(&g.s_full, elected);
         }
-        umma_commit_elected(&g.acc_full, elected);
       }
     } else {
       const uint64_t v0 = VTile::desc(sv), k0 = KTile<D>::desc(sk);
@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tds = tmem + kQDs + kHalf / 2 * half + quarter;
     const f2 sc = f2_make(p.scale_log2, p.scale_log2);
     uint8_t* stage = so + warp * kOutBytes;
-    // One warpgroup brings q into TMEM, the other da.  While a job ends, the next
-    // one's rows go no further than the second cache: held here they took 64
-    // registers and pushed others out to memory (1486 us against 1389).
+    // One warpgroup brings q into TMEM, the other da: the next job's as soon as this
+    // one's last scores and da . v have been formed, so that its first ones are formed
+    // while dq is written.
     const int width = half == 0 ? D : kDv;
     const auto rows_of = [&](int tile, int head) {
       const int64_t row = min(tile * kTile + mine, p.T - 1);
@@ -436,18 +436,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n = 0, turn = 0;   // steps; jobs with any
     bool ok = true;
     JobReader jobs(g.slots);
-    bool more = jobs.peek(words, &g.abort, st, KID_ATTN_DQ);
+    // Takes the next job, if there is one.
+    const auto take = [&] {
+      if (!jobs.peek(words, &g.abort, st, KID_ATTN_DQ)) return false;
+      jobs.pop();
+      const DqJob job = dq_job_of(words);
+      if (job.begin() < job.r.last) {
+        bring_rows(job.tile, job.head);
+        arrive_warp(&g.fixed_full);
+      }
+      return true;
+    };
+    bool more = take();
 #pragma unroll 1
     while (ok && more) {
       const DqJob job = dq_job_of(words);
-      jobs.pop();
       const int row = job.tile * kTile + mine, hq = job.head;
       const bool some = job.begin() < job.r.last;
       const int begin = start_of(row), seen0 = begin < 0 ? INT_MAX : window_start(p, row, begin);
       const int sink_end = begin < 0 ? 0 : begin + min(p.sinks, p.T);
       if (some) {
-        bring_rows(job.tile, hq);
-        arrive_warp(&g.fixed_full);
         const float* stat = p.stat + static_cast<int64_t>(hq) * 2 * p.Tp + row;
         const float z0 = __ldcg(stat), delta = __ldcg(stat + p.Tp);
         const f2 mz = f2_make(z0, z0), md = f2_make(delta, delta);
@@ -491,12 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      more = jobs.peek(words, &g.abort, st, KID_ATTN_DQ);
-      if (more) {
-        const uint16_t* next = rows_of(words[0].x, words[0].y);
-        prefetch_l2(next);
-        prefetch_l2(next + width - 1);
-      }
+      more = take();
       if (some) ok = wait_asleep(&g.acc_full, turn++ & 1, &g.abort, st, KID_ATTN_DQ);
       if (!ok) break;
       tc_fence_after();
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the zeros last: a descriptor points to them from what they complete)
   uint8_t *lses = so + 8 * kOutBytes, *deltas = lses + SQ * QN * kStatBytes, *ones = deltas + SD * QN * kStatBytes, *zeros = ones + kOnesBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) init_barriers(g, 1, 2);
+  if (threadIdx.x == 0) init_barriers(g, 1, 2, 2);
   if (threadIdx.x < kTile) {
     reinterpret_cast<uint4*>(ones)[threadIdx.x] = make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u);   // 1, 1, 1, 0 ...
     reinterpret_cast<uint4*>(zeros)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
