@@ -162,7 +162,7 @@ __device__ __forceinline__ bool write_box(uint32_t taddr, float f, bool some, ui
   const int lane = threadIdx.x & 31;
   uint32_t o[32];
   tmem_ld32(taddr, o);
-  tmem_ld_wait();
+  tmem_ld_wait(o);
   if (lane == 0) bulk_wait_read<0>();
   __syncwarp();
   float big = 0.f;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           uint32_t x[kHalf];
           tmem_load<kHalf>(ts, x);
-          tmem_ld_wait();
+          tmem_ld_wait(x);
           arrive_warp(&g.s_free);
           f2 w[kHalf / 2];
 #pragma unroll
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           tmem_load<kHalf>(tdp, x);
-          tmem_ld_wait();
+          tmem_ld_wait(x);
           arrive_warp(&g.dp_free);
           ok = free || wait_asleep(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DQ);
           if (!ok) break;
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = __all_sync(0xffffffffu, i0 >= ds0 && i0 + kHalf <= end);
         uint32_t x[kHalf];
         tmem_load<kHalf>(ts, x);
-        tmem_ld_wait();
+        tmem_ld_wait(x);
         arrive_warp(&g.s_free);
         bool free = n == 0 || mbar_test(&g.p_free, (n - 1) & 1);   // (looked at here, used below)
         f2 w[kHalf / 2];
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         tmem_load<kHalf>(tdp, x);
-        tmem_ld_wait();
+        tmem_ld_wait(x);
         arrive_warp(&g.dp_free);
         ok = free || wait_asleep(&g.ds_free, (n - 1) & 1, &g.abort, st, KID_ATTN_DKV);
         if (!ok) break;

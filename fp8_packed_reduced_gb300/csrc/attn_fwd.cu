@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t x[kKeys];
         tmem_load<kKeys>(ts, x);
-        tmem_ld_wait();
+        tmem_ld_wait(x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&g.s_free[t]);
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
               tmem_ld32(to + 32 * c, o);
-              tmem_ld_wait();
+              tmem_ld_wait(o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
               tmem_st32(to + 32 * c, o);
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < 2; ++b) {   // 64 columns at a time
         uint32_t o[64];
         tmem_load<64>(to + 64 * b, o);
-        tmem_ld_wait();
+        tmem_ld_wait(o);
         if (b == 1) {   // the next job's products may begin
           tc_fence_before();
           __syncwarp();

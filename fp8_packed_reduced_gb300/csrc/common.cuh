@@ -550,6 +550,14 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The same of what was read into x, which is used no earlier: the compiler does not
+// know the values to depend on the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&x)[N]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i]));
+}
 
 // ---------------------------------------------------------------------------
 // Numerics
