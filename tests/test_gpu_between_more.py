@@ -154,3 +154,18 @@ def test_attention_refuses_shapes_that_the_library_does(qk):
             qk.attention_forward(q, k, v)
         with pytest.raises(qk.QKVPError):
             qk.attention_forward(q, k, v, ws=torch.zeros(1 << 20, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_windows_and_sinks_of_any_size(qk, d):
+    """A window as long as the sequences, or first tokens that reach as far, hide nothing."""
+    T, Hq, H = 777, 4, 2
+    q, k, v, da = normal((Hq, T, d), 1), normal((H, T, d), 2), normal((H, T, 128), 3), normal((T, Hq * 128), 4)
+    C = torch.tensor([0, 300, 777], dtype=torch.int32, device=DEV)
+
+    def run(window, sinks):
+        a, lse = qk.attention_forward(q, k, v, C, window, sinks)
+        return a, lse, *qk.attention_backward(da, q, k, v, a, lse, C, window, sinks).values()
+    want = run(None, 0)
+    for window, sinks in ((477, 0), (2 ** 31 - 1, 0), (2 ** 40, 2 ** 40), (1, 477), (5, 2 ** 31 - 1), (None, 2 ** 31 - 1)):
+        assert all(torch.equal(x, y) for x, y in zip(want, run(window, sinks), strict=True)), (window, sinks)
